@@ -405,6 +405,138 @@ MLA_API int mla_v_up_proj(const void* latent, int64_t l_s0, int64_t l_s1, const 
                           cudaStream_t stream);
 
 /*
+ * The selector in front of sparse attention.  Every cached token has an index key of 128 values
+ * [nope (64) | rope (64)] in an index cache of its own, paged like the latent cache (same slots,
+ * same block table); every query row has Hi index heads with a weight each.  A step inserts the new
+ * keys (mla_index_q_cache_insert), scores the cached ones (mla_index_scores), selects the best
+ * (mla_index_select) and attends what was selected: mla_sparse_fwd over the selected slots, or
+ * mla_selected_decode over the selected pages.
+ *
+ * Index cache.  num_blocks blocks at block_stride_bytes, block_size keys each at
+ * entry_stride_bytes: 128 bf16 values (MLA_CACHE_BF16) or 128 E4M3 codes (MLA_CACHE_FP8; the codes
+ * of key (block, offset) stand for code * index_scales[block * scale_block_stride + offset], fp32).
+ * Base and strides of the codes are multiples of 16 bytes; scale_block_stride is a multiple of 4
+ * (>= block_size) and index_scales 16-byte aligned.  index_scales is NULL for MLA_CACHE_BF16.
+ *
+ * Rows and requests.  Rows are grouped by request: request b has rows cu_q_lens[b] ..
+ * cu_q_lens[b+1]-1 (device int32 [B + 1], non-decreasing; NULL: row b is request b).  seq_lens[b]
+ * (device int32 [B]) counts its keys, the rows' own included; row i of n sees positions
+ * 0 .. seq_lens[b] - n + i.  Rows outside every request are left as they are.
+ */
+
+/*
+ * Index queries and keys of new tokens: rotated, quantised, and the keys written to the cache, in
+ * one launch (the selector's counterpart of mla_q_concat_cache_insert).
+ *   y = [x[0:64] | rope(x[64:128])] in fp32 (the rotation of mla_q_concat_cache_insert).
+ *   MLA_CACHE_BF16: stored as bf16(y); w_out = weights * weight_scale.
+ *   MLA_CACHE_FP8:  scale s = 2^k of each 128-vector, k the least integer with amax <= 448 * 2^k
+ *                   (1 for a zero vector, k >= -126), codes e4m3(y / s); the scale of a query is
+ *                   folded into its weight: w_out = (weights * weight_scale) * s.
+ *
+ *   q            device bf16 [T, Hi, 128], strides (q_s0, q_s1); 1 <= Hi <= 64.
+ *   k            device bf16 [T, 128], row stride k_s0.
+ *   weights      device fp32 [T, Hi], row stride w_s0.
+ *   q_out        device out [T, Hi, 128] contiguous, 16-byte aligned: bf16, or E4M3 bytes.
+ *   w_out        device out fp32 [T, Hi] contiguous.
+ *   slot_mapping device int64 [T]; negative: the key is not inserted (the query is still written).
+ *                A slot whose block is out of range is skipped (MLA_DEVERR_SLOT).  Two tokens with
+ *                the same slot race for it.
+ *   positions, cos_sin_cache, max_position  as in mla_q_concat_cache_insert (both NULL: no RoPE).
+ */
+MLA_API int mla_index_q_cache_insert(const void* q, int64_t q_s0, int64_t q_s1, const void* k, int64_t k_s0,
+                                     const float* weights, int64_t w_s0, float weight_scale, void* q_out, float* w_out,
+                                     void* index_cache, mla_cache_format fmt, int64_t num_blocks,
+                                     int64_t block_stride_bytes, int64_t entry_stride_bytes, float* index_scales,
+                                     int64_t scale_block_stride, int32_t block_size, const int64_t* slot_mapping,
+                                     const int64_t* positions, const float* cos_sin_cache, int64_t max_position,
+                                     int32_t T, int32_t Hi, cudaStream_t stream);
+
+/*
+ * Cached index keys read back: row cu_seq_lens[b] + i of dst holds position seq_starts[b] + i of
+ * request b, bf16(code * scale) with the product in fp32, or the bf16 values as stored.
+ *   block_table  device int32 [batch, bt_cols], row stride bt_stride.
+ *   cu_seq_lens, seq_starts, num_tokens  as in mla_gather_context.
+ *   dst          device out bf16, rows of 128 values dst_row_stride elements apart.
+ * Rows at or past cu_seq_lens[batch] are not written.  A row whose page is not in the table, or whose
+ * block id is out of range, is written as zeros (MLA_DEVERR_BLOCK).
+ */
+MLA_API int mla_index_gather(const void* index_cache, mla_cache_format fmt, int64_t num_blocks,
+                             int64_t block_stride_bytes, int64_t entry_stride_bytes, const float* index_scales,
+                             int64_t scale_block_stride, int32_t block_size, const int32_t* block_table,
+                             int64_t bt_stride, int64_t bt_cols, const int32_t* cu_seq_lens,
+                             const int32_t* seq_starts, int32_t batch, int64_t num_tokens, void* dst,
+                             int64_t dst_row_stride, cudaStream_t stream);
+
+/*
+ * Scores of the cached index keys for every query row, on the tensor cores:
+ *   s[t, j] = scale[j] * sum_h weights[t, h] * max(q[t, h, :] . k[j, :], 0)        (fp32)
+ *   scores[t, c] = max of s[t, j] over the visible tokens j of block c
+ *                  (tokens c * block_tokens .. (c + 1) * block_tokens - 1).
+ * Products are exact, sums are fp32.  A NaN stays a NaN.
+ *
+ *   q            device [T, Hi, 128], strides (q_s0, q_s1) in elements: bf16 for a bf16 cache, E4M3
+ *                bytes for an fp8 one; 1 <= Hi <= 64, base and strides multiples of 16 bytes.
+ *   weights      device fp32 [T, Hi], row stride w_s0 (an fp8 query's scale folded in).
+ *   index_cache  block_size a power of two in 16..128 or a multiple of 128.
+ *   block_table  device int32 [B, bt_cols], row stride bt_stride.
+ *   block_tokens 1, 16, 32, 64 or 128.
+ *   scores       device out fp32 [T, width], row stride s_stride.  Only columns of visible blocks are
+ *                written; tokens past width * block_tokens are not scored.
+ * Tokens whose page is not in the table, or whose block id is out of range, score -inf
+ * (MLA_DEVERR_BLOCK).
+ */
+MLA_API int mla_index_scores(const void* q, int64_t q_s0, int64_t q_s1, const float* weights, int64_t w_s0,
+                             const void* index_cache, mla_cache_format fmt, int64_t num_blocks,
+                             int64_t block_stride_bytes, int64_t entry_stride_bytes, const float* index_scales,
+                             int64_t scale_block_stride, int32_t block_size, const int32_t* block_table,
+                             int64_t bt_stride, int64_t bt_cols, const int32_t* seq_lens, const int32_t* cu_q_lens,
+                             int32_t B, int32_t T, int32_t Hi, int32_t block_tokens, float* scores, int64_t s_stride,
+                             int64_t width, cudaStream_t stream);
+
+/*
+ * The topk best-scored blocks of every row, exactly: the largest scores, ties to the lowest index;
+ * -inf and NaN are never taken.  The first `first` and the last `last` visible blocks of a row are
+ * taken whatever their scores (first + last <= topk).
+ *
+ *   scores       device fp32 [T, width], row stride s_stride; columns past a row's visible blocks,
+ *                ceil(visible tokens / block_tokens), are not read.
+ *   blocks       device out int32 [T, topk], row stride b_stride: block indices in ascending order,
+ *                then -1.
+ *   slots        device out int32 [T, topk * block_tokens], row stride sl_stride, or NULL: the cache
+ *                slots (block id * page_size + offset) of the taken blocks' visible tokens through
+ *                block_table (device int32 [B, bt_cols]), -1 elsewhere: with kv_indptr[t] =
+ *                t * topk * block_tokens and has_invalid, the key lists of mla_sparse_fwd.  A page not
+ *                in the table or outside [0, num_blocks) gives -1 (MLA_DEVERR_BLOCK).
+ *   num_blocks * page_size must be below 2^31.
+ */
+MLA_API int mla_index_select(const float* scores, int64_t s_stride, int64_t width, const int32_t* seq_lens,
+                             const int32_t* cu_q_lens, int32_t B, int32_t T, int32_t block_tokens, int32_t topk,
+                             int32_t first, int32_t last, int32_t* blocks, int64_t b_stride, int32_t* slots,
+                             int64_t sl_stride, const int32_t* block_table, int64_t bt_stride, int64_t bt_cols,
+                             int32_t page_size, int64_t num_blocks, cudaStream_t stream);
+
+/*
+ * Decode over selected pages: row t attends the visible tokens of the pages blocks[t, 0 .. topk) of
+ * its request (block_size tokens each, any order; negative entries are skipped).  Everything else as
+ * mla_paged_decode: formats, scales, out and lse.
+ *   blocks       device int32 [T, topk], row stride b_stride.  A page listed twice counts twice; one
+ *                that is partly visible counts once, and listing it again, or a page without visible
+ *                tokens, is reported (MLA_DEVERR_INDEX).
+ *   workspace    device scratch of >= mla_selected_decode_workspace_size(...) bytes, 256-byte
+ *                aligned.  Contents need no initialising and are garbage afterwards.
+ * A row without a selected token, or outside every request, gets out = 0 and lse = -inf.
+ */
+MLA_API size_t mla_selected_decode_workspace_size(int32_t T, int32_t topk, int32_t block_size, int32_t H,
+                                                  int32_t num_sms);
+MLA_API int mla_selected_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache, mla_cache_format fmt,
+                                int64_t num_blocks, int64_t block_stride_bytes, int64_t entry_stride_bytes,
+                                int32_t block_size, const int32_t* block_table, int64_t bt_stride, int64_t bt_cols,
+                                const int32_t* seq_lens, const int32_t* cu_q_lens, const int32_t* blocks,
+                                int64_t b_stride, int32_t topk, int32_t B, int32_t T, int32_t H, float softmax_scale,
+                                float q_scale, float k_scale, void* out, int64_t o_s0, int64_t o_s1, float* lse,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Gather-and-dequantise (test and debugging aid): out[i, 0..575] = the exact fp32 values of
  * the entry at slots[i] (paged addressing as in mla_paged_decode; NoPE times its tile scale
  * for DS_MLA, raw E4M3 values for FP8).  Same record addressing and decode as the attention

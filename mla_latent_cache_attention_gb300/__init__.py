@@ -21,6 +21,15 @@ Entry points (same names as the C ABI, without the ``mla_`` prefix):
   merge_attn_states      prefix / suffix merge of partial attentions by their LSEs
   gather_dequant         paged entries -> exact fp32 values (test aid)
 
+The selector in front of sparse attention (an index key of 128 values per cached token):
+
+  index_q_cache_insert   index queries and keys rotated, quantised, keys inserted into the
+                         paged index cache (bf16, or E4M3 with a scale per key)
+  index_gather           cached index keys read back as bf16
+  index_scores           weighted relu scores of every visible token, or of blocks of tokens
+  index_select           the topk best blocks of every row (and their cache slots)
+  selected_decode        decode over the selected pages of a bf16 / fp8 / fp8_ds_mla cache
+
 Every tensor argument is checked here before the call (CUDA device, dtype, rank, unit
 innermost stride; index tensors contiguous), so that a wrong tensor raises instead of being
 read with the wrong layout.  Sparse indices may be int32 or int64.
@@ -89,6 +98,17 @@ def lib():
         L.mla_qkv_quant_cache_fp8_insert.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, vp, i64, i64, vp,
                                                      vp, vp, vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, i64,
                                                      i32, i32, i32, i32, vp]
+        L.mla_index_q_cache_insert.argtypes = [vp, i64, i64, vp, i64, vp, i64, f32, vp, vp, vp, i32, i64, i64, i64, vp,
+                                               i64, i32, vp, vp, vp, i64, i32, i32, vp]
+        L.mla_index_gather.argtypes = [vp, i32, i64, i64, i64, vp, i64, i32, vp, i64, i64, vp, vp, i32, i64, vp, i64, vp]
+        L.mla_index_scores.argtypes = [vp, i64, i64, vp, i64, vp, i32, i64, i64, i64, vp, i64, i32, vp, i64, i64, vp, vp,
+                                       i32, i32, i32, i32, vp, i64, i64, vp]
+        L.mla_index_select.argtypes = [vp, i64, i64, vp, vp, i32, i32, i32, i32, i32, i32, vp, i64, vp, i64, vp, i64,
+                                       i64, i32, i64, vp]
+        L.mla_selected_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        L.mla_selected_decode_workspace_size.restype = sz
+        L.mla_selected_decode.argtypes = [vp, i64, i64, vp, i32, i64, i64, i64, i32, vp, i64, i64, vp, vp, vp, i64, i32,
+                                          i32, i32, i32, f32, f32, f32, vp, i64, i64, vp, vp, sz, vp]
         L.mla_debug_stall_next_decode.argtypes = [i32]
         L.mla_debug_stall_next_decode.restype = None
         L.mla_debug_ds_cluster.argtypes = [i32]
@@ -96,7 +116,8 @@ def lib():
         for f in ("mla_q_concat_cache_insert", "mla_sparse_fwd", "mla_sparse_fwd_staged", "mla_paged_decode",
                   "mla_gather_dequant", "mla_key_concat_cache_insert", "mla_qkv_quant_cache_fp8_insert",
                   "mla_gather_context", "mla_merge_attn_states", "mla_sparse_fwd_ext", "mla_absorb_q",
-                  "mla_v_up_proj"):
+                  "mla_v_up_proj", "mla_index_q_cache_insert", "mla_index_gather", "mla_index_scores",
+                  "mla_index_select", "mla_selected_decode"):
             getattr(L, f).restype = ctypes.c_int
         L.mla_read_device_errors.restype = ctypes.c_int
         _lib = L
@@ -499,6 +520,237 @@ def merge_attn_states(prefix_output, prefix_lse, suffix_output, suffix_lse, *, o
             prefix_output.stride(1), _ptr(prefix_lse), _ptr(suffix_output), suffix_output.stride(0),
             suffix_output.stride(1), _ptr(suffix_lse), T, H, D, _stream(prefix_output)))
     return output, lse
+
+
+def _index_format(fmt) -> int:
+    fmt = _fmt(fmt)
+    if fmt not in (CACHE_BF16, CACHE_FP8):
+        raise ValueError("the index cache is bf16 or fp8")
+    return fmt
+
+
+def _index_geometry(index_cache, index_scales, fmt, dev):
+    """(num_blocks, block stride and entry stride in bytes, block_size, scale block stride) of an
+    index cache [num_blocks, block_size, 128] and its scales fp32 [num_blocks, block_size]."""
+    _need(index_cache, "index_cache", (torch.bfloat16,) if fmt == CACHE_BF16 else _BYTE_TYPES, dev, ndim=3)
+    if index_cache.shape[2] != 128:
+        raise ValueError(f"index keys have 128 values, got {index_cache.shape[2]}")
+    nb, bstride, estride, bs = _cache_geometry(index_cache)
+    if fmt == CACHE_BF16:
+        if index_scales is not None:
+            raise ValueError("index_scales are only for the fp8 index cache")
+        return nb, bstride, estride, bs, 0
+    _need(index_scales, "index_scales", (torch.float32,), dev, ndim=2)
+    if tuple(index_scales.shape) != (nb, bs):
+        raise ValueError(f"index_scales must be [num_blocks, block_size] = {(nb, bs)}, got {tuple(index_scales.shape)}")
+    return nb, bstride, estride, bs, index_scales.stride(0)
+
+
+def _row_counts(seq_lens, cu_q_lens, T, dev):
+    """The number of requests, checked against cu_q_lens (or one row per request)."""
+    _need(seq_lens, "seq_lens", (torch.int32,), dev, ndim=1, contiguous=True)
+    B = seq_lens.numel()
+    if cu_q_lens is not None:
+        _need(cu_q_lens, "cu_q_lens", (torch.int32,), dev, ndim=1, contiguous=True)
+        if cu_q_lens.numel() != B + 1:
+            raise ValueError(f"cu_q_lens must have B + 1 = {B + 1} entries, got {cu_q_lens.numel()}")
+    elif T != B:
+        raise ValueError(f"without cu_q_lens there is one row per request: {T} rows, {B} requests")
+    return B
+
+
+def _need_table(block_table, rows, dev):
+    _need(block_table, "block_table", (torch.int32,), dev, ndim=2)
+    if block_table.shape[0] < rows:
+        raise ValueError(f"block_table needs a row per request: {block_table.shape[0]} rows, {rows} requests")
+
+
+def index_q_cache_insert(q, k, weights, index_cache, index_scales, slot_mapping, *, fmt, weight_scale=1.0,
+                         positions=None, cos_sin_cache=None, q_out=None, w_out=None):
+    """Index queries [T, Hi, 128] and keys [T, 128] (bf16) rotated, quantised, and the keys written to
+    the index cache at slot_mapping.  Returns (q_out [T, Hi, 128]: bf16, or uint8 E4M3 codes;
+    w_out fp32 [T, Hi]: weights * weight_scale, times the query's scale for fp8)."""
+    fmt = _index_format(fmt)
+    dev = _cuda_device(q)
+    _need(q, "q", (torch.bfloat16,), dev, ndim=3)
+    T, Hi, width = q.shape
+    _need(k, "k", (torch.bfloat16,), dev)
+    if k.dim() == 3 and k.shape[1] == 1:      # [T, 1, 128] (a head axis of size 1)
+        k = k.squeeze(1)
+    _need(weights, "weights", (torch.float32,), dev, ndim=2)
+    _need(slot_mapping, "slot_mapping", (torch.int64,), dev, ndim=1, contiguous=True)
+    if width != 128 or tuple(k.shape) != (T, 128) or tuple(weights.shape) != (T, Hi) or slot_mapping.numel() != T:
+        raise ValueError("q must be [T, Hi, 128], k [T, 128], weights [T, Hi] and slot_mapping [T]")
+    if positions is not None:
+        _need(positions, "positions", (torch.int64,), dev, ndim=1, contiguous=True)
+        if positions.numel() != T:
+            raise ValueError(f"positions must have T = {T} entries")
+    if cos_sin_cache is not None:
+        _need(cos_sin_cache, "cos_sin_cache", (torch.float32,), dev, ndim=2, contiguous=True)
+        if cos_sin_cache.shape[1] != 64:
+            raise ValueError("cos_sin_cache must be [max_position, 64]")
+    out_type = torch.bfloat16 if fmt == CACHE_BF16 else torch.uint8
+    if q_out is None:
+        q_out = torch.empty((T, Hi, 128), dtype=out_type, device=dev)
+    if w_out is None:
+        w_out = torch.empty((T, Hi), dtype=torch.float32, device=dev)
+    _need(q_out, "q_out", (out_type,), dev, ndim=3, contiguous=True)
+    _need(w_out, "w_out", (torch.float32,), dev, ndim=2, contiguous=True)
+    if tuple(q_out.shape) != (T, Hi, 128) or tuple(w_out.shape) != (T, Hi):
+        raise ValueError("q_out must be [T, Hi, 128] and w_out [T, Hi]")
+    nb, bstride, estride, bs, sstride = _index_geometry(index_cache, index_scales, fmt, dev)
+    max_pos = 0 if cos_sin_cache is None else cos_sin_cache.shape[0]
+    with torch.cuda.device(dev):
+        _check(lib().mla_index_q_cache_insert(
+            _ptr(q), q.stride(0), q.stride(1), _ptr(k), k.stride(0), _ptr(weights), weights.stride(0),
+            float(weight_scale), _ptr(q_out), _ptr(w_out), _ptr(index_cache), fmt, nb, bstride, estride,
+            _ptr(index_scales), sstride, bs, _ptr(slot_mapping), _ptr(positions), _ptr(cos_sin_cache), max_pos, T, Hi,
+            _stream(q)))
+    return q_out, w_out
+
+
+def index_gather(index_cache, index_scales, block_table, cu_seq_lens, seq_starts=None, *, fmt, num_tokens, dst=None):
+    """Cached index keys as bf16 [num_tokens, 128]: rows cu_seq_lens[b] .. cu_seq_lens[b+1]-1 hold
+    request b's positions seq_starts[b] + i."""
+    fmt = _index_format(fmt)
+    dev = _cuda_device(index_cache)
+    nb, bstride, estride, bs, sstride = _index_geometry(index_cache, index_scales, fmt, dev)
+    _need(cu_seq_lens, "cu_seq_lens", (torch.int32,), dev, ndim=1, contiguous=True)
+    batch = cu_seq_lens.numel() - 1
+    _need_table(block_table, batch, dev)
+    if seq_starts is not None:
+        _need(seq_starts, "seq_starts", (torch.int32,), dev, ndim=1, contiguous=True)
+        if seq_starts.numel() < batch:
+            raise ValueError("seq_starts needs an entry per request")
+    if dst is None:
+        dst = torch.empty((num_tokens, 128), dtype=torch.bfloat16, device=dev)
+    _need(dst, "dst", (torch.bfloat16,), dev, ndim=2)
+    if tuple(dst.shape) != (num_tokens, 128):
+        raise ValueError(f"dst must be [num_tokens, 128] = {(num_tokens, 128)}")
+    with torch.cuda.device(dev):
+        _check(lib().mla_index_gather(
+            _ptr(index_cache), fmt, nb, bstride, estride, _ptr(index_scales), sstride, bs, _ptr(block_table),
+            block_table.stride(0), block_table.shape[1], _ptr(cu_seq_lens), _ptr(seq_starts), batch, int(num_tokens),
+            _ptr(dst), dst.stride(0), _stream(index_cache)))
+    return dst
+
+
+def index_scores(q, weights, index_cache, index_scales, block_table, seq_lens, cu_q_lens=None, *, fmt, block_tokens=1,
+                 max_context, scores=None):
+    """Scores sum_h weights[t, h] * relu(q[t, h] . k[j]) of every visible token (block_tokens = 1), or
+    their maximum over blocks of block_tokens.  q [T, Hi, 128] (bf16, or uint8 E4M3 codes with their
+    scales in the weights).  Returns scores fp32 [T, >= ceil(max_context / block_tokens)]; only the
+    columns of visible blocks are written."""
+    fmt = _index_format(fmt)
+    dev = _cuda_device(q)
+    _need(q, "q", (torch.bfloat16,) if fmt == CACHE_BF16 else _BYTE_TYPES, dev, ndim=3)
+    T, Hi, width = q.shape
+    _need(weights, "weights", (torch.float32,), dev, ndim=2)
+    if width != 128 or tuple(weights.shape) != (T, Hi):
+        raise ValueError("q must be [T, Hi, 128] and weights [T, Hi]")
+    B = _row_counts(seq_lens, cu_q_lens, T, dev)
+    _need_table(block_table, B, dev)
+    nb, bstride, estride, bs, sstride = _index_geometry(index_cache, index_scales, fmt, dev)
+    cols = -(-int(max_context) // int(block_tokens))
+    if scores is None:
+        scores = torch.empty((T, cols), dtype=torch.float32, device=dev)
+    _need(scores, "scores", (torch.float32,), dev, ndim=2)
+    if scores.shape[0] != T or scores.shape[1] < cols:
+        raise ValueError(f"scores must be [T, >= {cols}] with T = {T}, got {tuple(scores.shape)}")
+    with torch.cuda.device(dev):
+        _check(lib().mla_index_scores(
+            _ptr(q), q.stride(0), q.stride(1), _ptr(weights), weights.stride(0), _ptr(index_cache), fmt, nb, bstride,
+            estride, _ptr(index_scales), sstride, bs, _ptr(block_table), block_table.stride(0), block_table.shape[1],
+            _ptr(seq_lens), _ptr(cu_q_lens), B, T, Hi, int(block_tokens), _ptr(scores), scores.stride(0), cols,
+            _stream(q)))
+    return scores
+
+
+def index_select(scores, seq_lens, topk, cu_q_lens=None, *, block_tokens=1, first=0, last=0, block_table=None,
+                 page_size=0, num_blocks=0, blocks=None, slots=None):
+    """The topk best-scored blocks of every row, ascending, -1 after them; ties go to the lowest index,
+    -inf and NaN are never taken, the first `first` and last `last` visible blocks always.  With a
+    block_table (and page_size, num_blocks) also the cache slots of their visible tokens, for
+    sparse_fwd.  Returns (blocks int32 [T, topk], slots int32 [T, topk * block_tokens] or None)."""
+    dev = _cuda_device(scores)
+    _need(scores, "scores", (torch.float32,), dev, ndim=2)
+    T, width = scores.shape
+    B = _row_counts(seq_lens, cu_q_lens, T, dev)
+    topk, block_tokens = int(topk), int(block_tokens)
+    if topk < 1 or block_tokens < 1:
+        raise ValueError("topk and block_tokens must be >= 1")
+    if blocks is None:
+        blocks = torch.empty((T, topk), dtype=torch.int32, device=dev)
+    _need(blocks, "blocks", (torch.int32,), dev, ndim=2)
+    if tuple(blocks.shape) != (T, topk):
+        raise ValueError(f"blocks must be [T, topk] = {(T, topk)}")
+    if block_table is None:
+        if slots is not None:
+            raise ValueError("slots need a block_table")
+    else:
+        _need_table(block_table, B, dev)
+        if slots is None:
+            slots = torch.empty((T, topk * block_tokens), dtype=torch.int32, device=dev)
+        _need(slots, "slots", (torch.int32,), dev, ndim=2)
+        if tuple(slots.shape) != (T, topk * block_tokens):
+            raise ValueError(f"slots must be [T, topk * block_tokens] = {(T, topk * block_tokens)}")
+    with torch.cuda.device(dev):
+        _check(lib().mla_index_select(
+            _ptr(scores), scores.stride(0), width, _ptr(seq_lens), _ptr(cu_q_lens), B, T, block_tokens, topk,
+            int(first), int(last), _ptr(blocks), blocks.stride(0), _ptr(slots), 0 if slots is None else slots.stride(0),
+            _ptr(block_table), 0 if block_table is None else block_table.stride(0),
+            0 if block_table is None else block_table.shape[1], int(page_size), int(num_blocks), _stream(scores)))
+    return blocks, slots
+
+
+def selected_decode_workspace_size(T, topk, block_size, H, num_sms=0) -> int:
+    return int(lib().mla_selected_decode_workspace_size(T, topk, block_size, H, num_sms))
+
+
+def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, *, fmt, softmax_scale, q_scale=1.0,
+                    k_scale=1.0, out=None, return_lse=False, workspace=None, lse=None):
+    """Decode over the selected pages: row t of q [T, H, 576] attends the visible tokens of pages
+    blocks[t] (int32 [T, topk], negative entries skipped) of its request.  Returns (out [T, H, 512]
+    bf16, lse [T, H] or None), as paged_decode."""
+    fmt = _fmt(fmt)
+    dev = _cuda_device(q)
+    _need(q, "q", _BYTE_TYPES if fmt == CACHE_FP8 else (torch.bfloat16,), dev, ndim=3)
+    T, H, width = q.shape
+    if width != 576:
+        raise ValueError(f"q must be [T, H, 576], got {tuple(q.shape)}")
+    _need(kv_cache, "kv_cache", _BYTE_TYPES + (torch.bfloat16,), dev)
+    B = _row_counts(seq_lens, cu_q_lens, T, dev)
+    _need_table(block_table, B, dev)
+    _need(blocks, "blocks", (torch.int32,), dev, ndim=2)
+    if blocks.shape[0] != T:
+        raise ValueError(f"blocks must be [T, topk] with T = {T}, got {tuple(blocks.shape)}")
+    topk = blocks.shape[1]
+    if out is None:
+        out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", (torch.bfloat16,), dev, ndim=3)
+    if out.shape[0] != T or out.shape[1] != H or out.shape[2] < 512:
+        raise ValueError(f"out must be [T, H, >= 512], got {tuple(out.shape)}")
+    if return_lse and lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _need(lse, "lse", (torch.float32,), dev, ndim=2, contiguous=True)
+        if tuple(lse.shape) != (T, H):
+            raise ValueError(f"lse must be [T, H] = {(T, H)}")
+    nb, bstride, estride, bs = _cache_geometry(kv_cache)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = selected_decode_workspace_size(T, topk, bs, H)
+            if need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if workspace is not None:
+            _need(workspace, "workspace", _BYTE_TYPES, dev, contiguous=True)
+        _check(lib().mla_selected_decode(
+            _ptr(q), q.stride(0), q.stride(1), _ptr(kv_cache), fmt, nb, bstride, estride, bs, _ptr(block_table),
+            block_table.stride(0), block_table.shape[1], _ptr(seq_lens), _ptr(cu_q_lens), _ptr(blocks),
+            blocks.stride(0), topk, B, T, H, float(softmax_scale), float(q_scale), float(k_scale), _ptr(out),
+            out.stride(0), out.stride(1), _ptr(lse), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(q)))
+    return out, lse
 
 
 def gather_dequant(kv_cache, slots, *, fmt):

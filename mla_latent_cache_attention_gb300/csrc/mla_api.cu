@@ -10,6 +10,7 @@
 
 #include "mla.h"
 #include "mla_attn.cuh"
+#include "mla_host.h"
 #include "mla_internal.h"
 #include "mla_ds.cuh"
 #include "mla_paged_tma.cuh"
@@ -29,6 +30,8 @@ void prof_end(cudaStream_t s) {
   if (g_prof_start && g_prof_stop) cudaEventRecord(g_prof_stop, s);
 }
 
+}  // namespace
+
 int fail(int code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -42,15 +45,11 @@ int ok() {
   return MLA_OK;
 }
 
-struct DevInfo {
-  bool ready = false;
-  int sms = 0;
-  uint32_t* err = nullptr;
-};
+namespace {
 DevInfo g_dev[64];
 std::mutex g_dev_mu;
+}  // namespace
 
-// SM count and device error word of the current device (looked up once per device).
 int dev_info(DevInfo** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
@@ -70,7 +69,7 @@ int dev_info(DevInfo** out) {
   return MLA_OK;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+namespace {
 
 int entry_bytes(mla_cache_format f) {
   return f == MLA_CACHE_BF16 ? 1152 : f == MLA_CACHE_FP8 ? 576 : 656;
@@ -157,19 +156,16 @@ TmapEntry g_tmaps[16];
 int g_tmap_next = 0;
 std::mutex g_tmap_mu;
 
-// Rows per TMA box for a block size, or 0 when the page kernel does not serve it: the box
-// rows must divide the 128-key tile (block_size 16..128 a power of two) or be a whole
-// 128-row slice of a larger block.
-int tma_rows_for(int block_size, int keys_per_tile = 128) {
+}  // namespace
+
+int tma_rows_for(int block_size, int keys_per_tile) {
   if (block_size >= keys_per_tile) return (block_size % keys_per_tile == 0) ? keys_per_tile : 0;
   if (block_size >= 16 && (keys_per_tile % block_size) == 0) return block_size;
   return 0;
 }
 
-// 3-D uint8 tensor map (128-byte swizzle, or none): dims {x bytes, y, z}, strides {y, z} in
-// bytes.
 int tmap_3d(const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2], const uint32_t (&box)[3],
-            CUtensorMap* out, bool swizzle = true) {
+            CUtensorMap* out, bool swizzle) {
   TmapKey key{};
   key.base = base;
   key.swz = swizzle;
@@ -209,6 +205,8 @@ int tmap_3d(const void* base, const uint64_t (&dims)[3], const uint64_t (&stride
   *out = e.map;
   return MLA_OK;
 }
+
+namespace {
 
 // Column grouping of the page kernel: NQ query columns per item (16, 32 or 64; at most 32 for
 // bf16, whose 144 KB key tiles leave less room for the query), G groups per request and the
@@ -728,23 +726,20 @@ extern "C" size_t mla_paged_decode_workspace_size(int32_t B, int32_t q_len, int3
   return workspace_bytes_for(n_rows, H, sp);
 }
 
-extern "C" int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache,
-                                mla_cache_format fmt, int64_t num_blocks, int64_t block_stride_bytes,
-                                int64_t entry_stride_bytes, int32_t block_size,
-                                const int32_t* block_table, int64_t bt_stride, const int32_t* seq_lens,
-                                int32_t B, int32_t q_len, int32_t H, int32_t max_context,
-                                float softmax_scale, float q_scale, float k_scale, void* out,
-                                int64_t o_s0, int64_t o_s1, float* lse, void* workspace,
-                                size_t workspace_bytes, cudaStream_t stream) {
+int mla::check_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache, int fmt, int64_t num_blocks,
+                            int64_t block_stride_bytes, int64_t entry_stride_bytes, int32_t block_size,
+                            const int32_t* block_table, int64_t bt_stride, const int32_t* seq_lens, int32_t B,
+                            int32_t q_len, int32_t H, int32_t max_context, const void* out, int64_t o_s0, int64_t o_s1,
+                            const float* lse) {
   if (fmt != MLA_CACHE_BF16 && fmt != MLA_CACHE_FP8 && fmt != MLA_CACHE_FP8_DS_MLA)
-    return fail(MLA_ERR_INVALID, "unknown cache format %d", static_cast<int>(fmt));
+    return fail(MLA_ERR_INVALID, "unknown cache format %d", fmt);
   if (B < 0 || q_len < 1 || H < 1) return fail(MLA_ERR_INVALID, "bad shape B=%d q_len=%d H=%d", B, q_len, H);
   if (H > 128) return fail(MLA_ERR_UNSUPPORTED, "H must be <= 128, got %d", H);
   if (max_context < 1) return fail(MLA_ERR_INVALID, "max_context must be >= 1");
-  if (B == 0) return ok();
+  if (B == 0) return MLA_OK;
   if (!q || !kv_cache || !block_table || !seq_lens || !out) return fail(MLA_ERR_INVALID, "a required pointer is NULL");
   if (block_size < 1 || num_blocks < 1 || bt_stride < 1) return fail(MLA_ERR_INVALID, "bad cache geometry");
-  if (entry_stride_bytes < entry_bytes(fmt) || entry_stride_bytes % 16 || block_stride_bytes % 16 ||
+  if (entry_stride_bytes < entry_bytes(static_cast<mla_cache_format>(fmt)) || entry_stride_bytes % 16 || block_stride_bytes % 16 ||
       block_stride_bytes < entry_stride_bytes * block_size || !aligned(kv_cache, 16))
     return fail(MLA_ERR_INVALID, "cache entries need 16-byte alignment and non-overlapping strides");
   const int qalign = fmt == MLA_CACHE_FP8 ? 8 : 16;
@@ -753,6 +748,22 @@ extern "C" int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const
   if (!aligned(out, 2) || o_s1 < 512 || o_s0 < static_cast<int64_t>(H) * o_s1)
     return fail(MLA_ERR_INVALID, "bad out strides");
   if (lse && !aligned(lse, 4)) return fail(MLA_ERR_INVALID, "lse must be 4-byte aligned");
+  return MLA_OK;
+}
+
+extern "C" int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache,
+                                mla_cache_format fmt, int64_t num_blocks, int64_t block_stride_bytes,
+                                int64_t entry_stride_bytes, int32_t block_size,
+                                const int32_t* block_table, int64_t bt_stride, const int32_t* seq_lens,
+                                int32_t B, int32_t q_len, int32_t H, int32_t max_context,
+                                float softmax_scale, float q_scale, float k_scale, void* out,
+                                int64_t o_s0, int64_t o_s1, float* lse, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream) {
+  if (int rc = check_paged_decode(q, q_s0, q_s1, kv_cache, fmt, num_blocks, block_stride_bytes, entry_stride_bytes,
+                                  block_size, block_table, bt_stride, seq_lens, B, q_len, H, max_context, out, o_s0,
+                                  o_s1, lse))
+    return rc;
+  if (B == 0) return ok();
   DevInfo* d = nullptr;
   if (int rc = dev_info(&d)) return rc;
   const int64_t n_rows = static_cast<int64_t>(B) * q_len;

@@ -1,0 +1,556 @@
+// mla_index_scores.cu -- the cheap score that chooses what sparse attention reads: every visible
+// cached index key against the index queries of a row,
+//   s[t, j] = ks[j] * sum_h w[t, h] * relu(q[t, h, :] . k[j, :]),
+// stored per token, or as the maximum over blocks of 16..128 tokens.
+//
+// Design.  The key tile (128 keys x 128 values, E4M3 or bf16) is the M operand and the query rows
+// (up to 256 = 4 queries x 64 heads, 8 x 32, ...) the N operand of tcgen05.mma, so a TMEM lane
+// is a key and a column a (query, head): the sum over heads stays inside one thread, needs no
+// exchange, and a warp's 32 results are 32 neighbouring scores of one row.  relu and the weights
+// run between the two, on CUDA cores, in fp32; the weights of a thread's 64 columns stay in
+// registers for all key tiles of a query tile.
+//
+// Work is cut into units of one key tile x one query tile, enumerated over requests by a closed
+// form (a causal row sees seq_len - rows + i + 1 keys), and every CTA takes an equal contiguous
+// range of them: scores are independent, so nothing is merged and no counter is shared.
+//
+// Warps: 0 producer (TMA boxes of pages, lanes resolve page ids), 1 MMA issuer and TMEM owner,
+// 2..17 four epilogue groups of four warps, one 64-column slice of the accumulator each.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "mla_index.h"
+#include "mla_internal.h"
+#include "mla_paged_tma.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kIxCols = 256;                  // query rows (MMA N) of a tile
+constexpr int kIxThreads = 32 * 18;
+constexpr int kSegDepth = 4;
+
+// A run of key tiles of one query tile.
+struct Segment {
+  int t0, nq;          // first row and rows of the query tile
+  int j0, nt;          // first key tile and number of key tiles; nt = 0 ends the queue
+  int vis0;            // keys that row t0 sees (row t0 + i: vis0 + i), may be <= 0
+  int b, pad0, pad1;
+};
+
+template <int F>
+struct IndexCfg {
+  static_assert(F == kBF16 || F == kFP8, "format");
+  static constexpr int kHalves = F == kBF16 ? 2 : 1;            // 128-byte columns of a row
+  static constexpr int kTileBytes = 128 * 128 * kHalves;
+  static constexpr int kQBytes = kIxCols * 128 * kHalves;
+  static constexpr int kS = F == kBF16 ? 2 : 8;                 // key tiles in flight
+  static constexpr int kSc = kS + 2;                            // their scales (see the producer)
+  static constexpr int kQ = 0;
+  static constexpr int kRing = kQ + 2 * kQBytes;
+  static constexpr int kScale = kRing + kS * kTileBytes;
+  static constexpr int kRed = kScale + kSc * 512;               // block maxima of 16 warps x 8 queries
+  static constexpr int kSeg = kRed + 2 * 16 * 8 * 4;
+  static constexpr int kBad = kSeg + kSegDepth * 32;
+  static constexpr int kBar = kBad + ((kSc * 4 + 7) & ~7);
+  static constexpr int kNumBars = 2 * kS + kSc + 8 + 2 * kSegDepth + 8 + 1;
+  static constexpr int kMisc = kBar + kNumBars * 8;
+  static constexpr int kAlloc = kMisc + 64 + 1024;
+  static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+};
+
+// sum over y = 1..x of ceil(y / r) (0 for x <= 0)
+__device__ __forceinline__ int64_t ceil_sum(int64_t x, int r) {
+  if (x <= 0) return 0;
+  const int64_t q = x / r, s = x - q * r;
+  return r * (q * (q + 1) / 2) + s * (q + 1);
+}
+
+// Units of a request: query tiles of QT rows, tile i with ceil((a + i + 1) / r) key tiles, where
+// a = ceil((L - n) / QT) and r = 128 / QT: ceil((L - n + (i + 1) QT) / 128).
+struct Request {
+  int64_t a;
+  int row0, n, L, m;
+  int64_t units;
+};
+
+template <int QT>
+__device__ __forceinline__ Request load_request(const IndexScoresParams& p, int b) {
+  Request q;
+  if (p.cu_q) {
+    q.row0 = min(max(p.cu_q[b], 0), p.T);
+    q.n = max(min(p.cu_q[b + 1], p.T) - q.row0, 0);
+  } else {
+    q.row0 = b;
+    q.n = b < p.T ? 1 : 0;
+  }
+  q.L = max(p.seq_lens[b], 0);
+  q.m = (q.n + QT - 1) / QT;
+  const int d = q.L - q.n;
+  q.a = d >= 0 ? (d + QT - 1) / QT : -((-d) / QT);
+  q.units = ceil_sum(q.a + q.m, 128 / QT) - ceil_sum(q.a, 128 / QT);
+  return q;
+}
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+template <int F, int HP>
+__global__ void __launch_bounds__(kIxThreads, 1)
+    mla_index_scores_kernel(const __grid_constant__ IndexScoresParams p, const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_q) {
+  using C = IndexCfg<F>;
+  constexpr int S = C::kS, SC = C::kSc, HV = C::kHalves;
+  constexpr int QT = kIxCols / HP;             // queries of a tile
+  constexpr int QW = 64 / HP;                  // queries of an epilogue group
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qs = smem + C::kQ;
+  uint8_t* ring = smem + C::kRing;
+  float* scales = reinterpret_cast<float*>(smem + C::kScale);
+  float* red = reinterpret_cast<float*>(smem + C::kRed);
+  Segment* segs = reinterpret_cast<Segment*>(smem + C::kSeg);
+  uint32_t* bad = reinterpret_cast<uint32_t*>(smem + C::kBad);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar);
+  uint64_t* k_full = bars;                     // [S] key tile landed
+  uint64_t* k_empty = k_full + S;              // [S] its MMAs are done
+  uint64_t* sc_full = k_empty + S;             // [SC] scales and bad-page mask of a tile
+  uint64_t* q_full = sc_full + SC;             // [2]
+  uint64_t* q_empty = q_full + 2;              // [2]
+  uint64_t* d_full = q_empty + 2;              // [2] accumulator ready
+  uint64_t* d_empty = d_full + 2;              // [2] accumulator read
+  uint64_t* seg_full = d_empty + 2;
+  uint64_t* seg_empty = seg_full + kSegDepth;
+  uint64_t* red_full = seg_empty + kSegDepth;  // [4 groups][2] block maxima of the group's warps written
+  uint64_t* fin = red_full + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 8);
+  int64_t* start = reinterpret_cast<int64_t*>(smem + C::kMisc + 16);      // [0] first unit's request, [1] its offset, [2] units
+  int64_t* part = reinterpret_cast<int64_t*>(red);      // setup only: 18 warp totals
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < SC; ++i) mbar_init(&sc_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], 16);
+    }
+    for (int i = 0; i < kSegDepth; ++i) {
+      mbar_init(&seg_full[i], 1);
+      mbar_init(&seg_empty[i], 17);
+    }
+    for (int i = 0; i < 8; ++i) mbar_init(&red_full[i], 4);
+    mbar_init(fin, 1);
+    abort_flag[0] = 0;
+    abort_flag[1] = 0;
+    start[0] = p.B;
+    start[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  // ---- this CTA's range of units: [W c / G, W (c + 1) / G), and the request it starts in
+  int64_t total = 0, lo = 0, hi = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kIxThreads) {
+      const int b = b0 + tid;
+      const int64_t u = b < p.B ? load_request<QT>(p, b).units : 0;
+      int64_t inc = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      __syncthreads();
+      if (lane == 31) part[warp] = inc;
+      __syncthreads();
+      int64_t base = before, all = 0;
+      for (int w = 0; w < kIxThreads / 32; ++w) {
+        const int64_t v = part[w];
+        if (w < warp) base += v;
+        all += v;
+      }
+      if (pass == 1) {
+        const int64_t first = base + inc - u;
+        if (first <= lo && lo < first + u && lo < hi) {
+          start[0] = b;
+          start[1] = lo - first;
+        }
+      }
+      before += all;
+    }
+    if (pass == 0) {
+      total = before;
+      lo = total / gridDim.x * blockIdx.x + min(total % gridDim.x, static_cast<int64_t>(blockIdx.x));
+      hi = lo + total / gridDim.x + (blockIdx.x < total % gridDim.x ? 1 : 0);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ producer
+    int b = static_cast<int>(start[0]);
+    int64_t x = start[1], rem = hi - lo;
+    const int BR = p.BR, SP = 128 / BR;            // page slices of BR rows, SP of them a tile
+    const int TG = 32 / SP;                        // key tiles covered by one page lookup of the warp
+    int64_t tile = 0;                              // key tiles issued
+    int nseg = 0;
+    uint32_t errbits = 0;
+    bool ok = true;
+    while (ok && rem > 0 && b < p.B) {
+      const Request rq = load_request<QT>(p, b);
+      if (x >= rq.units) {
+        ++b;
+        x = 0;
+        continue;
+      }
+      // the query tile that holds unit x
+      constexpr int r = 128 / QT;
+      const int64_t fa = ceil_sum(rq.a, r);
+      int i0 = 0, i1 = rq.m - 1;
+      while (i0 < i1) {
+        const int mid = (i0 + i1 + 1) >> 1;
+        if (ceil_sum(rq.a + mid, r) - fa <= x) i0 = mid; else i1 = mid - 1;
+      }
+      const int64_t y = x - (ceil_sum(rq.a + i0, r) - fa);
+      const int64_t units_i = ceil_sum(rq.a + i0 + 1, r) - ceil_sum(rq.a + i0, r);
+      const int64_t take = min(units_i - y, rem);
+      x += take;
+      rem -= take;
+      Segment sg;
+      sg.t0 = rq.row0 + i0 * QT;
+      sg.nq = min(QT, rq.n - i0 * QT);
+      sg.vis0 = rq.L - rq.n + i0 * QT + 1;
+      sg.b = b;
+      sg.pad0 = sg.pad1 = 0;
+      // keys of the tile's last row, and those that have a column
+      const int64_t seen = min(static_cast<int64_t>(sg.vis0) + sg.nq - 1, p.cap);
+      const int64_t real = seen > 0 ? (seen + 127) / 128 : 0;
+      sg.j0 = static_cast<int>(y);
+      sg.nt = static_cast<int>(max(min(y + take, real) - y, static_cast<int64_t>(0)));
+      if (sg.nt == 0) continue;
+      const int k = nseg % kSegDepth;
+      if (nseg >= kSegDepth && !warp_wait(&seg_empty[k], ((nseg / kSegDepth) - 1) & 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      if (nseg >= 2 && !warp_wait(&q_empty[nseg & 1], ((nseg >> 1) - 1) & 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        segs[k] = sg;
+        mbar_arrive(&seg_full[k]);
+        mbar_arrive_expect_tx(&q_full[nseg & 1], C::kQBytes);
+#pragma unroll
+        for (int h = 0; h < HV; ++h)
+          tma_load_3d(qs + (nseg & 1) * C::kQBytes + h * kIxCols * 128, &tm_q, 128 * h, 0, sg.t0, &q_full[nseg & 1]);
+      }
+      ++nseg;
+      // page ids of the slices j SP .. (j + TG) SP - 1, one per lane, looked up a group ahead
+      auto lookup = [&](int j) -> int {
+        const int64_t kp = (static_cast<int64_t>(j) * SP + lane) * BR;
+        if (j >= sg.j0 + sg.nt || kp >= seen) return -2;                  // nothing to read
+        const int64_t col = kp / p.block_size;
+        const int id = col < p.bt_cols ? p.block_table[static_cast<int64_t>(b) * p.bt_stride + col] : -1;
+        return (id < 0 || id >= p.num_blocks) ? -1 : id;
+      };
+      int cur = lookup(sg.j0), nxt = -2;
+      for (int t = 0; t < sg.nt && ok; ++t, ++tile) {
+        const int in = t % TG;
+        if (in == 0) {
+          if (t > 0) cur = nxt;
+          nxt = lookup(sg.j0 + t + TG);
+        }
+        const int slot = static_cast<int>(tile % S), sslot = static_cast<int>(tile % SC);
+        // Tile n - S's MMAs are done, so tile n - S - 2's accumulator had been read: its scales
+        // (slot n - SC) are free as well.
+        if (tile >= S && !warp_wait(&k_empty[slot], static_cast<uint32_t>(tile / S - 1) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const int id = __shfl_sync(0xFFFFFFFFu, cur, in * SP + (lane < SP ? lane : 0));
+        const bool mine = lane < SP;
+        const uint32_t bm = __ballot_sync(0xFFFFFFFFu, mine && id == -1);
+        const uint32_t gm = __ballot_sync(0xFFFFFFFFu, mine && id >= 0);
+        if (bm) errbits |= 2u;
+        if (lane == 0) {
+          bad[sslot] = bm;
+          mbar_arrive_expect_tx(&k_full[slot], C::kTileBytes);
+          mbar_arrive_expect_tx(&sc_full[sslot], F == kFP8 ? __popc(gm) * BR * 4 : 0);
+        }
+        __syncwarp();
+        if (mine) {
+          const int64_t kp = (static_cast<int64_t>(sg.j0 + t) * SP + lane) * BR;
+          const int yy = static_cast<int>(kp % p.block_size), z = id >= 0 ? id : p.num_blocks;
+#pragma unroll
+          for (int h = 0; h < HV; ++h)
+            tma_load_3d(ring + slot * C::kTileBytes + h * 128 * 128 + lane * BR * 128, &tm_k, 128 * h, yy, z, &k_full[slot]);
+          if (F == kFP8 && id >= 0)
+            bulk_g2s(scales + sslot * 128 + lane * BR, p.key_scales + z * p.ks_stride + yy, BR * 4, &sc_full[sslot]);
+        }
+      }
+    }
+    if (ok) {      // end of the queue
+      const int k = nseg % kSegDepth;
+      if (nseg < kSegDepth || warp_wait(&seg_empty[k], ((nseg / kSegDepth) - 1) & 1, abort_flag)) {
+        if (lane == 0) {
+          Segment e{};
+          segs[k] = e;
+          mbar_arrive(&seg_full[k]);
+        }
+      }
+    }
+    // never leave copies in flight behind us
+    if (lane == 0) {
+      volatile int no_abort[2] = {0, 0};
+      for (int64_t q = tile > S ? tile - S : 0; q < tile; ++q)
+        mbar_wait(&k_full[q % S], static_cast<uint32_t>(q / S) & 1u, no_abort);
+      for (int64_t q = tile > SC ? tile - SC : 0; q < tile; ++q)
+        mbar_wait(&sc_full[q % SC], static_cast<uint32_t>(q / SC) & 1u, no_abort);
+      for (int q = nseg > 2 ? nseg - 2 : 0; q < nseg; ++q) mbar_wait(&q_full[q & 1], (q >> 1) & 1, no_abort);
+    }
+    __syncwarp();
+    if (lane == 0 && errbits) set_device_error(p.err, errbits);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint64_t dK0 = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
+      const uint64_t dQ0 = smem_desc(smem_u32(qs), 16, 1024, kSwizzle128B);
+      int64_t tile = 0;
+      bool ok = true, any = false;
+      for (int ns = 0; ok; ++ns) {
+        const int k = ns % kSegDepth;
+        if (!mbar_wait(&seg_full[k], (ns / kSegDepth) & 1, abort_flag)) break;
+        const int nt = segs[k].nt, nq = segs[k].nq;
+        mbar_arrive(&seg_empty[k]);
+        if (nt == 0) break;
+        if (!mbar_wait(&q_full[ns & 1], (ns >> 1) & 1, abort_flag)) break;
+        const int n = (nq * HP + 15) & ~15;      // columns: a multiple of 16
+        const uint32_t idesc = F == kBF16 ? idesc_f16(128, n, 1, 1, 0, 0) : idesc_e4m3(128, n, 0, 0);
+        const uint64_t dQ = desc_add(dQ0, static_cast<uint32_t>(ns & 1) * (C::kQBytes >> 4));
+        for (int t = 0; t < nt; ++t, ++tile) {
+          const int slot = static_cast<int>(tile % S), buf = static_cast<int>(tile & 1);
+          if (!mbar_wait(&k_full[slot], static_cast<uint32_t>(tile / S) & 1u, abort_flag) ||
+              (tile >= 2 && !mbar_wait(&d_empty[buf], static_cast<uint32_t>((tile >> 1) - 1) & 1u, abort_flag))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t dK = desc_add(dK0, static_cast<uint32_t>(slot) * (C::kTileBytes >> 4));
+#pragma unroll
+          for (int h = 0; h < HV; ++h)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t a = desc_add(dK, (h * 128 * 128 + kk * 32) >> 4);
+              const uint64_t bq = desc_add(dQ, (h * kIxCols * 128 + kk * 32) >> 4);
+              if (F == kBF16)
+                mma_f16_ss(tmem + buf * kIxCols, a, bq, idesc, h + kk > 0 ? 1u : 0u);
+              else
+                mma_f8_ss(tmem + buf * kIxCols, a, bq, idesc, h + kk > 0 ? 1u : 0u);
+            }
+          mma_commit(&d_full[buf]);
+          mma_commit(&k_empty[slot]);
+          if (t == nt - 1) mma_commit(&q_empty[ns & 1]);
+          any = true;
+        }
+      }
+      if (any) {      // no product is in flight when the accumulators are freed
+        volatile int no_abort[2] = {0, 0};
+        mma_commit(fin);
+        mbar_wait(fin, 0, no_abort);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const int quad = warp & 3, group = (warp - 2) >> 2;
+    const int key = 32 * quad + lane;             // TMEM lane = key of the tile
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16) + 64 * group;
+    const int bt = p.block_tokens;
+    int64_t tile = 0;
+    uint32_t uses[2] = {0, 0};                    // block maxima exchanged through red, per buffer
+    bool ok = true;
+    for (int ns = 0; ok; ++ns) {
+      const int k = ns % kSegDepth;
+      if (!warp_wait(&seg_full[k], (ns / kSegDepth) & 1, abort_flag)) break;
+      const Segment sg = segs[k];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[k]);
+      if (sg.nt == 0) break;
+      const bool has = group * QW < sg.nq;        // this group has queries
+      float w[64];
+      if (has) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          const int q = group * QW + c / HP, h = c % HP;
+          w[c] = (q < sg.nq && h < p.Hi) ? __ldg(p.weights + static_cast<int64_t>(sg.t0 + q) * p.w_stride + h) : 0.f;
+        }
+      }
+      for (int t = 0; t < sg.nt; ++t, ++tile) {
+        const int buf = static_cast<int>(tile & 1), sslot = static_cast<int>(tile % SC);
+        if (!warp_wait(&d_full[buf], static_cast<uint32_t>(tile >> 1) & 1u, abort_flag) ||
+            !warp_wait(&sc_full[sslot], static_cast<uint32_t>(tile / SC) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float v[QW];
+        bool is_bad = false;
+        if (has) {
+#pragma unroll
+          for (int q = 0; q < QW; ++q) v[q] = 0.f;
+#pragma unroll
+          for (int c0 = 0; c0 < 64; c0 += 16) {
+            float d[16];
+            tmem_ld16(tl + buf * kIxCols + c0, d);
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) v[(c0 + c) / HP] = fmaf(max_nan(d[c], 0.f), w[c0 + c], v[(c0 + c) / HP]);
+          }
+          // a key with infinities or NaN meets the zeros of the padded heads: sum the heads alone
+          if (p.Hi < HP) {
+#pragma unroll
+            for (int q = 0; q < QW; ++q) {
+              if (__any_sync(0xFFFFFFFFu, v[q] != v[q])) {
+                v[q] = 0.f;
+#pragma unroll
+                for (int c0 = 0; c0 < HP; c0 += 8) {
+                  uint32_t e[8];
+                  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                               : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3]), "=r"(e[4]), "=r"(e[5]), "=r"(e[6]), "=r"(e[7])
+                               : "r"(tl + buf * kIxCols + q * HP + c0));
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int c = 0; c < 8; ++c)
+                    if (c0 + c < p.Hi) v[q] = fmaf(max_nan(__uint_as_float(e[c]), 0.f), w[q * HP + c0 + c], v[q]);
+                }
+              }
+            }
+          }
+          if (F == kFP8) {
+            const float ks = scales[sslot * 128 + key];
+#pragma unroll
+            for (int q = 0; q < QW; ++q) v[q] *= ks;
+          }
+          is_bad = (bad[sslot] >> (key / p.BR)) & 1u;
+        }
+        // The accumulator is free once read; where warps exchange maxima below, the buffer's slot
+        // of red is too, so the release waits for that.
+        tc_fence_before();
+        __syncwarp();
+        const bool exchange = has && bt > 32;
+        if (lane == 0 && !exchange) mbar_arrive(&d_empty[buf]);
+        if (!has) continue;
+        const int64_t pos = static_cast<int64_t>(sg.j0 + t) * 128 + key;
+#pragma unroll
+        for (int q = 0; q < QW; ++q) {
+          const int qi = group * QW + q;
+          if (qi >= sg.nq) break;
+          const int64_t vis = min(static_cast<int64_t>(sg.vis0) + qi, p.cap);
+          float* row = p.scores + static_cast<int64_t>(sg.t0 + qi) * p.s_stride;
+          float val = is_bad ? -CUDART_INF_F : v[q];
+          if (bt == 1) {
+            if (pos < vis) row[pos] = val;
+            continue;
+          }
+          if (pos >= vis) val = -CUDART_INF_F;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1)
+            if (o < bt) val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, o));
+          if (!exchange) {
+            if ((lane & (bt - 1)) == 0 && pos < vis) row[pos / bt] = val;
+          } else if (lane == 0) {
+            red[(buf * 16 + group * 4 + quad) * 8 + q] = val;
+          }
+        }
+        if (exchange) {       // blocks of 64 or 128 keys: two or four warps of the group
+          uint64_t* rf = &red_full[group * 2 + buf];
+          if (lane == 0) mbar_arrive(rf);
+          const uint32_t par = uses[buf]++ & 1u;
+          const int wb = bt >> 5;                 // warps of a block; its first one joins them
+          if (quad % wb == 0) {
+            if (!warp_wait(rf, par, abort_flag)) {
+              ok = false;
+              break;
+            }
+            const int qi = group * QW + lane;
+            const int64_t vis = min(static_cast<int64_t>(sg.vis0) + qi, p.cap);
+            const int64_t p0 = static_cast<int64_t>(sg.j0 + t) * 128 + 32 * quad;
+            if (lane < QW && qi < sg.nq && p0 < vis) {
+              const float* r0 = red + (buf * 16 + group * 4 + quad) * 8 + lane;
+              float m = r0[0];
+              for (int o = 1; o < wb; ++o) m = max_nan(m, r0[8 * o]);
+              p.scores[static_cast<int64_t>(sg.t0 + qi) * p.s_stride + p0 / bt] = m;
+            }
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(&d_empty[buf]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (tid == 0 && *abort_flag == 2) set_device_error(p.err, 16u);
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int F, int HP>
+cudaError_t launch_hp(const IndexScoresParams& p, const void* tk, const void* tq, int grid, cudaStream_t stream) {
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(mla_index_scores_kernel<F, HP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             IndexCfg<F>::kAlloc);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  mla_index_scores_kernel<F, HP><<<grid, kIxThreads, IndexCfg<F>::kAlloc, stream>>>(
+      p, *static_cast<const CUtensorMap*>(tk), *static_cast<const CUtensorMap*>(tq));
+  return cudaGetLastError();
+}
+
+template <int F>
+cudaError_t launch_f(int hp, const IndexScoresParams& p, const void* tk, const void* tq, int grid, cudaStream_t stream) {
+  switch (hp) {
+    case 8: return launch_hp<F, 8>(p, tk, tq, grid, stream);
+    case 16: return launch_hp<F, 16>(p, tk, tq, grid, stream);
+    case 32: return launch_hp<F, 32>(p, tk, tq, grid, stream);
+    case 64: return launch_hp<F, 64>(p, tk, tq, grid, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_index_scores(int bf16, int hp, const IndexScoresParams& p, const void* tk, const void* tq, int grid,
+                                cudaStream_t stream) {
+  return bf16 ? launch_f<kBF16>(hp, p, tk, tq, grid, stream) : launch_f<kFP8>(hp, p, tk, tq, grid, stream);
+}
+
+}  // namespace mla
