@@ -496,9 +496,9 @@ MLA_API int mla_index_scores(const void* q, int64_t q_s0, int64_t q_s1, const fl
 /*
  * The topk best-scored blocks of every row, exactly: the largest scores, ties to the lowest index;
  * -inf and NaN are never taken.  The first `first` and the last `last` visible blocks of a row are
- * taken whatever their scores (first + last <= topk).
+ * taken whatever their scores (first + last <= topk).  1 <= topk <= 8192.
  *
- *   scores       device fp32 [T, width], row stride s_stride; columns past a row's visible blocks,
+ *   scores       device fp32 [T, width], width < 2^30, row stride s_stride; columns past a row's visible blocks,
  *                ceil(visible tokens / block_tokens), are not read.
  *   blocks       device out int32 [T, topk], row stride b_stride: block indices in ascending order,
  *                then -1.

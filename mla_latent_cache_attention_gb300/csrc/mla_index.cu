@@ -205,35 +205,213 @@ __global__ void __launch_bounds__(128) mla_index_gather_kernel(const IndexGather
 }
 
 // ------------------------------------------------------------------------------------------
-// Selection.  A score becomes a 32-bit key whose unsigned order is the scores' (0 = never taken:
-// -inf and NaN; all ones: a forced block), so the k-th largest key is found digit by digit
-// (11 + 11 + 10 bits) from histograms of the keys that match the digits so far.  A last pass in
-// index order takes every larger key and the first ones of those that equal it: ties go to the
-// lowest index, the list comes out ascending, and nothing depends on the order of atomics.
-constexpr int kSelThreads = 1024;
+// Selection.  A score becomes a 32-bit key whose unsigned order is the scores'; all ones is a forced
+// block, and -inf and NaN, which are never taken, have none.  Every score is read once: a CTA streams
+// its row (or its part of it) in index order and keeps those above the topk-th largest so far in a
+// list in shared memory.  An equal score later in the row has the higher index and loses the tie, so
+// "above" is enough.  When a chunk might not fit, the list is cut to its exact topk, which raises the
+// bound; of n scores in random order about topk (1 + ln(n / topk)) enter the list, and an ascending
+// row, the worst one, only costs more cuts.  The list keeps the row's order, so it comes out
+// ascending, and no result depends on the order of atomics.
+//
+// The cut finds the topk-th largest key from histograms of 2048 bins that divide the keys' own
+// range evenly: bins by leading bits would put scores of similar size into a few of them.
+//
+// Long rows in small batches are shared by a cluster: every CTA takes a part, the histograms of the
+// last cut are summed over the cluster, and every CTA writes its part's share.
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelPer = 8;                               // scores a thread takes from a chunk
+constexpr int kSelChunk = kSelThreads * kSelPer;
+constexpr int kSelBins = 2048;
+constexpr int kSelFixed = kSelBins * 4 + 512;
+constexpr uint32_t kForced = 0xFFFFFFFFu;
 
-struct SelRow {
-  const float* x;
-  int64_t n;               // visible blocks
-  int64_t lo, hi;          // forced: below lo, from hi on
-};
+// Shared memory of a row with topk: the list (topk + a chunk), a copy of topk entries for the cut.
+__host__ __device__ constexpr int64_t select_smem(int64_t topk) { return kSelFixed + (2 * topk + kSelChunk) * 8; }
 
-__device__ __forceinline__ uint32_t select_key(const SelRow& r, int64_t i) {
-  if (i >= r.n) return 0u;
-  if (i < r.lo || i >= r.hi) return 0xFFFFFFFFu;
-  const float f = r.x[i] + 0.f;          // -0 and +0 are equal
-  const uint32_t u = __float_as_uint(f);
-  const uint32_t key = u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
-  return (f != f || key < 0x00800000u) ? 0u : min(key, 0xFFFFFFFEu);
+__device__ __forceinline__ uint32_t score_key(float f) {        // f neither NaN nor -inf
+  const uint32_t u = __float_as_uint(f + 0.f);                  // -0 and +0 are equal
+  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float key_score(uint32_t key) {
+  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-__global__ void __launch_bounds__(kSelThreads) mla_index_select_kernel(const IndexSelectParams p) {
-  __shared__ uint32_t hist[2048];
-  __shared__ uint32_t wsum[32];
-  __shared__ int64_t srow[2];
-  __shared__ uint32_t sdig[3];       // digit, keys above it, keys in it
+struct SelShared {
+  uint32_t* hist;          // [kSelBins]
+  uint32_t* wsum;          // [2][kSelWarps]
+  uint32_t* stat;          // [4] smallest key, largest key, count of this CTA's list; spare
+  uint32_t* found;         // [4] bin, keys above it, keys in it
+};
+
+// The value at the same shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(p, rank)) : "memory");
+  return v;
+}
+
+// Keys above *thr are the list's k largest unforced ones, together with the first *ties that equal
+// it.  With ranks > 1 the list is that of all CTAs of the cluster.
+__device__ void find_threshold(const uint32_t* keys, int m, uint32_t k, int ranks, const SelShared& s, uint32_t* thr,
+                               uint32_t* ties) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int t = blockIdx.x;
+  uint32_t lo = kForced, hi = 0, n = 0;
+  for (int i = tid; i < m; i += kSelThreads) {
+    const uint32_t key = keys[i];
+    if (key != kForced) {
+      lo = min(lo, key);
+      hi = max(hi, key);
+      ++n;
+    }
+  }
+  lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+  hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+  n = __reduce_add_sync(0xFFFFFFFFu, n);
+  if (tid == 0) s.stat[0] = kForced, s.stat[1] = 0, s.stat[2] = 0;
+  __syncthreads();
+  if (lane == 0) {
+    atomicMin(&s.stat[0], lo);
+    atomicMax(&s.stat[1], hi);
+    atomicAdd(&s.stat[2], n);
+  }
+  __syncthreads();
+  if (ranks == 1) {
+    lo = s.stat[0], hi = s.stat[1], n = s.stat[2];
+  } else {
+    cluster_sync();
+    lo = kForced, hi = 0, n = 0;
+    for (int r = 0; r < ranks; ++r) {
+      lo = min(lo, ld_cluster_u32(&s.stat[0], r));
+      hi = max(hi, ld_cluster_u32(&s.stat[1], r));
+      n += ld_cluster_u32(&s.stat[2], r);
+    }
+  }
+  *ties = 0;
+  if (n <= k) {
+    *thr = 0;
+    if (ranks > 1) cluster_sync();      // the others have read stat
+    return;
+  }
+  uint32_t left = k, range = hi - lo;
+  if (k == 0) {
+    *thr = hi;
+    if (ranks > 1) cluster_sync();
+    return;
+  }
+  for (;;) {
+    const int bits = 32 - __clz(range), shift = bits > 11 ? bits - 11 : 0;
+    reinterpret_cast<uint4*>(s.hist)[tid] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for (int i = tid; i < m; i += kSelThreads) {
+      const uint32_t d = keys[i] - lo;
+      if (keys[i] >= lo && d <= range && keys[i] != kForced) atomicAdd(&s.hist[d >> shift], 1u);
+    }
+    __syncthreads();
+    // counts from the top: thread q has bins 2047 - 4 q .. 2044 - 4 q
+    uint4 c = make_uint4(0, 0, 0, 0);
+    if (ranks == 1) {
+      c = reinterpret_cast<const uint4*>(s.hist)[kSelThreads - 1 - tid];
+    } else {
+      cluster_sync();
+      for (int r = 0; r < ranks; ++r) {
+        const uint4 v = ld_cluster_v4(mapa_shared(s.hist + 4 * (kSelThreads - 1 - tid), r));
+        c.x += v.x, c.y += v.y, c.z += v.z, c.w += v.w;
+      }
+    }
+    const uint32_t own = c.x + c.y + c.z + c.w;
+    uint32_t inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) s.wsum[warp] = inc;
+    __syncthreads();
+    uint32_t before = inc - own;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w)
+      if (w < warp) before += s.wsum[w];
+    if (before < left && left <= before + own) {       // exactly one thread
+      uint32_t bin = kSelBins - 1 - 4 * tid, cnt = c.w;
+      if (left > before + cnt) before += cnt, --bin, cnt = c.z;
+      if (left > before + cnt) before += cnt, --bin, cnt = c.y;
+      if (left > before + cnt) before += cnt, --bin, cnt = c.x;
+      s.found[0] = bin;
+      s.found[1] = before;
+      s.found[2] = cnt;
+    }
+    __syncthreads();
+    if (ranks > 1) cluster_sync();      // the others have read hist (and stat)
+    left -= s.found[1];
+    lo += s.found[0] << shift;
+    if (s.found[2] == left) {           // the whole bin is taken
+      *thr = lo - 1;
+      return;
+    }
+    if (shift == 0) {
+      *thr = lo;
+      *ties = left;
+      return;
+    }
+    range = (1u << shift) - 1;
+  }
+}
+
+// In list order: put(position, entry) for every taken entry, positions from (g0 larger, e0 equal) on;
+// returns the list's own counts (larger | equal << 16).
+template <class Put>
+__device__ __forceinline__ uint32_t take_in_order(const uint32_t* keys, int m, uint32_t thr, uint32_t ties, uint32_t* wsum,
+                                                  uint32_t g0, uint32_t e0, bool count_only, Put put) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int span = ((m + kSelWarps - 1) / kSelWarps + 31) & ~31, from = warp * span, to = min(m, from + span);
+  uint32_t cnt = 0;
+  for (int i0 = from; i0 < to; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t key = i < to ? keys[i] : 0u;
+    cnt += __popc(__ballot_sync(0xFFFFFFFFu, i < to && key > thr)) | (__popc(__ballot_sync(0xFFFFFFFFu, i < to && key == thr)) << 16);
+  }
+  if (lane == 0) wsum[warp] = cnt;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) {
+    const uint32_t v = wsum[w];
+    if (w < warp) before += v;
+    all += v;
+  }
+  if (!count_only) {
+    uint32_t g = g0 + (before & 0xFFFFu), e = e0 + (before >> 16);
+    const uint32_t lt = (1u << lane) - 1;
+    for (int i0 = from; i0 < to; i0 += 32) {
+      const int i = i0 + lane;
+      const uint32_t key = i < to ? keys[i] : 0u;
+      const bool gt = i < to && key > thr, eq = i < to && key == thr;
+      const uint32_t bg = __ballot_sync(0xFFFFFFFFu, gt), be = __ballot_sync(0xFFFFFFFFu, eq);
+      const uint32_t eb = e + __popc(be & lt);
+      if (gt || (eq && eb < ties)) put(static_cast<int>(g + __popc(bg & lt) + min(eb, ties)), i);
+      g += __popc(bg);
+      e += __popc(be);
+    }
+  }
+  __syncthreads();
+  return all;
+}
+
+__global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const IndexSelectParams p, int ranks) {
+  extern __shared__ __align__(16) uint32_t sel_smem[];
+  SelShared s;
+  s.hist = sel_smem;
+  s.wsum = s.hist + kSelBins;
+  s.stat = s.wsum + 2 * kSelWarps;
+  s.found = s.stat + 4;
+  int64_t* srow = reinterpret_cast<int64_t*>(s.found + 4);       // [2]
+  uint32_t* keys = sel_smem + kSelFixed / 4;
+  uint32_t* idx = keys + p.topk + kSelChunk;
+  uint32_t* copy = idx + p.topk + kSelChunk;                     // [2][topk]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int t = blockIdx.x / ranks, rank = blockIdx.x % ranks;
   if (tid == 0) {
     int64_t vis = 0;
     srow[0] = row_request(p.cu_q, p.seq_lens, p.B, t, &vis);
@@ -242,101 +420,159 @@ __global__ void __launch_bounds__(kSelThreads) mla_index_select_kernel(const Ind
   __syncthreads();
   const int b = static_cast<int>(srow[0]);
   const int64_t vis = srow[1];
-  if (b < 0) return;
-  SelRow r;
-  r.x = p.scores + t * p.s_stride;
-  r.n = min((vis + p.block_tokens - 1) / p.block_tokens, p.width);
-  r.lo = p.first;
-  r.hi = r.n - p.last;
+  if (b < 0) return;       // every CTA of the cluster
+  const float* __restrict__ x = p.scores + t * p.s_stride;
+  const int n = static_cast<int>(min((vis + p.block_tokens - 1) / p.block_tokens, p.width));
+  const int f_lo = min(p.first, n), f_hi = max(f_lo, n - p.last);      // forced: below f_lo, from f_hi on
+  const uint32_t kk = p.topk - (f_lo + n - f_hi);                // places of the others
+  const int part = ((n + ranks - 1) / ranks + 3) & ~3;
+  const int from = min(n, rank * part), to = min(n, from + part);
+  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
+
+  // ---- stream: a warp takes 32 * kSelPer neighbouring scores of a chunk, 4 a lane and load
+  float cur[kSelPer], nxt[kSelPer];
+  auto load = [&](int c0, float (&v)[kSelPer]) {
+#pragma unroll
+    for (int j = 0; j < kSelPer / 4; ++j) {
+      const int i = c0 + warp * 32 * kSelPer + j * 128 + 4 * lane;
+      if (vec && i + 3 < to) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(x + i));
+        v[4 * j] = w.x, v[4 * j + 1] = w.y, v[4 * j + 2] = w.z, v[4 * j + 3] = w.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * j + e] = i + e < to ? __ldg(x + i + e) : CUDART_NAN_F;
+      }
+    }
+  };
+  int m = 0, flip = 0;
+  float bound = -CUDART_INF_F;
+  load(from, cur);
+  for (int c0 = from; c0 < to; c0 += kSelChunk) {
+    load(c0 + kSelChunk, nxt);
+    const bool forced_here = c0 < f_lo || c0 + kSelChunk > f_hi;
+    for (;;) {
+      // scores above the bound; NaN is not, and -inf is above nothing
+      uint32_t take = 0;
+#pragma unroll
+      for (int j = 0; j < kSelPer; ++j) take |= (cur[j] > bound ? 1u : 0u) << j;
+      if (forced_here) {
+#pragma unroll
+        for (int j = 0; j < kSelPer; ++j) {
+          const int i = c0 + warp * 32 * kSelPer + (j >> 2) * 128 + 4 * lane + (j & 3);
+          if (i < to && (i < f_lo || i >= f_hi)) take |= 1u << j;
+        }
+      }
+      // ranks in row order: load by load, lane by lane, then the lane's four
+      uint32_t at[kSelPer / 4], cnt = 0;
+#pragma unroll
+      for (int j = 0; j < kSelPer / 4; ++j) {
+        const uint32_t mine = (take >> (4 * j)) & 15u;
+        uint32_t inc = __popc(mine);
+        if (__any_sync(0xFFFFFFFFu, inc)) {
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += v;
+          }
+          at[j] = cnt + inc - __popc(mine);
+          cnt += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        } else {
+          at[j] = cnt;
+        }
+      }
+      uint32_t* ws = s.wsum + flip * kSelWarps;
+      flip ^= 1;
+      if (lane == 0) ws[warp] = cnt;
+      __syncthreads();
+      uint32_t before = m, all = 0;
+#pragma unroll
+      for (int w = 0; w < kSelWarps; ++w) {
+        const uint32_t v = ws[w];
+        if (w < warp) before += v;
+        all += v;
+      }
+      if (m + static_cast<int>(all) <= p.topk + kSelChunk) {
+#pragma unroll
+        for (int j = 0; j < kSelPer; ++j) {
+          if (!((take >> j) & 1u)) continue;
+          const int i = c0 + warp * 32 * kSelPer + (j >> 2) * 128 + 4 * lane + (j & 3);
+          const uint32_t pos = before + at[j >> 2] + __popc((take >> (4 * (j >> 2))) & ((1u << (j & 3)) - 1));
+          keys[pos] = i < f_lo || i >= f_hi ? kForced : score_key(cur[j]);
+          idx[pos] = i;
+        }
+        m += all;
+        break;
+      }
+      // cut the list to its topk, then take the chunk again
+      __syncthreads();
+      uint32_t thr, ties;
+      find_threshold(keys, m, kk, 1, s, &thr, &ties);
+      const uint32_t got = take_in_order(keys, m, thr, ties, s.wsum, 0, 0, false, [&](int pos, int i) {
+        copy[pos] = keys[i];
+        copy[p.topk + pos] = idx[i];
+      });
+      m = static_cast<int>((got & 0xFFFFu) + min(got >> 16, ties));
+      for (int i = tid; i < m; i += kSelThreads) {
+        keys[i] = copy[i];
+        idx[i] = copy[p.topk + i];
+      }
+      // everything kept equals the bound or is above it (thr itself when ties were cut, else the next
+      // key): a later score has to be above thr
+      bound = thr == 0 ? bound : kk == 0 ? CUDART_INF_F : key_score(thr);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < kSelPer; ++j) cur[j] = nxt[j];
+  }
+  __syncthreads();
+
+  // ---- the last cut, over the row
+  uint32_t thr, ties;
+  find_threshold(keys, m, kk, ranks, s, &thr, &ties);
   int32_t* out = p.blocks + t * p.b_stride;
   int32_t* out_slots = p.slots ? p.slots + t * p.sl_stride : nullptr;
-
-  // ---- the k-th largest key: keys above `thr` are taken, and the first `ties` that equal it
-  uint32_t thr = 0, ties = 0;
-  if (r.n > p.topk) {
-    uint32_t left = p.topk, prefix = 0;
-    for (int d = 0; d < 3; ++d) {
-      const int bits = d < 2 ? 11 : 10, shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = 1 << bits;
-      const int above = shift + bits;            // the digits found so far
-      for (int i = tid; i < bins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
-      for (int64_t i = tid; i < r.n; i += kSelThreads) {
-        const uint32_t key = select_key(r, i);
-        if (d == 0 || (key >> above) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
-      }
-      __syncthreads();
-      // suffix sums, two bins a thread from the top: thread q holds bins - 1 - 2q and the next
-      const int hi_bin = bins - 1 - 2 * tid;
-      const uint32_t c0 = hi_bin >= 0 ? hist[hi_bin] : 0, c1 = hi_bin > 0 ? hist[hi_bin - 1] : 0;
-      uint32_t inc = c0 + c1;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      if (lane == 31) wsum[warp] = inc;
-      __syncthreads();
-      uint32_t base = 0;
-      for (int w = 0; w < warp; ++w) base += wsum[w];
-      const uint32_t upto = base + inc, before = upto - c0 - c1;
-      if (before < left && left <= upto) {       // exactly one thread
-        const bool first = left <= before + c0;
-        sdig[0] = static_cast<uint32_t>(first ? hi_bin : hi_bin - 1);
-        sdig[1] = first ? before : before + c0;
-        sdig[2] = first ? c0 : c1;
-      }
-      __syncthreads();
-      prefix = (prefix << bits) | sdig[0];
-      left -= sdig[1];
+  const bool one = p.block_tokens == 1;
+  auto slot_of = [&](int64_t pos) -> int32_t {
+    if (pos >= vis) return -1;
+    const int64_t col = pos / p.page_size;
+    const int64_t id = col < p.bt_cols ? p.block_table[b * p.bt_stride + col] : -1;
+    if (id < 0 || id >= p.num_blocks) {
+      set_device_error(p.err, 2u);
+      return -1;
     }
-    thr = prefix;
-    ties = left;
-    if (thr == 0) ties = 0;      // fewer candidates than topk: keys of 0 are never taken
+    return static_cast<int32_t>(id * p.page_size + pos % p.page_size);
+  };
+  uint32_t g0 = 0, e0 = 0, g_all = 0, e_all = 0;
+  auto put = [&](int pos, int i) {
+    const int32_t c = static_cast<int32_t>(idx[i]);
+    out[pos] = c;
+    if (out_slots && one) out_slots[pos] = slot_of(c);
+    if (out_slots && !one)
+      for (int u = 0; u < p.block_tokens; ++u)
+        out_slots[static_cast<int64_t>(pos) * p.block_tokens + u] = slot_of(static_cast<int64_t>(c) * p.block_tokens + u);
+  };
+  if (ranks > 1) {
+    const uint32_t mine = take_in_order(keys, m, thr, ties, s.wsum, 0, 0, true, put);
+    if (tid == 0) s.stat[3] = mine;
+    cluster_sync();
+    for (int r = 0; r < ranks; ++r) {
+      const uint32_t v = ld_cluster_u32(&s.stat[3], r);
+      if (r < rank) g0 += v & 0xFFFFu, e0 += v >> 16;
+      g_all += v & 0xFFFFu, e_all += v >> 16;
+    }
+    cluster_sync();       // no CTA leaves while another may read its counts
+    take_in_order(keys, m, thr, ties, s.wsum, g0, e0, false, put);
+  } else {
+    const uint32_t v = take_in_order(keys, m, thr, ties, s.wsum, 0, 0, false, put);
+    g_all = v & 0xFFFFu, e_all = v >> 16;
   }
-
-  // ---- in index order: positions by prefix sums over (larger, equal)
-  uint32_t gt0 = 0, eq0 = 0;     // taken before this chunk
-  for (int64_t c0 = 0; c0 < r.n; c0 += kSelThreads) {
-    const int64_t i = c0 + tid;
-    const uint32_t key = select_key(r, i);
-    const bool gt = key > thr, eq = key == thr && thr != 0;
-    const uint32_t bg = __ballot_sync(0xFFFFFFFFu, gt), be = __ballot_sync(0xFFFFFFFFu, eq);
-    if (lane == 0) wsum[warp] = __popc(bg) | (__popc(be) << 16);
-    __syncthreads();
-    uint32_t before = 0, all = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      if (w < warp) before += wsum[w];
-      all += wsum[w];
-    }
-    const uint32_t lt = (1u << lane) - 1;
-    const uint32_t g = gt0 + (before & 0xFFFF) + __popc(bg & lt);
-    const uint32_t e = eq0 + (before >> 16) + __popc(be & lt);
-    if (gt || (eq && e < ties)) out[g + min(e, ties)] = static_cast<int32_t>(i);
-    gt0 += all & 0xFFFF;
-    eq0 += all >> 16;
-    __syncthreads();
-  }
-  const int taken = static_cast<int>(gt0 + min(eq0, ties));
-  for (int i = taken + tid; i < p.topk; i += kSelThreads) out[i] = -1;
-  if (!out_slots) return;
-  // ---- token slots of the taken blocks through the block table
-  __syncthreads();
-  const int64_t total = static_cast<int64_t>(p.topk) * p.block_tokens;
-  for (int64_t i = tid; i < total; i += kSelThreads) {
-    const int j = static_cast<int>(i / p.block_tokens);
-    int32_t slot = -1;
-    if (j < taken) {
-      const int64_t pos = static_cast<int64_t>(out[j]) * p.block_tokens + i % p.block_tokens;
-      if (pos < vis) {
-        const int64_t col = pos / p.page_size;
-        const int64_t id = col < p.bt_cols ? p.block_table[b * p.bt_stride + col] : -1;
-        if (id < 0 || id >= p.num_blocks)
-          set_device_error(p.err, 2u);
-        else
-          slot = static_cast<int32_t>(id * p.page_size + pos % p.page_size);
-      }
-    }
-    out_slots[i] = slot;
+  // ---- -1 after the list
+  const int taken = static_cast<int>(g_all + min(e_all, ties));
+  for (int i = taken + rank * kSelThreads + tid; i < p.topk; i += ranks * kSelThreads) out[i] = -1;
+  if (out_slots) {
+    const int64_t all = static_cast<int64_t>(p.topk) * p.block_tokens;
+    for (int64_t i = static_cast<int64_t>(taken) * p.block_tokens + rank * kSelThreads + tid; i < all; i += ranks * kSelThreads)
+      out_slots[i] = -1;
   }
 }
 
@@ -404,10 +640,34 @@ cudaError_t launch_index_gather(int bf16, const IndexGatherParams& p, cudaStream
   return cudaGetLastError();
 }
 
+static_assert(select_smem(kSelectMaxTopk) <= 227 * 1024, "shared memory budget");
+
 cudaError_t launch_index_select(const IndexSelectParams& p, int sms, cudaStream_t stream) {
-  (void)sms;
-  mla_index_select_kernel<<<p.T, kSelThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(mla_index_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  // CTAs that share a row: while the batch leaves SMs idle and a part keeps two chunks
+  int ranks = 1;
+  while (ranks < 8 && static_cast<int64_t>(p.T) * ranks * 2 <= 2 * sms && p.width / (ranks * 2) >= 2 * kSelChunk) ranks *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.T) * ranks);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(select_smem(p.topk));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mla_index_select_kernel, p, ranks);
 }
 
 cudaError_t launch_page_list(const PageListParams& p, cudaStream_t stream) {

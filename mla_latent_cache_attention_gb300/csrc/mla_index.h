@@ -7,6 +7,7 @@
 
 namespace mla {
 
+constexpr int kSelectMaxTopk = 8192;
 constexpr int kIndexDim = 128;    // values of an index query or key: [nope (64) | rope (64)]
 
 // Decode / prefill epilogue of the selector: index queries and keys rotated, quantised, inserted.

@@ -219,9 +219,10 @@ extern "C" int mla_index_select(const float* scores, int64_t s_stride, int64_t w
   if (int rc = check_rows(B, T, cu_q_lens)) return rc;
   if (block_tokens < 1) return fail(MLA_ERR_INVALID, "block_tokens must be >= 1, got %d", block_tokens);
   if (topk < 1) return fail(MLA_ERR_INVALID, "topk must be >= 1, got %d", topk);
+  if (topk > kSelectMaxTopk) return fail(MLA_ERR_UNSUPPORTED, "topk must be <= %d, got %d", kSelectMaxTopk, topk);
   if (first < 0 || last < 0 || static_cast<int64_t>(first) + last > topk)
     return fail(MLA_ERR_INVALID, "first and last must be >= 0 and fit in topk");
-  if (width < 0 || width >= (int64_t(1) << 31)) return fail(MLA_ERR_UNSUPPORTED, "width must be in [0, 2^31)");
+  if (width < 0 || width >= (int64_t(1) << 30)) return fail(MLA_ERR_UNSUPPORTED, "width must be in [0, 2^30)");
   if (B == 0 || T == 0) return ok();
   if (!scores || !seq_lens || !blocks) return fail(MLA_ERR_INVALID, "a required pointer is NULL");
   if (s_stride < width || !aligned(scores, 4)) return fail(MLA_ERR_INVALID, "bad scores rows");

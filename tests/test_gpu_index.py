@@ -686,3 +686,31 @@ def test_problems_of_size_zero(m):
     m.index_scores(z(2, 4, 128, dt=u8), z(2, 4), z(2, 16, 128, dt=u8), z(2, 16), z(2, 3, dt=i32), t_i32([0, 0]), fmt="fp8", max_context=8)
     torch.cuda.synchronize()
     assert m.read_device_errors() == 0
+
+
+@pytest.mark.parametrize("n,k", [(200000, 8192), (9000, 8192), (300001, 2048), (65536, 1), (33000, 4000)])
+@pytest.mark.parametrize("order", ["random", "ascending", "descending", "late"])
+def test_select_long_rows_in_every_order(m, n, k, order):
+    """Few rows: the row is shared by several CTAs.  Ascending scores cut the running list most often."""
+    rng = np.random.default_rng(n)
+    x = rng.standard_normal(n).astype(np.float32)
+    if order != "random":
+        x = np.sort(x) if order != "descending" else -np.sort(x)
+    if order == "late":
+        x[: n - n // 3] = x[0]
+    check_select(m, np.stack([x, np.round(x * 4)]), [n, n - 1], [1, 1], 1, k, first=min(2, k), last=0)
+
+
+@pytest.mark.parametrize("offset", [0, 1, 3])
+def test_select_rows_off_the_16_byte_grid(m, offset):
+    rng = np.random.default_rng(offset)
+    x = rng.standard_normal((3, 9001 + 4)).astype(np.float32)
+    t = f32(x)[:, offset:offset + 9001]
+    got, _ = m.index_select(t, t_i32([9001, 500, 9000]), 100)
+    want, _, _ = ref.select(x[:, offset:offset + 9001], [9001, 500, 9000], np.arange(4), 1, 100, 0, 0)
+    assert np.array_equal(got.cpu().numpy(), want)
+
+
+def test_select_topk_limit(m):
+    with pytest.raises(m.MLAError, match="topk must be"):
+        m.index_select(torch.zeros((1, 10), device="cuda"), t_i32([10]), 8193)
