@@ -205,45 +205,50 @@ __global__ void __launch_bounds__(128) mla_index_gather_kernel(const IndexGather
 }
 
 // ------------------------------------------------------------------------------------------
-// Selection.  A score becomes a 32-bit key whose unsigned order is the scores'; all ones is a forced
-// block, and -inf and NaN, which are never taken, have none.  Every score is read once: a CTA streams
-// its row (or its part of it) in index order and keeps those above the topk-th largest so far in a
-// list in shared memory.  An equal score later in the row has the higher index and loses the tie, so
-// "above" is enough.  When a chunk might not fit, the list is cut to its exact topk, which raises the
-// bound; of n scores in random order about topk (1 + ln(n / topk)) enter the list, and an ascending
-// row, the worst one, only costs more cuts.  The list keeps the row's order, so it comes out
-// ascending, and no result depends on the order of atomics.
+// Selection.  A score becomes a 32-bit key whose unsigned order is the scores'.  A row is streamed
+// once: a bound, taken from 4096 scores spread over the row so that it almost surely lies a little
+// below the topk-th largest, lets some topk (1 + a few standard deviations of the sample's rank) of
+// them into a list in shared memory.  The exact cut is made in the list: the topk-th largest key
+// from histograms of 2048 bins that divide the keys' own range evenly (bins by leading bits would
+// put scores of similar size into a few of them), and among keys that equal it the lowest indices, by
+// the same search over the indices.  The taken indices then become bits of a map of the row, whose
+// prefix counts give their ascending positions.  No result depends on the order of atomics.
 //
-// The cut finds the topk-th largest key from histograms of 2048 bins that divide the keys' own
-// range evenly: bins by leading bits would put scores of similar size into a few of them.
+// Where the bound lets in too few or too many (ties, or a row that repeats with the sample's stride)
+// the row is streamed again in order, and whenever the list is full it is cut to its exact topk, which
+// raises the bound; a later equal score has the higher index, so "above the bound" is enough.
 //
-// Long rows in small batches are shared by a cluster: every CTA takes a part, the histograms of the
-// last cut are summed over the cluster, and every CTA writes its part's share.
+// Long rows in small batches are shared by a cluster: every CTA streams a part, the histograms of the
+// cut are summed over the cluster, and every CTA writes its part's share.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelPer = 8;                               // scores a thread takes from a chunk
-constexpr int kSelChunk = kSelThreads * kSelPer;
+constexpr int kSelSample = 4096;
+constexpr int kSelChunk = 4096;                          // list entries beyond topk; scores of an ordered round
 constexpr int kSelBins = 2048;
-constexpr int kSelFixed = kSelBins * 4 + 512;
-constexpr uint32_t kForced = 0xFFFFFFFFu;
+constexpr int kSelFixed = kSelBins * 4 + 256;
 
-// Shared memory of a row with topk: the list (topk + a chunk), a copy of topk entries for the cut.
+// Shared memory of a row with topk: the list (topk + a chunk), a copy of topk entries for a cut.
 __host__ __device__ constexpr int64_t select_smem(int64_t topk) { return kSelFixed + (2 * topk + kSelChunk) * 8; }
 
-__device__ __forceinline__ uint32_t score_key(float f) {        // f neither NaN nor -inf
+__device__ __forceinline__ uint32_t score_key(float f) {        // f neither NaN nor -inf: at least 0x00800000
   const uint32_t u = __float_as_uint(f + 0.f);                  // -0 and +0 are equal
   return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 __device__ __forceinline__ float key_score(uint32_t key) {
   return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
+constexpr uint32_t kForcedKey = 0xFFFFFFFFu;
 
 struct SelShared {
-  uint32_t* hist;          // [kSelBins]
-  uint32_t* wsum;          // [2][kSelWarps]
-  uint32_t* stat;          // [4] smallest key, largest key, count of this CTA's list; spare
-  uint32_t* found;         // [4] bin, keys above it, keys in it
+  uint32_t hist[kSelBins];        // histogram, or the map of 65536 indices
+  uint32_t wsum[kSelWarps];
+  uint32_t stat[4];               // smallest key, largest key, their number, entries taken
+  uint32_t found[4];              // bin, keys above it, keys in it
+  uint32_t count;                 // entries of the list
+  uint32_t pad;
+  int64_t row[2];
 };
+static_assert(sizeof(SelShared) <= kSelFixed, "shared memory layout");
 
 // The value at the same shared-memory address in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t rank) {
@@ -252,15 +257,36 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t r
   return v;
 }
 
-// Keys above *thr are the list's k largest unforced ones, together with the first *ties that equal
-// it.  With ranks > 1 the list is that of all CTAs of the cluster.
-__device__ void find_threshold(const uint32_t* keys, int m, uint32_t k, int ranks, const SelShared& s, uint32_t* thr,
-                               uint32_t* ties) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t lo = kForced, hi = 0, n = 0;
+// Exclusive prefix of `own` over the threads of the CTA (two barriers).
+__device__ __forceinline__ uint32_t block_prefix(uint32_t own, uint32_t* wsum) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) wsum[warp] = inc;
+  __syncthreads();
+  uint32_t w = lane < warp ? wsum[lane & (kSelWarps - 1)] : 0u;       // warp <= 15
+  w = __reduce_add_sync(0xFFFFFFFFu, w);
+  __syncthreads();
+  return w + inc - own;
+}
+
+struct Cut {
+  uint32_t thr, ties;      // keys above thr, and `ties` of those that equal it
+};
+
+// The k largest of the keys val(0) .. val(m - 1) (0: none); with ranks > 1 of all CTAs' together.
+// `exact` false: the bin that holds the k-th largest is taken whole (at least k keys above thr).
+template <class Val>
+__device__ Cut find_cut(int m, uint32_t k, int ranks, bool exact, SelShared& s, Val val) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0, n = 0;
   for (int i = tid; i < m; i += kSelThreads) {
-    const uint32_t key = keys[i];
-    if (key != kForced) {
+    const uint32_t key = val(i);
+    if (key) {
       lo = min(lo, key);
       hi = max(hi, key);
       ++n;
@@ -269,7 +295,8 @@ __device__ void find_threshold(const uint32_t* keys, int m, uint32_t k, int rank
   lo = __reduce_min_sync(0xFFFFFFFFu, lo);
   hi = __reduce_max_sync(0xFFFFFFFFu, hi);
   n = __reduce_add_sync(0xFFFFFFFFu, n);
-  if (tid == 0) s.stat[0] = kForced, s.stat[1] = 0, s.stat[2] = 0;
+  __syncthreads();
+  if (tid == 0) s.stat[0] = 0xFFFFFFFFu, s.stat[1] = 0, s.stat[2] = 0;
   __syncthreads();
   if (lane == 0) {
     atomicMin(&s.stat[0], lo);
@@ -281,32 +308,24 @@ __device__ void find_threshold(const uint32_t* keys, int m, uint32_t k, int rank
     lo = s.stat[0], hi = s.stat[1], n = s.stat[2];
   } else {
     cluster_sync();
-    lo = kForced, hi = 0, n = 0;
+    lo = 0xFFFFFFFFu, hi = 0, n = 0;
     for (int r = 0; r < ranks; ++r) {
       lo = min(lo, ld_cluster_u32(&s.stat[0], r));
       hi = max(hi, ld_cluster_u32(&s.stat[1], r));
       n += ld_cluster_u32(&s.stat[2], r);
     }
+    cluster_sync();      // every CTA has read the others'
   }
-  *ties = 0;
-  if (n <= k) {
-    *thr = 0;
-    if (ranks > 1) cluster_sync();      // the others have read stat
-    return;
-  }
+  if (n <= k) return Cut{0u, 0u};
+  if (k == 0) return Cut{hi, 0u};
   uint32_t left = k, range = hi - lo;
-  if (k == 0) {
-    *thr = hi;
-    if (ranks > 1) cluster_sync();
-    return;
-  }
   for (;;) {
     const int bits = 32 - __clz(range), shift = bits > 11 ? bits - 11 : 0;
     reinterpret_cast<uint4*>(s.hist)[tid] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     for (int i = tid; i < m; i += kSelThreads) {
-      const uint32_t d = keys[i] - lo;
-      if (keys[i] >= lo && d <= range && keys[i] != kForced) atomicAdd(&s.hist[d >> shift], 1u);
+      const uint32_t key = val(i);
+      if (key >= lo && key - lo <= range) atomicAdd(&s.hist[(key - lo) >> shift], 1u);
     }
     __syncthreads();
     // counts from the top: thread q has bins 2047 - 4 q .. 2044 - 4 q
@@ -321,18 +340,7 @@ __device__ void find_threshold(const uint32_t* keys, int m, uint32_t k, int rank
       }
     }
     const uint32_t own = c.x + c.y + c.z + c.w;
-    uint32_t inc = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) s.wsum[warp] = inc;
-    __syncthreads();
-    uint32_t before = inc - own;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w)
-      if (w < warp) before += s.wsum[w];
+    uint32_t before = block_prefix(own, s.wsum);
     if (before < left && left <= before + own) {       // exactly one thread
       uint32_t bin = kSelBins - 1 - 4 * tid, cnt = c.w;
       if (left > before + cnt) before += cnt, --bin, cnt = c.z;
@@ -343,83 +351,63 @@ __device__ void find_threshold(const uint32_t* keys, int m, uint32_t k, int rank
       s.found[2] = cnt;
     }
     __syncthreads();
-    if (ranks > 1) cluster_sync();      // the others have read hist (and stat)
+    if (ranks > 1) cluster_sync();      // every CTA has read the others' histogram
     left -= s.found[1];
     lo += s.found[0] << shift;
-    if (s.found[2] == left) {           // the whole bin is taken
-      *thr = lo - 1;
-      return;
-    }
-    if (shift == 0) {
-      *thr = lo;
-      *ties = left;
-      return;
-    }
+    if (!exact || s.found[2] == left) return Cut{lo - 1, 0u};       // the whole bin
+    if (shift == 0) return Cut{lo, left};
     range = (1u << shift) - 1;
+    __syncthreads();                    // found has been read
   }
 }
 
-// In list order: put(position, entry) for every taken entry, positions from (g0 larger, e0 equal) on;
-// returns the list's own counts (larger | equal << 16).
-template <class Put>
-__device__ __forceinline__ uint32_t take_in_order(const uint32_t* keys, int m, uint32_t thr, uint32_t ties, uint32_t* wsum,
-                                                  uint32_t g0, uint32_t e0, bool count_only, Put put) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int span = ((m + kSelWarps - 1) / kSelWarps + 31) & ~31, from = warp * span, to = min(m, from + span);
-  uint32_t cnt = 0;
-  for (int i0 = from; i0 < to; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t key = i < to ? keys[i] : 0u;
-    cnt += __popc(__ballot_sync(0xFFFFFFFFu, i < to && key > thr)) | (__popc(__ballot_sync(0xFFFFFFFFu, i < to && key == thr)) << 16);
-  }
-  if (lane == 0) wsum[warp] = cnt;
-  __syncthreads();
-  uint32_t before = 0, all = 0;
+// Adds the entries of a warp's `take` bits (bit j: value v[j] at index i0 + 128 (j / 4) + 4 lane + j % 4)
+// to the list; those past its end are dropped, which the count shows.
+template <int N>
+__device__ __forceinline__ void append(uint2* list, uint32_t cap, uint32_t* count, uint32_t take, const float (&v)[N], int i0,
+                                       bool as_key, int f_lo, int f_hi) {
+  if (!__any_sync(0xFFFFFFFFu, take)) return;
+  const int lane = threadIdx.x & 31;
+  const uint32_t mine = __popc(take);
+  uint32_t inc = mine;
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    const uint32_t v = wsum[w];
-    if (w < warp) before += v;
-    all += v;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t w = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += w;
   }
-  if (!count_only) {
-    uint32_t g = g0 + (before & 0xFFFFu), e = e0 + (before >> 16);
-    const uint32_t lt = (1u << lane) - 1;
-    for (int i0 = from; i0 < to; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t key = i < to ? keys[i] : 0u;
-      const bool gt = i < to && key > thr, eq = i < to && key == thr;
-      const uint32_t bg = __ballot_sync(0xFFFFFFFFu, gt), be = __ballot_sync(0xFFFFFFFFu, eq);
-      const uint32_t eb = e + __popc(be & lt);
-      if (gt || (eq && eb < ties)) put(static_cast<int>(g + __popc(bg & lt) + min(eb, ties)), i);
-      g += __popc(bg);
-      e += __popc(be);
+  uint32_t base = 0;
+  if (lane == 31) base = atomicAdd(count, inc);
+  base = __shfl_sync(0xFFFFFFFFu, base, 31);
+  uint32_t pos = base + inc - mine;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if ((take >> j) & 1u) {
+      const int i = i0 + (j >> 2) * 128 + 4 * lane + (j & 3);
+      uint32_t bits = __float_as_uint(v[j]);
+      if (as_key) bits = i < f_lo || i >= f_hi ? kForcedKey : score_key(v[j]);
+      if (pos < cap) list[pos] = make_uint2(bits, static_cast<uint32_t>(i));
+      ++pos;
     }
   }
-  __syncthreads();
-  return all;
 }
 
 __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const IndexSelectParams p, int ranks) {
-  extern __shared__ __align__(16) uint32_t sel_smem[];
-  SelShared s;
-  s.hist = sel_smem;
-  s.wsum = s.hist + kSelBins;
-  s.stat = s.wsum + 2 * kSelWarps;
-  s.found = s.stat + 4;
-  int64_t* srow = reinterpret_cast<int64_t*>(s.found + 4);       // [2]
-  uint32_t* keys = sel_smem + kSelFixed / 4;
-  uint32_t* idx = keys + p.topk + kSelChunk;
-  uint32_t* copy = idx + p.topk + kSelChunk;                     // [2][topk]
+  extern __shared__ __align__(16) uint8_t sel_smem[];
+  SelShared& s = *reinterpret_cast<SelShared*>(sel_smem);
+  uint2* list = reinterpret_cast<uint2*>(sel_smem + kSelFixed);       // (score bits, then key; index)
+  const uint32_t cap = p.topk + kSelChunk;
+  uint2* copy = list + cap;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t = blockIdx.x / ranks, rank = blockIdx.x % ranks;
   if (tid == 0) {
     int64_t vis = 0;
-    srow[0] = row_request(p.cu_q, p.seq_lens, p.B, t, &vis);
-    srow[1] = vis;
+    s.row[0] = row_request(p.cu_q, p.seq_lens, p.B, t, &vis);
+    s.row[1] = vis;
+    s.count = 0;
   }
   __syncthreads();
-  const int b = static_cast<int>(srow[0]);
-  const int64_t vis = srow[1];
+  const int b = static_cast<int>(s.row[0]);
+  const int64_t vis = s.row[1];
   if (b < 0) return;       // every CTA of the cluster
   const float* __restrict__ x = p.scores + t * p.s_stride;
   const int n = static_cast<int>(min((vis + p.block_tokens - 1) / p.block_tokens, p.width));
@@ -428,151 +416,201 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
   const int part = ((n + ranks - 1) / ranks + 3) & ~3;
   const int from = min(n, rank * part), to = min(n, from + part);
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
-
-  // ---- stream: a warp takes 32 * kSelPer neighbouring scores of a chunk, 4 a lane and load
-  float cur[kSelPer], nxt[kSelPer];
-  auto load = [&](int c0, float (&v)[kSelPer]) {
+  // a lane's four scores at i .. i + 3; NaN past the part
+  auto load4 = [&](int i, float* v) {
+    if (vec && i + 3 < to) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(x + i));
+      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+    } else {
 #pragma unroll
-    for (int j = 0; j < kSelPer / 4; ++j) {
-      const int i = c0 + warp * 32 * kSelPer + j * 128 + 4 * lane;
-      if (vec && i + 3 < to) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(x + i));
-        v[4 * j] = w.x, v[4 * j + 1] = w.y, v[4 * j + 2] = w.z, v[4 * j + 3] = w.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * j + e] = i + e < to ? __ldg(x + i + e) : CUDART_NAN_F;
-      }
+      for (int e = 0; e < 4; ++e) v[e] = i + e < to ? __ldg(x + i + e) : CUDART_NAN_F;
     }
   };
-  int m = 0, flip = 0;
-  float bound = -CUDART_INF_F;
-  load(from, cur);
-  for (int c0 = from; c0 < to; c0 += kSelChunk) {
-    load(c0 + kSelChunk, nxt);
-    const bool forced_here = c0 < f_lo || c0 + kSelChunk > f_hi;
-    for (;;) {
-      // scores above the bound; NaN is not, and -inf is above nothing
-      uint32_t take = 0;
-#pragma unroll
-      for (int j = 0; j < kSelPer; ++j) take |= (cur[j] > bound ? 1u : 0u) << j;
-      if (forced_here) {
-#pragma unroll
-        for (int j = 0; j < kSelPer; ++j) {
-          const int i = c0 + warp * 32 * kSelPer + (j >> 2) * 128 + 4 * lane + (j & 3);
-          if (i < to && (i < f_lo || i >= f_hi)) take |= 1u << j;
-        }
-      }
-      // ranks in row order: load by load, lane by lane, then the lane's four
-      uint32_t at[kSelPer / 4], cnt = 0;
-#pragma unroll
-      for (int j = 0; j < kSelPer / 4; ++j) {
-        const uint32_t mine = (take >> (4 * j)) & 15u;
-        uint32_t inc = __popc(mine);
-        if (__any_sync(0xFFFFFFFFu, inc)) {
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-            if (lane >= o) inc += v;
-          }
-          at[j] = cnt + inc - __popc(mine);
-          cnt += __shfl_sync(0xFFFFFFFFu, inc, 31);
-        } else {
-          at[j] = cnt;
-        }
-      }
-      uint32_t* ws = s.wsum + flip * kSelWarps;
-      flip ^= 1;
-      if (lane == 0) ws[warp] = cnt;
-      __syncthreads();
-      uint32_t before = m, all = 0;
-#pragma unroll
-      for (int w = 0; w < kSelWarps; ++w) {
-        const uint32_t v = ws[w];
-        if (w < warp) before += v;
-        all += v;
-      }
-      if (m + static_cast<int>(all) <= p.topk + kSelChunk) {
-#pragma unroll
-        for (int j = 0; j < kSelPer; ++j) {
-          if (!((take >> j) & 1u)) continue;
-          const int i = c0 + warp * 32 * kSelPer + (j >> 2) * 128 + 4 * lane + (j & 3);
-          const uint32_t pos = before + at[j >> 2] + __popc((take >> (4 * (j >> 2))) & ((1u << (j & 3)) - 1));
-          keys[pos] = i < f_lo || i >= f_hi ? kForced : score_key(cur[j]);
-          idx[pos] = i;
-        }
-        m += all;
-        break;
-      }
-      // cut the list to its topk, then take the chunk again
-      __syncthreads();
-      uint32_t thr, ties;
-      find_threshold(keys, m, kk, 1, s, &thr, &ties);
-      const uint32_t got = take_in_order(keys, m, thr, ties, s.wsum, 0, 0, false, [&](int pos, int i) {
-        copy[pos] = keys[i];
-        copy[p.topk + pos] = idx[i];
-      });
-      m = static_cast<int>((got & 0xFFFFu) + min(got >> 16, ties));
-      for (int i = tid; i < m; i += kSelThreads) {
-        keys[i] = copy[i];
-        idx[i] = copy[p.topk + i];
-      }
-      // everything kept equals the bound or is above it (thr itself when ties were cut, else the next
-      // key): a later score has to be above thr
-      bound = thr == 0 ? bound : kk == 0 ? CUDART_INF_F : key_score(thr);
-      __syncthreads();
+  auto forced_bits = [&](int i0, int loads) -> uint32_t {
+    uint32_t f = 0;
+    for (int j = 0; j < 4 * loads; ++j) {
+      const int i = i0 + (j >> 2) * 128 + 4 * lane + (j & 3);
+      if (i < to && (i < f_lo || i >= f_hi)) f |= 1u << j;
     }
+    return f;
+  };
+
+  // ---- the bound: the score of the sample's rank that leaves about four standard deviations of room
+  float bound = -CUDART_INF_F;
+  bool strict = true;
+  if (n > static_cast<int>(cap)) {
+    uint32_t* keys = reinterpret_cast<uint32_t*>(list);
+    const int64_t step = n;      // sample i is score floor(i n / 4096), the same in every CTA of the cluster
 #pragma unroll
-    for (int j = 0; j < kSelPer; ++j) cur[j] = nxt[j];
+    for (int j = 0; j < kSelSample / kSelThreads; ++j) {
+      const int i = tid + j * kSelThreads;
+      const float f = __ldg(x + (i * step) / kSelSample);
+      keys[i] = f > -CUDART_INF_F ? score_key(f) : 0u;
+    }
+    __syncthreads();
+    const float r = static_cast<float>(kk) * kSelSample / n;
+    const Cut c = find_cut(kSelSample, static_cast<uint32_t>(r + 4.f * sqrtf(r) + 8.f), 1, false, s, [&](int i) { return keys[i]; });
+    if (c.thr) {
+      bound = key_score(c.thr + 1);
+      strict = false;
+    }
+    __syncthreads();
+  }
+  // ---- stream: a warp takes 512 neighbouring scores at a time, 4 a lane and load
+  for (int i0 = from + warp * 512; i0 < to; i0 += kSelWarps * 512) {
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load4(i0 + 128 * j + 4 * lane, v + 4 * j);
+    uint32_t take = 0;
+    if (strict) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) take |= (v[j] > bound ? 1u : 0u) << j;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) take |= (v[j] >= bound ? 1u : 0u) << j;
+    }
+    if (i0 < f_lo || i0 + 512 > f_hi) take |= forced_bits(i0, 4);
+    append(list, cap, &s.count, take, v, i0, false, f_lo, f_hi);
+  }
+  __syncthreads();
+  bool good = s.count <= cap;
+  uint32_t total = s.count;
+  if (ranks > 1) {
+    cluster_sync();
+    total = 0;
+    for (int r = 0; r < ranks; ++r) {
+      const uint32_t c = ld_cluster_u32(&s.count, r);
+      total += c;
+      good = good && c <= cap;
+    }
+    cluster_sync();
+  }
+  // fewer than topk although the row was not let in whole: the bound was too high
+  good = good && (strict || total >= static_cast<uint32_t>(p.topk));
+  int m = static_cast<int>(s.count);
+  if (good) {
+    for (int i = tid; i < m; i += kSelThreads) {
+      const int c = static_cast<int>(list[i].y);
+      list[i].x = c < f_lo || c >= f_hi ? kForcedKey : score_key(__uint_as_float(list[i].x));
+    }
+  } else {
+    // ---- in order, cutting the list whenever it is full
+    __syncthreads();
+    m = 0;
+    bound = -CUDART_INF_F;
+    for (int c0 = from; c0 < to; c0 += kSelChunk) {
+      const int i0 = c0 + warp * 256;
+      float v[8];
+      load4(i0 + 4 * lane, v);
+      load4(i0 + 128 + 4 * lane, v + 4);
+      for (;;) {
+        if (tid == 0) s.count = m;
+        __syncthreads();
+        uint32_t take = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) take |= (v[j] > bound ? 1u : 0u) << j;
+        if (i0 < f_lo || i0 + 256 > f_hi) take |= forced_bits(i0, 2);
+        append(list, cap, &s.count, take, v, i0, true, f_lo, f_hi);
+        __syncthreads();
+        const int now = static_cast<int>(s.count);
+        __syncthreads();
+        if (now <= static_cast<int>(cap)) {
+          m = now;
+          break;
+        }
+        // the list of the rounds before this one, cut to its topk; then the round again
+        const Cut c = find_cut(m, kk, 1, true, s, [&](int i) { return list[i].x == kForcedKey ? 0u : list[i].x; });
+        uint32_t first = 0;
+        if (c.ties) first = find_cut(m, c.ties, 1, true, s, [&](int i) { return list[i].x == c.thr ? ~list[i].y : 0u; }).thr;
+        if (tid == 0) s.count = 0;
+        __syncthreads();
+        for (int i = tid; i < m; i += kSelThreads) {
+          const uint2 e = list[i];
+          if (e.x > c.thr || (c.ties && e.x == c.thr && ~e.y > first)) copy[atomicAdd(&s.count, 1u)] = e;
+        }
+        __syncthreads();
+        m = static_cast<int>(s.count);
+        for (int i = tid; i < m; i += kSelThreads) list[i] = copy[i];
+        if (kk == 0)
+          bound = CUDART_INF_F;
+        else if (c.thr)
+          bound = key_score(c.thr);
+        __syncthreads();
+      }
+    }
   }
   __syncthreads();
 
   // ---- the last cut, over the row
-  uint32_t thr, ties;
-  find_threshold(keys, m, kk, ranks, s, &thr, &ties);
+  const Cut c = find_cut(m, kk, ranks, true, s, [&](int i) { return list[i].x == kForcedKey ? 0u : list[i].x; });
+  uint32_t first = 0;
+  if (c.ties) first = find_cut(m, c.ties, ranks, true, s, [&](int i) { return list[i].x == c.thr ? ~list[i].y : 0u; }).thr;
+  auto taken = [&](uint2 e) { return e.x > c.thr || (c.ties && e.x == c.thr && ~e.y > first); };
   int32_t* out = p.blocks + t * p.b_stride;
   int32_t* out_slots = p.slots ? p.slots + t * p.sl_stride : nullptr;
-  const bool one = p.block_tokens == 1;
-  auto slot_of = [&](int64_t pos) -> int32_t {
-    if (pos >= vis) return -1;
-    const int64_t col = pos / p.page_size;
-    const int64_t id = col < p.bt_cols ? p.block_table[b * p.bt_stride + col] : -1;
-    if (id < 0 || id >= p.num_blocks) {
-      set_device_error(p.err, 2u);
-      return -1;
-    }
-    return static_cast<int32_t>(id * p.page_size + pos % p.page_size);
-  };
-  uint32_t g0 = 0, e0 = 0, g_all = 0, e_all = 0;
-  auto put = [&](int pos, int i) {
-    const int32_t c = static_cast<int32_t>(idx[i]);
-    out[pos] = c;
-    if (out_slots && one) out_slots[pos] = slot_of(c);
-    if (out_slots && !one)
-      for (int u = 0; u < p.block_tokens; ++u)
-        out_slots[static_cast<int64_t>(pos) * p.block_tokens + u] = slot_of(static_cast<int64_t>(c) * p.block_tokens + u);
-  };
+  uint32_t at = 0, all = 0;      // positions before this CTA's part, and of the row
   if (ranks > 1) {
-    const uint32_t mine = take_in_order(keys, m, thr, ties, s.wsum, 0, 0, true, put);
-    if (tid == 0) s.stat[3] = mine;
+    uint32_t mine = 0;
+    for (int i = tid; i < m; i += kSelThreads) mine += taken(list[i]) ? 1u : 0u;
+    mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+    if (tid == 0) s.stat[3] = 0;
+    __syncthreads();
+    if (lane == 0) atomicAdd(&s.stat[3], mine);
+    __syncthreads();
     cluster_sync();
     for (int r = 0; r < ranks; ++r) {
       const uint32_t v = ld_cluster_u32(&s.stat[3], r);
-      if (r < rank) g0 += v & 0xFFFFu, e0 += v >> 16;
-      g_all += v & 0xFFFFu, e_all += v >> 16;
+      if (r < rank) at += v;
+      all += v;
     }
-    cluster_sync();       // no CTA leaves while another may read its counts
-    take_in_order(keys, m, thr, ties, s.wsum, g0, e0, false, put);
-  } else {
-    const uint32_t v = take_in_order(keys, m, thr, ties, s.wsum, 0, 0, false, put);
-    g_all = v & 0xFFFFu, e_all = v >> 16;
+    cluster_sync();       // no CTA leaves while another may read its count
   }
+  // ---- the map, 65536 indices at a time, and its bits in order
+  for (int w0 = from; w0 < to; w0 += 32 * kSelBins) {
+    reinterpret_cast<uint4*>(s.hist)[tid] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for (int i = tid; i < m; i += kSelThreads) {
+      const uint2 e = list[i];
+      const uint32_t d = e.y - w0;
+      if (d < 32 * kSelBins && taken(e)) atomicOr(&s.hist[d >> 5], 1u << (d & 31));
+    }
+    __syncthreads();
+    const uint4 w = reinterpret_cast<const uint4*>(s.hist)[tid];
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t own = __popc(w.x) + __popc(w.y) + __popc(w.z) + __popc(w.w);
+    uint32_t pos = at + block_prefix(own, s.wsum);
+    if (tid == kSelThreads - 1) s.found[0] = pos + own;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      for (uint32_t bits = words[u]; bits; bits &= bits - 1)
+        out[pos++] = w0 + 128 * tid + 32 * u + __ffs(bits) - 1;
+    }
+    __syncthreads();
+    at = s.found[0];
+    __syncthreads();
+  }
+  if (ranks == 1) all = at;
   // ---- -1 after the list
-  const int taken = static_cast<int>(g_all + min(e_all, ties));
-  for (int i = taken + rank * kSelThreads + tid; i < p.topk; i += ranks * kSelThreads) out[i] = -1;
-  if (out_slots) {
-    const int64_t all = static_cast<int64_t>(p.topk) * p.block_tokens;
-    for (int64_t i = static_cast<int64_t>(taken) * p.block_tokens + rank * kSelThreads + tid; i < all; i += ranks * kSelThreads)
-      out_slots[i] = -1;
+  for (int i = static_cast<int>(all) + rank * kSelThreads + tid; i < p.topk; i += ranks * kSelThreads) out[i] = -1;
+  if (!out_slots) return;
+  // ---- token slots of the taken blocks through the block table
+  if (ranks > 1) cluster_sync(); else __syncthreads();      // the list is written
+  const int64_t slots = static_cast<int64_t>(p.topk) * p.block_tokens;
+  for (int64_t i = rank * kSelThreads + tid; i < slots; i += ranks * kSelThreads) {
+    const int64_t j = i / p.block_tokens;
+    int32_t slot = -1;
+    if (j < all) {
+      const int64_t pos = static_cast<int64_t>(__ldcg(out + j)) * p.block_tokens + (i - j * p.block_tokens);
+      if (pos < vis) {
+        const int64_t col = pos / p.page_size;
+        const int64_t id = col < p.bt_cols ? p.block_table[b * p.bt_stride + col] : -1;
+        if (id < 0 || id >= p.num_blocks)
+          set_device_error(p.err, 2u);
+        else
+          slot = static_cast<int32_t>(id * p.page_size + pos % p.page_size);
+      }
+    }
+    out_slots[i] = slot;
   }
 }
 
