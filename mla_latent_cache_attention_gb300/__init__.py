@@ -522,47 +522,81 @@ def merge_attn_states(prefix_output, prefix_lse, suffix_output, suffix_lse, *, o
     return output, lse
 
 
+# The selector's calls are short on the device, so their checks are: one look per tensor, in the order
+# that costs least, and _need only to word the refusal.
+_BF16, _F32, _I32, _I64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
+_INDEX_TYPES = {CACHE_BF16: _BF16, CACHE_FP8: _BYTE_TYPES}
+_KV_TYPES = _BYTE_TYPES + _BF16
+
+
+def _strides(t, name, dtypes, dev, ndim):
+    """The strides of a tensor that passes _need's checks (unit innermost stride)."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == dev.index and t.dim() == ndim:
+        st = t.stride()
+        if st[-1] == 1:
+            return st
+    _need(t, name, dtypes, dev, ndim=ndim)
+    return t.stride()
+
+
+def _call(fn, dev, *args):
+    """fn(*args, current stream of dev) with dev current."""
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        _check(rc)
+
+
 def _index_format(fmt) -> int:
     fmt = _fmt(fmt)
-    if fmt not in (CACHE_BF16, CACHE_FP8):
+    if fmt not in _INDEX_TYPES:
         raise ValueError("the index cache is bf16 or fp8")
     return fmt
 
 
 def _index_geometry(index_cache, index_scales, fmt, dev):
-    """(num_blocks, block stride and entry stride in bytes, block_size, scale block stride) of an
-    index cache [num_blocks, block_size, 128] and its scales fp32 [num_blocks, block_size]."""
-    _need(index_cache, "index_cache", (torch.bfloat16,) if fmt == CACHE_BF16 else _BYTE_TYPES, dev, ndim=3)
-    if index_cache.shape[2] != 128:
-        raise ValueError(f"index keys have 128 values, got {index_cache.shape[2]}")
-    nb, bstride, estride, bs = _cache_geometry(index_cache)
+    """(num_blocks, block stride and entry stride in bytes, scales' address, their block stride,
+    block_size) of an index cache [num_blocks, block_size, 128] and its scales fp32
+    [num_blocks, block_size]."""
+    st = _strides(index_cache, "index_cache", _INDEX_TYPES[fmt], dev, 3)
+    nb, bs, width = index_cache.shape
+    if width != 128:
+        raise ValueError(f"index keys have 128 values, got {width}")
     if fmt == CACHE_BF16:
         if index_scales is not None:
             raise ValueError("index_scales are only for the fp8 index cache")
-        return nb, bstride, estride, bs, 0
-    _need(index_scales, "index_scales", (torch.float32,), dev, ndim=2)
-    if tuple(index_scales.shape) != (nb, bs):
+        return nb, 2 * st[0], 2 * st[1], None, 0, bs
+    ss = _strides(index_scales, "index_scales", _F32, dev, 2)
+    if index_scales.shape != (nb, bs):
         raise ValueError(f"index_scales must be [num_blocks, block_size] = {(nb, bs)}, got {tuple(index_scales.shape)}")
-    return nb, bstride, estride, bs, index_scales.stride(0)
+    return nb, st[0], st[1], index_scales.data_ptr(), ss[0], bs
 
 
-def _row_counts(seq_lens, cu_q_lens, T, dev):
-    """The number of requests, checked against cu_q_lens (or one row per request)."""
-    _need(seq_lens, "seq_lens", (torch.int32,), dev, ndim=1, contiguous=True)
-    B = seq_lens.numel()
-    if cu_q_lens is not None:
-        _need(cu_q_lens, "cu_q_lens", (torch.int32,), dev, ndim=1, contiguous=True)
-        if cu_q_lens.numel() != B + 1:
-            raise ValueError(f"cu_q_lens must have B + 1 = {B + 1} entries, got {cu_q_lens.numel()}")
-    elif T != B:
-        raise ValueError(f"without cu_q_lens there is one row per request: {T} rows, {B} requests")
-    return B
+def _requests(seq_lens, cu_q_lens, T, dev):
+    """The number of requests and cu_q_lens' address (None: one row per request)."""
+    _strides(seq_lens, "seq_lens", _I32, dev, 1)
+    B = seq_lens.shape[0]
+    if cu_q_lens is None:
+        if T != B:
+            raise ValueError(f"without cu_q_lens there is one row per request: {T} rows, {B} requests")
+        return B, None
+    _strides(cu_q_lens, "cu_q_lens", _I32, dev, 1)
+    if cu_q_lens.shape[0] != B + 1:
+        raise ValueError(f"cu_q_lens must have B + 1 = {B + 1} entries, got {cu_q_lens.shape[0]}")
+    return B, cu_q_lens.data_ptr()
 
 
-def _need_table(block_table, rows, dev):
-    _need(block_table, "block_table", (torch.int32,), dev, ndim=2)
-    if block_table.shape[0] < rows:
-        raise ValueError(f"block_table needs a row per request: {block_table.shape[0]} rows, {rows} requests")
+def _table(block_table, rows, dev):
+    """Address, row stride and columns of a block table with a row per request."""
+    st = _strides(block_table, "block_table", _I32, dev, 2)
+    have, cols = block_table.shape
+    if have < rows:
+        raise ValueError(f"block_table needs a row per request: {have} rows, {rows} requests")
+    return block_table.data_ptr(), max(st[0], cols), cols
 
 
 def index_q_cache_insert(q, k, weights, index_cache, index_scales, slot_mapping, *, fmt, weight_scale=1.0,
@@ -572,40 +606,45 @@ def index_q_cache_insert(q, k, weights, index_cache, index_scales, slot_mapping,
     w_out fp32 [T, Hi]: weights * weight_scale, times the query's scale for fp8)."""
     fmt = _index_format(fmt)
     dev = _cuda_device(q)
-    _need(q, "q", (torch.bfloat16,), dev, ndim=3)
+    qs = _strides(q, "q", _BF16, dev, 3)
     T, Hi, width = q.shape
-    _need(k, "k", (torch.bfloat16,), dev)
-    if k.dim() == 3 and k.shape[1] == 1:      # [T, 1, 128] (a head axis of size 1)
+    if isinstance(k, torch.Tensor) and k.dim() == 3 and k.shape[1] == 1:      # [T, 1, 128]
         k = k.squeeze(1)
-    _need(weights, "weights", (torch.float32,), dev, ndim=2)
-    _need(slot_mapping, "slot_mapping", (torch.int64,), dev, ndim=1, contiguous=True)
-    if width != 128 or tuple(k.shape) != (T, 128) or tuple(weights.shape) != (T, Hi) or slot_mapping.numel() != T:
+    ks = _strides(k, "k", _BF16, dev, 2)
+    ws = _strides(weights, "weights", _F32, dev, 2)
+    _strides(slot_mapping, "slot_mapping", _I64, dev, 1)
+    if width != 128 or k.shape != (T, 128) or weights.shape != (T, Hi) or slot_mapping.shape[0] != T:
         raise ValueError("q must be [T, Hi, 128], k [T, 128], weights [T, Hi] and slot_mapping [T]")
+    pos = cs = None
+    max_pos = 0
     if positions is not None:
-        _need(positions, "positions", (torch.int64,), dev, ndim=1, contiguous=True)
-        if positions.numel() != T:
+        _strides(positions, "positions", _I64, dev, 1)
+        if positions.shape[0] != T:
             raise ValueError(f"positions must have T = {T} entries")
+        pos = positions.data_ptr()
     if cos_sin_cache is not None:
-        _need(cos_sin_cache, "cos_sin_cache", (torch.float32,), dev, ndim=2, contiguous=True)
-        if cos_sin_cache.shape[1] != 64:
+        _need(cos_sin_cache, "cos_sin_cache", _F32, dev, ndim=2, contiguous=True)
+        max_pos, half = cos_sin_cache.shape
+        if half != 64:
             raise ValueError("cos_sin_cache must be [max_position, 64]")
-    out_type = torch.bfloat16 if fmt == CACHE_BF16 else torch.uint8
+        cs = cos_sin_cache.data_ptr()
+    out_types = _INDEX_TYPES[fmt]
     if q_out is None:
-        q_out = torch.empty((T, Hi, 128), dtype=out_type, device=dev)
+        q_out = torch.empty((T, Hi, 128), dtype=out_types[0], device=dev)
+    else:
+        _need(q_out, "q_out", out_types, dev, ndim=3, contiguous=True)
+        if q_out.shape != (T, Hi, 128):
+            raise ValueError("q_out must be [T, Hi, 128]")
     if w_out is None:
         w_out = torch.empty((T, Hi), dtype=torch.float32, device=dev)
-    _need(q_out, "q_out", (out_type,), dev, ndim=3, contiguous=True)
-    _need(w_out, "w_out", (torch.float32,), dev, ndim=2, contiguous=True)
-    if tuple(q_out.shape) != (T, Hi, 128) or tuple(w_out.shape) != (T, Hi):
-        raise ValueError("q_out must be [T, Hi, 128] and w_out [T, Hi]")
-    nb, bstride, estride, bs, sstride = _index_geometry(index_cache, index_scales, fmt, dev)
-    max_pos = 0 if cos_sin_cache is None else cos_sin_cache.shape[0]
-    with torch.cuda.device(dev):
-        _check(lib().mla_index_q_cache_insert(
-            _ptr(q), q.stride(0), q.stride(1), _ptr(k), k.stride(0), _ptr(weights), weights.stride(0),
-            float(weight_scale), _ptr(q_out), _ptr(w_out), _ptr(index_cache), fmt, nb, bstride, estride,
-            _ptr(index_scales), sstride, bs, _ptr(slot_mapping), _ptr(positions), _ptr(cos_sin_cache), max_pos, T, Hi,
-            _stream(q)))
+    else:
+        _need(w_out, "w_out", _F32, dev, ndim=2, contiguous=True)
+        if w_out.shape != (T, Hi):
+            raise ValueError("w_out must be [T, Hi]")
+    nb, bstride, estride, sc, sstride, bs = _index_geometry(index_cache, index_scales, fmt, dev)
+    _call(lib().mla_index_q_cache_insert, dev, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], weights.data_ptr(), ws[0],
+          float(weight_scale), q_out.data_ptr(), w_out.data_ptr(), index_cache.data_ptr(), fmt, nb, bstride, estride, sc, sstride,
+          bs, slot_mapping.data_ptr(), pos, cs, max_pos, T, Hi)
     return q_out, w_out
 
 
@@ -614,24 +653,24 @@ def index_gather(index_cache, index_scales, block_table, cu_seq_lens, seq_starts
     request b's positions seq_starts[b] + i."""
     fmt = _index_format(fmt)
     dev = _cuda_device(index_cache)
-    nb, bstride, estride, bs, sstride = _index_geometry(index_cache, index_scales, fmt, dev)
-    _need(cu_seq_lens, "cu_seq_lens", (torch.int32,), dev, ndim=1, contiguous=True)
-    batch = cu_seq_lens.numel() - 1
-    _need_table(block_table, batch, dev)
+    nb, bstride, estride, sc, sstride, bs = _index_geometry(index_cache, index_scales, fmt, dev)
+    _strides(cu_seq_lens, "cu_seq_lens", _I32, dev, 1)
+    batch = cu_seq_lens.shape[0] - 1
+    table, tstride, cols = _table(block_table, batch, dev)
+    starts = None
     if seq_starts is not None:
-        _need(seq_starts, "seq_starts", (torch.int32,), dev, ndim=1, contiguous=True)
-        if seq_starts.numel() < batch:
+        _strides(seq_starts, "seq_starts", _I32, dev, 1)
+        if seq_starts.shape[0] < batch:
             raise ValueError("seq_starts needs an entry per request")
+        starts = seq_starts.data_ptr()
+    num_tokens = int(num_tokens)
     if dst is None:
         dst = torch.empty((num_tokens, 128), dtype=torch.bfloat16, device=dev)
-    _need(dst, "dst", (torch.bfloat16,), dev, ndim=2)
-    if tuple(dst.shape) != (num_tokens, 128):
+    ds = _strides(dst, "dst", _BF16, dev, 2)
+    if dst.shape != (num_tokens, 128):
         raise ValueError(f"dst must be [num_tokens, 128] = {(num_tokens, 128)}")
-    with torch.cuda.device(dev):
-        _check(lib().mla_index_gather(
-            _ptr(index_cache), fmt, nb, bstride, estride, _ptr(index_scales), sstride, bs, _ptr(block_table),
-            block_table.stride(0), block_table.shape[1], _ptr(cu_seq_lens), _ptr(seq_starts), batch, int(num_tokens),
-            _ptr(dst), dst.stride(0), _stream(index_cache)))
+    _call(lib().mla_index_gather, dev, index_cache.data_ptr(), fmt, nb, bstride, estride, sc, sstride, bs, table, tstride,
+          cols, cu_seq_lens.data_ptr(), starts, batch, num_tokens, dst.data_ptr(), ds[0])
     return dst
 
 
@@ -643,26 +682,25 @@ def index_scores(q, weights, index_cache, index_scales, block_table, seq_lens, c
     columns of visible blocks are written."""
     fmt = _index_format(fmt)
     dev = _cuda_device(q)
-    _need(q, "q", (torch.bfloat16,) if fmt == CACHE_BF16 else _BYTE_TYPES, dev, ndim=3)
+    qs = _strides(q, "q", _INDEX_TYPES[fmt], dev, 3)
     T, Hi, width = q.shape
-    _need(weights, "weights", (torch.float32,), dev, ndim=2)
-    if width != 128 or tuple(weights.shape) != (T, Hi):
+    ws = _strides(weights, "weights", _F32, dev, 2)
+    if width != 128 or weights.shape != (T, Hi):
         raise ValueError("q must be [T, Hi, 128] and weights [T, Hi]")
-    B = _row_counts(seq_lens, cu_q_lens, T, dev)
-    _need_table(block_table, B, dev)
-    nb, bstride, estride, bs, sstride = _index_geometry(index_cache, index_scales, fmt, dev)
-    cols = -(-int(max_context) // int(block_tokens))
+    B, cu = _requests(seq_lens, cu_q_lens, T, dev)
+    table, tstride, tcols = _table(block_table, B, dev)
+    nb, bstride, estride, sc, sstride, bs = _index_geometry(index_cache, index_scales, fmt, dev)
+    block_tokens = int(block_tokens)
+    cols = -(-int(max_context) // block_tokens)
     if scores is None:
         scores = torch.empty((T, cols), dtype=torch.float32, device=dev)
-    _need(scores, "scores", (torch.float32,), dev, ndim=2)
-    if scores.shape[0] != T or scores.shape[1] < cols:
+    ss = _strides(scores, "scores", _F32, dev, 2)
+    rows, have = scores.shape
+    if rows != T or have < cols:
         raise ValueError(f"scores must be [T, >= {cols}] with T = {T}, got {tuple(scores.shape)}")
-    with torch.cuda.device(dev):
-        _check(lib().mla_index_scores(
-            _ptr(q), q.stride(0), q.stride(1), _ptr(weights), weights.stride(0), _ptr(index_cache), fmt, nb, bstride,
-            estride, _ptr(index_scales), sstride, bs, _ptr(block_table), block_table.stride(0), block_table.shape[1],
-            _ptr(seq_lens), _ptr(cu_q_lens), B, T, Hi, int(block_tokens), _ptr(scores), scores.stride(0), cols,
-            _stream(q)))
+    _call(lib().mla_index_scores, dev, q.data_ptr(), qs[0], qs[1], weights.data_ptr(), ws[0], index_cache.data_ptr(), fmt, nb,
+          bstride, estride, sc, sstride, bs, table, tstride, tcols, seq_lens.data_ptr(), cu, B, T, Hi, block_tokens,
+          scores.data_ptr(), max(ss[0], cols), cols)
     return scores
 
 
@@ -673,33 +711,32 @@ def index_select(scores, seq_lens, topk, cu_q_lens=None, *, block_tokens=1, firs
     block_table (and page_size, num_blocks) also the cache slots of their visible tokens, for
     sparse_fwd.  Returns (blocks int32 [T, topk], slots int32 [T, topk * block_tokens] or None)."""
     dev = _cuda_device(scores)
-    _need(scores, "scores", (torch.float32,), dev, ndim=2)
+    ss = _strides(scores, "scores", _F32, dev, 2)
     T, width = scores.shape
-    B = _row_counts(seq_lens, cu_q_lens, T, dev)
+    B, cu = _requests(seq_lens, cu_q_lens, T, dev)
     topk, block_tokens = int(topk), int(block_tokens)
     if topk < 1 or block_tokens < 1:
         raise ValueError("topk and block_tokens must be >= 1")
     if blocks is None:
         blocks = torch.empty((T, topk), dtype=torch.int32, device=dev)
-    _need(blocks, "blocks", (torch.int32,), dev, ndim=2)
-    if tuple(blocks.shape) != (T, topk):
+    bs = _strides(blocks, "blocks", _I32, dev, 2)
+    if blocks.shape != (T, topk):
         raise ValueError(f"blocks must be [T, topk] = {(T, topk)}")
-    if block_table is None:
-        if slots is not None:
-            raise ValueError("slots need a block_table")
-    else:
-        _need_table(block_table, B, dev)
+    table, tstride, tcols, sl, sl_stride = None, 0, 0, None, 0
+    if block_table is not None:
+        table, tstride, tcols = _table(block_table, B, dev)
+        per_row = topk * block_tokens
         if slots is None:
-            slots = torch.empty((T, topk * block_tokens), dtype=torch.int32, device=dev)
-        _need(slots, "slots", (torch.int32,), dev, ndim=2)
-        if tuple(slots.shape) != (T, topk * block_tokens):
-            raise ValueError(f"slots must be [T, topk * block_tokens] = {(T, topk * block_tokens)}")
-    with torch.cuda.device(dev):
-        _check(lib().mla_index_select(
-            _ptr(scores), scores.stride(0), width, _ptr(seq_lens), _ptr(cu_q_lens), B, T, block_tokens, topk,
-            int(first), int(last), _ptr(blocks), blocks.stride(0), _ptr(slots), 0 if slots is None else slots.stride(0),
-            _ptr(block_table), 0 if block_table is None else block_table.stride(0),
-            0 if block_table is None else block_table.shape[1], int(page_size), int(num_blocks), _stream(scores)))
+            slots = torch.empty((T, per_row), dtype=torch.int32, device=dev)
+        sl_stride = max(_strides(slots, "slots", _I32, dev, 2)[0], per_row)
+        if slots.shape != (T, per_row):
+            raise ValueError(f"slots must be [T, topk * block_tokens] = {(T, per_row)}")
+        sl = slots.data_ptr()
+    elif slots is not None:
+        raise ValueError("slots need a block_table")
+    _call(lib().mla_index_select, dev, scores.data_ptr(), max(ss[0], width), width, seq_lens.data_ptr(), cu, B, T,
+          block_tokens, topk, int(first), int(last), blocks.data_ptr(), max(bs[0], topk), sl, sl_stride, table, tstride,
+          tcols, int(page_size), int(num_blocks))
     return blocks, slots
 
 
@@ -714,42 +751,39 @@ def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, 
     bf16, lse [T, H] or None), as paged_decode."""
     fmt = _fmt(fmt)
     dev = _cuda_device(q)
-    _need(q, "q", _BYTE_TYPES if fmt == CACHE_FP8 else (torch.bfloat16,), dev, ndim=3)
+    qs = _strides(q, "q", _BYTE_TYPES if fmt == CACHE_FP8 else _BF16, dev, 3)
     T, H, width = q.shape
     if width != 576:
         raise ValueError(f"q must be [T, H, 576], got {tuple(q.shape)}")
-    _need(kv_cache, "kv_cache", _BYTE_TYPES + (torch.bfloat16,), dev)
-    B = _row_counts(seq_lens, cu_q_lens, T, dev)
-    _need_table(block_table, B, dev)
-    _need(blocks, "blocks", (torch.int32,), dev, ndim=2)
-    if blocks.shape[0] != T:
+    _need(kv_cache, "kv_cache", _KV_TYPES, dev)
+    B, cu = _requests(seq_lens, cu_q_lens, T, dev)
+    table, tstride, tcols = _table(block_table, B, dev)
+    ls = _strides(blocks, "blocks", _I32, dev, 2)
+    rows, topk = blocks.shape
+    if rows != T:
         raise ValueError(f"blocks must be [T, topk] with T = {T}, got {tuple(blocks.shape)}")
-    topk = blocks.shape[1]
     if out is None:
         out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", (torch.bfloat16,), dev, ndim=3)
-    if out.shape[0] != T or out.shape[1] != H or out.shape[2] < 512:
+    os_ = _strides(out, "out", _BF16, dev, 3)
+    if out.shape[:2] != (T, H) or out.shape[2] < 512:
         raise ValueError(f"out must be [T, H, >= 512], got {tuple(out.shape)}")
-    if return_lse and lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
     if lse is not None:
-        _need(lse, "lse", (torch.float32,), dev, ndim=2, contiguous=True)
-        if tuple(lse.shape) != (T, H):
+        _need(lse, "lse", _F32, dev, ndim=2, contiguous=True)
+        if lse.shape != (T, H):
             raise ValueError(f"lse must be [T, H] = {(T, H)}")
+    elif return_lse:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
     nb, bstride, estride, bs = _cache_geometry(kv_cache)
-    with torch.cuda.device(dev):
-        if workspace is None:
+    if workspace is None:
+        with torch.cuda.device(dev):
             need = selected_decode_workspace_size(T, topk, bs, H)
-            if need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if workspace is not None:
-            _need(workspace, "workspace", _BYTE_TYPES, dev, contiguous=True)
-        _check(lib().mla_selected_decode(
-            _ptr(q), q.stride(0), q.stride(1), _ptr(kv_cache), fmt, nb, bstride, estride, bs, _ptr(block_table),
-            block_table.stride(0), block_table.shape[1], _ptr(seq_lens), _ptr(cu_q_lens), _ptr(blocks),
-            blocks.stride(0), topk, B, T, H, float(softmax_scale), float(q_scale), float(k_scale), _ptr(out),
-            out.stride(0), out.stride(1), _ptr(lse), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(q)))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", _BYTE_TYPES, dev, contiguous=True)
+    _call(lib().mla_selected_decode, dev, q.data_ptr(), qs[0], qs[1], kv_cache.data_ptr(), fmt, nb, bstride, estride, bs,
+          table, tstride, tcols, seq_lens.data_ptr(), cu, blocks.data_ptr(), max(ls[0], topk), topk, B, T, H,
+          float(softmax_scale), float(q_scale), float(k_scale), out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, lse
 
 

@@ -14,7 +14,10 @@
 // form (a causal row sees seq_len - rows + i + 1 keys), and every CTA takes an equal contiguous
 // range of them: scores are independent, so nothing is merged and no counter is shared.
 //
-// Warps: 0 producer (TMA boxes of pages, lanes resolve page ids), 1 MMA issuer and TMEM owner,
+// A stage is one accumulator buffer of 256 columns: one key tile, or two or four where the query
+// tile has at most 128 or 64 columns (decode), so that the four epilogue groups always share it.
+//
+// Warps: 0 producer (TMA boxes of pages, lanes resolve page ids), 1 MMA issuer and TMEM owner, 
 // 2..17 four epilogue groups of four warps, one 64-column slice of the accumulator each.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -39,22 +42,32 @@ struct Segment {
   int b, pad0, pad1;
 };
 
+// Of a thread's 64 weights this many live in registers; the others are read from shared memory
+// for every tile, four by a broadcast load.  All 64 would not leave room for the accumulator's values
+// (18 warps have 96 registers each, and spills cost more than the loads).
+constexpr int kRegCols = 32;
+
+// Key tiles of a stage (one accumulator buffer): query tiles of few columns share it.
+__device__ __forceinline__ int stage_tiles(int cols) { return cols <= 64 ? 4 : cols <= 128 ? 2 : 1; }
+
 template <int F>
 struct IndexCfg {
   static_assert(F == kBF16 || F == kFP8, "format");
   static constexpr int kHalves = F == kBF16 ? 2 : 1;            // 128-byte columns of a row
   static constexpr int kTileBytes = 128 * 128 * kHalves;
   static constexpr int kQBytes = kIxCols * 128 * kHalves;
-  static constexpr int kS = F == kBF16 ? 2 : 8;                 // key tiles in flight
-  static constexpr int kSc = kS + 2;                            // their scales (see the producer)
+  static constexpr int kS = F == kBF16 ? 4 : 8;                 // key tiles in flight
+  static constexpr int kQB = F == kBF16 ? 1 : 2;                // query tiles in flight
+  static constexpr int kSc = kS + 12;                           // scales in flight (see the producer)
   static constexpr int kQ = 0;
-  static constexpr int kRing = kQ + 2 * kQBytes;
+  static constexpr int kRing = kQ + kQB * kQBytes;
   static constexpr int kScale = kRing + kS * kTileBytes;
   static constexpr int kRed = kScale + kSc * 512;               // block maxima of 16 warps x 8 queries
-  static constexpr int kSeg = kRed + 2 * 16 * 8 * 4;
+  static constexpr int kW = kRed + 2 * 16 * 8 * 4;              // weights of 16 warps' last columns
+  static constexpr int kSeg = kW + 16 * (64 - kRegCols) * 4;
   static constexpr int kBad = kSeg + kSegDepth * 32;
   static constexpr int kBar = kBad + ((kSc * 4 + 7) & ~7);
-  static constexpr int kNumBars = 2 * kS + kSc + 8 + 2 * kSegDepth + 8 + 1;
+  static constexpr int kNumBars = 2 * kS + kSc + 8 + 2 * kSegDepth + 8 + 1;      // as carved in the kernel
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kAlloc = kMisc + 64 + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
@@ -100,12 +113,39 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
+// A position in a ring of N slots and the parity of its pass.
+template <int N>
+struct Cursor {
+  int slot = 0;
+  uint32_t par = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == N) slot = 0, par ^= 1u;
+  }
+};
+
+// relu(d) * w summed into acc, for the C columns of one query: pairs of columns share an fma.f32x2
+__device__ __forceinline__ void fma2(uint64_t& acc, float x0, float x1, uint64_t w) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(x), "l"(w));
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+__device__ __forceinline__ float sum2(uint64_t a) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+  return x + y;
+}
+
 template <int F, int HP>
 __global__ void __launch_bounds__(kIxThreads, 1)
     mla_index_scores_kernel(const __grid_constant__ IndexScoresParams p, const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_q) {
   using C = IndexCfg<F>;
-  constexpr int S = C::kS, SC = C::kSc, HV = C::kHalves;
+  constexpr int S = C::kS, SC = C::kSc, HV = C::kHalves, QB = C::kQB;
   constexpr int QT = kIxCols / HP;             // queries of a tile
   constexpr int QW = 64 / HP;                  // queries of an epilogue group
   extern __shared__ uint8_t smem_raw[];
@@ -210,7 +250,9 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     int64_t x = start[1], rem = hi - lo;
     const int BR = p.BR, SP = 128 / BR;            // page slices of BR rows, SP of them a tile
     const int TG = 32 / SP;                        // key tiles covered by one page lookup of the warp
-    int64_t tile = 0;                              // key tiles issued
+    int tile = 0;                                  // key tiles issued
+    Cursor<S> kc;
+    Cursor<SC> sc;
     int nseg = 0;
     uint32_t errbits = 0;
     bool ok = true;
@@ -251,17 +293,18 @@ __global__ void __launch_bounds__(kIxThreads, 1)
         ok = false;
         break;
       }
-      if (nseg >= 2 && !warp_wait(&q_empty[nseg & 1], ((nseg >> 1) - 1) & 1, abort_flag)) {
+      const int qb = nseg % QB;
+      if (nseg >= QB && !warp_wait(&q_empty[qb], ((nseg / QB) - 1) & 1, abort_flag)) {
         ok = false;
         break;
       }
       if (lane == 0) {
         segs[k] = sg;
         mbar_arrive(&seg_full[k]);
-        mbar_arrive_expect_tx(&q_full[nseg & 1], C::kQBytes);
+        mbar_arrive_expect_tx(&q_full[qb], C::kQBytes);
 #pragma unroll
         for (int h = 0; h < HV; ++h)
-          tma_load_3d(qs + (nseg & 1) * C::kQBytes + h * kIxCols * 128, &tm_q, 128 * h, 0, sg.t0, &q_full[nseg & 1]);
+          tma_load_3d(qs + qb * C::kQBytes + h * kIxCols * 128, &tm_q, 128 * h, 0, sg.t0, &q_full[qb]);
       }
       ++nseg;
       // page ids of the slices j SP .. (j + TG) SP - 1, one per lane, looked up a group ahead
@@ -273,16 +316,17 @@ __global__ void __launch_bounds__(kIxThreads, 1)
         return (id < 0 || id >= p.num_blocks) ? -1 : id;
       };
       int cur = lookup(sg.j0), nxt = -2;
+      int in = 0;      // tile of the lookup group
       for (int t = 0; t < sg.nt && ok; ++t, ++tile) {
-        const int in = t % TG;
+        if (in == TG) in = 0;
         if (in == 0) {
           if (t > 0) cur = nxt;
           nxt = lookup(sg.j0 + t + TG);
         }
-        const int slot = static_cast<int>(tile % S), sslot = static_cast<int>(tile % SC);
-        // Tile n - S's MMAs are done, so tile n - S - 2's accumulator had been read: its scales
-        // (slot n - SC) are free as well.
-        if (tile >= S && !warp_wait(&k_empty[slot], static_cast<uint32_t>(tile / S - 1) & 1u, abort_flag)) {
+        const int slot = kc.slot, sslot = sc.slot;
+        // Tile n - S's MMAs are done, so the accumulators of the stage two before its own had been
+        // read: with at most 4 tiles a stage, the scales of tile n - S - 12 = n - SC are free.
+        if (tile >= S && !warp_wait(&k_empty[slot], kc.par ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
@@ -306,6 +350,9 @@ __global__ void __launch_bounds__(kIxThreads, 1)
           if (F == kFP8 && id >= 0)
             bulk_g2s(scales + sslot * 128 + lane * BR, p.key_scales + z * p.ks_stride + yy, BR * 4, &sc_full[sslot]);
         }
+        ++in;
+        kc.step();
+        sc.step();
       }
     }
     if (ok) {      // end of the queue
@@ -321,11 +368,9 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     // never leave copies in flight behind us
     if (lane == 0) {
       volatile int no_abort[2] = {0, 0};
-      for (int64_t q = tile > S ? tile - S : 0; q < tile; ++q)
-        mbar_wait(&k_full[q % S], static_cast<uint32_t>(q / S) & 1u, no_abort);
-      for (int64_t q = tile > SC ? tile - SC : 0; q < tile; ++q)
-        mbar_wait(&sc_full[q % SC], static_cast<uint32_t>(q / SC) & 1u, no_abort);
-      for (int q = nseg > 2 ? nseg - 2 : 0; q < nseg; ++q) mbar_wait(&q_full[q & 1], (q >> 1) & 1, no_abort);
+      for (int q = tile > S ? tile - S : 0; q < tile; ++q) mbar_wait(&k_full[q % S], (q / S) & 1, no_abort);
+      for (int q = tile > SC ? tile - SC : 0; q < tile; ++q) mbar_wait(&sc_full[q % SC], (q / SC) & 1, no_abort);
+      for (int q = nseg > QB ? nseg - QB : 0; q < nseg; ++q) mbar_wait(&q_full[q % QB], (q / QB) & 1, no_abort);
     }
     __syncwarp();
     if (lane == 0 && errbits) set_device_error(p.err, errbits);
@@ -334,45 +379,53 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     if (lane == 0) {
       const uint64_t dK0 = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
       const uint64_t dQ0 = smem_desc(smem_u32(qs), 16, 1024, kSwizzle128B);
-      int64_t tile = 0;
-      bool ok = true, any = false;
+      Cursor<S> kc;
+      int stage = 0;
+      bool ok = true;
       for (int ns = 0; ok; ++ns) {
-        const int k = ns % kSegDepth;
+        const int k = ns % kSegDepth, qb = ns % QB;
         if (!mbar_wait(&seg_full[k], (ns / kSegDepth) & 1, abort_flag)) break;
         const int nt = segs[k].nt, nq = segs[k].nq;
         mbar_arrive(&seg_empty[k]);
         if (nt == 0) break;
-        if (!mbar_wait(&q_full[ns & 1], (ns >> 1) & 1, abort_flag)) break;
+        if (!mbar_wait(&q_full[qb], (ns / QB) & 1, abort_flag)) break;
         const int n = (nq * HP + 15) & ~15;      // columns: a multiple of 16
+        const int G = stage_tiles(nq * HP), gcols = kIxCols / G;
         const uint32_t idesc = F == kBF16 ? idesc_f16(128, n, 1, 1, 0, 0) : idesc_e4m3(128, n, 0, 0);
-        const uint64_t dQ = desc_add(dQ0, static_cast<uint32_t>(ns & 1) * (C::kQBytes >> 4));
-        for (int t = 0; t < nt; ++t, ++tile) {
-          const int slot = static_cast<int>(tile % S), buf = static_cast<int>(tile & 1);
-          if (!mbar_wait(&k_full[slot], static_cast<uint32_t>(tile / S) & 1u, abort_flag) ||
-              (tile >= 2 && !mbar_wait(&d_empty[buf], static_cast<uint32_t>((tile >> 1) - 1) & 1u, abort_flag))) {
+        const uint64_t dQ = desc_add(dQ0, static_cast<uint32_t>(qb) * (C::kQBytes >> 4));
+        for (int t = 0; ok && t < nt; t += G, ++stage) {
+          const int buf = stage & 1, g1 = min(G, nt - t);
+          if (stage >= 2 && !mbar_wait(&d_empty[buf], ((stage >> 1) - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint64_t dK = desc_add(dK0, static_cast<uint32_t>(slot) * (C::kTileBytes >> 4));
-#pragma unroll
-          for (int h = 0; h < HV; ++h)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t a = desc_add(dK, (h * 128 * 128 + kk * 32) >> 4);
-              const uint64_t bq = desc_add(dQ, (h * kIxCols * 128 + kk * 32) >> 4);
-              if (F == kBF16)
-                mma_f16_ss(tmem + buf * kIxCols, a, bq, idesc, h + kk > 0 ? 1u : 0u);
-              else
-                mma_f8_ss(tmem + buf * kIxCols, a, bq, idesc, h + kk > 0 ? 1u : 0u);
+          for (int g = 0; g < g1; ++g) {
+            if (!mbar_wait(&k_full[kc.slot], kc.par, abort_flag)) {
+              ok = false;
+              break;
             }
+            tc_fence_after();
+            const uint64_t dK = desc_add(dK0, static_cast<uint32_t>(kc.slot) * (C::kTileBytes >> 4));
+            const uint32_t d = tmem + buf * kIxCols + g * gcols;
+#pragma unroll
+            for (int h = 0; h < HV; ++h)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t a = desc_add(dK, (h * 128 * 128 + kk * 32) >> 4);
+                const uint64_t bq = desc_add(dQ, (h * kIxCols * 128 + kk * 32) >> 4);
+                if (F == kBF16)
+                  mma_f16_ss(d, a, bq, idesc, h + kk > 0 ? 1u : 0u);
+                else
+                  mma_f8_ss(d, a, bq, idesc, h + kk > 0 ? 1u : 0u);
+              }
+            mma_commit(&k_empty[kc.slot]);
+            kc.step();
+          }
           mma_commit(&d_full[buf]);
-          mma_commit(&k_empty[slot]);
-          if (t == nt - 1) mma_commit(&q_empty[ns & 1]);
-          any = true;
+          if (t + G >= nt) mma_commit(&q_empty[qb]);
         }
       }
-      if (any) {      // no product is in flight when the accumulators are freed
+      {      // no product is in flight when the accumulators are freed
         volatile int no_abort[2] = {0, 0};
         mma_commit(fin);
         mbar_wait(fin, 0, no_abort);
@@ -385,8 +438,15 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     const int key = 32 * quad + lane;             // TMEM lane = key of the tile
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16) + 64 * group;
     const int bt = p.block_tokens;
-    int64_t tile = 0;
+    float* wrow = reinterpret_cast<float*>(smem + C::kW) + (warp - 2) * (64 - kRegCols);
+    static_assert(64 - kRegCols == 32, "a lane writes one weight");
+    constexpr int NA = QW <= 2 ? 2 : 1;           // independent sums of a query
+    int stage = 0;
+    int sbase = 0;                                // scale slot of the stage's first tile, and its parity
+    uint32_t spar = 0;
     uint32_t uses[2] = {0, 0};                    // block maxima exchanged through red, per buffer
+    const int cap = static_cast<int>(min(p.cap, static_cast<int64_t>(0x7FFFFFFF)));
+    const int br_shift = 31 - __clz(p.BR), bt_shift = 31 - __clz(bt);
     bool ok = true;
     for (int ns = 0; ok; ++ns) {
       const int k = ns % kSegDepth;
@@ -395,35 +455,69 @@ __global__ void __launch_bounds__(kIxThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&seg_empty[k]);
       if (sg.nt == 0) break;
-      const bool has = group * QW < sg.nq;        // this group has queries
-      float w[64];
-      if (has) {
+      // this group's tile of a stage, and its queries
+      const int G = stage_tiles(sg.nq * HP), per = 4 / G;
+      const int g = group / per, q0 = (group % per) * QW;
+      const int nq = min(QW, sg.nq - q0);         // <= 0: the group has none
+      auto weight = [&](int c) -> float {         // 0 for padded heads and queries
+        const int q = c / HP, h = c % HP;
+        return q < nq && h < p.Hi ? __ldg(p.weights + static_cast<int64_t>(sg.t0 + q0 + q) * p.w_stride + h) : 0.f;
+      };
+      uint64_t w[kRegCols / 2];                   // of the first columns, in pairs
+      if (nq > 0) {
+        __syncwarp();
+        wrow[lane] = weight(kRegCols + lane);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          const int q = group * QW + c / HP, h = c % HP;
-          w[c] = (q < sg.nq && h < p.Hi) ? __ldg(p.weights + static_cast<int64_t>(sg.t0 + q) * p.w_stride + h) : 0.f;
-        }
+        for (int c = 0; c < kRegCols; c += 2) w[c / 2] = pack2(weight(c), weight(c + 1));
+        __syncwarp();
       }
-      for (int t = 0; t < sg.nt; ++t, ++tile) {
-        const int buf = static_cast<int>(tile & 1), sslot = static_cast<int>(tile % SC);
-        if (!warp_wait(&d_full[buf], static_cast<uint32_t>(tile >> 1) & 1u, abort_flag) ||
-            !warp_wait(&sc_full[sslot], static_cast<uint32_t>(tile / SC) & 1u, abort_flag)) {
+      float* out = p.scores + static_cast<int64_t>(sg.t0 + q0) * p.s_stride;
+      const int vis0 = sg.vis0 + q0;
+      for (int t = 0; t < sg.nt; t += G, ++stage) {
+        const int buf = stage & 1;
+        const int tiles = min(G, sg.nt - t);
+        const bool has = nq > 0 && g < tiles;
+        int ss = sbase + g;
+        uint32_t sp = spar;
+        if (ss >= SC) ss -= SC, sp ^= 1u;
+        sbase += tiles;
+        if (sbase >= SC) sbase -= SC, spar ^= 1u;
+        if (!warp_wait(&d_full[buf], (stage >> 1) & 1, abort_flag) || (has && !warp_wait(&sc_full[ss], sp, abort_flag))) {
           ok = false;
           break;
         }
         tc_fence_after();
+        const bool exchange = has && bt > 32;
         float v[QW];
         bool is_bad = false;
         if (has) {
+          uint64_t acc[QW][NA];
 #pragma unroll
-          for (int q = 0; q < QW; ++q) v[q] = 0.f;
+          for (int q = 0; q < QW; ++q)
+#pragma unroll
+            for (int a = 0; a < NA; ++a) acc[q][a] = 0;
 #pragma unroll
           for (int c0 = 0; c0 < 64; c0 += 16) {
             float d[16];
             tmem_ld16(tl + buf * kIxCols + c0, d);
             tmem_ld_wait();
+            if (c0 < kRegCols) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[(c0 + c) / HP] = fmaf(max_nan(d[c], 0.f), w[c0 + c], v[(c0 + c) / HP]);
+              for (int c = 0; c < 16; c += 2)
+                fma2(acc[(c0 + c) / HP][(c / 2) % NA], max_nan(d[c], 0.f), max_nan(d[c + 1], 0.f), w[((c0 + c) / 2) % (kRegCols / 2)]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 16; c += 4) {
+                const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(wrow + c0 - kRegCols + c);
+                fma2(acc[(c0 + c) / HP][0], max_nan(d[c], 0.f), max_nan(d[c + 1], 0.f), ww.x);
+                fma2(acc[(c0 + c) / HP][NA - 1], max_nan(d[c + 2], 0.f), max_nan(d[c + 3], 0.f), ww.y);
+              }
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < QW; ++q) {
+            v[q] = sum2(acc[q][0]);
+            if (NA == 2) v[q] += sum2(acc[q][NA - 1]);
           }
           // a key with infinities or NaN meets the zeros of the padded heads: sum the heads alone
           if (p.Hi < HP) {
@@ -440,43 +534,41 @@ __global__ void __launch_bounds__(kIxThreads, 1)
                   tmem_ld_wait();
 #pragma unroll
                   for (int c = 0; c < 8; ++c)
-                    if (c0 + c < p.Hi) v[q] = fmaf(max_nan(__uint_as_float(e[c]), 0.f), w[q * HP + c0 + c], v[q]);
+                    if (c0 + c < p.Hi) v[q] = fmaf(max_nan(__uint_as_float(e[c]), 0.f), weight(q * HP + c0 + c), v[q]);
                 }
               }
             }
           }
           if (F == kFP8) {
-            const float ks = scales[sslot * 128 + key];
+            const float ks = scales[ss * 128 + key];
 #pragma unroll
             for (int q = 0; q < QW; ++q) v[q] *= ks;
           }
-          is_bad = (bad[sslot] >> (key / p.BR)) & 1u;
+          is_bad = (bad[ss] >> (key >> br_shift)) & 1u;
         }
         // The accumulator is free once read; where warps exchange maxima below, the buffer's slot
         // of red is too, so the release waits for that.
         tc_fence_before();
         __syncwarp();
-        const bool exchange = has && bt > 32;
         if (lane == 0 && !exchange) mbar_arrive(&d_empty[buf]);
         if (!has) continue;
-        const int64_t pos = static_cast<int64_t>(sg.j0 + t) * 128 + key;
+        const int pos = (sg.j0 + t + g) * 128 + key;
+        float* row = out;
 #pragma unroll
-        for (int q = 0; q < QW; ++q) {
-          const int qi = group * QW + q;
-          if (qi >= sg.nq) break;
-          const int64_t vis = min(static_cast<int64_t>(sg.vis0) + qi, p.cap);
-          float* row = p.scores + static_cast<int64_t>(sg.t0 + qi) * p.s_stride;
+        for (int q = 0; q < QW; ++q, row += p.s_stride) {
+          if (q >= nq) break;
+          const bool seen = pos < min(vis0 + q, cap);
           float val = is_bad ? -CUDART_INF_F : v[q];
           if (bt == 1) {
-            if (pos < vis) row[pos] = val;
+            if (seen) row[pos] = val;
             continue;
           }
-          if (pos >= vis) val = -CUDART_INF_F;
+          if (!seen) val = -CUDART_INF_F;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1)
             if (o < bt) val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, o));
           if (!exchange) {
-            if ((lane & (bt - 1)) == 0 && pos < vis) row[pos / bt] = val;
+            if ((lane & (bt - 1)) == 0 && seen) row[pos >> bt_shift] = val;
           } else if (lane == 0) {
             red[(buf * 16 + group * 4 + quad) * 8 + q] = val;
           }
@@ -486,19 +578,16 @@ __global__ void __launch_bounds__(kIxThreads, 1)
           if (lane == 0) mbar_arrive(rf);
           const uint32_t par = uses[buf]++ & 1u;
           const int wb = bt >> 5;                 // warps of a block; its first one joins them
-          if (quad % wb == 0) {
+          if ((quad & (wb - 1)) == 0) {
             if (!warp_wait(rf, par, abort_flag)) {
               ok = false;
               break;
             }
-            const int qi = group * QW + lane;
-            const int64_t vis = min(static_cast<int64_t>(sg.vis0) + qi, p.cap);
-            const int64_t p0 = static_cast<int64_t>(sg.j0 + t) * 128 + 32 * quad;
-            if (lane < QW && qi < sg.nq && p0 < vis) {
+            if (lane < nq && pos - lane < min(vis0 + lane, cap)) {
               const float* r0 = red + (buf * 16 + group * 4 + quad) * 8 + lane;
-              float m = r0[0];
-              for (int o = 1; o < wb; ++o) m = max_nan(m, r0[8 * o]);
-              p.scores[static_cast<int64_t>(sg.t0 + qi) * p.s_stride + p0 / bt] = m;
+              float mx = r0[0];
+              for (int o = 1; o < wb; ++o) mx = max_nan(mx, r0[8 * o]);
+              out[lane * p.s_stride + ((pos - lane) >> bt_shift)] = mx;
             }
             __syncwarp();
           }
