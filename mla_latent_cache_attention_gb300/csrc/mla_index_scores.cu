@@ -18,7 +18,7 @@
 // tile has at most 128 or 64 columns (decode), so that the four epilogue groups always share it.
 //
 // Warps: 0 producer (TMA boxes of pages, lanes resolve page ids), 1 MMA issuer and TMEM owner, 
-// 2..17 four epilogue groups of four warps, one 64-column slice of the accumulator each.
+// 2..17 four epilogue groups of four warps.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -42,11 +42,6 @@ struct Segment {
   int b, pad0, pad1;
 };
 
-// Of a thread's 64 weights this many live in registers; the others are read from shared memory
-// for every tile, four by a broadcast load.  All 64 would not leave room for the accumulator's values
-// (18 warps have 96 registers each, and spills cost more than the loads).
-constexpr int kRegCols = 32;
-
 // Key tiles of a stage (one accumulator buffer): query tiles of few columns share it.
 __device__ __forceinline__ int stage_tiles(int cols) { return cols <= 64 ? 4 : cols <= 128 ? 2 : 1; }
 
@@ -62,12 +57,12 @@ struct IndexCfg {
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + kQB * kQBytes;
   static constexpr int kScale = kRing + kS * kTileBytes;
-  static constexpr int kRed = kScale + kSc * 512;               // block maxima of 16 warps x 8 queries
-  static constexpr int kW = kRed + 2 * 16 * 8 * 4;              // weights of 16 warps' last columns
-  static constexpr int kSeg = kW + 16 * (64 - kRegCols) * 4;
+  static constexpr int kRed = kScale + kSc * 512;               // block maxima: 2 buffers x 4 slices x 4 warps x 8 queries
+  static constexpr int kW = kRed + 2 * 16 * 8 * 4;              // weights of 16 warps' 128 columns
+  static constexpr int kSeg = kW + 16 * 128 * 4;
   static constexpr int kBad = kSeg + kSegDepth * 32;
   static constexpr int kBar = kBad + ((kSc * 4 + 7) & ~7);
-  static constexpr int kNumBars = 2 * kS + kSc + 8 + 2 * kSegDepth + 8 + 1;      // as carved in the kernel
+  static constexpr int kNumBars = 2 * kS + kSc + 8 + 2 * kSegDepth + 4 + 1;      // as carved in the kernel
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kAlloc = kMisc + 64 + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
@@ -129,15 +124,16 @@ __device__ __forceinline__ void fma2(uint64_t& acc, float x0, float x1, uint64_t
   asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(x), "l"(w));
 }
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t x;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
-  return x;
-}
 __device__ __forceinline__ float sum2(uint64_t a) {
   float x, y;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
   return x + y;
+}
+
+// Bounded wait of a whole warp: one look by every lane where the phase has completed already.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait(bar, parity, abort_flag);
 }
 
 template <int F, int HP>
@@ -166,8 +162,8 @@ __global__ void __launch_bounds__(kIxThreads, 1)
   uint64_t* d_empty = d_full + 2;              // [2] accumulator read
   uint64_t* seg_full = d_empty + 2;
   uint64_t* seg_empty = seg_full + kSegDepth;
-  uint64_t* red_full = seg_empty + kSegDepth;  // [4 groups][2] block maxima of the group's warps written
-  uint64_t* fin = red_full + 8;
+  uint64_t* red_full = seg_empty + kSegDepth;  // [4] block maxima of a group's warps written
+  uint64_t* fin = red_full + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 8);
   int64_t* start = reinterpret_cast<int64_t*>(smem + C::kMisc + 16);      // [0] first unit's request, [1] its offset, [2] units
@@ -184,13 +180,13 @@ __global__ void __launch_bounds__(kIxThreads, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 16);
+      mbar_init(&d_empty[i], 8);
     }
     for (int i = 0; i < kSegDepth; ++i) {
       mbar_init(&seg_full[i], 1);
       mbar_init(&seg_empty[i], 17);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(&red_full[i], 4);
+    for (int i = 0; i < 4; ++i) mbar_init(&red_full[i], 4);
     mbar_init(fin, 1);
     abort_flag[0] = 0;
     abort_flag[1] = 0;
@@ -249,7 +245,9 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     int b = static_cast<int>(start[0]);
     int64_t x = start[1], rem = hi - lo;
     const int BR = p.BR, SP = 128 / BR;            // page slices of BR rows, SP of them a tile
+    const int SB = p.block_size / BR;              // slices of a page
     const int TG = 32 / SP;                        // key tiles covered by one page lookup of the warp
+    const uint32_t SM = (1u << SP) - 1;
     int tile = 0;                                  // key tiles issued
     Cursor<S> kc;
     Cursor<SC> sc;
@@ -307,48 +305,50 @@ __global__ void __launch_bounds__(kIxThreads, 1)
           tma_load_3d(qs + qb * C::kQBytes + h * kIxCols * 128, &tm_q, 128 * h, 0, sg.t0, &q_full[qb]);
       }
       ++nseg;
-      // page ids of the slices j SP .. (j + TG) SP - 1, one per lane, looked up a group ahead
-      auto lookup = [&](int j) -> int {
-        const int64_t kp = (static_cast<int64_t>(j) * SP + lane) * BR;
-        if (j >= sg.j0 + sg.nt || kp >= seen) return -2;                  // nothing to read
-        const int64_t col = kp / p.block_size;
-        const int id = col < p.bt_cols ? p.block_table[static_cast<int64_t>(b) * p.bt_stride + col] : -1;
+      // Pages of the slices j SP .. (j + TG) SP - 1, one per lane, looked up a group of TG tiles ahead;
+      // a lane then issues its own slice's copies when its tile comes.
+      const int s_end = static_cast<int>((seen + BR - 1) / BR);          // slices with a visible key
+      auto lookup = [&](int j, int& y) -> int {
+        const int sl = j * SP + lane, col = SB == 1 ? sl : sl / SB;
+        y = SB == 1 ? 0 : (sl - col * SB) * BR;
+        if (j >= sg.j0 + sg.nt || sl >= s_end) return -2;                 // nothing to read
+        const int id = col < p.bt_cols ? p.block_table[b * p.bt_stride + col] : -1;
         return (id < 0 || id >= p.num_blocks) ? -1 : id;
       };
-      int cur = lookup(sg.j0), nxt = -2;
-      int in = 0;      // tile of the lookup group
-      for (int t = 0; t < sg.nt && ok; ++t, ++tile) {
-        if (in == TG) in = 0;
-        if (in == 0) {
-          if (t > 0) cur = nxt;
-          nxt = lookup(sg.j0 + t + TG);
+      int cur, cy, nxt = 0, ny = 0;
+      nxt = lookup(sg.j0, ny);
+      uint32_t bad_m = 0, good_m = 0;
+      int in = TG;      // tile of the lookup group
+      for (int t = 0; t < sg.nt; ++t, ++tile) {
+        if (in == TG) {
+          in = 0;
+          cur = nxt;
+          cy = ny;
+          bad_m = __ballot_sync(0xFFFFFFFFu, cur == -1);
+          good_m = __ballot_sync(0xFFFFFFFFu, cur >= 0);
+          if (bad_m) errbits |= 2u;
+          nxt = lookup(sg.j0 + t + TG, ny);
         }
         const int slot = kc.slot, sslot = sc.slot;
         // Tile n - S's MMAs are done, so the accumulators of the stage two before its own had been
         // read: with at most 4 tiles a stage, the scales of tile n - S - 12 = n - SC are free.
-        if (tile >= S && !warp_wait(&k_empty[slot], kc.par ^ 1u, abort_flag)) {
+        if (tile >= S && !wait_all(&k_empty[slot], kc.par ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
-        const int id = __shfl_sync(0xFFFFFFFFu, cur, in * SP + (lane < SP ? lane : 0));
-        const bool mine = lane < SP;
-        const uint32_t bm = __ballot_sync(0xFFFFFFFFu, mine && id == -1);
-        const uint32_t gm = __ballot_sync(0xFFFFFFFFu, mine && id >= 0);
-        if (bm) errbits |= 2u;
         if (lane == 0) {
-          bad[sslot] = bm;
+          bad[sslot] = (bad_m >> (in * SP)) & SM;
           mbar_arrive_expect_tx(&k_full[slot], C::kTileBytes);
-          mbar_arrive_expect_tx(&sc_full[sslot], F == kFP8 ? __popc(gm) * BR * 4 : 0);
+          mbar_arrive_expect_tx(&sc_full[sslot], F == kFP8 ? __popc((good_m >> (in * SP)) & SM) * BR * 4 : 0);
         }
         __syncwarp();
-        if (mine) {
-          const int64_t kp = (static_cast<int64_t>(sg.j0 + t) * SP + lane) * BR;
-          const int yy = static_cast<int>(kp % p.block_size), z = id >= 0 ? id : p.num_blocks;
+        if (lane / SP == in) {
+          const int row = (lane - in * SP) * BR, z = cur >= 0 ? cur : p.num_blocks;
 #pragma unroll
           for (int h = 0; h < HV; ++h)
-            tma_load_3d(ring + slot * C::kTileBytes + h * 128 * 128 + lane * BR * 128, &tm_k, 128 * h, yy, z, &k_full[slot]);
-          if (F == kFP8 && id >= 0)
-            bulk_g2s(scales + sslot * 128 + lane * BR, p.key_scales + z * p.ks_stride + yy, BR * 4, &sc_full[sslot]);
+            tma_load_3d(ring + slot * C::kTileBytes + h * 128 * 128 + row * 128, &tm_k, 128 * h, cy, z, &k_full[slot]);
+          if (F == kFP8 && cur >= 0)
+            bulk_g2s(scales + sslot * 128 + row, p.key_scales + z * p.ks_stride + cy, BR * 4, &sc_full[sslot]);
         }
         ++in;
         kc.step();
@@ -434,164 +434,188 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ epilogue
-    const int quad = warp & 3, group = (warp - 2) >> 2;
+    // Two sets of two groups: a set takes every second stage (one accumulator buffer), so that one
+    // set's waits hide behind the other's work; a group takes two 64-column slices of the buffer.
+    const int quad = warp & 3, group = (warp - 2) >> 2, set = group >> 1;
     const int key = 32 * quad + lane;             // TMEM lane = key of the tile
-    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16) + 64 * group;
-    const int bt = p.block_tokens;
-    float* wrow = reinterpret_cast<float*>(smem + C::kW) + (warp - 2) * (64 - kRegCols);
-    static_assert(64 - kRegCols == 32, "a lane writes one weight");
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16) + set * kIxCols + (group & 1) * 128;
+    float* wrow = reinterpret_cast<float*>(smem + C::kW) + (warp - 2) * 128;
+    float* red_g = red + (group * 2 * 4 + quad) * 8;          // slice j at + 32 j
+    const bool padded = p.Hi < HP;
+    const int bt = p.block_tokens, br_shift = 31 - __clz(p.BR), bt_shift = 31 - __clz(bt);
+    const int cap = static_cast<int>(min(p.cap, static_cast<int64_t>(0x7FFFFFFF)));
     constexpr int NA = QW <= 2 ? 2 : 1;           // independent sums of a query
+    constexpr int CH = 16;                        // columns of a load
     int stage = 0;
     int sbase = 0;                                // scale slot of the stage's first tile, and its parity
     uint32_t spar = 0;
-    uint32_t uses[2] = {0, 0};                    // block maxima exchanged through red, per buffer
-    const int cap = static_cast<int>(min(p.cap, static_cast<int64_t>(0x7FFFFFFF)));
-    const int br_shift = 31 - __clz(p.BR), bt_shift = 31 - __clz(bt);
+    uint32_t uses = 0;                            // block maxima exchanged through red
     bool ok = true;
     for (int ns = 0; ok; ++ns) {
       const int k = ns % kSegDepth;
-      if (!warp_wait(&seg_full[k], (ns / kSegDepth) & 1, abort_flag)) break;
+      if (!wait_all(&seg_full[k], (ns / kSegDepth) & 1, abort_flag)) break;
       const Segment sg = segs[k];
       __syncwarp();
       if (lane == 0) mbar_arrive(&seg_empty[k]);
       if (sg.nt == 0) break;
-      // this group's tile of a stage, and its queries
+      // tile of a stage and queries of this group's two slices
       const int G = stage_tiles(sg.nq * HP), per = 4 / G;
-      const int g = group / per, q0 = (group % per) * QW;
-      const int nq = min(QW, sg.nq - q0);         // <= 0: the group has none
-      auto weight = [&](int c) -> float {         // 0 for padded heads and queries
+      int g[2] = {}, q0[2] = {}, nq[2] = {};
+      auto weight = [&](int j, int c) -> float {  // 0 for padded heads and queries
         const int q = c / HP, h = c % HP;
-        return q < nq && h < p.Hi ? __ldg(p.weights + static_cast<int64_t>(sg.t0 + q0 + q) * p.w_stride + h) : 0.f;
+        return q < nq[j] && h < p.Hi ? __ldg(p.weights + static_cast<int64_t>(sg.t0 + q0[j] + q) * p.w_stride + h) : 0.f;
       };
-      uint64_t w[kRegCols / 2];                   // of the first columns, in pairs
-      if (nq > 0) {
-        __syncwarp();
-        wrow[lane] = weight(kRegCols + lane);
+      __syncwarp();
 #pragma unroll
-        for (int c = 0; c < kRegCols; c += 2) w[c / 2] = pack2(weight(c), weight(c + 1));
-        __syncwarp();
+      for (int j = 0; j < 2; ++j) {
+        const int sl = (group & 1) * 2 + j;
+        g[j] = sl / per;
+        q0[j] = (sl % per) * QW;
+        nq[j] = max(min(QW, sg.nq - q0[j]), 0);
+        wrow[64 * j + lane] = weight(j, lane);
+        wrow[64 * j + 32 + lane] = weight(j, 32 + lane);
       }
-      float* out = p.scores + static_cast<int64_t>(sg.t0 + q0) * p.s_stride;
-      const int vis0 = sg.vis0 + q0;
+      __syncwarp();
       for (int t = 0; t < sg.nt; t += G, ++stage) {
-        const int buf = stage & 1;
         const int tiles = min(G, sg.nt - t);
-        const bool has = nq > 0 && g < tiles;
-        int ss = sbase + g;
-        uint32_t sp = spar;
-        if (ss >= SC) ss -= SC, sp ^= 1u;
+        const int sb = sbase;
+        const uint32_t sp = spar;
         sbase += tiles;
         if (sbase >= SC) sbase -= SC, spar ^= 1u;
-        if (!warp_wait(&d_full[buf], (stage >> 1) & 1, abort_flag) || (has && !warp_wait(&sc_full[ss], sp, abort_flag))) {
+        if ((stage & 1) != set) continue;
+        const bool has0 = nq[0] > 0 && g[0] < tiles, has1 = nq[1] > 0 && g[1] < tiles;      // has1 implies has0
+        int ss[2];
+        bool w = wait_all(&d_full[set], (stage >> 1) & 1, abort_flag);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          ss[j] = sb + g[j];
+          uint32_t par = sp;
+          if (ss[j] >= SC) ss[j] -= SC, par ^= 1u;
+          if (j == 0 ? has0 : has1 && g[1] != g[0]) w = w && wait_all(&sc_full[ss[j]], par, abort_flag);
+        }
+        if (!w) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const bool exchange = has && bt > 32;
-        float v[QW];
-        bool is_bad = false;
-        if (has) {
+        // sums of the slices: 16 columns at a time, the next ones loaded meanwhile
+        float v[2][QW];
+        float d[2][CH];
+        auto release = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&d_empty[set]);
+        };
+        auto chunks = [&](int j, bool more) {     // more: another slice follows
           uint64_t acc[QW][NA];
 #pragma unroll
           for (int q = 0; q < QW; ++q)
 #pragma unroll
             for (int a = 0; a < NA; ++a) acc[q][a] = 0;
 #pragma unroll
-          for (int c0 = 0; c0 < 64; c0 += 16) {
-            float d[16];
-            tmem_ld16(tl + buf * kIxCols + c0, d);
+          for (int u = 0; u < 64 / CH; ++u) {
             tmem_ld_wait();
-            if (c0 < kRegCols) {
+            if (u + 1 < 64 / CH)
+              tmem_ld_n<CH>(tl + 64 * j + CH * (u + 1), d[(u + 1) & 1]);
+            else if (more)
+              tmem_ld_n<CH>(tl + 64 * (j + 1), d[0]);
+            else if (!padded && bt <= 32)
+              release();                          // everything is in registers
 #pragma unroll
-              for (int c = 0; c < 16; c += 2)
-                fma2(acc[(c0 + c) / HP][(c / 2) % NA], max_nan(d[c], 0.f), max_nan(d[c + 1], 0.f), w[((c0 + c) / 2) % (kRegCols / 2)]);
-            } else {
-#pragma unroll
-              for (int c = 0; c < 16; c += 4) {
-                const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(wrow + c0 - kRegCols + c);
-                fma2(acc[(c0 + c) / HP][0], max_nan(d[c], 0.f), max_nan(d[c + 1], 0.f), ww.x);
-                fma2(acc[(c0 + c) / HP][NA - 1], max_nan(d[c + 2], 0.f), max_nan(d[c + 3], 0.f), ww.y);
-              }
+            for (int c = 0; c < CH; c += 4) {
+              const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(wrow + 64 * j + CH * u + c);
+              const float* x = d[u & 1] + c;
+              fma2(acc[(CH * u + c) / HP][0], max_nan(x[0], 0.f), max_nan(x[1], 0.f), ww.x);
+              fma2(acc[(CH * u + c) / HP][NA - 1], max_nan(x[2], 0.f), max_nan(x[3], 0.f), ww.y);
             }
           }
 #pragma unroll
           for (int q = 0; q < QW; ++q) {
-            v[q] = sum2(acc[q][0]);
-            if (NA == 2) v[q] += sum2(acc[q][NA - 1]);
+            v[j][q] = sum2(acc[q][0]);
+            if (NA == 2) v[j][q] += sum2(acc[q][NA - 1]);
           }
-          // a key with infinities or NaN meets the zeros of the padded heads: sum the heads alone
-          if (p.Hi < HP) {
+        };
+        if (has0) {
+          tmem_ld_n<CH>(tl, d[0]);
+          chunks(0, has1);
+          if (has1) chunks(1, false);
+        } else {
+          release();
+          continue;
+        }
+        const bool exchange = bt > 32;
+        // a key with infinities or NaN meets the zeros of the padded heads: sum the heads alone
+        if (padded) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (j == 1 && !has1) break;
 #pragma unroll
             for (int q = 0; q < QW; ++q) {
-              if (__any_sync(0xFFFFFFFFu, v[q] != v[q])) {
-                v[q] = 0.f;
-#pragma unroll
-                for (int c0 = 0; c0 < HP; c0 += 8) {
-                  uint32_t e[8];
-                  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                               : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3]), "=r"(e[4]), "=r"(e[5]), "=r"(e[6]), "=r"(e[7])
-                               : "r"(tl + buf * kIxCols + q * HP + c0));
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int c = 0; c < 8; ++c)
-                    if (c0 + c < p.Hi) v[q] = fmaf(max_nan(__uint_as_float(e[c]), 0.f), weight(q * HP + c0 + c), v[q]);
-                }
+              if (!__any_sync(0xFFFFFFFFu, v[j][q] != v[j][q])) continue;
+              float s = 0.f;
+#pragma unroll 1
+              for (int h = 0; h < p.Hi; ++h) {
+                uint32_t e;
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(e) : "r"(tl + 64 * j + q * HP + h));
+                tmem_ld_wait();
+                s = fmaf(max_nan(__uint_as_float(e), 0.f), wrow[64 * j + q * HP + h], s);
               }
+              v[j][q] = s;
             }
           }
-          if (F == kFP8) {
-            const float ks = scales[ss * 128 + key];
-#pragma unroll
-            for (int q = 0; q < QW; ++q) v[q] *= ks;
-          }
-          is_bad = (bad[ss] >> (key >> br_shift)) & 1u;
+          if (!exchange) release();
         }
-        // The accumulator is free once read; where warps exchange maxima below, the buffer's slot
-        // of red is too, so the release waits for that.
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && !exchange) mbar_arrive(&d_empty[buf]);
-        if (!has) continue;
-        const int pos = (sg.j0 + t + g) * 128 + key;
-        float* row = out;
 #pragma unroll
-        for (int q = 0; q < QW; ++q, row += p.s_stride) {
-          if (q >= nq) break;
-          const bool seen = pos < min(vis0 + q, cap);
-          float val = is_bad ? -CUDART_INF_F : v[q];
-          if (bt == 1) {
-            if (seen) row[pos] = val;
-            continue;
-          }
-          if (!seen) val = -CUDART_INF_F;
+        for (int j = 0; j < 2; ++j) {
+          if (j == 1 && !has1) break;
+          const float ks = F == kFP8 ? scales[ss[j] * 128 + key] : 1.f;
+          const uint32_t bm = bad[ss[j]];
+          const bool is_bad = bm && ((bm >> (key >> br_shift)) & 1u);
+          const int pos = (sg.j0 + t + g[j]) * 128 + key;
+          const int vis0 = sg.vis0 + q0[j];
+          float* row = p.scores + static_cast<int64_t>(sg.t0 + q0[j]) * p.s_stride;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1)
-            if (o < bt) val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, o));
-          if (!exchange) {
-            if ((lane & (bt - 1)) == 0 && seen) row[pos >> bt_shift] = val;
-          } else if (lane == 0) {
-            red[(buf * 16 + group * 4 + quad) * 8 + q] = val;
+          for (int q = 0; q < QW; ++q, row += p.s_stride) {
+            if (q >= nq[j]) break;
+            const bool seen = pos < min(vis0 + q, cap);
+            float val = is_bad ? -CUDART_INF_F : F == kFP8 ? v[j][q] * ks : v[j][q];
+            if (bt == 1) {
+              if (seen) row[pos] = val;
+              continue;
+            }
+            if (!seen) val = -CUDART_INF_F;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+              if (o < bt) val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, o));
+            if (!exchange) {
+              if ((lane & (bt - 1)) == 0 && seen) row[pos >> bt_shift] = val;
+            } else if (lane == 0) {
+              red_g[32 * j + q] = val;
+            }
           }
         }
         if (exchange) {       // blocks of 64 or 128 keys: two or four warps of the group
-          uint64_t* rf = &red_full[group * 2 + buf];
-          if (lane == 0) mbar_arrive(rf);
-          const uint32_t par = uses[buf]++ & 1u;
+          if (lane == 0) mbar_arrive(&red_full[group]);
+          const uint32_t par = uses++ & 1u;
           const int wb = bt >> 5;                 // warps of a block; its first one joins them
           if ((quad & (wb - 1)) == 0) {
-            if (!warp_wait(rf, par, abort_flag)) {
+            if (!wait_all(&red_full[group], par, abort_flag)) {
               ok = false;
               break;
             }
-            if (lane < nq && pos - lane < min(vis0 + lane, cap)) {
-              const float* r0 = red + (buf * 16 + group * 4 + quad) * 8 + lane;
-              float mx = r0[0];
-              for (int o = 1; o < wb; ++o) mx = max_nan(mx, r0[8 * o]);
-              out[lane * p.s_stride + ((pos - lane) >> bt_shift)] = mx;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (j == 1 && !has1) break;
+              const int p0 = (sg.j0 + t + g[j]) * 128 + 32 * quad;
+              if (lane < nq[j] && p0 < min(sg.vis0 + q0[j] + lane, cap)) {
+                float mx = red_g[32 * j + lane];
+                for (int o = 1; o < wb; ++o) mx = max_nan(mx, red_g[32 * j + 8 * o + lane]);
+                p.scores[static_cast<int64_t>(sg.t0 + q0[j] + lane) * p.s_stride + (p0 >> bt_shift)] = mx;
+              }
             }
-            __syncwarp();
           }
-          if (lane == 0) mbar_arrive(&d_empty[buf]);
+          // red is free with the buffer: written again only for the stage that next uses it
+          release();
         }
       }
     }
