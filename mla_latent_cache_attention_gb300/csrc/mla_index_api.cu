@@ -202,7 +202,8 @@ extern "C" int mla_index_scores(const void* q, int64_t q_s0, int64_t q_s1, const
   p.block_size = block_size;
   p.BR = rows;
   p.block_tokens = block_tokens;
-  p.cap = width > (int64_t(1) << 31) / block_tokens ? (int64_t(1) << 31) : width * block_tokens;
+  constexpr int64_t kMostKeys = (int64_t(1) << 31) - 1024;      // positions and tile edges stay in 32 bits
+  p.cap = width > kMostKeys / block_tokens ? kMostKeys : width * block_tokens;
   p.scores = scores;
   p.s_stride = s_stride;
   p.err = d->err;

@@ -62,7 +62,7 @@ struct IndexCfg {
   static constexpr int kSeg = kW + 16 * 128 * 4;
   static constexpr int kBad = kSeg + kSegDepth * 32;
   static constexpr int kBar = kBad + ((kSc * 4 + 7) & ~7);
-  static constexpr int kNumBars = 2 * kS + kSc + 8 + 2 * kSegDepth + 4 + 1;      // as carved in the kernel
+  static constexpr int kNumBars = 2 * kS + 8 + 2 * kSegDepth + 4 + 1;      // as carved in the kernel
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kAlloc = kMisc + 64 + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
@@ -130,6 +130,13 @@ __device__ __forceinline__ float sum2(uint64_t a) {
   return x + y;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+
 // Bounded wait of a whole warp: one look by every lane where the phase has completed already.
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
@@ -153,10 +160,9 @@ __global__ void __launch_bounds__(kIxThreads, 1)
   Segment* segs = reinterpret_cast<Segment*>(smem + C::kSeg);
   uint32_t* bad = reinterpret_cast<uint32_t*>(smem + C::kBad);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar);
-  uint64_t* k_full = bars;                     // [S] key tile landed
+  uint64_t* k_full = bars;                     // [S] key tile and its scales landed
   uint64_t* k_empty = k_full + S;              // [S] its MMAs are done
-  uint64_t* sc_full = k_empty + S;             // [SC] scales and bad-page mask of a tile
-  uint64_t* q_full = sc_full + SC;             // [2]
+  uint64_t* q_full = k_empty + S;              // [2]
   uint64_t* q_empty = q_full + 2;              // [2]
   uint64_t* d_full = q_empty + 2;              // [2] accumulator ready
   uint64_t* d_empty = d_full + 2;              // [2] accumulator read
@@ -175,11 +181,10 @@ __global__ void __launch_bounds__(kIxThreads, 1)
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
     }
-    for (int i = 0; i < SC; ++i) mbar_init(&sc_full[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
-      mbar_init(&d_full[i], 1);
+      mbar_init(&d_full[i], 2);      // the MMAs, and the issuer's own arrival (see there)
       mbar_init(&d_empty[i], 8);
     }
     for (int i = 0; i < kSegDepth; ++i) {
@@ -338,8 +343,7 @@ __global__ void __launch_bounds__(kIxThreads, 1)
         }
         if (lane == 0) {
           bad[sslot] = (bad_m >> (in * SP)) & SM;
-          mbar_arrive_expect_tx(&k_full[slot], C::kTileBytes);
-          mbar_arrive_expect_tx(&sc_full[sslot], F == kFP8 ? __popc((good_m >> (in * SP)) & SM) * BR * 4 : 0);
+          mbar_arrive_expect_tx(&k_full[slot], C::kTileBytes + (F == kFP8 ? __popc((good_m >> (in * SP)) & SM) * BR * 4 : 0));
         }
         __syncwarp();
         if (lane / SP == in) {
@@ -348,7 +352,7 @@ __global__ void __launch_bounds__(kIxThreads, 1)
           for (int h = 0; h < HV; ++h)
             tma_load_3d(ring + slot * C::kTileBytes + h * 128 * 128 + row * 128, &tm_k, 128 * h, cy, z, &k_full[slot]);
           if (F == kFP8 && cur >= 0)
-            bulk_g2s(scales + sslot * 128 + row, p.key_scales + z * p.ks_stride + cy, BR * 4, &sc_full[sslot]);
+            bulk_g2s(scales + sslot * 128 + row, p.key_scales + z * p.ks_stride + cy, BR * 4, &k_full[slot]);
         }
         ++in;
         kc.step();
@@ -369,67 +373,78 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     if (lane == 0) {
       volatile int no_abort[2] = {0, 0};
       for (int q = tile > S ? tile - S : 0; q < tile; ++q) mbar_wait(&k_full[q % S], (q / S) & 1, no_abort);
-      for (int q = tile > SC ? tile - SC : 0; q < tile; ++q) mbar_wait(&sc_full[q % SC], (q / SC) & 1, no_abort);
       for (int q = nseg > QB ? nseg - QB : 0; q < nseg; ++q) mbar_wait(&q_full[q % QB], (q / QB) & 1, no_abort);
     }
     __syncwarp();
     if (lane == 0 && errbits) set_device_error(p.err, errbits);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint64_t dK0 = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
-      const uint64_t dQ0 = smem_desc(smem_u32(qs), 16, 1024, kSwizzle128B);
-      Cursor<S> kc;
-      int stage = 0;
-      bool ok = true;
-      for (int ns = 0; ok; ++ns) {
-        const int k = ns % kSegDepth, qb = ns % QB;
-        if (!mbar_wait(&seg_full[k], (ns / kSegDepth) & 1, abort_flag)) break;
-        const int nt = segs[k].nt, nq = segs[k].nq;
-        mbar_arrive(&seg_empty[k]);
-        if (nt == 0) break;
-        if (!mbar_wait(&q_full[qb], (ns / QB) & 1, abort_flag)) break;
-        const int n = (nq * HP + 15) & ~15;      // columns: a multiple of 16
-        const int G = stage_tiles(nq * HP), gcols = kIxCols / G;
-        const uint32_t idesc = F == kBF16 ? idesc_f16(128, n, 1, 1, 0, 0) : idesc_e4m3(128, n, 0, 0);
-        const uint64_t dQ = desc_add(dQ0, static_cast<uint32_t>(qb) * (C::kQBytes >> 4));
-        for (int t = 0; ok && t < nt; t += G, ++stage) {
-          const int buf = stage & 1, g1 = min(G, nt - t);
-          if (stage >= 2 && !mbar_wait(&d_empty[buf], ((stage >> 1) - 1) & 1, abort_flag)) {
+    // The whole warp walks the loop and one elected lane issues: addresses and descriptors then stay
+    // warp-uniform (from a single-lane branch every operand of an MMA is moved to a uniform register
+    // first, and this warp, which shares its scheduler with four busy ones, set the kernel's pace).
+    const bool leader = elect_one();
+    const uint32_t hi_desc = static_cast<uint32_t>(smem_desc(0, 16, 1024, kSwizzle128B) >> 32);
+    const uint32_t dK0 = static_cast<uint32_t>(smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B));
+    const uint32_t dQ0 = static_cast<uint32_t>(smem_desc(smem_u32(qs), 16, 1024, kSwizzle128B));
+    auto desc = [&](uint32_t lo) -> uint64_t { return static_cast<uint64_t>(hi_desc) << 32 | lo; };
+    Cursor<S> kc;
+    uint32_t stage = 0;
+    bool ok = true;
+    for (uint32_t ns = 0; ok; ++ns) {
+      const uint32_t k = ns % kSegDepth, qb = ns % QB;
+      if (!wait_all(&seg_full[k], (ns / kSegDepth) & 1, abort_flag)) break;
+      const int nt = __shfl_sync(0xFFFFFFFFu, segs[k].nt, 0), nq = __shfl_sync(0xFFFFFFFFu, segs[k].nq, 0);
+      if (leader) mbar_arrive(&seg_empty[k]);
+      if (nt == 0) break;
+      if (!wait_all(&q_full[qb], (ns / QB) & 1, abort_flag)) break;
+      const int n = (nq * HP + 15) & ~15;      // columns: a multiple of 16
+      const int G = stage_tiles(nq * HP), gcols = kIxCols / G;
+      const uint32_t idesc = F == kBF16 ? idesc_f16(128, n, 1, 1, 0, 0) : idesc_e4m3(128, n, 0, 0);
+      const uint32_t dQ = dQ0 + qb * (C::kQBytes >> 4);
+      for (int t = 0; ok && t < nt; t += G, ++stage) {
+        const uint32_t buf = stage & 1;
+        const int g1 = min(G, nt - t);
+        if (stage >= 2 && !wait_all(&d_empty[buf], ((stage >> 1) - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        for (int g = 0; g < g1; ++g) {
+          if (!wait_all(&k_full[kc.slot], kc.par, abort_flag)) {
             ok = false;
             break;
           }
-          for (int g = 0; g < g1; ++g) {
-            if (!mbar_wait(&k_full[kc.slot], kc.par, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t dK = desc_add(dK0, static_cast<uint32_t>(kc.slot) * (C::kTileBytes >> 4));
-            const uint32_t d = tmem + buf * kIxCols + g * gcols;
+          tc_fence_after();
+          const uint32_t dK = dK0 + static_cast<uint32_t>(kc.slot) * (C::kTileBytes >> 4);
+          const uint32_t d = tmem + buf * kIxCols + g * gcols;
+          if (leader) {
 #pragma unroll
             for (int h = 0; h < HV; ++h)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t a = desc_add(dK, (h * 128 * 128 + kk * 32) >> 4);
-                const uint64_t bq = desc_add(dQ, (h * kIxCols * 128 + kk * 32) >> 4);
+                const uint64_t a = desc(dK + ((h * 128 * 128 + kk * 32) >> 4));
+                const uint64_t bq = desc(dQ + ((h * kIxCols * 128 + kk * 32) >> 4));
                 if (F == kBF16)
                   mma_f16_ss(d, a, bq, idesc, h + kk > 0 ? 1u : 0u);
                 else
                   mma_f8_ss(d, a, bq, idesc, h + kk > 0 ? 1u : 0u);
               }
             mma_commit(&k_empty[kc.slot]);
-            kc.step();
           }
+          kc.step();
+        }
+        if (leader) {
           mma_commit(&d_full[buf]);
+          // the scales and bad-page masks that came with the key tiles reach the epilogue by this
+          // thread's release (it has seen k_full)
+          mbar_arrive(&d_full[buf]);
           if (t + G >= nt) mma_commit(&q_empty[qb]);
         }
       }
-      {      // no product is in flight when the accumulators are freed
-        volatile int no_abort[2] = {0, 0};
-        mma_commit(fin);
-        mbar_wait(fin, 0, no_abort);
-      }
+    }
+    if (leader) {      // no product is in flight when the accumulators are freed
+      volatile int no_abort[2] = {0, 0};
+      mma_commit(fin);
+      mbar_wait(fin, 0, no_abort);
     }
     __syncwarp();
   } else {
@@ -442,17 +457,18 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     float* wrow = reinterpret_cast<float*>(smem + C::kW) + (warp - 2) * 128;
     float* red_g = red + (group * 2 * 4 + quad) * 8;          // slice j at + 32 j
     const bool padded = p.Hi < HP;
+    const bool early = !padded && p.block_tokens <= 32;       // nothing of the stage is needed after its columns
     const int bt = p.block_tokens, br_shift = 31 - __clz(p.BR), bt_shift = 31 - __clz(bt);
     const int cap = static_cast<int>(min(p.cap, static_cast<int64_t>(0x7FFFFFFF)));
     constexpr int NA = QW <= 2 ? 2 : 1;           // independent sums of a query
     constexpr int CH = 16;                        // columns of a load
-    int stage = 0;
-    int sbase = 0;                                // scale slot of the stage's first tile, and its parity
-    uint32_t spar = 0;
+    uint32_t stage = 0;                           // stages before the segment
+    int sbase = 0;                                // scale slot of the segment's first tile
+    uint32_t full_par = 0;                        // parity of the set's next stage
     uint32_t uses = 0;                            // block maxima exchanged through red
     bool ok = true;
-    for (int ns = 0; ok; ++ns) {
-      const int k = ns % kSegDepth;
+    for (uint32_t ns = 0; ok; ++ns) {
+      const uint32_t k = ns % kSegDepth;
       if (!wait_all(&seg_full[k], (ns / kSegDepth) & 1, abort_flag)) break;
       const Segment sg = segs[k];
       __syncwarp();
@@ -461,6 +477,8 @@ __global__ void __launch_bounds__(kIxThreads, 1)
       // tile of a stage and queries of this group's two slices
       const int G = stage_tiles(sg.nq * HP), per = 4 / G;
       int g[2] = {}, q0[2] = {}, nq[2] = {};
+      int lim[2] = {};                            // keys from the thread's first one that its first query sees
+      float* row[2] = {};                         // where its first score goes
       auto weight = [&](int j, int c) -> float {  // 0 for padded heads and queries
         const int q = c / HP, h = c % HP;
         return q < nq[j] && h < p.Hi ? __ldg(p.weights + static_cast<int64_t>(sg.t0 + q0[j] + q) * p.w_stride + h) : 0.f;
@@ -472,31 +490,26 @@ __global__ void __launch_bounds__(kIxThreads, 1)
         g[j] = sl / per;
         q0[j] = (sl % per) * QW;
         nq[j] = max(min(QW, sg.nq - q0[j]), 0);
+        const int first = (sg.j0 + g[j]) * 128 + key;
+        lim[j] = min(sg.vis0 + q0[j], cap) - first;
+        row[j] = p.scores + static_cast<int64_t>(sg.t0 + q0[j]) * p.s_stride + (first >> bt_shift);
         wrow[64 * j + lane] = weight(j, lane);
         wrow[64 * j + 32 + lane] = weight(j, 32 + lane);
       }
       __syncwarp();
-      for (int t = 0; t < sg.nt; t += G, ++stage) {
-        const int tiles = min(G, sg.nt - t);
-        const int sb = sbase;
-        const uint32_t sp = spar;
-        sbase += tiles;
-        if (sbase >= SC) sbase -= SC, spar ^= 1u;
-        if ((stage & 1) != set) continue;
-        const bool has0 = nq[0] > 0 && g[0] < tiles, has1 = nq[1] > 0 && g[1] < tiles;      // has1 implies has0
-        int ss[2];
-        bool w = wait_all(&d_full[set], (stage >> 1) & 1, abort_flag);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          ss[j] = sb + g[j];
-          uint32_t par = sp;
-          if (ss[j] >= SC) ss[j] -= SC, par ^= 1u;
-          if (j == 0 ? has0 : has1 && g[1] != g[0]) w = w && wait_all(&sc_full[ss[j]], par, abort_flag);
-        }
-        if (!w) {
+      const int first_own = (stage & 1) == static_cast<uint32_t>(set) ? 0 : G;
+      int ss = sbase + first_own;                 // scale slot of the stage's first tile
+      if (ss >= SC) ss -= SC;
+      for (int t = first_own; t < sg.nt; t += 2 * G) {
+        const bool has0 = nq[0] > 0 && t + g[0] < sg.nt, has1 = nq[1] > 0 && t + g[1] < sg.nt;      // has1 implies has0
+        if (!wait_all(&d_full[set], full_par, abort_flag)) {
           ok = false;
           break;
         }
+        full_par ^= 1u;
+        const int s0 = ss;
+        ss += 2 * G;
+        if (ss >= SC) ss -= SC;
         tc_fence_after();
         // sums of the slices: 16 columns at a time, the next ones loaded meanwhile
         float v[2][QW];
@@ -506,6 +519,11 @@ __global__ void __launch_bounds__(kIxThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&d_empty[set]);
         };
+        auto slot_of = [&](int j) -> int {
+          const int s = s0 + g[j];
+          return s >= SC ? s - SC : s;
+        };
+        float ks[2];
         auto chunks = [&](int j, bool more) {     // more: another slice follows
           uint64_t acc[QW][NA];
 #pragma unroll
@@ -519,7 +537,7 @@ __global__ void __launch_bounds__(kIxThreads, 1)
               tmem_ld_n<CH>(tl + 64 * j + CH * (u + 1), d[(u + 1) & 1]);
             else if (more)
               tmem_ld_n<CH>(tl + 64 * (j + 1), d[0]);
-            else if (!padded && bt <= 32)
+            else if (early)
               release();                          // everything is in registers
 #pragma unroll
             for (int c = 0; c < CH; c += 4) {
@@ -535,14 +553,19 @@ __global__ void __launch_bounds__(kIxThreads, 1)
             if (NA == 2) v[j][q] += sum2(acc[q][NA - 1]);
           }
         };
-        if (has0) {
-          tmem_ld_n<CH>(tl, d[0]);
-          chunks(0, has1);
-          if (has1) chunks(1, false);
-        } else {
+        if (!has0) {
           release();
           continue;
         }
+        tmem_ld_n<CH>(tl, d[0]);
+        // the keys' scales and bad pages, read before the release (their slots are reused after it)
+        const uint32_t bm[2] = {bad[slot_of(0)], has1 ? bad[slot_of(1)] : 0u};
+        if (F == kFP8) {
+          ks[0] = scales[slot_of(0) * 128 + key];
+          ks[1] = has1 ? scales[slot_of(1) * 128 + key] : 0.f;
+        }
+        chunks(0, has1);
+        if (has1) chunks(1, false);
         const bool exchange = bt > 32;
         // a key with infinities or NaN meets the zeros of the padded heads: sum the heads alone
         if (padded) {
@@ -563,32 +586,52 @@ __global__ void __launch_bounds__(kIxThreads, 1)
               v[j][q] = s;
             }
           }
-          if (!exchange) release();
+        }
+        if (F == kFP8) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < QW; ++q) v[j][q] *= ks[j];
+        }
+        if (bm[0] | bm[1]) {      // tokens of bad pages
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if ((bm[j] >> (key >> br_shift)) & 1u)
+#pragma unroll
+              for (int q = 0; q < QW; ++q) v[j][q] = -CUDART_INF_F;
+        }
+        if (!exchange && !early) release();
+        const int off = t * 128;
+        if (bt == 1) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (j == 1 && !has1) break;
+            if (QW == 1) {
+              if (off < lim[j]) row[j][off] = v[j][0];
+            } else {
+              float* r = row[j] + off;
+#pragma unroll
+              for (int q = 0; q < QW; ++q, r += p.s_stride)
+                if (q < nq[j] && off < min(lim[j] + q, cap - sg.j0 * 128 - g[j] * 128 - key)) *r = v[j][q];
+            }
+          }
+          continue;
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           if (j == 1 && !has1) break;
-          const float ks = F == kFP8 ? scales[ss[j] * 128 + key] : 1.f;
-          const uint32_t bm = bad[ss[j]];
-          const bool is_bad = bm && ((bm >> (key >> br_shift)) & 1u);
-          const int pos = (sg.j0 + t + g[j]) * 128 + key;
-          const int vis0 = sg.vis0 + q0[j];
-          float* row = p.scores + static_cast<int64_t>(sg.t0 + q0[j]) * p.s_stride;
+          float* r = row[j] + (off >> bt_shift);
+          const int edge = cap - sg.j0 * 128 - g[j] * 128 - key;
 #pragma unroll
-          for (int q = 0; q < QW; ++q, row += p.s_stride) {
+          for (int q = 0; q < QW; ++q, r += p.s_stride) {
             if (q >= nq[j]) break;
-            const bool seen = pos < min(vis0 + q, cap);
-            float val = is_bad ? -CUDART_INF_F : F == kFP8 ? v[j][q] * ks : v[j][q];
-            if (bt == 1) {
-              if (seen) row[pos] = val;
-              continue;
-            }
-            if (!seen) val = -CUDART_INF_F;
+            const bool seen = off < min(lim[j] + q, edge);
+            float val = seen ? v[j][q] : -CUDART_INF_F;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1)
               if (o < bt) val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, o));
             if (!exchange) {
-              if ((lane & (bt - 1)) == 0 && seen) row[pos >> bt_shift] = val;
+              if ((lane & (bt - 1)) == 0 && seen) *r = val;
             } else if (lane == 0) {
               red_g[32 * j + q] = val;
             }
@@ -618,6 +661,8 @@ __global__ void __launch_bounds__(kIxThreads, 1)
           release();
         }
       }
+      stage += (sg.nt + G - 1) / G;
+      sbase = (sbase + sg.nt) % SC;
     }
   }
 
