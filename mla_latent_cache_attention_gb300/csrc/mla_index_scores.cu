@@ -58,8 +58,7 @@ struct IndexCfg {
   static constexpr int kRing = kQ + kQB * kQBytes;
   static constexpr int kScale = kRing + kS * kTileBytes;
   static constexpr int kRed = kScale + kSc * 512;               // block maxima: 2 buffers x 4 slices x 4 warps x 8 queries
-  static constexpr int kW = kRed + 2 * 16 * 8 * 4;              // weights of 16 warps' 128 columns
-  static constexpr int kSeg = kW + 16 * 128 * 4;
+  static constexpr int kSeg = kRed + 2 * 16 * 8 * 4;
   static constexpr int kBad = kSeg + kSegDepth * 32;
   static constexpr int kBar = kBad + ((kSc * 4 + 7) & ~7);
   static constexpr int kNumBars = 2 * kS + 8 + 2 * kSegDepth + 4 + 1;      // as carved in the kernel
@@ -128,6 +127,25 @@ __device__ __forceinline__ float sum2(uint64_t a) {
   float x, y;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
   return x + y;
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+
+// 16 lanes x 32 columns: lane 4 a + b gets, of every 8 columns c, v[4 c] and v[4 c + 1] = TMEM lane a,
+// columns 2 b and 2 b + 1, and v[4 c + 2], v[4 c + 3] = TMEM lane a + 8.
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // One lane of a converged warp.
@@ -452,16 +470,19 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     // Two sets of two groups: a set takes every second stage (one accumulator buffer), so that one
     // set's waits hide behind the other's work; a group takes two 64-column slices of the buffer.
     const int quad = warp & 3, group = (warp - 2) >> 2, set = group >> 1;
-    const int key = 32 * quad + lane;             // TMEM lane = key of the tile
+    // A thread's keys and columns: a 16 x 256-bit load gives lane 4 a + b the columns 2 b, 2 b + 1 of
+    // every 8 for the keys a and a + 8, so its weights of 64 columns are 16 registers (a lane that had
+    // one key and all columns would need them all, and reading them from shared memory for every
+    // tile took twice the time of the products).  The four lanes of a key then exchange
+    // their sums, and lane 4 a + b ends with key a + 8 b.
+    const int la = lane >> 2, lb = lane & 3;
+    const int key = 32 * quad + la + 8 * lb;
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16) + set * kIxCols + (group & 1) * 128;
-    float* wrow = reinterpret_cast<float*>(smem + C::kW) + (warp - 2) * 128;
     float* red_g = red + (group * 2 * 4 + quad) * 8;          // slice j at + 32 j
     const bool padded = p.Hi < HP;
     const bool early = !padded && p.block_tokens <= 32;       // nothing of the stage is needed after its columns
     const int bt = p.block_tokens, br_shift = 31 - __clz(p.BR), bt_shift = 31 - __clz(bt);
     const int cap = static_cast<int>(min(p.cap, static_cast<int64_t>(0x7FFFFFFF)));
-    constexpr int NA = QW <= 2 ? 2 : 1;           // independent sums of a query
-    constexpr int CH = 16;                        // columns of a load
     uint32_t stage = 0;                           // stages before the segment
     int sbase = 0;                                // scale slot of the segment's first tile
     uint32_t full_par = 0;                        // parity of the set's next stage
@@ -483,7 +504,7 @@ __global__ void __launch_bounds__(kIxThreads, 1)
         const int q = c / HP, h = c % HP;
         return q < nq[j] && h < p.Hi ? __ldg(p.weights + static_cast<int64_t>(sg.t0 + q0[j] + q) * p.w_stride + h) : 0.f;
       };
-      __syncwarp();
+      uint64_t w[2][8];                           // of the slices' columns 8 c + 2 lb and the next
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int sl = (group & 1) * 2 + j;
@@ -493,10 +514,9 @@ __global__ void __launch_bounds__(kIxThreads, 1)
         const int first = (sg.j0 + g[j]) * 128 + key;
         lim[j] = min(sg.vis0 + q0[j], cap) - first;
         row[j] = p.scores + static_cast<int64_t>(sg.t0 + q0[j]) * p.s_stride + (first >> bt_shift);
-        wrow[64 * j + lane] = weight(j, lane);
-        wrow[64 * j + 32 + lane] = weight(j, 32 + lane);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[j][c] = pack2(weight(j, 8 * c + 2 * lb), weight(j, 8 * c + 2 * lb + 1));
       }
-      __syncwarp();
       const int first_own = (stage & 1) == static_cast<uint32_t>(set) ? 0 : G;
       int ss = sbase + first_own;                 // scale slot of the stage's first tile
       if (ss >= SC) ss -= SC;
@@ -511,9 +531,6 @@ __global__ void __launch_bounds__(kIxThreads, 1)
         ss += 2 * G;
         if (ss >= SC) ss -= SC;
         tc_fence_after();
-        // sums of the slices: 16 columns at a time, the next ones loaded meanwhile
-        float v[2][QW];
-        float d[2][CH];
         auto release = [&]() {
           tc_fence_before();
           __syncwarp();
@@ -523,49 +540,62 @@ __global__ void __launch_bounds__(kIxThreads, 1)
           const int s = s0 + g[j];
           return s >= SC ? s - SC : s;
         };
-        float ks[2];
-        auto chunks = [&](int j, bool more) {     // more: another slice follows
-          uint64_t acc[QW][NA];
-#pragma unroll
-          for (int q = 0; q < QW; ++q)
-#pragma unroll
-            for (int a = 0; a < NA; ++a) acc[q][a] = 0;
-#pragma unroll
-          for (int u = 0; u < 64 / CH; ++u) {
-            tmem_ld_wait();
-            if (u + 1 < 64 / CH)
-              tmem_ld_n<CH>(tl + 64 * j + CH * (u + 1), d[(u + 1) & 1]);
-            else if (more)
-              tmem_ld_n<CH>(tl + 64 * (j + 1), d[0]);
-            else if (early)
-              release();                          // everything is in registers
-#pragma unroll
-            for (int c = 0; c < CH; c += 4) {
-              const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(wrow + 64 * j + CH * u + c);
-              const float* x = d[u & 1] + c;
-              fma2(acc[(CH * u + c) / HP][0], max_nan(x[0], 0.f), max_nan(x[1], 0.f), ww.x);
-              fma2(acc[(CH * u + c) / HP][NA - 1], max_nan(x[2], 0.f), max_nan(x[3], 0.f), ww.y);
-            }
-          }
-#pragma unroll
-          for (int q = 0; q < QW; ++q) {
-            v[j][q] = sum2(acc[q][0]);
-            if (NA == 2) v[j][q] += sum2(acc[q][NA - 1]);
-          }
-        };
         if (!has0) {
           release();
           continue;
         }
-        tmem_ld_n<CH>(tl, d[0]);
         // the keys' scales and bad pages, read before the release (their slots are reused after it)
         const uint32_t bm[2] = {bad[slot_of(0)], has1 ? bad[slot_of(1)] : 0u};
+        float ks[2];
         if (F == kFP8) {
           ks[0] = scales[slot_of(0) * 128 + key];
           ks[1] = has1 ? scales[slot_of(1) * 128 + key] : 0.f;
         }
-        chunks(0, has1);
-        if (has1) chunks(1, false);
+        // Sums of the slices.  Load u of a slice: keys 16 (u / 2) .. + 15 of the warp's 32, columns
+        // 32 (u % 2) .. + 31; the next load is under way meanwhile.
+        float v[2][QW];
+        auto load = [&](int j, int u, float (&x)[16]) {
+          tmem_ld_16x256(tl + 64 * j + 32 * (u & 1) + (static_cast<uint32_t>(16 * (u >> 1)) << 16), x);
+        };
+        auto slice = [&](int j, bool more) {      // more: another slice follows
+          float y[4][QW];                         // keys la + 8 i
+          uint64_t acc[2][QW];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float d[16];
+            load(j, u, d);
+            tmem_ld_wait();
+            if (u == 3 && !more && early) release();                          // everything is in registers
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {         // 8 columns
+              const int q = (32 * (u & 1) + 8 * c) / HP;
+              const bool start = (32 * (u & 1) + 8 * c) % HP == 0;
+              const float* x = d + 4 * c;
+              const uint64_t ww = w[j][4 * (u & 1) + c];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                if (start) acc[r][q] = 0;
+                fma2(acc[r][q], max_nan(x[2 * r], 0.f), max_nan(x[2 * r + 1], 0.f), ww);
+              }
+            }
+            if (u & 1)
+#pragma unroll
+              for (int q = 0; q < QW; ++q)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) y[(u >> 1) * 2 + r][q] = sum2(acc[r][q]);
+          }
+          // the four lanes of a key: lane bit 1 keeps keys la, la + 8 or la + 16, la + 24, bit 0 one of them
+#pragma unroll
+          for (int q = 0; q < QW; ++q) {
+            const bool h = lb & 2, o = lb & 1;
+            const float k0 = h ? y[2][q] : y[0][q], k1 = h ? y[3][q] : y[1][q];
+            const float g0 = h ? y[0][q] : y[2][q], g1 = h ? y[1][q] : y[3][q];
+            const float z0 = k0 + __shfl_xor_sync(0xFFFFFFFFu, g0, 2), z1 = k1 + __shfl_xor_sync(0xFFFFFFFFu, g1, 2);
+            v[j][q] = (o ? z1 : z0) + __shfl_xor_sync(0xFFFFFFFFu, o ? z0 : z1, 1);
+          }
+        };
+        slice(0, has1);
+        if (has1) slice(1, false);
         const bool exchange = bt > 32;
         // a key with infinities or NaN meets the zeros of the padded heads: sum the heads alone
         if (padded) {
@@ -581,9 +611,9 @@ __global__ void __launch_bounds__(kIxThreads, 1)
                 uint32_t e;
                 asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(e) : "r"(tl + 64 * j + q * HP + h));
                 tmem_ld_wait();
-                s = fmaf(max_nan(__uint_as_float(e), 0.f), wrow[64 * j + q * HP + h], s);
+                s = fmaf(max_nan(__uint_as_float(e), 0.f), weight(j, q * HP + h), s);
               }
-              v[j][q] = s;
+              v[j][q] = __shfl_sync(0xFFFFFFFFu, s, la + 8 * lb);
             }
           }
         }
@@ -627,11 +657,14 @@ __global__ void __launch_bounds__(kIxThreads, 1)
             if (q >= nq[j]) break;
             const bool seen = off < min(lim[j] + q, edge);
             float val = seen ? v[j][q] : -CUDART_INF_F;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1)
-              if (o < bt) val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, o));
+            // over la and lb bit 0: 16 keys; over lb bit 1: 32
+            val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 4));
+            val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 8));
+            val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 16));
+            val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 1));
+            if (bt > 16) val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 2));
             if (!exchange) {
-              if ((lane & (bt - 1)) == 0 && seen) *r = val;
+              if ((key & (bt - 1)) == 0 && seen) *r = val;
             } else if (lane == 0) {
               red_g[32 * j + q] = val;
             }
