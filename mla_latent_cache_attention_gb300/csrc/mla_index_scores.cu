@@ -14,11 +14,8 @@
 // form (a causal row sees seq_len - rows + i + 1 keys), and every CTA takes an equal contiguous
 // range of them: scores are independent, so nothing is merged and no counter is shared.
 //
-// A stage is one accumulator buffer of 256 columns: one key tile, or two or four where the query
-// tile has at most 128 or 64 columns (decode), so that the four epilogue groups always share it.
-//
-// Warps: 0 producer (TMA boxes of pages, lanes resolve page ids), 1 MMA issuer and TMEM owner, 
-// 2..17 four epilogue groups of four warps.
+// Warps: 0 producer (TMA boxes of pages, lanes resolve page ids), 1 and 2 MMA issuers (1 owns TMEM),
+// 4..19 four epilogue groups of four warps.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -31,7 +28,7 @@ namespace mla {
 namespace {
 
 constexpr int kIxCols = 256;                  // query rows (MMA N) of a tile
-constexpr int kIxThreads = 32 * 18;
+constexpr int kIxThreads = 32 * 20;
 constexpr int kSegDepth = 4;
 
 // A run of key tiles of one query tile.
@@ -42,8 +39,12 @@ struct Segment {
   int b, pad0, pad1;
 };
 
-// Key tiles of a stage (one accumulator buffer): query tiles of few columns share it.
-__device__ __forceinline__ int stage_tiles(int cols) { return cols <= 64 ? 4 : cols <= 128 ? 2 : 1; }
+// A stage fills one of four accumulator buffers of 128 columns: half of the columns of a key tile, a
+// key tile of at most 128 columns, or two of at most 64.
+constexpr int kStageCols = 128;
+constexpr int kBufs = 4;
+__device__ __forceinline__ int stage_tiles(int cols) { return cols <= 64 ? 2 : 1; }
+__device__ __forceinline__ int tile_stages(int cols) { return cols > kStageCols ? 2 : 1; }
 
 template <int F>
 struct IndexCfg {
@@ -53,15 +54,15 @@ struct IndexCfg {
   static constexpr int kQBytes = kIxCols * 128 * kHalves;
   static constexpr int kS = F == kBF16 ? 4 : 8;                 // key tiles in flight
   static constexpr int kQB = F == kBF16 ? 1 : 2;                // query tiles in flight
-  static constexpr int kSc = kS + 12;                           // scales in flight (see the producer)
+  static constexpr int kSc = kS + 8;                            // scales in flight (see the producer)
   static constexpr int kQ = 0;
   static constexpr int kRing = kQ + kQB * kQBytes;
   static constexpr int kScale = kRing + kS * kTileBytes;
-  static constexpr int kRed = kScale + kSc * 512;               // block maxima: 2 buffers x 4 slices x 4 warps x 8 queries
+  static constexpr int kRed = kScale + kSc * 512;               // block maxima: 4 buffers x 2 groups x 4 warps x 8 queries
   static constexpr int kSeg = kRed + 2 * 16 * 8 * 4;
   static constexpr int kBad = kSeg + kSegDepth * 32;
   static constexpr int kBar = kBad + ((kSc * 4 + 7) & ~7);
-  static constexpr int kNumBars = 2 * kS + 8 + 2 * kSegDepth + 4 + 1;      // as carved in the kernel
+  static constexpr int kNumBars = 2 * kS + 4 + 2 * kBufs + 2 * kSegDepth + 8 + 2;      // as carved in the kernel
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kAlloc = kMisc + 64 + 1024;
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
@@ -155,10 +156,16 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// Bounded wait of a whole warp: one look by every lane where the phase has completed already.
+// The rest of a bounded wait, out of line: the roles' loops stay short (a warp that runs a loop once
+// a tile beside busy neighbours fetches all of its instructions again each time).
+__device__ __noinline__ bool wait_rest(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  return warp_wait(bar, parity, abort_flag);
+}
+
+// Bounded wait of a whole warp.
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-  return warp_wait(bar, parity, abort_flag);
+  return wait_rest(bar, parity, abort_flag);
 }
 
 template <int F, int HP>
@@ -170,7 +177,8 @@ __global__ void __launch_bounds__(kIxThreads, 1)
   constexpr int QT = kIxCols / HP;             // queries of a tile
   constexpr int QW = 64 / HP;                  // queries of an epilogue group
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // aligned by an offset, not through an integer: the compiler then still knows it is shared memory
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* qs = smem + C::kQ;
   uint8_t* ring = smem + C::kRing;
   float* scales = reinterpret_cast<float*>(smem + C::kScale);
@@ -182,35 +190,38 @@ __global__ void __launch_bounds__(kIxThreads, 1)
   uint64_t* k_empty = k_full + S;              // [S] its MMAs are done
   uint64_t* q_full = k_empty + S;              // [2]
   uint64_t* q_empty = q_full + 2;              // [2]
-  uint64_t* d_full = q_empty + 2;              // [2] accumulator ready
-  uint64_t* d_empty = d_full + 2;              // [2] accumulator read
-  uint64_t* seg_full = d_empty + 2;
+  uint64_t* d_full = q_empty + 2;              // [4] accumulator ready
+  uint64_t* d_empty = d_full + kBufs;          // [4] accumulator read
+  uint64_t* seg_full = d_empty + kBufs;
   uint64_t* seg_empty = seg_full + kSegDepth;
-  uint64_t* red_full = seg_empty + kSegDepth;  // [4] block maxima of a group's warps written
-  uint64_t* fin = red_full + 4;
+  uint64_t* red_full = seg_empty + kSegDepth;  // [4 groups][2] block maxima of a group's warps written
+  uint64_t* fin = red_full + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 8);
   int64_t* start = reinterpret_cast<int64_t*>(smem + C::kMisc + 16);      // [0] first unit's request, [1] its offset, [2] units
-  int64_t* part = reinterpret_cast<int64_t*>(red);      // setup only: 18 warp totals
+  int64_t* part = reinterpret_cast<int64_t*>(red);      // setup only: 20 warp totals
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
+      mbar_init(&k_empty[i], 2);      // both MMA warps
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
+      mbar_init(&q_empty[i], 2);
+    }
+    for (int i = 0; i < kBufs; ++i) {
       mbar_init(&d_full[i], 2);      // the MMAs, and the issuer's own arrival (see there)
       mbar_init(&d_empty[i], 8);
     }
     for (int i = 0; i < kSegDepth; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], 17);
+      mbar_init(&seg_empty[i], 18);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&red_full[i], 4);
-    mbar_init(fin, 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&red_full[i], 4);
+    mbar_init(&fin[0], 1);
+    mbar_init(&fin[1], 1);
     abort_flag[0] = 0;
     abort_flag[1] = 0;
     start[0] = p.B;
@@ -267,6 +278,7 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     // ------------------------------------------------------------------ producer
     int b = static_cast<int>(start[0]);
     int64_t x = start[1], rem = hi - lo;
+    const bool leader = elect_one();
     const int BR = p.BR, SP = 128 / BR;            // page slices of BR rows, SP of them a tile
     const int SB = p.block_size / BR;              // slices of a page
     const int TG = 32 / SP;                        // key tiles covered by one page lookup of the warp
@@ -328,8 +340,7 @@ __global__ void __launch_bounds__(kIxThreads, 1)
           tma_load_3d(qs + qb * C::kQBytes + h * kIxCols * 128, &tm_q, 128 * h, 0, sg.t0, &q_full[qb]);
       }
       ++nseg;
-      // Pages of the slices j SP .. (j + TG) SP - 1, one per lane, looked up a group of TG tiles ahead;
-      // a lane then issues its own slice's copies when its tile comes.
+      // Pages of the slices j SP .. (j + TG) SP - 1, one per lane, looked up a group of TG tiles ahead.
       const int s_end = static_cast<int>((seen + BR - 1) / BR);          // slices with a visible key
       auto lookup = [&](int j, int& y) -> int {
         const int sl = j * SP + lane, col = SB == 1 ? sl : sl / SB;
@@ -353,24 +364,26 @@ __global__ void __launch_bounds__(kIxThreads, 1)
           nxt = lookup(sg.j0 + t + TG, ny);
         }
         const int slot = kc.slot, sslot = sc.slot;
-        // Tile n - S's MMAs are done, so the accumulators of the stage two before its own had been
-        // read: with at most 4 tiles a stage, the scales of tile n - S - 12 = n - SC are free.
+        // Tile n - S's MMAs are done, so the accumulators of the stage four before its own had been
+        // read: with at most 2 tiles a stage, the scales of tile n - S - 8 and before are free.
         if (tile >= S && !wait_all(&k_empty[slot], kc.par ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
-        if (lane == 0) {
+        if (leader) {
           bad[sslot] = (bad_m >> (in * SP)) & SM;
           mbar_arrive_expect_tx(&k_full[slot], C::kTileBytes + (F == kFP8 ? __popc((good_m >> (in * SP)) & SM) * BR * 4 : 0));
         }
-        __syncwarp();
-        if (lane / SP == in) {
-          const int row = (lane - in * SP) * BR, z = cur >= 0 ? cur : p.num_blocks;
+#pragma unroll 1
+        for (int q = 0; q < SP; ++q) {
+          const int id = __shfl_sync(0xFFFFFFFFu, cur, in * SP + q), y = __shfl_sync(0xFFFFFFFFu, cy, in * SP + q);
+          if (leader) {
 #pragma unroll
-          for (int h = 0; h < HV; ++h)
-            tma_load_3d(ring + slot * C::kTileBytes + h * 128 * 128 + row * 128, &tm_k, 128 * h, cy, z, &k_full[slot]);
-          if (F == kFP8 && cur >= 0)
-            bulk_g2s(scales + sslot * 128 + row, p.key_scales + z * p.ks_stride + cy, BR * 4, &k_full[slot]);
+            for (int h = 0; h < HV; ++h)
+              tma_load_3d(ring + slot * C::kTileBytes + h * 128 * 128 + q * BR * 128, &tm_k, 128 * h, y, id >= 0 ? id : p.num_blocks, &k_full[slot]);
+            if (F == kFP8 && id >= 0)
+              bulk_g2s(scales + sslot * 128 + q * BR, p.key_scales + (id * p.ks_stride + y), BR * 4, &k_full[slot]);
+          }
         }
         ++in;
         kc.step();
@@ -395,8 +408,11 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     }
     __syncwarp();
     if (lane == 0 && errbits) set_device_error(p.err, errbits);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
+  } else if (warp <= 2) {
+    // ------------------------------------------------------------------ MMA issuers
+    // One for each set's stages: a single warp's loop (waits, 4 or 8 products, commits: some 700 cycles
+    // a stage beside the epilogue's warps) set the kernel's pace.
+    const uint32_t mine = warp - 1;
     // The whole warp walks the loop and one elected lane issues: addresses and descriptors then stay
     // warp-uniform (from a single-lane branch every operand of an MMA is moved to a uniform register
     // first, and this warp, which shares its scheduler with four busy ones, set the kernel's pace).
@@ -416,60 +432,70 @@ __global__ void __launch_bounds__(kIxThreads, 1)
       if (nt == 0) break;
       if (!wait_all(&q_full[qb], (ns / QB) & 1, abort_flag)) break;
       const int n = (nq * HP + 15) & ~15;      // columns: a multiple of 16
-      const int G = stage_tiles(nq * HP), gcols = kIxCols / G;
-      const uint32_t idesc = F == kBF16 ? idesc_f16(128, n, 1, 1, 0, 0) : idesc_e4m3(128, n, 0, 0);
+      const int G = stage_tiles(n), NS = tile_stages(n);
       const uint32_t dQ = dQ0 + qb * (C::kQBytes >> 4);
-      for (int t = 0; ok && t < nt; t += G, ++stage) {
-        const uint32_t buf = stage & 1;
+      for (int t = 0; ok && t < nt; t += G) {
         const int g1 = min(G, nt - t);
-        if (stage >= 2 && !wait_all(&d_empty[buf], ((stage >> 1) - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
+        uint32_t slots[2];
+        // every tile's barrier is waited for in order, the other warp's too: a phase is known to be over
+        // before the next one of its slot is waited for
         for (int g = 0; g < g1; ++g) {
-          if (!wait_all(&k_full[kc.slot], kc.par, abort_flag)) {
+          slots[g] = kc.slot;
+          if (!wait_all(&k_full[kc.slot], kc.par, abort_flag)) ok = false;
+          kc.step();
+        }
+        if (!ok) break;
+        for (int sub = 0; sub < NS; ++sub, ++stage) {
+          if ((stage & 1) != mine) {
+            if (NS == 1 && leader)
+              for (int g = 0; g < g1; ++g) mbar_arrive(&k_empty[slots[g]]);
+            continue;
+          }
+          const uint32_t buf = stage % kBufs;
+          if (stage >= kBufs && !wait_all(&d_empty[buf], (stage / kBufs - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t dK = dK0 + static_cast<uint32_t>(kc.slot) * (C::kTileBytes >> 4);
-          const uint32_t d = tmem + buf * kIxCols + g * gcols;
           if (leader) {
+            const int cols = min(n - sub * kStageCols, kStageCols);
+            const uint32_t idesc = F == kBF16 ? idesc_f16(128, cols, 1, 1, 0, 0) : idesc_e4m3(128, cols, 0, 0);
+            for (int g = 0; g < g1; ++g) {
+              const uint32_t dK = dK0 + slots[g] * (C::kTileBytes >> 4);
+              const uint32_t d = tmem + buf * kStageCols + g * 64;
 #pragma unroll
-            for (int h = 0; h < HV; ++h)
+              for (int h = 0; h < HV; ++h)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t a = desc(dK + ((h * 128 * 128 + kk * 32) >> 4));
-                const uint64_t bq = desc(dQ + ((h * kIxCols * 128 + kk * 32) >> 4));
-                if (F == kBF16)
-                  mma_f16_ss(d, a, bq, idesc, h + kk > 0 ? 1u : 0u);
-                else
-                  mma_f8_ss(d, a, bq, idesc, h + kk > 0 ? 1u : 0u);
-              }
-            mma_commit(&k_empty[kc.slot]);
+                for (int kk = 0; kk < 4; ++kk) {
+                  const uint64_t a = desc(dK + ((h * 128 * 128 + kk * 32) >> 4));
+                  const uint64_t bq = desc(dQ + sub * (kStageCols * 128 >> 4) + ((h * kIxCols * 128 + kk * 32) >> 4));
+                  if (F == kBF16)
+                    mma_f16_ss(d, a, bq, idesc, h + kk > 0 ? 1u : 0u);
+                  else
+                    mma_f8_ss(d, a, bq, idesc, h + kk > 0 ? 1u : 0u);
+                }
+              mma_commit(&k_empty[slots[g]]);
+            }
+            mma_commit(&d_full[buf]);
+            // the scales and bad-page masks that came with the key tiles reach the epilogue by this
+            // thread's release (it has seen k_full)
+            mbar_arrive(&d_full[buf]);
           }
-          kc.step();
-        }
-        if (leader) {
-          mma_commit(&d_full[buf]);
-          // the scales and bad-page masks that came with the key tiles reach the epilogue by this
-          // thread's release (it has seen k_full)
-          mbar_arrive(&d_full[buf]);
-          if (t + G >= nt) mma_commit(&q_empty[qb]);
         }
       }
+      if (ok && leader) mma_commit(&q_empty[qb]);
     }
     if (leader) {      // no product is in flight when the accumulators are freed
       volatile int no_abort[2] = {0, 0};
-      mma_commit(fin);
-      mbar_wait(fin, 0, no_abort);
+      mma_commit(&fin[mine]);
+      mbar_wait(&fin[mine], 0, no_abort);
     }
     __syncwarp();
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------------ epilogue
-    // Two sets of two groups: a set takes every second stage (one accumulator buffer), so that one
-    // set's waits hide behind the other's work; a group takes two 64-column slices of the buffer.
-    const int quad = warp & 3, group = (warp - 2) >> 2, set = group >> 1;
+    // Two sets of two groups: a set takes every second stage and has two of the four buffers, so that
+    // the products of its next stage run while it reads this one; a group takes 64 columns.
+    const int quad = warp & 3, group = (warp - 4) >> 2, set = group >> 1, sl = group & 1;
     // A thread's keys and columns: a 16 x 256-bit load gives lane 4 a + b the columns 2 b, 2 b + 1 of
     // every 8 for the keys a and a + 8, so its weights of 64 columns are 16 registers (a lane that had
     // one key and all columns would need them all, and reading them from shared memory for every
@@ -477,15 +503,14 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     // their sums, and lane 4 a + b ends with key a + 8 b.
     const int la = lane >> 2, lb = lane & 3;
     const int key = 32 * quad + la + 8 * lb;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16) + set * kIxCols + (group & 1) * 128;
-    float* red_g = red + (group * 2 * 4 + quad) * 8;          // slice j at + 32 j
+    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * quad) << 16) + sl * 64;
+    float* red_g = red + (sl * 4 + quad) * 8;     // of buffer u: 64 u further
     const bool padded = p.Hi < HP;
     const bool early = !padded && p.block_tokens <= 32;       // nothing of the stage is needed after its columns
     const int bt = p.block_tokens, br_shift = 31 - __clz(p.BR), bt_shift = 31 - __clz(bt);
-    const int cap = static_cast<int>(min(p.cap, static_cast<int64_t>(0x7FFFFFFF)));
+    const int cap = static_cast<int>(p.cap);
     uint32_t stage = 0;                           // stages before the segment
     int sbase = 0;                                // scale slot of the segment's first tile
-    uint32_t full_par = 0;                        // parity of the set's next stage
     uint32_t uses = 0;                            // block maxima exchanged through red
     bool ok = true;
     for (uint32_t ns = 0; ok; ++ns) {
@@ -495,83 +520,70 @@ __global__ void __launch_bounds__(kIxThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&seg_empty[k]);
       if (sg.nt == 0) break;
-      // tile of a stage and queries of this group's two slices
-      const int G = stage_tiles(sg.nq * HP), per = 4 / G;
-      int g[2] = {}, q0[2] = {}, nq[2] = {};
-      int lim[2] = {};                            // keys from the thread's first one that its first query sees
-      float* row[2] = {};                         // where its first score goes
-      auto weight = [&](int j, int c) -> float {  // 0 for padded heads and queries
+      // the segment's stages, the set's first one, and this group's tile and queries in it
+      const int n = (sg.nq * HP + 15) & ~15, G = stage_tiles(n), NS = tile_stages(n);
+      const int stages = NS == 2 ? 2 * sg.nt : (sg.nt + G - 1) / G;
+      const int i0 = static_cast<int>(stage & 1) ^ set;
+      const int g = G == 2 ? sl : 0;
+      const int q0 = G == 2 ? 0 : (NS == 2 ? i0 * kStageCols + sl * 64 : sl * 64) / HP;
+      const int nq = max(min(QW, sg.nq - q0), 0);
+      int t = (NS == 2 ? 0 : i0 * G) + g;         // tile of the set's next stage
+      const int dt = NS == 2 ? 1 : 2 * G;
+      int slot = sbase + t;                       // and its scale slot
+      if (slot >= SC) slot -= SC;
+      const int first = sg.j0 * 128 + key;
+      const int lim = min(sg.vis0 + q0, cap) - first;         // keys of the segment that the first query sees, less the thread's place
+      const int edge = cap - first;
+      float* row = p.scores + static_cast<int64_t>(sg.t0 + q0) * p.s_stride + (first >> bt_shift);
+      const float* wsrc = p.weights + static_cast<int64_t>(sg.t0 + q0) * p.w_stride;
+      auto weight = [&](int c) -> float {         // 0 for padded heads and queries
         const int q = c / HP, h = c % HP;
-        return q < nq[j] && h < p.Hi ? __ldg(p.weights + static_cast<int64_t>(sg.t0 + q0[j] + q) * p.w_stride + h) : 0.f;
+        return q < nq && h < p.Hi ? __ldg(wsrc + q * p.w_stride + h) : 0.f;
       };
-      uint64_t w[2][8];                           // of the slices' columns 8 c + 2 lb and the next
+      uint64_t w[8];                              // of the columns 8 c + 2 lb and the next
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int sl = (group & 1) * 2 + j;
-        g[j] = sl / per;
-        q0[j] = (sl % per) * QW;
-        nq[j] = max(min(QW, sg.nq - q0[j]), 0);
-        const int first = (sg.j0 + g[j]) * 128 + key;
-        lim[j] = min(sg.vis0 + q0[j], cap) - first;
-        row[j] = p.scores + static_cast<int64_t>(sg.t0 + q0[j]) * p.s_stride + (first >> bt_shift);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) w[j][c] = pack2(weight(j, 8 * c + 2 * lb), weight(j, 8 * c + 2 * lb + 1));
-      }
-      const int first_own = (stage & 1) == static_cast<uint32_t>(set) ? 0 : G;
-      int ss = sbase + first_own;                 // scale slot of the stage's first tile
-      if (ss >= SC) ss -= SC;
-      for (int t = first_own; t < sg.nt; t += 2 * G) {
-        const bool has0 = nq[0] > 0 && t + g[0] < sg.nt, has1 = nq[1] > 0 && t + g[1] < sg.nt;      // has1 implies has0
-        if (!wait_all(&d_full[set], full_par, abort_flag)) {
+      for (int c = 0; c < 8; ++c) w[c] = pack2(weight(8 * c + 2 * lb), weight(8 * c + 2 * lb + 1));
+      for (int i = i0; i < stages; i += 2, t += dt) {
+        const uint32_t at = stage + i, buf = at % kBufs;
+        const bool has = nq > 0 && t < sg.nt;
+        if (!wait_all(&d_full[buf], (at / kBufs) & 1, abort_flag)) {
           ok = false;
           break;
         }
-        full_par ^= 1u;
-        const int s0 = ss;
-        ss += 2 * G;
-        if (ss >= SC) ss -= SC;
+        const int s0 = slot;
+        slot += dt;
+        if (slot >= SC) slot -= SC;
         tc_fence_after();
         auto release = [&]() {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&d_empty[set]);
+          if (lane == 0) mbar_arrive(&d_empty[buf]);
         };
-        auto slot_of = [&](int j) -> int {
-          const int s = s0 + g[j];
-          return s >= SC ? s - SC : s;
-        };
-        if (!has0) {
+        if (!has) {
           release();
           continue;
         }
-        // the keys' scales and bad pages, read before the release (their slots are reused after it)
-        const uint32_t bm[2] = {bad[slot_of(0)], has1 ? bad[slot_of(1)] : 0u};
-        float ks[2];
-        if (F == kFP8) {
-          ks[0] = scales[slot_of(0) * 128 + key];
-          ks[1] = has1 ? scales[slot_of(1) * 128 + key] : 0.f;
-        }
-        // Sums of the slices.  Load u of a slice: keys 16 (u / 2) .. + 15 of the warp's 32, columns
-        // 32 (u % 2) .. + 31; the next load is under way meanwhile.
-        float v[2][QW];
-        auto load = [&](int j, int u, float (&x)[16]) {
-          tmem_ld_16x256(tl + 64 * j + 32 * (u & 1) + (static_cast<uint32_t>(16 * (u >> 1)) << 16), x);
-        };
-        auto slice = [&](int j, bool more) {      // more: another slice follows
+        // the key's scale and bad pages, read before the release (their slots are reused after it)
+        const uint32_t bm = bad[s0];
+        const float ks = F == kFP8 ? scales[s0 * 128 + key] : 1.f;
+        const uint32_t ta = tl + buf * kStageCols;
+        // Load u: keys 16 (u / 2) .. + 15 of the warp's 32, columns 32 (u % 2) .. + 31.
+        float v[QW];
+        {
           float y[4][QW];                         // keys la + 8 i
           uint64_t acc[2][QW];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             float d[16];
-            load(j, u, d);
+            tmem_ld_16x256(ta + 32 * (u & 1) + (static_cast<uint32_t>(16 * (u >> 1)) << 16), d);
             tmem_ld_wait();
-            if (u == 3 && !more && early) release();                          // everything is in registers
+            if (u == 3 && early) release();       // everything is in registers
 #pragma unroll
             for (int c = 0; c < 4; ++c) {         // 8 columns
               const int q = (32 * (u & 1) + 8 * c) / HP;
               const bool start = (32 * (u & 1) + 8 * c) % HP == 0;
               const float* x = d + 4 * c;
-              const uint64_t ww = w[j][4 * (u & 1) + c];
+              const uint64_t ww = w[4 * (u & 1) + c];
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
                 if (start) acc[r][q] = 0;
@@ -591,110 +603,77 @@ __global__ void __launch_bounds__(kIxThreads, 1)
             const float k0 = h ? y[2][q] : y[0][q], k1 = h ? y[3][q] : y[1][q];
             const float g0 = h ? y[0][q] : y[2][q], g1 = h ? y[1][q] : y[3][q];
             const float z0 = k0 + __shfl_xor_sync(0xFFFFFFFFu, g0, 2), z1 = k1 + __shfl_xor_sync(0xFFFFFFFFu, g1, 2);
-            v[j][q] = (o ? z1 : z0) + __shfl_xor_sync(0xFFFFFFFFu, o ? z0 : z1, 1);
+            v[q] = (o ? z1 : z0) + __shfl_xor_sync(0xFFFFFFFFu, o ? z0 : z1, 1);
           }
-        };
-        slice(0, has1);
-        if (has1) slice(1, false);
-        const bool exchange = bt > 32;
+        }
         // a key with infinities or NaN meets the zeros of the padded heads: sum the heads alone
         if (padded) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (j == 1 && !has1) break;
-#pragma unroll
-            for (int q = 0; q < QW; ++q) {
-              if (!__any_sync(0xFFFFFFFFu, v[j][q] != v[j][q])) continue;
-              float s = 0.f;
+          for (int q = 0; q < QW; ++q) {
+            if (!__any_sync(0xFFFFFFFFu, v[q] != v[q])) continue;
+            float s = 0.f;
 #pragma unroll 1
-              for (int h = 0; h < p.Hi; ++h) {
-                uint32_t e;
-                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(e) : "r"(tl + 64 * j + q * HP + h));
-                tmem_ld_wait();
-                s = fmaf(max_nan(__uint_as_float(e), 0.f), weight(j, q * HP + h), s);
-              }
-              v[j][q] = __shfl_sync(0xFFFFFFFFu, s, la + 8 * lb);
+            for (int h = 0; h < p.Hi; ++h) {
+              uint32_t e;
+              asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(e) : "r"(ta + q * HP + h));
+              tmem_ld_wait();
+              s = fmaf(max_nan(__uint_as_float(e), 0.f), weight(q * HP + h), s);
             }
+            v[q] = __shfl_sync(0xFFFFFFFFu, s, la + 8 * lb);
           }
         }
-        if (F == kFP8) {
+        const bool is_bad = bm && ((bm >> (key >> br_shift)) & 1u);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int q = 0; q < QW; ++q) v[j][q] *= ks[j];
-        }
-        if (bm[0] | bm[1]) {      // tokens of bad pages
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if ((bm[j] >> (key >> br_shift)) & 1u)
-#pragma unroll
-              for (int q = 0; q < QW; ++q) v[j][q] = -CUDART_INF_F;
-        }
+        for (int q = 0; q < QW; ++q) v[q] = is_bad ? -CUDART_INF_F : F == kFP8 ? v[q] * ks : v[q];
+        const bool exchange = bt > 32;
         if (!exchange && !early) release();
         const int off = t * 128;
+        float* r = row + (off >> bt_shift);
         if (bt == 1) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (j == 1 && !has1) break;
-            if (QW == 1) {
-              if (off < lim[j]) row[j][off] = v[j][0];
-            } else {
-              float* r = row[j] + off;
-#pragma unroll
-              for (int q = 0; q < QW; ++q, r += p.s_stride)
-                if (q < nq[j] && off < min(lim[j] + q, cap - sg.j0 * 128 - g[j] * 128 - key)) *r = v[j][q];
-            }
-          }
+          for (int q = 0; q < QW; ++q, r += p.s_stride)
+            if ((QW == 1 || q < nq) && off < (QW == 1 ? lim : min(lim + q, edge))) *r = v[q];
           continue;
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (j == 1 && !has1) break;
-          float* r = row[j] + (off >> bt_shift);
-          const int edge = cap - sg.j0 * 128 - g[j] * 128 - key;
-#pragma unroll
-          for (int q = 0; q < QW; ++q, r += p.s_stride) {
-            if (q >= nq[j]) break;
-            const bool seen = off < min(lim[j] + q, edge);
-            float val = seen ? v[j][q] : -CUDART_INF_F;
-            // over la and lb bit 0: 16 keys; over lb bit 1: 32
-            val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 4));
-            val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 8));
-            val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 16));
-            val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 1));
-            if (bt > 16) val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 2));
-            if (!exchange) {
-              if ((key & (bt - 1)) == 0 && seen) *r = val;
-            } else if (lane == 0) {
-              red_g[32 * j + q] = val;
-            }
+        for (int q = 0; q < QW; ++q, r += p.s_stride) {
+          if (q >= nq) break;
+          const bool seen = off < min(lim + q, edge);
+          float val = seen ? v[q] : -CUDART_INF_F;
+          // over la and lb bit 0: 16 keys; over lb bit 1: 32
+          val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 4));
+          val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 8));
+          val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 16));
+          val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 1));
+          if (bt > 16) val = max_nan(val, __shfl_xor_sync(0xFFFFFFFFu, val, 2));
+          if (!exchange) {
+            if ((key & (bt - 1)) == 0 && seen) *r = val;
+          } else if (lane == 0) {
+            red_g[64 * buf + q] = val;
           }
         }
         if (exchange) {       // blocks of 64 or 128 keys: two or four warps of the group
-          if (lane == 0) mbar_arrive(&red_full[group]);
-          const uint32_t par = uses++ & 1u;
+          uint64_t* rf = &red_full[group * 2 + (uses & 1)];
+          if (lane == 0) mbar_arrive(rf);
+          const uint32_t par = (uses++ >> 1) & 1u;
           const int wb = bt >> 5;                 // warps of a block; its first one joins them
           if ((quad & (wb - 1)) == 0) {
-            if (!wait_all(&red_full[group], par, abort_flag)) {
+            if (!wait_all(rf, par, abort_flag)) {
               ok = false;
               break;
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (j == 1 && !has1) break;
-              const int p0 = (sg.j0 + t + g[j]) * 128 + 32 * quad;
-              if (lane < nq[j] && p0 < min(sg.vis0 + q0[j] + lane, cap)) {
-                float mx = red_g[32 * j + lane];
-                for (int o = 1; o < wb; ++o) mx = max_nan(mx, red_g[32 * j + 8 * o + lane]);
-                p.scores[static_cast<int64_t>(sg.t0 + q0[j] + lane) * p.s_stride + (p0 >> bt_shift)] = mx;
-              }
+            const int p0 = sg.j0 * 128 + off + 32 * quad;
+            if (lane < nq && p0 < min(sg.vis0 + q0 + lane, cap)) {
+              float mx = red_g[64 * buf + lane];
+              for (int o = 1; o < wb; ++o) mx = max_nan(mx, red_g[64 * buf + 8 * o + lane]);
+              p.scores[static_cast<int64_t>(sg.t0 + q0 + lane) * p.s_stride + (p0 >> bt_shift)] = mx;
             }
           }
           // red is free with the buffer: written again only for the stage that next uses it
           release();
         }
       }
-      stage += (sg.nt + G - 1) / G;
+      stage += stages;
       sbase = (sbase + sg.nt) % SC;
     }
   }
