@@ -422,7 +422,8 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     const uint32_t dQ0 = static_cast<uint32_t>(smem_desc(smem_u32(qs), 16, 1024, kSwizzle128B));
     auto desc = [&](uint32_t lo) -> uint64_t { return static_cast<uint64_t>(hi_desc) << 32 | lo; };
     Cursor<S> kc;
-    uint32_t stage = 0;
+    uint32_t parity = 0;                       // of the stage count: this warp's stages are those of `mine`
+    uint32_t x = 0, empty_par = 1;             // buffer mine + 2 x, free at first
     bool ok = true;
     for (uint32_t ns = 0; ok; ++ns) {
       const uint32_t k = ns % kSegDepth, qb = ns % QB;
@@ -432,55 +433,63 @@ __global__ void __launch_bounds__(kIxThreads, 1)
       if (nt == 0) break;
       if (!wait_all(&q_full[qb], (ns / QB) & 1, abort_flag)) break;
       const int n = (nq * HP + 15) & ~15;      // columns: a multiple of 16
-      const int G = stage_tiles(n), NS = tile_stages(n);
-      const uint32_t dQ = dQ0 + qb * (C::kQBytes >> 4);
-      for (int t = 0; ok && t < nt; t += G) {
-        const int g1 = min(G, nt - t);
-        uint32_t slots[2];
-        // every tile's barrier is waited for in order, the other warp's too: a phase is known to be over
-        // before the next one of its slot is waited for
-        for (int g = 0; g < g1; ++g) {
-          slots[g] = kc.slot;
-          if (!wait_all(&k_full[kc.slot], kc.par, abort_flag)) ok = false;
-          kc.step();
+      const int G = stage_tiles(n);
+      const bool two = tile_stages(n) == 2;    // every tile has a stage of this warp, its first or second half
+      const int half = two && parity != mine ? 1 : 0;
+      const int cols = two ? (half ? n - kStageCols : kStageCols) : n;
+      const uint32_t idesc = F == kBF16 ? idesc_f16(128, cols, 1, 1, 0, 0) : idesc_e4m3(128, cols, 0, 0);
+      const uint32_t dQ = dQ0 + qb * (C::kQBytes >> 4) + half * (kStageCols * 128 >> 4);
+      int in = 0;                              // tile of the stage
+      // Every tile's barrier is waited for in order, the other warp's too: a phase is known to be over
+      // before the next one of its slot is waited for.
+#pragma unroll 1
+      for (int t = 0; t < nt; ++t) {
+        if (!wait_all(&k_full[kc.slot], kc.par, abort_flag)) {
+          ok = false;
+          break;
         }
-        if (!ok) break;
-        for (int sub = 0; sub < NS; ++sub, ++stage) {
-          if ((stage & 1) != mine) {
-            if (NS == 1 && leader)
-              for (int g = 0; g < g1; ++g) mbar_arrive(&k_empty[slots[g]]);
-            continue;
-          }
-          const uint32_t buf = stage % kBufs;
-          if (stage >= kBufs && !wait_all(&d_empty[buf], (stage / kBufs - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (leader) {
-            const int cols = min(n - sub * kStageCols, kStageCols);
-            const uint32_t idesc = F == kBF16 ? idesc_f16(128, cols, 1, 1, 0, 0) : idesc_e4m3(128, cols, 0, 0);
-            for (int g = 0; g < g1; ++g) {
-              const uint32_t dK = dK0 + slots[g] * (C::kTileBytes >> 4);
-              const uint32_t d = tmem + buf * kStageCols + g * 64;
+        const bool own = two || parity == mine, last = in + 1 == G || t + 1 == nt;
+        if (own && in == 0 && !wait_all(&d_empty[mine + 2 * x], empty_par, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (leader) {
+          if (own) {
+            tc_fence_after();
+            const uint32_t dK = dK0 + static_cast<uint32_t>(kc.slot) * (C::kTileBytes >> 4);
+            const uint32_t d = tmem + (mine + 2 * x) * kStageCols + in * 64;
 #pragma unroll
-              for (int h = 0; h < HV; ++h)
+            for (int h = 0; h < HV; ++h)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                  const uint64_t a = desc(dK + ((h * 128 * 128 + kk * 32) >> 4));
-                  const uint64_t bq = desc(dQ + sub * (kStageCols * 128 >> 4) + ((h * kIxCols * 128 + kk * 32) >> 4));
-                  if (F == kBF16)
-                    mma_f16_ss(d, a, bq, idesc, h + kk > 0 ? 1u : 0u);
-                  else
-                    mma_f8_ss(d, a, bq, idesc, h + kk > 0 ? 1u : 0u);
-                }
-              mma_commit(&k_empty[slots[g]]);
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t a = desc(dK + ((h * 128 * 128 + kk * 32) >> 4));
+                const uint64_t bq = desc(dQ + ((h * kIxCols * 128 + kk * 32) >> 4));
+                if (F == kBF16)
+                  mma_f16_ss(d, a, bq, idesc, h + kk > 0 ? 1u : 0u);
+                else
+                  mma_f8_ss(d, a, bq, idesc, h + kk > 0 ? 1u : 0u);
+              }
+            mma_commit(&k_empty[kc.slot]);
+            if (last) {
+              mma_commit(&d_full[mine + 2 * x]);
+              // the scales and bad-page masks that came with the key tiles reach the epilogue by this
+              // thread's release (it has seen k_full)
+              mbar_arrive(&d_full[mine + 2 * x]);
             }
-            mma_commit(&d_full[buf]);
-            // the scales and bad-page masks that came with the key tiles reach the epilogue by this
-            // thread's release (it has seen k_full)
-            mbar_arrive(&d_full[buf]);
+          } else {
+            mbar_arrive(&k_empty[kc.slot]);
           }
+        }
+        __syncwarp();
+        kc.step();
+        ++in;
+        if (last) {
+          in = 0;
+          if (own) {
+            x ^= 1u;
+            empty_par ^= x ^ 1u;
+          }
+          if (!two) parity ^= 1u;
         }
       }
       if (ok && leader) mma_commit(&q_empty[qb]);
