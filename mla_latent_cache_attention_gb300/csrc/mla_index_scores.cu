@@ -232,12 +232,18 @@ __global__ void __launch_bounds__(kIxThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  // ---- this CTA's range of units: [W c / G, W (c + 1) / G), and the request it starts in
-  int64_t total = 0, lo = 0, hi = 0;
-  for (int pass = 0; pass < 2; ++pass) {
+  if (warp == 0 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_k) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&tm_q) : "memory");
+  }
+  // ---- this CTA's range of units, [W c / G, W (c + 1) / G), and the request it starts in: a prefix sum
+  // over the requests' units, twice where one pass of the CTA does not hold them all
+  int64_t lo = 0, hi = 0;
+  const int chunks = (p.B + kIxThreads - 1) / kIxThreads;
+  for (int pass = 0; pass < (chunks > 1 ? 2 : 1); ++pass) {
     int64_t before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kIxThreads) {
-      const int b = b0 + tid;
+    for (int c = 0; c < chunks; ++c) {
+      const int b = c * kIxThreads + tid;
       const int64_t u = b < p.B ? load_request<QT>(p, b).units : 0;
       int64_t inc = u;
 #pragma unroll
@@ -249,12 +255,18 @@ __global__ void __launch_bounds__(kIxThreads, 1)
       if (lane == 31) part[warp] = inc;
       __syncthreads();
       int64_t base = before, all = 0;
+#pragma unroll
       for (int w = 0; w < kIxThreads / 32; ++w) {
         const int64_t v = part[w];
         if (w < warp) base += v;
         all += v;
       }
-      if (pass == 1) {
+      if (pass == 0 && c + 1 == chunks) {
+        const uint64_t total = static_cast<uint64_t>(before + all), each = total / gridDim.x, rest = total % gridDim.x;
+        lo = static_cast<int64_t>(each * blockIdx.x + (rest < blockIdx.x ? rest : blockIdx.x));
+        hi = lo + static_cast<int64_t>(each + (blockIdx.x < rest ? 1 : 0));
+      }
+      if (chunks == 1 || pass == 1) {
         const int64_t first = base + inc - u;
         if (first <= lo && lo < first + u && lo < hi) {
           start[0] = b;
@@ -262,11 +274,6 @@ __global__ void __launch_bounds__(kIxThreads, 1)
         }
       }
       before += all;
-    }
-    if (pass == 0) {
-      total = before;
-      lo = total / gridDim.x * blockIdx.x + min(total % gridDim.x, static_cast<int64_t>(blockIdx.x));
-      hi = lo + total / gridDim.x + (blockIdx.x < total % gridDim.x ? 1 : 0);
     }
   }
   tc_fence_before();
