@@ -441,7 +441,8 @@ MLA_API int mla_v_up_proj(const void* latent, int64_t l_s0, int64_t l_s1, const 
  *   slot_mapping device int64 [T]; negative: the key is not inserted (the query is still written).
  *                A slot whose block is out of range is skipped (MLA_DEVERR_SLOT).  Two tokens with
  *                the same slot race for it.
- *   positions, cos_sin_cache, max_position  as in mla_q_concat_cache_insert (both NULL: no RoPE).
+ *   positions, cos_sin_cache, max_position  as in mla_q_concat_cache_insert (both NULL: no RoPE);
+ *                cos_sin_cache 16-byte aligned.
  */
 MLA_API int mla_index_q_cache_insert(const void* q, int64_t q_s0, int64_t q_s1, const void* k, int64_t k_s0,
                                      const float* weights, int64_t w_s0, float weight_scale, void* q_out, float* w_out,

@@ -33,19 +33,20 @@ __device__ __forceinline__ int scale_exponent(float amax) {
   return k < -126 ? -126 : k;
 }
 
-// 8 consecutive bf16 values as fp32
-__device__ __forceinline__ void load_bf16x8(const uint16_t* __restrict__ src, bool vec, float (&x)[8]) {
-  if (vec) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// 8 consecutive bf16 values, as stored and as fp32
+__device__ __forceinline__ uint4 load_bf16x8(const uint16_t* __restrict__ src, bool vec) {
+  if (vec) return __ldcs(reinterpret_cast<const uint4*>(src));      // read once
+  uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
+  for (int i = 0; i < 4; ++i) w[i] = __ldg(src + 2 * i) | static_cast<uint32_t>(__ldg(src + 2 * i + 1)) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void bf16x8_values(const uint4 v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = bf16_value(__ldg(src + i));
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
 
@@ -63,144 +64,169 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
 //
 // Bound by memory: one read of every query and one write.  A half-warp owns a vector (8 values a
 // lane: a 16-byte load, an 8- or 16-byte store), the four butterflies of the maximum stay inside
-// it.  Vector Hi of a token is its key.
-constexpr int kInsVec = 2;      // vectors of a half-warp, their loads in flight together
+// it, and it has kVec vectors' loads in flight.  The first CTA of a token also inserts its key.
+// The rotated half of a vector: lane l >= 8 holds pairs 4 (l - 8) .. 4 (l - 8) + 3.
+__device__ __forceinline__ void rotate_vector(float (&x)[8], const float4 c4, const float4 s4, bool on) {
+  if (!on) return;
+  const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = x[2 * i], b = x[2 * i + 1];
+    x[2 * i] = __fmaf_rn(a, c[i], -__fmul_rn(b, s[i]));
+    x[2 * i + 1] = __fmaf_rn(b, c[i], __fmul_rn(a, s[i]));
+  }
+}
 
-template <bool kBf16>
+// Scale exponent and codes of a half-warp's vector.
+__device__ __forceinline__ uint2 quantise_vector(const float (&x)[8], uint32_t half, float& scale) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+  for (int m = 8; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, m));
+  const int k = scale_exponent(amax);
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);      // 2^-k, exact
+  scale = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+  uint32_t c[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t two = static_cast<uint32_t>(
+        __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3));
+    c[i >> 1] |= two << (16 * (i & 1));
+  }
+  return make_uint2(c[0], c[1]);
+}
+
+template <bool kBf16, int kVec>
 __global__ void __launch_bounds__(128) mla_index_insert_kernel(const IndexInsertParams p) {
   // a kernel launched next as a programmatic dependent may be scheduled now
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t t = blockIdx.x;
   const int hw = threadIdx.x >> 4, l = threadIdx.x & 15, d0 = 8 * l;
-  const int v0 = (blockIdx.y * 8 + hw) * kInsVec;
+  const int v0 = blockIdx.y * 8 * kVec + hw;      // vectors v0, v0 + 8, ...
   const uint32_t half = 0xFFFFu << (threadIdx.x & 16);
-  if (v0 > p.Hi) return;
-  float x[kInsVec][8];
-#pragma unroll
-  for (int u = 0; u < kInsVec; ++u) {
-    const int v = v0 + u;
-    if (v <= p.Hi) load_bf16x8((v < p.Hi ? p.q + t * p.q_s0 + v * p.q_s1 : p.k + t * p.k_s0) + d0, p.vec != 0, x[u]);
-  }
-  const int64_t slot = p.Hi < v0 + kInsVec ? p.slot_mapping[t] : -1;
+  const bool keyed = blockIdx.y == 0 && hw == 7;
+  const int64_t slot = keyed ? p.slot_mapping[t] : -1;
+  const float* cs = nullptr;
   if (p.positions) {
     int64_t pos = p.positions[t];
     if (pos < 0 || pos >= p.max_position) {
-      if (l == 0 && p.Hi < v0 + kInsVec) set_device_error(p.err, 8u);
+      if (l == 0 && keyed) set_device_error(p.err, 8u);
       pos = pos < 0 ? 0 : p.max_position - 1;
     }
-    if (l >= 8) {      // the rotated half: lane l holds pairs 4 (l - 8) .. 4 (l - 8) + 3
-      const float* cs = p.cos_sin + pos * 64 + 4 * (l - 8);
-      float c[4], s[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = __ldg(cs + i), s[i] = __ldg(cs + 32 + i);
-#pragma unroll
-      for (int u = 0; u < kInsVec; ++u) {
-        if (v0 + u > p.Hi) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[u][2 * i], b = x[u][2 * i + 1];
-          x[u][2 * i] = __fmaf_rn(a, c[i], -__fmul_rn(b, s[i]));
-          x[u][2 * i + 1] = __fmaf_rn(b, c[i], __fmul_rn(a, s[i]));
-        }
-      }
-    }
+    cs = p.cos_sin + pos * 64 + 4 * (l & 7);
   }
+  uint4 raw[kVec];
+  const uint16_t* q = p.q + t * p.q_s0 + d0;
 #pragma unroll
-  for (int u = 0; u < kInsVec; ++u) {
-    const int v = v0 + u;
-    if (v > p.Hi) break;
-    uint8_t* ent = nullptr;
-    int64_t blk = 0, off = 0;
-    if (v == p.Hi && slot >= 0) {
-      blk = slot / p.block_size;
-      off = slot - blk * p.block_size;
-      if (blk < p.num_blocks)
-        ent = p.cache + blk * p.block_stride + off * p.entry_stride;
-      else if (l == 0)
-        set_device_error(p.err, 4u);
-    }
+  for (int u = 0; u < kVec; ++u)
+    if (v0 + 8 * u < p.Hi) raw[u] = load_bf16x8(q + (v0 + 8 * u) * p.q_s1, p.vec != 0);
+  uint4 raw_k = make_uint4(0, 0, 0, 0);
+  if (keyed) raw_k = load_bf16x8(p.k + t * p.k_s0 + d0, p.vec != 0);
+  float4 c = make_float4(0.f, 0.f, 0.f, 0.f), s = c;
+  if (cs) c = __ldg(reinterpret_cast<const float4*>(cs)), s = __ldg(reinterpret_cast<const float4*>(cs + 32));
+  float w[kVec];
+  if (l == 0)
+#pragma unroll
+    for (int u = 0; u < kVec; ++u)
+      if (v0 + 8 * u < p.Hi) w[u] = __ldg(p.w + t * p.w_s0 + v0 + 8 * u);
+#pragma unroll
+  for (int u = 0; u < kVec; ++u) {
+    const int v = v0 + 8 * u;
+    if (v >= p.Hi) break;
+    float x[8];
+    bf16x8_values(raw[u], x);
+    rotate_vector(x, c, s, cs && l >= 8);
     const int64_t o = (t * p.Hi + v) * kIndexDim + d0;
     if (kBf16) {
-      const uint4 y = pack_bf16x8(x[u]);
-      if (v < p.Hi) {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.q_out) + o) = y;
-        if (l == 0) p.w_out[t * p.Hi + v] = p.w[t * p.w_s0 + v] * p.weight_scale;
-      } else if (ent) {
-        *reinterpret_cast<uint4*>(ent + 2 * d0) = y;
-      }
-      continue;
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.q_out) + o) = pack_bf16x8(x);
+      if (l == 0) p.w_out[t * p.Hi + v] = w[u] * p.weight_scale;
+    } else {
+      float sc;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q_out) + o) = quantise_vector(x, half, sc);
+      if (l == 0) p.w_out[t * p.Hi + v] = w[u] * p.weight_scale * sc;
     }
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[u][i]));
-#pragma unroll
-    for (int m = 8; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, m));
-    const int k = scale_exponent(amax);
-    const float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);      // 2^-k, exact
-    const float sc = k < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-    uint32_t c[2] = {0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t two = static_cast<uint32_t>(
-          __nv_cvt_float2_to_fp8x2(make_float2(x[u][2 * i] * inv, x[u][2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3));
-      c[i >> 1] |= two << (16 * (i & 1));
-    }
-    if (v < p.Hi) {
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q_out) + o) = make_uint2(c[0], c[1]);
-      if (l == 0) p.w_out[t * p.Hi + v] = p.w[t * p.w_s0 + v] * p.weight_scale * sc;
-    } else if (ent) {
-      *reinterpret_cast<uint2*>(ent + d0) = make_uint2(c[0], c[1]);
-      if (l == 0) p.scales[blk * p.sc_stride + off] = sc;
-    }
+  }
+  if (!keyed || slot < 0) return;
+  const int64_t blk = slot / p.block_size, off = slot - blk * p.block_size;
+  if (blk >= p.num_blocks) {
+    if (l == 0) set_device_error(p.err, 4u);
+    return;
+  }
+  uint8_t* ent = p.cache + blk * p.block_stride + off * p.entry_stride;
+  float k[8];
+  bf16x8_values(raw_k, k);
+  rotate_vector(k, c, s, cs && l >= 8);
+  if (kBf16) {
+    *reinterpret_cast<uint4*>(ent + 2 * d0) = pack_bf16x8(k);
+  } else {
+    float sc;
+    *reinterpret_cast<uint2*>(ent + d0) = quantise_vector(k, half, sc);
+    if (l == 0) p.scales[blk * p.sc_stride + off] = sc;
   }
 }
 
 // ------------------------------------------------------------------------------------------
 // Gather: row r of request b (cu[b] <= r < cu[b+1]) is position starts[b] + r - cu[b], as
-// bf16(code * scale).  A half-warp writes a 256-byte row, 8 values a lane.
-template <bool kBf16>
+// bf16(code * scale).  A warp takes kRows neighbouring rows: each lane finds one row's key (the search
+// over cu, the page, the scale: five dependent loads), then half-warps write the 256-byte rows, 8
+// values a lane, with those addresses.
+template <bool kBf16, int kRows>
 __global__ void __launch_bounds__(128) mla_index_gather_kernel(const IndexGatherParams p) {
-  const int l = threadIdx.x & 15, d0 = 8 * l;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 4);
-  if (r >= p.num_tokens || r >= p.cu[p.batch] || r < p.cu[0]) return;
-  int lo = 0, hi = p.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.cu[mid] <= r) lo = mid; else hi = mid - 1;
-  }
-  const int64_t pos = static_cast<int64_t>(p.starts ? p.starts[lo] : 0) + (r - p.cu[lo]);
-  const int64_t col = pos >= 0 ? pos / p.block_size : -1;
-  const int64_t blk = col >= 0 && col < p.bt_cols ? p.block_table[lo * p.bt_stride + col] : -1;
-  uint4 y = make_uint4(0, 0, 0, 0);
-  if (blk < 0 || blk >= p.num_blocks) {
-    if (l == 0) set_device_error(p.err, 2u);
-  } else {
-    const int64_t off = pos % p.block_size;
-    const uint8_t* ent = p.cache + blk * p.block_stride + off * p.entry_stride;
-    if (kBf16) {
-      y = __ldg(reinterpret_cast<const uint4*>(ent + 2 * d0));
+  const int lane = threadIdx.x & 31, l = lane & 15, d0 = 8 * l;
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5)) * kRows;
+  const int64_t end = min(p.num_tokens, static_cast<int64_t>(p.cu[p.batch]));
+  if (r0 >= end) return;
+  const uint8_t* ent = nullptr;      // null: zeros
+  float scale = 0.f;
+  const int64_t r = r0 + lane, first = p.cu[0];
+  if (lane < kRows && r < end && r >= first) {
+    int lo = 0, hi = p.batch - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.cu[mid] <= r) lo = mid; else hi = mid - 1;
+    }
+    const int64_t pos = static_cast<int64_t>(p.starts ? p.starts[lo] : 0) + (r - p.cu[lo]);
+    const int64_t col = pos >= 0 ? pos / p.block_size : -1;
+    const int64_t blk = col >= 0 && col < p.bt_cols ? p.block_table[lo * p.bt_stride + col] : -1;
+    if (blk < 0 || blk >= p.num_blocks) {
+      set_device_error(p.err, 2u);
     } else {
-      const uint2 c = __ldg(reinterpret_cast<const uint2*>(ent + d0));
-      const float s = __ldg(p.scales + blk * p.sc_stride + off);
+      const int64_t off = pos - col * p.block_size;
+      ent = p.cache + blk * p.block_stride + off * p.entry_stride;
+      if (!kBf16) scale = __ldg(p.scales + blk * p.sc_stride + off);
+    }
+  }
+#pragma unroll 8
+  for (int i = 0; i < kRows / 2; ++i) {
+    const int src = 2 * i + (lane >> 4);
+    const uint8_t* e = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(ent), src));
+    const float s = __shfl_sync(0xFFFFFFFFu, scale, src);
+    if (r0 + src >= end || r0 + src < first) continue;
+    uint4 y = make_uint4(0, 0, 0, 0);
+    if (kBf16) {
+      if (e) y = __ldg(reinterpret_cast<const uint4*>(e + 2 * d0));
+    } else if (e) {
+      const uint2 c = __ldg(reinterpret_cast<const uint2*>(e + d0));
       const uint32_t w[2] = {c.x, c.y};
       float x[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+      for (int j = 0; j < 4; ++j) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));      // exact
-        x[2 * i] = f.x * s;
-        x[2 * i + 1] = f.y * s;
+        x[2 * j] = f.x * s;
+        x[2 * j + 1] = f.y * s;
       }
       y = pack_bf16x8(x);
     }
-  }
-  uint16_t* dst = p.dst + r * p.dst_row + d0;
-  if (p.vec) {
-    *reinterpret_cast<uint4*>(dst) = y;
-  } else {
-    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+    uint16_t* dst = p.dst + (r0 + src) * p.dst_row + d0;
+    if (p.vec) {
+      *reinterpret_cast<uint4*>(dst) = y;
+    } else {
+      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dst[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+      for (int j = 0; j < 8; ++j) dst[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+    }
   }
 }
 
@@ -660,22 +686,36 @@ __global__ void __launch_bounds__(128) mla_page_list_kernel(const PageListParams
 
 }  // namespace
 
-cudaError_t launch_index_insert(int bf16, const IndexInsertParams& p, cudaStream_t stream) {
-  const dim3 grid(p.T, (p.Hi + 1 + 8 * kInsVec - 1) / (8 * kInsVec));
+namespace {
+
+template <int kVec>
+cudaError_t insert_launch(int bf16, const IndexInsertParams& p, cudaStream_t stream) {
+  const dim3 grid(p.T, (p.Hi + 8 * kVec - 1) / (8 * kVec));
   if (bf16)
-    mla_index_insert_kernel<true><<<grid, 128, 0, stream>>>(p);
+    mla_index_insert_kernel<true, kVec><<<grid, 128, 0, stream>>>(p);
   else
-    mla_index_insert_kernel<false><<<grid, 128, 0, stream>>>(p);
+    mla_index_insert_kernel<false, kVec><<<grid, 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
-cudaError_t launch_index_gather(int bf16, const IndexGatherParams& p, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((p.num_tokens + 7) / 8);
+template <int kRows>
+cudaError_t gather_launch(int bf16, const IndexGatherParams& p, cudaStream_t stream) {
+  const unsigned grid = static_cast<unsigned>((p.num_tokens + 4 * kRows - 1) / (4 * kRows));
   if (bf16)
-    mla_index_gather_kernel<true><<<grid, 128, 0, stream>>>(p);
+    mla_index_gather_kernel<true, kRows><<<grid, 128, 0, stream>>>(p);
   else
-    mla_index_gather_kernel<false><<<grid, 128, 0, stream>>>(p);
+    mla_index_gather_kernel<false, kRows><<<grid, 128, 0, stream>>>(p);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_index_insert(int bf16, const IndexInsertParams& p, cudaStream_t stream) {
+  return p.T >= 1024 ? insert_launch<4>(bf16, p, stream) : insert_launch<2>(bf16, p, stream);
+}
+
+cudaError_t launch_index_gather(int bf16, const IndexGatherParams& p, cudaStream_t stream) {
+  return p.num_tokens >= 16384 ? gather_launch<32>(bf16, p, stream) : gather_launch<2>(bf16, p, stream);
 }
 
 static_assert(select_smem(kSelectMaxTopk) <= 227 * 1024, "shared memory budget");

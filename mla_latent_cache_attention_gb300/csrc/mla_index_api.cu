@@ -69,6 +69,7 @@ extern "C" int mla_index_q_cache_insert(const void* q, int64_t q_s0, int64_t q_s
   if ((positions == nullptr) != (cos_sin_cache == nullptr))
     return fail(MLA_ERR_INVALID, "positions and cos_sin_cache must be given together");
   if (positions && max_position < 1) return fail(MLA_ERR_INVALID, "max_position must be >= 1");
+  if (!aligned(cos_sin_cache, 16)) return fail(MLA_ERR_INVALID, "cos_sin_cache must be 16-byte aligned");
   DevInfo* d = nullptr;
   if (int rc = dev_info(&d)) return rc;
   IndexInsertParams p{};
