@@ -283,6 +283,12 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const uint32_t* p, uint32_t r
   return v;
 }
 
+__device__ __forceinline__ uint2 ld_cluster_v2(uint32_t cluster_addr) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 // Exclusive prefix of `own` over the threads of the CTA (two barriers).
 __device__ __forceinline__ uint32_t block_prefix(uint32_t own, uint32_t* wsum) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -305,9 +311,8 @@ struct Cut {
 };
 
 // The k largest of the keys val(0) .. val(m - 1) (0: none); with ranks > 1 of all CTAs' together.
-// `exact` false: the bin that holds the k-th largest is taken whole (at least k keys above thr).
 template <class Val>
-__device__ Cut find_cut(int m, uint32_t k, int ranks, bool exact, SelShared& s, Val val) {
+__device__ Cut find_cut(int m, uint32_t k, int ranks, SelShared& s, Val val) {
   const int tid = threadIdx.x, lane = tid & 31;
   uint32_t lo = 0xFFFFFFFFu, hi = 0, n = 0;
   for (int i = tid; i < m; i += kSelThreads) {
@@ -380,7 +385,7 @@ __device__ Cut find_cut(int m, uint32_t k, int ranks, bool exact, SelShared& s, 
     if (ranks > 1) cluster_sync();      // every CTA has read the others' histogram
     left -= s.found[1];
     lo += s.found[0] << shift;
-    if (!exact || s.found[2] == left) return Cut{lo - 1, 0u};       // the whole bin
+    if (s.found[2] == left) return Cut{lo - 1, 0u};       // the whole bin
     if (shift == 0) return Cut{lo, left};
     range = (1u << shift) - 1;
     __syncthreads();                    // found has been read
@@ -425,11 +430,14 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
   uint2* copy = list + cap;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t = blockIdx.x / ranks, rank = blockIdx.x % ranks;
-  if (tid == 0) {
+  if (warp == 0) {
     int64_t vis = 0;
-    s.row[0] = row_request(p.cu_q, p.seq_lens, p.B, t, &vis);
-    s.row[1] = vis;
-    s.count = 0;
+    const int b = row_request(p.cu_q, p.seq_lens, p.B, t, &vis);
+    if (lane == 0) {
+      s.row[0] = b;
+      s.row[1] = vis;
+      s.count = 0;
+    }
   }
   __syncthreads();
   const int b = static_cast<int>(s.row[0]);
@@ -461,24 +469,69 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
     return f;
   };
 
-  // ---- the bound: the score of the sample's rank that leaves about four standard deviations of room
+  // ---- the bound: the score of the sample's rank that leaves room for its error.  The sample is 1024
+  // groups of four neighbours spread over the row (a whole sector each), the same in every CTA of
+  // the cluster; its histogram divides the scores' range evenly.
   float bound = -CUDART_INF_F;
   bool strict = true;
   if (n > static_cast<int>(cap)) {
-    uint32_t* keys = reinterpret_cast<uint32_t*>(list);
-    const int64_t step = n;      // sample i is score floor(i n / 4096), the same in every CTA of the cluster
+    float f[8];
+    float lo = CUDART_INF_F, hi = -CUDART_INF_F;
 #pragma unroll
-    for (int j = 0; j < kSelSample / kSelThreads; ++j) {
-      const int i = tid + j * kSelThreads;
-      const float f = __ldg(x + (i * step) / kSelSample);
-      keys[i] = f > -CUDART_INF_F ? score_key(f) : 0u;
+    for (int j = 0; j < 2; ++j) {
+      const int64_t g = tid + j * kSelThreads;
+      const int i = static_cast<int>((g * n) >> 10) & ~3;
+      if (vec && i + 3 < n) {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(x + i));
+        f[4 * j] = w.x, f[4 * j + 1] = w.y, f[4 * j + 2] = w.z, f[4 * j + 3] = w.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[4 * j + e] = i + e < n ? __ldg(x + i + e) : CUDART_NAN_F;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (fabsf(f[j]) < CUDART_INF_F) lo = fminf(lo, f[j]), hi = fmaxf(hi, f[j]);       // finite ones
+    // order of floats as integers: the warps' extremes meet in shared memory
+    const uint32_t wlo = __reduce_min_sync(0xFFFFFFFFu, score_key(lo)), whi = __reduce_max_sync(0xFFFFFFFFu, score_key(hi));
+    if (tid == 0) s.stat[0] = 0xFFFFFFFFu, s.stat[1] = 0, s.stat[2] = 0;
+    reinterpret_cast<uint4*>(s.hist)[tid] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    if (lane == 0) {
+      atomicMin(&s.stat[0], wlo);
+      atomicMax(&s.stat[1], whi);
     }
     __syncthreads();
-    const float r = static_cast<float>(kk) * kSelSample / n;
-    const Cut c = find_cut(kSelSample, static_cast<uint32_t>(r + 4.f * sqrtf(r) + 8.f), 1, false, s, [&](int i) { return keys[i]; });
-    if (c.thr) {
-      bound = key_score(c.thr + 1);
-      strict = false;
+    lo = key_score(s.stat[0]);
+    hi = key_score(s.stat[1]);
+    const float scale = 2047.f / (hi - lo);
+    if (hi > lo && scale > 0.f && scale < CUDART_INF_F) {
+      uint32_t inf = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (fabsf(f[j]) < CUDART_INF_F) atomicAdd(&s.hist[static_cast<int>((f[j] - lo) * scale)], 1u);
+        inf += f[j] == CUDART_INF_F ? 1u : 0u;
+      }
+      if (inf) atomicAdd(&s.hist[kSelBins - 1], inf);
+      __syncthreads();
+      const float r = static_cast<float>(kk) * kSelSample / n;
+      const uint32_t rank = static_cast<uint32_t>(r + 6.f * sqrtf(r) + 8.f);
+      const uint4 c = reinterpret_cast<const uint4*>(s.hist)[kSelThreads - 1 - tid];      // bins 2047 - 4 tid .. 2044 - 4 tid
+      const uint32_t own = c.x + c.y + c.z + c.w;
+      uint32_t before = block_prefix(own, s.wsum);
+      if (before < rank && rank <= before + own) {       // at most one thread
+        uint32_t bin = kSelBins - 1 - 4 * tid;
+        if (rank > before + c.w) before += c.w, --bin;
+        if (bin == kSelBins - 2 - 4 * tid && rank > before + c.z) before += c.z, --bin;
+        if (bin == kSelBins - 3 - 4 * tid && rank > before + c.y) --bin;
+        s.found[0] = __float_as_uint(lo + static_cast<float>(bin) / scale);
+        s.stat[2] = 1;
+      }
+      __syncthreads();
+      if (s.stat[2]) {
+        bound = __uint_as_float(s.found[0]);
+        strict = false;
+      }
     }
     __syncthreads();
   }
@@ -504,20 +557,33 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
   if (ranks > 1) {
     cluster_sync();
     total = 0;
-    for (int r = 0; r < ranks; ++r) {
-      const uint32_t c = ld_cluster_u32(&s.count, r);
-      total += c;
-      good = good && c <= cap;
-    }
+    for (int r = 0; r < ranks; ++r) total += ld_cluster_u32(&s.count, r);
+    good = total <= cap;
     cluster_sync();
   }
   // fewer than topk although the row was not let in whole: the bound was too high
   good = good && (strict || total >= static_cast<uint32_t>(p.topk));
   int m = static_cast<int>(s.count);
+  int cut_ranks = ranks;          // CTAs whose lists the last cut is over
   if (good) {
     for (int i = tid; i < m; i += kSelThreads) {
       const int c = static_cast<int>(list[i].y);
       list[i].x = c < f_lo || c >= f_hi ? kForcedKey : score_key(__uint_as_float(list[i].x));
+    }
+    if (ranks > 1) {
+      // the cluster's lists together fit: every CTA appends the others' to its own and cuts the whole
+      cluster_sync();
+      int at = m;
+      for (int r = 1; r < ranks; ++r) {
+        const uint32_t from_rank = (rank + r) % ranks;
+        const int count = static_cast<int>(ld_cluster_u32(&s.count, from_rank));
+        const uint32_t src = mapa_shared(list, from_rank);
+        for (int i = tid; i < count; i += kSelThreads) list[at + i] = ld_cluster_v2(src + 8 * i);
+        at += count;
+      }
+      m = at;
+      cut_ranks = 1;
+      cluster_sync();       // the lists have been read
     }
   } else {
     // ---- in order, cutting the list whenever it is full
@@ -545,9 +611,9 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
           break;
         }
         // the list of the rounds before this one, cut to its topk; then the round again
-        const Cut c = find_cut(m, kk, 1, true, s, [&](int i) { return list[i].x == kForcedKey ? 0u : list[i].x; });
+        const Cut c = find_cut(m, kk, 1, s, [&](int i) { return list[i].x == kForcedKey ? 0u : list[i].x; });
         uint32_t first = 0;
-        if (c.ties) first = find_cut(m, c.ties, 1, true, s, [&](int i) { return list[i].x == c.thr ? ~list[i].y : 0u; }).thr;
+        if (c.ties) first = find_cut(m, c.ties, 1, s, [&](int i) { return list[i].x == c.thr ? ~list[i].y : 0u; }).thr;
         if (tid == 0) s.count = 0;
         __syncthreads();
         for (int i = tid; i < m; i += kSelThreads) {
@@ -568,28 +634,34 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
   __syncthreads();
 
   // ---- the last cut, over the row
-  const Cut c = find_cut(m, kk, ranks, true, s, [&](int i) { return list[i].x == kForcedKey ? 0u : list[i].x; });
+  const Cut c = find_cut(m, kk, cut_ranks, s, [&](int i) { return list[i].x == kForcedKey ? 0u : list[i].x; });
   uint32_t first = 0;
-  if (c.ties) first = find_cut(m, c.ties, ranks, true, s, [&](int i) { return list[i].x == c.thr ? ~list[i].y : 0u; }).thr;
+  if (c.ties) first = find_cut(m, c.ties, cut_ranks, s, [&](int i) { return list[i].x == c.thr ? ~list[i].y : 0u; }).thr;
   auto taken = [&](uint2 e) { return e.x > c.thr || (c.ties && e.x == c.thr && ~e.y > first); };
   int32_t* out = p.blocks + t * p.b_stride;
   int32_t* out_slots = p.slots ? p.slots + t * p.sl_stride : nullptr;
   uint32_t at = 0, all = 0;      // positions before this CTA's part, and of the row
   if (ranks > 1) {
-    uint32_t mine = 0;
-    for (int i = tid; i < m; i += kSelThreads) mine += taken(list[i]) ? 1u : 0u;
+    uint32_t mine = 0;           // taken entries (| those before the part << 16, where the list is the row's)
+    for (int i = tid; i < m; i += kSelThreads)
+      if (taken(list[i])) mine += cut_ranks == 1 && list[i].y < static_cast<uint32_t>(from) ? 0x10001u : 1u;
     mine = __reduce_add_sync(0xFFFFFFFFu, mine);
     if (tid == 0) s.stat[3] = 0;
     __syncthreads();
     if (lane == 0) atomicAdd(&s.stat[3], mine);
     __syncthreads();
-    cluster_sync();
-    for (int r = 0; r < ranks; ++r) {
-      const uint32_t v = ld_cluster_u32(&s.stat[3], r);
-      if (r < rank) at += v;
-      all += v;
+    if (cut_ranks == 1) {
+      at = s.stat[3] >> 16;
+      all = s.stat[3] & 0xFFFFu;
+    } else {
+      cluster_sync();
+      for (int r = 0; r < ranks; ++r) {
+        const uint32_t v = ld_cluster_u32(&s.stat[3], r);
+        if (r < rank) at += v;
+        all += v;
+      }
+      cluster_sync();       // no CTA leaves while another may read its count
     }
-    cluster_sync();       // no CTA leaves while another may read its count
   }
   // ---- the map, 65536 indices at a time, and its bits in order
   for (int w0 = from; w0 < to; w0 += 32 * kSelBins) {
@@ -598,7 +670,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
     for (int i = tid; i < m; i += kSelThreads) {
       const uint2 e = list[i];
       const uint32_t d = e.y - w0;
-      if (d < 32 * kSelBins && taken(e)) atomicOr(&s.hist[d >> 5], 1u << (d & 31));
+      if (d < static_cast<uint32_t>(min(to - w0, 32 * kSelBins)) && taken(e)) atomicOr(&s.hist[d >> 5], 1u << (d & 31));
     }
     __syncthreads();
     const uint4 w = reinterpret_cast<const uint4*>(s.hist)[tid];

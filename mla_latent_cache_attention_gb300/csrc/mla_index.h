@@ -113,20 +113,32 @@ cudaError_t launch_index_scores(int bf16, int hp, const IndexScoresParams& p, co
 cudaError_t launch_index_select(const IndexSelectParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_page_list(const PageListParams& p, cudaStream_t stream);
 
-// Request of row t and the keys the row sees (seq_len - rows of the request + its place + 1),
-// by search over cu_q (null: row t is request t).  A row of no request gives -1.
+// Request of row t and the keys the row sees (seq_len - rows of the request + its place + 1), for a
+// whole warp: a 32-way search over cu_q (null: row t is request t).  A row of no request gives -1.
 __device__ __forceinline__ int row_request(const int32_t* cu_q, const int32_t* seq_lens, int B, int t, int64_t* visible) {
   int b = t, place = 0, n = 1;
   if (cu_q) {
-    if (t < cu_q[0] || t >= cu_q[B]) return -1;
-    int lo = 0, hi = B - 1;      // the last request that starts at or before t
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (cu_q[mid] <= t) lo = mid; else hi = mid - 1;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = B + 1;         // the last entry at or below t is in cu_q[lo .. lo + len)
+    bool found = true;
+    while (len > 1) {
+      const int step = (len + 31) / 32, i = lo + lane * step;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, lane * step < len && cu_q[i < B ? i : B] <= t);
+      if (m == 0) {
+        found = false;
+        break;
+      }
+      const int last = 31 - __clz(m);
+      lo += last * step;
+      len = min(step, len - last * step);
     }
+    if (!found || lo >= B) return -1;
     b = lo;
-    place = t - cu_q[b];
-    n = cu_q[b + 1] - cu_q[b];
+    const int first = cu_q[b];
+    if (t < first) return -1;
+    place = t - first;
+    n = cu_q[b + 1] - first;
+    if (place >= n) return -1;
   } else if (t >= B) {
     return -1;
   }
