@@ -251,7 +251,8 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelSample = 4096;
 constexpr int kSelChunk = 4096;                          // list entries beyond topk; scores of an ordered round
 constexpr int kSelBins = 2048;
-constexpr int kSelFixed = kSelBins * 4 + 256;
+constexpr int kSelAhead = 8192;                          // scores of a row that are asked for ahead of their use
+constexpr int kSelFixed = kSelBins * 4 + 512;
 
 // Shared memory of a row with topk: the list (topk + a chunk), a copy of topk entries for a cut.
 __host__ __device__ constexpr int64_t select_smem(int64_t topk) { return kSelFixed + (2 * topk + kSelChunk) * 8; }
@@ -267,12 +268,12 @@ constexpr uint32_t kForcedKey = 0xFFFFFFFFu;
 
 struct SelShared {
   uint32_t hist[kSelBins];        // histogram, or the map of 65536 indices
-  uint32_t wsum[kSelWarps];
+  uint32_t wsum[32];              // totals of the warps; the last keys of a cut
   uint32_t stat[4];               // smallest key, largest key, their number, entries taken
   uint32_t found[4];              // bin, keys above it, keys in it
   uint32_t count;                 // entries of the list
-  uint32_t pad;
-  int64_t row[2];
+  uint32_t counts[9];             // of the cluster's lists: prefix sums in the order they are appended
+  int64_t row[2];                 // request and visible keys
 };
 static_assert(sizeof(SelShared) <= kSelFixed, "shared memory layout");
 
@@ -388,15 +389,40 @@ __device__ Cut find_cut(int m, uint32_t k, int ranks, SelShared& s, Val val) {
     if (s.found[2] == left) return Cut{lo - 1, 0u};       // the whole bin
     if (shift == 0) return Cut{lo, left};
     range = (1u << shift) - 1;
+    const bool few = ranks == 1 && s.found[2] <= 32;
     __syncthreads();                    // found has been read
+    if (few) {                          // a warp ranks the bin's keys
+      if (tid == 0) s.found[3] = 0;
+      __syncthreads();
+      for (int i = tid; i < m; i += kSelThreads) {
+        const uint32_t key = val(i);
+        if (key >= lo && key - lo <= range) s.wsum[atomicAdd(&s.found[3], 1u)] = key;
+      }
+      __syncthreads();
+      if (tid < 32) {
+        const int cnt = static_cast<int>(s.found[3]);
+        const uint32_t key = lane < cnt ? s.wsum[lane] : 0u;
+        uint32_t above = 0, same = 0;
+        for (int i = 0; i < cnt; ++i) {
+          const uint32_t o = __shfl_sync(0xFFFFFFFFu, key, i);
+          above += o > key ? 1u : 0u;
+          same += o == key ? 1u : 0u;
+        }
+        if (lane < cnt && above < left && left <= above + same) {      // every lane that holds the key agrees
+          s.found[0] = left == above + same ? key - 1 : key;
+          s.found[1] = left == above + same ? 0u : left - above;
+        }
+      }
+      __syncthreads();
+      return Cut{s.found[0], s.found[1]};
+    }
   }
 }
 
-// Adds the entries of a warp's `take` bits (bit j: value v[j] at index i0 + 128 (j / 4) + 4 lane + j % 4)
+// Adds the entries of a warp's `take` bits (bit j: index i0 + 128 (j / 4) + 4 lane + j % 4 of x)
 // to the list; those past its end are dropped, which the count shows.
-template <int N>
-__device__ __forceinline__ void append(uint2* list, uint32_t cap, uint32_t* count, uint32_t take, const float (&v)[N], int i0,
-                                       bool as_key, int f_lo, int f_hi) {
+__device__ __forceinline__ void append(uint2* list, uint32_t cap, uint32_t* count, uint32_t take, const float* __restrict__ x,
+                                       int i0, bool as_key, int f_lo, int f_hi) {
   if (!__any_sync(0xFFFFFFFFu, take)) return;
   const int lane = threadIdx.x & 31;
   const uint32_t mine = __popc(take);
@@ -410,41 +436,36 @@ __device__ __forceinline__ void append(uint2* list, uint32_t cap, uint32_t* coun
   if (lane == 31) base = atomicAdd(count, inc);
   base = __shfl_sync(0xFFFFFFFFu, base, 31);
   uint32_t pos = base + inc - mine;
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    if ((take >> j) & 1u) {
-      const int i = i0 + (j >> 2) * 128 + 4 * lane + (j & 3);
-      uint32_t bits = __float_as_uint(v[j]);
-      if (as_key) bits = i < f_lo || i >= f_hi ? kForcedKey : score_key(v[j]);
+  // few are taken: their values are read again (from L1) instead of picked out of registers
+  while (__any_sync(0xFFFFFFFFu, take)) {
+    if (take) {
+      const int j = __ffs(take) - 1, i = i0 + (j >> 2) * 128 + 4 * lane + (j & 3);
+      take &= take - 1;
+      const float v = __ldg(x + i);
+      uint32_t bits = __float_as_uint(v);
+      if (as_key) bits = i < f_lo || i >= f_hi ? kForcedKey : score_key(v);
       if (pos < cap) list[pos] = make_uint2(bits, static_cast<uint32_t>(i));
       ++pos;
     }
   }
 }
 
-__global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const IndexSelectParams p, int ranks) {
-  extern __shared__ __align__(16) uint8_t sel_smem[];
-  SelShared& s = *reinterpret_cast<SelShared*>(sel_smem);
-  uint2* list = reinterpret_cast<uint2*>(sel_smem + kSelFixed);       // (score bits, then key; index)
+// Group g of the sample: four neighbours of the n scores.
+__device__ __forceinline__ int sample_at(int g, int n) { return static_cast<int>((static_cast<int64_t>(g) * n) >> 10) & ~3; }
+
+__device__ __forceinline__ int select_blocks_of(const IndexSelectParams& p, int64_t vis) {
+  return static_cast<int>(min((vis + p.block_tokens - 1) / p.block_tokens, p.width));
+}
+
+__device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, int rank, int ranks, int b, int64_t vis,
+                                           int resident, SelShared& s, uint2* list) {
   const uint32_t cap = p.topk + kSelChunk;
   uint2* copy = list + cap;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int t = blockIdx.x / ranks, rank = blockIdx.x % ranks;
-  if (warp == 0) {
-    int64_t vis = 0;
-    const int b = row_request(p.cu_q, p.seq_lens, p.B, t, &vis);
-    if (lane == 0) {
-      s.row[0] = b;
-      s.row[1] = vis;
-      s.count = 0;
-    }
-  }
+  if (tid == 0) s.count = 0;
   __syncthreads();
-  const int b = static_cast<int>(s.row[0]);
-  const int64_t vis = s.row[1];
-  if (b < 0) return;       // every CTA of the cluster
   const float* __restrict__ x = p.scores + t * p.s_stride;
-  const int n = static_cast<int>(min((vis + p.block_tokens - 1) / p.block_tokens, p.width));
+  const int n = select_blocks_of(p, vis);
   const int f_lo = min(p.first, n), f_hi = max(f_lo, n - p.last);      // forced: below f_lo, from f_hi on
   const uint32_t kk = p.topk - (f_lo + n - f_hi);                // places of the others
   const int part = ((n + ranks - 1) / ranks + 3) & ~3;
@@ -479,8 +500,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
     float lo = CUDART_INF_F, hi = -CUDART_INF_F;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int64_t g = tid + j * kSelThreads;
-      const int i = static_cast<int>((g * n) >> 10) & ~3;
+      const int i = sample_at(tid + j * kSelThreads, n);
       if (vec && i + 3 < n) {
         const float4 w = __ldg(reinterpret_cast<const float4*>(x + i));
         f[4 * j] = w.x, f[4 * j + 1] = w.y, f[4 * j + 2] = w.z, f[4 * j + 3] = w.w;
@@ -538,6 +558,8 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
   // ---- stream: a warp takes 512 neighbouring scores at a time, 4 a lane and load
   for (int i0 = from + warp * 512; i0 < to; i0 += kSelWarps * 512) {
     float v[16];
+    const int ahead = i0 + kSelAhead + 32 * lane;      // later scores, a line a lane
+    if (lane < 16 && ahead < to) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + ahead));
 #pragma unroll
     for (int j = 0; j < 4; ++j) load4(i0 + 128 * j + 4 * lane, v + 4 * j);
     uint32_t take = 0;
@@ -549,45 +571,53 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
       for (int j = 0; j < 16; ++j) take |= (v[j] >= bound ? 1u : 0u) << j;
     }
     if (i0 < f_lo || i0 + 512 > f_hi) take |= forced_bits(i0, 4);
-    append(list, cap, &s.count, take, v, i0, false, f_lo, f_hi);
+    append(list, cap, &s.count, take, x, i0, false, f_lo, f_hi);
+  }
+  // The row that will follow on this SM: its start comes into L2 while this one is cut.
+  if (resident > 0 && tid < 32 && t + resident < p.T) {
+    const float* next = p.scores + static_cast<int64_t>(t + resident) * p.s_stride;
+    for (int i = 32 * lane; i < min(n, kSelAhead); i += 1024) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i));
   }
   __syncthreads();
-  bool good = s.count <= cap;
   uint32_t total = s.count;
+  int m = static_cast<int>(min(total, cap));
+  for (int i = tid; i < m; i += kSelThreads) {
+    const int c = static_cast<int>(list[i].y);
+    list[i].x = c < f_lo || c >= f_hi ? kForcedKey : score_key(__uint_as_float(list[i].x));
+  }
   if (ranks > 1) {
     cluster_sync();
-    total = 0;
-    for (int r = 0; r < ranks; ++r) total += ld_cluster_u32(&s.count, r);
-    good = total <= cap;
-    cluster_sync();
+    if (warp == 0) {      // counts of the other CTAs' lists, from the next one on
+      uint32_t c = lane < ranks ? ld_cluster_u32(&s.count, (rank + lane) % ranks) : 0u;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, c, o);
+        if (lane >= o) c += v;
+      }
+      if (lane < 8) s.counts[lane + 1] = c;
+    }
+    __syncthreads();
+    total = s.counts[ranks];
   }
-  // fewer than topk although the row was not let in whole: the bound was too high
-  good = good && (strict || total >= static_cast<uint32_t>(p.topk));
-  int m = static_cast<int>(s.count);
+  // Too many for the list, or fewer than topk although the row was not let in whole (the bound was too
+  // high): not good.
+  const bool good = total <= cap && (strict || total >= static_cast<uint32_t>(p.topk));
   int cut_ranks = ranks;          // CTAs whose lists the last cut is over
   if (good) {
-    for (int i = tid; i < m; i += kSelThreads) {
-      const int c = static_cast<int>(list[i].y);
-      list[i].x = c < f_lo || c >= f_hi ? kForcedKey : score_key(__uint_as_float(list[i].x));
-    }
     if (ranks > 1) {
       // the cluster's lists together fit: every CTA appends the others' to its own and cuts the whole
-      cluster_sync();
-      int at = m;
-      for (int r = 1; r < ranks; ++r) {
-        const uint32_t from_rank = (rank + r) % ranks;
-        const int count = static_cast<int>(ld_cluster_u32(&s.count, from_rank));
-        const uint32_t src = mapa_shared(list, from_rank);
-        for (int i = tid; i < count; i += kSelThreads) list[at + i] = ld_cluster_v2(src + 8 * i);
-        at += count;
+      for (int i = m + tid; i < static_cast<int>(total); i += kSelThreads) {
+        int r = 1;
+        while (static_cast<uint32_t>(i) >= s.counts[r + 1]) ++r;
+        list[i] = ld_cluster_v2(mapa_shared(list + (i - s.counts[r]), (rank + r) % ranks));
       }
-      m = at;
+      m = static_cast<int>(total);
       cut_ranks = 1;
-      cluster_sync();       // the lists have been read
     }
+    if (ranks > 1) cluster_sync();       // the lists have been read
   } else {
     // ---- in order, cutting the list whenever it is full
-    __syncthreads();
+    if (ranks > 1) cluster_sync(); else __syncthreads();       // the counts have been read
     m = 0;
     bound = -CUDART_INF_F;
     for (int c0 = from; c0 < to; c0 += kSelChunk) {
@@ -602,7 +632,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
 #pragma unroll
         for (int j = 0; j < 8; ++j) take |= (v[j] > bound ? 1u : 0u) << j;
         if (i0 < f_lo || i0 + 256 > f_hi) take |= forced_bits(i0, 2);
-        append(list, cap, &s.count, take, v, i0, true, f_lo, f_hi);
+        append(list, cap, &s.count, take, x, i0, true, f_lo, f_hi);
         __syncthreads();
         const int now = static_cast<int>(s.count);
         __syncthreads();
@@ -712,6 +742,23 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
   }
 }
 
+__global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const IndexSelectParams p, int ranks, int resident) {
+  extern __shared__ __align__(16) uint8_t sel_smem[];
+  SelShared& s = *reinterpret_cast<SelShared*>(sel_smem);
+  uint2* list = reinterpret_cast<uint2*>(sel_smem + kSelFixed);       // (score bits, then key; index)
+  const int t = blockIdx.x / ranks, rank = blockIdx.x % ranks;
+  if (threadIdx.x < 32) {
+    int64_t vis = 0;
+    const int b = row_request(p.cu_q, p.seq_lens, p.B, t, &vis);
+    if (threadIdx.x == 0) {
+      s.row[0] = b;
+      s.row[1] = vis;
+    }
+  }
+  __syncthreads();
+  if (s.row[0] >= 0) select_row(p, t, rank, ranks, static_cast<int>(s.row[0]), s.row[1], resident, s, list);
+}
+
 // ------------------------------------------------------------------------------------------
 // Page lists.  One warp per row keeps the visible pages of its list in order and puts the partly
 // visible one (the row's newest page, when its last tokens are hidden or unwritten) last, so that
@@ -805,9 +852,10 @@ cudaError_t launch_index_select(const IndexSelectParams& p, int sms, cudaStream_
   }
   // CTAs that share a row: while the batch leaves SMs idle and a part keeps two chunks
   int ranks = 1;
-  while (ranks < 8 && static_cast<int64_t>(p.T) * ranks * 2 <= 2 * sms && p.width / (ranks * 2) >= 2 * kSelChunk) ranks *= 2;
+  while (ranks < 8 && static_cast<int64_t>(p.T) * ranks * 2 <= sms && p.width / (ranks * 2) >= 2 * kSelChunk) ranks *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.T) * ranks);
+  const int resident = ranks == 1 && p.T > 3 * sms ? 3 * sms : 0;
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(select_smem(p.topk));
   cfg.stream = stream;
@@ -817,7 +865,7 @@ cudaError_t launch_index_select(const IndexSelectParams& p, int sms, cudaStream_
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_index_select_kernel, p, ranks);
+  return cudaLaunchKernelEx(&cfg, mla_index_select_kernel, p, ranks, resident);
 }
 
 cudaError_t launch_page_list(const PageListParams& p, cudaStream_t stream) {
