@@ -105,7 +105,7 @@ def lib():
                                        i32, i32, i32, i32, vp, i64, i64, vp]
         L.mla_index_select.argtypes = [vp, i64, i64, vp, vp, i32, i32, i32, i32, i32, i32, vp, i64, vp, i64, vp, i64,
                                        i64, i32, i64, vp]
-        L.mla_selected_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        L.mla_selected_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
         L.mla_selected_decode_workspace_size.restype = sz
         L.mla_selected_decode.argtypes = [vp, i64, i64, vp, i32, i64, i64, i64, i32, vp, i64, i64, vp, vp, vp, i64, i32,
                                           i32, i32, i32, f32, f32, f32, vp, i64, i64, vp, vp, sz, vp]
@@ -740,8 +740,8 @@ def index_select(scores, seq_lens, topk, cu_q_lens=None, *, block_tokens=1, firs
     return blocks, slots
 
 
-def selected_decode_workspace_size(T, topk, block_size, H, num_sms=0) -> int:
-    return int(lib().mla_selected_decode_workspace_size(T, topk, block_size, H, num_sms))
+def selected_decode_workspace_size(fmt, T, topk, block_size, H, num_sms=0) -> int:
+    return int(lib().mla_selected_decode_workspace_size(_fmt(fmt), T, topk, block_size, H, num_sms))
 
 
 def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, *, fmt, softmax_scale, q_scale=1.0,
@@ -774,13 +774,17 @@ def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, 
     elif return_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=dev)
     nb, bstride, estride, bs = _cache_geometry(kv_cache)
+    L = lib()
     if workspace is None:
-        with torch.cuda.device(dev):
-            need = selected_decode_workspace_size(T, topk, bs, H)
+        if torch.cuda.current_device() == dev.index:
+            need = L.mla_selected_decode_workspace_size(fmt, T, topk, bs, H, 0)
+        else:
+            with torch.cuda.device(dev):
+                need = L.mla_selected_decode_workspace_size(fmt, T, topk, bs, H, 0)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", _BYTE_TYPES, dev, contiguous=True)
-    _call(lib().mla_selected_decode, dev, q.data_ptr(), qs[0], qs[1], kv_cache.data_ptr(), fmt, nb, bstride, estride, bs,
+    _call(L.mla_selected_decode, dev, q.data_ptr(), qs[0], qs[1], kv_cache.data_ptr(), fmt, nb, bstride, estride, bs,
           table, tstride, tcols, seq_lens.data_ptr(), cu, blocks.data_ptr(), max(ls[0], topk), topk, B, T, H,
           float(softmax_scale), float(q_scale), float(k_scale), out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(),
           workspace.data_ptr(), workspace.numel() * workspace.element_size())

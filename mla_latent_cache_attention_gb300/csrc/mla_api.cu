@@ -75,11 +75,6 @@ int entry_bytes(mla_cache_format f) {
   return f == MLA_CACHE_BF16 ? 1152 : f == MLA_CACHE_FP8 ? 576 : 656;
 }
 
-struct SplitPlan {
-  int n_splits;
-  int64_t chunk;
-};
-
 // Split-K plan of the paged decode.  The split count depends on the number of (request,
 // column group) units, max_context and the SM count only -- never on seq_lens -- as the
 // pages' decode core fixes its split count from the deployment's longest sequence.  Aim for
@@ -101,6 +96,8 @@ int64_t plan_units(int64_t B, int q_len, int H) {
   return B * ((static_cast<int64_t>(q_len) * H + 63) / 64);
 }
 
+}  // namespace
+
 // Partials [S][rows][H][512] fp32, their LSEs, and one scheduler word.
 size_t workspace_bytes_for(int64_t n_rows, int H, const SplitPlan& sp) {
   if (sp.n_splits <= 1) return 0;
@@ -108,6 +105,13 @@ size_t workspace_bytes_for(int64_t n_rows, int H, const SplitPlan& sp) {
   const size_t pl = static_cast<size_t>(sp.n_splits) * n_rows * H * sizeof(float);
   return ((po + 255) & ~size_t(255)) + ((pl + 255) & ~size_t(255)) + 256;
 }
+
+uint32_t* sched_word(void* workspace, int64_t n_rows, int H, const SplitPlan& sp) {
+  if (sp.n_splits <= 1) return nullptr;
+  return reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + workspace_bytes_for(n_rows, H, sp) - 256);
+}
+
+namespace {
 
 // Test aid: wait limit (microseconds) of the next page-kernel launch on this thread, whose
 // producer then issues no loads; 0 = none armed.
@@ -766,9 +770,55 @@ extern "C" int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const
   if (B == 0) return ok();
   DevInfo* d = nullptr;
   if (int rc = dev_info(&d)) return rc;
+  return run_paged_decode(q, q_s0, q_s1, kv_cache, fmt, num_blocks, block_stride_bytes, entry_stride_bytes, block_size,
+                          block_table, bt_stride, seq_lens, B, q_len, H, max_context, softmax_scale, q_scale, k_scale, out,
+                          o_s0, o_s1, lse, workspace, workspace_bytes,
+                          plan_splits(plan_units(B, q_len, H), max_context, d->sms), false, stream);
+}
+
+// Split plan of a decode over selected pages: `context` keys a row at most, all rows alike.  The split
+// count with the least estimated time: waves of work items (3.3 us a 128-key tile, 6 us an item's start and
+// end, as measured for the three formats), and the merge of the partials where there are several.
+// Against the long contexts' rule of at least four tiles a split: 16 pages of 64 (bf16, 32 rows, 16
+// heads) 35 -> 25 us with four splits instead of two; 32 pages (fp8_ds_mla, 128 rows, 96 heads) 412 -> 315 us
+// with one instead of four.
+SplitPlan mla::plan_selected(int fmt, int64_t T, int H, int64_t context, int sms) {
+  const int64_t tiles = (context + kTile - 1) / kTile;
+  int64_t groups = 1, slots = sms;
+  ColPlan cp{};
+  if (fmt == MLA_CACHE_FP8_DS_MLA) {
+    groups = (H + 15) / 16;
+    if (groups % 2 == 0) groups /= 2, slots /= 2;       // pairs of CTAs
+  } else if (plan_columns(fmt, H, 1, &cp)) {
+    groups = cp.G;
+  } else {
+    groups = (H + kRows - 1) / kRows;
+  }
+  if (slots < 1) slots = 1;
+  int64_t best = 1;
+  double best_us = 0;
+  for (int64_t s = 1; s <= tiles && s <= 64; ++s) {
+    const int64_t per = (tiles + s - 1) / s;
+    if (s > 1 && (tiles + per - 1) / per != s) continue;       // the same parts as a smaller count
+    const int64_t waves = (T * groups * s + slots - 1) / slots;
+    double us = static_cast<double>(waves) * (3.3 * per + 6.0);
+    if (s > 1) us += 3.0 + 4096.0 * static_cast<double>(s * T * H) / 5e6;
+    if (s == 1 || us < best_us) best = s, best_us = us;
+  }
+  return SplitPlan{static_cast<int>(best), (tiles + best - 1) / best * kTile};
+}
+
+int mla::run_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache, int cache_fmt, int64_t num_blocks,
+                          int64_t block_stride_bytes, int64_t entry_stride_bytes, int32_t block_size,
+                          const int32_t* block_table, int64_t bt_stride, const int32_t* seq_lens, int32_t B,
+                          int32_t q_len, int32_t H, int32_t max_context, float softmax_scale, float q_scale,
+                          float k_scale, void* out, int64_t o_s0, int64_t o_s1, float* lse, void* workspace,
+                          size_t workspace_bytes, const SplitPlan& sp, bool sched_ready, cudaStream_t stream) {
+  const mla_cache_format fmt = static_cast<mla_cache_format>(cache_fmt);
+  DevInfo* d = nullptr;
+  if (int rc = dev_info(&d)) return rc;
   const int64_t n_rows = static_cast<int64_t>(B) * q_len;
   const int n_hgroups = (H + kRows - 1) / kRows;
-  const SplitPlan sp = plan_splits(plan_units(B, q_len, H), max_context, d->sms);
   const size_t need = workspace_bytes_for(n_rows, H, sp);
   if (need > 0) {
     if (!workspace || workspace_bytes < need)
@@ -780,11 +830,9 @@ extern "C" int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const
   uint32_t* sched = nullptr;
   if (sp.n_splits > 1) {
     const size_t po = static_cast<size_t>(sp.n_splits) * n_rows * H * kLora * sizeof(float);
-    const size_t pl = static_cast<size_t>(sp.n_splits) * n_rows * H * sizeof(float);
     part_o = static_cast<float*>(workspace);
     part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ((po + 255) & ~size_t(255)));
-    sched = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + ((po + 255) & ~size_t(255)) +
-                                        ((pl + 255) & ~size_t(255)));
+    sched = sched_word(workspace, n_rows, H, sp);
   }
   const float sigma = fmt == MLA_CACHE_FP8 ? softmax_scale * q_scale * k_scale : softmax_scale;
   const float out_scale = fmt == MLA_CACHE_FP8 ? k_scale : 1.f;
@@ -836,7 +884,7 @@ extern "C" int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const
     p.sched = sched;
     p.err = d->err;
     p.partial = sp.n_splits > 1 ? 1 : 0;
-    if (sched && launch_sched_reset(sched, stream) != cudaSuccess)
+    if (sched && !sched_ready && launch_sched_reset(sched, stream) != cudaSuccess)
       return fail(MLA_ERR_CUDA, "scheduler reset failed: %s", cudaGetErrorString(cudaGetLastError()));
     prof_begin(stream);
     const cudaError_t e =
@@ -919,7 +967,7 @@ extern "C" int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const
     p.wait_us = g_stall_next_us;
     p.stall = g_stall_next_us > 0 ? 1 : 0;
     g_stall_next_us = 0;
-    if (sched && launch_sched_reset(sched, stream) != cudaSuccess)
+    if (sched && !sched_ready && launch_sched_reset(sched, stream) != cudaSuccess)
       return fail(MLA_ERR_CUDA, "scheduler reset failed: %s", cudaGetErrorString(cudaGetLastError()));
     const int grid = grid_for(items, d->sms);
     prof_begin(stream);

@@ -34,4 +34,23 @@ int check_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv
                        int32_t q_len, int32_t H, int32_t max_context, const void* out, int64_t o_s0, int64_t o_s1,
                        const float* lse);
 
+
+// Split-K plan of a paged decode: n_splits parts of `chunk` keys.
+struct SplitPlan {
+  int n_splits;
+  int64_t chunk;
+};
+SplitPlan plan_selected(int fmt, int64_t T, int H, int64_t context, int sms);
+// Workspace of a plan, and the address of its scheduler word there (null without splits).
+size_t workspace_bytes_for(int64_t n_rows, int H, const SplitPlan& sp);
+uint32_t* sched_word(void* workspace, int64_t n_rows, int H, const SplitPlan& sp);
+// mla_paged_decode after its checks, with a plan; sched_ready: the scheduler word is zeroed by earlier
+// work of the stream.
+int run_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache, int cache_fmt, int64_t num_blocks,
+                     int64_t block_stride_bytes, int64_t entry_stride_bytes, int32_t block_size,
+                     const int32_t* block_table, int64_t bt_stride, const int32_t* seq_lens, int32_t B, int32_t q_len,
+                     int32_t H, int32_t max_context, float softmax_scale, float q_scale, float k_scale, void* out,
+                     int64_t o_s0, int64_t o_s1, float* lse, void* workspace, size_t workspace_bytes,
+                     const SplitPlan& sp, bool sched_ready, cudaStream_t stream);
+
 }  // namespace mla

@@ -766,7 +766,11 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
 __global__ void __launch_bounds__(128) mla_page_list_kernel(const PageListParams p) {
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  // launched as a programmatic dependent of the work before it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.sched && blockIdx.x == 0 && threadIdx.x == 0) *p.sched = 0u;
   if (t >= p.T) return;
+  const int c_first = lane < p.topk ? p.blocks[t * p.b_stride + lane] : -1;      // under way with the search below
   int64_t vis = 0;
   const int b = row_request(p.cu_q, p.seq_lens, p.B, t, &vis);
   if (b < 0) {
@@ -784,7 +788,7 @@ __global__ void __launch_bounds__(128) mla_page_list_kernel(const PageListParams
     return c < p.bt_cols ? p.block_table[b * p.bt_stride + c] : -1;
   };
   for (int c0 = 0; c0 < p.topk; c0 += 32) {
-    const int c = c0 + lane < p.topk ? src[c0 + lane] : -1;
+    const int c = c0 == 0 ? c_first : c0 + lane < p.topk ? src[c0 + lane] : -1;
     const bool is_part = part > 0 && c == full;
     const bool ok = c >= 0 && c < full;
     if (c >= 0 && !ok && !is_part) errbits |= 1u;
@@ -869,8 +873,7 @@ cudaError_t launch_index_select(const IndexSelectParams& p, int sms, cudaStream_
 }
 
 cudaError_t launch_page_list(const PageListParams& p, cudaStream_t stream) {
-  mla_page_list_kernel<<<(p.T + 3) / 4, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(mla_page_list_kernel, dim3((p.T + 3) / 4), dim3(128), 0, stream, p);
 }
 
 }  // namespace mla

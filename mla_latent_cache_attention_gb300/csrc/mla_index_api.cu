@@ -274,12 +274,18 @@ static size_t selected_list_bytes(int32_t T, int32_t topk) {
   return lens + table;
 }
 
-extern "C" size_t mla_selected_decode_workspace_size(int32_t T, int32_t topk, int32_t block_size, int32_t H,
-                                                     int32_t num_sms) {
+extern "C" size_t mla_selected_decode_workspace_size(mla_cache_format fmt, int32_t T, int32_t topk, int32_t block_size,
+                                                     int32_t H, int32_t num_sms) {
   if (T <= 0 || topk <= 0 || block_size <= 0 || H <= 0) return 0;
   const int64_t ctx = static_cast<int64_t>(topk) * block_size;
   if (ctx >= (1 << 30)) return 0;
-  return selected_list_bytes(T, topk) + mla_paged_decode_workspace_size(T, 1, H, static_cast<int32_t>(ctx), num_sms);
+  int sms = num_sms;
+  if (sms <= 0) {
+    DevInfo* d = nullptr;
+    if (dev_info(&d) != MLA_OK) return 0;
+    sms = d->sms;
+  }
+  return selected_list_bytes(T, topk) + workspace_bytes_for(T, H, plan_selected(fmt, T, H, ctx, sms));
 }
 
 extern "C" int mla_selected_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache,
@@ -297,10 +303,14 @@ extern "C" int mla_selected_decode(const void* q, int64_t q_s0, int64_t q_s1, co
   if (B == 0 || T == 0) return ok();
   if (!seq_lens || !blocks) return fail(MLA_ERR_INVALID, "a required pointer is NULL");
   if (b_stride < topk || !aligned(blocks, 4)) return fail(MLA_ERR_INVALID, "bad blocks rows");
+  if (H < 1 || H > 128) return fail(MLA_ERR_UNSUPPORTED, "H must be in [1, 128], got %d", H);
   if (int rc = check_table(block_table, bt_stride, bt_cols, B)) return rc;
   const size_t lists = selected_list_bytes(T, topk);
-  const size_t need = mla_selected_decode_workspace_size(T, topk, block_size, H, 0);
-  if (!workspace || workspace_bytes < need || workspace_bytes < lists)
+  DevInfo* d = nullptr;
+  if (int rc = dev_info(&d)) return rc;
+  const SplitPlan sp = plan_selected(fmt, T, H, static_cast<int64_t>(topk) * block_size, d->sms);
+  const size_t need = lists + workspace_bytes_for(T, H, sp);
+  if (!workspace || workspace_bytes < need)
     return fail(MLA_ERR_INVALID, "workspace too small: need %zu bytes, got %zu", need, workspace_bytes);
   if (!aligned(workspace, 256)) return fail(MLA_ERR_INVALID, "workspace must be 256-byte aligned");
   const int32_t ctx = topk * block_size;
@@ -309,8 +319,6 @@ extern "C" int mla_selected_decode(const void* q, int64_t q_s0, int64_t q_s1, co
   if (int rc = check_paged_decode(q, q_s0, q_s1, kv_cache, fmt, num_blocks, block_stride_bytes, entry_stride_bytes,
                                   block_size, block_table, topk, seq_lens, T, 1, H, ctx, out, o_s0, o_s1, lse))
     return rc;
-  DevInfo* d = nullptr;
-  if (int rc = dev_info(&d)) return rc;
   PageListParams p{};
   p.blocks = blocks;
   p.b_stride = b_stride;
@@ -325,10 +333,11 @@ extern "C" int mla_selected_decode(const void* q, int64_t q_s0, int64_t q_s1, co
   p.block_size = block_size;
   p.lens = static_cast<int32_t*>(workspace);
   p.table = p.lens + ((static_cast<size_t>(T) * 4 + 255) & ~size_t(255)) / 4;
+  p.sched = sched_word(rest, T, H, sp);
   p.err = d->err;
   if (launch_page_list(p, stream) != cudaSuccess)
     return fail(MLA_ERR_CUDA, "page list launch failed: %s", cudaGetErrorString(cudaGetLastError()));
-  return mla_paged_decode(q, q_s0, q_s1, kv_cache, fmt, num_blocks, block_stride_bytes, entry_stride_bytes, block_size,
+  return run_paged_decode(q, q_s0, q_s1, kv_cache, fmt, num_blocks, block_stride_bytes, entry_stride_bytes, block_size,
                           p.table, topk, p.lens, T, 1, H, ctx, softmax_scale, q_scale, k_scale, out, o_s0, o_s1, lse,
-                          rest, workspace_bytes - lists, stream);
+                          rest, workspace_bytes - lists, sp, true, stream);
 }
