@@ -9,6 +9,8 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include <cmath>
+
 #include "mla_index.h"
 #include "mla_internal.h"
 #include "mla_ptx.cuh"
@@ -249,13 +251,21 @@ __global__ void __launch_bounds__(128) mla_index_gather_kernel(const IndexGather
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelSample = 4096;
-constexpr int kSelChunk = 4096;                          // list entries beyond topk; scores of an ordered round
+constexpr int kSelChunk = 2048;                          // scores of an ordered round
 constexpr int kSelBins = 2048;
-constexpr int kSelAhead = 8192;                          // scores of a row that are asked for ahead of their use
 constexpr int kSelFixed = kSelBins * 4 + 512;
 
-// Shared memory of a row with topk: the list (topk + a chunk), a copy of topk entries for a cut.
-__host__ __device__ constexpr int64_t select_smem(int64_t topk) { return kSelFixed + (2 * topk + kSelChunk) * 8; }
+// Entries of the list: topk and room beyond it, for an ordered round or for what the bound lets in: the
+// score of rank rho = r + 6 sqrt(r) + 8 of a sample of 4096, r = topk 4096 / n, lets in n / 4096 times
+// rho +- sqrt(rho) of n; six of those are kept (with 3.5, one of 4096 rows overflowed, and its ordered
+// pass took 40 us longer than the others).  What shared memory leaves of an SM is L1, and loads in flight
+// take place there: with 25 KB a row more the same kernel took 352 us instead of 290 us for 4096 rows of 65536.
+inline int select_capacity(int64_t topk, int64_t width) {
+  const double per = static_cast<double>(width) / kSelSample, r = topk / per;
+  const double rho = r + 6.0 * sqrt(r) + 8.0, most = (200 * 1024 - kSelFixed) / 8.0 - topk;
+  const double want = per * (rho + 6.0 * sqrt(rho)) - topk, room = want < most ? want : most;
+  return static_cast<int>(topk + (room > kSelChunk ? room : kSelChunk));
+}
 
 __device__ __forceinline__ uint32_t score_key(float f) {        // f neither NaN nor -inf: at least 0x00800000
   const uint32_t u = __float_as_uint(f + 0.f);                  // -0 and +0 are equal
@@ -457,10 +467,78 @@ __device__ __forceinline__ int select_blocks_of(const IndexSelectParams& p, int6
   return static_cast<int>(min((vis + p.block_tokens - 1) / p.block_tokens, p.width));
 }
 
+// A lane's four scores at i .. i + 3 of x; NaN from `to` on.
+__device__ __forceinline__ void load_scores(const float* __restrict__ x, bool vec, int i, int to, float* v) {
+  if (vec && i + 3 < to) {
+    const float4 w = __ldg(reinterpret_cast<const float4*>(x + i));
+    v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = i + e < to ? __ldg(x + i + e) : CUDART_NAN_F;
+  }
+}
+
+// Bits of a warp's scores at i0 + 128 (j / 4) + 4 lane + j % 4 that are forced.
+__device__ __forceinline__ uint32_t forced_bits(int i0, int loads, int to, int f_lo, int f_hi) {
+  uint32_t f = 0;
+  for (int j = 0; j < 4 * loads; ++j) {
+    const int i = i0 + (j >> 2) * 128 + 4 * (threadIdx.x & 31) + (j & 3);
+    if (i < to && (i < f_lo || i >= f_hi)) f |= 1u << j;
+  }
+  return f;
+}
+
+// The list of a part in the ordered way: rounds in index order, the list cut to its kk largest whenever it
+// is full.  Returns its length.  Out of line, so that the usual way keeps its registers.
+__device__ __noinline__ int ordered_list(const float* __restrict__ x, bool vec, int from, int to, int f_lo, int f_hi, uint32_t kk,
+                                         uint32_t cap, SelShared& s, uint2* list) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int m = 0;
+  float bound = -CUDART_INF_F;
+  for (int c0 = from; c0 < to; c0 += kSelChunk) {
+    const int i0 = c0 + warp * 128;
+    float v[4];
+    load_scores(x, vec, i0 + 4 * lane, to, v);
+    for (;;) {
+      if (tid == 0) s.count = m;
+      __syncthreads();
+      uint32_t take = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) take |= (v[j] > bound ? 1u : 0u) << j;
+      if (i0 < f_lo || i0 + 128 > f_hi) take |= forced_bits(i0, 1, to, f_lo, f_hi);
+      append(list, cap, &s.count, take, x, i0, true, f_lo, f_hi);
+      __syncthreads();
+      const int now = static_cast<int>(s.count);
+      __syncthreads();
+      if (now <= static_cast<int>(cap)) {
+        m = now;
+        break;
+      }
+      // the list of the rounds before this one, cut; then the round again
+      const Cut c = find_cut(m, kk, 1, s, [&](int i) { return list[i].x == kForcedKey ? 0u : list[i].x; });
+      uint32_t first = 0;
+      if (c.ties) first = find_cut(m, c.ties, 1, s, [&](int i) { return list[i].x == c.thr ? ~list[i].y : 0u; }).thr;
+      if (tid == 0) s.count = 0;
+      __syncthreads();
+      for (int i1 = 0; i1 < m; i1 += kSelThreads) {      // to the front, which has been read
+        const uint2 e = i1 + tid < m ? list[i1 + tid] : make_uint2(0u, 0u);
+        __syncthreads();
+        if (i1 + tid < m && (e.x > c.thr || (c.ties && e.x == c.thr && ~e.y > first))) list[atomicAdd(&s.count, 1u)] = e;
+        __syncthreads();
+      }
+      m = static_cast<int>(s.count);
+      if (kk == 0)
+        bound = CUDART_INF_F;
+      else if (c.thr)
+        bound = key_score(c.thr);
+      __syncthreads();
+    }
+  }
+  return m;
+}
+
 __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, int rank, int ranks, int b, int64_t vis,
-                                           int resident, SelShared& s, uint2* list) {
-  const uint32_t cap = p.topk + kSelChunk;
-  uint2* copy = list + cap;
+                                           uint32_t cap, SelShared& s, uint2* list) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) s.count = 0;
   __syncthreads();
@@ -471,25 +549,6 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
   const int part = ((n + ranks - 1) / ranks + 3) & ~3;
   const int from = min(n, rank * part), to = min(n, from + part);
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
-  // a lane's four scores at i .. i + 3; NaN past the part
-  auto load4 = [&](int i, float* v) {
-    if (vec && i + 3 < to) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(x + i));
-      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = i + e < to ? __ldg(x + i + e) : CUDART_NAN_F;
-    }
-  };
-  auto forced_bits = [&](int i0, int loads) -> uint32_t {
-    uint32_t f = 0;
-    for (int j = 0; j < 4 * loads; ++j) {
-      const int i = i0 + (j >> 2) * 128 + 4 * lane + (j & 3);
-      if (i < to && (i < f_lo || i >= f_hi)) f |= 1u << j;
-    }
-    return f;
-  };
-
   // ---- the bound: the score of the sample's rank that leaves room for its error.  The sample is 1024
   // groups of four neighbours spread over the row (a whole sector each), the same in every CTA of
   // the cluster; its histogram divides the scores' range evenly.
@@ -558,10 +617,8 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
   // ---- stream: a warp takes 512 neighbouring scores at a time, 4 a lane and load
   for (int i0 = from + warp * 512; i0 < to; i0 += kSelWarps * 512) {
     float v[16];
-    const int ahead = i0 + kSelAhead + 32 * lane;      // later scores, a line a lane
-    if (lane < 16 && ahead < to) asm volatile("prefetch.global.L2 [%0];" ::"l"(x + ahead));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load4(i0 + 128 * j + 4 * lane, v + 4 * j);
+    for (int j = 0; j < 4; ++j) load_scores(x, vec, i0 + 128 * j + 4 * lane, to, v + 4 * j);
     uint32_t take = 0;
     if (strict) {
 #pragma unroll
@@ -570,13 +627,8 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
 #pragma unroll
       for (int j = 0; j < 16; ++j) take |= (v[j] >= bound ? 1u : 0u) << j;
     }
-    if (i0 < f_lo || i0 + 512 > f_hi) take |= forced_bits(i0, 4);
+    if (i0 < f_lo || i0 + 512 > f_hi) take |= forced_bits(i0, 4, to, f_lo, f_hi);
     append(list, cap, &s.count, take, x, i0, false, f_lo, f_hi);
-  }
-  // The row that will follow on this SM: its start comes into L2 while this one is cut.
-  if (resident > 0 && tid < 32 && t + resident < p.T) {
-    const float* next = p.scores + static_cast<int64_t>(t + resident) * p.s_stride;
-    for (int i = 32 * lane; i < min(n, kSelAhead); i += 1024) asm volatile("prefetch.global.L2 [%0];" ::"l"(next + i));
   }
   __syncthreads();
   uint32_t total = s.count;
@@ -616,50 +668,8 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
     }
     if (ranks > 1) cluster_sync();       // the lists have been read
   } else {
-    // ---- in order, cutting the list whenever it is full
     if (ranks > 1) cluster_sync(); else __syncthreads();       // the counts have been read
-    m = 0;
-    bound = -CUDART_INF_F;
-    for (int c0 = from; c0 < to; c0 += kSelChunk) {
-      const int i0 = c0 + warp * 256;
-      float v[8];
-      load4(i0 + 4 * lane, v);
-      load4(i0 + 128 + 4 * lane, v + 4);
-      for (;;) {
-        if (tid == 0) s.count = m;
-        __syncthreads();
-        uint32_t take = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) take |= (v[j] > bound ? 1u : 0u) << j;
-        if (i0 < f_lo || i0 + 256 > f_hi) take |= forced_bits(i0, 2);
-        append(list, cap, &s.count, take, x, i0, true, f_lo, f_hi);
-        __syncthreads();
-        const int now = static_cast<int>(s.count);
-        __syncthreads();
-        if (now <= static_cast<int>(cap)) {
-          m = now;
-          break;
-        }
-        // the list of the rounds before this one, cut to its topk; then the round again
-        const Cut c = find_cut(m, kk, 1, s, [&](int i) { return list[i].x == kForcedKey ? 0u : list[i].x; });
-        uint32_t first = 0;
-        if (c.ties) first = find_cut(m, c.ties, 1, s, [&](int i) { return list[i].x == c.thr ? ~list[i].y : 0u; }).thr;
-        if (tid == 0) s.count = 0;
-        __syncthreads();
-        for (int i = tid; i < m; i += kSelThreads) {
-          const uint2 e = list[i];
-          if (e.x > c.thr || (c.ties && e.x == c.thr && ~e.y > first)) copy[atomicAdd(&s.count, 1u)] = e;
-        }
-        __syncthreads();
-        m = static_cast<int>(s.count);
-        for (int i = tid; i < m; i += kSelThreads) list[i] = copy[i];
-        if (kk == 0)
-          bound = CUDART_INF_F;
-        else if (c.thr)
-          bound = key_score(c.thr);
-        __syncthreads();
-      }
-    }
+    m = ordered_list(x, vec, from, to, f_lo, f_hi, kk, cap, s, list);
   }
   __syncthreads();
 
@@ -742,7 +752,7 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
   }
 }
 
-__global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const IndexSelectParams p, int ranks, int resident) {
+__global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const IndexSelectParams p, int ranks, int cap) {
   extern __shared__ __align__(16) uint8_t sel_smem[];
   SelShared& s = *reinterpret_cast<SelShared*>(sel_smem);
   uint2* list = reinterpret_cast<uint2*>(sel_smem + kSelFixed);       // (score bits, then key; index)
@@ -756,7 +766,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
     }
   }
   __syncthreads();
-  if (s.row[0] >= 0) select_row(p, t, rank, ranks, static_cast<int>(s.row[0]), s.row[1], resident, s, list);
+  if (s.row[0] >= 0) select_row(p, t, rank, ranks, static_cast<int>(s.row[0]), s.row[1], cap, s, list);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -841,7 +851,7 @@ cudaError_t launch_index_gather(int bf16, const IndexGatherParams& p, cudaStream
   return p.num_tokens >= 16384 ? gather_launch<32>(bf16, p, stream) : gather_launch<2>(bf16, p, stream);
 }
 
-static_assert(select_smem(kSelectMaxTopk) <= 227 * 1024, "shared memory budget");
+static_assert(kSelFixed + (kSelectMaxTopk + kSelChunk) * 8 <= 200 * 1024, "shared memory budget");
 
 cudaError_t launch_index_select(const IndexSelectParams& p, int sms, cudaStream_t stream) {
   static bool configured[64] = {};
@@ -850,18 +860,18 @@ cudaError_t launch_index_select(const IndexSelectParams& p, int sms, cudaStream_
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    e = cudaFuncSetAttribute(mla_index_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    e = cudaFuncSetAttribute(mla_index_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  // CTAs that share a row: while the batch leaves SMs idle and a part keeps two chunks
+  // CTAs that share a row: while the batch leaves SMs idle and a part keeps 8192 scores
   int ranks = 1;
-  while (ranks < 8 && static_cast<int64_t>(p.T) * ranks * 2 <= sms && p.width / (ranks * 2) >= 2 * kSelChunk) ranks *= 2;
+  while (ranks < 8 && static_cast<int64_t>(p.T) * ranks * 2 <= sms && p.width / (ranks * 2) >= 8192) ranks *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.T) * ranks);
-  const int resident = ranks == 1 && p.T > 3 * sms ? 3 * sms : 0;
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(select_smem(p.topk));
+  const int cap = select_capacity(p.topk, p.width > 1 ? p.width : 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(kSelFixed) + static_cast<size_t>(cap) * 8;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -869,7 +879,7 @@ cudaError_t launch_index_select(const IndexSelectParams& p, int sms, cudaStream_
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_index_select_kernel, p, ranks, resident);
+  return cudaLaunchKernelEx(&cfg, mla_index_select_kernel, p, ranks, cap);
 }
 
 cudaError_t launch_page_list(const PageListParams& p, cudaStream_t stream) {
