@@ -527,14 +527,19 @@ def merge_attn_states(prefix_output, prefix_lse, suffix_output, suffix_lse, *, o
 _BF16, _F32, _I32, _I64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
 _INDEX_TYPES = {CACHE_BF16: _BF16, CACHE_FP8: _BYTE_TYPES}
 _KV_TYPES = _BYTE_TYPES + _BF16
+_current_device = torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _strides(t, name, dtypes, dev, ndim):
     """The strides of a tensor that passes _need's checks (unit innermost stride)."""
-    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == dev.index and t.dim() == ndim:
-        st = t.stride()
-        if st[-1] == 1:
-            return st
+    try:
+        if t.dtype in dtypes and t.get_device() == dev.index:
+            st = t.stride()
+            if len(st) == ndim and st[-1] == 1:
+                return st
+    except AttributeError:
+        pass                # not a tensor: _need says so
     _need(t, name, dtypes, dev, ndim=ndim)
     return t.stride()
 
@@ -542,20 +547,23 @@ def _strides(t, name, dtypes, dev, ndim):
 def _call(fn, dev, *args):
     """fn(*args, current stream of dev) with dev current."""
     index = dev.index
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if _current_device() == index:
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+            rc = fn(*args, _raw_stream(index))
     if rc:
         _check(rc)
 
 
+_INDEX_FORMATS = {"bf16": CACHE_BF16, "auto": CACHE_BF16, "fp8": CACHE_FP8, CACHE_BF16: CACHE_BF16, CACHE_FP8: CACHE_FP8}
+
+
 def _index_format(fmt) -> int:
-    fmt = _fmt(fmt)
-    if fmt not in _INDEX_TYPES:
+    found = _INDEX_FORMATS.get(fmt)
+    if found is None:
         raise ValueError("the index cache is bf16 or fp8")
-    return fmt
+    return found
 
 
 def _index_geometry(index_cache, index_scales, fmt, dev):
@@ -623,7 +631,8 @@ def index_q_cache_insert(q, k, weights, index_cache, index_scales, slot_mapping,
             raise ValueError(f"positions must have T = {T} entries")
         pos = positions.data_ptr()
     if cos_sin_cache is not None:
-        _need(cos_sin_cache, "cos_sin_cache", _F32, dev, ndim=2, contiguous=True)
+        if _strides(cos_sin_cache, "cos_sin_cache", _F32, dev, 2)[0] != 64:
+            _need(cos_sin_cache, "cos_sin_cache", _F32, dev, ndim=2, contiguous=True)
         max_pos, half = cos_sin_cache.shape
         if half != 64:
             raise ValueError("cos_sin_cache must be [max_position, 64]")
@@ -755,7 +764,9 @@ def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, 
     T, H, width = q.shape
     if width != 576:
         raise ValueError(f"q must be [T, H, 576], got {tuple(q.shape)}")
-    _need(kv_cache, "kv_cache", _KV_TYPES, dev)
+    if isinstance(kv_cache, torch.Tensor) and kv_cache.dim() == 4 and kv_cache.shape[1] == 1:      # a head axis of size 1
+        kv_cache = kv_cache.squeeze(1)
+    kvs = _strides(kv_cache, "kv_cache", _KV_TYPES, dev, 3)
     B, cu = _requests(seq_lens, cu_q_lens, T, dev)
     table, tstride, tcols = _table(block_table, B, dev)
     ls = _strides(blocks, "blocks", _I32, dev, 2)
@@ -773,10 +784,11 @@ def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, 
             raise ValueError(f"lse must be [T, H] = {(T, H)}")
     elif return_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    nb, bstride, estride, bs = _cache_geometry(kv_cache)
+    nb, bs, _ = kv_cache.shape
+    es = kv_cache.element_size()
     L = lib()
     if workspace is None:
-        if torch.cuda.current_device() == dev.index:
+        if _current_device() == dev.index:
             need = L.mla_selected_decode_workspace_size(fmt, T, topk, bs, H, 0)
         else:
             with torch.cuda.device(dev):
@@ -784,7 +796,7 @@ def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, 
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", _BYTE_TYPES, dev, contiguous=True)
-    _call(L.mla_selected_decode, dev, q.data_ptr(), qs[0], qs[1], kv_cache.data_ptr(), fmt, nb, bstride, estride, bs,
+    _call(L.mla_selected_decode, dev, q.data_ptr(), qs[0], qs[1], kv_cache.data_ptr(), fmt, nb, es * kvs[0], es * kvs[1], bs,
           table, tstride, tcols, seq_lens.data_ptr(), cu, blocks.data_ptr(), max(ls[0], topk), topk, B, T, H,
           float(softmax_scale), float(q_scale), float(k_scale), out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(),
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
