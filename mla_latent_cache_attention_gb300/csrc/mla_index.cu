@@ -67,6 +67,7 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
 // Bound by memory: one read of every query and one write.  A half-warp owns a vector (8 values a
 // lane: a 16-byte load, an 8- or 16-byte store), the four butterflies of the maximum stay inside
 // it, and it has kVec vectors' loads in flight.  The first CTA of a token also inserts its key.
+// Measured: 8191 tokens of 64 heads (211 MB) 44 us, 4.7 TB/s, issuing 71 % of the time.
 // The rotated half of a vector: lane l >= 8 holds pairs 4 (l - 8) .. 4 (l - 8) + 3.
 __device__ __forceinline__ void rotate_vector(float (&x)[8], const float4 c4, const float4 s4, bool on) {
   if (!on) return;
@@ -172,7 +173,8 @@ __global__ void __launch_bounds__(128) mla_index_insert_kernel(const IndexInsert
 // Gather: row r of request b (cu[b] <= r < cu[b+1]) is position starts[b] + r - cu[b], as
 // bf16(code * scale).  A warp takes kRows neighbouring rows: each lane finds one row's key (the search
 // over cu, the page, the scale: five dependent loads), then half-warps write the 256-byte rows, 8
-// values a lane, with those addresses.
+// values a lane, with those addresses.  Measured: 242000 keys of 13 requests (94 MB) 19 us, 5.0 TB/s; a row
+// by a half-warp that finds it itself 34 us.
 template <bool kBf16, int kRows>
 __global__ void __launch_bounds__(128) mla_index_gather_kernel(const IndexGatherParams p) {
   const int lane = threadIdx.x & 31, l = lane & 15, d0 = 8 * l;
@@ -246,8 +248,12 @@ __global__ void __launch_bounds__(128) mla_index_gather_kernel(const IndexGather
 // the row is streamed again in order, and whenever the list is full it is cut to its exact topk, which
 // raises the bound; a later equal score has the higher index, so "above the bound" is enough.
 //
-// Long rows in small batches are shared by a cluster: every CTA streams a part, the histograms of the
-// cut are summed over the cluster, and every CTA writes its part's share.
+// Long rows in small batches are shared by a cluster: every CTA streams a part, appends the others' lists
+// to its own, cuts the whole and writes its part's share.  (In order, the lists are topk each: they
+// stay apart, and the histograms of the last cut are summed over the cluster.)
+//
+// Measured (GB300): 4096 rows of up to 65536 scores, topk 2048: 290 us, 3.7 TB/s (1.07 GB read once);
+// 32 rows of up to 131072 with their slots: 20 us; 128 rows of up to 512 blocks, topk 32: 9 us.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelSample = 4096;
@@ -550,8 +556,9 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
   const int from = min(n, rank * part), to = min(n, from + part);
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
   // ---- the bound: the score of the sample's rank that leaves room for its error.  The sample is 1024
-  // groups of four neighbours spread over the row (a whole sector each), the same in every CTA of
-  // the cluster; its histogram divides the scores' range evenly.
+  // groups of four neighbours spread over the row (16 of a sector's 32 bytes each: single scores would touch
+  // half of a long row's sectors), the same in every CTA of the cluster; its histogram divides the
+  // scores' range evenly.
   float bound = -CUDART_INF_F;
   bool strict = true;
   if (n > static_cast<int>(cap)) {
@@ -843,12 +850,17 @@ cudaError_t gather_launch(int bf16, const IndexGatherParams& p, cudaStream_t str
 
 }  // namespace
 
+// Four vectors a half-warp for many, two for few (one wave of CTAs either way, the shorter ones end
+// sooner): 8191 tokens of 64 heads 41.7 against 48.3 us, 512 4.3 against 4.6, 256 3.6 against 3.2, 32 2.9 against
+// 2.4.  Eight held 80 registers a thread and took 49 us for 8191.
 cudaError_t launch_index_insert(int bf16, const IndexInsertParams& p, cudaStream_t stream) {
-  return p.T >= 1024 ? insert_launch<4>(bf16, p, stream) : insert_launch<2>(bf16, p, stream);
+  return static_cast<int64_t>(p.T) * p.Hi >= 32768 ? insert_launch<4>(bf16, p, stream) : insert_launch<2>(bf16, p, stream);
 }
 
+// Eight rows a warp for many, two for few: 100000 rows 7.6 against 11.8 us, 32000 4.1 against 5.2, 16000 3.8
+// against 3.6, 1021 3.3 against 2.5.  (32 rows a warp: 100000 8.4, 1021 6.5.)
 cudaError_t launch_index_gather(int bf16, const IndexGatherParams& p, cudaStream_t stream) {
-  return p.num_tokens >= 16384 ? gather_launch<32>(bf16, p, stream) : gather_launch<2>(bf16, p, stream);
+  return p.num_tokens >= 16384 ? gather_launch<8>(bf16, p, stream) : gather_launch<2>(bf16, p, stream);
 }
 
 static_assert(kSelFixed + (kSelectMaxTopk + kSelChunk) * 8 <= 200 * 1024, "shared memory budget");

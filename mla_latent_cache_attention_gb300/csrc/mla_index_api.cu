@@ -309,6 +309,8 @@ extern "C" int mla_selected_decode(const void* q, int64_t q_s0, int64_t q_s1, co
   DevInfo* d = nullptr;
   if (int rc = dev_info(&d)) return rc;
   const SplitPlan sp = plan_selected(fmt, T, H, static_cast<int64_t>(topk) * block_size, d->sms);
+  // (the work items of the decode: at most 8 column groups a row and split)
+  if (static_cast<int64_t>(T) * 8 * sp.n_splits >= (int64_t(1) << 31)) return fail(MLA_ERR_UNSUPPORTED, "too many rows");
   const size_t need = lists + workspace_bytes_for(T, H, sp);
   if (!workspace || workspace_bytes < need)
     return fail(MLA_ERR_INVALID, "workspace too small: need %zu bytes, got %zu", need, workspace_bytes);

@@ -108,7 +108,7 @@ __device__ __forceinline__ Request load_request(const IndexScoresParams& p, int 
     q.row0 = b;
     q.n = b < p.T ? 1 : 0;
   }
-  q.L = max(p.seq_lens[b], 0);
+  q.L = min(max(p.seq_lens[b], 0), 0x7FFFF000);      // positions of a tile's rows stay in 32 bits
   q.m = (q.n + QT - 1) / QT;
   const int d = q.L - q.n;
   q.a = d >= 0 ? (d + QT - 1) / QT : -((-d) / QT);
