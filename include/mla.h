@@ -525,7 +525,8 @@ MLA_API int mla_index_select(const float* scores, int64_t s_stride, int64_t widt
  *                tokens, is reported (MLA_DEVERR_INDEX).
  *   workspace    device scratch of >= mla_selected_decode_workspace_size(...) bytes, 256-byte
  *                aligned.  Contents need no initialising and are garbage afterwards.
- * A row without a selected token, or outside every request, gets out = 0 and lse = -inf.
+ * A row without a selected token, or outside every request, gets out = 0 and lse = -inf (B = 0: nothing
+ * is launched or written).
  */
 MLA_API size_t mla_selected_decode_workspace_size(mla_cache_format fmt, int32_t T, int32_t topk, int32_t block_size,
                                                   int32_t H, int32_t num_sms);

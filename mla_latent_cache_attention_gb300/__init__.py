@@ -699,8 +699,10 @@ def index_scores(q, weights, index_cache, index_scales, block_table, seq_lens, c
     B, cu = _requests(seq_lens, cu_q_lens, T, dev)
     table, tstride, tcols = _table(block_table, B, dev)
     nb, bstride, estride, sc, sstride, bs = _index_geometry(index_cache, index_scales, fmt, dev)
-    block_tokens = int(block_tokens)
-    cols = -(-int(max_context) // block_tokens)
+    block_tokens, max_context = int(block_tokens), int(max_context)
+    if not 1 <= block_tokens <= 0x7FFFFFFF or max_context < 0:      # (ctypes would wrap a larger one)
+        raise ValueError("block_tokens must be in [1, 2^31) and max_context >= 0")
+    cols = -(-max_context // block_tokens)
     if scores is None:
         scores = torch.empty((T, cols), dtype=torch.float32, device=dev)
     ss = _strides(scores, "scores", _F32, dev, 2)
@@ -723,9 +725,11 @@ def index_select(scores, seq_lens, topk, cu_q_lens=None, *, block_tokens=1, firs
     ss = _strides(scores, "scores", _F32, dev, 2)
     T, width = scores.shape
     B, cu = _requests(seq_lens, cu_q_lens, T, dev)
-    topk, block_tokens = int(topk), int(block_tokens)
+    topk, block_tokens, first, last, page_size, num_blocks = map(int, (topk, block_tokens, first, last, page_size, num_blocks))
     if topk < 1 or block_tokens < 1:
         raise ValueError("topk and block_tokens must be >= 1")
+    if max(topk, block_tokens, abs(first), abs(last), abs(page_size)) > 0x7FFFFFFF:      # ctypes would wrap them
+        raise ValueError("topk, block_tokens, first, last and page_size are 32-bit")
     if blocks is None:
         blocks = torch.empty((T, topk), dtype=torch.int32, device=dev)
     bs = _strides(blocks, "blocks", _I32, dev, 2)
@@ -744,8 +748,8 @@ def index_select(scores, seq_lens, topk, cu_q_lens=None, *, block_tokens=1, firs
     elif slots is not None:
         raise ValueError("slots need a block_table")
     _call(lib().mla_index_select, dev, scores.data_ptr(), max(ss[0], width), width, seq_lens.data_ptr(), cu, B, T,
-          block_tokens, topk, int(first), int(last), blocks.data_ptr(), max(bs[0], topk), sl, sl_stride, table, tstride,
-          tcols, int(page_size), int(num_blocks))
+          block_tokens, topk, first, last, blocks.data_ptr(), max(bs[0], topk), sl, sl_stride, table, tstride,
+          tcols, page_size, num_blocks)
     return blocks, slots
 
 
@@ -784,6 +788,11 @@ def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, 
             raise ValueError(f"lse must be [T, H] = {(T, H)}")
     elif return_lse:
         lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    if B == 0:              # every row is outside every request
+        out[..., :512].zero_()
+        if lse is not None:
+            lse.fill_(float("-inf"))
+        return out, lse
     nb, bs, _ = kv_cache.shape
     es = kv_cache.element_size()
     L = lib()

@@ -511,6 +511,35 @@ def test_selected_rows_of_no_request_are_zero(m):
     check_selected(m, "fp8", 16, [1, 2], [100, 200], 64, [[0, 1], [2], [0, 3]], seed=5, pad_rows=3)
 
 
+def test_selected_without_requests_is_zero(m):
+    """Three rows and no request at all (a padded batch): zeros and -inf, with buffers handed in too."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    q = torch.zeros((3, 16, 576), dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros((2, 64, 576), dtype=torch.bfloat16, device="cuda")
+    out = torch.full((3, 16, 520), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((3, 16), 7.0, device="cuda")
+    got, l = m.selected_decode(q, kv, torch.zeros((0, 2), **i32), torch.zeros(0, **i32), torch.zeros((3, 2), **i32),
+                               torch.zeros(1, **i32), fmt="bf16", softmax_scale=0.1, out=out, lse=lse)
+    assert got is out and l is lse
+    assert bool((out[..., :512] == 0).all()) and bool((out[..., 512:] == 7).all()) and bool((lse == -float("inf")).all())
+
+
+def test_sizes_past_32_bits_are_refused(m):
+    """Sizes that would wrap in the call's 32-bit arguments."""
+    x = torch.zeros((2, 8), device="cuda")
+    seq = torch.full((2,), 8, dtype=torch.int32, device="cuda")
+    for kw in (dict(block_tokens=2 ** 32 + 1), dict(first=2 ** 32), dict(last=2 ** 32), dict(page_size=2 ** 32 + 64)):
+        with pytest.raises(ValueError, match="32-bit"):
+            m.index_select(x, seq, 4, **kw)
+    with pytest.raises(ValueError, match="32-bit"):
+        m.index_select(x, seq, 2 ** 32 + 4)
+    q, w = torch.zeros((2, 8, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros((2, 8), device="cuda")
+    cache, table = torch.zeros((2, 64, 128), dtype=torch.bfloat16, device="cuda"), torch.zeros((2, 1), dtype=torch.int32, device="cuda")
+    for kw in (dict(block_tokens=0), dict(block_tokens=2 ** 32 + 16), dict(max_context=-1)):
+        with pytest.raises(ValueError, match="block_tokens"):
+            m.index_scores(q, w, cache, None, table, seq, **{"fmt": "bf16", "max_context": 8, **kw})
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_selected_split_over_a_long_list(m, fmt):
     check_selected(m, fmt, 16, [1], [64 * 90 + 5], 64, [list(range(0, 91, 2))], seed=6)
