@@ -238,28 +238,33 @@ __global__ void __launch_bounds__(128) mla_index_gather_kernel(const IndexGather
 // Selection.  A score becomes a 32-bit key whose unsigned order is the scores'.  A row is streamed
 // once: a bound, taken from 4096 scores spread over the row so that it almost surely lies a little
 // below the topk-th largest, lets some topk (1 + a few standard deviations of the sample's rank) of
-// them into a list in shared memory.  The exact cut is made in the list: the topk-th largest key
-// from histograms of 2048 bins that divide the keys' own range evenly (bins by leading bits would
-// put scores of similar size into a few of them), and among keys that equal it the lowest indices, by
-// the same search over the indices.  The taken indices then become bits of a map of the row, whose
-// prefix counts give their ascending positions.  No result depends on the order of atomics.
+// them into a list in shared memory.  The exact cut is made in the list.  Its scores are counted in bins
+// that divide the range above the bound evenly; the bin of the topk-th holds a few of them, which are
+// ranked directly, an equal score with a lower index before.  Where no bound was taken (a short row) or a
+// bin holds many (equal scores), the cut is the topk-th largest key, from histograms of 2048 bins that
+// divide the keys' own range evenly (bins by leading bits would put scores of similar size into a few of
+// them), and among keys that equal it the lowest indices, by the same search over the indices.  The
+// taken indices then become bits of a map of the row, whose prefix counts give their ascending
+// positions.  No result depends on the order of atomics.
 //
 // Where the bound lets in too few or too many (ties, or a row that repeats with the sample's stride)
 // the row is streamed again in order, and whenever the list is full it is cut to its exact topk, which
 // raises the bound; a later equal score has the higher index, so "above the bound" is enough.
 //
-// Long rows in small batches are shared by a cluster: every CTA streams a part, appends the others' lists
-// to its own, cuts the whole and writes its part's share.  (In order, the lists are topk each: they
-// stay apart, and the histograms of the last cut are summed over the cluster.)
+// Long rows in small batches are shared by a cluster: every CTA streams a part and keeps a list of its
+// own; the counts are summed over the cluster, and the few keys in the bin of the cut are read by all.
+// (Before, every CTA read the others' lists and cut the whole: 20.3 -> 17.0 us for the 32 rows below.)
 //
-// Measured (GB300): 4096 rows of up to 65536 scores, topk 2048: 290 us, 3.7 TB/s (1.07 GB read once);
-// 32 rows of up to 131072 with their slots: 20 us; 128 rows of up to 512 blocks, topk 32: 9 us.
+// Measured (GB300): 4096 rows of up to 65536 scores, topk 2048: 288 us, 3.7 TB/s (1.07 GB read once;
+// a row's sample waits for its 1024 sectors behind the other rows' streams, 7 of its 32 us);
+// 32 rows of up to 131072 with their slots: 17 us; 128 rows of up to 512 blocks, topk 32: 7.7 us.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelSample = 4096;
 constexpr int kSelChunk = 2048;                          // scores of an ordered round
 constexpr int kSelBins = 2048;
-constexpr int kSelFixed = kSelBins * 4 + 512;
+constexpr int kSelNear = 128;                            // keys of the cut's bin that are ranked directly
+constexpr int kSelFixed = kSelBins * 4 + kSelNear * 8 + 512;
 
 // Entries of the list: topk and room beyond it, for an ordered round or for what the bound lets in: the
 // score of rank rho = r + 6 sqrt(r) + 8 of a sample of 4096, r = topk 4096 / n, lets in n / 4096 times
@@ -288,8 +293,9 @@ struct SelShared {
   uint32_t stat[4];               // smallest key, largest key, their number, entries taken
   uint32_t found[4];              // bin, keys above it, keys in it
   uint32_t count;                 // entries of the list
-  uint32_t counts[9];             // of the cluster's lists: prefix sums in the order they are appended
+  uint32_t nears;                 // entries of near
   int64_t row[2];                 // request and visible keys
+  uint2 near[kSelNear];           // this CTA's (key, index) in the bin of the cut
 };
 static_assert(sizeof(SelShared) <= kSelFixed, "shared memory layout");
 
@@ -304,6 +310,12 @@ __device__ __forceinline__ uint2 ld_cluster_v2(uint32_t cluster_addr) {
   uint2 v;
   asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cluster_addr) : "memory");
   return v;
+}
+
+// Every CTA's value at p: lane r has that of CTA r of the cluster (0 from `ranks` on).
+__device__ __forceinline__ uint32_t ld_ranks(const uint32_t* p, int ranks) {
+  const int lane = threadIdx.x & 31;
+  return lane < ranks ? ld_cluster_u32(p, lane) : 0u;
 }
 
 // Exclusive prefix of `own` over the threads of the CTA (two barriers).
@@ -435,6 +447,15 @@ __device__ Cut find_cut(int m, uint32_t k, int ranks, SelShared& s, Val val) {
   }
 }
 
+// Bins of the scores that a bound lets in: evenly from the bound on, the last one for what lies past it.
+// Scores in order are in bins in order, whatever the roundings.
+struct Bins {
+  float from, scale;          // scale 0: not counted
+  __device__ __forceinline__ uint32_t of(float v) const {
+    return min(static_cast<uint32_t>(__float2int_rz((v - from) * scale)), static_cast<uint32_t>(kSelBins - 1));
+  }
+};
+
 // Adds the entries of a warp's `take` bits (bit j: index i0 + 128 (j / 4) + 4 lane + j % 4 of x)
 // to the list; those past its end are dropped, which the count shows.
 __device__ __forceinline__ void append(uint2* list, uint32_t cap, uint32_t* count, uint32_t take, const float* __restrict__ x,
@@ -543,6 +564,84 @@ __device__ __noinline__ int ordered_list(const float* __restrict__ x, bool vec, 
   return m;
 }
 
+// The cut of the kk largest (kk > 0) from the counts of `bins`: the bin that holds the kk-th, and among its
+// keys, where they are few, the one with kk - 1 before it in order (a lower index is before an equal key).
+// `at`: those taken before this CTA's part.  False if the bin holds too many.
+__device__ __forceinline__ bool cut_of_bins(int m, uint32_t kk, int ranks, SelShared& s, const uint2* list, const Bins bins,
+                                            Cut& cut, uint32_t& first, uint32_t& at_out) {
+  const int tid = threadIdx.x, lane = tid & 31, rank = ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  uint4 c = make_uint4(0, 0, 0, 0);      // thread q: bins 2047 - 4 q .. 2044 - 4 q
+  if (ranks == 1) {
+    c = reinterpret_cast<const uint4*>(s.hist)[kSelThreads - 1 - tid];
+  } else {
+    for (int r = 0; r < ranks; r += 2) {         // two loads under way
+      const uint4 v = ld_cluster_v4(mapa_shared(s.hist + 4 * (kSelThreads - 1 - tid), r));
+      const uint4 u = ld_cluster_v4(mapa_shared(s.hist + 4 * (kSelThreads - 1 - tid), r + 1));
+      c.x += v.x + u.x, c.y += v.y + u.y, c.z += v.z + u.z, c.w += v.w + u.w;
+    }
+  }
+  const uint32_t own = c.x + c.y + c.z + c.w;
+  if (tid == 0) s.nears = 0, s.stat[2] = 0, s.stat[3] = 0;
+  uint32_t before = block_prefix(own, s.wsum);
+  if (before < kk && kk <= before + own) {       // exactly one thread
+    uint32_t bin = kSelBins - 1 - 4 * tid, cnt = c.w;
+    if (kk > before + cnt) before += cnt, --bin, cnt = c.z;
+    if (kk > before + cnt) before += cnt, --bin, cnt = c.y;
+    if (kk > before + cnt) before += cnt, --bin, cnt = c.x;
+    s.found[0] = bin;
+    s.found[1] = before;
+    s.found[2] = cnt;
+  }
+  __syncthreads();
+  const uint32_t bin = s.found[0], left = kk - s.found[1], cnt = s.found[2];
+  if (cnt > kSelNear) return false;
+  uint32_t above = 0;                            // forced, or of a bin above
+  for (int i = tid; i < m; i += kSelThreads) {
+    const uint2 e = list[i];
+    const uint32_t b = e.x == kForcedKey ? static_cast<uint32_t>(kSelBins) : bins.of(key_score(e.x));
+    if (b == bin) s.near[atomicAdd(&s.nears, 1u)] = e;
+    above += b > bin ? 1u : 0u;
+  }
+  const uint2* all = s.near;
+  uint32_t r = 0;        // the CTA that has entry tid
+  if (ranks == 1) {
+    __syncthreads();
+  } else {
+    above = __reduce_add_sync(0xFFFFFFFFu, above);
+    if (lane == 0) atomicAdd(&s.stat[3], above);
+    cluster_sync();      // the others' keys are there, and they have read this CTA's counts
+    all = reinterpret_cast<const uint2*>(s.hist);
+    if (tid < kSelNear) {
+      const uint32_t n = ld_ranks(&s.nears, ranks);
+      uint32_t at = tid;
+      bool past = true;                  // entry tid is past the CTAs' so far
+      for (int i = 0; i < ranks; ++i) {
+        const uint32_t here = __shfl_sync(0xFFFFFFFFu, n, i);
+        if (past) r = i;
+        past = past && at >= here;
+        if (past) at -= here;
+      }
+      if (!past) reinterpret_cast<uint2*>(s.hist)[tid] = ld_cluster_v2(mapa_shared(s.near + at, r));
+    }
+    __syncthreads();
+  }
+  if (tid < static_cast<int>(cnt)) {
+    const uint2 e = all[tid];
+    uint32_t ahead = 0;
+    for (uint32_t i = 0; i < cnt; ++i) {
+      const uint2 o = all[i];
+      ahead += o.x > e.x || (o.x == e.x && o.y < e.y) ? 1u : 0u;
+    }
+    if (ahead + 1 == left) s.found[0] = e.x, s.found[1] = e.y;
+    if (ahead < left && r < static_cast<uint32_t>(rank)) atomicAdd(&s.stat[2], 1u);
+  }
+  __syncthreads();
+  if (ranks > 1) at_out = s.stat[2] + __reduce_add_sync(0xFFFFFFFFu, lane < rank ? ld_ranks(&s.stat[3], ranks) : 0u);
+  cut = Cut{s.found[0], 1u};
+  first = ~s.found[1] - 1u;         // indices up to the cut's own
+  return true;
+}
+
 __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, int rank, int ranks, int b, int64_t vis,
                                            uint32_t cap, SelShared& s, uint2* list) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -561,6 +660,7 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
   // scores' range evenly.
   float bound = -CUDART_INF_F;
   bool strict = true;
+  Bins bins{0.f, 0.f};
   if (n > static_cast<int>(cap)) {
     float f[8];
     float lo = CUDART_INF_F, hi = -CUDART_INF_F;
@@ -617,98 +717,105 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
       if (s.stat[2]) {
         bound = __uint_as_float(s.found[0]);
         strict = false;
+        // room above the sample's largest: the row's tail may be as long again
+        const float scale2 = (kSelBins / 2 - 1) / (hi - bound);
+        if (hi > bound && scale2 > 0.f && scale2 < CUDART_INF_F) bins = Bins{bound, scale2};
+        reinterpret_cast<uint4*>(s.hist)[tid] = make_uint4(0, 0, 0, 0);
       }
     }
     __syncthreads();
   }
-  // ---- stream: a warp takes 512 neighbouring scores at a time, 4 a lane and load
-  for (int i0 = from + warp * 512; i0 < to; i0 += kSelWarps * 512) {
+  // ---- stream: a warp takes 512 neighbouring scores at a time, 4 a lane and load; of a row that is let in
+  // whole 128, so that a short one is shared by the warps
+  if (strict) {
+    for (int i0 = from + warp * 128; i0 < to; i0 += kSelWarps * 128) {
+      const int i = i0 + 4 * lane;
+      float v[4];
+      load_scores(x, vec, i, to, v);
+      uint32_t take = forced_bits(i0, 1, to, f_lo, f_hi);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) take |= (v[j] > bound ? 1u : 0u) << j;
+      const uint32_t mine = __popc(take);
+      uint32_t inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t w = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += w;
+      }
+      uint32_t pos = 0;
+      if (lane == 31) pos = atomicAdd(&s.count, inc);
+      pos = __shfl_sync(0xFFFFFFFFu, pos, 31) + inc - mine;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (take >> j & 1u) {
+          if (pos < cap) list[pos] = make_uint2(__float_as_uint(v[j]), static_cast<uint32_t>(i + j));
+          ++pos;
+        }
+    }
+  }
+  for (int i0 = strict ? to : from + warp * 512; i0 < to; i0 += kSelWarps * 512) {
     float v[16];
 #pragma unroll
     for (int j = 0; j < 4; ++j) load_scores(x, vec, i0 + 128 * j + 4 * lane, to, v + 4 * j);
     uint32_t take = 0;
-    if (strict) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) take |= (v[j] > bound ? 1u : 0u) << j;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) take |= (v[j] >= bound ? 1u : 0u) << j;
-    }
+    for (int j = 0; j < 16; ++j) take |= (v[j] >= bound ? 1u : 0u) << j;
     if (i0 < f_lo || i0 + 512 > f_hi) take |= forced_bits(i0, 4, to, f_lo, f_hi);
     append(list, cap, &s.count, take, x, i0, false, f_lo, f_hi);
   }
   __syncthreads();
   uint32_t total = s.count;
   int m = static_cast<int>(min(total, cap));
+  bool fits = total <= cap;
+  // the scores become keys, and are counted
   for (int i = tid; i < m; i += kSelThreads) {
-    const int c = static_cast<int>(list[i].y);
-    list[i].x = c < f_lo || c >= f_hi ? kForcedKey : score_key(__uint_as_float(list[i].x));
+    const uint2 e = list[i];
+    const int at = static_cast<int>(e.y);
+    const bool forced = at < f_lo || at >= f_hi;
+    const float v = __uint_as_float(e.x);
+    list[i].x = forced ? kForcedKey : score_key(v);
+    if (bins.scale > 0.f && !forced) atomicAdd(&s.hist[bins.of(v)], 1u);
   }
-  if (ranks > 1) {
-    cluster_sync();
-    if (warp == 0) {      // counts of the other CTAs' lists, from the next one on
-      uint32_t c = lane < ranks ? ld_cluster_u32(&s.count, (rank + lane) % ranks) : 0u;
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, c, o);
-        if (lane >= o) c += v;
-      }
-      if (lane < 8) s.counts[lane + 1] = c;
-    }
+  if (ranks == 1) {
     __syncthreads();
-    total = s.counts[ranks];
-  }
-  // Too many for the list, or fewer than topk although the row was not let in whole (the bound was too
-  // high): not good.
-  const bool good = total <= cap && (strict || total >= static_cast<uint32_t>(p.topk));
-  int cut_ranks = ranks;          // CTAs whose lists the last cut is over
-  if (good) {
-    if (ranks > 1) {
-      // the cluster's lists together fit: every CTA appends the others' to its own and cuts the whole
-      for (int i = m + tid; i < static_cast<int>(total); i += kSelThreads) {
-        int r = 1;
-        while (static_cast<uint32_t>(i) >= s.counts[r + 1]) ++r;
-        list[i] = ld_cluster_v2(mapa_shared(list + (i - s.counts[r]), (rank + r) % ranks));
-      }
-      m = static_cast<int>(total);
-      cut_ranks = 1;
-    }
-    if (ranks > 1) cluster_sync();       // the lists have been read
   } else {
-    if (ranks > 1) cluster_sync(); else __syncthreads();       // the counts have been read
-    m = ordered_list(x, vec, from, to, f_lo, f_hi, kk, cap, s, list);
+    cluster_sync();
+    const uint32_t c = ld_ranks(&s.count, ranks);
+    total = __reduce_add_sync(0xFFFFFFFFu, c);
+    fits = __all_sync(0xFFFFFFFFu, c <= cap);
   }
-  __syncthreads();
+  // Too many for a list, or fewer than topk although the row was not let in whole (the bound was too
+  // high): not good.
+  const bool good = fits && (strict || total >= static_cast<uint32_t>(p.topk));
 
-  // ---- the last cut, over the row
-  const Cut c = find_cut(m, kk, cut_ranks, s, [&](int i) { return list[i].x == kForcedKey ? 0u : list[i].x; });
+  // ---- the cut, over the row
+  Cut c{0, 0};
   uint32_t first = 0;
-  if (c.ties) first = find_cut(m, c.ties, cut_ranks, s, [&](int i) { return list[i].x == c.thr ? ~list[i].y : 0u; }).thr;
+  uint32_t at = 0, all = p.topk;      // positions before this CTA's part, and of the row
+  const bool binned = good && kk > 0 && bins.scale > 0.f && cut_of_bins(m, kk, ranks, s, list, bins, c, first, at);
+  if (!binned) {
+    if (ranks > 1) cluster_sync(); else __syncthreads();           // the counts have been read
+    if (!good) {
+      m = ordered_list(x, vec, from, to, f_lo, f_hi, kk, cap, s, list);
+      __syncthreads();
+    }
+    c = find_cut(m, kk, ranks, s, [&](int i) { return list[i].x == kForcedKey ? 0u : list[i].x; });
+    if (c.ties) first = find_cut(m, c.ties, ranks, s, [&](int i) { return list[i].x == c.thr ? ~list[i].y : 0u; }).thr;
+  }
   auto taken = [&](uint2 e) { return e.x > c.thr || (c.ties && e.x == c.thr && ~e.y > first); };
   int32_t* out = p.blocks + t * p.b_stride;
   int32_t* out_slots = p.slots ? p.slots + t * p.sl_stride : nullptr;
-  uint32_t at = 0, all = 0;      // positions before this CTA's part, and of the row
-  if (ranks > 1) {
-    uint32_t mine = 0;           // taken entries (| those before the part << 16, where the list is the row's)
-    for (int i = tid; i < m; i += kSelThreads)
-      if (taken(list[i])) mine += cut_ranks == 1 && list[i].y < static_cast<uint32_t>(from) ? 0x10001u : 1u;
+  if (ranks > 1 && !binned) {
+    uint32_t mine = 0;
+    for (int i = tid; i < m; i += kSelThreads) mine += taken(list[i]) ? 1u : 0u;
     mine = __reduce_add_sync(0xFFFFFFFFu, mine);
     if (tid == 0) s.stat[3] = 0;
     __syncthreads();
     if (lane == 0) atomicAdd(&s.stat[3], mine);
-    __syncthreads();
-    if (cut_ranks == 1) {
-      at = s.stat[3] >> 16;
-      all = s.stat[3] & 0xFFFFu;
-    } else {
-      cluster_sync();
-      for (int r = 0; r < ranks; ++r) {
-        const uint32_t v = ld_cluster_u32(&s.stat[3], r);
-        if (r < rank) at += v;
-        all += v;
-      }
-      cluster_sync();       // no CTA leaves while another may read its count
-    }
+    cluster_sync();
+    const uint32_t v = ld_ranks(&s.stat[3], ranks);
+    at = __reduce_add_sync(0xFFFFFFFFu, lane < rank ? v : 0u);
+    all = __reduce_add_sync(0xFFFFFFFFu, v);
   }
   // ---- the map, 65536 indices at a time, and its bits in order
   for (int w0 = from; w0 < to; w0 += 32 * kSelBins) {
@@ -737,9 +844,10 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
   if (ranks == 1) all = at;
   // ---- -1 after the list
   for (int i = static_cast<int>(all) + rank * kSelThreads + tid; i < p.topk; i += ranks * kSelThreads) out[i] = -1;
+  // the list is written, and no CTA leaves while another may read its count
+  if (ranks > 1) cluster_sync(); else __syncthreads();
   if (!out_slots) return;
   // ---- token slots of the taken blocks through the block table
-  if (ranks > 1) cluster_sync(); else __syncthreads();      // the list is written
   const int64_t slots = static_cast<int64_t>(p.topk) * p.block_tokens;
   for (int64_t i = rank * kSelThreads + tid; i < slots; i += ranks * kSelThreads) {
     const int64_t j = i / p.block_tokens;

@@ -740,6 +740,32 @@ def test_select_rows_off_the_16_byte_grid(m, offset):
     assert np.array_equal(got.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("rows", [1, 160])      # rows shared by a cluster, and one CTA each
+@pytest.mark.parametrize("n,k", [(9000, 600), (70001, 513), (140000, 2048)])
+@pytest.mark.parametrize("kind", ["grid", "outlier", "infinite", "forced"])
+def test_select_crowded_cuts(m, rows, n, k, kind):
+    """Equal scores at the cut, a range that an outlier stretches, more infinities than places, forced blocks on
+    both sides of the cut."""
+    rng = np.random.default_rng(n + k)
+    x = rng.standard_normal((2, n)).astype(np.float32)
+    if kind == "grid":
+        x = (np.round(x * 256) / 256).astype(np.float32)
+    elif kind == "outlier":
+        x[0, n // 3] = 1e6
+        x[1, n // 2] = np.inf
+    elif kind == "infinite":
+        x[0, rng.permutation(n)[:k + 40]] = np.inf
+        x[1, rng.permutation(n)[:k // 2]] = np.inf
+    first, last = (5, 9) if kind == "forced" else (0, 0)
+    if rows == 1:
+        check_select(m, x[:1], [n], [1], 1, k, first, last, slots=True, ps=64, seed=n)
+        check_select(m, x[1:], [n - 7], [1], 1, k, first, last, slots=True, ps=64, seed=n)
+        return
+    got, _ = m.index_select(f32(x).repeat(rows // 2, 1), t_i32([n, n - 7] * (rows // 2)), k, first=first, last=last)
+    want, _, _ = ref.select(x, [n, n - 7], np.arange(3), 1, k, first, last)
+    assert np.array_equal(got.cpu().numpy(), np.tile(want, (rows // 2, 1)))
+
+
 def test_select_topk_limit(m):
     with pytest.raises(m.MLAError, match="topk must be"):
         m.index_select(torch.zeros((1, 10), device="cuda"), t_i32([10]), 8193)
