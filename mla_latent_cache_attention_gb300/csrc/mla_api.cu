@@ -776,13 +776,17 @@ extern "C" int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const
                           plan_splits(plan_units(B, q_len, H), max_context, d->sms), false, stream);
 }
 
-// Split plan of a decode over selected pages: `context` keys a row at most, all rows alike.  The split
-// count with the least estimated time: waves of work items (3.3 us a 128-key tile, 6 us an item's start and
-// end, as measured for the three formats), and the merge of the partials where there are several.
-// Against the long contexts' rule of at least four tiles a split: 16 pages of 64 (bf16, 32 rows, 16
-// heads) 35 -> 25 us with four splits instead of two; 32 pages (fp8_ds_mla, 128 rows, 96 heads) 412 -> 315 us
-// with one instead of four.
-SplitPlan mla::plan_selected(int fmt, int64_t T, int H, int64_t context, int sms) {
+// Plan of a decode over selected pages: `context` keys a row at most, all rows alike.  The split count with
+// the least estimated time: waves of work items (3.3 us a 128-key tile, 6 us an item's start and end, as
+// measured for the three formats), and the merge of the partials where there are several.  Against the
+// long contexts' rule of at least four tiles a split: 16 pages of 64 (bf16, 32 rows, 16 heads) 35 -> 25 us with
+// four splits instead of two; 32 pages (fp8_ds_mla, 128 rows, 96 heads) 412 -> 315 us with one instead of four.
+//
+// Where the last of several waves is nearly empty, its rows become a launch of their own, split over all
+// the SMs, if the estimate with 4 us for that launch is 3 % less: the fp8_ds_mla case above 314 -> 297 us (126 rows and
+// 2), 64 rows of 128 heads 215 -> 211; bf16, 160 rows of 64 heads, 32 pages, 276 -> 217, 200 of 16 heads, 16 pages, 101 -> 86;
+// fp8, 160 rows of 64 heads, 16 pages, 74 -> 62.
+mla::SelectedPlan mla::plan_selected(int fmt, int64_t T, int H, int64_t context, int sms) {
   const int64_t tiles = (context + kTile - 1) / kTile;
   int64_t groups = 1, slots = sms;
   ColPlan cp{};
@@ -795,17 +799,33 @@ SplitPlan mla::plan_selected(int fmt, int64_t T, int H, int64_t context, int sms
     groups = (H + kRows - 1) / kRows;
   }
   if (slots < 1) slots = 1;
-  int64_t best = 1;
-  double best_us = 0;
-  for (int64_t s = 1; s <= tiles && s <= 64; ++s) {
-    const int64_t per = (tiles + s - 1) / s;
-    if (s > 1 && (tiles + per - 1) / per != s) continue;       // the same parts as a smaller count
-    const int64_t waves = (T * groups * s + slots - 1) / slots;
-    double us = static_cast<double>(waves) * (3.3 * per + 6.0);
-    if (s > 1) us += 3.0 + 4096.0 * static_cast<double>(s * T * H) / 5e6;
-    if (s == 1 || us < best_us) best = s, best_us = us;
+  auto alike = [&](int64_t rows, double* us_out) -> SplitPlan {
+    int64_t best = 1;
+    double best_us = 0;
+    for (int64_t s = 1; s <= tiles && s <= 64; ++s) {
+      const int64_t per = (tiles + s - 1) / s;
+      if (s > 1 && (tiles + per - 1) / per != s) continue;       // the same parts as a smaller count
+      const int64_t waves = (rows * groups * s + slots - 1) / slots;
+      double us = static_cast<double>(waves) * (3.3 * per + 6.0);
+      if (s > 1) us += 3.0 + 4096.0 * static_cast<double>(s * rows * H) / 5e6;
+      if (s == 1 || us < best_us) best = s, best_us = us;
+    }
+    *us_out = best_us;
+    return SplitPlan{static_cast<int>(best), (tiles + best - 1) / best * kTile};
+  };
+  SelectedPlan plan{T, {}, {}};
+  double us = 0, tail_us = 0;
+  plan.main = alike(T, &us);
+  const int64_t waves = T * groups / slots, rows = waves * slots / groups;       // whole waves of unsplit items
+  if (rows > 0 && rows < T) {
+    const SplitPlan tail = alike(T - rows, &tail_us);
+    if (static_cast<double>(waves) * (3.3 * tiles + 6.0) + tail_us + 4.0 < 0.97 * us) {
+      plan.rows = rows;
+      plan.main = SplitPlan{1, tiles * kTile};
+      plan.tail = tail;
+    }
   }
-  return SplitPlan{static_cast<int>(best), (tiles + best - 1) / best * kTile};
+  return plan;
 }
 
 int mla::run_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache, int cache_fmt, int64_t num_blocks,

@@ -40,7 +40,12 @@ struct SplitPlan {
   int n_splits;
   int64_t chunk;
 };
-SplitPlan plan_selected(int fmt, int64_t T, int H, int64_t context, int sms);
+// Plan of a decode over selected pages: rows [0, rows) in one launch, the rest (if any) in another.
+struct SelectedPlan {
+  int64_t rows;
+  SplitPlan main, tail;
+};
+SelectedPlan plan_selected(int fmt, int64_t T, int H, int64_t context, int sms);
 // Workspace of a plan, and the address of its scheduler word there (null without splits).
 size_t workspace_bytes_for(int64_t n_rows, int H, const SplitPlan& sp);
 uint32_t* sched_word(void* workspace, int64_t n_rows, int H, const SplitPlan& sp);

@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(128) mla_page_list_kernel(const PageListParams
   const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   // launched as a programmatic dependent of the work before it
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (p.sched && blockIdx.x == 0 && threadIdx.x == 0) *p.sched = 0u;
+  if (blockIdx.x == 0 && threadIdx.x < 2 && p.sched[threadIdx.x]) *p.sched[threadIdx.x] = 0u;
   if (t >= p.T) return;
   const int c_first = lane < p.topk ? p.blocks[t * p.b_stride + lane] : -1;      // under way with the search below
   int64_t vis = 0;

@@ -102,7 +102,7 @@ struct PageListParams {
   int B, T, block_size;
   int32_t* table;          // [T, topk]
   int32_t* lens;           // [T]
-  uint32_t* sched;         // scheduler word of the decode, zeroed here, or null
+  uint32_t* sched[2];      // scheduler words of the decode's launches, zeroed here, or null
   uint32_t* err;
 };
 

@@ -285,7 +285,8 @@ extern "C" size_t mla_selected_decode_workspace_size(mla_cache_format fmt, int32
     if (dev_info(&d) != MLA_OK) return 0;
     sms = d->sms;
   }
-  return selected_list_bytes(T, topk) + workspace_bytes_for(T, H, plan_selected(fmt, T, H, ctx, sms));
+  const SelectedPlan sp = plan_selected(fmt, T, H, ctx, sms);
+  return selected_list_bytes(T, topk) + workspace_bytes_for(sp.rows, H, sp.main) + workspace_bytes_for(T - sp.rows, H, sp.tail);
 }
 
 extern "C" int mla_selected_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache,
@@ -308,10 +309,12 @@ extern "C" int mla_selected_decode(const void* q, int64_t q_s0, int64_t q_s1, co
   const size_t lists = selected_list_bytes(T, topk);
   DevInfo* d = nullptr;
   if (int rc = dev_info(&d)) return rc;
-  const SplitPlan sp = plan_selected(fmt, T, H, static_cast<int64_t>(topk) * block_size, d->sms);
+  const SelectedPlan sp = plan_selected(fmt, T, H, static_cast<int64_t>(topk) * block_size, d->sms);
   // (the work items of the decode: at most 8 column groups a row and split)
-  if (static_cast<int64_t>(T) * 8 * sp.n_splits >= (int64_t(1) << 31)) return fail(MLA_ERR_UNSUPPORTED, "too many rows");
-  const size_t need = lists + workspace_bytes_for(T, H, sp);
+  if (static_cast<int64_t>(T) * 8 * (sp.main.n_splits > sp.tail.n_splits ? sp.main.n_splits : sp.tail.n_splits) >= (int64_t(1) << 31))
+    return fail(MLA_ERR_UNSUPPORTED, "too many rows");
+  const int32_t rows = static_cast<int32_t>(sp.rows), more = T - rows;
+  const size_t part = workspace_bytes_for(rows, H, sp.main), need = lists + part + workspace_bytes_for(more, H, sp.tail);
   if (!workspace || workspace_bytes < need)
     return fail(MLA_ERR_INVALID, "workspace too small: need %zu bytes, got %zu", need, workspace_bytes);
   if (!aligned(workspace, 256)) return fail(MLA_ERR_INVALID, "workspace must be 256-byte aligned");
@@ -335,11 +338,21 @@ extern "C" int mla_selected_decode(const void* q, int64_t q_s0, int64_t q_s1, co
   p.block_size = block_size;
   p.lens = static_cast<int32_t*>(workspace);
   p.table = p.lens + ((static_cast<size_t>(T) * 4 + 255) & ~size_t(255)) / 4;
-  p.sched = sched_word(rest, T, H, sp);
+  p.sched[0] = sched_word(rest, rows, H, sp.main);
+  p.sched[1] = sched_word(rest + part, more, H, sp.tail);
   p.err = d->err;
   if (launch_page_list(p, stream) != cudaSuccess)
     return fail(MLA_ERR_CUDA, "page list launch failed: %s", cudaGetErrorString(cudaGetLastError()));
-  return run_paged_decode(q, q_s0, q_s1, kv_cache, fmt, num_blocks, block_stride_bytes, entry_stride_bytes, block_size,
-                          p.table, topk, p.lens, T, 1, H, ctx, softmax_scale, q_scale, k_scale, out, o_s0, o_s1, lse,
-                          rest, workspace_bytes - lists, sp, true, stream);
+  if (int rc = run_paged_decode(q, q_s0, q_s1, kv_cache, fmt, num_blocks, block_stride_bytes, entry_stride_bytes, block_size,
+                                p.table, topk, p.lens, rows, 1, H, ctx, softmax_scale, q_scale, k_scale, out, o_s0, o_s1, lse,
+                                rest, part, sp.main, true, stream))
+    return rc;
+  if (more == 0) return ok();
+  const int64_t qe = fmt == MLA_CACHE_FP8 ? 1 : 2;
+  return run_paged_decode(static_cast<const uint8_t*>(q) + rows * q_s0 * qe, q_s0, q_s1, kv_cache, fmt, num_blocks,
+                          block_stride_bytes, entry_stride_bytes, block_size, p.table + static_cast<int64_t>(rows) * topk, topk,
+                          p.lens + rows, more, 1, H, ctx, softmax_scale, q_scale, k_scale,
+                          static_cast<uint8_t*>(out) + rows * o_s0 * 2, o_s0, o_s1,
+                          lse ? lse + static_cast<int64_t>(rows) * H : nullptr, rest + part, need - lists - part, sp.tail, true,
+                          stream);
 }

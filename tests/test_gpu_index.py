@@ -540,6 +540,18 @@ def test_sizes_past_32_bits_are_refused(m):
             m.index_scores(q, w, cache, None, table, seq, **{"fmt": "bf16", "max_context": 8, **kw})
 
 
+@pytest.mark.parametrize("fmt,T,H", [("fp8_ds_mla", 26, 96), ("bf16", 40, 128), ("fp8", 78, 128), ("fp8", 156, 16)])
+def test_selected_rows_beyond_a_whole_wave(m, fmt, T, H):
+    """A batch whose last rows take a launch of their own; empty, short and unowned rows among them."""
+    rng = np.random.default_rng(T)
+    lens = rng.integers(900, 1100, T)
+    lens[-1] = 37
+    lists = [sorted(rng.permutation(-(-int(n) // 64))[:16].tolist()) for n in lens]
+    lists[0] = lists[T - 2] = []
+    check_selected(m, fmt, H, [1] * T, lens.astype(np.int32), 64, lists, seed=T)
+    check_selected(m, fmt, H, [1] * (T - 3), lens[:T - 3].astype(np.int32), 64, lists, seed=T, pad_rows=3)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_selected_split_over_a_long_list(m, fmt):
     check_selected(m, fmt, 16, [1], [64 * 90 + 5], 64, [list(range(0, 91, 2))], seed=6)

@@ -141,6 +141,13 @@ def test_selected_workspace_holds_the_lists_and_the_partials(L):
     n = lambda fmt, T, k, bs, H, sms=152: L.mla_selected_decode_workspace_size(fmt, T, k, bs, H, sms)
     assert n(0, 0, 4, 64, 16) == 0 and n(0, 4, 0, 64, 16) == 0
     assert n(0, 3, 2, 64, 16) == 256 + 256
-    # 128 rows of 96 heads keep one part; a single row of a long list is cut into many
-    assert n(2, 128, 32, 64, 96) == 512 + 128 * 32 * 4
+    # 126 rows of 96 heads are five waves of whole rows; of 128 the last two are cut, by themselves
+    assert n(2, 126, 32, 64, 96) == 512 + 126 * 32 * 4
+    assert 512 + 128 * 32 * 4 + 2 * 2 * 96 * 2048 <= n(2, 128, 32, 64, 96) < 512 + 128 * 32 * 4 + 2 * 17 * 96 * 2048
+    # the rows beyond a whole wave
+    lists = lambda T, k: -(-T * 4 // 256) * 256 + -(-T * k * 4 // 256) * 256
+    for fmt, T, H, rows in ((2, 26, 96, 25), (0, 40, 128, 38), (1, 78, 128, 76)):
+        assert n(fmt, rows, 16, 64, H) == lists(rows, 16)
+        assert n(fmt, T, 16, 64, H) >= lists(T, 16) + (T - rows) * 2 * H * 2048
+    # a single row of a long list is cut into many
     assert n(0, 1, 256, 64, 16) > 256 + 1024 + 16 * 512 * 4 * 8
