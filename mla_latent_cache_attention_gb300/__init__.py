@@ -37,6 +37,8 @@ read with the wrong layout.  Sparse indices may be int32 or int64.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -522,13 +524,33 @@ def merge_attn_states(prefix_output, prefix_lse, suffix_output, suffix_lse, *, o
     return output, lse
 
 
-# The selector's calls are short on the device, so their checks are: one look per tensor, in the order
-# that costs least, and _need only to word the refusal.
+# The selector's calls are short on the device.  The plain ones (tensors as documented, on the current
+# device) are marshalled in C (csrc/mla_marshal.cpp), which declines every other call with None: the Python
+# form below then serves it, or words the refusal.
 _BF16, _F32, _I32, _I64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
 _INDEX_TYPES = {CACHE_BF16: _BF16, CACHE_FP8: _BYTE_TYPES}
 _KV_TYPES = _BYTE_TYPES + _BF16
 _current_device = torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+_marshal = None
+
+
+def _plain():
+    """The C marshalling of the selector's calls (built with libmla.so; raises if it is missing)."""
+    global _marshal
+    if _marshal is None:
+        lib()
+        if not os.path.exists(_build.MARSHAL):
+            raise ImportError(f"mla_marshal.so not built ({_build.MARSHAL}); run mla_latent_cache_attention_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("mla_marshal", _build.MARSHAL)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("mla_marshal", loader))
+        loader.exec_module(mod)
+        mod.init(torch.Tensor, torch.empty, getattr(torch._C, "_cuda_getDevice", _current_device), _raw_stream, _check,
+                 torch.bfloat16, torch.uint8, torch.int8, torch.float32, torch.int32, torch.int64)
+        _marshal = mod
+    return _marshal
 
 
 def _strides(t, name, dtypes, dev, ndim):
@@ -613,6 +635,10 @@ def index_q_cache_insert(q, k, weights, index_cache, index_scales, slot_mapping,
     the index cache at slot_mapping.  Returns (q_out [T, Hi, 128]: bf16, or uint8 E4M3 codes;
     w_out fp32 [T, Hi]: weights * weight_scale, times the query's scale for fp8)."""
     fmt = _index_format(fmt)
+    done = (_marshal or _plain()).insert(q, k, weights, index_cache, index_scales, slot_mapping, fmt, weight_scale, positions,
+                                         cos_sin_cache, q_out, w_out)
+    if done is not None:
+        return done
     dev = _cuda_device(q)
     qs = _strides(q, "q", _BF16, dev, 3)
     T, Hi, width = q.shape
@@ -661,6 +687,9 @@ def index_gather(index_cache, index_scales, block_table, cu_seq_lens, seq_starts
     """Cached index keys as bf16 [num_tokens, 128]: rows cu_seq_lens[b] .. cu_seq_lens[b+1]-1 hold
     request b's positions seq_starts[b] + i."""
     fmt = _index_format(fmt)
+    done = (_marshal or _plain()).gather(index_cache, index_scales, block_table, cu_seq_lens, seq_starts, fmt, num_tokens, dst)
+    if done is not None:
+        return done
     dev = _cuda_device(index_cache)
     nb, bstride, estride, sc, sstride, bs = _index_geometry(index_cache, index_scales, fmt, dev)
     _strides(cu_seq_lens, "cu_seq_lens", _I32, dev, 1)
@@ -690,6 +719,10 @@ def index_scores(q, weights, index_cache, index_scales, block_table, seq_lens, c
     scales in the weights).  Returns scores fp32 [T, >= ceil(max_context / block_tokens)]; only the
     columns of visible blocks are written."""
     fmt = _index_format(fmt)
+    done = (_marshal or _plain()).scores(q, weights, index_cache, index_scales, block_table, seq_lens, cu_q_lens, fmt, block_tokens,
+                                         max_context, scores)
+    if done is not None:
+        return done
     dev = _cuda_device(q)
     qs = _strides(q, "q", _INDEX_TYPES[fmt], dev, 3)
     T, Hi, width = q.shape
@@ -721,6 +754,10 @@ def index_select(scores, seq_lens, topk, cu_q_lens=None, *, block_tokens=1, firs
     -inf and NaN are never taken, the first `first` and last `last` visible blocks always.  With a
     block_table (and page_size, num_blocks) also the cache slots of their visible tokens, for
     sparse_fwd.  Returns (blocks int32 [T, topk], slots int32 [T, topk * block_tokens] or None)."""
+    done = (_marshal or _plain()).select(scores, seq_lens, topk, cu_q_lens, block_tokens, first, last, block_table, page_size,
+                                         num_blocks, blocks, slots)
+    if done is not None:
+        return done
     dev = _cuda_device(scores)
     ss = _strides(scores, "scores", _F32, dev, 2)
     T, width = scores.shape
@@ -763,6 +800,10 @@ def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, 
     blocks[t] (int32 [T, topk], negative entries skipped) of its request.  Returns (out [T, H, 512]
     bf16, lse [T, H] or None), as paged_decode."""
     fmt = _fmt(fmt)
+    done = (_marshal or _plain()).selected(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens, fmt, softmax_scale, q_scale,
+                                           k_scale, out, return_lse, workspace, lse)
+    if done is not None:
+        return done
     dev = _cuda_device(q)
     qs = _strides(q, "q", _BYTE_TYPES if fmt == CACHE_FP8 else _BF16, dev, 3)
     T, H, width = q.shape

@@ -1,7 +1,8 @@
 """Build libmla.so (the CUDA library behind include/mla.h) for sm_103a with nvcc.
 
 Each translation unit compiles in its own nvcc process (in parallel); the objects link into
-``mla_latent_cache_attention_gb300/_build/libmla.so`` against the shared CUDA runtime.
+``mla_latent_cache_attention_gb300/_build/libmla.so`` against the shared CUDA runtime.  Beside it,
+``mla_marshal.so`` is the C marshalling of the selector's Python calls (linked to libmla.so).
 """
 from __future__ import annotations
 
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmla.so")
+MARSHAL = os.path.join(BUILD, "mla_marshal.so")
 
 SOURCES = ["mla_api.cu", "mla_small_kernels.cu", "mla_attn_bf16.cu", "mla_attn_fp8.cu", "mla_attn_ds.cu",
            "mla_noalloc.cu", "mla_paged_tma_bf16.cu", "mla_paged_tma_fp8.cu", "mla_ds.cu", "mla_head_bmm.cu",
@@ -39,9 +42,9 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -69,6 +72,13 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [nv, "-O2", "-std=c++17", "-Xcompiler", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, "-shared",
+           "-cudart", "shared", os.path.join(CSRC, "mla_marshal.cpp"), "-o", tmp, "-L", BUILD, "-lmla", "-Xlinker", "-rpath=$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building mla_marshal.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
     return LIB
 
 

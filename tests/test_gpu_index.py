@@ -616,6 +616,95 @@ class Chain:
             assert_lse_close(lse[b], l, f"request {b}")
 
 
+class Declined:
+    """A marshalling that serves nothing: every call takes its Python form."""
+    insert = gather = scores = select = selected = staticmethod(lambda *a: None)
+
+
+@pytest.mark.parametrize("topk,bt", [(64, 1), (4, 64)])
+@pytest.mark.parametrize("given", [False, True])
+def test_both_marshallings_give_the_same(m, monkeypatch, topk, bt, given):
+    """The C marshalling of plain calls and the Python form, with new outputs and with buffers handed in (rows
+    of wider tensors among them)."""
+    def run():
+        c = Chain(seed=11)
+        B, Hi, H = c.B, c.Hi, c.H
+        e = lambda *s, dtype=torch.int32: torch.zeros(s, dtype=dtype, device="cuda")
+        bf = torch.bfloat16
+        o = {}
+        if given:
+            o = dict(i=dict(q_out=e(B, Hi, 128, dtype=torch.int8), w_out=e(B, Hi, dtype=torch.float32)),
+                     s=dict(scores=e(B, 1100, dtype=torch.float32)[:, 3:1080]), k=dict(blocks=e(B, topk + 5)[:, :topk]),
+                     d=dict(out=e(B, H, 520, dtype=bf), lse=e(B, H, dtype=torch.float32), workspace=e(1 << 22, dtype=torch.uint8)),
+                     g=dict(dst=e(300, 136, dtype=bf)[:, :128]))
+            if bt == 1:
+                o["k"]["slots"] = e(B, topk + 3)[:, :topk]
+        qi, wi = m.index_q_cache_insert(c.q, c.k, c.w, c.cache, c.scales, c.slots, fmt="fp8", weight_scale=0.05, positions=c.pos,
+                                        cos_sin_cache=c.cs, **o.get("i", {}))
+        cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+        sc = m.index_scores(qi, wi, c.cache, c.scales, c.table, c.seq, cu, fmt="fp8", block_tokens=bt, max_context=1024, **o.get("s", {}))
+        table = dict(block_table=c.table, page_size=c.ps, num_blocks=c.nb) if bt == 1 else dict(first=1, last=1)
+        blocks, slots = m.index_select(sc, c.seq, topk, cu, block_tokens=bt, **table, **o.get("k", {}))
+        pages = blocks if bt > 1 else torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+        out, lse = m.selected_decode(c.mq, c.rec, c.table, c.seq, pages, cu, fmt="fp8_ds_mla", softmax_scale=0.07, return_lse=True,
+                                     **o.get("d", {}))
+        _, none = m.selected_decode(c.mq, c.rec, c.table, c.seq, pages, fmt="fp8_ds_mla", softmax_scale=0.07)
+        lens = torch.clamp(c.seq, max=60)
+        back = m.index_gather(c.cache, c.scales, c.table, torch.cat([cu[:1], torch.cumsum(lens, 0).int()]), cu[:-1] * 0, fmt="fp8",
+                              num_tokens=300, **o.get("g", {}))
+        assert none is None
+        visible = torch.arange(sc.shape[1], device="cuda") < ((c.seq + bt - 1) // bt)[:, None]
+        n = int(lens.sum())
+        return [qi.view(torch.uint8), wi, torch.where(visible, sc, 0), blocks, blocks if slots is None else slots, out[..., :512], lse, back[:n]]
+
+    m._plain()
+    served = []
+    real = m._marshal
+
+    class Counted:
+        def __getattr__(self, name):
+            def call(*a):
+                r = getattr(real, name)(*a)
+                served.append(r is not None)
+                return r
+            return call
+
+    monkeypatch.setattr(m, "_marshal", Counted())
+    a = run()
+    assert len(served) == 6 and all(served)
+    monkeypatch.setattr(m, "_marshal", Declined())
+    b = run()
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_marshalling_declines_what_is_not_plain(m):
+    """Calls that the C marshalling leaves to the Python form, which serves or refuses them."""
+    p = m._plain()
+    c = Chain(seed=3)
+    ins = [c.q, c.k, c.w, c.cache, c.scales, c.slots, 1, 1.0, c.pos, c.cs, None, None]
+    assert p.insert(*ins) is not None
+    for i, v in [(0, c.q.cpu()), (0, c.q.float()), (0, c.q[:, :, :64]), (0, c.q.transpose(1, 2)), (1, c.k[:, None]), (1, c.k[:-1]),
+                 (2, c.w.double()), (3, c.cache[..., :64]), (4, None), (4, c.scales[:, :-1]), (5, c.slots.int()), (6, 0), (7, 1),
+                 (8, c.pos[:-1]), (9, c.cs[:, :32]), (10, torch.empty_like(c.q)), (11, c.w.t().contiguous().t()), (0, None), (0, 3)]:
+        assert p.insert(*ins[:i], v, *ins[i + 1:]) is None, i
+    x = torch.zeros((c.B, 64), device="cuda")
+    sel = [x, c.seq, 4, None, 1, 0, 0, None, 0, 0, None, None]
+    assert p.select(*sel) is not None
+    for i, v in [(0, x.t()), (1, c.seq.long()), (1, c.seq[:-1]), (2, 0), (2, 2 ** 32 + 4), (2, 4.0), (4, 0), (5, 2 ** 31), (11, x.int())]:
+        assert p.select(*sel[:i], v, *sel[i + 1:]) is None, i
+    with pytest.raises(m.MLAError, match="first and last"):
+        p.select(*sel[:5], 3, 3, *sel[7:])
+    pages = torch.zeros((c.B, 2), dtype=torch.int32, device="cuda")
+    dec = [c.mq, c.rec, c.table, c.seq, pages, None, 2, 0.1, 1.0, 1.0, None, False, None, None]
+    assert p.selected(*dec) is not None
+    for i, v in [(0, c.mq[..., :512]), (1, c.rec[:, None]), (2, c.table[:-1]), (3, c.seq[:0]), (4, pages[:-1]), (7, 1), (11, 1),
+                 (10, torch.zeros((c.B, c.H, 256), dtype=torch.bfloat16, device="cuda")), (12, torch.zeros(8, device="cuda"))]:
+        assert p.selected(*dec[:i], v, *dec[i + 1:]) is None, i
+    with pytest.raises(m.MLAError, match="workspace too small"):
+        p.selected(*dec[:12], torch.empty(0, dtype=torch.uint8, device="cuda"), None)
+    assert p.insert() is None and p.gather(1) is None and p.scores() is None
+
+
 @pytest.mark.parametrize("topk,bt", [(64, 1), (4, 64)])
 def test_run_of_them_together(m, topk, bt):
     c = Chain(seed=topk)
