@@ -67,7 +67,8 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
 // Bound by memory: one read of every query and one write.  A half-warp owns a vector (8 values a
 // lane: a 16-byte load, an 8- or 16-byte store), the four butterflies of the maximum stay inside
 // it, and it has kVec vectors' loads in flight.  The first CTA of a token also inserts its key.
-// Measured: 8191 tokens of 64 heads (211 MB) 44 us, 4.7 TB/s, issuing 71 % of the time.
+// Measured: 8191 tokens of 64 heads (211 MB) 41.6 us, 5.1 TB/s, issuing 71 % of the time; the stores are marked
+// as streaming (42.9 us without).
 // The rotated half of a vector: lane l >= 8 holds pairs 4 (l - 8) .. 4 (l - 8) + 3.
 __device__ __forceinline__ void rotate_vector(float (&x)[8], const float4 c4, const float4 s4, bool on) {
   if (!on) return;
@@ -142,11 +143,11 @@ __global__ void __launch_bounds__(128) mla_index_insert_kernel(const IndexInsert
     rotate_vector(x, c, s, cs && l >= 8);
     const int64_t o = (t * p.Hi + v) * kIndexDim + d0;
     if (kBf16) {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.q_out) + o) = pack_bf16x8(x);
+      __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.q_out) + o), pack_bf16x8(x));
       if (l == 0) p.w_out[t * p.Hi + v] = w[u] * p.weight_scale;
     } else {
       float sc;
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q_out) + o) = quantise_vector(x, half, sc);
+      __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q_out) + o), quantise_vector(x, half, sc));
       if (l == 0) p.w_out[t * p.Hi + v] = w[u] * p.weight_scale * sc;
     }
   }
@@ -171,27 +172,30 @@ __global__ void __launch_bounds__(128) mla_index_insert_kernel(const IndexInsert
 
 // ------------------------------------------------------------------------------------------
 // Gather: row r of request b (cu[b] <= r < cu[b+1]) is position starts[b] + r - cu[b], as
-// bf16(code * scale).  A warp takes kRows neighbouring rows: each lane finds one row's key (the search
-// over cu, the page, the scale: five dependent loads), then half-warps write the 256-byte rows, 8
-// values a lane, with those addresses.  Measured: 242000 keys of 13 requests (94 MB) 19 us, 5.0 TB/s; a row
-// by a half-warp that finds it itself 34 us.
+// bf16(code * scale).  A warp takes kRows neighbouring rows at a time: each lane finds one row's key (the
+// search over cu, the page, the scale: five dependent loads), then half-warps write the 256-byte rows, 8
+// values a lane, with those addresses.  The next rows' keys are found while this step's values are on
+// their way (without that 512000 rows took 42 us instead of 35).  Stores are marked as streaming: 242000 rows 21.3
+// -> 18.1 us.  Measured past L2: 256000 keys of 8 requests (100 MB) 16.5 us, 6.0 TB/s, where a row by a half-warp
+// that finds it itself took 34 us.
 template <bool kBf16, int kRows>
 __global__ void __launch_bounds__(128) mla_index_gather_kernel(const IndexGatherParams p) {
-  const int lane = threadIdx.x & 31, l = lane & 15, d0 = 8 * l;
-  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5)) * kRows;
-  const int64_t end = min(p.num_tokens, static_cast<int64_t>(p.cu[p.batch]));
-  if (r0 >= end) return;
-  const uint8_t* ent = nullptr;      // null: zeros
-  float scale = 0.f;
-  const int64_t r = r0 + lane, first = p.cu[0];
-  if (lane < kRows && r < end && r >= first) {
+  const int lane = threadIdx.x & 31, d0 = 8 * (lane & 15);
+  const int64_t end = min(p.num_tokens, static_cast<int64_t>(p.cu[p.batch])), first = p.cu[0];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 4 * kRows;
+  // lane u < kRows: the key and scale of row r0 + u (no key: zeros)
+  auto lookup = [&](int64_t r0, const uint8_t*& ent, float& scale) {
+    ent = nullptr;
+    scale = 0.f;
+    const int64_t r = r0 + lane;
+    if (lane >= kRows || r >= end || r < first) return;
     int lo = 0, hi = p.batch - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (p.cu[mid] <= r) lo = mid; else hi = mid - 1;
     }
     const int64_t pos = static_cast<int64_t>(p.starts ? p.starts[lo] : 0) + (r - p.cu[lo]);
-    const int64_t col = pos >= 0 ? pos / p.block_size : -1;
+    const int64_t col = pos >= 0 ? static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.block_size) : -1;      // below 2^32
     const int64_t blk = col >= 0 && col < p.bt_cols ? p.block_table[lo * p.bt_stride + col] : -1;
     if (blk < 0 || blk >= p.num_blocks) {
       set_device_error(p.err, 2u);
@@ -200,36 +204,53 @@ __global__ void __launch_bounds__(128) mla_index_gather_kernel(const IndexGather
       ent = p.cache + blk * p.block_stride + off * p.entry_stride;
       if (!kBf16) scale = __ldg(p.scales + blk * p.sc_stride + off);
     }
-  }
-#pragma unroll 8
-  for (int i = 0; i < kRows / 2; ++i) {
-    const int src = 2 * i + (lane >> 4);
-    const uint8_t* e = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(ent), src));
-    const float s = __shfl_sync(0xFFFFFFFFu, scale, src);
-    if (r0 + src >= end || r0 + src < first) continue;
-    uint4 y = make_uint4(0, 0, 0, 0);
-    if (kBf16) {
-      if (e) y = __ldg(reinterpret_cast<const uint4*>(e + 2 * d0));
-    } else if (e) {
-      const uint2 c = __ldg(reinterpret_cast<const uint2*>(e + d0));
-      const uint32_t w[2] = {c.x, c.y};
-      float x[8];
+  };
+  int64_t r0 = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5)) * kRows;
+  const uint8_t* ent;
+  float scale;
+  lookup(r0, ent, scale);
+  for (; r0 < end; r0 += step) {
+    uint4 raw[kRows / 2];
+    float s[kRows / 2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));      // exact
-        x[2 * j] = f.x * s;
-        x[2 * j + 1] = f.y * s;
+    for (int i = 0; i < kRows / 2; ++i) {
+      const int src = 2 * i + (lane >> 4);
+      const uint8_t* e = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(ent), src));
+      s[i] = __shfl_sync(0xFFFFFFFFu, scale, src);
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (kBf16) {
+        if (e) raw[i] = __ldg(reinterpret_cast<const uint4*>(e + 2 * d0));
+      } else if (e) {
+        const uint2 c = __ldg(reinterpret_cast<const uint2*>(e + d0));
+        raw[i].x = c.x, raw[i].y = c.y;
       }
-      y = pack_bf16x8(x);
     }
-    uint16_t* dst = p.dst + (r0 + src) * p.dst_row + d0;
-    if (p.vec) {
-      *reinterpret_cast<uint4*>(dst) = y;
-    } else {
-      const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+    if (r0 + step < end) lookup(r0 + step, ent, scale);       // while the keys are on their way
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dst[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+    for (int i = 0; i < kRows / 2; ++i) {
+      const int64_t r = r0 + 2 * i + (lane >> 4);
+      if (r >= end || r < first) continue;
+      uint4 y = raw[i];
+      if (!kBf16) {
+        const uint32_t w[2] = {y.x, y.y};
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));      // exact
+          x[2 * j] = f.x * s[i];
+          x[2 * j + 1] = f.y * s[i];
+        }
+        y = pack_bf16x8(x);
+      }
+      uint16_t* dst = p.dst + r * p.dst_row + d0;
+      if (p.vec) {
+        __stcs(reinterpret_cast<uint4*>(dst), y);
+      } else {
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dst[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+      }
     }
   }
 }
@@ -946,9 +967,11 @@ cudaError_t insert_launch(int bf16, const IndexInsertParams& p, cudaStream_t str
   return cudaGetLastError();
 }
 
+// (32 warps an SM, each with several steps; 24 and 40 within 3 %)
 template <int kRows>
-cudaError_t gather_launch(int bf16, const IndexGatherParams& p, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>((p.num_tokens + 4 * kRows - 1) / (4 * kRows));
+cudaError_t gather_launch(int bf16, const IndexGatherParams& p, int sms, cudaStream_t stream) {
+  const int64_t all = (p.num_tokens + 4 * kRows - 1) / (4 * kRows), once = static_cast<int64_t>(sms) * 8;
+  const unsigned grid = static_cast<unsigned>(all < once ? all : once);
   if (bf16)
     mla_index_gather_kernel<true, kRows><<<grid, 128, 0, stream>>>(p);
   else
@@ -965,10 +988,10 @@ cudaError_t launch_index_insert(int bf16, const IndexInsertParams& p, cudaStream
   return static_cast<int64_t>(p.T) * p.Hi >= 32768 ? insert_launch<4>(bf16, p, stream) : insert_launch<2>(bf16, p, stream);
 }
 
-// Eight rows a warp for many, two for few: 100000 rows 7.6 against 11.8 us, 32000 4.1 against 5.2, 16000 3.8
-// against 3.6, 1021 3.3 against 2.5.  (32 rows a warp: 100000 8.4, 1021 6.5.)
-cudaError_t launch_index_gather(int bf16, const IndexGatherParams& p, cudaStream_t stream) {
-  return p.num_tokens >= 16384 ? gather_launch<8>(bf16, p, stream) : gather_launch<2>(bf16, p, stream);
+// 16 rows a warp for many, two for few: 512000 rows 35 against 78 us, 64000 5.4 against 10.4, 12000 3.5 against 3.6,
+// 8192 3.1 against 3.0, 1021 3.0 against 2.4.  (8 rows: 512000 37 us, 32 rows 42.)
+cudaError_t launch_index_gather(int bf16, const IndexGatherParams& p, int sms, cudaStream_t stream) {
+  return p.num_tokens >= 10240 ? gather_launch<16>(bf16, p, sms, stream) : gather_launch<2>(bf16, p, sms, stream);
 }
 
 static_assert(kSelFixed + (kSelectMaxTopk + kSelChunk) * 8 <= 200 * 1024, "shared memory budget");

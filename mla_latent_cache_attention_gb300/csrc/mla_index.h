@@ -107,7 +107,7 @@ struct PageListParams {
 };
 
 cudaError_t launch_index_insert(int bf16, const IndexInsertParams& p, cudaStream_t stream);
-cudaError_t launch_index_gather(int bf16, const IndexGatherParams& p, cudaStream_t stream);
+cudaError_t launch_index_gather(int bf16, const IndexGatherParams& p, int sms, cudaStream_t stream);
 // hp: heads padded to 8, 16, 32 or 64; tk / tq point to CUtensorMaps of the cache and the queries
 cudaError_t launch_index_scores(int bf16, int hp, const IndexScoresParams& p, const void* tk, const void* tq, int grid,
                                 cudaStream_t stream);

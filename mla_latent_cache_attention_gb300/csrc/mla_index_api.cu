@@ -140,7 +140,7 @@ extern "C" int mla_index_gather(const void* index_cache, mla_cache_format fmt, i
   p.dst_row = dst_row_stride;
   p.vec = aligned(dst, 16) && dst_row_stride % 8 == 0;
   p.err = d->err;
-  if (launch_index_gather(fmt == MLA_CACHE_BF16, p, stream) != cudaSuccess)
+  if (launch_index_gather(fmt == MLA_CACHE_BF16, p, d->sms, stream) != cudaSuccess)
     return fail(MLA_ERR_CUDA, "index gather launch failed: %s", cudaGetErrorString(cudaGetLastError()));
   return ok();
 }
