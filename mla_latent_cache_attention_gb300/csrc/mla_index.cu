@@ -276,8 +276,8 @@ __global__ void __launch_bounds__(128) mla_index_gather_kernel(const IndexGather
 // own; the counts are summed over the cluster, and the few keys in the bin of the cut are read by all.
 // (Before, every CTA read the others' lists and cut the whole: 20.3 -> 17.0 us for the 32 rows below.)
 //
-// Measured (GB300): 4096 rows of up to 65536 scores, topk 2048: 288 us, 3.7 TB/s (1.07 GB read once;
-// a row's sample waits for its 1024 sectors behind the other rows' streams, 7 of its 32 us);
+// Measured (GB300): 4096 rows of up to 65536 scores, topk 2048: 267 us, 4.0 TB/s (1.07 GB read once;
+// a row's sample waits for its 512 sectors behind the other rows' streams);
 // 32 rows of up to 131072 with their slots: 17 us; 128 rows of up to 512 blocks, topk 32: 7.7 us.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
@@ -508,8 +508,8 @@ __device__ __forceinline__ void append(uint2* list, uint32_t cap, uint32_t* coun
   }
 }
 
-// Group g of the sample: four neighbours of the n scores.
-__device__ __forceinline__ int sample_at(int g, int n) { return static_cast<int>((static_cast<int64_t>(g) * n) >> 10) & ~3; }
+// Four of the sample's scores: half g % 2 of one of 512 groups of eight neighbours (a sector) spread over the n.
+__device__ __forceinline__ int sample_at(int g, int n) { return (static_cast<int>((static_cast<int64_t>(g >> 1) * n) >> 9) & ~7) + 4 * (g & 1); }
 
 __device__ __forceinline__ int select_blocks_of(const IndexSelectParams& p, int64_t vis) {
   return static_cast<int>(min((vis + p.block_tokens - 1) / p.block_tokens, p.width));
@@ -675,10 +675,10 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
   const int part = ((n + ranks - 1) / ranks + 3) & ~3;
   const int from = min(n, rank * part), to = min(n, from + part);
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
-  // ---- the bound: the score of the sample's rank that leaves room for its error.  The sample is 1024
-  // groups of four neighbours spread over the row (16 of a sector's 32 bytes each: single scores would touch
-  // half of a long row's sectors), the same in every CTA of the cluster; its histogram divides the
-  // scores' range evenly.
+  // ---- the bound: the score of the sample's rank that leaves room for its error.  The sample is 512
+  // groups of eight neighbours spread over the row (whole sectors: 1024 groups of four waited for twice as many
+  // requests, 4096 rows of 65536 took 288 us instead of 267), the same in every CTA of the cluster; its
+  // histogram divides the scores' range evenly.
   float bound = -CUDART_INF_F;
   bool strict = true;
   Bins bins{0.f, 0.f};
@@ -776,8 +776,17 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
   }
   for (int i0 = strict ? to : from + warp * 512; i0 < to; i0 += kSelWarps * 512) {
     float v[16];
+    if (vec && i0 + 512 <= to) {
+      const float4* x4 = reinterpret_cast<const float4*>(x + i0) + lane;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load_scores(x, vec, i0 + 128 * j + 4 * lane, to, v + 4 * j);
+      for (int j = 0; j < 4; ++j) {
+        const float4 w = __ldg(x4 + 32 * j);
+        v[4 * j] = w.x, v[4 * j + 1] = w.y, v[4 * j + 2] = w.z, v[4 * j + 3] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load_scores(x, vec, i0 + 128 * j + 4 * lane, to, v + 4 * j);
+    }
     uint32_t take = 0;
 #pragma unroll
     for (int j = 0; j < 16; ++j) take |= (v[j] >= bound ? 1u : 0u) << j;
