@@ -268,15 +268,19 @@ __global__ void __launch_bounds__(128) mla_index_gather_kernel(const IndexGather
 // taken indices then become bits of a map of the row, whose prefix counts give their ascending
 // positions.  No result depends on the order of atomics.
 //
-// Where the bound lets in too few or too many (ties, or a row that repeats with the sample's stride)
-// the row is streamed again in order, and whenever the list is full it is cut to its exact topk, which
-// raises the bound; a later equal score has the higher index, so "above the bound" is enough.
+// Where the bound lets in too few or too many, the row is streamed once more with the sample's rank that the
+// count now gives for the middle of the list's room: a row whose neighbours resemble one another misses its
+// place more often than its sample's size says (1024 rows of 65536 scores, without this: a moving mean of 32
+// 149 instead of 97 us, blocks of 16 equal ones and a little noise 162 instead of 105).  Where that does not
+// help (equal scores, a row that repeats with the sample's stride) it is streamed in order, and whenever the
+// list is full it is cut to its exact topk, which raises the bound; a later equal score has the higher index,
+// so "above the bound" is enough.
 //
 // Long rows in small batches are shared by a cluster: every CTA streams a part and keeps a list of its
 // own; the counts are summed over the cluster, and the few keys in the bin of the cut are read by all.
 // (Before, every CTA read the others' lists and cut the whole: 20.3 -> 17.0 us for the 32 rows below.)
 //
-// Measured (GB300): 4096 rows of up to 65536 scores, topk 2048: 267 us, 4.0 TB/s (1.07 GB read once;
+// Measured (GB300): 4096 rows of up to 65536 scores, topk 2048: 271 us, 4.0 TB/s (1.07 GB read once;
 // a row's sample waits for its 512 sectors behind the other rows' streams);
 // 32 rows of up to 131072 with their slots: 17 us; 128 rows of up to 512 blocks, topk 32: 7.7 us.
 constexpr int kSelThreads = 512;
@@ -314,6 +318,7 @@ struct SelShared {
   uint32_t stat[4];               // smallest key, largest key, their number, entries taken
   uint32_t found[4];              // bin, keys above it, keys in it
   uint32_t count;                 // entries of the list
+  float again, tried;             // factor of the sample's rank (1 at first), the bound before
   uint32_t nears;                 // entries of near
   int64_t row[2];                 // request and visible keys
   uint2 near[kSelNear];           // this CTA's (key, index) in the bin of the cut
@@ -663,91 +668,79 @@ __device__ __forceinline__ bool cut_of_bins(int m, uint32_t kk, int ranks, SelSh
   return true;
 }
 
-__device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, int rank, int ranks, int b, int64_t vis,
-                                           uint32_t cap, SelShared& s, uint2* list) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) s.count = 0;
-  __syncthreads();
-  const float* __restrict__ x = p.scores + t * p.s_stride;
-  const int n = select_blocks_of(p, vis);
-  const int f_lo = min(p.first, n), f_hi = max(f_lo, n - p.last);      // forced: below f_lo, from f_hi on
-  const uint32_t kk = p.topk - (f_lo + n - f_hi);                // places of the others
-  const int part = ((n + ranks - 1) / ranks + 3) & ~3;
-  const int from = min(n, rank * part), to = min(n, from + part);
-  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
-  // ---- the bound: the score of the sample's rank that leaves room for its error.  The sample is 512
-  // groups of eight neighbours spread over the row (whole sectors: 1024 groups of four waited for twice as many
-  // requests, 4096 rows of 65536 took 288 us instead of 267), the same in every CTA of the cluster; its
-  // histogram divides the scores' range evenly.
-  float bound = -CUDART_INF_F;
-  bool strict = true;
-  Bins bins{0.f, 0.f};
-  if (n > static_cast<int>(cap)) {
-    float f[8];
-    float lo = CUDART_INF_F, hi = -CUDART_INF_F;
+// The bound of a row of n scores: the one of rank `rank` (1: the largest) in the sample, and the scale of the bins
+// from there on (0: none, -1: no bound).  The sample is 512 groups of eight neighbours spread over the row (whole
+// sectors: 1024 groups of four waited for twice as many requests, 4096 rows of 65536 took 288 us instead of
+// 267), the same in every CTA of the cluster; its histogram divides the scores' range evenly.  Leaves hist
+// empty.
+__device__ __forceinline__ float2 sample_bound(const float* __restrict__ x, bool vec, int n, uint32_t rank, SelShared& s) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  float f[8];
+  float lo = CUDART_INF_F, hi = -CUDART_INF_F;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = sample_at(tid + j * kSelThreads, n);
-      if (vec && i + 3 < n) {
-        const float4 w = __ldg(reinterpret_cast<const float4*>(x + i));
-        f[4 * j] = w.x, f[4 * j + 1] = w.y, f[4 * j + 2] = w.z, f[4 * j + 3] = w.w;
-      } else {
+  for (int j = 0; j < 2; ++j) {
+    const int i = sample_at(tid + j * kSelThreads, n);
+    if (vec && i + 3 < n) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(x + i));
+      f[4 * j] = w.x, f[4 * j + 1] = w.y, f[4 * j + 2] = w.z, f[4 * j + 3] = w.w;
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[4 * j + e] = i + e < n ? __ldg(x + i + e) : CUDART_NAN_F;
-      }
+      for (int e = 0; e < 4; ++e) f[4 * j + e] = i + e < n ? __ldg(x + i + e) : CUDART_NAN_F;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (fabsf(f[j]) < CUDART_INF_F) lo = fminf(lo, f[j]), hi = fmaxf(hi, f[j]);       // finite ones
-    // order of floats as integers: the warps' extremes meet in shared memory
-    const uint32_t wlo = __reduce_min_sync(0xFFFFFFFFu, score_key(lo)), whi = __reduce_max_sync(0xFFFFFFFFu, score_key(hi));
-    if (tid == 0) s.stat[0] = 0xFFFFFFFFu, s.stat[1] = 0, s.stat[2] = 0;
-    reinterpret_cast<uint4*>(s.hist)[tid] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    if (lane == 0) {
-      atomicMin(&s.stat[0], wlo);
-      atomicMax(&s.stat[1], whi);
-    }
-    __syncthreads();
-    lo = key_score(s.stat[0]);
-    hi = key_score(s.stat[1]);
-    const float scale = 2047.f / (hi - lo);
-    if (hi > lo && scale > 0.f && scale < CUDART_INF_F) {
-      uint32_t inf = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (fabsf(f[j]) < CUDART_INF_F) atomicAdd(&s.hist[static_cast<int>((f[j] - lo) * scale)], 1u);
-        inf += f[j] == CUDART_INF_F ? 1u : 0u;
-      }
-      if (inf) atomicAdd(&s.hist[kSelBins - 1], inf);
-      __syncthreads();
-      const float r = static_cast<float>(kk) * kSelSample / n;
-      const uint32_t rank = static_cast<uint32_t>(r + 6.f * sqrtf(r) + 8.f);
-      const uint4 c = reinterpret_cast<const uint4*>(s.hist)[kSelThreads - 1 - tid];      // bins 2047 - 4 tid .. 2044 - 4 tid
-      const uint32_t own = c.x + c.y + c.z + c.w;
-      uint32_t before = block_prefix(own, s.wsum);
-      if (before < rank && rank <= before + own) {       // at most one thread
-        uint32_t bin = kSelBins - 1 - 4 * tid;
-        if (rank > before + c.w) before += c.w, --bin;
-        if (bin == kSelBins - 2 - 4 * tid && rank > before + c.z) before += c.z, --bin;
-        if (bin == kSelBins - 3 - 4 * tid && rank > before + c.y) --bin;
-        s.found[0] = __float_as_uint(lo + static_cast<float>(bin) / scale);
-        s.stat[2] = 1;
-      }
-      __syncthreads();
-      if (s.stat[2]) {
-        bound = __uint_as_float(s.found[0]);
-        strict = false;
-        // room above the sample's largest: the row's tail may be as long again
-        const float scale2 = (kSelBins / 2 - 1) / (hi - bound);
-        if (hi > bound && scale2 > 0.f && scale2 < CUDART_INF_F) bins = Bins{bound, scale2};
-        reinterpret_cast<uint4*>(s.hist)[tid] = make_uint4(0, 0, 0, 0);
-      }
-    }
-    __syncthreads();
   }
-  // ---- stream: a warp takes 512 neighbouring scores at a time, 4 a lane and load; of a row that is let in
-  // whole 128, so that a short one is shared by the warps
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (fabsf(f[j]) < CUDART_INF_F) lo = fminf(lo, f[j]), hi = fmaxf(hi, f[j]);       // finite ones
+  // order of floats as integers: the warps' extremes meet in shared memory
+  const uint32_t wlo = __reduce_min_sync(0xFFFFFFFFu, score_key(lo)), whi = __reduce_max_sync(0xFFFFFFFFu, score_key(hi));
+  if (tid == 0) s.stat[0] = 0xFFFFFFFFu, s.stat[1] = 0, s.stat[2] = 0;
+  reinterpret_cast<uint4*>(s.hist)[tid] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  if (lane == 0) {
+    atomicMin(&s.stat[0], wlo);
+    atomicMax(&s.stat[1], whi);
+  }
+  __syncthreads();
+  lo = key_score(s.stat[0]);
+  hi = key_score(s.stat[1]);
+  const float scale = 2047.f / (hi - lo);
+  if (hi > lo && scale > 0.f && scale < CUDART_INF_F) {
+    uint32_t inf = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (fabsf(f[j]) < CUDART_INF_F) atomicAdd(&s.hist[static_cast<int>((f[j] - lo) * scale)], 1u);
+      inf += f[j] == CUDART_INF_F ? 1u : 0u;
+    }
+    if (inf) atomicAdd(&s.hist[kSelBins - 1], inf);
+    __syncthreads();
+    const uint4 c = reinterpret_cast<const uint4*>(s.hist)[kSelThreads - 1 - tid];      // bins 2047 - 4 tid .. 2044 - 4 tid
+    const uint32_t own = c.x + c.y + c.z + c.w;
+    uint32_t before = block_prefix(own, s.wsum);
+    if (before < rank && rank <= before + own) {       // at most one thread
+      uint32_t bin = kSelBins - 1 - 4 * tid;
+      if (rank > before + c.w) before += c.w, --bin;
+      if (bin == kSelBins - 2 - 4 * tid && rank > before + c.z) before += c.z, --bin;
+      if (bin == kSelBins - 3 - 4 * tid && rank > before + c.y) --bin;
+      s.found[0] = __float_as_uint(lo + static_cast<float>(bin) / scale);
+      s.stat[2] = 1;
+    }
+    __syncthreads();
+    reinterpret_cast<uint4*>(s.hist)[tid] = make_uint4(0, 0, 0, 0);
+    if (s.stat[2]) {
+      const float bound = __uint_as_float(s.found[0]);
+      // room above the sample's largest: the row's tail may be as long again
+      const float bins = (kSelBins / 2 - 1) / (hi - bound);
+      return make_float2(bound, hi > bound && bins > 0.f && bins < CUDART_INF_F ? bins : 0.f);
+    }
+  }
+  return make_float2(0.f, -1.f);
+}
+
+// Streams x[from .. to) and lists what the bound lets in (and the forced).  A warp takes 512 neighbouring scores
+// at a time, 4 a lane and load; of a row that is let in whole 128, so that a short one is shared by the warps.
+__device__ __forceinline__ void let_in(const float* __restrict__ x, bool vec, int from, int to, int f_lo, int f_hi, float bound,
+                                    bool strict, uint32_t cap, SelShared& s, uint2* list) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (strict) {
     for (int i0 = from + warp * 128; i0 < to; i0 += kSelWarps * 128) {
       const int i = i0 + 4 * lane;
@@ -793,39 +786,91 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
     if (i0 < f_lo || i0 + 512 > f_hi) take |= forced_bits(i0, 4, to, f_lo, f_hi);
     append(list, cap, &s.count, take, x, i0, false, f_lo, f_hi);
   }
+}
+
+// Rank in the sample of a bound that lets in the kk largest of n scores almost surely.
+__device__ __forceinline__ float sample_rank(uint32_t kk, int n) {
+  const float r = static_cast<float>(kk) * kSelSample / n;
+  return r + 6.f * sqrtf(r) + 8.f;
+}
+
+// A part's list of what the bound of the sample's rank rho lets in, as keys, counted in `bins`.
+struct List {
+  int m;               // entries
+  uint32_t total;      // of the row, with those that had no place
+  bool good;           // all have a place, and they are at least topk or the row's all
+  bool strict;         // no bound
+  Bins bins;
+  float bound;
+};
+
+__device__ __forceinline__ List list_of(const float* __restrict__ x, bool vec, int n, int from, int to, int f_lo, int f_hi, float rho,
+                                        float tried, int ranks, uint32_t cap, int topk, SelShared& s, uint2* list) {
+  const int tid = threadIdx.x;
+  List l{0, 0, false, true, Bins{0.f, 0.f}, -CUDART_INF_F};
+  float& bound = l.bound;
+  if (tid == 0) s.count = 0;
   __syncthreads();
-  uint32_t total = s.count;
-  int m = static_cast<int>(min(total, cap));
-  bool fits = total <= cap;
-  // the scores become keys, and are counted
-  for (int i = tid; i < m; i += kSelThreads) {
+  if (n > static_cast<int>(cap)) {
+    const float2 found = sample_bound(x, vec, n, static_cast<uint32_t>(fminf(fmaxf(rho, 1.f), kSelSample - 1.f)), s);
+    if (found.y >= 0.f) bound = found.x, l.bins = Bins{found.x, found.y}, l.strict = false;
+  }
+  if (bound == tried) return l;
+  let_in(x, vec, from, to, f_lo, f_hi, bound, l.strict, cap, s, list);
+  __syncthreads();
+  l.total = s.count;
+  l.m = static_cast<int>(min(l.total, cap));
+  bool fits = l.total <= cap;
+  for (int i = tid; i < l.m; i += kSelThreads) {
     const uint2 e = list[i];
     const int at = static_cast<int>(e.y);
     const bool forced = at < f_lo || at >= f_hi;
     const float v = __uint_as_float(e.x);
     list[i].x = forced ? kForcedKey : score_key(v);
-    if (bins.scale > 0.f && !forced) atomicAdd(&s.hist[bins.of(v)], 1u);
+    if (l.bins.scale > 0.f && !forced) atomicAdd(&s.hist[l.bins.of(v)], 1u);
   }
   if (ranks == 1) {
     __syncthreads();
   } else {
     cluster_sync();
     const uint32_t c = ld_ranks(&s.count, ranks);
-    total = __reduce_add_sync(0xFFFFFFFFu, c);
+    l.total = __reduce_add_sync(0xFFFFFFFFu, c);
     fits = __all_sync(0xFFFFFFFFu, c <= cap);
   }
-  // Too many for a list, or fewer than topk although the row was not let in whole (the bound was too
-  // high): not good.
-  const bool good = fits && (strict || total >= static_cast<uint32_t>(p.topk));
+  l.good = fits && (l.strict || l.total >= static_cast<uint32_t>(topk));
+  return l;
+}
+
+__device__ __forceinline__ bool select_row(const IndexSelectParams& p, int t, int rank, int ranks, int b, int64_t vis,
+                                           uint32_t cap, SelShared& s, uint2* list) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const float* __restrict__ x = p.scores + t * p.s_stride;
+  const int n = select_blocks_of(p, vis);
+  const int f_lo = min(p.first, n), f_hi = max(f_lo, n - p.last);      // forced: below f_lo, from f_hi on
+  const uint32_t kk = p.topk - (f_lo + n - f_hi);                // places of the others
+  const int part = ((n + ranks - 1) / ranks + 3) & ~3;
+  const int from = min(n, rank * part), to = min(n, from + part);
+  const bool vec = (reinterpret_cast<uintptr_t>(x) & 15) == 0;
+  // ---- the bound: the score of the sample's rank that leaves room for its error
+  const List l = list_of(x, vec, n, from, to, f_lo, f_hi, sample_rank(kk, n) * s.again, s.tried, ranks, cap, p.topk, s, list);
+  int m = l.m;
 
   // ---- the cut, over the row
   Cut c{0, 0};
   uint32_t first = 0;
   uint32_t at = 0, all = p.topk;      // positions before this CTA's part, and of the row
-  const bool binned = good && kk > 0 && bins.scale > 0.f && cut_of_bins(m, kk, ranks, s, list, bins, c, first, at);
+  const bool binned = l.good && kk > 0 && l.bins.scale > 0.f && cut_of_bins(m, kk, ranks, s, list, l.bins, c, first, at);
   if (!binned) {
     if (ranks > 1) cluster_sync(); else __syncthreads();           // the counts have been read
-    if (!good) {
+    if (!l.good) {
+      if (!l.strict && s.again == 1.f) {       // once more, with a rank for the middle of the list's room
+        if (tid == 0) {
+          s.again = 0.5f * static_cast<float>(p.topk + cap) / static_cast<float>(l.total);
+          s.tried = l.bound;
+        }
+        __syncthreads();
+        return false;
+      }
       m = ordered_list(x, vec, from, to, f_lo, f_hi, kk, cap, s, list);
       __syncthreads();
     }
@@ -876,7 +921,7 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
   for (int i = static_cast<int>(all) + rank * kSelThreads + tid; i < p.topk; i += ranks * kSelThreads) out[i] = -1;
   // the list is written, and no CTA leaves while another may read its count
   if (ranks > 1) cluster_sync(); else __syncthreads();
-  if (!out_slots) return;
+  if (!out_slots) return true;
   // ---- token slots of the taken blocks through the block table
   const int64_t slots = static_cast<int64_t>(p.topk) * p.block_tokens;
   for (int64_t i = rank * kSelThreads + tid; i < slots; i += ranks * kSelThreads) {
@@ -895,6 +940,7 @@ __device__ __forceinline__ void select_row(const IndexSelectParams& p, int t, in
     }
     out_slots[i] = slot;
   }
+  return true;
 }
 
 __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const IndexSelectParams p, int ranks, int cap) {
@@ -908,10 +954,14 @@ __global__ void __launch_bounds__(kSelThreads, 3) mla_index_select_kernel(const 
     if (threadIdx.x == 0) {
       s.row[0] = b;
       s.row[1] = vis;
+      s.again = 1.f;
+      s.tried = CUDART_NAN_F;
     }
   }
   __syncthreads();
-  if (s.row[0] >= 0) select_row(p, t, rank, ranks, static_cast<int>(s.row[0]), s.row[1], cap, s, list);
+  if (s.row[0] < 0) return;
+  while (!select_row(p, t, rank, ranks, static_cast<int>(s.row[0]), s.row[1], cap, s, list)) {
+  }
 }
 
 // ------------------------------------------------------------------------------------------

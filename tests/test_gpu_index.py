@@ -843,10 +843,10 @@ def test_select_rows_off_the_16_byte_grid(m, offset):
 
 @pytest.mark.parametrize("rows", [1, 160])      # rows shared by a cluster, and one CTA each
 @pytest.mark.parametrize("n,k", [(9000, 600), (70001, 513), (140000, 2048)])
-@pytest.mark.parametrize("kind", ["grid", "outlier", "infinite", "forced"])
+@pytest.mark.parametrize("kind", ["grid", "outlier", "infinite", "forced", "blocks", "waves", "periodic"])
 def test_select_crowded_cuts(m, rows, n, k, kind):
     """Equal scores at the cut, a range that an outlier stretches, more infinities than places, forced blocks on
-    both sides of the cut."""
+    both sides of the cut; rows whose neighbours resemble one another, or that repeat with the sample's stride."""
     rng = np.random.default_rng(n + k)
     x = rng.standard_normal((2, n)).astype(np.float32)
     if kind == "grid":
@@ -857,6 +857,13 @@ def test_select_crowded_cuts(m, rows, n, k, kind):
     elif kind == "infinite":
         x[0, rng.permutation(n)[:k + 40]] = np.inf
         x[1, rng.permutation(n)[:k // 2]] = np.inf
+    elif kind == "blocks":
+        x = np.repeat(x[:, :n // 16 + 1], 16, 1)[:, :n] + np.float32(0.02) * x
+    elif kind == "waves":
+        x = np.sin(np.arange(n) / np.array([[90.0], [700.0]])).astype(np.float32) + np.float32(0.1) * x
+    elif kind == "periodic":
+        x[:, :: max(1, n // 512)] += 9
+        x[1] = -x[1]
     first, last = (5, 9) if kind == "forced" else (0, 0)
     if rows == 1:
         check_select(m, x[:1], [n], [1], 1, k, first, last, slots=True, ps=64, seed=n)
