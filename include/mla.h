@@ -73,9 +73,10 @@ MLA_API int mla_read_device_errors(uint32_t* flags, cudaStream_t stream);
 
 /*
  * Profiling aid.  While both events are non-NULL, every attention-kernel launch made by
- * mla_sparse_fwd / mla_paged_decode on the calling host thread is bracketed by
+ * mla_sparse_fwd / mla_paged_decode / mla_selected_decode on the calling host thread is bracketed by
  * cudaEventRecord(start) and cudaEventRecord(stop) on the call's stream (the split-K merge
- * and the epilogue are outside the bracket).  Pass NULL, NULL to stop.  The events are the
+ * and the epilogue are outside the bracket; where mla_selected_decode makes two launches, the
+ * events keep the second).  Pass NULL, NULL to stop.  The events are the
  * caller's; the library only records them.
  */
 MLA_API void mla_profile_attention_events(cudaEvent_t start, cudaEvent_t stop);
