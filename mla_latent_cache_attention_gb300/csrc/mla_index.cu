@@ -861,9 +861,10 @@ __device__ __forceinline__ bool select_row(const IndexSelectParams& p, int t, in
   uint32_t at = 0, all = p.topk;      // positions before this CTA's part, and of the row
   const bool binned = l.good && kk > 0 && l.bins.scale > 0.f && cut_of_bins(m, kk, ranks, s, list, l.bins, c, first, at);
   if (!binned) {
+    const bool fresh = s.again == 1.f;         // read before the barrier: thread 0 writes it after
     if (ranks > 1) cluster_sync(); else __syncthreads();           // the counts have been read
     if (!l.good) {
-      if (!l.strict && s.again == 1.f) {       // once more, with a rank for the middle of the list's room
+      if (!l.strict && fresh) {                // once more, with a rank for the middle of the list's room
         if (tid == 0) {
           s.again = 0.5f * static_cast<float>(p.topk + cap) / static_cast<float>(l.total);
           s.tried = l.bound;
