@@ -896,7 +896,11 @@ __global__ void __launch_bounds__(PagedCfg<F, NQ>::kThreads, 1)
         // one barrier decides: nothing to do (common), or move the reference (or abort)
         if (C::kPvSplit) tc_fence_before();
         const bool rare = named_bar_or(1, NT, need || !w);
-        if (C::kPvSplit && stid == 0) mbar_arrive(&s_free[gt & 1]);     // every thread has read S
+        // Every thread has read S; QK of tile gt + 2 may overwrite it.  A tile that moves the reference reads S
+        // again below: where the ring holds blocks of tile gt + 2 beside two whole tiles, S stays until then
+        // (a ring of two tiles holds none before PV of tile gt, which follows).
+        constexpr bool kEarlyS = R <= 2 * NB;
+        if (C::kPvSplit && stid == 0 && (kEarlyS || !rare)) mbar_arrive(&s_free[gt & 1]);
         bool pv_waited = false;
         if (rare) {
           ok = named_bar_and(1, NT, w);
@@ -949,6 +953,11 @@ __global__ void __launch_bounds__(PagedCfg<F, NQ>::kThreads, 1)
             }
           }
           load_s(s, gt, t);
+          if (C::kPvSplit && !kEarlyS) {
+            tc_fence_before();
+            named_bar_sync(1, NT);
+            if (stid == 0) mbar_arrive(&s_free[gt & 1]);
+          }
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
