@@ -1,0 +1,89 @@
+"""Layouts of the selector's tensors on the GPU, through both forms of the binding: refused on the host, or
+served as the packed ones."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+BF, U8, F32, I32, I64 = torch.bfloat16, torch.uint8, torch.float32, torch.int32, torch.int64
+
+
+class Declined:
+    """A marshalling that serves nothing: every call takes its Python form."""
+    insert = gather = scores = select = selected = staticmethod(lambda *a: None)
+
+
+@pytest.fixture(params=["C form", "Python form"])
+def m(request, monkeypatch):
+    import mla_latent_cache_attention_gb300 as mod
+    mod.lib()
+    mod._plain()
+    if request.param == "Python form":
+        monkeypatch.setattr(mod, "_marshal", Declined())
+    return mod
+
+
+def z(*s, dt):
+    return torch.zeros(s, dtype=dt, device="cuda")
+
+
+def test_rows_that_overlap_are_refused(m):
+    """Expanded tensors and others whose rows are closer than they are long."""
+    T, k, cols, W = 4, 8, 5, 40
+    one = lambda n, dt: z(1, n, dt=dt).expand(T, -1)
+    q, w, c, s = z(T, 2, 128, dt=U8), z(T, 2, dt=F32), z(3, 16, 128, dt=U8), z(3, 16, dt=F32)
+    lens, cu, good = z(T, dt=I32), z(T + 1, dt=I32), z(T, cols, dt=I32)
+    refused = lambda what: pytest.raises(m.MLAError, match=what)
+    with refused("block_table"):
+        m.index_gather(c, s, one(cols, I32), cu, fmt="fp8", num_tokens=3)
+    with refused("block_table"):
+        m.index_scores(q, w, c, s, one(cols, I32), lens, fmt="fp8", max_context=W)
+    for out in (one(W, F32), torch.as_strided(z(500, dt=F32), (T, W), (W - 1, 1))):
+        with refused("scores rows"):
+            m.index_scores(q, w, c, s, good, lens, fmt="fp8", max_context=W, scores=out)
+        with refused("scores rows"):
+            m.index_select(out, lens, k)
+    x = z(T, W, dt=F32)
+    with refused("blocks rows"):
+        m.index_select(x, lens, k, blocks=one(k, I32))
+    with refused("slots rows"):
+        m.index_select(x, lens, k, block_table=good, page_size=16, num_blocks=3, slots=one(k, I32))
+    with refused("block_table"):
+        m.index_select(x, lens, k, block_table=one(cols, I32), page_size=16, num_blocks=3)
+    dec = lambda t, b: m.selected_decode(z(T, 2, 576, dt=BF), z(3, 16, 576, dt=BF), t, lens, b, fmt="bf16", softmax_scale=1.0)
+    with refused("blocks rows"):
+        dec(good, one(k, I32))
+    with refused("block_table"):
+        dec(one(cols, I32), torch.full((T, k), -1, dtype=I32, device="cuda"))
+    assert m.read_device_errors() == 0
+
+
+def test_rows_further_apart_than_they_are_long(m):
+    """Every row tensor as a part of a wider one."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    T, k, cols, W, ps = 5, 6, 4, 40, 16
+    wide = lambda t, by: torch.nn.functional.pad(t, (0, by), value=7)[:, :t.shape[1]]
+    x = torch.randn((T, W), generator=g, device="cuda")
+    table = torch.randint(0, 20, (T, cols), generator=g, device="cuda", dtype=I32)
+    lens = torch.tensor([40, 1, 17, 33, 0], dtype=I32, device="cuda")
+    a = m.index_select(x, lens, k, block_table=table, page_size=ps, num_blocks=20)
+    b = m.index_select(wide(x, 3), lens, k, block_table=wide(table, 2), page_size=ps, num_blocks=20, blocks=wide(a[0] * 0, 5),
+                       slots=wide(a[1] * 0, 1))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    q, w = torch.randn((T, 3, 128), generator=g, device="cuda").to(BF), torch.rand((T, 3), generator=g, device="cuda")
+    c = torch.randn((20, ps, 128), generator=g, device="cuda").to(BF)
+    s = z(T, W, dt=F32)
+    m.index_scores(q, w, c, None, table, lens, fmt="bf16", max_context=W, scores=s)
+    t = wide(z(T, W, dt=F32), 9)
+    m.index_scores(q, wide(w, 1), c, None, wide(table, 3), lens, fmt="bf16", max_context=W, scores=t)
+    assert torch.equal(s, t)
+    pages = a[0] // ps
+    pages = torch.where(a[0] >= 0, pages, -1)[:, :1].contiguous()
+    kv, mq = torch.randn((20, ps, 576), generator=g, device="cuda").to(BF), torch.randn((T, 2, 576), generator=g, device="cuda").to(BF)
+    o = m.selected_decode(mq, kv, table, lens, pages, fmt="bf16", softmax_scale=0.1)[0]
+    p = m.selected_decode(mq, kv, wide(table, 2), lens, wide(pages, 4), fmt="bf16", softmax_scale=0.1)[0]
+    assert torch.equal(o, p)
+    cu = torch.tensor([0, 3, 4, 8, 8, 8], dtype=I32, device="cuda")
+    assert torch.equal(m.index_gather(c, None, table, cu, fmt="bf16", num_tokens=8),
+                       m.index_gather(c, None, wide(table, 2), cu, fmt="bf16", num_tokens=8, dst=wide(z(8, 128, dt=BF), 4)))
+    assert m.read_device_errors() == 0
