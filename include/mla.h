@@ -578,13 +578,9 @@ MLA_API int mla_sparse_fwd_staged(const void* q, int64_t q_s0, int64_t q_s1, con
 MLA_API void mla_debug_stall_next_decode(int32_t wait_us);
 
 /*
- * Test aid: how mla_paged_decode runs an fp8_ds_mla cache on the calling host thread.  The
- * q_len * H columns of a request form G groups of 16.  size 2, 3 or 6: where size divides G,
- * the groups run as clusters of that many CTAs, which take adjacent groups of the same request
- * and split range and each issue a share of every page tile's copies with cluster multicast
- * into all of them, so each key crosses L2 -> SM once per cluster.  size 1: one CTA per group.
- * Any other value restores the library's choice (pairs where G is even).  The results are the
- * same bit for bit.
+ * Without effect, kept for its callers.  It chose how many CTAs shared the page tiles of an
+ * fp8_ds_mla decode; the q_len * H columns of a request now always run as groups of 16, one CTA
+ * each, with the results that every choice gave.
  */
 MLA_API void mla_debug_ds_cluster(int32_t size);
 

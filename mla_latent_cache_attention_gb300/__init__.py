@@ -879,7 +879,6 @@ def debug_stall_next_decode(wait_us: int):
 
 
 def debug_ds_cluster(size: int = 0) -> None:
-    """Test aid (mla_debug_ds_cluster): fp8_ds_mla decodes on this host thread run the head
-    groups of a request as clusters of `size` CTAs (2, 3 or 6) that share each page tile, one
-    CTA per group (1), or as the library chooses (0: pairs where the group count is even)."""
+    """Without effect, kept for its callers: fp8_ds_mla decodes run one CTA per group of 16 columns,
+    with the results that every choice gave."""
     lib().mla_debug_ds_cluster(int(size))

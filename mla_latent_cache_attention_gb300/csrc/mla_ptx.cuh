@@ -104,15 +104,8 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// The same bounded wait with acquire at cluster scope (see mbar_try_wait_cl_ns).
-__device__ __forceinline__ bool mbar_wait_cl(uint64_t* bar, uint32_t parity, volatile int* abort_flag);
-
 // ------------------------------------------------------------------------------ clusters
-// A CTA pair (thread-block cluster) shares page tiles: each CTA issues part of a tile's
-// copies with cluster multicast, and signals the other CTA's barriers remotely.  Every
-// remote operation happens between the cluster barrier after setup (both CTAs' barriers are
-// initialised) and the one before exit (neither CTA leaves while the other may still write
-// into it).
+// The CTAs of a cluster that share one row of the selection read one another's shared memory.
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
@@ -132,15 +125,6 @@ __device__ __forceinline__ uint32_t mapa_shared(const void* p, uint32_t rank) {
   return r;
 }
 
-// Arrive (release at cluster scope) on an mbarrier of another CTA of the cluster.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-__device__ __forceinline__ void st_cluster_u64(uint32_t cluster_addr, uint64_t v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr), "l"(v) : "memory");
-}
-
 __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t cluster_addr) {
   uint4 v;
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -148,34 +132,6 @@ __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t cluster_addr) {
                : "r"(cluster_addr)
                : "memory");
   return v;
-}
-
-// try_wait with acquire at cluster scope: for phases completed by other CTAs' arrivals, so
-// that what they wrote before arriving is visible (and what we write next is ordered after
-// their reads).
-__device__ __forceinline__ bool mbar_try_wait_cl_ns(uint64_t* bar, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
-      : "memory");
-  return ok != 0;
-}
-
-__device__ __forceinline__ bool mbar_wait_cl(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  uint64_t t0 = globaltimer();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait_cl_ns(bar, parity, 2000)) return true;
-    if ((it & 7u) == 0) {
-      if (*abort_flag) return false;
-      if (globaltimer() - t0 > wait_limit_ns(abort_flag)) {
-        *abort_flag = 2;
-        return false;
-      }
-    }
-  }
 }
 
 // ------------------------------------------------------------------------------ async copies
@@ -254,16 +210,6 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Arrive on the mbarrier at the same shared-memory offset in every CTA of `mask` once every
-// previously issued tcgen05.mma of this thread completed.
-__device__ __forceinline__ void mma_commit_mc(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
-      "h"(mask)
       : "memory");
 }
 
