@@ -525,12 +525,16 @@ MLA_API int mla_index_select(const float* scores, int64_t s_stride, int64_t widt
  *                that is partly visible counts once, and listing it again, or a page without visible
  *                tokens, is reported (MLA_DEVERR_INDEX).
  *   workspace    device scratch of >= mla_selected_decode_workspace_size(...) bytes, 256-byte
- *                aligned.  Contents need no initialising and are garbage afterwards.
+ *                aligned.  Contents need no initialising and are garbage afterwards.  The size is that of
+ *                exactly T rows; fewer rows are split over the SMs and may need more.
+ *                mla_selected_decode_workspace_bound is enough for every call of 1 .. max_T rows.
  * A row without a selected token, or outside every request, gets out = 0 and lse = -inf (B = 0: nothing
  * is launched or written).
  */
 MLA_API size_t mla_selected_decode_workspace_size(mla_cache_format fmt, int32_t T, int32_t topk, int32_t block_size,
                                                   int32_t H, int32_t num_sms);
+MLA_API size_t mla_selected_decode_workspace_bound(mla_cache_format fmt, int32_t max_T, int32_t topk,
+                                                   int32_t block_size, int32_t H, int32_t num_sms);
 MLA_API int mla_selected_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache, mla_cache_format fmt,
                                 int64_t num_blocks, int64_t block_stride_bytes, int64_t entry_stride_bytes,
                                 int32_t block_size, const int32_t* block_table, int64_t bt_stride, int64_t bt_cols,

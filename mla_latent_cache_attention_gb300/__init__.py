@@ -107,8 +107,9 @@ def lib():
                                        i32, i32, i32, i32, vp, i64, i64, vp]
         L.mla_index_select.argtypes = [vp, i64, i64, vp, vp, i32, i32, i32, i32, i32, i32, vp, i64, vp, i64, vp, i64,
                                        i64, i32, i64, vp]
-        L.mla_selected_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
-        L.mla_selected_decode_workspace_size.restype = sz
+        for f in (L.mla_selected_decode_workspace_size, L.mla_selected_decode_workspace_bound):
+            f.argtypes = [i32, i32, i32, i32, i32, i32]
+            f.restype = sz
         L.mla_selected_decode.argtypes = [vp, i64, i64, vp, i32, i64, i64, i64, i32, vp, i64, i64, vp, vp, vp, i64, i32,
                                           i32, i32, i32, f32, f32, f32, vp, i64, i64, vp, vp, sz, vp]
         L.mla_debug_stall_next_decode.argtypes = [i32]
@@ -797,7 +798,13 @@ def index_select(scores, seq_lens, topk, cu_q_lens=None, *, block_tokens=1, firs
 
 
 def selected_decode_workspace_size(fmt, T, topk, block_size, H, num_sms=0) -> int:
+    """Bytes of workspace of a selected_decode of exactly T rows (fewer rows may need more)."""
     return int(lib().mla_selected_decode_workspace_size(_fmt(fmt), T, topk, block_size, H, num_sms))
+
+
+def selected_decode_workspace_bound(fmt, max_T, topk, block_size, H, num_sms=0) -> int:
+    """Bytes of workspace that are enough for every selected_decode of 1 .. max_T rows."""
+    return int(lib().mla_selected_decode_workspace_bound(_fmt(fmt), max_T, topk, block_size, H, num_sms))
 
 
 def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, *, fmt, softmax_scale, q_scale=1.0,

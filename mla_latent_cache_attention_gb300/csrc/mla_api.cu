@@ -768,45 +768,73 @@ extern "C" int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const
 // the SMs, if the estimate with 4 us for that launch is 3 % less: the fp8_ds_mla case above 314 -> 297 us (126 rows and
 // 2), 64 rows of 128 heads 215 -> 211; bf16, 160 rows of 64 heads, 32 pages, 276 -> 217, 200 of 16 heads, 16 pages, 101 -> 86;
 // fp8, 160 rows of 64 heads, 16 pages, 74 -> 62.
-mla::SelectedPlan mla::plan_selected(int fmt, int64_t T, int H, int64_t context, int sms) {
-  const int64_t tiles = (context + kTile - 1) / kTile;
-  const int64_t slots = sms < 1 ? 1 : sms;
-  int64_t groups = 1;
+namespace {
+
+// What the estimate of a selected decode depends on beside its rows.
+struct SelectedShape {
+  int64_t tiles, groups, slots;      // key tiles of a row, column groups of a row, CTAs at once
+  int H;
+};
+
+SelectedShape selected_shape(int fmt, int H, int64_t context, int sms) {
+  SelectedShape s{(context + kTile - 1) / kTile, (H + kRows - 1) / kRows, sms < 1 ? 1 : sms, H};
   ColPlan cp{};
-  if (fmt == MLA_CACHE_FP8_DS_MLA) {
-    groups = (H + 15) / 16;
-  } else if (plan_columns(fmt, H, 1, &cp)) {
-    groups = cp.G;
-  } else {
-    groups = (H + kRows - 1) / kRows;
+  if (fmt == MLA_CACHE_FP8_DS_MLA)
+    s.groups = (H + 15) / 16;
+  else if (plan_columns(fmt, H, 1, &cp))
+    s.groups = cp.G;
+  return s;
+}
+
+// The split of `rows` rows in one launch, and its estimated time.
+SplitPlan split_alike(const SelectedShape& c, int64_t rows, double* us_out) {
+  int64_t best = 1;
+  double best_us = 0;
+  for (int64_t s = 1; s <= c.tiles && s <= 64; ++s) {
+    const int64_t per = (c.tiles + s - 1) / s;
+    if (s > 1 && (c.tiles + per - 1) / per != s) continue;       // the same parts as a smaller count
+    const int64_t waves = (rows * c.groups * s + c.slots - 1) / c.slots;
+    double us = static_cast<double>(waves) * (3.3 * per + 6.0);
+    if (s > 1) us += 3.0 + 4096.0 * static_cast<double>(s * rows * c.H) / 5e6;
+    if (s == 1 || us < best_us) best = s, best_us = us;
   }
-  auto alike = [&](int64_t rows, double* us_out) -> SplitPlan {
-    int64_t best = 1;
-    double best_us = 0;
-    for (int64_t s = 1; s <= tiles && s <= 64; ++s) {
-      const int64_t per = (tiles + s - 1) / s;
-      if (s > 1 && (tiles + per - 1) / per != s) continue;       // the same parts as a smaller count
-      const int64_t waves = (rows * groups * s + slots - 1) / slots;
-      double us = static_cast<double>(waves) * (3.3 * per + 6.0);
-      if (s > 1) us += 3.0 + 4096.0 * static_cast<double>(s * rows * H) / 5e6;
-      if (s == 1 || us < best_us) best = s, best_us = us;
-    }
-    *us_out = best_us;
-    return SplitPlan{static_cast<int>(best), (tiles + best - 1) / best * kTile};
-  };
+  *us_out = best_us;
+  return SplitPlan{static_cast<int>(best), (c.tiles + best - 1) / best * kTile};
+}
+
+}  // namespace
+
+mla::SelectedPlan mla::plan_selected(int fmt, int64_t T, int H, int64_t context, int sms) {
+  const SelectedShape c = selected_shape(fmt, H, context, sms);
   SelectedPlan plan{T, {}, {}};
   double us = 0, tail_us = 0;
-  plan.main = alike(T, &us);
-  const int64_t waves = T * groups / slots, rows = waves * slots / groups;       // whole waves of unsplit items
+  plan.main = split_alike(c, T, &us);
+  const int64_t waves = T * c.groups / c.slots, rows = waves * c.slots / c.groups;       // whole waves of unsplit items
   if (rows > 0 && rows < T) {
-    const SplitPlan tail = alike(T - rows, &tail_us);
-    if (static_cast<double>(waves) * (3.3 * tiles + 6.0) + tail_us + 4.0 < 0.97 * us) {
+    const SplitPlan tail = split_alike(c, T - rows, &tail_us);
+    if (static_cast<double>(waves) * (3.3 * c.tiles + 6.0) + tail_us + 4.0 < 0.97 * us) {
       plan.rows = rows;
-      plan.main = SplitPlan{1, tiles * kTile};
+      plan.main = SplitPlan{1, c.tiles * kTile};
       plan.tail = tail;
     }
   }
   return plan;
+}
+
+// Both parts of a plan are split as so many rows alone are.  With s > 1 splits and w = rows groups / slots, an
+// estimate is at least w (3.3 tiles + 6 s) + 3, and less than (w + 1) (3.3 tiles + 6) without: from
+// w = (3.3 tiles + 3) / 6 on rows are never split.
+size_t mla::selected_partials_bound(int fmt, int64_t T, int H, int64_t context, int sms) {
+  const SelectedShape c = selected_shape(fmt, H, context, sms);
+  const double most = static_cast<double>(c.slots) * (3.3 * c.tiles + 3.0) / (6.0 * c.groups) + 1.0;
+  const int64_t end = static_cast<double>(T) < most ? T : static_cast<int64_t>(most);
+  size_t bytes = 0;
+  for (int64_t rows = 1; rows <= end; ++rows) {
+    double us = 0;
+    const size_t need = workspace_bytes_for(rows, H, split_alike(c, rows, &us));
+    if (need > bytes) bytes = need;
+  }
+  return bytes;
 }
 
 int mla::run_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache, int cache_fmt, int64_t num_blocks,

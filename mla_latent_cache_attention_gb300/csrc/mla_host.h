@@ -46,6 +46,8 @@ struct SelectedPlan {
   SplitPlan main, tail;
 };
 SelectedPlan plan_selected(int fmt, int64_t T, int H, int64_t context, int sms);
+// The largest workspace_bytes_for of the parts of plan_selected over 1 .. T rows.
+size_t selected_partials_bound(int fmt, int64_t T, int H, int64_t context, int sms);
 // Workspace of a plan, and the address of its scheduler word there (null without splits).
 size_t workspace_bytes_for(int64_t n_rows, int H, const SplitPlan& sp);
 uint32_t* sched_word(void* workspace, int64_t n_rows, int H, const SplitPlan& sp);

@@ -274,19 +274,32 @@ static size_t selected_list_bytes(int32_t T, int32_t topk) {
   return lens + table;
 }
 
+namespace {
+
+// The SM count of a workspace query: as given, or the current device's (0: no size).
+int query_sms(int32_t T, int32_t topk, int32_t block_size, int32_t H, int32_t num_sms) {
+  if (T <= 0 || topk <= 0 || block_size <= 0 || H <= 0) return 0;
+  if (static_cast<int64_t>(topk) * block_size >= (1 << 30)) return 0;
+  if (num_sms > 0) return num_sms;
+  DevInfo* d = nullptr;
+  return dev_info(&d) == MLA_OK ? d->sms : 0;
+}
+
+}  // namespace
+
 extern "C" size_t mla_selected_decode_workspace_size(mla_cache_format fmt, int32_t T, int32_t topk, int32_t block_size,
                                                      int32_t H, int32_t num_sms) {
-  if (T <= 0 || topk <= 0 || block_size <= 0 || H <= 0) return 0;
-  const int64_t ctx = static_cast<int64_t>(topk) * block_size;
-  if (ctx >= (1 << 30)) return 0;
-  int sms = num_sms;
-  if (sms <= 0) {
-    DevInfo* d = nullptr;
-    if (dev_info(&d) != MLA_OK) return 0;
-    sms = d->sms;
-  }
-  const SelectedPlan sp = plan_selected(fmt, T, H, ctx, sms);
+  const int sms = query_sms(T, topk, block_size, H, num_sms);
+  if (sms == 0) return 0;
+  const SelectedPlan sp = plan_selected(fmt, T, H, static_cast<int64_t>(topk) * block_size, sms);
   return selected_list_bytes(T, topk) + workspace_bytes_for(sp.rows, H, sp.main) + workspace_bytes_for(T - sp.rows, H, sp.tail);
+}
+
+extern "C" size_t mla_selected_decode_workspace_bound(mla_cache_format fmt, int32_t max_T, int32_t topk,
+                                                      int32_t block_size, int32_t H, int32_t num_sms) {
+  const int sms = query_sms(max_T, topk, block_size, H, num_sms);
+  if (sms == 0) return 0;
+  return selected_list_bytes(max_T, topk) + selected_partials_bound(fmt, max_T, H, static_cast<int64_t>(topk) * block_size, sms);
 }
 
 extern "C" int mla_selected_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache,

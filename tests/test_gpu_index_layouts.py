@@ -87,3 +87,30 @@ def test_rows_further_apart_than_they_are_long(m):
     assert torch.equal(m.index_gather(c, None, table, cu, fmt="bf16", num_tokens=8),
                        m.index_gather(c, None, wide(table, 2), cu, fmt="bf16", num_tokens=8, dst=wide(z(8, 128, dt=BF), 4)))
     assert m.read_device_errors() == 0
+
+
+@pytest.mark.parametrize("fmt,H", [("bf16", 16), ("fp8", 64), ("fp8_ds_mla", 96)])
+def test_one_workspace_for_a_batch_that_shrinks(m, fmt, H):
+    """A workspace for 160 rows serves every smaller batch, with the results of a workspace of its own."""
+    g = torch.Generator(device="cuda").manual_seed(H)
+    ps, k, nb, most = 64, 16, 40, 160
+    if fmt == "bf16":
+        kv = torch.randn((nb, ps, 576), generator=g, device="cuda").to(BF)
+    else:
+        kv = torch.randint(0, 0x60, (nb, ps, 576), generator=g, device="cuda", dtype=torch.int32).to(U8)
+        if fmt == "fp8_ds_mla":
+            sc = torch.full((nb, ps, 4), 0.01, device="cuda").view(U8)
+            kv = torch.cat([kv[..., :512], sc, torch.randn((nb, ps, 64), generator=g, device="cuda").to(BF).view(U8)], -1).contiguous()
+    q = torch.randn((most, H, 576), generator=g, device="cuda").to(BF)
+    if fmt == "fp8":
+        q = torch.randint(0, 0x40, (most, H, 576), generator=g, device="cuda", dtype=torch.int32).to(U8)
+    table = torch.randint(0, nb, (most, 20), generator=g, device="cuda", dtype=I32)
+    lens = torch.randint(1, 20 * ps, (most,), generator=g, device="cuda", dtype=I32)
+    pages = torch.arange(k, device="cuda", dtype=I32).expand(most, k)
+    pages = torch.where(pages * ps < lens[:, None], pages, -1)
+    ws = torch.empty(m.selected_decode_workspace_bound(fmt, most, k, ps, H), dtype=U8, device="cuda")
+    for T in (160, 153, 152, 100, 64, 33, 32, 17, 8, 3, 1):
+        run = lambda **kw: m.selected_decode(q[:T], kv, table[:T], lens[:T], pages[:T], fmt=fmt, softmax_scale=0.01, return_lse=True, **kw)
+        (a, la), (b, lb) = run(workspace=ws), run()
+        assert torch.equal(a, b) and torch.equal(la, lb), T
+    assert m.read_device_errors() == 0
