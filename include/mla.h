@@ -501,7 +501,8 @@ MLA_API int mla_index_scores(const void* q, int64_t q_s0, int64_t q_s1, const fl
  * taken whatever their scores (first + last <= topk).  1 <= topk <= 8192.
  *
  *   scores       device fp32 [T, width], width < 2^30, row stride s_stride; columns past a row's visible blocks,
- *                ceil(visible tokens / block_tokens), are not read.
+ *                ceil(visible tokens / block_tokens), are not read.  With width 0 scores may be NULL (and
+ *                block_table too): every row's list is empty.
  *   blocks       device out int32 [T, topk], row stride b_stride: block indices in ascending order,
  *                then -1.
  *   slots        device out int32 [T, topk * block_tokens], row stride sl_stride, or NULL: the cache

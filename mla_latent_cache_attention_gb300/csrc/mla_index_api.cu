@@ -226,14 +226,16 @@ extern "C" int mla_index_select(const float* scores, int64_t s_stride, int64_t w
     return fail(MLA_ERR_INVALID, "first and last must be >= 0 and fit in topk");
   if (width < 0 || width >= (int64_t(1) << 30)) return fail(MLA_ERR_UNSUPPORTED, "width must be in [0, 2^30)");
   if (B == 0 || T == 0) return ok();
-  if (!scores || !seq_lens || !blocks) return fail(MLA_ERR_INVALID, "a required pointer is NULL");
+  // (without a column no score and no page is looked at: every row is a list of none)
+  if ((!scores && width > 0) || !seq_lens || !blocks) return fail(MLA_ERR_INVALID, "a required pointer is NULL");
   if (s_stride < width || !aligned(scores, 4)) return fail(MLA_ERR_INVALID, "bad scores rows");
   if (b_stride < topk || !aligned(blocks, 4)) return fail(MLA_ERR_INVALID, "bad blocks rows");
   if (slots) {
     const int64_t n = static_cast<int64_t>(topk) * block_tokens;
     if (n >= (int64_t(1) << 31)) return fail(MLA_ERR_UNSUPPORTED, "topk * block_tokens must be below 2^31");
     if (sl_stride < n || !aligned(slots, 4)) return fail(MLA_ERR_INVALID, "bad slots rows");
-    if (int rc = check_table(block_table, bt_stride, bt_cols, B)) return rc;
+    if (width > 0)
+      if (int rc = check_table(block_table, bt_stride, bt_cols, B)) return rc;
     if (page_size < 1 || num_blocks < 1) return fail(MLA_ERR_INVALID, "slots need page_size and num_blocks");
     if (num_blocks >= (int64_t(1) << 31) || num_blocks * page_size >= (int64_t(1) << 31))
       return fail(MLA_ERR_UNSUPPORTED, "num_blocks * page_size must be below 2^31");

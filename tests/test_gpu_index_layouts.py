@@ -114,3 +114,26 @@ def test_one_workspace_for_a_batch_that_shrinks(m, fmt, H):
         (a, la), (b, lb) = run(workspace=ws), run()
         assert torch.equal(a, b) and torch.equal(la, lb), T
     assert m.read_device_errors() == 0
+
+
+def test_scores_without_columns_select_nothing(m):
+    """A step of which no request has a context yet: scores of width 0, rows of -1."""
+    T, k = 3, 4
+    cu = torch.tensor([0, 2, 3], dtype=I32, device="cuda")
+    lens = z(2, dt=I32)
+    sc = m.index_scores(z(T, 4, 128, dt=U8), z(T, 4, dt=F32), z(2, 16, 128, dt=U8), z(2, 16, dt=F32), z(2, 3, dt=I32), lens, cu,
+                        fmt="fp8", max_context=0)
+    assert sc.shape == (T, 0)
+    for bt in (1, 16):
+        for table in (z(2, 3, dt=I32), z(2, 0, dt=I32)):
+            blocks, slots = m.index_select(sc, lens, k, cu, block_tokens=bt, first=1, last=1, block_table=table, page_size=16, num_blocks=2)
+            assert blocks.tolist() == [[-1] * k] * T and slots.tolist() == [[-1] * (k * bt)] * T
+    blocks, none = m.index_select(sc, lens, k, cu)
+    assert blocks.tolist() == [[-1] * k] * T and none is None
+    # keys that the width leaves out
+    blocks, _ = m.index_select(sc, lens + 40, k, cu)
+    assert blocks.tolist() == [[-1] * k] * T
+    out, lse = m.selected_decode(z(T, 2, 576, dt=BF), z(2, 16, 576, dt=BF), z(2, 3, dt=I32), lens, blocks, cu, fmt="bf16",
+                                 softmax_scale=1.0, return_lse=True)
+    assert not out.any() and torch.isneginf(lse).all()
+    assert m.read_device_errors() == 0

@@ -150,3 +150,15 @@ def test_c_form_hands_over_the_true_row_strides(c_form):
     dec = lambda t, b: (Stand((T, 2, 576), BF), Stand((3, 16, 576), BF), t, lens, b, None, 0, 1.0, 1.0, 1.0, None, False, None, None)
     refused("selected", "blocks rows", *dec(good, thin(k, I32)))
     refused("selected", "block_table", *dec(table, Stand((T, k), I32)))
+
+
+# ------------------------------------------------------------------------------------------ no columns
+
+def test_selection_without_columns_needs_no_scores(m):
+    """Width 0: the address of scores (and of a table of no columns) may be NULL.  The call is given a bad
+    page size, which is looked at last, so that it is refused either way."""
+    L, FAKE = m.lib(), 1 << 20
+    select = lambda x, width, table: L.mla_index_select(x, width, width, FAKE, FAKE, 2, 3, 1, 8, 0, 0, FAKE, 8, FAKE, 8, table, 0, 0, 0, 0, None)
+    assert select(None, 0, None) == INVALID and b"page_size" in L.mla_last_error()
+    assert select(None, 5, FAKE) == INVALID and b"pointer" in L.mla_last_error()
+    assert select(FAKE, 5, None) == INVALID and b"block_table" in L.mla_last_error()
