@@ -531,6 +531,7 @@ def merge_attn_states(prefix_output, prefix_lse, suffix_output, suffix_lse, *, o
 _BF16, _F32, _I32, _I64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
 _INDEX_TYPES = {CACHE_BF16: _BF16, CACHE_FP8: _BYTE_TYPES}
 _KV_TYPES = _BYTE_TYPES + _BF16
+_KV_BYTES = {CACHE_BF16: 1152, CACHE_FP8: 576, CACHE_FP8_DS_MLA: 656}
 _current_device = torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -824,7 +825,10 @@ def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, 
         raise ValueError(f"q must be [T, H, 576], got {tuple(q.shape)}")
     if isinstance(kv_cache, torch.Tensor) and kv_cache.dim() == 4 and kv_cache.shape[1] == 1:      # a head axis of size 1
         kv_cache = kv_cache.squeeze(1)
-    kvs = _strides(kv_cache, "kv_cache", _KV_TYPES, dev, 3)
+    kvs = _strides(kv_cache, "kv_cache", _KV_TYPES if fmt == CACHE_BF16 else _BYTE_TYPES, dev, 3)
+    es = kv_cache.element_size()
+    if kv_cache.shape[2] * es < _KV_BYTES.get(fmt, 0):
+        raise ValueError(f"entries of this cache format have {_KV_BYTES[fmt]} bytes, kv_cache has {kv_cache.shape[2] * es}")
     B, cu = _requests(seq_lens, cu_q_lens, T, dev)
     table, tstride, tcols = _table(block_table, B, dev)
     ls = _strides(blocks, "blocks", _I32, dev, 2)
@@ -848,7 +852,6 @@ def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, 
             lse.fill_(float("-inf"))
         return out, lse
     nb, bs, _ = kv_cache.shape
-    es = kv_cache.element_size()
     L = lib()
     if workspace is None:
         if _current_device() == dev.index:

@@ -137,3 +137,14 @@ def test_scores_without_columns_select_nothing(m):
                                  softmax_scale=1.0, return_lse=True)
     assert not out.any() and torch.isneginf(lse).all()
     assert m.read_device_errors() == 0
+
+
+def test_caches_of_another_format_are_refused(m):
+    q, t, n, b = z(2, 4, 576, dt=BF), z(2, 5, dt=I32), z(2, dt=I32), torch.full((2, 2), -1, dtype=I32, device="cuda")
+    run = lambda fmt, kv: m.selected_decode(z(2, 4, 576, dt=U8) if fmt == "fp8" else q, kv, t, n, b, fmt=fmt, softmax_scale=1.0)
+    for fmt, dt, w in (("fp8", BF, 576), ("fp8_ds_mla", BF, 576), ("fp8_ds_mla", U8, 576), ("bf16", U8, 576), ("bf16", BF, 512), ("fp8", U8, 512)):
+        with pytest.raises((ValueError, TypeError), match="kv_cache"):
+            run(fmt, z(3, 16, 1200, dt=dt)[..., :w])
+    for fmt, dt, w in (("fp8", U8, 576), ("fp8_ds_mla", U8, 656), ("bf16", U8, 1152), ("bf16", BF, 576)):
+        assert not run(fmt, z(3, 16, 1200, dt=dt)[..., :w])[0].any()
+    assert m.read_device_errors() == 0

@@ -162,3 +162,41 @@ def test_selection_without_columns_needs_no_scores(m):
     assert select(None, 0, None) == INVALID and b"page_size" in L.mla_last_error()
     assert select(None, 5, FAKE) == INVALID and b"pointer" in L.mla_last_error()
     assert select(FAKE, 5, None) == INVALID and b"block_table" in L.mla_last_error()
+
+
+# ------------------------------------------------------------------------------------------ caches of another format
+
+KV = [("bf16", BF, 576, True), ("bf16", U8, 1152, True), ("fp8", U8, 576, True), ("fp8", I8, 640, True), ("fp8_ds_mla", U8, 656, True),
+      ("fp8_ds_mla", U8, 1152, True), ("bf16", BF, 512, False), ("bf16", U8, 576, False), ("fp8", BF, 576, False), ("fp8", U8, 512, False),
+      ("fp8_ds_mla", BF, 576, False), ("fp8_ds_mla", U8, 576, False), ("fp8_ds_mla", BF, 656, False)]
+
+
+def decode_args(fmt, dtype, width, tensor):
+    q = tensor((2, 4, 576), U8 if fmt == "fp8" else BF)
+    return q, tensor((3, 16, width), dtype), tensor((2, 5), I32), tensor((2,), I32), tensor((2, 2), I32)
+
+
+@pytest.mark.parametrize("fmt,dtype,width,fits", KV)
+def test_python_form_refuses_a_cache_of_another_format(m, python_form, fmt, dtype, width, fits):
+    args = decode_args(fmt, dtype, width, lambda shape, dt: torch.zeros(shape, dtype=dt))
+    run = lambda: m.selected_decode(*args, fmt=fmt, softmax_scale=1.0, workspace=torch.zeros(1 << 16, dtype=U8))
+    if fits:
+        run()
+        assert len(python_form) == 1
+        return
+    with pytest.raises((ValueError, TypeError), match="kv_cache"):
+        run()
+    assert not python_form
+
+
+@pytest.mark.parametrize("fmt,dtype,width,fits", KV)
+def test_c_form_declines_a_cache_of_another_format(c_form, fmt, dtype, width, fits):
+    """One that fits reaches the C entry, which refuses the workspace here."""
+    args = decode_args(fmt, dtype, width, Stand)
+    number = {"bf16": 0, "fp8": 1, "fp8_ds_mla": 2}[fmt]
+    run = lambda: c_form.selected(*args, None, number, 1.0, 1.0, 1.0, None, False, Stand((8,), U8, ptr=(1 << 20) + 8), None)
+    if fits:
+        with pytest.raises(Refused):
+            run()
+    else:
+        assert run() is None
