@@ -40,6 +40,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -539,18 +540,27 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda in
 _marshal = None
 
 
+class _Declined:
+    """In place of the C marshalling where it is not built: every call takes its Python form."""
+    insert = gather = scores = select = selected = staticmethod(lambda *args: None)
+
+
 def _plain():
-    """The C marshalling of the selector's calls (built with libmla.so; raises if it is missing)."""
+    """The C marshalling of the selector's calls, built with libmla.so for this interpreter (without it, a warning
+    and the Python form of every call)."""
     global _marshal
     if _marshal is None:
         lib()
-        if not os.path.exists(_build.MARSHAL):
-            raise ImportError(f"mla_marshal.so not built ({_build.MARSHAL}); run mla_latent_cache_attention_gb300.build.build()")
-        loader = importlib.machinery.ExtensionFileLoader("mla_marshal", _build.MARSHAL)
-        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("mla_marshal", loader))
-        loader.exec_module(mod)
-        mod.init(torch.Tensor, torch.empty, getattr(torch._C, "_cuda_getDevice", _current_device), _raw_stream, _check,
-                 torch.bfloat16, torch.uint8, torch.int8, torch.float32, torch.int32, torch.int64)
+        try:
+            loader = importlib.machinery.ExtensionFileLoader("mla_marshal", _build.MARSHAL)
+            mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("mla_marshal", loader))
+            loader.exec_module(mod)
+            mod.init(torch.Tensor, torch.empty, getattr(torch._C, "_cuda_getDevice", _current_device), _raw_stream, _check,
+                     torch.bfloat16, torch.uint8, torch.int8, torch.float32, torch.int32, torch.int64)
+        except ImportError as e:
+            warnings.warn(f"the selector's calls take their Python form: {e}; mla_latent_cache_attention_gb300.build.build() builds "
+                          "their C marshalling")
+            mod = _Declined
         _marshal = mod
     return _marshal
 
