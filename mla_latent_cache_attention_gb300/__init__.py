@@ -566,22 +566,20 @@ def _plain():
 
 
 def _strides(t, name, dtypes, dev, ndim):
-    """The strides of a tensor that passes _need's checks (unit innermost stride)."""
+    """The strides of a tensor that passes _need's checks (unit innermost stride), for the C entry, which refuses
+    rows that overlap (an expanded tensor's do).  The stride of a dimension of one entry means nothing: where it
+    is below what the entry spans, that is handed over."""
     try:
-        if t.dtype in dtypes and t.get_device() == dev.index:
-            st = t.stride()
-            if len(st) == ndim and st[-1] == 1:
-                return st
+        plain = t.dtype in dtypes and t.get_device() == dev.index and t.dim() == ndim and t.stride(-1) == 1
     except AttributeError:
-        pass                # not a tensor: _need says so
-    _need(t, name, dtypes, dev, ndim=ndim)
-    return t.stride()
-
-
-def _row_stride(t, strides, length):
-    """The row stride of a 2-D tensor for the C entry, which refuses one below the rows' length (rows that
-    overlap, as an expanded tensor's do).  The stride of a single row means nothing: its length then."""
-    return strides[0] if t.shape[0] > 1 else max(strides[0], length)
+        plain = False           # not a tensor: _need says so
+    if not plain:
+        _need(t, name, dtypes, dev, ndim=ndim)
+    st = list(t.stride())
+    for i in range(ndim - 2, -1, -1):
+        if t.shape[i] <= 1:
+            st[i] = max(st[i], t.shape[i + 1] * st[i + 1])
+    return st
 
 
 def _call(fn, dev, *args):
@@ -644,7 +642,7 @@ def _table(block_table, rows, dev):
     have, cols = block_table.shape
     if have < rows:
         raise ValueError(f"block_table needs a row per request: {have} rows, {rows} requests")
-    return block_table.data_ptr(), _row_stride(block_table, st, cols), cols
+    return block_table.data_ptr(), st[0], cols
 
 
 def index_q_cache_insert(q, k, weights, index_cache, index_scales, slot_mapping, *, fmt, weight_scale=1.0,
@@ -762,7 +760,7 @@ def index_scores(q, weights, index_cache, index_scales, block_table, seq_lens, c
         raise ValueError(f"scores must be [T, >= {cols}] with T = {T}, got {tuple(scores.shape)}")
     _call(lib().mla_index_scores, dev, q.data_ptr(), qs[0], qs[1], weights.data_ptr(), ws[0], index_cache.data_ptr(), fmt, nb,
           bstride, estride, sc, sstride, bs, table, tstride, tcols, seq_lens.data_ptr(), cu, B, T, Hi, block_tokens,
-          scores.data_ptr(), _row_stride(scores, ss, cols), cols)
+          scores.data_ptr(), ss[0], cols)
     return scores
 
 
@@ -796,14 +794,14 @@ def index_select(scores, seq_lens, topk, cu_q_lens=None, *, block_tokens=1, firs
         per_row = topk * block_tokens
         if slots is None:
             slots = torch.empty((T, per_row), dtype=torch.int32, device=dev)
-        sl_stride = _row_stride(slots, _strides(slots, "slots", _I32, dev, 2), per_row)
+        sl_stride = _strides(slots, "slots", _I32, dev, 2)[0]
         if slots.shape != (T, per_row):
             raise ValueError(f"slots must be [T, topk * block_tokens] = {(T, per_row)}")
         sl = slots.data_ptr()
     elif slots is not None:
         raise ValueError("slots need a block_table")
-    _call(lib().mla_index_select, dev, scores.data_ptr(), _row_stride(scores, ss, width), width, seq_lens.data_ptr(), cu, B, T,
-          block_tokens, topk, first, last, blocks.data_ptr(), _row_stride(blocks, bs, topk), sl, sl_stride, table, tstride,
+    _call(lib().mla_index_select, dev, scores.data_ptr(), ss[0], width, seq_lens.data_ptr(), cu, B, T,
+          block_tokens, topk, first, last, blocks.data_ptr(), bs[0], sl, sl_stride, table, tstride,
           tcols, page_size, num_blocks)
     return blocks, slots
 
@@ -873,7 +871,7 @@ def selected_decode(q, kv_cache, block_table, seq_lens, blocks, cu_q_lens=None, 
     else:
         _need(workspace, "workspace", _BYTE_TYPES, dev, contiguous=True)
     _call(L.mla_selected_decode, dev, q.data_ptr(), qs[0], qs[1], kv_cache.data_ptr(), fmt, nb, es * kvs[0], es * kvs[1], bs,
-          table, tstride, tcols, seq_lens.data_ptr(), cu, blocks.data_ptr(), _row_stride(blocks, ls, topk), topk, B, T, H,
+          table, tstride, tcols, seq_lens.data_ptr(), cu, blocks.data_ptr(), ls[0], topk, B, T, H,
           float(softmax_scale), float(q_scale), float(k_scale), out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(),
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, lse

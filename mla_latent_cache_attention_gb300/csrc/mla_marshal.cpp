@@ -83,6 +83,11 @@ bool read(PyObject* o, long dev, int ndim, Tensor* t, PyObject* t0, PyObject* t1
   for (int i = 0; i < ndim; ++i)
     if (!as_i64(PyTuple_GET_ITEM(st.p, i), &t->stride[i]) || !as_i64(PyTuple_GET_ITEM(sh.p, i), &t->size[i])) return false;
   if (t->stride[ndim - 1] != 1) return false;
+  // the C entries refuse rows that overlap; the stride of a dimension of one entry means nothing
+  for (int i = ndim - 2; i >= 0; --i) {
+    const int64_t span = t->size[i + 1] * t->stride[i + 1];
+    if (t->size[i] <= 1 && t->stride[i] < span) t->stride[i] = span;
+  }
   Ref p(PyObject_CallMethodNoArgs(o, s_ptr));
   if (!p.p) return false;
   t->ptr = static_cast<char*>(PyLong_AsVoidPtr(p.p));
@@ -96,12 +101,6 @@ bool packed(const Tensor& t, int ndim) {
     n *= t.size[i];
   }
   return true;
-}
-
-// The row stride of a 2-D tensor for the C entry, which refuses one below the rows' length (rows that
-// overlap, as an expanded tensor's do).  The stride of a single row means nothing: its length then.
-int64_t row_stride(const Tensor& t, int64_t length) {
-  return t.size[0] > 1 || t.stride[0] > length ? t.stride[0] : length;
 }
 
 // The current device, if it is the tensor's.
@@ -221,7 +220,7 @@ bool read_table(PyObject* table, int64_t rows, long dev, Table* o) {
   if (!read(table, dev, 2, &t, g_i32) || t.size[0] < rows) return false;
   o->ptr = reinterpret_cast<const int32_t*>(t.ptr);
   o->cols = t.size[1];
-  o->stride = row_stride(t, o->cols);
+  o->stride = t.stride[0];
   return true;
 }
 
@@ -328,7 +327,7 @@ PyObject* py_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_BEGIN_ALLOW_THREADS
   rc = mla_index_scores(q.ptr, q.stride[0], q.stride[1], as<float>(w), w.stride[0], c.keys.ptr, static_cast<mla_cache_format>(fmt),
                         c.nb, c.block, c.entry, c.sc, c.sc_stride, c.bs, tab.ptr, tab.stride, tab.cols, r.lens, r.cu, r.B,
-                        static_cast<int32_t>(T), static_cast<int32_t>(H), bt, as<float>(s), row_stride(s, cols), cols, stream);
+                        static_cast<int32_t>(T), static_cast<int32_t>(H), bt, as<float>(s), s.stride[0], cols, stream);
   Py_END_ALLOW_THREADS
   if (rc) return refused(rc);
   return out.release();
@@ -355,7 +354,6 @@ PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (a[7] != Py_None) {
     if (!read_table(a[7], r.B, dev, &tab) || !output(a[11], dev, 2, slot_size, g_i32, nullptr, device.p, &s, &slots))
       return not_plain();
-    s.stride[0] = row_stride(s, per_row);
   } else if (a[11] != Py_None) {
     return not_plain();
   }
@@ -363,8 +361,8 @@ PyObject* py_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!stream_of(dev, &stream)) return not_plain();
   int rc;
   Py_BEGIN_ALLOW_THREADS
-  rc = mla_index_select(as<float>(x), row_stride(x, width), width, r.lens, r.cu, r.B, static_cast<int32_t>(T), bt,
-                        topk, first, last, as<int32_t>(b), row_stride(b, topk), as<int32_t>(s), s.stride[0],
+  rc = mla_index_select(as<float>(x), x.stride[0], width, r.lens, r.cu, r.B, static_cast<int32_t>(T), bt,
+                        topk, first, last, as<int32_t>(b), b.stride[0], as<int32_t>(s), s.stride[0],
                         tab.ptr, tab.stride, tab.cols, page, nb, stream);
   Py_END_ALLOW_THREADS
   if (rc) return refused(rc);
@@ -419,7 +417,7 @@ PyObject* py_selected(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_BEGIN_ALLOW_THREADS
   rc = mla_selected_decode(q.ptr, q.stride[0], q.stride[1], kv.ptr, static_cast<mla_cache_format>(fmt), kv.size[0], es * kv.stride[0],
                            es * kv.stride[1], bs, tab.ptr, tab.stride, tab.cols, r.lens, r.cu, as<int32_t>(blk),
-                           row_stride(blk, topk), static_cast<int32_t>(topk), r.B, static_cast<int32_t>(T),
+                           blk.stride[0], static_cast<int32_t>(topk), r.B, static_cast<int32_t>(T),
                            static_cast<int32_t>(H), sm, qsc, ksc, o.ptr, o.stride[0], o.stride[1], as<float>(l), ws.ptr,
                            static_cast<size_t>(bytes), stream);
   Py_END_ALLOW_THREADS

@@ -148,3 +148,27 @@ def test_caches_of_another_format_are_refused(m):
     for fmt, dt, w in (("fp8", U8, 576), ("fp8_ds_mla", U8, 656), ("bf16", U8, 1152), ("bf16", BF, 576)):
         assert not run(fmt, z(3, 16, 1200, dt=dt)[..., :w])[0].any()
     assert m.read_device_errors() == 0
+
+
+def test_single_rows_of_transposed_tensors(m):
+    """One row and one index head as transposes of columns give: the stride of the row is 1."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")
+    thin = lambda t: t.reshape(-1, 1).contiguous().t()           # [1, n], strides (1, 1)
+    x, w, k = thin(r(40)), thin(r(3)), thin(r(128).to(BF))
+    assert x.stride() == (1, 1)
+    lens, table = torch.tensor([40], dtype=I32, device="cuda"), thin(torch.tensor([2, 0, 1], dtype=I32, device="cuda"))
+    a = m.index_select(x, lens, 6, block_table=table, page_size=16, num_blocks=3)
+    b = m.index_select(x.clone(memory_format=torch.contiguous_format).reshape(1, 40), lens, 6, block_table=table.reshape(1, 3),
+                       page_size=16, num_blocks=3)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    q = r(1, 3, 128).to(BF)
+    res = []
+    for kk, ww in ((k, w), (k.reshape(1, 128).clone(), w.reshape(1, 3).clone())):
+        c, s = z(3, 16, 128, dt=U8), z(3, 16, dt=F32)
+        slot = torch.tensor([37], dtype=I64, device="cuda")
+        qo, wo = m.index_q_cache_insert(q, kk, ww, c, s, slot, fmt="fp8")
+        sc = m.index_scores(qo, wo if ww is not w else thin(wo[0]), c, s, table, lens, fmt="fp8", max_context=40)
+        res.append([qo, wo, c, s, sc])
+    assert all(torch.equal(i, j) for i, j in zip(*res))
+    assert m.read_device_errors() == 0

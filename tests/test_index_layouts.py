@@ -200,3 +200,46 @@ def test_c_form_declines_a_cache_of_another_format(c_form, fmt, dtype, width, fi
             run()
     else:
         assert run() is None
+
+
+# ------------------------------------------------------------------------------------------ dimensions of one entry
+
+def test_python_form_of_single_rows_and_heads(m, python_form):
+    """A dimension of one entry is handed over with what the entry spans, whatever its stride (1 here, as of a
+    transposed column)."""
+    thin = lambda *shape, dt: torch.as_strided(torch.zeros(4096, dtype=dt), shape, tuple([1] * len(shape)))
+    lens, cu = torch.zeros(1, dtype=I32), torch.zeros(2, dtype=I32)
+    q, w, c, s = thin(1, 1, 128, dt=BF), thin(1, 1, dt=F32), thin(1, 1, 128, dt=BF), thin(1, 4, dt=F32)
+    m.index_q_cache_insert(q, thin(1, 128, dt=BF), w, c, None, torch.zeros(1, dtype=I64), fmt="bf16")
+    m.index_scores(q, w, c, None, thin(1, 3, dt=I32), lens, fmt="bf16", max_context=4)
+    c8 = torch.as_strided(torch.zeros(4096, dtype=U8), (1, 4, 128), (1, 128, 1))
+    m.index_gather(c8, s, thin(1, 3, dt=I32), cu, fmt="fp8", num_tokens=1, dst=thin(1, 128, dt=BF))
+    m.selected_decode(thin(1, 1, 576, dt=BF), thin(1, 1, 576, dt=BF), thin(1, 3, dt=I32), lens, thin(1, 2, dt=I32), fmt="bf16",
+                      softmax_scale=1.0, out=thin(1, 1, 520, dt=BF), workspace=torch.zeros(1 << 12, dtype=U8))
+    insert, scores, gather, decode = [a for _, a in python_form]
+    assert [insert[i] for i in (1, 2, 4, 6, 13, 14)] == [128, 128, 128, 1, 256, 256]
+    assert [scores[i] for i in (1, 2, 4, 8, 9, 14)] == [128, 128, 1, 256, 256, 3]
+    assert [gather[i] for i in (3, 4, 6, 9, 16)] == [512, 128, 4, 3, 128]
+    assert [decode[i] for i in (1, 2, 6, 7, 10, 15, 24, 25)] == [576, 576, 1152, 1152, 3, 2, 520, 520]
+
+
+def test_c_form_of_single_rows_and_heads(c_form):
+    """The same: the only refusal is the one that each call is given, or that there is no device here."""
+    thin = lambda *shape, dt: Stand(shape, dt, tuple([1] * len(shape)))
+    lens = Stand((1,), I32)
+    with pytest.raises(Refused, match="page_size"):
+        c_form.select(thin(1, 9, dt=F32), lens, 4, None, 1, 0, 0, thin(1, 3, dt=I32), 0, 3, thin(1, 4, dt=I32), thin(1, 4, dt=I32))
+    with pytest.raises(Refused, match="cudaGetDevice"):
+        c_form.selected(thin(1, 1, 576, dt=BF), thin(1, 1, 576, dt=BF), thin(1, 3, dt=I32), lens, thin(1, 2, dt=I32), None, 0, 1.0, 1.0, 1.0,
+                        thin(1, 1, 520, dt=BF), False, Stand((1 << 20,), U8, ptr=(1 << 20) + 8), None)
+    q, c, s = thin(1, 1, 128, dt=BF), thin(1, 1, 128, dt=BF), thin(1, 9, dt=F32)
+    with pytest.raises(Refused, match="must be given together"):
+        c_form.insert(q, thin(1, 128, dt=BF), thin(1, 1, dt=F32), c, None, Stand((1,), I64), 0, 1.0, None, thin(1, 64, dt=F32), None, None)
+    with pytest.raises(Refused, match="NULL"):
+        c_form.gather(c, None, thin(1, 3, dt=I32), Stand((2,), I32, ptr=0), None, 0, 1, thin(1, 128, dt=BF))
+    with pytest.raises(Refused, match="scores rows"):       # the last check: an odd address
+        c_form.scores(q, thin(1, 1, dt=F32), c16(), None, thin(1, 3, dt=I32), lens, None, 0, 1, 9, Stand((1, 9), F32, (1, 1), ptr=(1 << 20) + 1))
+
+
+def c16():
+    return Stand((1, 16, 128), BF, (1, 128, 1))
