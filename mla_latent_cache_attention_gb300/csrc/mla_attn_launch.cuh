@@ -7,7 +7,7 @@ namespace mla {
 
 template <int F, bool kSparse>
 cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t stream) {
-  static bool configured[64] = {};
+  static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

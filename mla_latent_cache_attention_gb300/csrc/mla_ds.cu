@@ -7,7 +7,7 @@ namespace {
 
 template <bool kSparse>
 cudaError_t configure(int dev) {
-  static bool configured[64] = {};
+  static std::atomic<bool> configured[64];
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(mla_ds_kernel<kSparse>,

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kHbThreads, 1) mla_head_bmm_kernel(const HeadB
 int head_bmm_smem_bytes(int K) { return 384 * K + 64 + 1024; }
 
 cudaError_t launch_head_bmm(const HeadBmmParams& p, cudaStream_t stream) {
-  static int configured[64] = {};
+  static std::atomic<int> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

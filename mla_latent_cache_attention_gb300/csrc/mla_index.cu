@@ -1057,7 +1057,7 @@ cudaError_t launch_index_gather(int bf16, const IndexGatherParams& p, int sms, c
 static_assert(kSelFixed + (kSelectMaxTopk + kSelChunk) * 8 <= 200 * 1024, "shared memory budget");
 
 cudaError_t launch_index_select(const IndexSelectParams& p, int sms, cudaStream_t stream) {
-  static bool configured[64] = {};
+  static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

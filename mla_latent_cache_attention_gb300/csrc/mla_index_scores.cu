@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kIxThreads, 1)
 
 template <int F, int HP>
 cudaError_t launch_hp(const IndexScoresParams& p, const void* tk, const void* tq, int grid, cudaStream_t stream) {
-  static bool configured[64] = {};
+  static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

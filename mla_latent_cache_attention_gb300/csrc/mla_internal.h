@@ -1,6 +1,7 @@
 // mla_internal.h -- parameter blocks and launchers shared by the library's translation
 // units (not part of the public C ABI).
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <utility>
 #include <cuda_runtime.h>

@@ -8,7 +8,7 @@ namespace {
 template <int NQ>
 cudaError_t launch_nq(const PagedParams& p, const void* tkv, const void* tq, int grid, cudaStream_t stream) {
   using C = PagedCfg<kFP8, NQ>;
-  static bool configured[64] = {};
+  static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
