@@ -650,7 +650,10 @@ __global__ void __launch_bounds__(kIxThreads, 1)
               tmem_ld_wait();
               s = fmaf(max_nan(__uint_as_float(e), 0.f), weight(q * HP + h), s);
             }
-            v[q] = __shfl_sync(0xFFFFFFFFu, s, la + 8 * lb);
+            // (in another order of the sum: only for the keys that need it, so that the others' bits do not depend on
+            // what lies beside them, unwritten slots among it)
+            s = __shfl_sync(0xFFFFFFFFu, s, la + 8 * lb);
+            if (v[q] != v[q]) v[q] = s;
           }
         }
         const bool is_bad = bm && ((bm >> (key >> br_shift)) & 1u);

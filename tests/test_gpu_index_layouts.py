@@ -172,3 +172,33 @@ def test_single_rows_of_transposed_tensors(m):
         res.append([qo, wo, c, s, sc])
     assert all(torch.equal(i, j) for i, j in zip(*res))
     assert m.read_device_errors() == 0
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "bf16"])
+@pytest.mark.parametrize("Hi,bt", [(5, 1), (21, 1), (33, 16), (5, 64)])
+def test_scores_do_not_depend_on_what_lies_beside_a_key(m, fmt, Hi, bt):
+    """The same keys with NaN or zeros in the unwritten rest of their page, and with a NaN key among them: every other
+    key has the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(Hi)
+    n, ps = 200, 64
+    table, lens = torch.tensor([[3, 1, 0, 2]], dtype=I32, device="cuda"), torch.tensor([n], dtype=I32, device="cuda")
+    w = torch.randn((1, Hi), generator=g, device="cuda")
+    if fmt == "bf16":
+        c, s, nan = torch.randn((4, ps, 128), generator=g, device="cuda").to(BF), None, float("nan")
+        q = torch.randn((1, Hi, 128), generator=g, device="cuda").to(BF)
+    else:
+        code = lambda *shape: (torch.randint(0, 0x50, shape, generator=g, device="cuda", dtype=I32)
+                               + 128 * torch.randint(0, 2, shape, generator=g, device="cuda", dtype=I32)).to(U8)
+        c, s, nan = code(4, ps, 128), torch.rand((4, ps), generator=g, device="cuda"), 0x7F
+        q = code(1, Hi, 128)
+    c[2, n - 192:] = 0
+    run = lambda c: m.index_scores(q, w, c, s, table, lens, fmt=fmt, block_tokens=bt, max_context=n)
+    want = run(c)
+    tail = c.clone()
+    tail[2, n - 192:] = nan
+    assert torch.equal(run(tail), want)
+    tail[1, 5] = nan            # position 69
+    got = run(tail)
+    at = 69 // bt
+    assert torch.isnan(got[0, at]) and torch.equal(torch.cat([got[0, :at], got[0, at + 1:]]), torch.cat([want[0, :at], want[0, at + 1:]]))
+    assert m.read_device_errors() == 0
