@@ -202,3 +202,70 @@ def test_scores_do_not_depend_on_what_lies_beside_a_key(m, fmt, Hi, bt):
     at = 69 // bt
     assert torch.isnan(got[0, at]) and torch.equal(torch.cat([got[0, :at], got[0, at + 1:]]), torch.cat([want[0, :at], want[0, at + 1:]]))
     assert m.read_device_errors() == 0
+
+
+@pytest.mark.parametrize("fmt,H", [("bf16", 16), ("bf16", 40), ("fp8", 16), ("fp8", 32), ("fp8", 64), ("fp8_ds_mla", 96)])
+@pytest.mark.parametrize("ps", [64, 48])
+def test_selected_rows_do_not_depend_on_what_lies_beside_them(m, fmt, H, ps):
+    """The same bits with NaN or zeros in the unwritten rest of a page, and beside rows of other lengths."""
+    g = torch.Generator(device="cuda").manual_seed(H)
+    n, T = 11 * ps + 5, 6
+    if fmt == "bf16":
+        kv, nan = torch.randn((20, ps, 576), generator=g, device="cuda").to(BF), float("nan")
+    else:
+        code = torch.randint(0, 0x50, (20, ps, 576), generator=g, device="cuda", dtype=I32)
+        kv, nan = (code + 128 * torch.randint(0, 2, (20, ps, 576), generator=g, device="cuda", dtype=I32)).to(U8), 0x7F
+        if fmt == "fp8_ds_mla":
+            sc = torch.rand((20, ps, 4), generator=g, device="cuda").view(U8)
+            kv, nan = torch.cat([kv[..., :512], sc, torch.randn((20, ps, 64), generator=g, device="cuda").to(BF).view(U8)], -1).contiguous(), 0xFF
+    q = torch.randn((T, H, 576), generator=g, device="cuda").to(BF)
+    if fmt == "fp8":
+        q = torch.randint(0, 0x40, (T, H, 576), generator=g, device="cuda", dtype=I32).to(U8)
+    table = torch.randperm(20, generator=g, device="cuda").to(I32)[:12].expand(T, 12).contiguous()
+    lens = torch.tensor([n, n, 1, n, 3 * ps, n], dtype=I32, device="cuda")
+    pages = torch.tensor([[0, 3, 4, 11]] * 2 + [[0, -1, -1, -1]] + [[11, 0, 7, 9], [2, 1, -1, -1], [11, -1, -1, -1]], dtype=I32, device="cuda")
+    run = lambda kv, lens=lens, pages=pages: m.selected_decode(q, kv, table, lens, pages, fmt=fmt, softmax_scale=0.02, return_lse=True)
+    out, lse = run(kv)
+    assert bool(torch.isfinite(out).all() and torch.isfinite(lse).all())
+    for v in (nan, 0):
+        stale = kv.clone()
+        last = int(table[0, 11])
+        stale[last, 5:] = v             # past the contexts' end
+        o, l = run(stale)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    # other rows of other lengths, and none: the first row's bits stay
+    o, l = run(kv, lens=torch.tensor([n, 0, 5, 2, 0, 1], dtype=I32, device="cuda"),
+               pages=torch.tensor([[0, 3, 4, 11], [-1] * 4, [0, -1, -1, -1], [0, -1, -1, -1], [-1] * 4, [0, -1, -1, -1]], dtype=I32, device="cuda"))
+    assert torch.equal(o[0], out[0]) and torch.equal(l[0], lse[0])
+    assert m.read_device_errors() == 0
+
+
+def test_rows_before_and_after_the_requests(m):
+    """Rows ahead of cu_q_lens[0] and behind its last entry: left as they are (zeros and -inf from the attention)."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    T, ps = 7, 16
+    cu, lens = torch.tensor([2, 4, 5], dtype=I32, device="cuda"), torch.tensor([20, 9], dtype=I32, device="cuda")
+    table = torch.tensor([[2, 0], [1, 3]], dtype=I32, device="cuda")
+    cache = torch.randn((4, ps, 128), generator=g, device="cuda").to(BF)
+    q, w = torch.randn((T, 3, 128), generator=g, device="cuda").to(BF), torch.rand((T, 3), generator=g, device="cuda")
+    sc = torch.full((T, 20), 5.0, device="cuda")
+    m.index_scores(q, w, cache, None, table, lens, cu, fmt="bf16", max_context=20, scores=sc)
+    want = m.index_scores(q[2:5].contiguous(), w[2:5], cache, None, table, lens, cu - 2, fmt="bf16", max_context=20, scores=sc[2:5].clone())
+    outside = [0, 1, 5, 6]
+    assert torch.equal(sc[2:5], want) and bool((sc[outside] == 5).all())
+    blocks, slots = torch.full((T, 4), 77, dtype=I32, device="cuda"), torch.full((T, 4), 78, dtype=I32, device="cuda")
+    m.index_select(sc, lens, 4, cu, block_table=table, page_size=ps, num_blocks=4, blocks=blocks, slots=slots)
+    b, s = m.index_select(sc[2:5], lens, 4, cu - 2, block_table=table, page_size=ps, num_blocks=4)
+    assert torch.equal(blocks[2:5], b) and torch.equal(slots[2:5], s)
+    assert bool((blocks[outside] == 77).all()) and bool((slots[outside] == 78).all())
+    kv, mq = torch.randn((4, ps, 576), generator=g, device="cuda").to(BF), torch.randn((T, 2, 576), generator=g, device="cuda").to(BF)
+    pages = torch.zeros((T, 1), dtype=I32, device="cuda")
+    o, l = m.selected_decode(mq, kv, table, lens, pages, cu, fmt="bf16", softmax_scale=0.1, return_lse=True)
+    p, k = m.selected_decode(mq[2:5].contiguous(), kv, table, lens, pages[2:5], cu - 2, fmt="bf16", softmax_scale=0.1, return_lse=True)
+    assert torch.equal(o[2:5], p) and torch.equal(l[2:5], k)
+    assert not o[outside].any() and bool(torch.isneginf(l[outside]).all())
+    dst = torch.full((9, 128), 3.0, device="cuda").to(BF)
+    m.index_gather(cache, None, table, cu, fmt="bf16", num_tokens=9, dst=dst)
+    assert torch.equal(dst[2:5], torch.stack([cache[2, 0], cache[2, 1], cache[1, 0]]))
+    assert bool((dst[:2] == 3).all() and (dst[5:] == 3).all())
+    assert m.read_device_errors() == 0
