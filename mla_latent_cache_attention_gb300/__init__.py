@@ -701,7 +701,8 @@ def index_q_cache_insert(q, k, weights, index_cache, index_scales, slot_mapping,
 
 def index_gather(index_cache, index_scales, block_table, cu_seq_lens, seq_starts=None, *, fmt, num_tokens, dst=None):
     """Cached index keys as bf16 [num_tokens, 128]: rows cu_seq_lens[b] .. cu_seq_lens[b+1]-1 hold
-    request b's positions seq_starts[b] + i."""
+    request b's positions seq_starts[b] + i.  Rows of no request are not written: a dst that is not handed
+    in has there what the allocator left."""
     fmt = _index_format(fmt)
     done = (_marshal or _plain()).gather(index_cache, index_scales, block_table, cu_seq_lens, seq_starts, fmt, num_tokens, dst)
     if done is not None:
@@ -733,7 +734,7 @@ def index_scores(q, weights, index_cache, index_scales, block_table, seq_lens, c
     """Scores sum_h weights[t, h] * relu(q[t, h] . k[j]) of every visible token (block_tokens = 1), or
     their maximum over blocks of block_tokens.  q [T, Hi, 128] (bf16, or uint8 E4M3 codes with their
     scales in the weights).  Returns scores fp32 [T, >= ceil(max_context / block_tokens)]; only the
-    columns of visible blocks are written."""
+    columns of visible blocks are written, and no row outside every request."""
     fmt = _index_format(fmt)
     done = (_marshal or _plain()).scores(q, weights, index_cache, index_scales, block_table, seq_lens, cu_q_lens, fmt, block_tokens,
                                          max_context, scores)
@@ -769,7 +770,9 @@ def index_select(scores, seq_lens, topk, cu_q_lens=None, *, block_tokens=1, firs
     """The topk best-scored blocks of every row, ascending, -1 after them; ties go to the lowest index,
     -inf and NaN are never taken, the first `first` and last `last` visible blocks always.  With a
     block_table (and page_size, num_blocks) also the cache slots of their visible tokens, for
-    sparse_fwd.  Returns (blocks int32 [T, topk], slots int32 [T, topk * block_tokens] or None)."""
+    sparse_fwd.  Returns (blocks int32 [T, topk], slots int32 [T, topk * block_tokens] or None).  Rows outside
+    every request are not written: for a padded batch whose slots go to sparse_fwd hand in slots filled
+    with -1."""
     done = (_marshal or _plain()).select(scores, seq_lens, topk, cu_q_lens, block_tokens, first, last, block_table, page_size,
                                          num_blocks, blocks, slots)
     if done is not None:

@@ -765,9 +765,9 @@ extern "C" int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const
 // four splits instead of two; 32 pages (fp8_ds_mla, 128 rows, 96 heads) 412 -> 315 us with one instead of four.
 //
 // Where the last of several waves is nearly empty, its rows become a launch of their own, split over all
-// the SMs, if the estimate with 4 us for that launch is 3 % less: the fp8_ds_mla case above 314 -> 297 us (126 rows and
-// 2), 64 rows of 128 heads 215 -> 211; bf16, 160 rows of 64 heads, 32 pages, 276 -> 217, 200 of 16 heads, 16 pages, 101 -> 86;
-// fp8, 160 rows of 64 heads, 16 pages, 74 -> 62.
+// the SMs, if the estimate with 4 us for that launch is 3 % less: the fp8_ds_mla case above 315 -> 293 us (126 rows and
+// 2), 64 rows of 128 heads 216 -> 208; bf16, 160 rows of 64 heads, 32 pages, 276 -> 217, 200 of 16 heads, 16 pages, 101 -> 86;
+// fp8, 160 rows of 64 heads, 16 pages, 75 -> 62.
 namespace {
 
 // What the estimate of a selected decode depends on beside its rows.

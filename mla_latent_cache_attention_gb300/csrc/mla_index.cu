@@ -281,7 +281,8 @@ __global__ void __launch_bounds__(128) mla_index_gather_kernel(const IndexGather
 // (Before, every CTA read the others' lists and cut the whole: 20.3 -> 17.0 us for the 32 rows below.)
 //
 // Measured (GB300): 4096 rows of up to 65536 scores, topk 2048: 271 us, 4.0 TB/s (1.07 GB read once;
-// a row's sample waits for its 512 sectors behind the other rows' streams);
+// a row's sample waits for its 512 sectors behind the other rows' streams), 313 us with their slots (divisions and
+// two dependent loads for each of 8 million);
 // 32 rows of up to 131072 with their slots: 17 us; 128 rows of up to 512 blocks, topk 32: 7.7 us.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
