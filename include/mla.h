@@ -4,12 +4,17 @@
  *
  * A cache entry is [kv_c_normed (512) | k_pe (64)], one "head" shared by all query heads
  * (MQA, num_kv_heads = 1).  Queries are absorbed to [ql_nope (512) | q_pe (64)]; the value
- * is the first 512 values of the same entry.  Three entry formats:
+ * is the first 512 values of the same entry.  Four entry formats:
  *
  *   MLA_CACHE_BF16        576 bf16 values, 1152 bytes.
  *   MLA_CACHE_FP8         576 E4M3 values, 576 bytes, one per-tensor scale (k_scale).
  *   MLA_CACHE_FP8_DS_MLA  656-byte record: 512 E4M3 | 4 fp32 scales, one per 128-wide
  *                         tile of the 512 | 64 bf16 rope values ("self-scaling").
+ *   MLA_CACHE_MXFP4       400-byte record: 512 E2M1 codes (256 bytes, value 2i in the low half of
+ *                         byte i) | 16 E8M0 scales, one per 32-wide group of the 512 (a byte
+ *                         each, 2^(byte - 127); 255: the group is NaN) | 64 bf16 rope values
+ *                         ("self-scaling").  Served by the decode and prefill epilogues of the
+ *                         bf16 cache, mla_paged_decode, mla_selected_decode and mla_gather_context.
  *
  * Conventions for every entry point:
  *   - Pointers marked "device" are device memory owned by the caller; the library never
@@ -46,7 +51,8 @@ extern "C" {
 typedef enum {
   MLA_CACHE_BF16 = 0,
   MLA_CACHE_FP8 = 1,
-  MLA_CACHE_FP8_DS_MLA = 2
+  MLA_CACHE_FP8_DS_MLA = 2,
+  MLA_CACHE_MXFP4 = 3
 } mla_cache_format;
 
 #define MLA_OK 0
@@ -93,8 +99,8 @@ MLA_API void mla_profile_attention_events(cudaEvent_t start, cudaEvent_t stop);
  *   q_pe         device bf16 [B, H, 64], strides (qp_s0, qp_s1).
  *   kv_c_normed  device bf16 [B, 512], row stride kv_s0.
  *   k_pe         device bf16 [B, 64] (or [B, 1, 64]), row stride kp_s0.
- *   mqa_q        device out, contiguous [B, H, 576]: bf16 for MLA_CACHE_BF16 and
- *                MLA_CACHE_FP8_DS_MLA; E4M3 bytes for MLA_CACHE_FP8, where every element is
+ *   mqa_q        device out, contiguous [B, H, 576]: bf16 for MLA_CACHE_BF16,
+ *                MLA_CACHE_FP8_DS_MLA and MLA_CACHE_MXFP4; E4M3 bytes for MLA_CACHE_FP8, where every element is
  *                e4m3_sat(x * q_scale_inv).
  *   kv_cache     device cache: num_blocks blocks at block_stride_bytes, block_size entries
  *                each at entry_stride_bytes (>= the format's entry size).  Entry of slot s:
@@ -103,7 +109,12 @@ MLA_API void mla_profile_attention_events(cudaEvent_t start, cudaEvent_t stop);
  *                  FP8:    e4m3_sat(x * cache_scale_inv) for all 576 values;
  *                  DS_MLA: per 128-tile scale s = 2^k, k the least integer with
  *                          amax <= 448 * 2^k (s = 1 for an all-zero tile, k >= -126),
- *                          codes e4m3(x / s), scales as fp32, rope as bf16.
+ *                          codes e4m3(x / s), scales as fp32, rope as bf16;
+ *                  MXFP4:  per 32-group scale s = 2^k, k = max(k_min, K - 14, -126) with k_min the
+ *                          least integer with amax <= 6 * 2^k_min and K the largest k_min of the
+ *                          record's groups; codes e2m1(x / s) (to nearest, ties to even), scales
+ *                          as bytes k + 127, rope as bf16.  A group that holds an infinity or a
+ *                          NaN is stored as byte 255 with codes 0 and read as NaN.
  *   slot_mapping device int64 [B]; a negative slot skips that token's insert (the query is
  *                still written).
  *   q_scale_inv, cache_scale_inv  device fp32 scalars; required for MLA_CACHE_FP8, must be
@@ -113,7 +124,7 @@ MLA_API void mla_profile_attention_events(cudaEvent_t start, cudaEvent_t stop);
  *                GPT-J style on pairs (2i, 2i+1): y0 = fma(x0, c, -(x1*s)),
  *                y1 = fma(x1, c, x0*s) in fp32, applied to q_pe and k_pe before storing.
  * Errors: MLA_ERR_INVALID for NULL tensors, bad strides, mismatched scale / RoPE arguments,
- * misaligned pointers (bf16 tensors 2-byte aligned; bf16 / fp8_ds_mla cache entries
+ * misaligned pointers (bf16 tensors 2-byte aligned; bf16 / fp8_ds_mla / mxfp4 cache entries
  * 4-byte aligned).
  */
 MLA_API int mla_q_concat_cache_insert(const void* ql_nope, int64_t ql_s0, int64_t ql_s1,
@@ -128,7 +139,7 @@ MLA_API int mla_q_concat_cache_insert(const void* ql_nope, int64_t ql_s0, int64_
                               int32_t H, cudaStream_t stream);
 
 /*
- * Prefill epilogue for the bf16 and fp8_ds_mla caches: full per-head key, query RoPE in place
+ * Prefill epilogue for the bf16, fp8_ds_mla and mxfp4 caches: full per-head key, query RoPE in place
  * and latent insert, in one launch.
  * Follows: "vllm.models.kimi_k3.nvidia.ops.fused_mla_key_concat_kv_cache",
  * fused_mla_key_concat_kv_cache_insert (bf16 cache) and fused_mla_key_concat_ds_mla_insert
@@ -141,7 +152,7 @@ MLA_API int mla_q_concat_cache_insert(const void* ql_nope, int64_t ql_s0, int64_
  *   kv_c_normed  device bf16 [Tp, 512], row stride kv_s0.
  *   k_out        device out bf16 [Tp, H, dn + 64] contiguous: [k_nope[t, h] | rope(k_pe[t])]
  *                (the rotated k_pe of a token is shared by all its heads).
- *   kv_cache, fmt  MLA_CACHE_BF16 or MLA_CACHE_FP8_DS_MLA cache, geometry as in
+ *   kv_cache, fmt  MLA_CACHE_BF16, MLA_CACHE_FP8_DS_MLA or MLA_CACHE_MXFP4 cache, geometry as in
  *                mla_q_concat_cache_insert; token t's latent [kv_c_normed | rope(k_pe)] is
  *                written at slot_mapping[t] in the same format and rounding as there (a
  *                negative slot skips it; a slot whose block is out of range is skipped and
@@ -149,7 +160,7 @@ MLA_API int mla_q_concat_cache_insert(const void* ql_nope, int64_t ql_s0, int64_
  *   positions / cos_sin_cache / max_position  as in mla_q_concat_cache_insert (both NULL: no
  *                RoPE).  RoPE pairs are (2i, 2i+1) of the 64 rope values.
  * Errors: MLA_ERR_INVALID for NULL tensors, overlapping strides, misaligned (odd) bf16
- * pointers, a cache format other than the two above; MLA_ERR_UNSUPPORTED for dn not a positive
+ * pointers, a cache format other than the three above; MLA_ERR_UNSUPPORTED for dn not a positive
  * multiple of 8.
  */
 MLA_API int mla_key_concat_cache_insert(void* q, int64_t q_s0, int64_t q_s1, const void* k_nope, int64_t kn_s0,
@@ -268,7 +279,7 @@ MLA_API size_t mla_paged_decode_workspace_size(int32_t B, int32_t q_len, int32_t
  * bmm2_scale = k_scale for plain fp8) and pad_requests (length 0 -> zero output).
  *
  *   q            device [B * q_len, H, 576], strides (q_s0, q_s1) in elements; bf16 for the
- *                BF16 and DS_MLA caches, E4M3 bytes (raw codes, scale q_scale) for FP8.
+ *                BF16, DS_MLA and MXFP4 caches, E4M3 bytes (raw codes, scale q_scale) for FP8.
  *                Rows are grouped by request: row b*q_len + i is request b's query i.
  *   kv_cache     device, num_blocks blocks at block_stride_bytes, block_size entries each at
  *                entry_stride_bytes (multiple of 16, >= entry size).
@@ -277,9 +288,9 @@ MLA_API size_t mla_paged_decode_workspace_size(int32_t B, int32_t q_len, int32_t
  *                q_len new tokens included); query row i sees positions 0 .. L - q_len + i.
  *                0 <= seq_lens[b]; lengths beyond max_context are served but unbalanced.
  *   max_context  upper bound of seq_lens used to fix the split count (> 0).
- *   softmax_scale, q_scale, k_scale  logits = softmax_scale * q.k (BF16, DS_MLA) or
+ *   softmax_scale, q_scale, k_scale  logits = softmax_scale * q.k (BF16, DS_MLA, MXFP4) or
  *                softmax_scale * q_scale * k_scale * q8.k8 (FP8, raw codes), FP8 output
- *                multiplied by k_scale; q_scale / k_scale are ignored for BF16 and DS_MLA.
+ *                multiplied by k_scale; q_scale / k_scale are ignored for the other caches.
  *   out          device bf16 [B * q_len, H, >= 512], strides (o_s0, o_s1).
  *   lse          device fp32 [B * q_len, H] contiguous, natural log; NULL to skip.
  *   workspace    device scratch of >= mla_paged_decode_workspace_size(...) bytes, 256-byte
@@ -343,9 +354,10 @@ MLA_API int mla_paged_decode_noalloc(const void* q, int64_t q_s0, int64_t q_s1, 
  *                position seq_starts[b] + i of request b.
  *   num_tokens   rows of dst; rows at or past cu_seq_lens[batch] are not written.
  *   out_kind     MLA_GATHER_BF16: dst rows of 576 bf16 values -- bf16 entries as stored; plain
- *                fp8 entries e4m3 * scale; fp8_ds_mla codes e4m3 * tile scale and the bf16 rope;
- *                every product in fp32, rounded once to bf16 (round to nearest even).
- *                MLA_GATHER_RAW: dst rows of the entry bytes as stored (1152 / 576 / 656).
+ *                fp8 entries e4m3 * scale; fp8_ds_mla codes e4m3 * tile scale and the bf16 rope,
+ *                mxfp4 codes e2m1 * group scale and the bf16 rope; every product in fp32,
+ *                rounded once to bf16 (round to nearest even).
+ *                MLA_GATHER_RAW: dst rows of the entry bytes as stored (1152 / 576 / 656 / 400).
  *   scale        the plain fp8 cache's dequantisation scale (k_scale); unused otherwise.
  *   dst          device out, rows dst_row_stride_bytes apart.
  * A row whose block id is out of range is written as zeros and sets MLA_DEVERR_BLOCK.

@@ -46,9 +46,9 @@ import torch
 
 from . import build as _build
 
-CACHE_BF16, CACHE_FP8, CACHE_FP8_DS_MLA = 0, 1, 2
-ENTRY_BYTES = {CACHE_BF16: 1152, CACHE_FP8: 576, CACHE_FP8_DS_MLA: 656}
-_FMT_NAMES = {"bf16": CACHE_BF16, "auto": CACHE_BF16, "fp8": CACHE_FP8, "fp8_ds_mla": CACHE_FP8_DS_MLA}
+CACHE_BF16, CACHE_FP8, CACHE_FP8_DS_MLA, CACHE_MXFP4 = 0, 1, 2, 3
+ENTRY_BYTES = {CACHE_BF16: 1152, CACHE_FP8: 576, CACHE_FP8_DS_MLA: 656, CACHE_MXFP4: 400}
+_FMT_NAMES = {"bf16": CACHE_BF16, "auto": CACHE_BF16, "fp8": CACHE_FP8, "fp8_ds_mla": CACHE_FP8_DS_MLA, "mxfp4": CACHE_MXFP4}
 
 _lib = None
 
@@ -532,7 +532,7 @@ def merge_attn_states(prefix_output, prefix_lse, suffix_output, suffix_lse, *, o
 _BF16, _F32, _I32, _I64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
 _INDEX_TYPES = {CACHE_BF16: _BF16, CACHE_FP8: _BYTE_TYPES}
 _KV_TYPES = _BYTE_TYPES + _BF16
-_KV_BYTES = {CACHE_BF16: 1152, CACHE_FP8: 576, CACHE_FP8_DS_MLA: 656}
+_KV_BYTES = ENTRY_BYTES
 _current_device = torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 

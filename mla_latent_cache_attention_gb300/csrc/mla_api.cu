@@ -13,6 +13,7 @@
 #include "mla_host.h"
 #include "mla_internal.h"
 #include "mla_ds.cuh"
+#include "mla_fp4.cuh"
 #include "mla_paged_tma.cuh"
 
 namespace mla {
@@ -72,7 +73,11 @@ int dev_info(DevInfo** out) {
 namespace {
 
 int entry_bytes(mla_cache_format f) {
-  return f == MLA_CACHE_BF16 ? 1152 : f == MLA_CACHE_FP8 ? 576 : 656;
+  return f == MLA_CACHE_BF16 ? 1152 : f == MLA_CACHE_FP8 ? 576 : f == MLA_CACHE_FP8_DS_MLA ? 656 : kFp4Entry;
+}
+
+bool known_format(int f) {
+  return f == MLA_CACHE_BF16 || f == MLA_CACHE_FP8 || f == MLA_CACHE_FP8_DS_MLA || f == MLA_CACHE_MXFP4;
 }
 
 // Split-K plan of the paged decode.  The split count depends on the number of (request,
@@ -202,6 +207,12 @@ struct ColPlan {
   int nq, G, box_h, box_q;
 };
 bool plan_columns(int fmt, int H, int q_len, ColPlan* cp) {
+  if (fmt == MLA_CACHE_MXFP4) {      // 16 or 32 consecutive columns of any shape: its query is read without a box
+    const int64_t cols = static_cast<int64_t>(H) * q_len;
+    const int nq = cols <= 16 ? 16 : 32;
+    *cp = ColPlan{nq, static_cast<int>((cols + nq - 1) / nq), 0, 0};
+    return true;
+  }
   const int nqmax = fmt == MLA_CACHE_BF16 ? 32 : 64;
   const int cols = H * q_len;
   if (cols <= nqmax) {
@@ -268,7 +279,7 @@ extern "C" int mla_q_concat_cache_insert(const void* ql_nope, int64_t ql_s0, int
                                          const int64_t* positions, const float* cos_sin_cache,
                                          int64_t max_position, int32_t B, int32_t H,
                                          cudaStream_t stream) {
-  if (fmt != MLA_CACHE_BF16 && fmt != MLA_CACHE_FP8 && fmt != MLA_CACHE_FP8_DS_MLA)
+  if (!known_format(fmt))
     return fail(MLA_ERR_INVALID, "unknown cache format %d", static_cast<int>(fmt));
   if (B < 0 || H < 1) return fail(MLA_ERR_INVALID, "bad shape B=%d H=%d", B, H);
   if (B == 0) return ok();
@@ -283,7 +294,7 @@ extern "C" int mla_q_concat_cache_insert(const void* ql_nope, int64_t ql_s0, int
   if (entry_stride_bytes < entry_bytes(fmt) || block_stride_bytes < entry_stride_bytes * block_size)
     return fail(MLA_ERR_INVALID, "cache strides smaller than the entries");
   if (fmt != MLA_CACHE_FP8 && (entry_stride_bytes % 4 || block_stride_bytes % 4 || !aligned(kv_cache, 4)))
-    return fail(MLA_ERR_INVALID, "bf16 / fp8_ds_mla cache entries must be 4-byte aligned");
+    return fail(MLA_ERR_INVALID, "bf16 / fp8_ds_mla / mxfp4 cache entries must be 4-byte aligned");
   if (fmt == MLA_CACHE_FP8) {
     if (!q_scale_inv || !cache_scale_inv)
       return fail(MLA_ERR_INVALID, "the fp8 cache needs q_scale_inv and cache_scale_inv");
@@ -348,7 +359,7 @@ static int prefill_common_checks(const void* q, int64_t q_s0, int64_t q_s1, cons
       block_stride_bytes < entry_stride_bytes * block_size)
     return fail(MLA_ERR_INVALID, "cache strides smaller than the entries");
   if (fmt != MLA_CACHE_FP8 && (entry_stride_bytes % 4 || block_stride_bytes % 4 || !aligned(kv_cache, 4)))
-    return fail(MLA_ERR_INVALID, "bf16 / fp8_ds_mla cache entries must be 4-byte aligned");
+    return fail(MLA_ERR_INVALID, "bf16 / fp8_ds_mla / mxfp4 cache entries must be 4-byte aligned");
   if ((positions == nullptr) != (cos_sin_cache == nullptr))
     return fail(MLA_ERR_INVALID, "positions and cos_sin_cache must be given together");
   if (positions && max_position < 1) return fail(MLA_ERR_INVALID, "max_position must be >= 1");
@@ -362,8 +373,8 @@ extern "C" int mla_key_concat_cache_insert(void* q, int64_t q_s0, int64_t q_s1, 
                                            int32_t block_size, const int64_t* slot_mapping, const int64_t* positions,
                                            const float* cos_sin_cache, int64_t max_position, int32_t Tp, int32_t H,
                                            int32_t dn, cudaStream_t stream) {
-  if (fmt != MLA_CACHE_BF16 && fmt != MLA_CACHE_FP8_DS_MLA)
-    return fail(MLA_ERR_INVALID, "the key-concat epilogue writes a bf16 or fp8_ds_mla cache (format %d)",
+  if (!known_format(fmt) || fmt == MLA_CACHE_FP8)
+    return fail(MLA_ERR_INVALID, "the key-concat epilogue writes a bf16, fp8_ds_mla or mxfp4 cache (format %d)",
                 static_cast<int>(fmt));
   if (Tp < 0 || H < 1) return fail(MLA_ERR_INVALID, "bad shape Tp=%d H=%d", Tp, H);
   if (Tp == 0) return ok();
@@ -717,7 +728,7 @@ int mla::check_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const voi
                             const int32_t* block_table, int64_t bt_stride, const int32_t* seq_lens, int32_t B,
                             int32_t q_len, int32_t H, int32_t max_context, const void* out, int64_t o_s0, int64_t o_s1,
                             const float* lse) {
-  if (fmt != MLA_CACHE_BF16 && fmt != MLA_CACHE_FP8 && fmt != MLA_CACHE_FP8_DS_MLA)
+  if (!known_format(fmt))
     return fail(MLA_ERR_INVALID, "unknown cache format %d", fmt);
   if (B < 0 || q_len < 1 || H < 1) return fail(MLA_ERR_INVALID, "bad shape B=%d q_len=%d H=%d", B, q_len, H);
   if (H > 128) return fail(MLA_ERR_UNSUPPORTED, "H must be <= 128, got %d", H);
@@ -936,7 +947,7 @@ int mla::run_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void*
     }
     return ok();
   }
-  const bool tma_fmt = fmt != MLA_CACHE_FP8_DS_MLA;
+  const bool tma_fmt = fmt == MLA_CACHE_BF16 || fmt == MLA_CACHE_FP8;
   // keys per tile of the page kernel (a template choice; 128 for both formats, measured
   // faster than 64-key tiles for bf16 despite the deeper ring those allow)
   const int tma_rows_p = tma_rows_for(block_size, 128);
@@ -998,6 +1009,49 @@ int mla::run_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void*
     prof_begin(stream);
     e = fmt == MLA_CACHE_BF16 ? launch_paged_tma_bf16(cp.nq, p, &tkv, &tq, grid, stream)
                               : launch_paged_tma_fp8(cp.nq, p, &tkv, &tq, grid, stream);
+    prof_end(stream);
+  } else if (fmt == MLA_CACHE_MXFP4) {
+    plan_columns(MLA_CACHE_MXFP4, H, q_len, &cp);
+    const int64_t items = static_cast<int64_t>(sp.n_splits) * B * cp.G;
+    if (items >= (int64_t(1) << 31) - (1 << 20)) return fail(MLA_ERR_UNSUPPORTED, "too many work items");
+    if (max_context >= (1 << 30)) return fail(MLA_ERR_UNSUPPORTED, "max_context must be below 2^30");
+    Fp4Params p{};
+    p.q = static_cast<const uint8_t*>(q);
+    p.q_s0b = q_s0 * 2;
+    p.q_s1b = q_s1 * 2;
+    p.kv = static_cast<const uint8_t*>(kv_cache);
+    p.blk_stride = block_stride_bytes;
+    p.ent_stride = entry_stride_bytes;
+    p.H = H;
+    p.q_len = q_len;
+    p.B = B;
+    p.G = cp.G;
+    p.cols = H * q_len;
+    p.block_table = block_table;
+    p.bt_stride = bt_stride;
+    p.seq_lens = seq_lens;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.chunk = static_cast<int>(sp.chunk);
+    p.n_splits = sp.n_splits;
+    p.n_items = static_cast<int>(items);
+    p.n_rows = static_cast<int>(n_rows);
+    p.sig2 = softmax_scale * 1.4426950408889634f;
+    p.out = static_cast<uint8_t*>(out);
+    p.o_s0b = o_s0 * 2;
+    p.o_s1b = o_s1 * 2;
+    p.lse = lse;
+    p.part_o = part_o;
+    p.part_lse = part_lse;
+    p.sched = sched;
+    p.err = d->err;
+    p.wait_us = g_stall_next_us;
+    p.stall = g_stall_next_us > 0 ? 1 : 0;
+    g_stall_next_us = 0;
+    if (sched && !sched_ready && launch_sched_reset(sched, stream) != cudaSuccess)
+      return fail(MLA_ERR_CUDA, "scheduler reset failed: %s", cudaGetErrorString(cudaGetLastError()));
+    prof_begin(stream);
+    e = launch_fp4_paged(cp.nq, p, grid_for(items, d->sms), stream);
     prof_end(stream);
   } else {
     const int64_t items = n_rows * n_hgroups * sp.n_splits;
@@ -1066,7 +1120,7 @@ extern "C" int mla_gather_dequant(const void* kv_cache, mla_cache_format fmt, in
                                   int64_t block_stride_bytes, int64_t entry_stride_bytes,
                                   int32_t block_size, const int64_t* slots, int64_t n, float* out,
                                   cudaStream_t stream) {
-  if (fmt != MLA_CACHE_BF16 && fmt != MLA_CACHE_FP8 && fmt != MLA_CACHE_FP8_DS_MLA)
+  if (!known_format(fmt))
     return fail(MLA_ERR_INVALID, "unknown cache format %d", static_cast<int>(fmt));
   if (n < 0) return fail(MLA_ERR_INVALID, "n must be >= 0");
   if (n == 0) return ok();
@@ -1075,7 +1129,7 @@ extern "C" int mla_gather_dequant(const void* kv_cache, mla_cache_format fmt, in
       block_stride_bytes < entry_stride_bytes * block_size)
     return fail(MLA_ERR_INVALID, "bad cache geometry");
   if (fmt != MLA_CACHE_FP8 && (entry_stride_bytes % 4 || block_stride_bytes % 4 || !aligned(kv_cache, 4)))
-    return fail(MLA_ERR_INVALID, "bf16 / fp8_ds_mla entries must be 4-byte aligned");
+    return fail(MLA_ERR_INVALID, "bf16 / fp8_ds_mla / mxfp4 entries must be 4-byte aligned");
   if (n > (int64_t(1) << 33)) return fail(MLA_ERR_UNSUPPORTED, "n too large");
   DevInfo* d = nullptr;
   if (int rc = dev_info(&d)) return rc;
@@ -1100,7 +1154,7 @@ extern "C" int mla_gather_context(const void* kv_cache, mla_cache_format fmt, in
                                   const int32_t* block_table, int64_t bt_stride, const int32_t* cu_seq_lens,
                                   const int32_t* seq_starts, int32_t batch, int64_t num_tokens, int32_t out_kind,
                                   float scale, void* dst, int64_t dst_row_stride_bytes, cudaStream_t stream) {
-  if (fmt != MLA_CACHE_BF16 && fmt != MLA_CACHE_FP8 && fmt != MLA_CACHE_FP8_DS_MLA)
+  if (!known_format(fmt))
     return fail(MLA_ERR_INVALID, "unknown cache format %d", static_cast<int>(fmt));
   if (out_kind != MLA_GATHER_BF16 && out_kind != MLA_GATHER_RAW)
     return fail(MLA_ERR_INVALID, "unknown gather output kind %d", out_kind);
@@ -1114,8 +1168,9 @@ extern "C" int mla_gather_context(const void* kv_cache, mla_cache_format fmt, in
   if (dst_row_stride_bytes < row_bytes) return fail(MLA_ERR_INVALID, "dst rows overlap");
   if (out_kind == MLA_GATHER_BF16 && (!aligned(dst, 2) || dst_row_stride_bytes % 2))
     return fail(MLA_ERR_INVALID, "bf16 dst rows must be 2-byte aligned");
-  if (fmt == MLA_CACHE_FP8_DS_MLA && (entry_stride_bytes % 4 || block_stride_bytes % 4 || !aligned(kv_cache, 4)))
-    return fail(MLA_ERR_INVALID, "fp8_ds_mla entries must be 4-byte aligned");
+  if ((fmt == MLA_CACHE_FP8_DS_MLA || fmt == MLA_CACHE_MXFP4) &&
+      (entry_stride_bytes % 4 || block_stride_bytes % 4 || !aligned(kv_cache, 4)))
+    return fail(MLA_ERR_INVALID, "fp8_ds_mla / mxfp4 entries must be 4-byte aligned");
   if (fmt == MLA_CACHE_BF16 && (entry_stride_bytes % 2 || block_stride_bytes % 2 || !aligned(kv_cache, 2)))
     return fail(MLA_ERR_INVALID, "bf16 entries must be 2-byte aligned");
   if (num_tokens >= (int64_t(1) << 33)) return fail(MLA_ERR_UNSUPPORTED, "num_tokens too large");

@@ -185,6 +185,7 @@ cudaError_t launch_attn_paged_ds(const AttnParams& p, int grid, cudaStream_t str
 // qbox_h x qbox_q).
 struct PagedParams;
 struct DsParams;
+struct Fp4Params;
 // fp8_ds_mla attention: sparse records gathered by vector loads; paged records by TMA boxes
 // (`tkv` as above over the 656-byte record, `tsc` the same geometry unswizzled with 16-byte
 // boxes for the scales).
@@ -194,5 +195,8 @@ cudaError_t launch_paged_tma_bf16(int nq, const PagedParams& p, const void* tkv,
                                   cudaStream_t stream);
 cudaError_t launch_paged_tma_fp8(int nq, const PagedParams& p, const void* tkv, const void* tq, int grid,
                                  cudaStream_t stream);
+
+// mxfp4 paged decode, nq (16 or 32) query columns per item
+cudaError_t launch_fp4_paged(int nq, const Fp4Params& p, int grid, cudaStream_t stream);
 
 }  // namespace mla

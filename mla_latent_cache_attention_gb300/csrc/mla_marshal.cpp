@@ -385,7 +385,7 @@ PyObject* py_selected(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !read(a[1], dev, 3, &kv, g_u8, g_i8, fmt == MLA_CACHE_BF16 ? g_bf16 : nullptr) || !read(a[4], dev, 2, &blk, g_i32))
     return not_plain();
   const int64_t T = q.size[0], H = q.size[1], topk = blk.size[1], es = kv.type == 2 ? 2 : 1;
-  const int64_t entry = fmt == MLA_CACHE_BF16 ? 1152 : fmt == MLA_CACHE_FP8 ? 576 : 656;
+  const int64_t entry = fmt == MLA_CACHE_BF16 ? 1152 : fmt == MLA_CACHE_FP8 ? 576 : fmt == MLA_CACHE_MXFP4 ? 400 : 656;
   if (H > INT32_MAX || topk > INT32_MAX || kv.size[1] > INT32_MAX || kv.size[2] * es < entry || q.size[2] != 576 || blk.size[0] != T ||
       !read_requests(a[3], a[5], T, dev, &r) || r.B == 0 || !read_table(a[2], r.B, dev, &tab))
     return not_plain();

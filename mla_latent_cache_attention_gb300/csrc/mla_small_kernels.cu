@@ -5,6 +5,7 @@
 //   * gather-and-dequantise of cache entries (a test aid with the kernels' addressing).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -51,9 +52,26 @@ __device__ __forceinline__ int ds_tile_exponent(float amax) {
   return k < -126 ? -126 : k;
 }
 
+// mxfp4: the values of the two codes of a byte (value 2i in the low half), and the scale of an exponent byte.
+__device__ __forceinline__ float2 fp4x2_to_float2(uint32_t byte) {
+  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ float e8m0_scale(uint32_t b) {
+  return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FC00000u : b << 23);
+}
+
+// The least k with amax <= 6 * 2^k from the fp32 bits of amax (6 * 2^k = 1.5 * 2^(k + 2)); for amax = 0 or
+// subnormal something below every k that counts.
+__device__ __forceinline__ int fp4_group_exponent(uint32_t amax) {
+  const int e = static_cast<int>(amax >> 23);
+  return e == 0 ? -1000 : e - 127 - 2 + ((amax & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+}
+
 // Write one cache entry (128 threads): [kv_c | rope(k_pe)] as bf16 (F = 0), as
 // e4m3_sat(x * cinv) (F = 1), or as a 656-byte fp8_ds_mla record (F = 2: per-128-tile scale
-// 2^k from ds_tile_exponent, codes e4m3(x / 2^k), rope bf16).  cs: the RoPE row or null.
+// 2^k from ds_tile_exponent, codes e4m3(x / 2^k), rope bf16), or as a 400-byte mxfp4 record (F = 3, see
+// include/mla.h; all 128 threads meet at a barrier).  cs: the RoPE row or null.
 template <int F>
 __device__ __forceinline__ void insert_latent(uint8_t* ent, const uint16_t* __restrict__ kc,
                                               const uint16_t* __restrict__ kr, const float* __restrict__ cs, float cinv,
@@ -68,8 +86,9 @@ __device__ __forceinline__ void insert_latent(uint8_t* ent, const uint16_t* __re
       ent[512 + 2 * tid] = e4m3_sat(y0 * cinv);
       ent[512 + 2 * tid + 1] = e4m3_sat(y1 * cinv);
     } else {
-      reinterpret_cast<uint16_t*>(ent + 528)[2 * tid] = bf16_bits(y0);
-      reinterpret_cast<uint16_t*>(ent + 528)[2 * tid + 1] = bf16_bits(y1);
+      constexpr int kRope = F == 2 ? 528 : 272;
+      reinterpret_cast<uint16_t*>(ent + kRope)[2 * tid] = bf16_bits(y0);
+      reinterpret_cast<uint16_t*>(ent + kRope)[2 * tid + 1] = bf16_bits(y1);
     }
   }
   // NoPE part: warp w owns the 128-wide tile w, 4 values per lane
@@ -83,6 +102,30 @@ __device__ __forceinline__ void insert_latent(uint8_t* ent, const uint16_t* __re
   } else if (F == 1) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) ent[128 * w + 4 * lane + i] = e4m3_sat(x[i] * cinv);
+  } else if (F == 3) {
+    // eight lanes a group; the record's largest exponent by way of shared memory.  Magnitudes compare as
+    // bits: an infinity or a NaN is larger than every number.
+    __shared__ int kmax[4];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    const bool finite = amax < 0x7F800000u;
+    int k = finite ? fp4_group_exponent(amax) : -1000;
+    int top = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 8));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+    if (lane == 0) kmax[w] = top;
+    __syncthreads();
+    k = max(k, max(max(max(kmax[0], kmax[1]), max(kmax[2], kmax[3])) - 14, -126));
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);   // 2^-k, exact
+    uint32_t c = 0;
+    if (finite) {
+      c = __nv_cvt_float2_to_fp4x2(make_float2(x[0] * inv, x[1] * inv), __NV_E2M1, cudaRoundNearest);
+      c |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(x[2] * inv, x[3] * inv), __NV_E2M1, cudaRoundNearest)) << 8;
+    }
+    reinterpret_cast<uint16_t*>(ent)[32 * w + lane] = static_cast<uint16_t>(c);
+    if ((lane & 7) == 0) ent[256 + 4 * w + (lane >> 3)] = static_cast<uint8_t>(finite ? k + 127 : 255);
   } else {
     float amax = 0.f;
 #pragma unroll
@@ -193,7 +236,8 @@ __global__ void __launch_bounds__(128) mla_epilogue_kernel(const EpiParams p) {
 // Prefill epilogues.  "vllm.models.kimi_k3.nvidia.ops.fused_mla_key_concat_kv_cache":
 //   F = 0 / 2  fused_mla_key_concat_kv_cache_insert / fused_mla_key_concat_ds_mla_insert:
 //              k_out[t, h] = [k_nope[t, h] | rope(k_pe[t])] (bf16), the last 64 values of
-//              q[t, h] rotated in place, the latent inserted into the bf16 / fp8_ds_mla cache;
+//              q[t, h] rotated in place, the latent inserted into the bf16 / fp8_ds_mla cache
+//              (F = 3: the same with the mxfp4 cache);
 //   F = 1      fused_mla_qkv_quant_kv_cache_fp8_insert: q / k / v quantised to E4M3 with their
 //              own scales (q rotated on the way, not in place), the latent into the plain fp8
 //              cache with the cache scale.
@@ -327,8 +371,10 @@ cudaError_t launch_prefill_epilogue(int fmt, const PrefillEpiParams& p, int Tp, 
     mla_prefill_epilogue_kernel<0><<<grid, 128, 0, stream>>>(p);
   else if (fmt == 1)
     mla_prefill_epilogue_kernel<1><<<grid, 128, 0, stream>>>(p);
-  else
+  else if (fmt == 2)
     mla_prefill_epilogue_kernel<2><<<grid, 128, 0, stream>>>(p);
+  else
+    mla_prefill_epilogue_kernel<3><<<grid, 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -434,11 +480,14 @@ __global__ void mla_gather_kernel(const GatherParams p) {
       } else if (F == 1) {
         __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(ent[d]), __NV_E4M3);
         v = __half2float(__half(h));
+      } else if (F == 3 && d < 512) {
+        const float2 f = fp4x2_to_float2(ent[d >> 1]);
+        v = ((d & 1) ? f.y : f.x) * e8m0_scale(ent[256 + (d >> 5)]);
       } else if (d < 512) {
         __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(ent[d]), __NV_E4M3);
         v = __half2float(__half(h)) * reinterpret_cast<const float*>(ent + 512)[d >> 7];
       } else {
-        v = bf16_at(reinterpret_cast<const uint16_t*>(ent + 528) + (d - 512));
+        v = bf16_at(reinterpret_cast<const uint16_t*>(ent + (F == 2 ? 528 : 272)) + (d - 512));
       }
     }
     o[d] = v;
@@ -452,8 +501,10 @@ cudaError_t launch_epilogue(int fmt, const EpiParams& p, int B, cudaStream_t str
     mla_epilogue_kernel<0><<<grid, 128, 0, stream>>>(p);
   else if (fmt == 1)
     mla_epilogue_kernel<1><<<grid, 128, 0, stream>>>(p);
-  else
+  else if (fmt == 2)
     mla_epilogue_kernel<2><<<grid, 128, 0, stream>>>(p);
+  else
+    mla_epilogue_kernel<3><<<grid, 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -496,8 +547,10 @@ cudaError_t launch_gather(int fmt, const GatherParams& p, cudaStream_t stream) {
     mla_gather_kernel<0><<<grid, 128, 0, stream>>>(p);
   else if (fmt == 1)
     mla_gather_kernel<1><<<grid, 128, 0, stream>>>(p);
-  else
+  else if (fmt == 2)
     mla_gather_kernel<2><<<grid, 128, 0, stream>>>(p);
+  else
+    mla_gather_kernel<3><<<grid, 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -537,7 +590,7 @@ __global__ void __launch_bounds__(128) mla_gather_context_kernel(const GatherCtx
   const int b = lo;
   const int64_t pos = (p.starts ? p.starts[b] : 0) + (r - p.cu[b]);
   const int64_t blk = p.block_table[static_cast<int64_t>(b) * p.bt_stride + pos / p.block_size];
-  constexpr int kEntry = F == 0 ? 1152 : F == 1 ? 576 : 656;
+  constexpr int kEntry = F == 0 ? 1152 : F == 1 ? 576 : F == 2 ? 656 : 400;
   constexpr int kOut = KIND == 1 ? kEntry : 1152;
   uint8_t* dst = p.dst + r * p.dst_row;
   if (blk < 0 || blk >= p.num_blocks) {
@@ -556,6 +609,13 @@ __global__ void __launch_bounds__(128) mla_gather_context_kernel(const GatherCtx
         if (F == 1) {
           x = __half2float(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(ent[d]), __NV_E4M3)) * p.scale;
           o[d] = bf16_bits(x);
+        } else if (F == 3) {
+          if (d < 512) {
+            const float2 f = fp4x2_to_float2(ent[d >> 1]);
+            o[d] = bf16_bits(((d & 1) ? f.y : f.x) * e8m0_scale(ent[256 + (d >> 5)]));
+          } else {
+            o[d] = static_cast<uint16_t>(ent[272 + 2 * (d - 512)] | (ent[273 + 2 * (d - 512)] << 8));
+          }
         } else if (d < 512) {
           const float sj = *reinterpret_cast<const float*>(ent + 512 + 4 * (d >> 7));
           o[d] = bf16_bits(__half2float(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(ent[d]), __NV_E4M3)) * sj);
@@ -577,6 +637,19 @@ __global__ void __launch_bounds__(128) mla_gather_context_kernel(const GatherCtx
       out[2 * i] = o[0];
       out[2 * i + 1] = o[1];
     }
+  } else if (F == 3) {
+    // lane l: 16 codes of half a group -> 16 bf16 values
+    const float sj = e8m0_scale(__ldg(ent + 256 + (lane >> 1)));
+    const uint2 cw = __ldg(reinterpret_cast<const uint2*>(ent) + lane);
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = fp4x2_to_float2(((i < 4 ? cw.x : cw.y) >> (8 * (i & 3))) & 0xFFu);
+      r[i] = static_cast<uint32_t>(bf16_bits(f.x * sj)) | (static_cast<uint32_t>(bf16_bits(f.y * sj)) << 16);
+    }
+    out[2 * lane] = make_uint4(r[0], r[1], r[2], r[3]);
+    out[2 * lane + 1] = make_uint4(r[4], r[5], r[6], r[7]);
+    if (lane < 8) out[64 + lane] = __ldg(src + 17 + lane);     // rope bytes 272.. -> values 512..
   } else {
     uint4 o[2];
     const float sj = __ldg(reinterpret_cast<const float*>(ent + 512) + (lane >> 3));
@@ -592,11 +665,13 @@ cudaError_t launch_gather_context(int fmt, int kind, const GatherCtxParams& p, c
   if (kind == 1) {
     if (fmt == 0) mla_gather_context_kernel<0, 1><<<grid, 128, 0, stream>>>(p);
     else if (fmt == 1) mla_gather_context_kernel<1, 1><<<grid, 128, 0, stream>>>(p);
-    else mla_gather_context_kernel<2, 1><<<grid, 128, 0, stream>>>(p);
+    else if (fmt == 2) mla_gather_context_kernel<2, 1><<<grid, 128, 0, stream>>>(p);
+    else mla_gather_context_kernel<3, 1><<<grid, 128, 0, stream>>>(p);
   } else {
     if (fmt == 0) mla_gather_context_kernel<0, 0><<<grid, 128, 0, stream>>>(p);
     else if (fmt == 1) mla_gather_context_kernel<1, 0><<<grid, 128, 0, stream>>>(p);
-    else mla_gather_context_kernel<2, 0><<<grid, 128, 0, stream>>>(p);
+    else if (fmt == 2) mla_gather_context_kernel<2, 0><<<grid, 128, 0, stream>>>(p);
+    else mla_gather_context_kernel<3, 0><<<grid, 128, 0, stream>>>(p);
   }
   return cudaGetLastError();
 }
