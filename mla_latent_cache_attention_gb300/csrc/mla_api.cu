@@ -1015,13 +1015,14 @@ int mla::run_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void*
     const int64_t items = static_cast<int64_t>(sp.n_splits) * B * cp.G;
     if (items >= (int64_t(1) << 31) - (1 << 20)) return fail(MLA_ERR_UNSUPPORTED, "too many work items");
     if (max_context >= (1 << 30)) return fail(MLA_ERR_UNSUPPORTED, "max_context must be below 2^30");
+    if (block_stride_bytes >= (int64_t(1) << 32)) return fail(MLA_ERR_UNSUPPORTED, "mxfp4 blocks must be below 4 GB");
     Fp4Params p{};
     p.q = static_cast<const uint8_t*>(q);
     p.q_s0b = q_s0 * 2;
     p.q_s1b = q_s1 * 2;
     p.kv = static_cast<const uint8_t*>(kv_cache);
-    p.blk_stride = block_stride_bytes;
-    p.ent_stride = entry_stride_bytes;
+    p.blk_stride = static_cast<uint32_t>(block_stride_bytes);
+    p.ent_stride = static_cast<uint32_t>(entry_stride_bytes);
     p.H = H;
     p.q_len = q_len;
     p.B = B;
@@ -1030,8 +1031,9 @@ int mla::run_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void*
     p.block_table = block_table;
     p.bt_stride = bt_stride;
     p.seq_lens = seq_lens;
-    p.num_blocks = num_blocks;
+    p.num_blocks = static_cast<uint32_t>(num_blocks < (int64_t(1) << 31) ? num_blocks : int64_t(1) << 31);
     p.block_size = block_size;
+    p.bs_shift = (block_size & (block_size - 1)) == 0 ? 31 - __builtin_clz(static_cast<unsigned>(block_size)) : -1;
     p.chunk = static_cast<int>(sp.chunk);
     p.n_splits = sp.n_splits;
     p.n_items = static_cast<int>(items);
@@ -1051,6 +1053,8 @@ int mla::run_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void*
     if (sched && !sched_ready && launch_sched_reset(sched, stream) != cudaSuccess)
       return fail(MLA_ERR_CUDA, "scheduler reset failed: %s", cudaGetErrorString(cudaGetLastError()));
     prof_begin(stream);
+    p.two16 = 1u << 16;
+    p.two31 = 1u << 31;
     e = launch_fp4_paged(cp.nq, p, grid_for(items, d->sms), stream);
     prof_end(stream);
   } else {

@@ -28,3 +28,12 @@ cudaError_t launch_fp4_paged(int nq, const Fp4Params& p, int grid, cudaStream_t 
 }
 
 }  // namespace mla
+
+#ifdef MLA_TIMELINE
+extern "C" __attribute__((visibility("default"))) int mla_debug_timeline_fp4(void* events, void* counts) {
+  cudaMemcpyFromSymbol(events, mla::g_tl, sizeof(mla::g_tl));
+  cudaMemcpyFromSymbol(counts, mla::g_tl_n, sizeof(mla::g_tl_n));
+  const int zero[mla::kTlCtas][mla::kTlRoles] = {};
+  return cudaMemcpyToSymbol(mla::g_tl_n, zero, sizeof(zero)) == cudaSuccess ? 0 : -3;
+}
+#endif

@@ -12,7 +12,7 @@
 //   * One work item = one request x one group of NQ query columns (a column is a (query token, head) pair) x
 //     one split of its keys.  Tiles of 128 keys, two in shared memory: 4 x 16 KB of E4M3 and 16 KB of bf16 k_pe
 //     each, K-major with 128-byte swizzle, read by both products.
-//   * Eight loader warps take 16 keys of a tile each: 16-byte loads straight from the pages (a lane holds one
+//   * Sixteen loader warps take 8 keys of a tile each: 16-byte loads straight from the pages (a lane holds one
 //     group: 32 codes and their exponent) one tile ahead in registers, block ids two tiles ahead.  A group's
 //     exponent below K picks two words that hold the E4M3 bytes of the eight magnitudes at that scale; a byte
 //     permute turns four codes into four bytes.  That is 1.5 instructions a code, where the conversion
@@ -26,8 +26,8 @@
 //     stacked along N and added in the epilogue.  The reference m moves only when a logit passes it by kTau.
 //   * Roles hand over through mbarriers, each waited with a time limit.
 //
-// Warps: 0 scheduler, 1 QK issuer (TMEM owner), 2..5 softmax + query preparation + epilogue, 6 PV issuer,
-// 7..14 loaders.
+// Warps: 0 scheduler, 1 QK issuer (TMEM owner), 2 PV issuer, then four (NQ = 16) or eight softmax warps (which also
+// prepare the query and write the results), then 16 loaders.
 #pragma once
 #include "mla_ds.cuh"
 
@@ -40,13 +40,13 @@ struct Fp4Params {
   const uint8_t* q;               // bf16 [rows][H][>=576]
   int64_t q_s0b, q_s1b;
   const uint8_t* kv;
-  int64_t blk_stride, ent_stride;
+  uint32_t blk_stride, ent_stride;
   int H, q_len, B, G, cols;       // G groups of NQ columns of the q_len * H
   const int32_t* block_table;
   int64_t bt_stride;
   const int32_t* seq_lens;
-  int64_t num_blocks;
-  int block_size;
+  uint32_t num_blocks;
+  int block_size, bs_shift;       // bs_shift: log2 of it, or -1
   int chunk, n_splits, n_items, n_rows;
   float sig2;                     // softmax scale * log2(e)
   uint8_t* out;
@@ -57,13 +57,16 @@ struct Fp4Params {
   uint32_t* sched;
   uint32_t* err;
   int wait_us, stall;             // test aids, as in PagedParams
+  uint32_t two16, two31;          // 2^16, 2^31
 };
 
 template <int NQ_>
 struct Fp4Cfg {
   static_assert(NQ_ == 16 || NQ_ == 32, "columns per item");
   static constexpr int NQ = NQ_, NB = 5;
-  static constexpr int kLoadWarps = 8, kPvWarp = 6, kFirstLoad = 7;
+  static constexpr int NC = 16;                                   // columns of a softmax thread
+  static constexpr int kSW = 4 * (NQ / NC);                       // softmax warps: two column halves where NQ = 32
+  static constexpr int kLoadWarps = 16, kPvWarp = 2, kFirstSm = 4, kFirstLoad = kFirstSm + kSW;
   static constexpr int kThreads = 32 * (kFirstLoad + kLoadWarps);
   static constexpr int kRing = 0;                                 // 2 x 5 x 16 KB
   static constexpr int kQ = kRing + 2 * NB * kSlotBytes;          // 4 x (2 NQ rows x 128 B): hi rows, then lo rows
@@ -77,7 +80,8 @@ struct Fp4Cfg {
   static constexpr int kLut = kAlph + NQ * 4;                     // [16] x 8 B
   static constexpr int kItems = kLut + 16 * 8;
   static constexpr int kBar = kItems + kItemDepth * 32;
-  static constexpr int kNumBars = 2 + 2 + 2 + 2 + 4 + 2 * kItemDepth;
+  static constexpr int kParts = 2;                                // commits of a tile's PV
+  static constexpr int kNumBars = 2 * NB + 2 + 2 + 2 * kParts + 4 + 2 * kItemDepth;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kTotal = kMisc + 16;
   static constexpr int kAlloc = kTotal + 1024;
@@ -88,14 +92,18 @@ struct Fp4Cfg {
   static_assert(kTmemO + 8 * NQ <= kTmemCols, "TMEM budget");
 };
 
-// The E4M3 bytes of four codes (the low four nibbles of mag7 = w & 0x77777777 and sgn8 = w & 0x88888888): the
-// magnitudes picked from the eight bytes of lut, and the sign bits, which a permute of 0x80 in sign mode
-// turns into 0xFF (bit 6 of 0x80 is clear, of 0xFF set).
-__device__ __forceinline__ uint32_t fp4x4_to_e4m3(uint2 lut, uint32_t mag7, uint32_t sgn8) {
-  uint32_t m, s;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(m) : "r"(lut.x), "r"(lut.y), "r"(mag7));
-  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(s) : "r"(0x80u), "r"(sgn8));
-  return m | ((s << 1) & 0x80808080u);
+// The E4M3 bytes of eight codes: the magnitudes picked by permutes from the eight bytes of lut, with the codes as
+// selectors, the sign bits by permutes from 0x00 and 0x80.  Permutes, logic and shifts share a pipe of half rate, the
+// one that bounds the loaders, so the three right shifts are made by products (the high word of x 2^16 and x 2^31, whose
+// factors come as arguments: a constant would become the shift again).
+__device__ __forceinline__ uint2 fp4x8_to_e4m3(uint2 lut, uint32_t w, uint32_t two16, uint32_t two31) {
+  const uint32_t mag = w & 0x77777777u, sgn = __umulhi(w, two31) & 0x44444444u;
+  uint32_t m0, m1, s0, s1;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(m0) : "r"(lut.x), "r"(lut.y), "r"(mag));
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(m1) : "r"(lut.x), "r"(lut.y), "r"(__umulhi(mag, two16)));
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(s0) : "r"(0u), "r"(0x80u), "r"(sgn));
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(s1) : "r"(0u), "r"(0x80u), "r"(__umulhi(sgn, two16)));
+  return make_uint2(m0 | s0, m1 | s1);
 }
 
 template <int NQ>
@@ -103,7 +111,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
   using C = Fp4Cfg<NQ>;
   constexpr int NB = C::NB;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);      // (known to be shared: no generic accesses)
   uint8_t* ring = smem + C::kRing;
   uint8_t* qs = smem + C::kQ;
   uint8_t* qr = smem + C::kQRope;
@@ -117,32 +125,32 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
   uint2* lut = reinterpret_cast<uint2*>(smem + C::kLut);
   WorkItem* items = reinterpret_cast<WorkItem*>(smem + C::kItems);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar);
-  uint64_t* full = bars;                  // [2] the loader warps have written the tile
-  uint64_t* s_full = bars + 2;            // [2] QK done
-  uint64_t* s_free = bars + 4;            // [2] the softmax has read S
-  uint64_t* pv_done = bars + 6;           // [2]
-  uint64_t* p_full = bars + 8;            // P is written (one arrival per softmax warp)
-  uint64_t* q_full = bars + 9;
-  uint64_t* fin = bars + 10;
-  uint64_t* fin_pv = bars + 11;
-  uint64_t* item_full = bars + 12;
+  uint64_t* full = bars;                  // [2][NB] the loader warps have written the slot (k_pe and the scales first)
+  uint64_t* s_full = full + 2 * NB;       // [2] QK done
+  uint64_t* s_free = s_full + 2;          // [2] the softmax has read S
+  uint64_t* pv_part = s_free + 2;         // [2][kParts] PV of the value tiles done
+  uint64_t* p_full = pv_part + 2 * C::kParts;      // P is written (one arrival per softmax warp)
+  uint64_t* q_full = p_full + 1;
+  uint64_t* fin = p_full + 2;
+  uint64_t* fin_pv = p_full + 3;
+  uint64_t* item_full = p_full + 4;
   uint64_t* item_empty = item_full + kItemDepth;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMisc + 4);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  TL_DECL;
 
   // the split-K merge may be scheduled now; it waits for this grid to complete
   if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) {
-    if (lane < C::kNumBars) {
+    for (int i = lane; i < C::kNumBars; i += 32) {
       uint32_t count = 1;
-      if (lane < 2) count = C::kLoadWarps;
-      if (&bars[lane] == p_full) count = 4;                                  // the softmax warps
-      if (&bars[lane] >= item_empty) count = 3 + C::kLoadWarps;              // the roles
-      mbar_init(&bars[lane], count);
+      if (i < 2 * NB) count = C::kLoadWarps;
+      if (&bars[i] == p_full) count = C::kSW;                                // the softmax warps
+      if (&bars[i] >= item_empty) count = 3 + C::kLoadWarps;                 // the roles
+      mbar_init(&bars[i], count);
     }
-    static_assert(C::kNumBars <= 32, "one lane a barrier");
     if (lane == 0) {
       *abort_flag = 0;
       abort_flag[1] = p.wait_us;
@@ -153,7 +161,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 2 && lane < 16) {
+  if (warp == 3 && lane < 16) {
     // magnitudes 0, .5, 1, 1.5 | 2, 3, 4, 6 times 2^(6 - lane) in E4M3: exact down to 2^-9, zero below
     // (entry 15 is all zeros)
     uint32_t w[2] = {0u, 0u};
@@ -230,25 +238,37 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         for (int t = 0; t < it.ntiles && ok; ++t) {
           const int gt = g + t, h = gt & 1;
           if (gt >= 2 && !mbar_wait(&s_free[h], static_cast<uint32_t>((gt - 2) >> 1) & 1u, abort_flag)) ok = false;
-          if (ok && !mbar_wait(&full[h], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag)) ok = false;
           if (!ok) break;
-          tc_fence_after();
+          TL(1, 1);
           const uint32_t dS = tmem + h * C::kS;
-#pragma unroll 1
-          for (int b = 0; b < NB; ++b) {
-            const uint64_t aK = desc_add(dK0, static_cast<uint32_t>((h * NB + b) * (kSlotBytes >> 4)));
-            if (b < 4) {
-              const uint64_t bQ = desc_add(dQ0, static_cast<uint32_t>(b * (2 * NQ * 128 >> 4)));
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_f8_ss(dS, desc_add(aK, (kk * 32) >> 4), desc_add(bQ, (kk * 32) >> 4), kIdNope, (b | kk) ? 1u : 0u);
-            } else {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_f16_ss(dS + 2 * NQ, desc_add(aK, (kk * 32) >> 4), desc_add(dQr, (kk * 32) >> 4), kIdRope, kk > 0 ? 1u : 0u);
-            }
+          const uint32_t use = static_cast<uint32_t>(gt >> 1) & 1u;
+          // as the loaders finish the slots: k_pe and two code tiles, then the other two
+          if (!mbar_wait(&full[h * NB + 1], use, abort_flag)) {
+            ok = false;
+            break;
           }
+          tc_fence_after();
+          TL(1, 2);
+          {
+            const uint64_t aK = desc_add(dK0, static_cast<uint32_t>((h * NB + 4) * (kSlotBytes >> 4)));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ss(dS + 2 * NQ, desc_add(aK, (kk * 32) >> 4), desc_add(dQr, (kk * 32) >> 4), kIdRope, kk > 0 ? 1u : 0u);
+          }
+#pragma unroll 1
+          for (int b = 0; b < 4 && ok; ++b) {
+            if (b == 2) ok = mbar_wait(&full[h * NB + 3], use, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t aK = desc_add(dK0, static_cast<uint32_t>((h * NB + b) * (kSlotBytes >> 4)));
+            const uint64_t bQ = desc_add(dQ0, static_cast<uint32_t>(b * (2 * NQ * 128 >> 4)));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f8_ss(dS, desc_add(aK, (kk * 32) >> 4), desc_add(bQ, (kk * 32) >> 4), kIdNope, (b | kk) ? 1u : 0u);
+          }
+          if (!ok) break;
           mma_commit(&s_full[h]);
+          TL(1, 3);
         }
         g += it.ntiles;
       }
@@ -279,6 +299,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
             break;
           }
           tc_fence_after();
+          TL(2, 1);
           const uint32_t acc0 = t == 0 ? 0u : 1u;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -287,8 +308,9 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
             for (int kk = 0; kk < 4; ++kk)
               mma_f8_ss(tmem + C::kTmemO + 2 * NQ * j, desc_add(aV, (kk * 4096) >> 4), desc_add(dP0, (kk * NQ * 64) >> 4), kIdPv,
                         kk > 0 ? 1u : acc0);
+            if ((j + 1) % (4 / C::kParts) == 0) mma_commit(&pv_part[(gt & 1) * C::kParts + j / (4 / C::kParts)]);
           }
-          mma_commit(&pv_done[gt & 1]);
+          TL(2, 2);
         }
         g += it.ntiles;
       }
@@ -297,17 +319,20 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       mbar_wait(fin_pv, 0, no_abort);
     }
     __syncwarp();
+  } else if (warp == 3) {
+    // (warps 0..3 are the control roles; the softmax warps start at a multiple of four, their TMEM lane quadrant)
   } else if (warp >= C::kFirstLoad) {
     // ------------------------------------------------------------------ loaders
-    // Warp w owns keys 16 w .. 16 w + 15 of every tile.  Step i loads keys 2 i and 2 i + 1: lane = 8 j + 4 kb + u is
-    // group 4 j + u of key 2 i + kb, so that a quarter of the warp stores to one block's eight 16-byte columns
-    // (the swizzle puts an even and the next odd row in different ones).  k_pe: lane = 8 r + c is chunk c of
-    // key 4 i + r.
+    // Warp w owns keys 8 w .. 8 w + 7 of every tile, four lanes a key: lane = 4 r + u takes, of key r, the groups 4 j + u
+    // of the four code tiles j and two 16-byte pieces of k_pe.  A quarter of the warp so stores an even and the next
+    // odd row, whose columns the swizzle keeps apart.
+    constexpr int KW = kTile / C::kLoadWarps;
+    static_assert(KW == 8, "four lanes a key, a warp's rows one swizzle group");
     const int w = warp - C::kFirstLoad;
-    const int kb = (lane >> 2) & 1, j = lane >> 3, u = lane & 3, grp = 4 * j + u;
-    const int rc = lane & 7, rr = lane >> 3;
+    const int key = lane >> 2, u = lane & 3;
     struct Cursor {
-      int b, k0, end, t, ntiles;      // request (-1: past the last tile), item's first key, its end, tile, tiles
+      const int32_t* table;      // the request's block ids; null: past the last tile
+      int kp, end, left;         // this lane's key of the tile, the item's end, tiles after this one
     };
     int nit = 0;
     bool ok = true;
@@ -316,56 +341,74 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         const int k = nit % kItemDepth;
         if (!warp_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag)) {
           ok = false;
-          c.b = -1;
+          c.table = nullptr;
           return;
         }
-        c.b = items[k].b;
-        c.k0 = items[k].k0;
-        c.end = c.k0 + items[k].n;
-        c.ntiles = items[k].ntiles;
-        c.t = 0;
+        const int b = items[k].b, k0 = items[k].k0, n = items[k].n, ntiles = items[k].ntiles;
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[k]);
         ++nit;
-        if (c.b < 0 || c.ntiles > 0) return;
+        c.table = b < 0 ? nullptr : p.block_table + static_cast<int64_t>(b) * p.bt_stride;
+        c.kp = k0 + KW * w + key;
+        c.end = k0 + n;
+        c.left = ntiles - 1;
+        if (b < 0 || ntiles > 0) return;
       }
     };
     auto advance = [&](Cursor& c) {
-      if (c.b >= 0 && ++c.t >= c.ntiles) next_item(c);
+      if (!c.table) return;
+      c.kp += kTile;
+      if (--c.left < 0) next_item(c);
     };
     uint32_t errbits = 0;
-    // lane l < 16: block id of key 16 w + l of the cursor's tile (-1: no such key)
-    auto ask = [&](const Cursor& c, int& at) -> int {
-      at = 0;
-      const int kp = c.k0 + c.t * kTile + 16 * w + lane;
-      if (c.b < 0 || lane >= 16 || kp >= c.end) return -1;
-      const int col = kp / p.block_size;
-      at = kp - col * p.block_size;
-      const int id = p.block_table[static_cast<int64_t>(c.b) * p.bt_stride + col];
-      return id < 0 || id >= p.num_blocks ? -2 : id;
+    // this lane's key of a tile: its block id (as read: looked at a tile later, by found; kNoKey: there is none) and
+    // its place there
+    constexpr int kNoKey = -0x7FFFFFFF;
+    struct Ask {
+      int id, at;
     };
-    // its record, or null
-    auto record = [&](int id, int at) -> const uint8_t* {
-      if (id == -2) errbits |= 2u;
-      return id < 0 ? nullptr : p.kv + static_cast<int64_t>(id) * p.blk_stride + static_cast<int64_t>(at) * p.ent_stride;
+    auto ask = [&](const Cursor& c) -> Ask {
+      Ask a{kNoKey, 0};
+      if (c.table && c.kp < c.end) {
+        const int col = p.bs_shift >= 0 ? c.kp >> p.bs_shift : c.kp / p.block_size;
+        a.at = c.kp - col * p.block_size;
+        a.id = __ldg(c.table + col);
+      }
+      return a;
     };
-    uint4 code[8], rope[4];
-    uint32_t ex[8];
-    auto rec_of = [&](const uint8_t* mine, int key) -> const uint8_t* {
-      return reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(mine), key));
+    auto found = [&](const Ask& a) -> const uint8_t* {      // the key's record, or null
+      if (static_cast<uint32_t>(a.id) < p.num_blocks)
+        return p.kv + static_cast<uint64_t>(static_cast<uint32_t>(a.id)) * p.blk_stride + static_cast<uint64_t>(static_cast<uint32_t>(a.at)) * p.ent_stride;
+      if (a.id != kNoKey) errbits |= 2u;
+      return nullptr;
     };
-    auto load_step = [&](const uint8_t* mine, int i) {
-      const uint8_t* r = rec_of(mine, 2 * i + kb);
-      code[i] = make_uint4(0, 0, 0, 0);
-      ex[i] = 0;
-      if (r) {
-        code[i] = __ldg(reinterpret_cast<const uint4*>(r) + grp);
-        ex[i] = __ldg(r + kFp4Exps + grp);
+    // A tile's records are asked of memory into L2 one tile before its loads: the loads of a tile, issued together
+    // when the registers of the tile before are free, then find them there.  (Loads issued register by
+    // register between the conversions ran at a load's whole latency a step: the few scoreboards of a warp
+    // are shared by old and new loads.)
+    const bool one_run = p.block_size % KW == 0 && p.ent_stride == kFp4Entry;      // the warp's 16 records lie together
+    auto prefetch = [&](const uint8_t* r) {
+      if (one_run) {      // (a bulk prefetch a key takes the loaders longer than one for all)
+        if (lane == 0 && r) bulk_prefetch_l2(r, KW * kFp4Entry);
+      } else if (u == 0 && r) {
+        bulk_prefetch_l2(r, kFp4Entry);
       }
     };
-    auto load_rope = [&](const uint8_t* mine, int i) {
-      const uint8_t* r = rec_of(mine, 4 * i + rr);
-      rope[i] = r ? __ldg(reinterpret_cast<const uint4*>(r + kFp4Rope) + rc) : make_uint4(0, 0, 0, 0);
+    uint4 code[4], rope[2], ex;
+    bool live = false;
+    auto load_tile = [&](const uint8_t* r) {
+      live = r != nullptr;
+      if (r) {
+        ex = __ldg(reinterpret_cast<const uint4*>(r + kFp4Exps));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) rope[i] = __ldg(reinterpret_cast<const uint4*>(r + kFp4Rope) + 2 * u + i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code[i] = __ldg(reinterpret_cast<const uint4*>(r) + 4 * i + u);
+      } else {      // an absent key is all zeros
+        ex = rope[0] = rope[1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) code[i] = make_uint4(0, 0, 0, 0);
+      }
     };
     Cursor c{};
     next_item(c);
@@ -373,81 +416,87 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       // test aid: write nothing, so that the other roles' waits run out under the launch's short limit
       ok = false;
     }
-    int at1 = 0;
-    int id1 = ask(c, at1);
-    const uint8_t* mine = record(id1, at1);         // records of the tile whose loads are issued next
-    uint32_t live = __ballot_sync(0xFFFFFFFFu, mine != nullptr);
-    bool have = c.b >= 0;                           // a tile is in the registers
-#pragma unroll
-    for (int i = 0; i < 8; ++i) load_step(mine, i);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) load_rope(mine, i);
+    // tile 0 in the registers, records of tile 1, block ids of tile 2
+    bool have = c.table != nullptr, have1, have2;
+    load_tile(found(ask(c)));
     advance(c);
-    int id2, at2;
-    id2 = ask(c, at2);
+    have1 = c.table != nullptr;
+    const uint8_t* next = found(ask(c));
+    prefetch(next);
+    advance(c);
+    have2 = c.table != nullptr;
+    Ask asked = ask(c);
+    // offset of column 2 u of key r's row in a slot; column 2 u + 1 is 16 away (by exclusive or)
+    const uint32_t o0 = (KW * w + key) * 128 + (((2 * u) ^ key) << 4), o1 = o0 ^ 16u;
     for (int gt = 0; ok && have; ++gt) {
-      const bool have1 = c.b >= 0;
-      mine = record(id2, at2);                      // the next tile's
-      const uint32_t live1 = __ballot_sync(0xFFFFFFFFu, mine != nullptr);
-      if (have1) advance(c);
-      id2 = ask(c, at2);                            // and block ids of the one after it
-      if (gt >= 2 && !warp_wait(&pv_done[gt & 1], static_cast<uint32_t>((gt - 2) >> 1) & 1u, abort_flag)) break;
-      uint8_t* tile = ring + (gt & 1) * NB * kSlotBytes;
-      float* sk = scl + (gt & 1) * kTile;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int key = 2 * i + kb, row = 16 * w + key;
-        // the record's largest exponent, at least 2^-60 (what is smaller than 2^-74 then reads as zero, and the
-        // sums over keys stay inside fp32)
-        uint32_t K = ex[i];
-        K = max(K, __shfl_xor_sync(0xFFFFFFFFu, K, 1));
-        K = max(K, __shfl_xor_sync(0xFFFFFFFFu, K, 2));
-        K = max(K, __shfl_xor_sync(0xFFFFFFFFu, K, 8));
-        K = max(K, __shfl_xor_sync(0xFFFFFFFFu, K, 16));
-        K = max(K, 67u);
-        if ((lane & 0x1B) == 0)
-          // exponent 255: a NaN in the record; -1: no such block
-          sk[row] = !((live >> key) & 1u) ? -1.f : K == 255u ? CUDART_NAN_F : __uint_as_float((K - 6u) << 23);
-        const uint2 l2 = lut[min(K - ex[i], 15u)];
-        const uint32_t cw[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const uint32_t m7 = cw[v] & 0x77777777u, s8 = cw[v] & 0x88888888u;
-          o[2 * v] = fp4x4_to_e4m3(l2, m7, s8);
-          o[2 * v + 1] = fp4x4_to_e4m3(l2, m7 >> 16, s8 >> 16);
-        }
-        uint8_t* blk = tile + j * kSlotBytes;
-        *reinterpret_cast<uint4*>(blk + sw128(row, 2 * u)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(blk + sw128(row, 2 * u + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-        load_step(mine, i);
-      }
+      const int h = gt & 1;
+      const uint32_t used = static_cast<uint32_t>((gt - 2) >> 1) & 1u;      // phase of tile gt - 2
+      uint8_t* tile = ring + h * NB * kSlotBytes;
+      auto written = [&](int slot) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[h * NB + slot]);
+      };
+      if (w == 0 && lane == 0) TL(4, 1);
+      // the record's largest exponent, at least 2^-60: what is smaller than 2^-74 reads as zero, and the sums over
+      // keys stay inside fp32.  e: the exponents of this lane's groups.
+      const uint32_t word[4] = {ex.x, ex.y, ex.z, ex.w};
+      uint32_t K = 67u, e[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        *reinterpret_cast<uint4*>(tile + 4 * kSlotBytes + sw128(16 * w + 4 * i + rr, rc)) = rope[i];
-        load_rope(mine, i);
+        e[i] = __byte_perm(word[i], 0u, 0x4440u | u);
+        K = max(K, e[i]);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[gt & 1]);
-      live = live1;
+      K = max(K, __shfl_xor_sync(0xFFFFFFFFu, K, 1));
+      K = max(K, __shfl_xor_sync(0xFFFFFFFFu, K, 2));
+      // k_pe and the scale: free after QK of tile gt - 2 and its softmax, and so after its PV
+      if (gt >= 2 && !warp_wait(&pv_part[h * C::kParts], used, abort_flag)) break;
+      if (w == 0 && lane == 0) TL(4, 2);
+      *reinterpret_cast<uint4*>(tile + 4 * kSlotBytes + o0) = rope[0];
+      *reinterpret_cast<uint4*>(tile + 4 * kSlotBytes + o1) = rope[1];
+      if (u == 0)      // exponent 255: a NaN in the record; -1: no such key
+        scl[h * kTile + KW * w + key] = !live ? -1.f : K == 255u ? CUDART_NAN_F : __uint_as_float((K - 6u) << 23);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (C::kParts > 1 && i > 0 && i % (4 / C::kParts) == 0 && gt >= 2)
+          ok = ok && warp_wait(&pv_part[h * C::kParts + i / (4 / C::kParts)], used, abort_flag);
+        if (!ok) break;
+        const uint2 l2 = lut[min(K - e[i], 15u)];
+        const uint2 a0 = fp4x8_to_e4m3(l2, code[i].x, p.two16, p.two31), a1 = fp4x8_to_e4m3(l2, code[i].y, p.two16, p.two31);
+        const uint2 a2 = fp4x8_to_e4m3(l2, code[i].z, p.two16, p.two31), a3 = fp4x8_to_e4m3(l2, code[i].w, p.two16, p.two31);
+        *reinterpret_cast<uint4*>(tile + i * kSlotBytes + o0) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+        *reinterpret_cast<uint4*>(tile + i * kSlotBytes + o1) = make_uint4(a2.x, a2.y, a3.x, a3.y);
+        if (i & 1) written(i);
+      }
+      if (!ok) break;
+      if (w == 0 && lane == 0) TL(4, 3);
+      // (the block ids are looked at before new loads are on their way, whose scoreboards they may share)
+      const uint8_t* after = found(asked);
+      prefetch(after);
+      load_tile(next);
+      advance(c);
+      asked = ask(c);
+      next = after;
       have = have1;
+      have1 = have2;
+      have2 = c.table != nullptr;
     }
     errbits = __reduce_or_sync(0xFFFFFFFFu, errbits);
     if (lane == 0 && errbits) set_device_error(p.err, errbits);
   } else {
     // ------------------------------------------------------------------ softmax, query, epilogue
-    constexpr int NT = 128;
+    constexpr int NT = 32 * C::kSW, NC = C::NC;
     const int quad = warp & 3;
     const int row = quad * 32 + lane;           // key of the tile (S^T lane), latent of a block (O^T lane)
-    const int stid = tid - 64;
+    const int stid = tid - 32 * C::kFirstSm;
+    const int c0 = (stid >> 7) * NC;            // first column of this thread
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    // w = 2^(s' - m + kPExp) <= 2^(kTau + kPExp) = 2^8
-    constexpr float kTau = 3.f, kPExp = 5.f;
+    // w = 2^(s' - m + kPExp) <= 2^(kTau + kPExp) = 2^8.  mref holds m - kPExp.
+    constexpr float kTau = 7.f, kPExp = 1.f;
     // the query of an item: thread (c = stid / 8, part = stid % 8) takes elements 64 part .. + 63 of a column
     auto prep_query = [&](const WorkItem& qi) {
 #pragma unroll 1
-      for (int c = stid >> 3; c < NQ; c += 16) {
+      for (int c = stid >> 3; c < NQ; c += NT / 8) {
         const int part = stid & 7;
         const int cg = qi.g * NQ + c;
         const bool live = cg < p.cols;
@@ -498,203 +547,234 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       if (stid == 0) mbar_arrive(q_full);
     };
     int nit = 0, g = 0;
-    bool ok = true;
+    bool ok = true, failed = false;      // failed: a wait of this thread's warp ran out in the tile before
+    bool q_ready = false;                // the item's query was prepared during the one before
     while (ok) {
       const int k = nit % kItemDepth;
       bool w = warp_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag);
       const WorkItem it = items[k];
       ++nit;
-      if (stid < NQ) mref[stid] = -CUDART_INF_F;
+      if (stid < NQ) mref[stid] = -3e38f;         // no reference yet: every logit passes it, and -inf - m is no NaN
       if (!named_bar_and(1, NT, w)) break;
       if (it.b < 0) break;
-      if (it.ntiles > 0) prep_query(it);
-      const int cgb = it.g * NQ;
-      float l_part[NQ];
+      if (it.ntiles > 0 && !q_ready) prep_query(it);
+      q_ready = false;
+      const int cgb = it.g * NQ + c0;             // global column of this thread's first
+      float l_part[NC];
 #pragma unroll
-      for (int c = 0; c < NQ; ++c) l_part[c] = 0.f;
-      // s' of this thread's key for the columns, masked; ks: the key's 2^(K - 6)
-      auto load_s = [&](float (&s)[NQ], int gt, int t, float ks) {
-        const uint32_t ts = tl + (gt & 1) * C::kS;
+      for (int c = 0; c < NC; ++c) l_part[c] = 0.f;
+      // s' of this thread's key for its columns, masked; ks: the key's 2^(K - 6)
+      auto load_s = [&](float (&s)[NC], int gt, int t, float ks) {
+        const uint32_t ts = tl + (gt & 1) * C::kS + c0;
         const int kpos = it.k0 + t * kTile + row;
         const bool rv = kpos < it.k0 + it.n && !(ks < 0.f);
-        const float kexp = static_cast<float>(static_cast<int>(__float_as_uint(ks) >> 23) - 127);
+        // (the rows of absent keys are zeros: 0 * 0 - inf)
+        const float kexp = rv ? static_cast<float>(static_cast<int>(__float_as_uint(ks) >> 23) - 127) : -CUDART_INF_F;
+        const float km = rv ? ks : 0.f;
+        float r[NC];              // lo, then rope (all three at once do not fit the registers)
+        tmem_ld16(ts, s);
+        tmem_ld16(ts + NQ, r);
+        tmem_ld_wait();
 #pragma unroll
-        for (int c0 = 0; c0 < NQ; c0 += 16) {
-          float hi[16], lo[16], rp[16];
-          tmem_ld16(ts + c0, hi);
-          tmem_ld16(ts + NQ + c0, lo);
-          tmem_ld16(ts + 2 * NQ + c0, rp);
-          tmem_ld_wait();
+        for (int c = 0; c < NC; ++c) s[c] = fmaf(r[c], 0.0625f, s[c]);
+        tmem_ld16(ts + 2 * NQ, r);
+        tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float x = fmaf(fmaf(lo[c], 0.0625f, hi[c]), colf[c0 + c] * ks, fmaf(rp[c], p.sig2, kexp));
-            s[c0 + c] = rv ? x : -CUDART_INF_F;
-          }
+        for (int c = 0; c < NC; c += 4) {
+          const float4 f4 = *reinterpret_cast<const float4*>(colf + c0 + c);
+          const float ff[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            s[c + y] = fmaf(s[c + y], ff[y] * km, fmaf(r[c + y], p.sig2, kexp));
         }
         // spec-verify: query token qi sees keys up to L - q_len + qi
         const int dq = kpos - it.L + p.q_len;
         if (rv && dq > 0) {
 #pragma unroll
-          for (int c = 0; c < NQ; ++c)
+          for (int c = 0; c < NC; ++c)
             if ((cgb + c) / p.H < dq) s[c] = -CUDART_INF_F;
         }
       };
       for (int t = 0; t < it.ntiles; ++t) {
         const int gt = g + t;
         w = warp_wait(&s_full[gt & 1], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag);
-        w = w && warp_wait(&full[gt & 1], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag);      // its scales (long complete)
+        w = w && warp_wait(&full[(gt & 1) * NB + 1], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag);      // its scales (long there)
         tc_fence_after();
         const float ks = scl[(gt & 1) * kTile + row];
-        float s[NQ];
-        load_s(s, gt, t, ks);
-        bool need = false;
+        if (stid == 0) TL(3, 1);
+        float d[NC];              // s', then s' - m + kPExp, then the weights
+        load_s(d, gt, t, ks);
+        if (stid == 0) TL(3, 2);
+        auto against = [&]() {
 #pragma unroll
-        for (int c = 0; c < NQ; c += 4) {
-          const float4 m4 = *reinterpret_cast<const float4*>(mref + c);
-          const float mm[4] = {m4.x, m4.y, m4.z, m4.w};
+          for (int c = 0; c < NC; c += 4) {
+            const float4 m4 = *reinterpret_cast<const float4*>(mref + c0 + c);
+            d[c] -= m4.x;
+            d[c + 1] -= m4.y;
+            d[c + 2] -= m4.z;
+            d[c + 3] -= m4.w;
+          }
+        };
+        against();
+        float most = d[0];
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            need |= (s[c + y] > mm[y] + kTau) | ((mm[y] == -CUDART_INF_F) & (s[c + y] > -CUDART_INF_F));
-        }
+        for (int c = 1; c < NC; ++c) most = fmaxf(most, d[c]);
+        // (the weights for the reference as it is, while the other warps come to the barrier)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) d[c] = ex2(d[c]);
         tc_fence_before();
-        const bool rare = named_bar_or(1, NT, need || !w);
+        const bool rare = named_bar_or(1, NT, most > kTau + kPExp || !w || failed);
         bool pv_waited = false;
+        // every thread has read S[gt & 1]; a tile that moves the reference reads it again below
+        if (stid == 0 && !rare) mbar_arrive(&s_free[gt & 1]);
         if (rare) {
-          ok = named_bar_and(1, NT, w);
+          ok = named_bar_and(1, NT, w && !failed);
           if (!ok) break;
           float* rb = red_m + (gt & 1) * NQ * 4;
+          load_s(d, gt, t, ks);
           {
-            const float wm = warp_col_reduce<NQ, true>(s, lane);
-            if (NQ == 32 || lane < 16) rb[(lane % NQ) * 4 + quad] = wm;
+            const float wm = warp_col_reduce<NC, true>(d, lane);      // (it leaves d in pieces)
+            if (lane < NC) rb[(c0 + lane) * 4 + quad] = wm;
           }
           named_bar_sync(1, NT);
-          const float4 q4 = reinterpret_cast<const float4*>(rb)[lane % NQ];
-          const float mt_l = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w));
-          const float mo_l = mref[lane % NQ];
+          const int cl = c0 + (lane % NC);
+          const float4 q4 = reinterpret_cast<const float4*>(rb)[cl];
+          const float mt_l = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w)) - kPExp;
+          const float mo_l = mref[cl];
           const float mn_l = fmaxf(mo_l, mt_l);
-          const float alpha_lane = (mo_l == -CUDART_INF_F) ? 0.f : ex2(mo_l - mn_l);
+          const float alpha_lane = ex2(mo_l - mn_l);
           const bool resc = __any_sync(0xFFFFFFFFu, mn_l != mo_l);
           named_bar_sync(1, NT);
-          if (quad == 0 && (NQ == 32 || lane < 16)) {
-            mref[lane % NQ] = mn_l;
-            alph[lane % NQ] = alpha_lane;
+          if (quad == 0 && lane < NC) {
+            mref[cl] = mn_l;
+            alph[cl] = alpha_lane;
           }
           named_bar_sync(1, NT);
 #pragma unroll
-          for (int c = 0; c < NQ; ++c) l_part[c] *= alph[c];
+          for (int c = 0; c < NC; ++c) l_part[c] *= alph[c0 + c];
           // O of the previous tiles moves to the new reference once PV of the last tile is done
           if (t > 0) {
-            w = warp_wait(&pv_done[(gt - 1) & 1], static_cast<uint32_t>((gt - 1) >> 1) & 1u, abort_flag);
+            w = warp_wait(&pv_part[((gt - 1) & 1) * C::kParts + C::kParts - 1], static_cast<uint32_t>((gt - 1) >> 1) & 1u, abort_flag);
             tc_fence_after();
             pv_waited = true;
             if (w && resc) {
 #pragma unroll 1
-              for (int x = 0; x < 8 * NQ; x += 16) {      // O_j: hi columns, then lo columns
-                float o[16];
-                tmem_ld16(tl + C::kTmemO + x, o);
+              for (int x = 0; x < 8 * NQ; x += NQ) {      // O_j: this thread's hi columns, then its lo columns
+                tmem_ld16(tl + C::kTmemO + x + c0, d);
                 tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 16; ++c) o[c] *= alph[(x + c) % NQ];
-                tmem_st16(tl + C::kTmemO + x, o);
+                for (int c = 0; c < NC; ++c) d[c] *= alph[c0 + c];
+                tmem_st16(tl + C::kTmemO + x + c0, d);
               }
               tmem_st_wait();
             }
           }
-          load_s(s, gt, t, ks);
+          load_s(d, gt, t, ks);
+          against();
+#pragma unroll
+          for (int c = 0; c < NC; ++c) d[c] = ex2(d[c]);
           tc_fence_before();
           named_bar_sync(1, NT);
+          if (stid == 0) mbar_arrive(&s_free[gt & 1]);
         }
-        // every thread has read S[gt & 1] for good
-        if (stid == 0) mbar_arrive(&s_free[gt & 1]);
+        if (stid == 0) TL(3, rare ? 30 : 3);
         const float ik = __uint_as_float((254u << 23) - __float_as_uint(ks < 0.f ? 1.f : ks));      // 1 / ks
+        // hi = E4M3 of the weight in f16 (11 bits of it are more than the two terms keep), lo = E4M3 of 16 times the
+        // exact rest
+        uint32_t hw[4], lw[4];
 #pragma unroll
-        for (int c = 0; c < NQ; ++c) {
-          const float mr = mref[c];
-          const float mu = (mr == -CUDART_INF_F) ? 0.f : mr;
-          s[c] = ex2(s[c] - mu + kPExp);
-          l_part[c] = fmaf(s[c], ik, l_part[c]);
+        for (int y = 0; y < 4; ++y) {
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const __half2 a = __floats2half2_rn(d[4 * y + 2 * z], d[4 * y + 2 * z + 1]);
+            hi[z] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(a), __NV_SATFINITE, __NV_E4M3);
+            const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi[z]), __NV_E4M3);
+            const __half2 r = __hmul2(__hsub2(a, __half2(b)), __float2half2_rn(16.f));
+            lo[z] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
+          }
+          hw[y] = hi[0] | (hi[1] << 16);
+          lw[y] = lo[0] | (lo[1] << 16);
         }
         if (t > 0 && !pv_waited) {
-          w = warp_wait(&pv_done[(gt - 1) & 1], static_cast<uint32_t>((gt - 1) >> 1) & 1u, abort_flag);   // P is free
+          w = warp_wait(&pv_part[((gt - 1) & 1) * C::kParts + C::kParts - 1], static_cast<uint32_t>((gt - 1) >> 1) & 1u, abort_flag);   // P is free
           tc_fence_after();
         }
+        if (stid == 0) TL(3, 4);
         // 8 keys x 16 columns core matrices, 8-key groups 16 NQ bytes apart; hi columns, then lo columns
         uint8_t* prow = ps + (row >> 3) * (16 * NQ) + (row & 7) * 16;
-#pragma unroll
-        for (int c = 0; c < NQ; c += 16) {
-          uint32_t hw[4], lw[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float a0 = s[c + 4 * y], a1 = s[c + 4 * y + 1], a2 = s[c + 4 * y + 2], a3 = s[c + 4 * y + 3];
-            const uint32_t h01 = e4m3x2_sat(a0, a1), h23 = e4m3x2_sat(a2, a3);
-            const float2 f01 = e4m3x2_to_float2(h01), f23 = e4m3x2_to_float2(h23);
-            hw[y] = h01 | (h23 << 16);
-            lw[y] = e4m3x2_sat(16.f * (a0 - f01.x), 16.f * (a1 - f01.y)) |
-                    (e4m3x2_sat(16.f * (a2 - f23.x), 16.f * (a3 - f23.y)) << 16);
-          }
-          *reinterpret_cast<uint4*>(prow + (c >> 4) * 128) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-          *reinterpret_cast<uint4*>(prow + ((NQ + c) >> 4) * 128) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-        }
+        *reinterpret_cast<uint4*>(prow + (c0 >> 4) * 128) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+        *reinterpret_cast<uint4*>(prow + ((NQ + c0) >> 4) * 128) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && w) mbar_arrive(p_full);
-        ok = named_bar_and(1, NT, w);
-        if (!ok) break;
+        if (lane == 0 && w) mbar_arrive(p_full);      // (where w is false the next barrier of the group ends the item)
+        failed = failed || !w;
+        if (stid == 0) TL(3, 5);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) l_part[c] = fmaf(d[c], ik, l_part[c]);      // while PV runs
       }
       if (!ok) break;
+      // the next item's query while PV runs and the results are written
+      const bool more = warp_wait(&item_full[nit % kItemDepth], (nit / kItemDepth) & 1, abort_flag);
+      if (named_bar_and(1, NT, more)) {
+        const WorkItem qi = items[nit % kItemDepth];
+        if (qi.b >= 0 && qi.ntiles > 0) {
+          prep_query(qi);
+          q_ready = true;
+        }
+      }
       // ---- epilogue: O / l and the LSE of every column of the item
+      if (stid == 0) TL(3, 6);
       w = true;
       if (it.ntiles > 0) {
-        w = warp_wait(&pv_done[(g + it.ntiles - 1) & 1], static_cast<uint32_t>((g + it.ntiles - 1) >> 1) & 1u, abort_flag);
+        w = warp_wait(&pv_part[((g + it.ntiles - 1) & 1) * C::kParts + C::kParts - 1], static_cast<uint32_t>((g + it.ntiles - 1) >> 1) & 1u, abort_flag);
         tc_fence_after();
       }
       g += it.ntiles;
       {
-        const float lw = warp_col_reduce<NQ, false>(l_part, lane);
-        if (NQ == 32 || lane < 16) red_l[(lane % NQ) * 4 + quad] = lw;
+        const float lw = warp_col_reduce<NC, false>(l_part, lane);
+        if (lane < NC) red_l[(c0 + lane) * 4 + quad] = lw;
       }
-      ok = named_bar_and(1, NT, w);
+      ok = named_bar_and(1, NT, w && !failed);
       if (!ok) break;
-      const int cl = lane % NQ;
+      const int cl = c0 + (lane % NC);
       float inv_l, lse_l;
       {
         const float4 q4 = reinterpret_cast<const float4*>(red_l)[cl];
         const float l = (q4.x + q4.y) + (q4.z + q4.w);
         const bool none = l == 0.f;             // no visible key (a NaN goes on)
         inv_l = none ? 0.f : __fdividef(1.f, l);
-        lse_l = none ? -CUDART_INF_F : (mref[cl] + __log2f(l) - kPExp) * 0.69314718055994531f;
+        lse_l = none ? -CUDART_INF_F : (mref[cl] + __log2f(l)) * 0.69314718055994531f;
       }
       const bool final_out = p.n_splits == 1;
       // (row, head) of column cg: the flat index row * H + head is b * q_len * H + cg
       const int64_t flat0 = static_cast<int64_t>(it.b) * p.q_len * p.H + cgb;
-      const int ncol = min(NQ, p.cols - cgb);
+      const int ncol = min(NC, p.cols - cgb);       // may be none
       const int64_t o_wrap = p.o_s0b - static_cast<int64_t>(p.H) * p.o_s1b;
 #pragma unroll 1
-      for (int jq = 0; jq < 4 * (NQ / 16); ++jq) {
-        const int jj = jq / (NQ / 16), cs = 16 * (jq % (NQ / 16));
-        if (cs >= ncol) continue;
-        float o[16];
+      for (int jj = 0; jj < 4 && ncol > 0; ++jj) {
+        float o[NC];
         if (it.ntiles > 0) {
-          float lo[16];
-          tmem_ld16(tl + C::kTmemO + 2 * NQ * jj + cs, o);
-          tmem_ld16(tl + C::kTmemO + 2 * NQ * jj + NQ + cs, lo);
+          float lo[NC];
+          tmem_ld16(tl + C::kTmemO + 2 * NQ * jj + c0, o);
+          tmem_ld16(tl + C::kTmemO + 2 * NQ * jj + NQ + c0, lo);
           tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 16; ++c) o[c] = fmaf(lo[c], 0.0625f, o[c]);
+          for (int c = 0; c < NC; ++c) o[c] = fmaf(lo[c], 0.0625f, o[c]);
         } else {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) o[c] = 0.f;
+          for (int c = 0; c < NC; ++c) o[c] = 0.f;
         }
         const int d = 128 * jj + row;
         if (final_out) {
-          int h = (cgb + cs) % p.H;
-          uint8_t* ptr = p.out + (static_cast<int64_t>(it.b) * p.q_len + (cgb + cs) / p.H) * p.o_s0b +
+          int h = cgb % p.H;
+          uint8_t* ptr = p.out + (static_cast<int64_t>(it.b) * p.q_len + cgb / p.H) * p.o_s0b +
                          static_cast<int64_t>(h) * p.o_s1b + 2 * d;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float iv = __shfl_sync(0xFFFFFFFFu, inv_l, cs + c);
-            if (cs + c < ncol) *reinterpret_cast<__nv_bfloat16*>(ptr) = __float2bfloat16_rn(o[c] * iv);
+          for (int c = 0; c < NC; ++c) {
+            const float iv = __shfl_sync(0xFFFFFFFFu, inv_l, c);
+            if (c < ncol) *reinterpret_cast<__nv_bfloat16*>(ptr) = __float2bfloat16_rn(o[c] * iv);
             ptr += p.o_s1b;
             if (++h == p.H) {
               h = 0;
@@ -702,19 +782,19 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
             }
           }
         } else {
-          float* dst = p.part_o + ((static_cast<int64_t>(it.s) * p.n_rows * p.H + flat0 + cs) * kLora + d);
+          float* dst = p.part_o + ((static_cast<int64_t>(it.s) * p.n_rows * p.H + flat0) * kLora + d);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float iv = __shfl_sync(0xFFFFFFFFu, inv_l, cs + c);
-            if (cs + c < ncol) dst[static_cast<int64_t>(c) * kLora] = o[c] * iv;
+          for (int c = 0; c < NC; ++c) {
+            const float iv = __shfl_sync(0xFFFFFFFFu, inv_l, c);
+            if (c < ncol) dst[static_cast<int64_t>(c) * kLora] = o[c] * iv;
           }
         }
       }
-      if (row < 32 && (NQ == 32 || lane < 16) && cl < ncol) {
+      if (quad == 0 && lane < ncol) {
         if (final_out) {
-          if (p.lse) p.lse[flat0 + cl] = lse_l;
+          if (p.lse) p.lse[flat0 + lane] = lse_l;
         } else {
-          p.part_lse[static_cast<int64_t>(it.s) * p.n_rows * p.H + flat0 + cl] = lse_l;
+          p.part_lse[static_cast<int64_t>(it.s) * p.n_rows * p.H + flat0 + lane] = lse_l;
         }
       }
       tc_fence_before();
