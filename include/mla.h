@@ -66,6 +66,7 @@ typedef enum {
 #define MLA_DEVERR_SLOT 4u        /* insert slot whose block is outside [0, num_blocks) */
 #define MLA_DEVERR_POSITION 8u    /* RoPE position outside [0, max_position) (clamped) */
 #define MLA_DEVERR_TIMEOUT 16u    /* an in-kernel wait gave up (pipeline fault); outputs invalid */
+#define MLA_DEVERR_FREE 32u       /* mla_plan_step: a request got no blocks or rows, or returned blocks found no place */
 
 /* Message of the last non-OK return on the calling thread ("" if none). */
 MLA_API const char* mla_last_error(void);
@@ -416,6 +417,83 @@ MLA_API int mla_absorb_q(const void* q_nope, int64_t qn_s0, int64_t qn_s1, const
 MLA_API int mla_v_up_proj(const void* latent, int64_t l_s0, int64_t l_s1, const void* w_uv, const void* gate,
                           int64_t g_s0, void* out, int64_t o_s0, int64_t o_s1, int32_t B, int32_t H, int32_t V,
                           cudaStream_t stream);
+
+/* Element types of mla_rope. */
+#define MLA_TYPE_BF16 0
+#define MLA_TYPE_FP16 1
+#define MLA_TYPE_FP32 2
+
+/*
+ * Rotary positions of queries and, in the same launch, of keys: outside the fused epilogues, for any width of the
+ * rotated part, either layout of its pairs, and its inverse.
+ *   Pair i (of R / 2) of a head is (2i, 2i + 1) of the rotated values, or (i, i + R / 2) with half != 0.  With c, s the
+ *   table's row of the token's position: a' = a c - b s, b' = b c + a s in fp32 (y0 = fma(a, c, -(b*s)), y1 =
+ *   fma(b, c, a*s)), rounded once to the type.  inverse != 0 takes -s: the transposed rotation, the rotation's gradient.
+ *
+ *   type         MLA_TYPE_BF16, MLA_TYPE_FP16 or MLA_TYPE_FP32, of all four tensors.
+ *   q            device [T, H, D], element strides (q_s0, q_s1); the R values from q_at on of every head are rotated,
+ *                the others copied.  D <= 1024.
+ *   q_out        device out [T, H, D], strides (qo_s0, qo_s1): q itself (same address and strides: in place) or memory
+ *                that does not meet q's.
+ *   k, k_out     the same for [T, Hk, Dk] with k_at; both NULL: none.  In place both or neither.
+ *   positions    device int64 [T], in [0, max_position) (others are clamped and set MLA_DEVERR_POSITION).
+ *   cos_sin      device fp32 [max_position, R] contiguous: R / 2 cosines, then R / 2 sines.  R even, 2 .. 512.
+ */
+MLA_API int mla_rope(int32_t type, const void* q, int64_t q_s0, int64_t q_s1, void* q_out, int64_t qo_s0, int64_t qo_s1,
+                     int32_t H, int32_t D, int32_t q_at, const void* k, int64_t k_s0, int64_t k_s1, void* k_out,
+                     int64_t ko_s0, int64_t ko_s1, int32_t Hk, int32_t Dk, int32_t k_at, const int64_t* positions,
+                     const float* cos_sin, int64_t max_position, int32_t R, int32_t half, int32_t inverse, int32_t T,
+                     cudaStream_t stream);
+
+/* Scalings of mla_rope_table. */
+#define MLA_ROPE_PLAIN 0
+#define MLA_ROPE_LINEAR 1
+#define MLA_ROPE_NTK 2
+#define MLA_ROPE_YARN 3
+
+/*
+ * The table of mla_rope and of the fused epilogues (R = 64 there): row p holds m cos(p f_i), then m sin(p f_i), of the
+ * R / 2 frequencies f_i, angles in 64 bits, rounded once to fp32.  With g_i = base^(-2i / R):
+ *   PLAIN   f_i = g_i.
+ *   LINEAR  f_i = g_i / factor (positions interpolated).
+ *   NTK     f_i = (base factor^(R / (R - 2)))^(-2i / R) (R > 2).
+ *   YARN    f_i = g_i (1 - r_i) + g_i / factor r_i, r_i = clamp((i - lo) / (hi - lo), 0, 1), with lo and hi the pairs that turn
+ *           beta_fast and beta_slow times over `original` positions: c(beta) = R ln(original / (2 pi beta)) / (2 ln base),
+ *           lo = max(floor(c(beta_fast)), 0), hi = min(ceil(c(beta_slow)), R - 1), hi = lo + 0.001 where they meet.
+ *   m is attn_scale (for YARN usually 0.1 ln(factor) + 1).
+ * Arguments of other scalings are ignored.  out: device fp32 [max_position, R] contiguous; R even, 2 .. 512.
+ */
+MLA_API int mla_rope_table(float* out, int64_t max_position, int32_t R, double base, int32_t scaling, double factor,
+                           int64_t original, double beta_fast, double beta_slow, double attn_scale, cudaStream_t stream);
+
+/*
+ * The blocks and slots of a step, from the requests' lengths, without the host: what the inserts and the decode of a paged
+ * cache take.  Blocks come from a stack of free ones (the top is free_blocks[num_free - 1]).
+ *   1. finished[b] != 0: the request's ceil(seq_lens[b] / block_size) blocks go on top of the stack, in the order of the
+ *      requests and of their tables; its length becomes 0 (the place may take a new request in the same step).
+ *   2. Request b with L cached and n = new_lens[b] new tokens takes its ceil((L + n) / block_size) - ceil(L / block_size)
+ *      new blocks from the top of the stack, in the order of the requests, into its next table entries.
+ *   3. Its rows cu_q_lens[b] .. cu_q_lens[b+1]-1 of the step hold positions L .. L + n - 1 and their slots
+ *      (block * block_size + offset).  Rows past the last request's get position 0 and slot -1.
+ * A request whose blocks are no longer there, whose table row is too short or whose rows end past T is not served
+ * (later ones that need no more than is left are): it takes nothing, keeps its length, its rows have slot -1, and
+ * MLA_DEVERR_FREE is set; so too where returned blocks pass the stack's capacity (those are lost).
+ *
+ *   seq_lens     device int32 [B]: cached tokens before the step (negative: 0).   new_lens  device int32 [B].
+ *   finished     device bytes [B], or NULL (none).
+ *   block_table  device int32 [B, cols], row stride t_stride; new entries are written, no others.
+ *   free_blocks  device int32 [capacity]; num_free  device int32 [1].
+ *   seq_out      device out int32 [B]: L + n (L where not served); may be seq_lens itself.
+ *   num_free_out device out int32 [1]; may be num_free itself.
+ *   served       device out bytes [B]: 1, or 0 where not served.
+ *   cu_q_lens    device out int32 [B + 1] (no more than T).
+ *   slots, positions  device out int64 [T].
+ * Whole numbers only: the same inputs give the same outputs.
+ */
+MLA_API int mla_plan_step(const int32_t* seq_lens, const int32_t* new_lens, const uint8_t* finished, int32_t* block_table,
+                          int64_t t_stride, int32_t cols, int32_t* free_blocks, int64_t capacity, const int32_t* num_free,
+                          int32_t* seq_out, int32_t* num_free_out, uint8_t* served, int32_t* cu_q_lens, int64_t* slots,
+                          int64_t* positions, int32_t B, int32_t T, int32_t block_size, cudaStream_t stream);
 
 /*
  * The selector in front of sparse attention.  Every cached token has an index key of 128 values

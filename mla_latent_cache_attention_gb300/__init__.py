@@ -8,8 +8,8 @@ importing the binding raises.
 Entry points (same names as the C ABI, without the ``mla_`` prefix):
 
   q_concat_cache_insert  decode epilogue: mqa_q = [ql_nope | q_pe] (+ GPT-J RoPE), latent
-                         insert into a bf16 / plain fp8 / fp8_ds_mla paged cache
-  key_concat_cache_insert   prefill epilogue (bf16 / fp8_ds_mla cache): full key
+                         insert into a bf16 / plain fp8 / fp8_ds_mla / mxfp4 paged cache
+  key_concat_cache_insert   prefill epilogue (bf16 / fp8_ds_mla / mxfp4 cache): full key
                          [k_nope | rope(k_pe)], q RoPE in place, latent insert
   qkv_quant_cache_fp8_insert  prefill epilogue (plain fp8 cache): E4M3 q / k / v with their
                          own scales, latent insert with the cache scale
@@ -21,6 +21,12 @@ Entry points (same names as the C ABI, without the ``mla_`` prefix):
   merge_attn_states      prefix / suffix merge of partial attentions by their LSEs
   gather_dequant         paged entries -> exact fp32 values (test aid)
 
+Around a step:
+
+  plan_step              blocks, slots, positions and row offsets of a step from the requests' lengths
+  rope                   rotary positions of queries and keys: any width, both layouts, inverse
+  rope_table             the table of cosines and sines, plain or scaled for long contexts
+
 The selector in front of sparse attention (an index key of 128 values per cached token):
 
   index_q_cache_insert   index queries and keys rotated, quantised, keys inserted into the
@@ -28,7 +34,7 @@ The selector in front of sparse attention (an index key of 128 values per cached
   index_gather           cached index keys read back as bf16
   index_scores           weighted relu scores of every visible token, or of blocks of tokens
   index_select           the topk best blocks of every row (and their cache slots)
-  selected_decode        decode over the selected pages of a bf16 / fp8 / fp8_ds_mla cache
+  selected_decode        decode over the selected pages of a bf16 / fp8 / fp8_ds_mla / mxfp4 cache
 
 Every tensor argument is checked here before the call (CUDA device, dtype, rank, unit
 innermost stride; index tensors contiguous), so that a wrong tensor raises instead of being
@@ -39,6 +45,7 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import math
 import os
 import warnings
 
@@ -113,6 +120,11 @@ def lib():
             f.restype = sz
         L.mla_selected_decode.argtypes = [vp, i64, i64, vp, i32, i64, i64, i64, i32, vp, i64, i64, vp, vp, vp, i64, i32,
                                           i32, i32, i32, f32, f32, f32, vp, i64, i64, vp, vp, sz, vp]
+        f64 = ctypes.c_double
+        L.mla_rope.argtypes = [i32, vp, i64, i64, vp, i64, i64, i32, i32, i32, vp, i64, i64, vp, i64, i64, i32, i32, i32, vp, vp, i64,
+                               i32, i32, i32, i32, vp]
+        L.mla_rope_table.argtypes = [vp, i64, i32, f64, i32, f64, i64, f64, f64, f64, vp]
+        L.mla_plan_step.argtypes = [vp, vp, vp, vp, i64, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp]
         L.mla_debug_stall_next_decode.argtypes = [i32]
         L.mla_debug_stall_next_decode.restype = None
         L.mla_debug_ds_cluster.argtypes = [i32]
@@ -121,7 +133,7 @@ def lib():
                   "mla_gather_dequant", "mla_key_concat_cache_insert", "mla_qkv_quant_cache_fp8_insert",
                   "mla_gather_context", "mla_merge_attn_states", "mla_sparse_fwd_ext", "mla_absorb_q",
                   "mla_v_up_proj", "mla_index_q_cache_insert", "mla_index_gather", "mla_index_scores",
-                  "mla_index_select", "mla_selected_decode"):
+                  "mla_index_select", "mla_selected_decode", "mla_rope", "mla_rope_table", "mla_plan_step"):
             getattr(L, f).restype = ctypes.c_int
         L.mla_read_device_errors.restype = ctypes.c_int
         _lib = L
@@ -185,13 +197,15 @@ def _index_i32(t, name, device, lo, hi):
     return t
 
 
-def _cache_geometry(kv_cache: torch.Tensor):
+def _cache_geometry(kv_cache: torch.Tensor, fmt=None):
     """[num_blocks, block_size, entry_stride] view of a paged cache (any 1- or 2-byte dtype)."""
     es = kv_cache.element_size()
     if kv_cache.dim() == 4 and kv_cache.shape[1] == 1:      # [nb, 1, bs, entry] (a head axis of size 1)
         kv_cache = kv_cache.squeeze(1)
     if kv_cache.dim() != 3 or kv_cache.stride(2) != 1:
         raise ValueError("kv_cache must be [num_blocks, block_size, entry] with a unit innermost stride")
+    if fmt == CACHE_MXFP4 and (es != 1 or kv_cache.shape[2] < ENTRY_BYTES[fmt]):
+        raise ValueError(f"mxfp4 records are {ENTRY_BYTES[fmt]} bytes of uint8, kv_cache has {kv_cache.shape[2]} of {kv_cache.dtype}")
     return kv_cache.shape[0], kv_cache.stride(0) * es, kv_cache.stride(1) * es, kv_cache.shape[1]
 
 
@@ -222,6 +236,10 @@ def q_concat_cache_insert(ql_nope, q_pe, kv_c_normed, k_pe, kv_cache, slot_mappi
     """Decode epilogue.  Returns mqa_q [B, H, 576] (bf16, or uint8 E4M3 codes for fp8);
     writes kv_cache in place."""
     fmt = _fmt(fmt)
+    done = (_step or _plain_step()).q_concat(ql_nope, q_pe, kv_c_normed, k_pe, kv_cache, slot_mapping, fmt, q_scale_inv, cache_scale_inv,
+                                             positions, cos_sin_cache, mqa_q)
+    if done is not None:
+        return done
     dev = _cuda_device(ql_nope)
     bf = (torch.bfloat16,)
     _need(ql_nope, "ql_nope", bf, dev, ndim=3)
@@ -242,7 +260,7 @@ def q_concat_cache_insert(ql_nope, q_pe, kv_c_normed, k_pe, kv_cache, slot_mappi
         mqa_q = torch.empty((B, H, 576), dtype=dt, device=dev)
     _need(mqa_q, "mqa_q", _BYTE_TYPES if fmt == CACHE_FP8 else bf, dev, ndim=3, contiguous=True)
     _need(kv_cache, "kv_cache", _BYTE_TYPES + bf, dev)
-    nb, bstride, estride, bs = _cache_geometry(kv_cache)
+    nb, bstride, estride, bs = _cache_geometry(kv_cache, fmt)
     max_pos = 0 if cos_sin_cache is None else cos_sin_cache.shape[0]
     with torch.cuda.device(dev):
         _check(lib().mla_q_concat_cache_insert(
@@ -273,15 +291,18 @@ def _prefill_common(q, k_nope, k_pe, kv_c_normed, slot_mapping, positions, cos_s
 
 def key_concat_cache_insert(q, k_nope, k_pe, kv_c_normed, kv_cache, slot_mapping, *, fmt, positions=None,
                             cos_sin_cache=None, k_out=None):
-    """Prefill epilogue for the bf16 / fp8_ds_mla cache.  Rotates the rope part of q in place
+    """Prefill epilogue for the bf16 / fp8_ds_mla / mxfp4 cache.  Rotates the rope part of q in place
     (when positions are given), writes kv_cache in place and returns k_out [Tp, H, dn + 64]."""
     fmt = _fmt(fmt)
+    done = (_step or _plain_step()).key_concat(q, k_nope, k_pe, kv_c_normed, kv_cache, slot_mapping, fmt, positions, cos_sin_cache, k_out)
+    if done is not None:
+        return done
     dev, k_pe, Tp, H, dn = _prefill_common(q, k_nope, k_pe, kv_c_normed, slot_mapping, positions, cos_sin_cache)
     if k_out is None:
         k_out = torch.empty((Tp, H, dn + 64), dtype=torch.bfloat16, device=dev)
     _need(k_out, "k_out", (torch.bfloat16,), dev, ndim=3, contiguous=True)
     _need(kv_cache, "kv_cache", _BYTE_TYPES + (torch.bfloat16,), dev)
-    nb, bstride, estride, bs = _cache_geometry(kv_cache)
+    nb, bstride, estride, bs = _cache_geometry(kv_cache, fmt)
     max_pos = 0 if cos_sin_cache is None else cos_sin_cache.shape[0]
     with torch.cuda.device(dev):
         _check(lib().mla_key_concat_cache_insert(
@@ -396,6 +417,10 @@ def paged_decode(q, kv_cache, block_table, seq_lens, *, fmt, q_len=1, max_contex
     """Paged decode / spec-verify.  q [B*q_len, H, 576] (bf16, or uint8 E4M3 codes for fp8).
     Returns (out [B*q_len, H, 512] bf16, lse or None)."""
     fmt = _fmt(fmt)
+    done = (_step or _plain_step()).paged(q, kv_cache, block_table, seq_lens, fmt, q_len, max_context, softmax_scale, q_scale, k_scale,
+                                          out, return_lse, workspace, lse)
+    if done is not None:
+        return done
     dev = _cuda_device(q)
     _need(q, "q", _BYTE_TYPES if fmt == CACHE_FP8 else (torch.bfloat16,), dev, ndim=3)
     _need(kv_cache, "kv_cache", _BYTE_TYPES + (torch.bfloat16,), dev)
@@ -420,7 +445,7 @@ def paged_decode(q, kv_cache, block_table, seq_lens, *, fmt, q_len=1, max_contex
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         if workspace is not None:
             _need(workspace, "workspace", _BYTE_TYPES, dev, contiguous=True)
-        nb, bstride, estride, bs = _cache_geometry(kv_cache)
+        nb, bstride, estride, bs = _cache_geometry(kv_cache, fmt)
         _check(lib().mla_paged_decode(
             _ptr(q), q.stride(0), q.stride(1), _ptr(kv_cache), fmt, nb, bstride, estride, bs,
             _ptr(block_table), block_table.stride(0), _ptr(seq_lens), B, q_len, H, int(max_context),
@@ -479,6 +504,9 @@ def gather_context(kv_cache, block_table, cu_seq_lens, seq_starts=None, *, fmt, 
     positions seq_starts[b] + i.  Returns dst [num_tokens, 576] bf16 (raw=False) or
     [num_tokens, entry bytes] uint8 (raw=True)."""
     fmt = _fmt(fmt)
+    done = (_step or _plain_step()).context(kv_cache, block_table, cu_seq_lens, seq_starts, fmt, num_tokens, raw, scale, dst)
+    if done is not None:
+        return done
     dev = _cuda_device(kv_cache)
     _need(kv_cache, "kv_cache", _BYTE_TYPES + (torch.bfloat16,), dev)
     _need(block_table, "block_table", (torch.int32,), dev, ndim=2)
@@ -492,7 +520,7 @@ def gather_context(kv_cache, block_table, cu_seq_lens, seq_starts=None, *, fmt, 
         dst = (torch.empty((num_tokens, ENTRY_BYTES[fmt]), dtype=torch.uint8, device=dev) if raw else
                torch.empty((num_tokens, 576), dtype=torch.bfloat16, device=dev))
     _need(dst, "dst", _BYTE_TYPES if raw else (torch.bfloat16,), dev, ndim=2)
-    nb, bstride, estride, bs = _cache_geometry(kv_cache)
+    nb, bstride, estride, bs = _cache_geometry(kv_cache, fmt)
     with torch.cuda.device(dev):
         _check(lib().mla_gather_context(_ptr(kv_cache), fmt, nb, bstride, estride, bs, _ptr(block_table),
                                         block_table.stride(0), _ptr(cu_seq_lens), _ptr(seq_starts), batch,
@@ -538,6 +566,24 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda in
 
 
 _marshal = None
+_step = None                # its functions for the cache's and the step's calls, or _DeclinedStep
+
+
+class _DeclinedStep:
+    """In place of the C marshalling of the cache's and the step's calls where it is not built."""
+    q_concat = key_concat = paged = context = rope = plan = staticmethod(lambda *args: None)
+
+
+def _plain_step():
+    """The C marshalling of the cache's and the step's calls: _plain's module."""
+    global _step
+    mod = _plain()
+    if hasattr(mod, "init_step"):
+        mod.init_step(torch.float16, torch.bool)
+        _step = mod
+    else:
+        _step = _DeclinedStep
+    return _step
 
 
 class _Declined:
@@ -885,7 +931,7 @@ def gather_dequant(kv_cache, slots, *, fmt):
     fmt = _fmt(fmt)
     dev = _cuda_device(kv_cache)
     _need(slots, "slots", (torch.int64,), dev, ndim=1, contiguous=True)
-    nb, bstride, estride, bs = _cache_geometry(kv_cache)
+    nb, bstride, estride, bs = _cache_geometry(kv_cache, fmt)
     out = torch.empty((slots.numel(), 576), dtype=torch.float32, device=dev)
     with torch.cuda.device(dev):
         _check(lib().mla_gather_dequant(_ptr(kv_cache), fmt, nb, bstride, estride, bs, _ptr(slots),
@@ -903,3 +949,141 @@ def debug_ds_cluster(size: int = 0) -> None:
     """Without effect, kept for its callers: fp8_ds_mla decodes run one CTA per group of 16 columns,
     with the results that every choice gave."""
     lib().mla_debug_ds_cluster(int(size))
+
+
+# ------------------------------------------------------------------------------------------ around a step
+
+_ROPE_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_ROPE_LAYOUTS = {"interleaved": False, "half": True}
+_ROPE_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rope_table(max_position, dim, *, base=10000.0, scaling=None, factor=1.0, original=0, beta_fast=32.0, beta_slow=1.0,
+               attn_scale=None, device=None):
+    """The table of rope and of the fused epilogues (dim 64 there): fp32 [max_position, dim], dim / 2 cosines, then dim / 2
+    sines of every position, from angles in 64 bits.  scaling: None, "linear" (positions interpolated by factor), "ntk"
+    (the base raised for factor) or "yarn" (pairs that turn more than beta_fast times over the `original` positions
+    as they are, less than beta_slow times interpolated, a ramp between).  attn_scale multiplies the table; None is
+    0.1 ln(factor) + 1 for yarn with a factor above 1, else 1."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(map(repr, _ROPE_SCALINGS))}, got {scaling!r}")
+    max_position, dim, original = int(max_position), int(dim), int(original)
+    if not 0 <= max_position < 2 ** 40 or not 2 <= dim <= 512 or dim % 2 or not abs(original) < 2 ** 62:
+        raise ValueError("max_position must be >= 0 and dim an even number from 2 to 512")
+    factor = float(factor)
+    if attn_scale is None:
+        attn_scale = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1.0 else 1.0
+    dev = torch.device("cuda" if device is None else device)
+    if dev.type != "cuda":
+        raise ValueError("the table is made on a CUDA device")
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    out = torch.empty((max_position, dim), dtype=torch.float32, device=dev)
+    _call(lib().mla_rope_table, dev, out.data_ptr(), max_position, dim, float(base), _ROPE_SCALINGS[scaling], factor, original,
+          float(beta_fast), float(beta_slow), float(attn_scale))
+    return out
+
+
+def _rope_at(at, width, R, name):
+    at = width - R if at is None else int(at)
+    if not 0 <= at <= width - R:
+        raise ValueError(f"{name}: {R} rotated values from {at} on do not fit {width}")
+    return at
+
+
+def rope(q, positions, cos_sin_cache, k=None, *, layout="interleaved", inverse=False, q_at=None, k_at=None, q_out=None, k_out=None):
+    """Rotary positions of q [T, H, D] and k [T, Hk, Dk] (bf16, fp16 or fp32) in one launch.  The R values from q_at / k_at on
+    (by default the last R of a head; R is the width of cos_sin_cache, see rope_table) turn by their token's angles, in
+    pairs (2i, 2i + 1) ("interleaved") or (i, i + R / 2) ("half"); the others are copied.  inverse=True turns back: the
+    transposed rotation, which takes the gradient of the output to the input's.  q_out / k_out: new tensors, or q / k
+    themselves (in place, both or neither).  Returns q_out, or (q_out, k_out) where k is given."""
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"layout must be 'interleaved' or 'half', got {layout!r}")
+    half = _ROPE_LAYOUTS[layout]
+    done = (_step or _plain_step()).rope(q, positions, cos_sin_cache, k, half, inverse, -1 if q_at is None else q_at, -1 if k_at is None else k_at,
+                                         q_out, k_out) if (q_at is None or q_at >= 0) and (k_at is None or k_at >= 0) else None
+    if done is not None:
+        return done
+    dev = _cuda_device(q)
+    types = tuple(_ROPE_TYPES)
+    qs = _strides(q, "q", types, dev, 3)
+    same = (q.dtype,)
+    T, H, D = q.shape
+    _strides(positions, "positions", _I64, dev, 1)
+    if positions.shape[0] != T:
+        raise ValueError(f"positions must have T = {T} entries")
+    _need(cos_sin_cache, "cos_sin_cache", _F32, dev, ndim=2, contiguous=True)
+    max_pos, R = cos_sin_cache.shape
+    if R < 2 or R % 2 or R > 512:
+        raise ValueError(f"cos_sin_cache must have an even width from 2 to 512, got {R}")
+
+    def out_of(x, out, name):
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        st = _strides(out, name, same, dev, 3)
+        if out.shape != x.shape:
+            raise ValueError(f"{name} must be {tuple(x.shape)}, got {tuple(out.shape)}")
+        return out, st
+
+    q_at = _rope_at(q_at, D, R, "q")
+    q_out, qos = out_of(q, q_out, "q_out")
+    k_args = [None, 0, 0, None, 0, 0, 0, 0, 0]
+    if k is not None:
+        ks = _strides(k, "k", same, dev, 3)
+        if k.shape[0] != T:
+            raise ValueError(f"k must have T = {T} tokens, got {k.shape[0]}")
+        k_at = _rope_at(k_at, k.shape[2], R, "k")
+        k_out, kos = out_of(k, k_out, "k_out")
+        k_args = [k.data_ptr(), ks[0], ks[1], k_out.data_ptr(), kos[0], kos[1], k.shape[1], k.shape[2], k_at]
+    elif k_out is not None or k_at is not None:
+        raise ValueError("k_out and k_at need k")
+    _call(lib().mla_rope, dev, _ROPE_TYPES[q.dtype], q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), qos[0], qos[1], H, D, q_at, *k_args,
+          positions.data_ptr(), cos_sin_cache.data_ptr(), max_pos, R, int(half), int(bool(inverse)), T)
+    return q_out if k is None else (q_out, k_out)
+
+
+def plan_step(seq_lens, new_lens, block_table, free_blocks, num_free, *, block_size, num_tokens, finished=None, seq_lens_out=None,
+              num_free_out=None, served=None, slot_mapping=None, positions=None, cu_q_lens=None):
+    """The blocks and slots of a step, without the host.  seq_lens int32 [B] (cached tokens), new_lens int32 [B] (tokens of the
+    step), block_table int32 [B, cols] and free_blocks int32 [capacity] (a stack, its top at num_free - 1; both written in
+    place), num_free int32 [1], finished bool [B] or None.  The blocks of finished requests go back to the stack, every
+    request takes those that its new tokens need, in order.  Returns (slot_mapping int64 [num_tokens], -1 in rows of no
+    request; positions int64 [num_tokens]; cu_q_lens int32 [B + 1]; the new lengths int32 [B]; the new num_free int32 [1]).
+    seq_lens_out and num_free_out may be seq_lens and num_free themselves; served (bool [B]) says which requests got
+    their blocks: the others keep their length, and their rows have slot -1 (device error 32)."""
+    done = (_step or _plain_step()).plan(seq_lens, new_lens, block_table, free_blocks, num_free, block_size, num_tokens, finished, seq_lens_out,
+                                         num_free_out, served, slot_mapping, positions, cu_q_lens)
+    if done is not None:
+        return done
+    dev = _cuda_device(seq_lens)
+    _strides(seq_lens, "seq_lens", _I32, dev, 1)
+    B = seq_lens.shape[0]
+    T, block_size = int(num_tokens), int(block_size)
+    if B < 1 or not 0 <= T <= _INT32_MAX or not 1 <= block_size <= _INT32_MAX:
+        raise ValueError("at least one request, num_tokens >= 0 and block_size >= 1 are needed")
+    table, tstride, cols = _table(block_table, B, dev)
+
+    def vector(t, name, types, n, new=True):
+        if t is None and new:
+            t = torch.empty((n,), dtype=types[0], device=dev)
+        _strides(t, name, types, dev, 1)
+        if t.shape[0] != n:
+            raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+        return t
+
+    vector(new_lens, "new_lens", _I32, B, False)
+    vector(num_free, "num_free", _I32, 1, False)
+    _strides(free_blocks, "free_blocks", _I32, dev, 1)
+    flags = (torch.bool, torch.uint8)
+    if finished is not None:
+        vector(finished, "finished", flags, B, False)
+    slot_mapping = vector(slot_mapping, "slot_mapping", _I64, T)
+    positions = vector(positions, "positions", _I64, T)
+    cu_q_lens = vector(cu_q_lens, "cu_q_lens", _I32, B + 1)
+    seq_lens_out = vector(seq_lens_out, "seq_lens_out", _I32, B)
+    num_free_out = vector(num_free_out, "num_free_out", _I32, 1)
+    served = vector(served, "served", flags, B)
+    _call(lib().mla_plan_step, dev, seq_lens.data_ptr(), new_lens.data_ptr(), None if finished is None else finished.data_ptr(), table,
+          tstride, cols, free_blocks.data_ptr(), free_blocks.shape[0], num_free.data_ptr(), seq_lens_out.data_ptr(),
+          num_free_out.data_ptr(), served.data_ptr(), cu_q_lens.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), B, T, block_size)
+    return slot_mapping, positions, cu_q_lens, seq_lens_out, num_free_out

@@ -26,7 +26,7 @@ MARSHAL = os.path.join(BUILD, "mla_marshal" + (sysconfig.get_config_var("EXT_SUF
 
 SOURCES = ["mla_api.cu", "mla_small_kernels.cu", "mla_attn_bf16.cu", "mla_attn_fp8.cu", "mla_attn_ds.cu",
            "mla_noalloc.cu", "mla_paged_tma_bf16.cu", "mla_paged_tma_fp8.cu", "mla_ds.cu", "mla_fp4.cu", "mla_head_bmm.cu",
-           "mla_index.cu", "mla_index_scores.cu", "mla_index_api.cu"]
+           "mla_index.cu", "mla_index_scores.cu", "mla_index_api.cu", "mla_rope.cu", "mla_plan.cu", "mla_step_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
