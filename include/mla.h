@@ -273,6 +273,14 @@ MLA_API size_t mla_paged_decode_workspace_size(int32_t B, int32_t q_len, int32_t
                                        int32_t num_sms);
 
 /*
+ * The same for a cache of the given format.  The others' is mla_paged_decode_workspace_size; the decode of MLA_CACHE_MXFP4
+ * cuts the keys of all requests into equal runs, one a CTA, and needs room for two partial results of each: its size
+ * depends on (B, q_len * H, the SM count) only, and is never 0.
+ */
+MLA_API size_t mla_paged_decode_workspace_size_for(mla_cache_format fmt, int32_t B, int32_t q_len, int32_t H,
+                                                   int32_t max_context, int32_t num_sms);
+
+/*
  * Paged MLA decode and spec-verify.
  * Follows: "vllm.models.kimi_k3.nvidia.specialized_decode.cutedsl.mla.prepared" --
  * PreparedMla.stock_core / trtllm_decode (q query tokens per request, causal among them;
@@ -294,7 +302,7 @@ MLA_API size_t mla_paged_decode_workspace_size(int32_t B, int32_t q_len, int32_t
  *                multiplied by k_scale; q_scale / k_scale are ignored for the other caches.
  *   out          device bf16 [B * q_len, H, >= 512], strides (o_s0, o_s1).
  *   lse          device fp32 [B * q_len, H] contiguous, natural log; NULL to skip.
- *   workspace    device scratch of >= mla_paged_decode_workspace_size(...) bytes, 256-byte
+ *   workspace    device scratch of >= mla_paged_decode_workspace_size_for(fmt, ...) bytes, 256-byte
  *                aligned (may be NULL when that size is 0).  Contents need no initialising
  *                and are garbage afterwards.
  * A query row with no visible key gets out = 0 and lse = -inf.
@@ -318,7 +326,7 @@ MLA_API int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const vo
  * to a scratch array inside the library (a file-scope __device__ buffer of 64 MiB, held on
  * every device where the library's code is loaded until the process exits).  The call
  * allocates nothing.
- *   - Shapes whose split-K scratch (mla_paged_decode_workspace_size) exceeds 64 MiB are
+ *   - Shapes whose split-K scratch (mla_paged_decode_workspace_size_for) exceeds 64 MiB are
  *     rejected with MLA_ERR_UNSUPPORTED and a message in mla_last_error().
  *   - The first call on a device looks up the scratch's device address (once per device, with
  *     that device current); make that first call before any stream capture.

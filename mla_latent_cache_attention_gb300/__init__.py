@@ -86,6 +86,8 @@ def lib():
                                      i32, i32, vp]
         L.mla_paged_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32]
         L.mla_paged_decode_workspace_size.restype = sz
+        L.mla_paged_decode_workspace_size_for.argtypes = [i32, i32, i32, i32, i32, i32]
+        L.mla_paged_decode_workspace_size_for.restype = sz
         L.mla_paged_decode.argtypes = [vp, i64, i64, vp, i32, i64, i64, i64, i32, vp, i64, vp, i32, i32, i32,
                                        i32, f32, f32, f32, vp, i64, i64, vp, vp, sz, vp]
         L.mla_paged_decode_noalloc.argtypes = [vp, i64, i64, vp, i32, i64, i64, i64, i32, vp, i64, vp, i32, i32,
@@ -408,8 +410,11 @@ def sparse_fwd(q, kv_records, kv_indptr, kv_indices, softmax_scale, *, has_inval
     return out, lse
 
 
-def paged_decode_workspace_size(B, q_len, H, max_context, num_sms=0) -> int:
-    return int(lib().mla_paged_decode_workspace_size(B, q_len, H, max_context, num_sms))
+def paged_decode_workspace_size(B, q_len, H, max_context, num_sms=0, fmt=None) -> int:
+    """Bytes of workspace of a paged_decode; fmt has to be given for the mxfp4 cache, whose decode splits in its own way."""
+    if fmt is None:
+        return int(lib().mla_paged_decode_workspace_size(B, q_len, H, max_context, num_sms))
+    return int(lib().mla_paged_decode_workspace_size_for(_fmt(fmt), B, q_len, H, max_context, num_sms))
 
 
 def paged_decode(q, kv_cache, block_table, seq_lens, *, fmt, q_len=1, max_context, softmax_scale,
@@ -440,7 +445,7 @@ def paged_decode(q, kv_cache, block_table, seq_lens, *, fmt, q_len=1, max_contex
         if tuple(lse.shape) != (rows, H):
             raise ValueError(f"lse must be [B * q_len, H] = {(rows, H)}")
     with torch.cuda.device(dev):
-        need = paged_decode_workspace_size(B, q_len, H, max_context)
+        need = paged_decode_workspace_size(B, q_len, H, max_context, fmt=fmt)
         if workspace is None and need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         if workspace is not None:

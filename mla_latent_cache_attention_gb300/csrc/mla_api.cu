@@ -207,12 +207,6 @@ struct ColPlan {
   int nq, G, box_h, box_q;
 };
 bool plan_columns(int fmt, int H, int q_len, ColPlan* cp) {
-  if (fmt == MLA_CACHE_MXFP4) {      // 16 or 32 consecutive columns of any shape: its query is read without a box
-    const int64_t cols = static_cast<int64_t>(H) * q_len;
-    const int nq = cols <= 16 ? 16 : 32;
-    *cp = ColPlan{nq, static_cast<int>((cols + nq - 1) / nq), 0, 0};
-    return true;
-  }
   const int nqmax = fmt == MLA_CACHE_BF16 ? 32 : 64;
   const int cols = H * q_len;
   if (cols <= nqmax) {
@@ -723,6 +717,101 @@ extern "C" size_t mla_paged_decode_workspace_size(int32_t B, int32_t q_len, int3
   return workspace_bytes_for(n_rows, H, sp);
 }
 
+extern "C" size_t mla_paged_decode_workspace_size_for(mla_cache_format fmt, int32_t B, int32_t q_len, int32_t H,
+                                                      int32_t max_context, int32_t num_sms) {
+  if (fmt != MLA_CACHE_MXFP4) return mla_paged_decode_workspace_size(B, q_len, H, max_context, num_sms);
+  if (B <= 0 || q_len <= 0 || H <= 0 || max_context <= 0) return 0;
+  if (num_sms <= 0) {
+    DevInfo* d = nullptr;
+    if (dev_info(&d) != MLA_OK) return 0;
+    num_sms = d->sms;
+  }
+  return fp4_workspace_bytes(B, q_len, H, num_sms);
+}
+
+// ---- mxfp4: equal runs of tiles (mla_fp4.cuh)
+namespace {
+
+// Query columns of a CTA, their groups, and the runs: as many as the SMs have room for beside the groups.
+struct Fp4Plan {
+  int nq;
+  int64_t G, W;
+};
+Fp4Plan fp4_plan(int q_len, int H, int sms) {
+  const int64_t cols = static_cast<int64_t>(q_len) * H;
+  const int nq = cols <= 16 ? 16 : 32;
+  const int64_t G = (cols + nq - 1) / nq;
+  return Fp4Plan{nq, G, sms > G ? sms / G : 1};
+}
+
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t mla::fp4_workspace_bytes(int64_t B, int q_len, int H, int sms) {
+  const size_t parts = static_cast<size_t>(2 * fp4_plan(q_len, H, sms).W) * q_len * H;
+  return round256(parts * kLora * sizeof(float)) + round256(parts * sizeof(float)) + round256((B + 1) * sizeof(int64_t));
+}
+
+int mla::run_fp4_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache, int64_t num_blocks,
+                        int64_t block_stride_bytes, int64_t entry_stride_bytes, int32_t block_size, const int32_t* block_table,
+                        int64_t bt_stride, const int32_t* seq_lens, int32_t B, int32_t q_len, int32_t H, float softmax_scale,
+                        void* out, int64_t o_s0, int64_t o_s1, float* lse, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream) {
+  DevInfo* d = nullptr;
+  if (int rc = dev_info(&d)) return rc;
+  const Fp4Plan plan = fp4_plan(q_len, H, d->sms);
+  if (static_cast<int64_t>(B) * q_len * H >= (int64_t(1) << 31) || plan.G * plan.W >= (int64_t(1) << 31))
+    return fail(MLA_ERR_UNSUPPORTED, "too many rows");
+  if (block_stride_bytes >= (int64_t(1) << 32)) return fail(MLA_ERR_UNSUPPORTED, "mxfp4 blocks must be below 4 GB");
+  const size_t need = fp4_workspace_bytes(B, q_len, H, d->sms);
+  if (!workspace || workspace_bytes < need)
+    return fail(MLA_ERR_INVALID, "workspace too small: need %zu bytes, got %zu", need, workspace_bytes);
+  if (!aligned(workspace, 256)) return fail(MLA_ERR_INVALID, "workspace must be 256-byte aligned");
+  const size_t parts = static_cast<size_t>(2 * plan.W) * q_len * H;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  Fp4Params p{};
+  p.q = static_cast<const uint8_t*>(q);
+  p.q_s0b = q_s0 * 2;
+  p.q_s1b = q_s1 * 2;
+  p.kv = static_cast<const uint8_t*>(kv_cache);
+  p.blk_stride = static_cast<uint32_t>(block_stride_bytes);
+  p.ent_stride = static_cast<uint32_t>(entry_stride_bytes);
+  p.H = H;
+  p.q_len = q_len;
+  p.B = B;
+  p.G = static_cast<int>(plan.G);
+  p.cols = H * q_len;
+  p.block_table = block_table;
+  p.bt_stride = bt_stride;
+  p.seq_lens = seq_lens;
+  p.num_blocks = static_cast<uint32_t>(num_blocks < (int64_t(1) << 31) ? num_blocks : int64_t(1) << 31);
+  p.block_size = block_size;
+  p.bs_shift = (block_size & (block_size - 1)) == 0 ? 31 - __builtin_clz(static_cast<unsigned>(block_size)) : -1;
+  p.W = static_cast<int>(plan.W);
+  p.sig2 = softmax_scale * 1.4426950408889634f;
+  p.out = static_cast<uint8_t*>(out);
+  p.o_s0b = o_s0 * 2;
+  p.o_s1b = o_s1 * 2;
+  p.lse = lse;
+  p.part_o = reinterpret_cast<float*>(ws);
+  p.part_lse = reinterpret_cast<float*>(ws + round256(parts * kLora * sizeof(float)));
+  p.first = reinterpret_cast<int64_t*>(ws + round256(parts * kLora * sizeof(float)) + round256(parts * sizeof(float)));
+  p.err = d->err;
+  p.wait_us = g_stall_next_us;
+  p.stall = g_stall_next_us > 0 ? 1 : 0;
+  g_stall_next_us = 0;
+  p.two16 = 1u << 16;
+  p.two31 = 1u << 31;
+  prof_begin(stream);
+  cudaError_t e = launch_fp4_paged(plan.nq, p, stream);
+  prof_end(stream);
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "decode attention launch failed: %s", cudaGetErrorString(e));
+  if (launch_fp4_merge(p, stream) != cudaSuccess)
+    return fail(MLA_ERR_CUDA, "merge launch failed: %s", cudaGetErrorString(cudaGetLastError()));
+  return ok();
+}
+
 int mla::check_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache, int fmt, int64_t num_blocks,
                             int64_t block_stride_bytes, int64_t entry_stride_bytes, int32_t block_size,
                             const int32_t* block_table, int64_t bt_stride, const int32_t* seq_lens, int32_t B,
@@ -763,6 +852,9 @@ extern "C" int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const
   if (B == 0) return ok();
   DevInfo* d = nullptr;
   if (int rc = dev_info(&d)) return rc;
+  if (fmt == MLA_CACHE_MXFP4)
+    return run_fp4_decode(q, q_s0, q_s1, kv_cache, num_blocks, block_stride_bytes, entry_stride_bytes, block_size, block_table, bt_stride,
+                          seq_lens, B, q_len, H, softmax_scale, out, o_s0, o_s1, lse, workspace, workspace_bytes, stream);
   return run_paged_decode(q, q_s0, q_s1, kv_cache, fmt, num_blocks, block_stride_bytes, entry_stride_bytes, block_size,
                           block_table, bt_stride, seq_lens, B, q_len, H, max_context, softmax_scale, q_scale, k_scale, out,
                           o_s0, o_s1, lse, workspace, workspace_bytes,
@@ -1009,53 +1101,6 @@ int mla::run_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void*
     prof_begin(stream);
     e = fmt == MLA_CACHE_BF16 ? launch_paged_tma_bf16(cp.nq, p, &tkv, &tq, grid, stream)
                               : launch_paged_tma_fp8(cp.nq, p, &tkv, &tq, grid, stream);
-    prof_end(stream);
-  } else if (fmt == MLA_CACHE_MXFP4) {
-    plan_columns(MLA_CACHE_MXFP4, H, q_len, &cp);
-    const int64_t items = static_cast<int64_t>(sp.n_splits) * B * cp.G;
-    if (items >= (int64_t(1) << 31) - (1 << 20)) return fail(MLA_ERR_UNSUPPORTED, "too many work items");
-    if (max_context >= (1 << 30)) return fail(MLA_ERR_UNSUPPORTED, "max_context must be below 2^30");
-    if (block_stride_bytes >= (int64_t(1) << 32)) return fail(MLA_ERR_UNSUPPORTED, "mxfp4 blocks must be below 4 GB");
-    Fp4Params p{};
-    p.q = static_cast<const uint8_t*>(q);
-    p.q_s0b = q_s0 * 2;
-    p.q_s1b = q_s1 * 2;
-    p.kv = static_cast<const uint8_t*>(kv_cache);
-    p.blk_stride = static_cast<uint32_t>(block_stride_bytes);
-    p.ent_stride = static_cast<uint32_t>(entry_stride_bytes);
-    p.H = H;
-    p.q_len = q_len;
-    p.B = B;
-    p.G = cp.G;
-    p.cols = H * q_len;
-    p.block_table = block_table;
-    p.bt_stride = bt_stride;
-    p.seq_lens = seq_lens;
-    p.num_blocks = static_cast<uint32_t>(num_blocks < (int64_t(1) << 31) ? num_blocks : int64_t(1) << 31);
-    p.block_size = block_size;
-    p.bs_shift = (block_size & (block_size - 1)) == 0 ? 31 - __builtin_clz(static_cast<unsigned>(block_size)) : -1;
-    p.chunk = static_cast<int>(sp.chunk);
-    p.n_splits = sp.n_splits;
-    p.n_items = static_cast<int>(items);
-    p.n_rows = static_cast<int>(n_rows);
-    p.sig2 = softmax_scale * 1.4426950408889634f;
-    p.out = static_cast<uint8_t*>(out);
-    p.o_s0b = o_s0 * 2;
-    p.o_s1b = o_s1 * 2;
-    p.lse = lse;
-    p.part_o = part_o;
-    p.part_lse = part_lse;
-    p.sched = sched;
-    p.err = d->err;
-    p.wait_us = g_stall_next_us;
-    p.stall = g_stall_next_us > 0 ? 1 : 0;
-    g_stall_next_us = 0;
-    if (sched && !sched_ready && launch_sched_reset(sched, stream) != cudaSuccess)
-      return fail(MLA_ERR_CUDA, "scheduler reset failed: %s", cudaGetErrorString(cudaGetLastError()));
-    prof_begin(stream);
-    p.two16 = 1u << 16;
-    p.two31 = 1u << 31;
-    e = launch_fp4_paged(cp.nq, p, grid_for(items, d->sms), stream);
     prof_end(stream);
   } else {
     const int64_t items = n_rows * n_hgroups * sp.n_splits;

@@ -9,8 +9,11 @@
 // as zero.)
 //
 // How (GB300 design):
-//   * One work item = one request x one group of NQ query columns (a column is a (query token, head) pair) x
-//     one split of its keys.  Tiles of 128 keys, two in shared memory: 4 x 16 KB of E4M3 and 16 KB of bf16 k_pe
+//   * The key tiles of all requests, one after the other, are cut into equal runs, one for each CTA of a group of NQ query
+//     columns (a column is a (query token, head) pair); the CTAs of all groups take the same run side by side and meet
+//     its records in L2.  Where a run begins or ends inside a request its part is a partial result, at most two a CTA,
+//     which a second kernel joins; the lengths are read on the GPU, so a captured graph stays balanced.  (Splits of
+//     equal length, handed out by a counter: 32 requests of 1024 to 8192 keys 63 us.)  Tiles of 128 keys, two in shared memory: 4 x 16 KB of E4M3 and 16 KB of bf16 k_pe
 //     each, K-major with 128-byte swizzle, read by both products.
 //   * Sixteen loader warps take 8 keys of a tile each: 16-byte loads straight from the pages (a lane holds one
 //     group: 32 codes and their exponent) one tile ahead in registers, block ids two tiles ahead.  A group's
@@ -47,14 +50,14 @@ struct Fp4Params {
   const int32_t* seq_lens;
   uint32_t num_blocks;
   int block_size, bs_shift;       // bs_shift: log2 of it, or -1
-  int chunk, n_splits, n_items, n_rows;
+  int W;                          // runs of tiles: the grid is W x G
   float sig2;                     // softmax scale * log2(e)
   uint8_t* out;
   int64_t o_s0b, o_s1b;
   float* lse;
-  float* part_o;                  // [n_splits][n_rows][H][512] fp32 (n_splits > 1)
-  float* part_lse;
-  uint32_t* sched;
+  float* part_o;                  // [2 W][q_len * H][512] fp32: slot 2 w + 1 a request that begins in run w and goes on,
+  float* part_lse;                // slot 2 w one that began before
+  int64_t* first;                 // [B + 1]: first tile of every request with keys; [B]: tiles of a run
   uint32_t* err;
   int wait_us, stall;             // test aids, as in PagedParams
   uint32_t two16, two31;          // 2^16, 2^31
@@ -185,32 +188,59 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
 
   if (warp == 0) {
     // ------------------------------------------------------------------ scheduler
+    auto tiles_of = [&](int b) -> int64_t { return (static_cast<int64_t>(max(p.seq_lens[b], 0)) + kTile - 1) / kTile; };
+    // a lane sums a run of requests; the lane that holds this CTA's first tile looks for its request
+    const int per_lane = (p.B + 31) / 32, b0 = min(lane * per_lane, p.B), b1 = min(b0 + per_lane, p.B);
+    int64_t sum = 0;
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) sum += tiles_of(b);
+    int64_t end = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, end, o);
+      if (lane >= o) end += v;
+    }
+    const int64_t total = __shfl_sync(0xFFFFFFFFu, end, 31), run = total > 0 ? (total + p.W - 1) / p.W : 1;
+    const int w = static_cast<int>(blockIdx.x) / p.G, g = static_cast<int>(blockIdx.x) % p.G;
+    const int64_t lo = min(w * run, total), hi = min(lo + run, total);
+    int b = p.B;
+    int64_t t0 = end - sum;      // first tile of request b
+    if (lo < hi && t0 <= lo && lo < end) {
+      b = b0;
+      for (int64_t n; (n = tiles_of(b)) <= lo - t0; ++b) t0 += n;
+    }
+    const uint32_t who = __ballot_sync(0xFFFFFFFFu, b < p.B);
+    const int src = who ? __ffs(who) - 1 : 0;
+    b = __shfl_sync(0xFFFFFFFFu, b, src);
+    t0 = __shfl_sync(0xFFFFFFFFu, t0, src);
     if (lane == 0) {
-      int stride_k = 0, nitem = 0;
-      for (;;) {
+      if (blockIdx.x == 0) p.first[p.B] = run;
+      int64_t t = lo;
+      for (int nitem = 0;; ++nitem) {
         WorkItem it{};
-        for (;;) {      // the next ticket with work (empty splits are skipped: the merge ignores them)
-          const int item = p.sched ? static_cast<int>(atomicAdd(p.sched, 1u)) : static_cast<int>(blockIdx.x + stride_k * gridDim.x);
-          ++stride_k;
-          it.b = -1;
-          if (item >= p.n_items || item < 0) break;
-          const int bg = p.B * p.G;
-          it.s = item / bg;
-          it.b = (item % bg) / p.G;
-          it.g = item % p.G;
-          it.L = max(p.seq_lens[it.b], 0);
-          const int64_t k0 = static_cast<int64_t>(it.s) * p.chunk;
-          const int left = k0 < it.L ? it.L - static_cast<int>(k0) : 0;
-          it.k0 = left > 0 ? static_cast<int>(k0) : 0;
-          it.n = it.s == p.n_splits - 1 ? left : min(left, p.chunk);      // the last split takes what passes max_context
-          it.ntiles = (it.n >> 7) + ((it.n & 127) ? 1 : 0);
-          if (it.n > 0 || p.n_splits == 1) break;
+        it.b = -1;
+        if (t < hi) {
+          const int64_t n = tiles_of(b);
+          it.b = b;
+          it.g = g;
+          it.L = p.seq_lens[b];
+          it.ntiles = static_cast<int>(min(hi, t0 + n) - t);
+          it.k0 = static_cast<int>((t - t0) * kTile);
+          it.n = static_cast<int>(min(static_cast<int64_t>(it.L) - it.k0, static_cast<int64_t>(it.ntiles) * kTile));
+          it.pad = it.ntiles == n;                      // the whole request: final
+          it.s = 2 * w + (t == t0 ? 1 : 0);
+          if (t == t0 && g == 0) p.first[b] = t0;
+          t += it.ntiles;
+          if (t == t0 + n) {
+            t0 = t;
+            do ++b;
+            while (b < p.B && p.seq_lens[b] <= 0);
+          }
         }
         const int k = nitem % kItemDepth;
         if (nitem >= kItemDepth && !mbar_wait(&item_empty[k], static_cast<uint32_t>((nitem / kItemDepth) - 1) & 1u, abort_flag)) break;
         items[k] = it;
         mbar_arrive(&item_full[k]);
-        ++nitem;
         if (it.b < 0) break;
       }
     }
@@ -232,7 +262,6 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         mbar_arrive(&item_empty[k]);
         ++nit;
         if (it.b < 0) break;
-        if (it.ntiles == 0) continue;
         if (!mbar_wait(q_full, nq & 1, abort_flag)) break;
         ++nq;
         for (int t = 0; t < it.ntiles && ok; ++t) {
@@ -352,7 +381,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         c.kp = k0 + KW * w + key;
         c.end = k0 + n;
         c.left = ntiles - 1;
-        if (b < 0 || ntiles > 0) return;
+        return;
       }
     };
     auto advance = [&](Cursor& c) {
@@ -557,7 +586,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       if (stid < NQ) mref[stid] = -3e38f;         // no reference yet: every logit passes it, and -inf - m is no NaN
       if (!named_bar_and(1, NT, w)) break;
       if (it.b < 0) break;
-      if (it.ntiles > 0 && !q_ready) prep_query(it);
+      if (!q_ready) prep_query(it);
       q_ready = false;
       const int cgb = it.g * NQ + c0;             // global column of this thread's first
       float l_part[NC];
@@ -719,15 +748,14 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       const bool more = warp_wait(&item_full[nit % kItemDepth], (nit / kItemDepth) & 1, abort_flag);
       if (named_bar_and(1, NT, more)) {
         const WorkItem qi = items[nit % kItemDepth];
-        if (qi.b >= 0 && qi.ntiles > 0) {
+        if (qi.b >= 0) {
           prep_query(qi);
           q_ready = true;
         }
       }
       // ---- epilogue: O / l and the LSE of every column of the item
       if (stid == 0) TL(3, 6);
-      w = true;
-      if (it.ntiles > 0) {
+      {
         w = warp_wait(&pv_part[((g + it.ntiles - 1) & 1) * C::kParts + C::kParts - 1], static_cast<uint32_t>((g + it.ntiles - 1) >> 1) & 1u, abort_flag);
         tc_fence_after();
       }
@@ -747,24 +775,21 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         inv_l = none ? 0.f : __fdividef(1.f, l);
         lse_l = none ? -CUDART_INF_F : (mref[cl] + __log2f(l)) * 0.69314718055994531f;
       }
-      const bool final_out = p.n_splits == 1;
-      // (row, head) of column cg: the flat index row * H + head is b * q_len * H + cg
-      const int64_t flat0 = static_cast<int64_t>(it.b) * p.q_len * p.H + cgb;
+      const bool final_out = it.pad != 0;
+      // (row, head) of column cg: the flat index row * H + head is b * q_len * H + cg; a partial's is s * q_len * H + cg
+      const int64_t flat0 = static_cast<int64_t>(final_out ? it.b : it.s) * p.cols + cgb;
       const int ncol = min(NC, p.cols - cgb);       // may be none
       const int64_t o_wrap = p.o_s0b - static_cast<int64_t>(p.H) * p.o_s1b;
 #pragma unroll 1
       for (int jj = 0; jj < 4 && ncol > 0; ++jj) {
         float o[NC];
-        if (it.ntiles > 0) {
+        {
           float lo[NC];
           tmem_ld16(tl + C::kTmemO + 2 * NQ * jj + c0, o);
           tmem_ld16(tl + C::kTmemO + 2 * NQ * jj + NQ + c0, lo);
           tmem_ld_wait();
 #pragma unroll
           for (int c = 0; c < NC; ++c) o[c] = fmaf(lo[c], 0.0625f, o[c]);
-        } else {
-#pragma unroll
-          for (int c = 0; c < NC; ++c) o[c] = 0.f;
         }
         const int d = 128 * jj + row;
         if (final_out) {
@@ -782,7 +807,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
             }
           }
         } else {
-          float* dst = p.part_o + ((static_cast<int64_t>(it.s) * p.n_rows * p.H + flat0) * kLora + d);
+          float* dst = p.part_o + (flat0 * kLora + d);
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             const float iv = __shfl_sync(0xFFFFFFFFu, inv_l, c);
@@ -794,7 +819,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         if (final_out) {
           if (p.lse) p.lse[flat0 + lane] = lse_l;
         } else {
-          p.part_lse[static_cast<int64_t>(it.s) * p.n_rows * p.H + flat0 + lane] = lse_l;
+          p.part_lse[flat0 + lane] = lse_l;
         }
       }
       tc_fence_before();

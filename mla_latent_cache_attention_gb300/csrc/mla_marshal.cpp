@@ -563,7 +563,8 @@ PyObject* py_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   int64_t bytes = 0;
   if (a[12] == Py_None) {
-    bytes = static_cast<int64_t>(mla_paged_decode_workspace_size(static_cast<int32_t>(B), q_len, static_cast<int32_t>(H), ctx, 0));
+    bytes = static_cast<int64_t>(mla_paged_decode_workspace_size_for(static_cast<mla_cache_format>(fmt), static_cast<int32_t>(B), q_len,
+                                                                     static_cast<int32_t>(H), ctx, 0));
     if (bytes > 0 && !output(a[12], dev, 1, &bytes, g_u8, nullptr, device.p, &ws, &work)) return not_plain();
   } else {
     if (!read(a[12], dev, 1, &ws, g_u8, g_i8)) return not_plain();

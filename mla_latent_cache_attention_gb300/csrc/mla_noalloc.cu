@@ -71,7 +71,7 @@ extern "C" int mla_paged_decode_noalloc(const void* q, int64_t q_s0, int64_t q_s
                                         float softmax_scale, float q_scale, float k_scale, void* out,
                                         int64_t o_s0, int64_t o_s1, float* lse, cudaStream_t stream) {
   if (B > 0 && q_len > 0 && H > 0 && max_context > 0) {
-    const size_t need = mla_paged_decode_workspace_size(B, q_len, H, max_context, 0);
+    const size_t need = mla_paged_decode_workspace_size_for(fmt, B, q_len, H, max_context, 0);
     if (need > kNoAllocScratchBytes) {
       char msg[256];
       snprintf(msg, sizeof msg,

@@ -379,7 +379,7 @@ def test_captured_and_replayed(m):
         q = m.q_concat_cache_insert(ql, qpe, lat, kpe, cache, slots, fmt="mxfp4")
         return m.paged_decode(q, cache, table, seq, fmt="mxfp4", max_context=9000, softmax_scale=SCALE, return_lse=True, workspace=ws)
 
-    n = m.paged_decode_workspace_size(B, 1, H, 9000)
+    n = m.paged_decode_workspace_size(B, 1, H, 9000, fmt="mxfp4")
     graphs = []
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
