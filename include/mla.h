@@ -275,7 +275,7 @@ MLA_API size_t mla_paged_decode_workspace_size(int32_t B, int32_t q_len, int32_t
 /*
  * The same for a cache of the given format.  The others' is mla_paged_decode_workspace_size; the decode of MLA_CACHE_MXFP4
  * cuts the keys of all requests into equal runs, one a CTA, and needs room for two partial results of each: its size
- * depends on (B, q_len * H, the SM count) only, and is never 0.
+ * depends on q_len * H and the SM count only.
  */
 MLA_API size_t mla_paged_decode_workspace_size_for(mla_cache_format fmt, int32_t B, int32_t q_len, int32_t H,
                                                    int32_t max_context, int32_t num_sms);

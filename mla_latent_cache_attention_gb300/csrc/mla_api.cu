@@ -726,7 +726,7 @@ extern "C" size_t mla_paged_decode_workspace_size_for(mla_cache_format fmt, int3
     if (dev_info(&d) != MLA_OK) return 0;
     num_sms = d->sms;
   }
-  return fp4_workspace_bytes(B, q_len, H, num_sms);
+  return fp4_workspace_bytes(q_len, H, num_sms);
 }
 
 // ---- mxfp4: equal runs of tiles (mla_fp4.cuh)
@@ -748,9 +748,9 @@ size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
 }  // namespace
 
-size_t mla::fp4_workspace_bytes(int64_t B, int q_len, int H, int sms) {
+size_t mla::fp4_workspace_bytes(int q_len, int H, int sms) {
   const size_t parts = static_cast<size_t>(2 * fp4_plan(q_len, H, sms).W) * q_len * H;
-  return round256(parts * kLora * sizeof(float)) + round256(parts * sizeof(float)) + round256((B + 1) * sizeof(int64_t));
+  return round256(parts * kLora * sizeof(float)) + round256(parts * sizeof(float)) + round256((2 * static_cast<size_t>(fp4_plan(q_len, H, sms).W) + 1) * sizeof(int64_t));
 }
 
 int mla::run_fp4_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache, int64_t num_blocks,
@@ -764,7 +764,7 @@ int mla::run_fp4_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* k
   if (static_cast<int64_t>(B) * q_len * H >= (int64_t(1) << 31) || plan.G * plan.W >= (int64_t(1) << 31))
     return fail(MLA_ERR_UNSUPPORTED, "too many rows");
   if (block_stride_bytes >= (int64_t(1) << 32)) return fail(MLA_ERR_UNSUPPORTED, "mxfp4 blocks must be below 4 GB");
-  const size_t need = fp4_workspace_bytes(B, q_len, H, d->sms);
+  const size_t need = fp4_workspace_bytes(q_len, H, d->sms);
   if (!workspace || workspace_bytes < need)
     return fail(MLA_ERR_INVALID, "workspace too small: need %zu bytes, got %zu", need, workspace_bytes);
   if (!aligned(workspace, 256)) return fail(MLA_ERR_INVALID, "workspace must be 256-byte aligned");
@@ -787,7 +787,8 @@ int mla::run_fp4_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* k
   p.seq_lens = seq_lens;
   p.num_blocks = static_cast<uint32_t>(num_blocks < (int64_t(1) << 31) ? num_blocks : int64_t(1) << 31);
   p.block_size = block_size;
-  p.bs_shift = (block_size & (block_size - 1)) == 0 ? 31 - __builtin_clz(static_cast<unsigned>(block_size)) : -1;
+  while ((int64_t(1) << p.bs_shift) < block_size) ++p.bs_shift;
+  p.bs_magic = static_cast<uint32_t>(((uint64_t(1) << (31 + p.bs_shift)) + block_size - 1) / block_size);
   p.W = static_cast<int>(plan.W);
   p.sig2 = softmax_scale * 1.4426950408889634f;
   p.out = static_cast<uint8_t*>(out);
@@ -796,7 +797,7 @@ int mla::run_fp4_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* k
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_lse = reinterpret_cast<float*>(ws + round256(parts * kLora * sizeof(float)));
-  p.first = reinterpret_cast<int64_t*>(ws + round256(parts * kLora * sizeof(float)) + round256(parts * sizeof(float)));
+  p.span = reinterpret_cast<int64_t*>(ws + round256(parts * kLora * sizeof(float)) + round256(parts * sizeof(float)));
   p.err = d->err;
   p.wait_us = g_stall_next_us;
   p.stall = g_stall_next_us > 0 ? 1 : 0;

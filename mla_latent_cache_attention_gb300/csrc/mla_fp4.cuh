@@ -49,7 +49,8 @@ struct Fp4Params {
   int64_t bt_stride;
   const int32_t* seq_lens;
   uint32_t num_blocks;
-  int block_size, bs_shift;       // bs_shift: log2 of it, or -1
+  int block_size, bs_shift;       // n / block_size = n bs_magic / 2^(31 + bs_shift) for n < 2^31: bs_shift = ceil(log2(block_size)),
+  uint32_t bs_magic;              // bs_magic = ceil(2^(31 + bs_shift) / block_size)
   int W;                          // runs of tiles: the grid is W x G
   float sig2;                     // softmax scale * log2(e)
   uint8_t* out;
@@ -57,7 +58,8 @@ struct Fp4Params {
   float* lse;
   float* part_o;                  // [2 W][q_len * H][512] fp32: slot 2 w + 1 a request that begins in run w and goes on,
   float* part_lse;                // slot 2 w one that began before
-  int64_t* first;                 // [B + 1]: first tile of every request with keys; [B]: tiles of a run
+  int64_t* span;                  // [W][2]: first tile and number of the request that begins in run w and goes on (-1: none),
+                                  // then the tiles of a run
   uint32_t* err;
   int wait_us, stall;             // test aids, as in PagedParams
   uint32_t two16, two31;          // 2^16, 2^31
@@ -69,7 +71,7 @@ struct Fp4Cfg {
   static constexpr int NQ = NQ_, NB = 5;
   static constexpr int NC = 16;                                   // columns of a softmax thread
   static constexpr int kSW = 4 * (NQ / NC);                       // softmax warps: two column halves where NQ = 32
-  static constexpr int kLoadWarps = 16, kPvWarp = 2, kFirstSm = 4, kFirstLoad = kFirstSm + kSW;
+  static constexpr int kLoadWarps = 8, kPvWarp = 2, kFirstSm = 4, kFirstLoad = kFirstSm + kSW;
   static constexpr int kThreads = 32 * (kFirstLoad + kLoadWarps);
   static constexpr int kRing = 0;                                 // 2 x 5 x 16 KB
   static constexpr int kQ = kRing + 2 * NB * kSlotBytes;          // 4 x (2 NQ rows x 128 B): hi rows, then lo rows
@@ -214,8 +216,8 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     b = __shfl_sync(0xFFFFFFFFu, b, src);
     t0 = __shfl_sync(0xFFFFFFFFu, t0, src);
     if (lane == 0) {
-      if (blockIdx.x == 0) p.first[p.B] = run;
-      int64_t t = lo;
+      if (blockIdx.x == 0) p.span[2 * p.W] = run;
+      int64_t t = lo, on_t = 0, on_b = -1;
       for (int nitem = 0;; ++nitem) {
         WorkItem it{};
         it.b = -1;
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
           it.n = static_cast<int>(min(static_cast<int64_t>(it.L) - it.k0, static_cast<int64_t>(it.ntiles) * kTile));
           it.pad = it.ntiles == n;                      // the whole request: final
           it.s = 2 * w + (t == t0 ? 1 : 0);
-          if (t == t0 && g == 0) p.first[b] = t0;
+          if (t == t0 && it.ntiles < n) on_t = t0, on_b = b;
           t += it.ntiles;
           if (t == t0 + n) {
             t0 = t;
@@ -242,6 +244,10 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         items[k] = it;
         mbar_arrive(&item_full[k]);
         if (it.b < 0) break;
+      }
+      if (g == 0) {
+        p.span[2 * w] = on_t;
+        p.span[2 * w + 1] = on_b;
       }
     }
     __syncwarp();
@@ -349,14 +355,24 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     }
     __syncwarp();
   } else if (warp == 3) {
-    // (warps 0..3 are the control roles; the softmax warps start at a multiple of four, their TMEM lane quadrant)
+    // ------------------------------------------------------------------ requests without keys: zeros, every W-th one
+    const int w = static_cast<int>(blockIdx.x) / p.G, c0 = static_cast<int>(blockIdx.x) % p.G * NQ, c1 = min(c0 + NQ, p.cols);
+    for (int b = w; b < p.B; b += p.W) {
+      if (p.seq_lens[b] > 0) continue;
+      for (int c = c0; c < c1; ++c) {
+        const int64_t r = static_cast<int64_t>(b) * p.q_len + c / p.H;
+        uint8_t* o = p.out + r * p.o_s0b + static_cast<int64_t>(c % p.H) * p.o_s1b;
+        for (int d = lane; d < kLora; d += 32) *reinterpret_cast<uint16_t*>(o + 2 * d) = 0;
+        if (p.lse && lane == 0) p.lse[r * p.H + c % p.H] = -CUDART_INF_F;
+      }
+    }
   } else if (warp >= C::kFirstLoad) {
     // ------------------------------------------------------------------ loaders
-    // Warp w owns keys 8 w .. 8 w + 7 of every tile, four lanes a key: lane = 4 r + u takes, of key r, the groups 4 j + u
-    // of the four code tiles j and two 16-byte pieces of k_pe.  A quarter of the warp so stores an even and the next
-    // odd row, whose columns the swizzle keeps apart.
-    constexpr int KW = kTile / C::kLoadWarps;
-    static_assert(KW == 8, "four lanes a key, a warp's rows one swizzle group");
+    // Warp w owns keys KW w .. KW w + KW - 1 of every tile, four lanes a key: lane = 4 r + u takes, of keys r, r + 8, ..., the
+    // groups 4 j + u of the four code tiles j and two 16-byte pieces of k_pe.  A quarter of the warp so stores an even
+    // and the next odd row, whose columns the swizzle keeps apart.
+    constexpr int KW = kTile / C::kLoadWarps, KL = KW / 8;
+    static_assert(KW % 8 == 0, "a lane's rows are whole swizzle groups apart");
     const int w = warp - C::kFirstLoad;
     const int key = lane >> 2, u = lane & 3;
     struct Cursor {
@@ -390,53 +406,74 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       if (--c.left < 0) next_item(c);
     };
     uint32_t errbits = 0;
-    // this lane's key of a tile: its block id (as read: looked at a tile later, by found; kNoKey: there is none) and
-    // its place there
+    // this lane's keys of a tile: block ids (as read: looked at a tile later, by found; kNoKey: there is none) and places
+    // there
     constexpr int kNoKey = -0x7FFFFFFF;
     struct Ask {
-      int id, at;
+      int id[KL], at[KL];
     };
     auto ask = [&](const Cursor& c) -> Ask {
-      Ask a{kNoKey, 0};
-      if (c.table && c.kp < c.end) {
-        const int col = p.bs_shift >= 0 ? c.kp >> p.bs_shift : c.kp / p.block_size;
-        a.at = c.kp - col * p.block_size;
-        a.id = __ldg(c.table + col);
+      Ask a;
+#pragma unroll
+      for (int y = 0; y < KL; ++y) {
+        const int kp = c.kp + 8 * y;
+        a.id[y] = kNoKey;
+        a.at[y] = 0;
+        if (c.table && kp < c.end) {
+          const int col = static_cast<int>(__umulhi(2u * static_cast<uint32_t>(kp), p.bs_magic) >> p.bs_shift);      // kp / block_size
+          a.at[y] = kp - col * p.block_size;
+          a.id[y] = __ldg(c.table + col);
+        }
       }
       return a;
     };
-    auto found = [&](const Ask& a) -> const uint8_t* {      // the key's record, or null
-      if (static_cast<uint32_t>(a.id) < p.num_blocks)
-        return p.kv + static_cast<uint64_t>(static_cast<uint32_t>(a.id)) * p.blk_stride + static_cast<uint64_t>(static_cast<uint32_t>(a.at)) * p.ent_stride;
-      if (a.id != kNoKey) errbits |= 2u;
-      return nullptr;
+    struct Records {
+      const uint8_t* r[KL];      // null: no such key or block
+    };
+    auto found = [&](const Ask& a) -> Records {
+      Records f;
+#pragma unroll
+      for (int y = 0; y < KL; ++y) {
+        const bool good = static_cast<uint32_t>(a.id[y]) < p.num_blocks;
+        if (!good && a.id[y] != kNoKey) errbits |= 2u;
+        f.r[y] = good ? p.kv + static_cast<uint64_t>(static_cast<uint32_t>(a.id[y])) * p.blk_stride +
+                            static_cast<uint64_t>(static_cast<uint32_t>(a.at[y])) * p.ent_stride
+                      : nullptr;
+      }
+      return f;
     };
     // A tile's records are asked of memory into L2 one tile before its loads: the loads of a tile, issued together
     // when the registers of the tile before are free, then find them there.  (Loads issued register by
     // register between the conversions ran at a load's whole latency a step: the few scoreboards of a warp
     // are shared by old and new loads.)
     const bool one_run = p.block_size % KW == 0 && p.ent_stride == kFp4Entry;      // the warp's 16 records lie together
-    auto prefetch = [&](const uint8_t* r) {
+    auto prefetch = [&](const Records& f) {
       if (one_run) {      // (a bulk prefetch a key takes the loaders longer than one for all)
-        if (lane == 0 && r) bulk_prefetch_l2(r, KW * kFp4Entry);
-      } else if (u == 0 && r) {
-        bulk_prefetch_l2(r, kFp4Entry);
+        if (lane == 0 && f.r[0]) bulk_prefetch_l2(f.r[0], KW * kFp4Entry);
+      } else {
+#pragma unroll
+        for (int y = 0; y < KL; ++y)
+          if (u == y && f.r[y]) bulk_prefetch_l2(f.r[y], kFp4Entry);
       }
     };
-    uint4 code[4], rope[2], ex;
-    bool live = false;
-    auto load_tile = [&](const uint8_t* r) {
-      live = r != nullptr;
-      if (r) {
-        ex = __ldg(reinterpret_cast<const uint4*>(r + kFp4Exps));
+    uint4 code[KL][4], rope[KL][2], ex[KL];
+    bool live[KL];
+    auto load_tile = [&](const Records& f) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) rope[i] = __ldg(reinterpret_cast<const uint4*>(r + kFp4Rope) + 2 * u + i);
+      for (int y = 0; y < KL; ++y) {
+        const uint8_t* r = f.r[y];
+        live[y] = r != nullptr;
+        if (r) {
+          ex[y] = __ldg(reinterpret_cast<const uint4*>(r + kFp4Exps));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) code[i] = __ldg(reinterpret_cast<const uint4*>(r) + 4 * i + u);
-      } else {      // an absent key is all zeros
-        ex = rope[0] = rope[1] = make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < 2; ++i) rope[y][i] = __ldg(reinterpret_cast<const uint4*>(r + kFp4Rope) + 2 * u + i);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) code[i] = make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < 4; ++i) code[y][i] = __ldg(reinterpret_cast<const uint4*>(r) + 4 * i + u);
+        } else {      // an absent key is all zeros
+          ex[y] = rope[y][0] = rope[y][1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) code[y][i] = make_uint4(0, 0, 0, 0);
+        }
       }
     };
     Cursor c{};
@@ -450,12 +487,12 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     load_tile(found(ask(c)));
     advance(c);
     have1 = c.table != nullptr;
-    const uint8_t* next = found(ask(c));
+    Records next = found(ask(c));
     prefetch(next);
     advance(c);
     have2 = c.table != nullptr;
     Ask asked = ask(c);
-    // offset of column 2 u of key r's row in a slot; column 2 u + 1 is 16 away (by exclusive or)
+    // offset of column 2 u of key r's row in a slot; column 2 u + 1 is 16 away (by exclusive or), key r + 8 1024 away
     const uint32_t o0 = (KW * w + key) * 128 + (((2 * u) ^ key) << 4), o1 = o0 ^ 16u;
     for (int gt = 0; ok && have; ++gt) {
       const int h = gt & 1;
@@ -467,40 +504,52 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         if (lane == 0) mbar_arrive(&full[h * NB + slot]);
       };
       if (w == 0 && lane == 0) TL(4, 1);
-      // the record's largest exponent, at least 2^-60: what is smaller than 2^-74 reads as zero, and the sums over
+      // the records' largest exponents, at least 2^-60: what is smaller than 2^-74 reads as zero, and the sums over
       // keys stay inside fp32.  e: the exponents of this lane's groups.
-      const uint32_t word[4] = {ex.x, ex.y, ex.z, ex.w};
-      uint32_t K = 67u, e[4];
+      uint32_t K[KL], e[KL][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e[i] = __byte_perm(word[i], 0u, 0x4440u | u);
-        K = max(K, e[i]);
+      for (int y = 0; y < KL; ++y) {
+        const uint32_t word[4] = {ex[y].x, ex[y].y, ex[y].z, ex[y].w};
+        K[y] = 67u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e[y][i] = __byte_perm(word[i], 0u, 0x4440u | u);
+          K[y] = max(K[y], e[y][i]);
+        }
       }
-      K = max(K, __shfl_xor_sync(0xFFFFFFFFu, K, 1));
-      K = max(K, __shfl_xor_sync(0xFFFFFFFFu, K, 2));
+#pragma unroll
+      for (int o = 1; o <= 2; ++o)
+#pragma unroll
+        for (int y = 0; y < KL; ++y) K[y] = max(K[y], __shfl_xor_sync(0xFFFFFFFFu, K[y], o));
       // k_pe and the scale: free after QK of tile gt - 2 and its softmax, and so after its PV
       if (gt >= 2 && !warp_wait(&pv_part[h * C::kParts], used, abort_flag)) break;
       if (w == 0 && lane == 0) TL(4, 2);
-      *reinterpret_cast<uint4*>(tile + 4 * kSlotBytes + o0) = rope[0];
-      *reinterpret_cast<uint4*>(tile + 4 * kSlotBytes + o1) = rope[1];
-      if (u == 0)      // exponent 255: a NaN in the record; -1: no such key
-        scl[h * kTile + KW * w + key] = !live ? -1.f : K == 255u ? CUDART_NAN_F : __uint_as_float((K - 6u) << 23);
+#pragma unroll
+      for (int y = 0; y < KL; ++y) {
+        *reinterpret_cast<uint4*>(tile + 4 * kSlotBytes + 1024 * y + o0) = rope[y][0];
+        *reinterpret_cast<uint4*>(tile + 4 * kSlotBytes + 1024 * y + o1) = rope[y][1];
+        if (u == y)      // exponent 255: a NaN in the record; -1: no such key
+          scl[h * kTile + KW * w + 8 * y + key] = !live[y] ? -1.f : K[y] == 255u ? CUDART_NAN_F : __uint_as_float((K[y] - 6u) << 23);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (C::kParts > 1 && i > 0 && i % (4 / C::kParts) == 0 && gt >= 2)
           ok = ok && warp_wait(&pv_part[h * C::kParts + i / (4 / C::kParts)], used, abort_flag);
         if (!ok) break;
-        const uint2 l2 = lut[min(K - e[i], 15u)];
-        const uint2 a0 = fp4x8_to_e4m3(l2, code[i].x, p.two16, p.two31), a1 = fp4x8_to_e4m3(l2, code[i].y, p.two16, p.two31);
-        const uint2 a2 = fp4x8_to_e4m3(l2, code[i].z, p.two16, p.two31), a3 = fp4x8_to_e4m3(l2, code[i].w, p.two16, p.two31);
-        *reinterpret_cast<uint4*>(tile + i * kSlotBytes + o0) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-        *reinterpret_cast<uint4*>(tile + i * kSlotBytes + o1) = make_uint4(a2.x, a2.y, a3.x, a3.y);
+#pragma unroll
+        for (int y = 0; y < KL; ++y) {
+          const uint2 l2 = lut[min(K[y] - e[y][i], 15u)];
+          const uint2 a0 = fp4x8_to_e4m3(l2, code[y][i].x, p.two16, p.two31), a1 = fp4x8_to_e4m3(l2, code[y][i].y, p.two16, p.two31);
+          const uint2 a2 = fp4x8_to_e4m3(l2, code[y][i].z, p.two16, p.two31), a3 = fp4x8_to_e4m3(l2, code[y][i].w, p.two16, p.two31);
+          *reinterpret_cast<uint4*>(tile + i * kSlotBytes + 1024 * y + o0) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+          *reinterpret_cast<uint4*>(tile + i * kSlotBytes + 1024 * y + o1) = make_uint4(a2.x, a2.y, a3.x, a3.y);
+        }
         if (i & 1) written(i);
       }
       if (!ok) break;
       if (w == 0 && lane == 0) TL(4, 3);
       // (the block ids are looked at before new loads are on their way, whose scoreboards they may share)
-      const uint8_t* after = found(asked);
+      const Records after = found(asked);
       prefetch(after);
       load_tile(next);
       advance(c);

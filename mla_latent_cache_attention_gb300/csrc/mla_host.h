@@ -60,8 +60,8 @@ int run_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_c
                      int64_t o_s0, int64_t o_s1, float* lse, void* workspace, size_t workspace_bytes,
                      const SplitPlan& sp, bool sched_ready, cudaStream_t stream);
 
-// Workspace of an mxfp4 decode of B requests, and that decode after its checks (check_paged_decode).
-size_t fp4_workspace_bytes(int64_t B, int q_len, int H, int sms);
+// Workspace of an mxfp4 decode, and that decode after its checks (check_paged_decode).
+size_t fp4_workspace_bytes(int q_len, int H, int sms);
 int run_fp4_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache, int64_t num_blocks,
                    int64_t block_stride_bytes, int64_t entry_stride_bytes, int32_t block_size, const int32_t* block_table,
                    int64_t bt_stride, const int32_t* seq_lens, int32_t B, int32_t q_len, int32_t H, float softmax_scale,

@@ -293,7 +293,7 @@ extern "C" size_t mla_selected_decode_workspace_size(mla_cache_format fmt, int32
                                                      int32_t H, int32_t num_sms) {
   const int sms = query_sms(T, topk, block_size, H, num_sms);
   if (sms == 0) return 0;
-  if (fmt == MLA_CACHE_MXFP4) return selected_list_bytes(T, topk) + fp4_workspace_bytes(T, 1, H, sms);
+  if (fmt == MLA_CACHE_MXFP4) return selected_list_bytes(T, topk) + fp4_workspace_bytes(1, H, sms);
   const SelectedPlan sp = plan_selected(fmt, T, H, static_cast<int64_t>(topk) * block_size, sms);
   return selected_list_bytes(T, topk) + workspace_bytes_for(sp.rows, H, sp.main) + workspace_bytes_for(T - sp.rows, H, sp.tail);
 }
@@ -302,7 +302,7 @@ extern "C" size_t mla_selected_decode_workspace_bound(mla_cache_format fmt, int3
                                                       int32_t block_size, int32_t H, int32_t num_sms) {
   const int sms = query_sms(max_T, topk, block_size, H, num_sms);
   if (sms == 0) return 0;
-  if (fmt == MLA_CACHE_MXFP4) return selected_list_bytes(max_T, topk) + fp4_workspace_bytes(max_T, 1, H, sms);      // grows with the rows
+  if (fmt == MLA_CACHE_MXFP4) return selected_list_bytes(max_T, topk) + fp4_workspace_bytes(1, H, sms);
   return selected_list_bytes(max_T, topk) + selected_partials_bound(fmt, max_T, H, static_cast<int64_t>(topk) * block_size, sms);
 }
 
@@ -332,7 +332,7 @@ extern "C" int mla_selected_decode(const void* q, int64_t q_s0, int64_t q_s1, co
   if (static_cast<int64_t>(T) * 8 * (sp.main.n_splits > sp.tail.n_splits ? sp.main.n_splits : sp.tail.n_splits) >= (int64_t(1) << 31))
     return fail(MLA_ERR_UNSUPPORTED, "too many rows");
   const int32_t rows = static_cast<int32_t>(sp.rows), more = T - rows;
-  const size_t part = workspace_bytes_for(rows, H, sp.main), need = lists + (fp4 ? fp4_workspace_bytes(T, 1, H, d->sms) : part + workspace_bytes_for(more, H, sp.tail));
+  const size_t part = workspace_bytes_for(rows, H, sp.main), need = lists + (fp4 ? fp4_workspace_bytes(1, H, d->sms) : part + workspace_bytes_for(more, H, sp.tail));
   if (!workspace || workspace_bytes < need)
     return fail(MLA_ERR_INVALID, "workspace too small: need %zu bytes, got %zu", need, workspace_bytes);
   if (!aligned(workspace, 256)) return fail(MLA_ERR_INVALID, "workspace must be 256-byte aligned");
