@@ -29,8 +29,8 @@
 //     stacked along N and added in the epilogue.  The reference m moves only when a logit passes it by kTau.
 //   * Roles hand over through mbarriers, each waited with a time limit.
 //
-// Warps: 0 scheduler, 1 QK issuer (TMEM owner), 2 PV issuer, then four (NQ = 16) or eight softmax warps (which also
-// prepare the query and write the results), then 16 loaders.
+// Warps: 0 scheduler, 1 QK issuer (TMEM owner), 2 PV issuer, then four softmax warps (which also prepare the query and
+// write the results), then 8 loaders.
 #pragma once
 #include "mla_ds.cuh"
 
@@ -69,9 +69,9 @@ template <int NQ_>
 struct Fp4Cfg {
   static_assert(NQ_ == 16 || NQ_ == 32, "columns per item");
   static constexpr int NQ = NQ_, NB = 5;
-  static constexpr int NC = 16;                                   // columns of a softmax thread
-  static constexpr int kSW = 4 * (NQ / NC);                       // softmax warps: two column halves where NQ = 32
-  static constexpr int kLoadWarps = 8, kPvWarp = 2, kFirstSm = 4, kFirstLoad = kFirstSm + kSW;
+  static constexpr int NC = NQ;                                   // columns of a softmax thread
+  static constexpr int kSW = 4 * (NQ / NC);                       // softmax warps
+  static constexpr int kLoadWarps = 8, kPvWarp = 2, kFirstSm = 3, kFirstLoad = kFirstSm + kSW;
   static constexpr int kThreads = 32 * (kFirstLoad + kLoadWarps);
   static constexpr int kRing = 0;                                 // 2 x 5 x 16 KB
   static constexpr int kQ = kRing + 2 * NB * kSlotBytes;          // 4 x (2 NQ rows x 128 B): hi rows, then lo rows
@@ -109,6 +109,58 @@ __device__ __forceinline__ uint2 fp4x8_to_e4m3(uint2 lut, uint32_t w, uint32_t t
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(s0) : "r"(0u), "r"(0x80u), "r"(sgn));
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(s1) : "r"(0u), "r"(0x80u), "r"(__umulhi(sgn, two16)));
   return make_uint2(m0 | s0, m1 | s1);
+}
+
+// One lane of a warp that goes along as a whole: which, the hardware says.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+// The products and commits of mla_ptx.cuh, issued where `on`.
+__device__ __forceinline__ void mma_f8_if(bool on, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(on ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_if(bool on, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc), "r"(on ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_if(bool on, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(on ? 1u : 0u)
+      : "memory");
+}
+
+// A group of warps waits through its first one, the others at a hardware barrier: a warp that polls takes issue slots from
+// the others (a try_wait comes back after some 70 ns, whatever its time limit; polled by every softmax and loader warp, the
+// waits were 4500 of 10000 instructions a tile).  Every thread of the group leaves with the same answer.
+__device__ __forceinline__ bool group_wait(bool first, uint32_t id, uint32_t threads, uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  bool w = true;
+  if (first) w = warp_wait(bar, parity, abort_flag);
+  return named_bar_and(id, threads, w);
+}
+// A wait that is in no hurry.
+__device__ __forceinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_test_wait(bar, parity)) {
+    __nanosleep(500);
+    if (*abort_flag) return false;
+    // (work items last as long as they last: this is no pipeline's wait)
+    if (globaltimer() - t0 > 10 * kWaitNs) {
+      *abort_flag = 2;
+      return false;
+    }
+  }
+  return true;
 }
 
 template <int NQ>
@@ -166,7 +218,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 3 && lane < 16) {
+  if (warp == 0 && lane < 16) {
     // magnitudes 0, .5, 1, 1.5 | 2, 3, 4, 6 times 2^(6 - lane) in E4M3: exact down to 2^-9, zero below
     // (entry 15 is all zeros)
     uint32_t w[2] = {0u, 0u};
@@ -240,7 +292,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
           }
         }
         const int k = nitem % kItemDepth;
-        if (nitem >= kItemDepth && !mbar_wait(&item_empty[k], static_cast<uint32_t>((nitem / kItemDepth) - 1) & 1u, abort_flag)) break;
+        if (nitem >= kItemDepth && !slow_wait(&item_empty[k], static_cast<uint32_t>((nitem / kItemDepth) - 1) & 1u, abort_flag)) break;
         items[k] = it;
         mbar_arrive(&item_full[k]);
         if (it.b < 0) break;
@@ -251,9 +303,21 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       }
     }
     __syncwarp();
+    // requests without keys: zeros, every W-th one
+    for (int z = w; z < p.B; z += p.W) {
+      if (p.seq_lens[z] > 0) continue;
+      for (int c = g * NQ; c < min(g * NQ + NQ, p.cols); ++c) {
+        const int64_t r = static_cast<int64_t>(z) * p.q_len + c / p.H;
+        uint8_t* o = p.out + r * p.o_s0b + static_cast<int64_t>(c % p.H) * p.o_s1b;
+        for (int d = lane; d < kLora; d += 32) *reinterpret_cast<uint16_t*>(o + 2 * d) = 0;
+        if (p.lse && lane == 0) p.lse[r * p.H + c % p.H] = -CUDART_INF_F;
+      }
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ QK issuer
-    if (lane == 0) {
+    // (the warp goes along as a whole, so that the descriptors stay in uniform registers; one lane issues)
+    {
+      const bool one = elect_one();
       const uint64_t dK0 = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
       const uint64_t dQ0 = smem_desc(smem_u32(qs), 16, 1024, kSwizzle128B);
       const uint64_t dQr = smem_desc(smem_u32(qr), 16, 1024, kSwizzle128B);
@@ -263,58 +327,60 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       int nit = 0, nq = 0, g = 0;
       while (ok) {
         const int k = nit % kItemDepth;
-        if (!mbar_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag)) break;
+        if (!warp_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag)) break;
         const WorkItem it = items[k];
-        mbar_arrive(&item_empty[k]);
+        __syncwarp();
+        if (one) mbar_arrive(&item_empty[k]);
         ++nit;
         if (it.b < 0) break;
-        if (!mbar_wait(q_full, nq & 1, abort_flag)) break;
+        if (!warp_wait(q_full, nq & 1, abort_flag)) break;
         ++nq;
         for (int t = 0; t < it.ntiles && ok; ++t) {
           const int gt = g + t, h = gt & 1;
-          if (gt >= 2 && !mbar_wait(&s_free[h], static_cast<uint32_t>((gt - 2) >> 1) & 1u, abort_flag)) ok = false;
+          if (gt >= 2 && !warp_wait(&s_free[h], static_cast<uint32_t>((gt - 2) >> 1) & 1u, abort_flag)) ok = false;
           if (!ok) break;
-          TL(1, 1);
+          if (lane == 0) TL(1, 1);
           const uint32_t dS = tmem + h * C::kS;
           const uint32_t use = static_cast<uint32_t>(gt >> 1) & 1u;
           // as the loaders finish the slots: k_pe and two code tiles, then the other two
-          if (!mbar_wait(&full[h * NB + 1], use, abort_flag)) {
+          if (!warp_wait(&full[h * NB + 1], use, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          TL(1, 2);
+          if (lane == 0) TL(1, 2);
           {
             const uint64_t aK = desc_add(dK0, static_cast<uint32_t>((h * NB + 4) * (kSlotBytes >> 4)));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f16_ss(dS + 2 * NQ, desc_add(aK, (kk * 32) >> 4), desc_add(dQr, (kk * 32) >> 4), kIdRope, kk > 0 ? 1u : 0u);
+              mma_f16_if(one, dS + 2 * NQ, desc_add(aK, (kk * 32) >> 4), desc_add(dQr, (kk * 32) >> 4), kIdRope, kk > 0 ? 1u : 0u);
           }
 #pragma unroll 1
           for (int b = 0; b < 4 && ok; ++b) {
-            if (b == 2) ok = mbar_wait(&full[h * NB + 3], use, abort_flag);
+            if (b == 2) ok = warp_wait(&full[h * NB + 3], use, abort_flag);
             if (!ok) break;
             tc_fence_after();
             const uint64_t aK = desc_add(dK0, static_cast<uint32_t>((h * NB + b) * (kSlotBytes >> 4)));
             const uint64_t bQ = desc_add(dQ0, static_cast<uint32_t>(b * (2 * NQ * 128 >> 4)));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f8_ss(dS, desc_add(aK, (kk * 32) >> 4), desc_add(bQ, (kk * 32) >> 4), kIdNope, (b | kk) ? 1u : 0u);
+              mma_f8_if(one, dS, desc_add(aK, (kk * 32) >> 4), desc_add(bQ, (kk * 32) >> 4), kIdNope, (b | kk) ? 1u : 0u);
           }
           if (!ok) break;
-          mma_commit(&s_full[h]);
-          TL(1, 3);
+          mma_commit_if(one, &s_full[h]);
+          if (lane == 0) TL(1, 3);
         }
         g += it.ntiles;
       }
-      mma_commit(fin);
+      mma_commit_if(one, fin);
       volatile int no_abort[2] = {0, 0};
       mbar_wait(fin, 0, no_abort);
     }
     __syncwarp();
   } else if (warp == C::kPvWarp) {
     // ------------------------------------------------------------------ PV issuer
-    if (lane == 0) {
+    {
+      const bool one = elect_one();
       const uint64_t dV0 = smem_desc(smem_u32(ring), kSlotBytes, 1024, kSwizzle128B);
       const uint64_t dP0 = smem_desc(smem_u32(ps), 2 * NQ * 8, 128, kSwizzleNone);
       constexpr uint32_t kIdPv = idesc_e4m3(128, 2 * NQ, 1, 1);
@@ -322,50 +388,39 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       int nit = 0, g = 0;
       while (ok) {
         const int k = nit % kItemDepth;
-        if (!mbar_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag)) break;
+        if (!warp_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag)) break;
         const WorkItem it = items[k];
-        mbar_arrive(&item_empty[k]);
+        __syncwarp();
+        if (one) mbar_arrive(&item_empty[k]);
         ++nit;
         if (it.b < 0) break;
         for (int t = 0; t < it.ntiles; ++t) {
           const int gt = g + t;
-          if (!mbar_wait(p_full, static_cast<uint32_t>(gt) & 1u, abort_flag)) {
+          if (!warp_wait(p_full, static_cast<uint32_t>(gt) & 1u, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          TL(2, 1);
+          if (lane == 0) TL(2, 1);
           const uint32_t acc0 = t == 0 ? 0u : 1u;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint64_t aV = desc_add(dV0, static_cast<uint32_t>(((gt & 1) * NB + j) * (kSlotBytes >> 4)));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_f8_ss(tmem + C::kTmemO + 2 * NQ * j, desc_add(aV, (kk * 4096) >> 4), desc_add(dP0, (kk * NQ * 64) >> 4), kIdPv,
+              mma_f8_if(one, tmem + C::kTmemO + 2 * NQ * j, desc_add(aV, (kk * 4096) >> 4), desc_add(dP0, (kk * NQ * 64) >> 4), kIdPv,
                         kk > 0 ? 1u : acc0);
-            if ((j + 1) % (4 / C::kParts) == 0) mma_commit(&pv_part[(gt & 1) * C::kParts + j / (4 / C::kParts)]);
+            if ((j + 1) % (4 / C::kParts) == 0) mma_commit_if(one, &pv_part[(gt & 1) * C::kParts + j / (4 / C::kParts)]);
           }
-          TL(2, 2);
+          if (lane == 0) TL(2, 2);
         }
         g += it.ntiles;
       }
-      mma_commit(fin_pv);
+      mma_commit_if(one, fin_pv);
       volatile int no_abort[2] = {0, 0};
       mbar_wait(fin_pv, 0, no_abort);
     }
     __syncwarp();
-  } else if (warp == 3) {
-    // ------------------------------------------------------------------ requests without keys: zeros, every W-th one
-    const int w = static_cast<int>(blockIdx.x) / p.G, c0 = static_cast<int>(blockIdx.x) % p.G * NQ, c1 = min(c0 + NQ, p.cols);
-    for (int b = w; b < p.B; b += p.W) {
-      if (p.seq_lens[b] > 0) continue;
-      for (int c = c0; c < c1; ++c) {
-        const int64_t r = static_cast<int64_t>(b) * p.q_len + c / p.H;
-        uint8_t* o = p.out + r * p.o_s0b + static_cast<int64_t>(c % p.H) * p.o_s1b;
-        for (int d = lane; d < kLora; d += 32) *reinterpret_cast<uint16_t*>(o + 2 * d) = 0;
-        if (p.lse && lane == 0) p.lse[r * p.H + c % p.H] = -CUDART_INF_F;
-      }
-    }
   } else if (warp >= C::kFirstLoad) {
     // ------------------------------------------------------------------ loaders
     // Warp w owns keys KW w .. KW w + KW - 1 of every tile, four lanes a key: lane = 4 r + u takes, of keys r, r + 8, ..., the
@@ -384,7 +439,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     auto next_item = [&](Cursor& c) {
       for (;;) {
         const int k = nit % kItemDepth;
-        if (!warp_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag)) {
+        if (!group_wait(w == 0, 2, 32 * C::kLoadWarps, &item_full[k], (nit / kItemDepth) & 1, abort_flag)) {
           ok = false;
           c.table = nullptr;
           return;
@@ -456,6 +511,9 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
           if (u == y && f.r[y]) bulk_prefetch_l2(f.r[y], kFp4Entry);
       }
     };
+    // k_pe's pieces of this lane: the two halves of 64 bytes, in the other order in odd rows (whose columns the swizzle takes to
+    // the even rows' then)
+    auto piece = [&](int i) { return u + 4 * (i ^ (key & 1)); };
     uint4 code[KL][4], rope[KL][2], ex[KL];
     bool live[KL];
     auto load_tile = [&](const Records& f) {
@@ -466,7 +524,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         if (r) {
           ex[y] = __ldg(reinterpret_cast<const uint4*>(r + kFp4Exps));
 #pragma unroll
-          for (int i = 0; i < 2; ++i) rope[y][i] = __ldg(reinterpret_cast<const uint4*>(r + kFp4Rope) + 2 * u + i);
+          for (int i = 0; i < 2; ++i) rope[y][i] = __ldg(reinterpret_cast<const uint4*>(r + kFp4Rope) + piece(i));
 #pragma unroll
           for (int i = 0; i < 4; ++i) code[y][i] = __ldg(reinterpret_cast<const uint4*>(r) + 4 * i + u);
         } else {      // an absent key is all zeros
@@ -526,16 +584,15 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       if (w == 0 && lane == 0) TL(4, 2);
 #pragma unroll
       for (int y = 0; y < KL; ++y) {
-        *reinterpret_cast<uint4*>(tile + 4 * kSlotBytes + 1024 * y + o0) = rope[y][0];
-        *reinterpret_cast<uint4*>(tile + 4 * kSlotBytes + 1024 * y + o1) = rope[y][1];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<uint4*>(tile + 4 * kSlotBytes + 1024 * y + (KW * w + key) * 128 + ((piece(i) ^ key) << 4)) = rope[y][i];
         if (u == y)      // exponent 255: a NaN in the record; -1: no such key
           scl[h * kTile + KW * w + 8 * y + key] = !live[y] ? -1.f : K[y] == 255u ? CUDART_NAN_F : __uint_as_float((K[y] - 6u) << 23);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (C::kParts > 1 && i > 0 && i % (4 / C::kParts) == 0 && gt >= 2)
-          ok = ok && warp_wait(&pv_part[h * C::kParts + i / (4 / C::kParts)], used, abort_flag);
-        if (!ok) break;
+        if (C::kParts > 1 && i == 2 && gt >= 2) ok = ok && warp_wait(&pv_part[h * C::kParts + 1], used, abort_flag);
 #pragma unroll
         for (int y = 0; y < KL; ++y) {
           const uint2 l2 = lut[min(K[y] - e[y][i], 15u)];
@@ -546,7 +603,6 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         }
         if (i & 1) written(i);
       }
-      if (!ok) break;
       if (w == 0 && lane == 0) TL(4, 3);
       // (the block ids are looked at before new loads are on their way, whose scoreboards they may share)
       const Records after = found(asked);
@@ -629,12 +685,11 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     bool q_ready = false;                // the item's query was prepared during the one before
     while (ok) {
       const int k = nit % kItemDepth;
-      bool w = warp_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag);
+      bool w = group_wait(warp == C::kFirstSm, 1, NT, &item_full[k], (nit / kItemDepth) & 1, abort_flag);
       const WorkItem it = items[k];
       ++nit;
       if (stid < NQ) mref[stid] = -3e38f;         // no reference yet: every logit passes it, and -inf - m is no NaN
-      if (!named_bar_and(1, NT, w)) break;
-      if (it.b < 0) break;
+      if (!w || it.b < 0) break;
       if (!q_ready) prep_query(it);
       q_ready = false;
       const int cgb = it.g * NQ + c0;             // global column of this thread's first
@@ -649,21 +704,23 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         // (the rows of absent keys are zeros: 0 * 0 - inf)
         const float kexp = rv ? static_cast<float>(static_cast<int>(__float_as_uint(ks) >> 23) - 127) : -CUDART_INF_F;
         const float km = rv ? ks : 0.f;
-        float r[NC];              // lo, then rope (all three at once do not fit the registers)
-        tmem_ld16(ts, s);
-        tmem_ld16(ts + NQ, r);
-        tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < NC; ++c) s[c] = fmaf(r[c], 0.0625f, s[c]);
-        tmem_ld16(ts + 2 * NQ, r);
-        tmem_ld_wait();
+        for (int c1 = 0; c1 < NC; c1 += 16) {
+          float a[16], r[16];
+          tmem_ld16(ts + c1, a);
+          tmem_ld16(ts + NQ + c1, r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < NC; c += 4) {
-          const float4 f4 = *reinterpret_cast<const float4*>(colf + c0 + c);
-          const float ff[4] = {f4.x, f4.y, f4.z, f4.w};
+          for (int c = 0; c < 16; ++c) a[c] = fmaf(r[c], 0.0625f, a[c]);
+          tmem_ld16(ts + 2 * NQ + c1, r);
+          tmem_ld_wait();
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            s[c + y] = fmaf(s[c + y], ff[y] * km, fmaf(r[c + y], p.sig2, kexp));
+          for (int c = 0; c < 16; c += 4) {
+            const float4 f4 = *reinterpret_cast<const float4*>(colf + c0 + c1 + c);
+            const float ff[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) s[c1 + c + y] = fmaf(a[c + y], ff[y] * km, fmaf(r[c + y], p.sig2, kexp));
+          }
         }
         // spec-verify: query token qi sees keys up to L - q_len + qi
         const int dq = kpos - it.L + p.q_len;
@@ -675,8 +732,12 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       };
       for (int t = 0; t < it.ntiles; ++t) {
         const int gt = g + t;
-        w = warp_wait(&s_full[gt & 1], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag);
-        w = w && warp_wait(&full[(gt & 1) * NB + 1], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag);      // its scales (long there)
+        // (the tile's scales, written with its first slots, are there long before S)
+        w = true;
+        if (warp == C::kFirstSm)
+          w = warp_wait(&full[(gt & 1) * NB + 1], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag) &&
+              warp_wait(&s_full[gt & 1], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag);
+        w = named_bar_and(1, NT, w);
         tc_fence_after();
         const float ks = scl[(gt & 1) * kTile + row];
         if (stid == 0) TL(3, 1);
@@ -738,11 +799,15 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
             if (w && resc) {
 #pragma unroll 1
               for (int x = 0; x < 8 * NQ; x += NQ) {      // O_j: this thread's hi columns, then its lo columns
-                tmem_ld16(tl + C::kTmemO + x + c0, d);
-                tmem_ld_wait();
+#pragma unroll 1
+                for (int c1 = c0; c1 < c0 + NC; c1 += 16) {
+                  float o[16];
+                  tmem_ld16(tl + C::kTmemO + x + c1, o);
+                  tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < NC; ++c) d[c] *= alph[c0 + c];
-                tmem_st16(tl + C::kTmemO + x + c0, d);
+                  for (int c = 0; c < 16; ++c) o[c] *= alph[c1 + c];
+                  tmem_st16(tl + C::kTmemO + x + c1, o);
+                }
               }
               tmem_st_wait();
             }
@@ -759,9 +824,9 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         const float ik = __uint_as_float((254u << 23) - __float_as_uint(ks < 0.f ? 1.f : ks));      // 1 / ks
         // hi = E4M3 of the weight in f16 (11 bits of it are more than the two terms keep), lo = E4M3 of 16 times the
         // exact rest
-        uint32_t hw[4], lw[4];
+        uint32_t hw[NC / 4], lw[NC / 4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        for (int y = 0; y < NC / 4; ++y) {
           uint32_t hi[2], lo[2];
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
@@ -781,8 +846,11 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         if (stid == 0) TL(3, 4);
         // 8 keys x 16 columns core matrices, 8-key groups 16 NQ bytes apart; hi columns, then lo columns
         uint8_t* prow = ps + (row >> 3) * (16 * NQ) + (row & 7) * 16;
-        *reinterpret_cast<uint4*>(prow + (c0 >> 4) * 128) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-        *reinterpret_cast<uint4*>(prow + ((NQ + c0) >> 4) * 128) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+#pragma unroll
+        for (int y = 0; y < NC / 4; y += 4) {
+          *reinterpret_cast<uint4*>(prow + (c0 / 16 + y / 4) * 128) = make_uint4(hw[y], hw[y + 1], hw[y + 2], hw[y + 3]);
+          *reinterpret_cast<uint4*>(prow + ((NQ + c0) / 16 + y / 4) * 128) = make_uint4(lw[y], lw[y + 1], lw[y + 2], lw[y + 3]);
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -794,8 +862,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       }
       if (!ok) break;
       // the next item's query while PV runs and the results are written
-      const bool more = warp_wait(&item_full[nit % kItemDepth], (nit / kItemDepth) & 1, abort_flag);
-      if (named_bar_and(1, NT, more)) {
+      if (group_wait(warp == C::kFirstSm, 1, NT, &item_full[nit % kItemDepth], (nit / kItemDepth) & 1, abort_flag)) {
         const WorkItem qi = items[nit % kItemDepth];
         if (qi.b >= 0) {
           prep_query(qi);
@@ -830,25 +897,24 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       const int ncol = min(NC, p.cols - cgb);       // may be none
       const int64_t o_wrap = p.o_s0b - static_cast<int64_t>(p.H) * p.o_s1b;
 #pragma unroll 1
-      for (int jj = 0; jj < 4 && ncol > 0; ++jj) {
-        float o[NC];
-        {
-          float lo[NC];
-          tmem_ld16(tl + C::kTmemO + 2 * NQ * jj + c0, o);
-          tmem_ld16(tl + C::kTmemO + 2 * NQ * jj + NQ + c0, lo);
-          tmem_ld_wait();
+      for (int jc = 0; jc < 4 * (NC / 16); ++jc) {
+        const int jj = jc / (NC / 16), c1 = 16 * (jc % (NC / 16));
+        if (c1 >= ncol) continue;
+        float o[16], lo[16];
+        tmem_ld16(tl + C::kTmemO + 2 * NQ * jj + c0 + c1, o);
+        tmem_ld16(tl + C::kTmemO + 2 * NQ * jj + NQ + c0 + c1, lo);
+        tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < NC; ++c) o[c] = fmaf(lo[c], 0.0625f, o[c]);
-        }
+        for (int c = 0; c < 16; ++c) o[c] = fmaf(lo[c], 0.0625f, o[c]);
         const int d = 128 * jj + row;
         if (final_out) {
-          int h = cgb % p.H;
-          uint8_t* ptr = p.out + (static_cast<int64_t>(it.b) * p.q_len + cgb / p.H) * p.o_s0b +
+          int h = (cgb + c1) % p.H;
+          uint8_t* ptr = p.out + (static_cast<int64_t>(it.b) * p.q_len + (cgb + c1) / p.H) * p.o_s0b +
                          static_cast<int64_t>(h) * p.o_s1b + 2 * d;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float iv = __shfl_sync(0xFFFFFFFFu, inv_l, c);
-            if (c < ncol) *reinterpret_cast<__nv_bfloat16*>(ptr) = __float2bfloat16_rn(o[c] * iv);
+          for (int c = 0; c < 16; ++c) {
+            const float iv = __shfl_sync(0xFFFFFFFFu, inv_l, c1 + c);
+            if (c1 + c < ncol) *reinterpret_cast<__nv_bfloat16*>(ptr) = __float2bfloat16_rn(o[c] * iv);
             ptr += p.o_s1b;
             if (++h == p.H) {
               h = 0;
@@ -856,11 +922,11 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
             }
           }
         } else {
-          float* dst = p.part_o + (flat0 * kLora + d);
+          float* dst = p.part_o + ((flat0 + c1) * kLora + d);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float iv = __shfl_sync(0xFFFFFFFFu, inv_l, c);
-            if (c < ncol) dst[static_cast<int64_t>(c) * kLora] = o[c] * iv;
+          for (int c = 0; c < 16; ++c) {
+            const float iv = __shfl_sync(0xFFFFFFFFu, inv_l, c1 + c);
+            if (c1 + c < ncol) dst[static_cast<int64_t>(c) * kLora] = o[c] * iv;
           }
         }
       }
