@@ -21,6 +21,7 @@ struct RopeParams {
   int64_t max_position;
   int T, R;
   int inverse;
+  int joint;                           // the heads of both are one run of the same shape (launch_rope)
   uint32_t* err;
 };
 

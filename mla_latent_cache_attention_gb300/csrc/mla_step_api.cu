@@ -51,7 +51,8 @@ extern "C" int mla_rope(int32_t type, const void* q, int64_t q_s0, int64_t q_s1,
   if (!aligned(positions, 8) || !aligned(cos_sin, 4)) return fail(MLA_ERR_INVALID, "positions and cos_sin must be aligned to their types");
   const int bytes = type == MLA_TYPE_FP32 ? 4 : 2;
   RopeParams p{};
-  bool vec = true, in0 = false, in1 = false;
+  // whole pieces of 16 bytes, and of their pairs' cosines and sines
+  bool vec = aligned(cos_sin, 16) && R % 8 == 0, in0 = false, in1 = false;
   if (int rc = rope_tensor("q", q, q_s0, q_s1, q_out, qo_s0, qo_s1, T, H, D, q_at, R, bytes, half != 0, &p.x[0], &vec, &in0)) return rc;
   if (k) {
     if (int rc = rope_tensor("k", k, k_s0, k_s1, k_out, ko_s0, ko_s1, T, Hk, Dk, k_at, R, bytes, half != 0, &p.x[1], &vec, &in1)) return rc;
