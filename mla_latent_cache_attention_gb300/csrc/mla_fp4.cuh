@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   TL_DECL;
 
-  // the split-K merge may be scheduled now; it waits for this grid to complete
+  if (tid == 0) TL(0, 1);
+  // the merge may be scheduled now; it waits for this grid to complete
   if (tid == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) {
     for (int i = lane; i < C::kNumBars; i += 32) {
@@ -237,12 +238,13 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // launched as a programmatic dependent of the previous kernel in the stream: its writes (the query, the
-  // cache, the scheduler reset) are visible past this wait
+  // cache) are visible past this wait
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tid == 0) TL(0, 2);
 
   if (warp == 0) {
     // ------------------------------------------------------------------ scheduler
-    auto tiles_of = [&](int b) -> int64_t { return (static_cast<int64_t>(max(p.seq_lens[b], 0)) + kTile - 1) / kTile; };
+    auto tiles_of = [&](int b) -> int64_t { return static_cast<int64_t>((static_cast<uint32_t>(max(p.seq_lens[b], 0)) + (kTile - 1)) / kTile); };
     // a lane sums a run of requests; the lane that holds this CTA's first tile looks for its request
     const int per_lane = (p.B + 31) / 32, b0 = min(lane * per_lane, p.B), b1 = min(b0 + per_lane, p.B);
     int64_t sum = 0;
@@ -254,7 +256,12 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       const int64_t v = __shfl_up_sync(0xFFFFFFFFu, end, o);
       if (lane >= o) end += v;
     }
-    const int64_t total = __shfl_sync(0xFFFFFFFFu, end, 31), run = total > 0 ? (total + p.W - 1) / p.W : 1;
+    const int64_t total = __shfl_sync(0xFFFFFFFFu, end, 31);
+    // (a division in 32 bits where that is enough: one in 64 takes a lone lane 0.3 us)
+    const int64_t run = total <= 0 ? 1
+                        : total < (int64_t(1) << 31) - p.W
+                            ? static_cast<int64_t>((static_cast<uint32_t>(total) + static_cast<uint32_t>(p.W - 1)) / static_cast<uint32_t>(p.W))
+                            : (total + p.W - 1) / p.W;
     const int w = static_cast<int>(blockIdx.x) / p.G, g = static_cast<int>(blockIdx.x) % p.G;
     const int64_t lo = min(w * run, total), hi = min(lo + run, total);
     int b = p.B;
@@ -268,6 +275,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     b = __shfl_sync(0xFFFFFFFFu, b, src);
     t0 = __shfl_sync(0xFFFFFFFFu, t0, src);
     if (lane == 0) {
+      TL(0, 3);
       if (blockIdx.x == 0) p.span[2 * p.W] = run;
       int64_t t = lo, on_t = 0, on_b = -1;
       for (int nitem = 0;; ++nitem) {
@@ -690,7 +698,9 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       ++nit;
       if (stid < NQ) mref[stid] = -3e38f;         // no reference yet: every logit passes it, and -inf - m is no NaN
       if (!w || it.b < 0) break;
+      if (stid == 0) TL(3, 20);
       if (!q_ready) prep_query(it);
+      if (stid == 0) TL(3, 21);
       q_ready = false;
       const int cgb = it.g * NQ + c0;             // global column of this thread's first
       float l_part[NC];
@@ -939,12 +949,14 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       }
       tc_fence_before();
       named_bar_sync(1, NT);
+      if (stid == 0) TL(3, 7);
       if (stid == 0) mbar_arrive(&item_empty[k]);
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if (tid == 0) TL(0, 9);
   if (tid == 0 && *abort_flag == 2) set_device_error(p.err, 16u);
   if (warp == 1) {
     tc_fence_after();
