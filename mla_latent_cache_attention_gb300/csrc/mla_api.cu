@@ -404,6 +404,7 @@ extern "C" int mla_key_concat_cache_insert(void* q, int64_t q_s0, int64_t q_s1, 
   p.H = H;
   p.dn = dn;
   p.vec = aligned(k_nope, 16) && aligned(k_out, 16) && kn_s0 % 8 == 0 && kn_s1 % 8 == 0;
+  p.vec_q = p.vec && aligned(q, 16) && q_s0 % 8 == 0 && q_s1 % 8 == 0;
   p.err = d->err;
   if (launch_prefill_epilogue(static_cast<int>(fmt), p, Tp, stream) != cudaSuccess)
     return fail(MLA_ERR_CUDA, "prefill epilogue launch failed: %s", cudaGetErrorString(cudaGetLastError()));

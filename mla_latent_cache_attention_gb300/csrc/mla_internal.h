@@ -84,6 +84,7 @@ struct PrefillEpiParams {
   int64_t max_position;
   int H, dn, dv;
   int vec;                 // every row, stride and base 16-byte aligned: 8-element vector accesses
+  int vec_q;               // key concat: the queries' rope parts too
   uint32_t* err;
 };
 

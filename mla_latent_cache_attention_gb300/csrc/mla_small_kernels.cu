@@ -71,7 +71,7 @@ __device__ __forceinline__ int fp4_group_exponent(uint32_t amax) {
 // Write one cache entry (128 threads): [kv_c | rope(k_pe)] as bf16 (F = 0), as
 // e4m3_sat(x * cinv) (F = 1), or as a 656-byte fp8_ds_mla record (F = 2: per-128-tile scale
 // 2^k from ds_tile_exponent, codes e4m3(x / 2^k), rope bf16), or as a 400-byte mxfp4 record (F = 3, see
-// include/mla.h; all 128 threads meet at a barrier).  cs: the RoPE row or null.
+// include/mla.h; the 128 threads meet at barrier 1).  cs: the RoPE row or null.
 template <int F>
 __device__ __forceinline__ void insert_latent(uint8_t* ent, const uint16_t* __restrict__ kc,
                                               const uint16_t* __restrict__ kr, const float* __restrict__ cs, float cinv,
@@ -116,7 +116,7 @@ __device__ __forceinline__ void insert_latent(uint8_t* ent, const uint16_t* __re
     int top = max(k, __shfl_xor_sync(0xFFFFFFFFu, k, 8));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
     if (lane == 0) kmax[w] = top;
-    __syncthreads();
+    named_bar_sync(1, 128);
     k = max(k, max(max(max(kmax[0], kmax[1]), max(kmax[2], kmax[3])) - 14, -126));
     const float inv = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);   // 2^-k, exact
     uint32_t c = 0;
@@ -365,7 +365,91 @@ __global__ void __launch_bounds__(128) mla_prefill_epilogue_kernel(const Prefill
                    cs, (F == 1) ? *p.cache_scale_inv : 1.f, tid);
 }
 
+// The key-concat epilogues where every row is whole 16-byte pieces: 16 heads of a token a CTA, and all its loads on their
+// way before it looks at the position (the form above, a pair a thread and four heads a CTA, waits for position, table and
+// values one after the other: 8191 tokens of 16 heads 58 us).  The same arithmetic.
+template <int F>
+__global__ void __launch_bounds__(256) mla_key_concat_kernel(const PrefillEpiParams p) {
+  constexpr int kHeads = 16, kAtOnce = 2;
+  const int t = blockIdx.x, g = blockIdx.y, tid = threadIdx.x;
+  const int H = p.H, dn = p.dn, de = dn + 64, cn = dn >> 3;
+  const int h_lo = kHeads * g, nh = min(H - h_lo, kHeads);
+  __shared__ alignas(16) uint16_t kpr[64];      // rope(k_pe[t])
+  const int64_t pos_in = p.positions ? p.positions[t] : 0;
+  const int64_t slot = g == 0 ? p.slot_mapping[t] : -1;
+  // NoPE pieces of the keys
+  const uint16_t* kn = p.k_nope + t * p.kn_s0;
+  uint16_t* ko = p.k_out + (static_cast<int64_t>(t) * H + h_lo) * de;
+  const int n = nh * cn;
+  uint4 v[kAtOnce];
+#pragma unroll
+  for (int u = 0; u < kAtOnce; ++u) {
+    const int i = tid + 256 * u;
+    if (i < n) v[u] = __ldg(reinterpret_cast<const uint4*>(kn + (h_lo + i / cn) * p.kn_s1 + (i % cn) * 8));
+  }
+  // a rope piece of the queries: 8 lanes a head
+  const int hq = tid >> 3, cq = tid & 7;
+  const bool turns = p.positions && hq < nh;
+  uint16_t* qp = p.q + t * p.q_s0 + (h_lo + hq) * p.q_s1 + dn + 8 * cq;
+  uint4 qv = make_uint4(0, 0, 0, 0);
+  if (turns) qv = *reinterpret_cast<const uint4*>(qp);
+  const uint16_t* __restrict__ kr = p.k_pe + t * p.kp_s0;
+  float k0 = 0.f, k1 = 0.f;
+  if (tid < 32) k0 = bf16_at(kr + 2 * tid), k1 = bf16_at(kr + 2 * tid + 1);
+  const float* __restrict__ cs = nullptr;
+  if (p.positions) {
+    int64_t pos = pos_in;
+    if (pos < 0 || pos >= p.max_position) {
+      if (tid == 0 && g == 0) set_device_error(p.err, 8u);
+      pos = pos < 0 ? 0 : p.max_position - 1;
+    }
+    cs = p.cos_sin + pos * 64;
+  }
+#pragma unroll
+  for (int u = 0; u < kAtOnce; ++u) {
+    const int i = tid + 256 * u;
+    if (i < n) *reinterpret_cast<uint4*>(ko + (i / cn) * de + (i % cn) * 8) = v[u];
+  }
+  for (int i = tid + 256 * kAtOnce; i < n; i += 256)
+    *reinterpret_cast<uint4*>(ko + (i / cn) * de + (i % cn) * 8) = __ldg(reinterpret_cast<const uint4*>(kn + (h_lo + i / cn) * p.kn_s1 + (i % cn) * 8));
+  if (tid < 32) {
+    if (cs) rope_pair(k0, k1, cs[tid], cs[32 + tid], k0, k1);
+    kpr[2 * tid] = bf16_bits(k0);
+    kpr[2 * tid + 1] = bf16_bits(k1);
+  }
+  __syncthreads();
+  if (turns) {
+    uint32_t w[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float y0 = __uint_as_float(w[e] << 16), y1 = __uint_as_float(w[e] & 0xFFFF0000u);
+      rope_pair(y0, y1, cs[4 * cq + e], cs[32 + 4 * cq + e], y0, y1);
+      w[e] = static_cast<uint32_t>(bf16_bits(y0)) | (static_cast<uint32_t>(bf16_bits(y1)) << 16);
+    }
+    *reinterpret_cast<uint4*>(qp) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (hq < nh) *reinterpret_cast<uint4*>(ko + hq * de + dn + 8 * cq) = reinterpret_cast<const uint4*>(kpr)[cq];
+  // the latent, by the upper four warps
+  if (slot < 0 || tid < 128) return;
+  const int64_t blk = slot / p.block_size;
+  if (blk >= p.num_blocks) {
+    if (tid == 128) set_device_error(p.err, 4u);
+    return;
+  }
+  insert_latent<F>(p.cache + blk * p.block_stride + (slot % p.block_size) * p.entry_stride, p.kv_c + t * p.kv_s0, kr, cs, 1.f, tid - 128);
+}
+
 cudaError_t launch_prefill_epilogue(int fmt, const PrefillEpiParams& p, int Tp, cudaStream_t stream) {
+  if (fmt != 1 && p.vec_q) {
+    const dim3 wide(Tp, (p.H + 15) / 16);
+    if (fmt == 0)
+      mla_key_concat_kernel<0><<<wide, 256, 0, stream>>>(p);
+    else if (fmt == 2)
+      mla_key_concat_kernel<2><<<wide, 256, 0, stream>>>(p);
+    else
+      mla_key_concat_kernel<3><<<wide, 256, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
   const dim3 grid(Tp, (p.H + 3) / 4);
   if (fmt == 0)
     mla_prefill_epilogue_kernel<0><<<grid, 128, 0, stream>>>(p);
@@ -637,19 +721,6 @@ __global__ void __launch_bounds__(128) mla_gather_context_kernel(const GatherCtx
       out[2 * i] = o[0];
       out[2 * i + 1] = o[1];
     }
-  } else if (F == 3) {
-    // lane l: 16 codes of half a group -> 16 bf16 values
-    const float sj = e8m0_scale(__ldg(ent + 256 + (lane >> 1)));
-    const uint2 cw = __ldg(reinterpret_cast<const uint2*>(ent) + lane);
-    uint32_t r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = fp4x2_to_float2(((i < 4 ? cw.x : cw.y) >> (8 * (i & 3))) & 0xFFu);
-      r[i] = static_cast<uint32_t>(bf16_bits(f.x * sj)) | (static_cast<uint32_t>(bf16_bits(f.y * sj)) << 16);
-    }
-    out[2 * lane] = make_uint4(r[0], r[1], r[2], r[3]);
-    out[2 * lane + 1] = make_uint4(r[4], r[5], r[6], r[7]);
-    if (lane < 8) out[64 + lane] = __ldg(src + 17 + lane);     // rope bytes 272.. -> values 512..
   } else {
     uint4 o[2];
     const float sj = __ldg(reinterpret_cast<const float*>(ent + 512) + (lane >> 3));
@@ -657,6 +728,74 @@ __global__ void __launch_bounds__(128) mla_gather_context_kernel(const GatherCtx
     out[2 * lane] = o[0];
     out[2 * lane + 1] = o[1];
     if (lane < 8) out[64 + lane] = __ldg(src + 33 + lane);     // rope bytes 528.. -> values 512..
+  }
+}
+
+// mxfp4 entries as bf16, aligned: 400 bytes read and 1152 written a row, bound by memory.  A warp has kFp4Rows rows, found by
+// a lane each, and all their loads on their way before the first store.  Lane l has 8 codes of groups l / 4 and 8 + l / 4, so
+// that 8 bf16 values of every lane are 512 bytes in a row (16 codes of one group a lane, one row a warp at a time: 84 us for
+// 242000 rows).
+constexpr int kFp4Rows = 8;
+
+__global__ void __launch_bounds__(128) mla_gather_context_fp4_kernel(const GatherCtxParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5)) * kFp4Rows;
+  const int64_t end = min(p.num_tokens, static_cast<int64_t>(p.cu[p.batch]));
+  if (r0 >= end) return;
+  const uint8_t* ent = nullptr;
+  if (lane < kFp4Rows && r0 + lane < end) {
+    const int64_t r = r0 + lane;
+    int lo = 0, hi = p.batch - 1;         // the last request b with cu[b] <= r
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.cu[mid] <= r) lo = mid; else hi = mid - 1;
+    }
+    const int64_t pos = (p.starts ? p.starts[lo] : 0) + (r - p.cu[lo]);
+    const int64_t col = pos / p.block_size, blk = p.block_table[static_cast<int64_t>(lo) * p.bt_stride + col];
+    if (blk >= 0 && blk < p.num_blocks)
+      ent = p.cache + blk * p.block_stride + (pos - col * p.block_size) * p.entry_stride;
+    else
+      set_device_error(p.err, 2u);
+  }
+  uint32_t code[kFp4Rows][2], ex[kFp4Rows][2];
+  uint4 rope[kFp4Rows / 4];
+  auto row_of = [&](int i) -> const uint8_t* {
+    return reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(ent), i));
+  };
+#pragma unroll
+  for (int i = 0; i < kFp4Rows; ++i) {
+    const uint8_t* a = row_of(i);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      code[i][j] = a ? __ldg(reinterpret_cast<const uint32_t*>(a) + 32 * j + lane) : 0u;
+      ex[i][j] = a ? __ldg(a + 256 + 8 * j + (lane >> 2)) : 0u;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kFp4Rows / 4; ++i) {      // k_pe: eight lanes a row
+    const uint8_t* a = row_of(4 * i + (lane >> 3));
+    rope[i] = a ? __ldg(reinterpret_cast<const uint4*>(a + 272) + (lane & 7)) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < kFp4Rows; ++i) {
+    if (r0 + i >= end) break;
+    uint4* out = reinterpret_cast<uint4*>(p.dst + (r0 + i) * p.dst_row);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float sj = e8m0_scale(ex[i][j]);
+      uint32_t v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = fp4x2_to_float2((code[i][j] >> (8 * k)) & 0xFFu);
+        v[k] = static_cast<uint32_t>(bf16_bits(f.x * sj)) | (static_cast<uint32_t>(bf16_bits(f.y * sj)) << 16);
+      }
+      __stcs(out + 32 * j + lane, make_uint4(v[0], v[1], v[2], v[3]));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kFp4Rows / 4; ++i) {
+    const int64_t r = r0 + 4 * i + (lane >> 3);
+    if (r < end) __stcs(reinterpret_cast<uint4*>(p.dst + r * p.dst_row) + 64 + (lane & 7), rope[i]);
   }
 }
 
@@ -671,7 +810,8 @@ cudaError_t launch_gather_context(int fmt, int kind, const GatherCtxParams& p, c
     if (fmt == 0) mla_gather_context_kernel<0, 0><<<grid, 128, 0, stream>>>(p);
     else if (fmt == 1) mla_gather_context_kernel<1, 0><<<grid, 128, 0, stream>>>(p);
     else if (fmt == 2) mla_gather_context_kernel<2, 0><<<grid, 128, 0, stream>>>(p);
-    else mla_gather_context_kernel<3, 0><<<grid, 128, 0, stream>>>(p);
+    else if (!p.vec) mla_gather_context_kernel<3, 0><<<grid, 128, 0, stream>>>(p);
+    else mla_gather_context_fp4_kernel<<<static_cast<unsigned>((p.num_tokens + 4 * kFp4Rows - 1) / (4 * kFp4Rows)), 128, 0, stream>>>(p);
   }
   return cudaGetLastError();
 }
