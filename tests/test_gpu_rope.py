@@ -74,6 +74,29 @@ def test_shapes(m, dt, layout, T, H, D, R, at, inverse):
     assert m.read_device_errors() == 0
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("T,H,Hk,D,R,at", [(1, 1, 1, 64, 64, 0), (5, 3, 2, 96, 64, 32), (2, 64, 64, 128, 128, 0), (3, 1, 7, 1024, 512, 256), (4, 90, 1, 1024, 8, 1016),
+                                           (4099, 56, 8, 128, 128, 0), (4099, 60, 4, 136, 64, 8)])
+def test_keys_of_the_queries_shape(m, dt, layout, T, H, Hk, D, R, at):
+    """Up to tensors larger than the L2."""
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    q, k = torch.randn((T, H, D), generator=g, device="cuda").to(dt), torch.randn((T, Hk, D), generator=g, device="cuda").to(dt)
+    pos, tab = torch.randint(0, 5000, (T,), generator=g, device="cuda"), table(5000, R).cuda()
+    qo, ko = m.rope(q, pos, tab, k, layout=layout, q_at=at, k_at=at)
+    some = torch.randint(0, T, (min(T, 64),), generator=g, device="cuda") if T > 64 else torch.arange(T, device="cuda")
+    some[-1] = T - 1
+    for got, x in ((qo, q), (ko, k)):
+        xs, ps = x[some].cpu(), pos[some].cpu()
+        near(got[some], turned(xs, ps, tab.cpu(), layout, at), xs, layout, at, R)
+    # each alone, in place, and from a table that is not aligned to pieces: the same bits
+    odd = torch.empty(tab.numel() + 1, device="cuda")[1:].view_as(tab).copy_(tab)
+    assert torch.equal(m.rope(q, pos, tab, layout=layout, q_at=at), qo) and torch.equal(m.rope(k, pos, odd, layout=layout, q_at=at), ko)
+    assert torch.equal(m.rope(q, pos, odd, layout=layout, q_at=at), qo)
+    m.rope(q, pos, tab, k, layout=layout, q_at=at, k_at=at, q_out=q, k_out=k)
+    assert torch.equal(q, qo) and torch.equal(k, ko) and m.read_device_errors() == 0
+
+
 @pytest.mark.parametrize("layout", ["interleaved", "half"])
 def test_slices_of_one_buffer(m, layout):
     """q and k as strided slices of a fused projection, in place; what lies between stays."""
