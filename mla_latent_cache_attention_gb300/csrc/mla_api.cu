@@ -740,7 +740,7 @@ struct Fp4Plan {
 };
 Fp4Plan fp4_plan(int q_len, int H, int sms) {
   const int64_t cols = static_cast<int64_t>(q_len) * H;
-  const int nq = cols <= 16 ? 16 : 32;
+  const int nq = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
   const int64_t G = (cols + nq - 1) / nq;
   return Fp4Plan{nq, G, sms > G ? sms / G : 1};
 }

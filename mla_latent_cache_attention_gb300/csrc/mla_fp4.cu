@@ -14,7 +14,7 @@ __global__ void __launch_bounds__(256) mla_fp4_merge_kernel(const __grid_constan
   const int c = blockIdx.x, w0 = blockIdx.y, tid = threadIdx.x;
   const int64_t b = p.span[2 * w0 + 1];
   if (b < 0) return;
-  const int64_t run = p.span[2 * p.W], t1 = p.span[2 * w0] + (static_cast<int64_t>(p.seq_lens[b]) + kTile - 1) / kTile;
+  const int64_t run = p.span[2 * p.W], t1 = p.span[2 * w0] + (static_cast<int64_t>(p.seq_lens[b]) + p.keys - 1) / p.keys;
   const int n = static_cast<int>((t1 - 1) / run) - w0 + 1;
   // part i is slot 2 (w0 + i), the first one 2 w0 + 1
   auto at = [&](int i) -> int64_t { return (2 * static_cast<int64_t>(w0 + i) + (i == 0 ? 1 : 0)) * p.cols + c; };
@@ -62,8 +62,9 @@ __global__ void __launch_bounds__(256) mla_fp4_merge_kernel(const __grid_constan
 }
 
 template <int NQ>
-cudaError_t launch_nq(const Fp4Params& p, int grid, cudaStream_t stream) {
+cudaError_t launch_nq(Fp4Params& p, int grid, cudaStream_t stream) {
   using C = Fp4Cfg<NQ>;
+  p.keys = C::kKeys;
   static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -79,8 +80,9 @@ cudaError_t launch_nq(const Fp4Params& p, int grid, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_fp4_paged(int nq, const Fp4Params& p, cudaStream_t stream) {
-  return nq == 16 ? launch_nq<16>(p, p.W * p.G, stream) : launch_nq<32>(p, p.W * p.G, stream);
+cudaError_t launch_fp4_paged(int nq, Fp4Params& p, cudaStream_t stream) {
+  const int grid = p.W * p.G;
+  return nq == 16 ? launch_nq<16>(p, grid, stream) : nq == 32 ? launch_nq<32>(p, grid, stream) : launch_nq<64>(p, grid, stream);
 }
 
 cudaError_t launch_fp4_merge(const Fp4Params& p, cudaStream_t stream) {

@@ -13,23 +13,38 @@
 //     columns (a column is a (query token, head) pair); the CTAs of all groups take the same run side by side and meet
 //     its records in L2.  Where a run begins or ends inside a request its part is a partial result, at most two a CTA,
 //     which a second kernel joins; the lengths are read on the GPU, so a captured graph stays balanced.  (Splits of
-//     equal length, handed out by a counter: 32 requests of 1024 to 8192 keys 63 us.)  Tiles of 128 keys, two in shared memory: 4 x 16 KB of E4M3 and 16 KB of bf16 k_pe
-//     each, K-major with 128-byte swizzle, read by both products.
-//   * Sixteen loader warps take 8 keys of a tile each: 16-byte loads straight from the pages (a lane holds one
-//     group: 32 codes and their exponent) one tile ahead in registers, block ids two tiles ahead.  A group's
-//     exponent below K picks two words that hold the E4M3 bytes of the eight magnitudes at that scale; a byte
-//     permute turns four codes into four bytes.  That is 1.5 instructions a code, where the conversion
-//     instructions by way of f16 take as many but run at half rate.
+//     equal length, handed out by a counter: 32 requests of 1024 to 8192 keys 63 us, 41 so.)
+//   * Two tiles in shared memory, each four slots of E4M3 codes of 128 values and bf16 k_pe, K-major with 128-byte swizzle, read by
+//     both products.  Up to 32 columns take tiles of 128 keys.  More take 64 at once: what bounds them is a tile's conversion
+//     and the products' reads of it, whose cost hardly depends on the columns (4 x 16 rows over 16k to 128k keys, 64 requests:
+//     two groups of 32 1350 us, one of 64 1010).  64 columns leave room for two tiles of 112 keys (14 a loader warp), of which
+//     the products' last 16 rows are taken from what lies behind; of 128 keys only seven slots of eight fit, so that a tile
+//     waited for the PV of the one before (1071 us).
+//   * Eight loader warps take 16 (14) keys of a tile each: 16-byte loads straight from the pages one tile ahead in
+//     registers, block ids two tiles ahead.  A group's exponent below K picks two words that hold the E4M3 bytes of the eight
+//     magnitudes at that scale; a byte permute turns four codes into four bytes.  That is 1.5 instructions a code,
+//     where the conversion instructions by way of f16 take as many but run at half rate.
 //   * Products on the 5th-generation tensor cores with keys (latents) as M = 128 and query columns as N.
-//     S^T = V Q^T: the bf16 query of a column as two E4M3 terms hi + 2^-4 lo of 2^e q, stacked along N (they
-//     carry its 8 bits down to 2^-6 of the scaled range's 448); k_pe . q_pe as a bf16 product of its own.
+//     S^T = V Q^T: the bf16 query of a column as two E4M3 terms hi + 2^-4 lo of 2^e q (they carry its 8 bits down to 2^-6
+//     of the scaled range's 448); k_pe . q_pe as a bf16 product of its own.
 //   * Online softmax over s' = s + K - 6: the weight of a key's codes is w = 2^(s' - m), its share of the row
 //     sum w 2^(6 - K) = 2^(s - m), so the key's scale costs one multiplication.  The weights enter
-//     O^T += V^T P as two E4M3 terms hi + 2^-4 lo (to 2^-8 of a weight, down to 2^-11 of the reference),
-//     stacked along N and added in the epilogue.  The reference m moves only when a logit passes it by kTau.
-//   * Roles hand over through mbarriers, each waited with a time limit.
+//     O^T += V^T P as two E4M3 terms hi + 2^-4 lo (to 2^-8 of a weight, down to 2^-11 of the reference).
+//     The reference m moves only when a logit passes it by kTau.
+//   * hi and lo terms are stacked along N, with accumulators of their own that the epilogue adds; at 64 columns the tensor memory has
+//     no room for those, and hi and the plain rest lo = x - hi go to the same accumulator, one after the other along K.  A
+//     rest is then kept to 2^-10 of the scaled range: a query's value to 2^-18 of the column's largest, a weight to 2^-13 of the
+//     reference (which lies higher in E4M3's range for it, and kTau lower).
+//   * Roles hand over through mbarriers, each waited with a time limit.  Waits between the products and what feeds them are
+//     polled: a suspended thread (try_wait) was woken 0.5 to 1 us late, four times a tile (1390 -> 1095 us; of 16 columns 43 ->
+//     39).  The scheduler and the wait for a work item are not in a hurry.
 //
-// Warps: 0 scheduler, 1 QK issuer (TMEM owner), 2 PV issuer, then four softmax warps (which also prepare the query and
+// What bounds it now, 64 columns (3.6 us a tile of 112 keys): loaders (3.4 us: load latency, then conversion and 1.4 us of stores),
+// softmax (1.8 us, ordered after QK) and the tensor pipe, whose operand reads (6 KB a product of 33 cycles) share
+// the data path of shared memory with both: 2.5 us of 68 products at 75 cycles each.  Up to 32 columns: the chain of load, conversion,
+// QK, softmax and PV of two tiles (2.7 us a tile).
+//
+// Warps: 0 scheduler, 1 QK issuer (TMEM owner), 2 PV issuer, then the softmax warps (which also prepare the query and
 // write the results), then 8 loaders.
 #pragma once
 #include "mla_ds.cuh"
@@ -51,7 +66,7 @@ struct Fp4Params {
   uint32_t num_blocks;
   int block_size, bs_shift;       // n / block_size = n bs_magic / 2^(31 + bs_shift) for n < 2^31: bs_shift = ceil(log2(block_size)),
   uint32_t bs_magic;              // bs_magic = ceil(2^(31 + bs_shift) / block_size)
-  int W;                          // runs of tiles: the grid is W x G
+  int W, keys;                    // runs of tiles: the grid is W x G; keys of a tile (Fp4Cfg::kKeys)
   float sig2;                     // softmax scale * log2(e)
   uint8_t* out;
   int64_t o_s0b, o_s1b;
@@ -67,14 +82,24 @@ struct Fp4Params {
 
 template <int NQ_>
 struct Fp4Cfg {
-  static_assert(NQ_ == 16 || NQ_ == 32, "columns per item");
-  static constexpr int NQ = NQ_, NB = 5;
-  static constexpr int NC = NQ;                                   // columns of a softmax thread
+  static_assert(NQ_ == 16 || NQ_ == 32 || NQ_ == 64, "columns per item");
+  static constexpr int NQ = NQ_;
+  static constexpr bool kWide = NQ == 64;                         // hi and lo terms along K, short tiles (see above)
+  static constexpr int kN = kWide ? NQ : 2 * NQ;                  // columns of a code product
+  // keys of a tile: 128, or 112 of the 128 rows of a product where the columns leave two tiles of 128 no room
+  static constexpr int kKeys = kWide ? 112 : 128, kSlot = kKeys * 128, kRopes = kWide ? 1 : 2;
+  static constexpr int NC = NQ < 32 ? NQ : 32;                    // columns of a softmax thread
   static constexpr int kSW = 4 * (NQ / NC);                       // softmax warps
-  static constexpr int kLoadWarps = 8, kPvWarp = 2, kFirstSm = 3, kFirstLoad = kFirstSm + kSW;
+  static constexpr int kLoadWarps = 8, kPvWarp = 2, kFirstSm = kWide ? 4 : 3, kFirstLoad = kFirstSm + kSW;
   static constexpr int kThreads = 32 * (kFirstLoad + kLoadWarps);
-  static constexpr int kRing = 0;                                 // 2 x 5 x 16 KB
-  static constexpr int kQ = kRing + 2 * NB * kSlotBytes;          // 4 x (2 NQ rows x 128 B): hi rows, then lo rows
+  // 640 threads start with 96 registers; the warps of the issuers leave the others what those need (61440 in all, as at
+  // the start)
+  static constexpr int kIssueRegs = 32, kSoftmaxRegs = 120, kLoadRegs = 104;
+  static_assert(!kWide || (kThreads == 640 && 128 * kIssueRegs + 256 * kSoftmaxRegs + 256 * kLoadRegs <= 640 * 96), "registers of the launch");
+  static constexpr int kRing = 0;                                 // code tiles
+  static constexpr int kPad = (128 - kKeys) * 128;                // of the last slot's products: zeros
+  static constexpr int kRope = kRing + 8 * kSlot + kPad;          // k_pe
+  static constexpr int kQ = kRope + kRopes * kSlot;               // 4 x (2 NQ rows x 128 B): hi rows, then lo rows
   static constexpr int kQRope = kQ + 4 * 2 * NQ * 128;            // NQ x 128 B
   static constexpr int kP = kQRope + NQ * 128;                    // 128 keys x 2 NQ
   static constexpr int kScale = kP + kTile * 2 * NQ;              // [2][128] fp32: 2^(K - 6), -1 masked
@@ -83,18 +108,22 @@ struct Fp4Cfg {
   static constexpr int kMref = kColF + NQ * 4;                    // [NQ]
   static constexpr int kAlph = kMref + NQ * 4;                    // [NQ]
   static constexpr int kLut = kAlph + NQ * 4;                     // [16] x 8 B
-  static constexpr int kItems = kLut + 16 * 8;
+  static constexpr int kBelow = kLut + 16 * 8;                    // [128] x 16 B
+  static constexpr int kItems = kBelow + kTile * 16;
   static constexpr int kBar = kItems + kItemDepth * 32;
-  static constexpr int kParts = 2;                                // commits of a tile's PV
-  static constexpr int kNumBars = 2 * NB + 2 + 2 + 2 * kParts + 4 + 2 * kItemDepth;
+  static constexpr int kParts = 2;                    // commits of a tile's PV
+  static constexpr int kNumBars = 4 + 2 + 2 + 2 * kParts + 4 + 2 * kItemDepth;
   static constexpr int kMisc = kBar + kNumBars * 8;
   static constexpr int kTotal = kMisc + 16;
   static constexpr int kAlloc = kTotal + 1024;
   static_assert(kAlloc <= kSmemLimit, "shared memory budget");
-  static constexpr int kS = 3 * NQ;                               // S: hi, lo, rope columns; two of them
-  static constexpr int kTmemO = 2 * kS;                           // O_j at kTmemO + 2 NQ j: hi, lo
-  static constexpr int kTmemCols = kTmemO + 8 * NQ <= 256 ? 256 : 512;
-  static_assert(kTmemO + 8 * NQ <= kTmemCols, "TMEM budget");
+  static constexpr int kS = kN + NQ;                              // S: codes, then rope columns; two of them
+  static constexpr int kTmemO = 2 * kS;                           // O_j at kTmemO + kN j
+  static constexpr int kTmemCols = kTmemO + 4 * kN <= 256 ? 256 : 512;
+  static_assert(kTmemO + 4 * kN <= kTmemCols, "TMEM budget");
+  // The lo terms of E4M3 pairs: 16 times the rest where they have columns of their own, the rest itself where they add to
+  // the hi terms' (rests below 2^-10 are lost).  The weights are 2^(kPExp + kTau) at most (2^8.75 of 448).
+  static constexpr float kLo = kWide ? 1.f : 16.f, kTau = kWide ? 5.f : 7.f, kPExp = kWide ? 3.75f : 1.f;
 };
 
 // The E4M3 bytes of eight codes: the magnitudes picked by permutes from the eight bytes of lut, with the codes as
@@ -148,6 +177,28 @@ __device__ __forceinline__ bool group_wait(bool first, uint32_t id, uint32_t thr
   if (first) w = warp_wait(bar, parity, abort_flag);
   return named_bar_and(id, threads, w);
 }
+// A wait that is in a hurry: an issuer's, polled.
+__device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_test_wait(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t now = globaltimer();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > wait_limit_ns(abort_flag)) {
+        *abort_flag = 2;
+        return false;
+      }
+    }
+  }
+}
+// The same by one lane of a warp.
+__device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  bool w = true;
+  if ((threadIdx.x & 31) == 0) w = spin_wait(bar, parity, abort_flag);
+  return __shfl_sync(0xFFFFFFFFu, w ? 1 : 0, 0) != 0;
+}
 // A wait that is in no hurry.
 __device__ __forceinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   const uint64_t t0 = globaltimer();
@@ -166,7 +217,6 @@ __device__ __forceinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volati
 template <int NQ>
 __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const __grid_constant__ Fp4Params p) {
   using C = Fp4Cfg<NQ>;
-  constexpr int NB = C::NB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);      // (known to be shared: no generic accesses)
   uint8_t* ring = smem + C::kRing;
@@ -182,8 +232,8 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
   uint2* lut = reinterpret_cast<uint2*>(smem + C::kLut);
   WorkItem* items = reinterpret_cast<WorkItem*>(smem + C::kItems);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar);
-  uint64_t* full = bars;                  // [2][NB] the loader warps have written the slot (k_pe and the scales first)
-  uint64_t* s_full = full + 2 * NB;       // [2] QK done
+  uint64_t* full = bars;                  // [2][2] the loader warps have written two code tiles, and k_pe and the scales with one of them
+  uint64_t* s_full = full + 4;            // [2] QK done
   uint64_t* s_free = s_full + 2;          // [2] the softmax has read S
   uint64_t* pv_part = s_free + 2;         // [2][kParts] PV of the value tiles done
   uint64_t* p_full = pv_part + 2 * C::kParts;      // P is written (one arrival per softmax warp)
@@ -204,7 +254,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
   if (warp == 0) {
     for (int i = lane; i < C::kNumBars; i += 32) {
       uint32_t count = 1;
-      if (i < 2 * NB) count = C::kLoadWarps;
+      if (i < 4) count = C::kLoadWarps;
       if (&bars[i] == p_full) count = C::kSW;                                // the softmax warps
       if (&bars[i] >= item_empty) count = 3 + C::kLoadWarps;                 // the roles
       mbar_init(&bars[i], count);
@@ -219,6 +269,11 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
+  // Products read 128 rows: of a shorter tile's last ones they take those behind the slot (the next slot's codes, in the end a
+  // pad), whose scores are masked and whose weights are zeros: numbers all of them, once these are zeros.
+  if constexpr (C::kKeys < kTile)
+    for (int i = tid; i < 9 * C::kPad / 16; i += C::kThreads)
+      *reinterpret_cast<uint4*>(ring + i / (C::kPad / 16) * C::kSlot + i % (C::kPad / 16) * 16) = make_uint4(0, 0, 0, 0);
   if (warp == 0 && lane < 16) {
     // magnitudes 0, .5, 1, 1.5 | 2, 3, 4, 6 times 2^(6 - lane) in E4M3: exact down to 2^-9, zero below
     // (entry 15 is all zeros)
@@ -233,6 +288,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     }
     lut[lane] = make_uint2(w[0], w[1]);
   }
+  if (C::kKeys < kTile) fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -242,202 +298,213 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0) TL(0, 2);
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ scheduler
-    auto tiles_of = [&](int b) -> int64_t { return static_cast<int64_t>((static_cast<uint32_t>(max(p.seq_lens[b], 0)) + (kTile - 1)) / kTile); };
-    // a lane sums a run of requests; the lane that holds this CTA's first tile looks for its request
-    const int per_lane = (p.B + 31) / 32, b0 = min(lane * per_lane, p.B), b1 = min(b0 + per_lane, p.B);
-    int64_t sum = 0;
+  // (the registers are set inside the roles' branches: the compiler gives a branch what it sets)
+  if (warp < C::kFirstSm) {
+    if constexpr (C::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
+    if (warp == 0) {
+      // ------------------------------------------------------------------ scheduler
+      auto tiles_of = [&](int b) -> int64_t { return static_cast<int64_t>((static_cast<uint32_t>(max(p.seq_lens[b], 0)) + (C::kKeys - 1)) / C::kKeys); };
+      // a lane sums a run of requests; the lane that holds this CTA's first tile looks for its request
+      const int per_lane = (p.B + 31) / 32, b0 = min(lane * per_lane, p.B), b1 = min(b0 + per_lane, p.B);
+      int64_t sum = 0;
 #pragma unroll 4
-    for (int b = b0; b < b1; ++b) sum += tiles_of(b);
-    int64_t end = sum;
+      for (int b = b0; b < b1; ++b) sum += tiles_of(b);
+      int64_t end = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, end, o);
-      if (lane >= o) end += v;
-    }
-    const int64_t total = __shfl_sync(0xFFFFFFFFu, end, 31);
-    // (a division in 32 bits where that is enough: one in 64 takes a lone lane 0.3 us)
-    const int64_t run = total <= 0 ? 1
-                        : total < (int64_t(1) << 31) - p.W
-                            ? static_cast<int64_t>((static_cast<uint32_t>(total) + static_cast<uint32_t>(p.W - 1)) / static_cast<uint32_t>(p.W))
-                            : (total + p.W - 1) / p.W;
-    const int w = static_cast<int>(blockIdx.x) / p.G, g = static_cast<int>(blockIdx.x) % p.G;
-    const int64_t lo = min(w * run, total), hi = min(lo + run, total);
-    int b = p.B;
-    int64_t t0 = end - sum;      // first tile of request b
-    if (lo < hi && t0 <= lo && lo < end) {
-      b = b0;
-      for (int64_t n; (n = tiles_of(b)) <= lo - t0; ++b) t0 += n;
-    }
-    const uint32_t who = __ballot_sync(0xFFFFFFFFu, b < p.B);
-    const int src = who ? __ffs(who) - 1 : 0;
-    b = __shfl_sync(0xFFFFFFFFu, b, src);
-    t0 = __shfl_sync(0xFFFFFFFFu, t0, src);
-    if (lane == 0) {
-      TL(0, 3);
-      if (blockIdx.x == 0) p.span[2 * p.W] = run;
-      int64_t t = lo, on_t = 0, on_b = -1;
-      for (int nitem = 0;; ++nitem) {
-        WorkItem it{};
-        it.b = -1;
-        if (t < hi) {
-          const int64_t n = tiles_of(b);
-          it.b = b;
-          it.g = g;
-          it.L = p.seq_lens[b];
-          it.ntiles = static_cast<int>(min(hi, t0 + n) - t);
-          it.k0 = static_cast<int>((t - t0) * kTile);
-          it.n = static_cast<int>(min(static_cast<int64_t>(it.L) - it.k0, static_cast<int64_t>(it.ntiles) * kTile));
-          it.pad = it.ntiles == n;                      // the whole request: final
-          it.s = 2 * w + (t == t0 ? 1 : 0);
-          if (t == t0 && it.ntiles < n) on_t = t0, on_b = b;
-          t += it.ntiles;
-          if (t == t0 + n) {
-            t0 = t;
-            do ++b;
-            while (b < p.B && p.seq_lens[b] <= 0);
+      for (int o = 1; o < 32; o *= 2) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, end, o);
+        if (lane >= o) end += v;
+      }
+      const int64_t total = __shfl_sync(0xFFFFFFFFu, end, 31);
+      // (a division in 32 bits where that is enough: one in 64 takes a lone lane 0.3 us)
+      const int64_t run = total <= 0 ? 1
+                          : total < (int64_t(1) << 31) - p.W
+                              ? static_cast<int64_t>((static_cast<uint32_t>(total) + static_cast<uint32_t>(p.W - 1)) / static_cast<uint32_t>(p.W))
+                              : (total + p.W - 1) / p.W;
+      const int w = static_cast<int>(blockIdx.x) / p.G, g = static_cast<int>(blockIdx.x) % p.G;
+      const int64_t lo = min(w * run, total), hi = min(lo + run, total);
+      int b = p.B;
+      int64_t t0 = end - sum;      // first tile of request b
+      if (lo < hi && t0 <= lo && lo < end) {
+        b = b0;
+        for (int64_t n; (n = tiles_of(b)) <= lo - t0; ++b) t0 += n;
+      }
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, b < p.B);
+      const int src = who ? __ffs(who) - 1 : 0;
+      b = __shfl_sync(0xFFFFFFFFu, b, src);
+      t0 = __shfl_sync(0xFFFFFFFFu, t0, src);
+      if (lane == 0) {
+        TL(0, 3);
+        if (blockIdx.x == 0) p.span[2 * p.W] = run;
+        int64_t t = lo, on_t = 0, on_b = -1;
+        for (int nitem = 0;; ++nitem) {
+          WorkItem it{};
+          it.b = -1;
+          if (t < hi) {
+            const int64_t n = tiles_of(b);
+            it.b = b;
+            it.g = g;
+            it.L = p.seq_lens[b];
+            it.ntiles = static_cast<int>(min(hi, t0 + n) - t);
+            it.k0 = static_cast<int>((t - t0) * C::kKeys);
+            it.n = static_cast<int>(min(static_cast<int64_t>(it.L) - it.k0, static_cast<int64_t>(it.ntiles) * C::kKeys));
+            it.pad = it.ntiles == n;                      // the whole request: final
+            it.s = 2 * w + (t == t0 ? 1 : 0);
+            if (t == t0 && it.ntiles < n) on_t = t0, on_b = b;
+            t += it.ntiles;
+            if (t == t0 + n) {
+              t0 = t;
+              do ++b;
+              while (b < p.B && p.seq_lens[b] <= 0);
+            }
           }
+          const int k = nitem % kItemDepth;
+          if (nitem >= kItemDepth && !slow_wait(&item_empty[k], static_cast<uint32_t>((nitem / kItemDepth) - 1) & 1u, abort_flag)) break;
+          items[k] = it;
+          mbar_arrive(&item_full[k]);
+          if (it.b < 0) break;
         }
-        const int k = nitem % kItemDepth;
-        if (nitem >= kItemDepth && !slow_wait(&item_empty[k], static_cast<uint32_t>((nitem / kItemDepth) - 1) & 1u, abort_flag)) break;
-        items[k] = it;
-        mbar_arrive(&item_full[k]);
-        if (it.b < 0) break;
+        if (g == 0) {
+          p.span[2 * w] = on_t;
+          p.span[2 * w + 1] = on_b;
+        }
       }
-      if (g == 0) {
-        p.span[2 * w] = on_t;
-        p.span[2 * w + 1] = on_b;
+      __syncwarp();
+      // requests without keys: zeros, every W-th one
+      for (int z = w; z < p.B; z += p.W) {
+        if (p.seq_lens[z] > 0) continue;
+        for (int c = g * NQ; c < min(g * NQ + NQ, p.cols); ++c) {
+          const int64_t r = static_cast<int64_t>(z) * p.q_len + c / p.H;
+          uint8_t* o = p.out + r * p.o_s0b + static_cast<int64_t>(c % p.H) * p.o_s1b;
+          for (int d = lane; d < kLora; d += 32) *reinterpret_cast<uint16_t*>(o + 2 * d) = 0;
+          if (p.lse && lane == 0) p.lse[r * p.H + c % p.H] = -CUDART_INF_F;
+        }
       }
-    }
-    __syncwarp();
-    // requests without keys: zeros, every W-th one
-    for (int z = w; z < p.B; z += p.W) {
-      if (p.seq_lens[z] > 0) continue;
-      for (int c = g * NQ; c < min(g * NQ + NQ, p.cols); ++c) {
-        const int64_t r = static_cast<int64_t>(z) * p.q_len + c / p.H;
-        uint8_t* o = p.out + r * p.o_s0b + static_cast<int64_t>(c % p.H) * p.o_s1b;
-        for (int d = lane; d < kLora; d += 32) *reinterpret_cast<uint16_t*>(o + 2 * d) = 0;
-        if (p.lse && lane == 0) p.lse[r * p.H + c % p.H] = -CUDART_INF_F;
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ QK issuer
-    // (the warp goes along as a whole, so that the descriptors stay in uniform registers; one lane issues)
-    {
-      const bool one = elect_one();
-      const uint64_t dK0 = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
-      const uint64_t dQ0 = smem_desc(smem_u32(qs), 16, 1024, kSwizzle128B);
-      const uint64_t dQr = smem_desc(smem_u32(qr), 16, 1024, kSwizzle128B);
-      constexpr uint32_t kIdNope = idesc_e4m3(128, 2 * NQ, 0, 0);
-      constexpr uint32_t kIdRope = idesc_f16(128, NQ, 1, 1, 0, 0);
-      bool ok = true;
-      int nit = 0, nq = 0, g = 0;
-      while (ok) {
-        const int k = nit % kItemDepth;
-        if (!warp_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag)) break;
-        const WorkItem it = items[k];
-        __syncwarp();
-        if (one) mbar_arrive(&item_empty[k]);
-        ++nit;
-        if (it.b < 0) break;
-        if (!warp_wait(q_full, nq & 1, abort_flag)) break;
-        ++nq;
-        for (int t = 0; t < it.ntiles && ok; ++t) {
-          const int gt = g + t, h = gt & 1;
-          if (gt >= 2 && !warp_wait(&s_free[h], static_cast<uint32_t>((gt - 2) >> 1) & 1u, abort_flag)) ok = false;
-          if (!ok) break;
-          if (lane == 0) TL(1, 1);
-          const uint32_t dS = tmem + h * C::kS;
-          const uint32_t use = static_cast<uint32_t>(gt >> 1) & 1u;
-          // as the loaders finish the slots: k_pe and two code tiles, then the other two
-          if (!warp_wait(&full[h * NB + 1], use, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) TL(1, 2);
-          {
-            const uint64_t aK = desc_add(dK0, static_cast<uint32_t>((h * NB + 4) * (kSlotBytes >> 4)));
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16_if(one, dS + 2 * NQ, desc_add(aK, (kk * 32) >> 4), desc_add(dQr, (kk * 32) >> 4), kIdRope, kk > 0 ? 1u : 0u);
-          }
-#pragma unroll 1
-          for (int b = 0; b < 4 && ok; ++b) {
-            if (b == 2) ok = warp_wait(&full[h * NB + 3], use, abort_flag);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------------ QK issuer
+      // (the warp goes along as a whole, so that the descriptors stay in uniform registers; one lane issues)
+      {
+        const bool one = elect_one();
+        const uint64_t dK0 = smem_desc(smem_u32(ring), 16, 1024, kSwizzle128B);
+        const uint64_t dR0 = smem_desc(smem_u32(smem + C::kRope), 16, 1024, kSwizzle128B);
+        const uint64_t dQ0 = smem_desc(smem_u32(qs), 16, 1024, kSwizzle128B);
+        const uint64_t dQr = smem_desc(smem_u32(qr), 16, 1024, kSwizzle128B);
+        constexpr uint32_t kIdNope = idesc_e4m3(128, C::kN, 0, 0);
+        constexpr uint32_t kIdRope = idesc_f16(128, NQ, 1, 1, 0, 0);
+        bool ok = true;
+        int nit = 0, nq = 0, g = 0;
+        while (ok) {
+          const int k = nit % kItemDepth;
+          if (!warp_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag)) break;
+          const WorkItem it = items[k];
+          __syncwarp();
+          if (one) mbar_arrive(&item_empty[k]);
+          ++nit;
+          if (it.b < 0) break;
+          if (!warp_wait(q_full, nq & 1, abort_flag)) break;
+          ++nq;
+          for (int t = 0; t < it.ntiles && ok; ++t) {
+            const int gt = g + t, h = gt & 1;
+            if (gt >= 2 && !warp_wait(&s_free[h], static_cast<uint32_t>((gt - 2) >> 1) & 1u, abort_flag)) ok = false;
             if (!ok) break;
+            if (lane == 0) TL(1, 1);
+            const uint32_t dS = tmem + h * C::kS;
+            const uint32_t use = static_cast<uint32_t>(gt >> 1) & 1u;
+            // as the loaders finish the slots: two code tiles, then the other two; k_pe comes with the first ones, or last
+            // where it has one slot only
+            auto rope_product = [&]() {
+              const uint64_t aK = desc_add(dR0, static_cast<uint32_t>((gt % C::kRopes) * (C::kSlot >> 4)));
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_f16_if(one, dS + C::kN, desc_add(aK, (kk * 32) >> 4), desc_add(dQr, (kk * 32) >> 4), kIdRope, kk > 0 ? 1u : 0u);
+            };
+#pragma unroll 1
+            for (int b = 0; b < 4 && ok; ++b) {
+              if ((b & 1) == 0) {
+                ok = __all_sync(0xFFFFFFFFu, spin_wait(&full[2 * h + (b >> 1)], use, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) TL(1, 2);
+                if (b == (C::kRopes == 1 ? 2 : 0)) rope_product();
+              }
+              const uint64_t aK = desc_add(dK0, static_cast<uint32_t>((4 * h + b) * (C::kSlot >> 4)));
+              const uint64_t bQ = desc_add(dQ0, static_cast<uint32_t>(b * (2 * NQ * 128 >> 4)));
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                mma_f8_if(one, dS, desc_add(aK, (kk * 32) >> 4), desc_add(bQ, (kk * 32) >> 4), kIdNope, (b | kk) ? 1u : 0u);
+                if constexpr (C::kWide) mma_f8_if(one, dS, desc_add(aK, (kk * 32) >> 4), desc_add(bQ, (NQ * 128 + kk * 32) >> 4), kIdNope, 1u);
+              }
+            }
+            if (!ok) break;
+            mma_commit_if(one, &s_full[h]);
+            if (lane == 0) TL(1, 3);
+          }
+          g += it.ntiles;
+        }
+        mma_commit_if(one, fin);
+        volatile int no_abort[2] = {0, 0};
+        mbar_wait(fin, 0, no_abort);
+      }
+      __syncwarp();
+    } else if (warp == C::kPvWarp) {
+      // ------------------------------------------------------------------ PV issuer
+      {
+        const bool one = elect_one();
+        const uint64_t dV0 = smem_desc(smem_u32(ring), C::kSlot, 1024, kSwizzle128B);
+        const uint64_t dP0 = smem_desc(smem_u32(ps), 2 * NQ * 8, 128, kSwizzleNone);
+        constexpr uint32_t kIdPv = idesc_e4m3(128, C::kN, 1, 1);
+        bool ok = true;
+        int nit = 0, g = 0;
+        while (ok) {
+          const int k = nit % kItemDepth;
+          if (!warp_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag)) break;
+          const WorkItem it = items[k];
+          __syncwarp();
+          if (one) mbar_arrive(&item_empty[k]);
+          ++nit;
+          if (it.b < 0) break;
+          for (int t = 0; t < it.ntiles; ++t) {
+            const int gt = g + t;
+            if (!__all_sync(0xFFFFFFFFu, spin_wait(p_full, static_cast<uint32_t>(gt) & 1u, abort_flag))) {
+              ok = false;
+              break;
+            }
             tc_fence_after();
-            const uint64_t aK = desc_add(dK0, static_cast<uint32_t>((h * NB + b) * (kSlotBytes >> 4)));
-            const uint64_t bQ = desc_add(dQ0, static_cast<uint32_t>(b * (2 * NQ * 128 >> 4)));
+            if (lane == 0) TL(2, 1);
+            const uint32_t acc0 = t == 0 ? 0u : 1u;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f8_if(one, dS, desc_add(aK, (kk * 32) >> 4), desc_add(bQ, (kk * 32) >> 4), kIdNope, (b | kk) ? 1u : 0u);
+            for (int j = 0; j < 4; ++j) {
+              const uint64_t aV = desc_add(dV0, static_cast<uint32_t>((4 * (gt & 1) + j) * (C::kSlot >> 4)));
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                mma_f8_if(one, tmem + C::kTmemO + C::kN * j, desc_add(aV, (kk * 4096) >> 4), desc_add(dP0, (kk * NQ * 64) >> 4), kIdPv, kk > 0 ? 1u : acc0);
+                if constexpr (C::kWide)
+                  mma_f8_if(one, tmem + C::kTmemO + C::kN * j, desc_add(aV, (kk * 4096) >> 4), desc_add(dP0, (kk * NQ * 64 + NQ * 8) >> 4), kIdPv, 1u);
+              }
+              if ((j + 1) % (4 / C::kParts) == 0) mma_commit_if(one, &pv_part[(gt & 1) * C::kParts + j / (4 / C::kParts)]);
+            }
+            if (lane == 0) TL(2, 2);
           }
-          if (!ok) break;
-          mma_commit_if(one, &s_full[h]);
-          if (lane == 0) TL(1, 3);
+          g += it.ntiles;
         }
-        g += it.ntiles;
+        mma_commit_if(one, fin_pv);
+        volatile int no_abort[2] = {0, 0};
+        mbar_wait(fin_pv, 0, no_abort);
       }
-      mma_commit_if(one, fin);
-      volatile int no_abort[2] = {0, 0};
-      mbar_wait(fin, 0, no_abort);
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp == C::kPvWarp) {
-    // ------------------------------------------------------------------ PV issuer
-    {
-      const bool one = elect_one();
-      const uint64_t dV0 = smem_desc(smem_u32(ring), kSlotBytes, 1024, kSwizzle128B);
-      const uint64_t dP0 = smem_desc(smem_u32(ps), 2 * NQ * 8, 128, kSwizzleNone);
-      constexpr uint32_t kIdPv = idesc_e4m3(128, 2 * NQ, 1, 1);
-      bool ok = true;
-      int nit = 0, g = 0;
-      while (ok) {
-        const int k = nit % kItemDepth;
-        if (!warp_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag)) break;
-        const WorkItem it = items[k];
-        __syncwarp();
-        if (one) mbar_arrive(&item_empty[k]);
-        ++nit;
-        if (it.b < 0) break;
-        for (int t = 0; t < it.ntiles; ++t) {
-          const int gt = g + t;
-          if (!warp_wait(p_full, static_cast<uint32_t>(gt) & 1u, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (lane == 0) TL(2, 1);
-          const uint32_t acc0 = t == 0 ? 0u : 1u;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint64_t aV = desc_add(dV0, static_cast<uint32_t>(((gt & 1) * NB + j) * (kSlotBytes >> 4)));
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f8_if(one, tmem + C::kTmemO + 2 * NQ * j, desc_add(aV, (kk * 4096) >> 4), desc_add(dP0, (kk * NQ * 64) >> 4), kIdPv,
-                        kk > 0 ? 1u : acc0);
-            if ((j + 1) % (4 / C::kParts) == 0) mma_commit_if(one, &pv_part[(gt & 1) * C::kParts + j / (4 / C::kParts)]);
-          }
-          if (lane == 0) TL(2, 2);
-        }
-        g += it.ntiles;
-      }
-      mma_commit_if(one, fin_pv);
-      volatile int no_abort[2] = {0, 0};
-      mbar_wait(fin_pv, 0, no_abort);
-    }
-    __syncwarp();
   } else if (warp >= C::kFirstLoad) {
+    if constexpr (C::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kLoadRegs));
     // ------------------------------------------------------------------ loaders
-    // Warp w owns keys KW w .. KW w + KW - 1 of every tile, four lanes a key: lane = 4 r + u takes, of keys r, r + 8, ..., the
-    // groups 4 j + u of the four code tiles j and two 16-byte pieces of k_pe.  A quarter of the warp so stores an even
-    // and the next odd row, whose columns the swizzle keeps apart.
-    constexpr int KW = kTile / C::kLoadWarps, KL = KW / 8;
-    static_assert(KW % 8 == 0, "a lane's rows are whole swizzle groups apart");
+    // Warp w owns keys KW w .. KW w + KW - 1 of every tile.  Lane k < 16 finds key k's record and has its exponents; the
+    // codes and k_pe are loaded eight lanes a key, 128 bytes in a row: lane 16 a + 8 b + 4 c + u takes, of keys 4 m + 2 a + c, the
+    // groups 8 h + 4 b + u (code tile 2 h + b) and a piece of k_pe.  A quarter of the warp so stores an even and the next odd
+    // row, whose columns the swizzle keeps apart.  (Four lanes a key, 64 bytes in a row: a third more time in the loads.)
+    constexpr int KW = C::kKeys / C::kLoadWarps;      // 16 or 14
+    static_assert(KW <= 16 && KW % 2 == 0, "a lane of half a warp for each key");
     const int w = warp - C::kFirstLoad;
-    const int key = lane >> 2, u = lane & 3;
+    const int u = lane & 3, kb = (lane >> 3) & 1, key0 = 2 * (lane >> 4) + ((lane >> 2) & 1);      // key of m: 4 m + key0
+    uint4* below = reinterpret_cast<uint4*>(smem + C::kBelow) + 16 * w;                             // [key] 16 bytes: exponents below K
     struct Cursor {
       const int32_t* table;      // the request's block ids; null: past the last tile
       int kp, end, left;         // this lane's key of the tile, the item's end, tiles after this one
@@ -457,7 +524,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         if (lane == 0) mbar_arrive(&item_empty[k]);
         ++nit;
         c.table = b < 0 ? nullptr : p.block_table + static_cast<int64_t>(b) * p.bt_stride;
-        c.kp = k0 + KW * w + key;
+        c.kp = k0 + KW * w + lane;
         c.end = k0 + n;
         c.left = ntiles - 1;
         return;
@@ -465,80 +532,60 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     };
     auto advance = [&](Cursor& c) {
       if (!c.table) return;
-      c.kp += kTile;
+      c.kp += C::kKeys;
       if (--c.left < 0) next_item(c);
     };
     uint32_t errbits = 0;
-    // this lane's keys of a tile: block ids (as read: looked at a tile later, by found; kNoKey: there is none) and places
-    // there
+    // this lane's key of a tile: block id (as read: looked at a tile later, by found; kNoKey: there is none) and place there
     constexpr int kNoKey = -0x7FFFFFFF;
     struct Ask {
-      int id[KL], at[KL];
+      int id, at;
     };
     auto ask = [&](const Cursor& c) -> Ask {
-      Ask a;
-#pragma unroll
-      for (int y = 0; y < KL; ++y) {
-        const int kp = c.kp + 8 * y;
-        a.id[y] = kNoKey;
-        a.at[y] = 0;
-        if (c.table && kp < c.end) {
-          const int col = static_cast<int>(__umulhi(2u * static_cast<uint32_t>(kp), p.bs_magic) >> p.bs_shift);      // kp / block_size
-          a.at[y] = kp - col * p.block_size;
-          a.id[y] = __ldg(c.table + col);
-        }
+      Ask a{kNoKey, 0};
+      if (c.table && lane < KW && c.kp < c.end) {
+        const int col = static_cast<int>(__umulhi(2u * static_cast<uint32_t>(c.kp), p.bs_magic) >> p.bs_shift);      // kp / block_size
+        a.at = c.kp - col * p.block_size;
+        a.id = __ldg(c.table + col);
       }
       return a;
     };
-    struct Records {
-      const uint8_t* r[KL];      // null: no such key or block
-    };
-    auto found = [&](const Ask& a) -> Records {
-      Records f;
-#pragma unroll
-      for (int y = 0; y < KL; ++y) {
-        const bool good = static_cast<uint32_t>(a.id[y]) < p.num_blocks;
-        if (!good && a.id[y] != kNoKey) errbits |= 2u;
-        f.r[y] = good ? p.kv + static_cast<uint64_t>(static_cast<uint32_t>(a.id[y])) * p.blk_stride +
-                            static_cast<uint64_t>(static_cast<uint32_t>(a.at[y])) * p.ent_stride
-                      : nullptr;
-      }
-      return f;
+    auto found = [&](const Ask& a) -> const uint8_t* {      // null: no such key or block
+      const bool good = static_cast<uint32_t>(a.id) < p.num_blocks;
+      if (!good && a.id != kNoKey) errbits |= 2u;
+      return good ? p.kv + static_cast<uint64_t>(static_cast<uint32_t>(a.id)) * p.blk_stride +
+                        static_cast<uint64_t>(static_cast<uint32_t>(a.at)) * p.ent_stride
+                  : nullptr;
     };
     // A tile's records are asked of memory into L2 one tile before its loads: the loads of a tile, issued together
     // when the registers of the tile before are free, then find them there.  (Loads issued register by
     // register between the conversions ran at a load's whole latency a step: the few scoreboards of a warp
     // are shared by old and new loads.)
-    const bool one_run = p.block_size % KW == 0 && p.ent_stride == kFp4Entry;      // the warp's 16 records lie together
-    auto prefetch = [&](const Records& f) {
-      if (one_run) {      // (a bulk prefetch a key takes the loaders longer than one for all)
-        if (lane == 0 && f.r[0]) bulk_prefetch_l2(f.r[0], KW * kFp4Entry);
+    auto prefetch = [&](const uint8_t* r, int at) {
+      if (!r) return;
+      if (p.ent_stride == kFp4Entry) {      // one for the records that lie together (one a key takes the loaders longer)
+        if (lane == 0 || at == 0) bulk_prefetch_l2(r, min(KW - lane, p.block_size - at) * kFp4Entry);
       } else {
-#pragma unroll
-        for (int y = 0; y < KL; ++y)
-          if (u == y && f.r[y]) bulk_prefetch_l2(f.r[y], kFp4Entry);
+        bulk_prefetch_l2(r, kFp4Entry);
       }
     };
-    // k_pe's pieces of this lane: the two halves of 64 bytes, in the other order in odd rows (whose columns the swizzle takes to
+    // k_pe's piece of this lane: the halves of 64 bytes in the other order in odd rows (whose columns the swizzle takes to
     // the even rows' then)
-    auto piece = [&](int i) { return u + 4 * (i ^ (key & 1)); };
-    uint4 code[KL][4], rope[KL][2], ex[KL];
-    bool live[KL];
-    auto load_tile = [&](const Records& f) {
+    const int piece = u + 4 * (kb ^ (key0 & 1));
+    uint4 code[4][2], rope[4], ex = make_uint4(0, 0, 0, 0);
+    bool live = false;      // lane k: key k is there
+    auto load_tile = [&](const uint8_t* own) {
+      live = own != nullptr;
+      ex = live ? __ldg(reinterpret_cast<const uint4*>(own + kFp4Exps)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int y = 0; y < KL; ++y) {
-        const uint8_t* r = f.r[y];
-        live[y] = r != nullptr;
+      for (int m = 0; m < 4; ++m) {
+        const uint8_t* r = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(own), 4 * m + key0));
         if (r) {
-          ex[y] = __ldg(reinterpret_cast<const uint4*>(r + kFp4Exps));
+          rope[m] = __ldg(reinterpret_cast<const uint4*>(r + kFp4Rope) + piece);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) rope[y][i] = __ldg(reinterpret_cast<const uint4*>(r + kFp4Rope) + piece(i));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) code[y][i] = __ldg(reinterpret_cast<const uint4*>(r) + 4 * i + u);
+          for (int h = 0; h < 2; ++h) code[m][h] = __ldg(reinterpret_cast<const uint4*>(r) + 8 * h + 4 * kb + u);
         } else {      // an absent key is all zeros
-          ex[y] = rope[y][0] = rope[y][1] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) code[y][i] = make_uint4(0, 0, 0, 0);
+          rope[m] = code[m][0] = code[m][1] = make_uint4(0, 0, 0, 0);
         }
       }
     };
@@ -553,68 +600,90 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     load_tile(found(ask(c)));
     advance(c);
     have1 = c.table != nullptr;
-    Records next = found(ask(c));
-    prefetch(next);
+    Ask asked = ask(c);
+    const uint8_t* next = found(asked);
+    prefetch(next, asked.at);
     advance(c);
     have2 = c.table != nullptr;
-    Ask asked = ask(c);
-    // offset of column 2 u of key r's row in a slot; column 2 u + 1 is 16 away (by exclusive or), key r + 8 1024 away
-    const uint32_t o0 = (KW * w + key) * 128 + (((2 * u) ^ key) << 4), o1 = o0 ^ 16u;
+    asked = ask(c);
+    // row 4 m + key0 of this warp's in a slot, and there column 2 u (column 2 u + 1 is 16 away, by exclusive or) and k_pe's
+    // piece; with m the swizzle's row changes by four
+    const int row0 = KW * w + key0;
+    const uint32_t o0 = row0 * 128 + (((2 * u) ^ (row0 & 7)) << 4), r0 = row0 * 128 + ((piece ^ (row0 & 7)) << 4);
     for (int gt = 0; ok && have; ++gt) {
       const int h = gt & 1;
       const uint32_t used = static_cast<uint32_t>((gt - 2) >> 1) & 1u;      // phase of tile gt - 2
-      uint8_t* tile = ring + h * NB * kSlotBytes;
+      // the slots of code tiles 2 i and 2 i + 1: free after the PV that read what lay there
+      auto free_slots = [&](int i) -> bool { return gt < 2 || warp_spin(&pv_part[h * C::kParts + i], used, abort_flag); };
+      uint8_t* tile = ring + 4 * h * C::kSlot;
       auto written = [&](int slot) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[h * NB + slot]);
+        if (lane == 0) mbar_arrive(&full[2 * h + slot]);
       };
       if (w == 0 && lane == 0) TL(4, 1);
-      // the records' largest exponents, at least 2^-60: what is smaller than 2^-74 reads as zero, and the sums over
-      // keys stay inside fp32.  e: the exponents of this lane's groups.
-      uint32_t K[KL], e[KL][4];
+      // the record's largest exponent, at least 2^-60: what is smaller than 2^-74 reads as zero, and the sums over
+      // keys stay inside fp32
+      uint32_t K;
+      {
+        const uint32_t word[4] = {ex.x, ex.y, ex.z, ex.w};
+        uint32_t top = 0u;      // of the even and the odd bytes
 #pragma unroll
-      for (int y = 0; y < KL; ++y) {
-        const uint32_t word[4] = {ex[y].x, ex[y].y, ex[y].z, ex[y].w};
-        K[y] = 67u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          e[y][i] = __byte_perm(word[i], 0u, 0x4440u | u);
-          K[y] = max(K[y], e[y][i]);
-        }
+        for (int i = 0; i < 4; ++i) top = __vmaxu2(top, __vmaxu2(word[i] & 0x00FF00FFu, (word[i] >> 8) & 0x00FF00FFu));
+        K = max(max(top & 0xFFFFu, top >> 16), 67u);
+        const uint32_t K4 = K * 0x01010101u;      // (no byte of K4 - word borrows)
+        if (lane < KW) below[lane] = make_uint4(K4 - ex.x, K4 - ex.y, K4 - ex.z, K4 - ex.w);
+        __syncwarp();
       }
+      // k_pe and the scale.  Of two slots of k_pe this tile's is free after QK of tile gt - 2, and so after its PV; the only one
+      // after QK of tile gt - 1.  The scale of tile gt - 2 was read before its PV.
+      auto put_rope = [&]() {
+        uint8_t* at = smem + C::kRope + (gt % C::kRopes) * C::kSlot;
 #pragma unroll
-      for (int o = 1; o <= 2; ++o)
+        for (int m = 0; m < 4; ++m)
+          if (4 * m + key0 < KW) *reinterpret_cast<uint4*>(at + 512 * m + (r0 ^ ((m & 1) << 6))) = rope[m];
+        if (lane < KW)      // exponent 255: a NaN in the record; -1: no such key
+          scl[h * kTile + KW * w + lane] = !live ? -1.f : K == 255u ? CUDART_NAN_F : __uint_as_float((K - 6u) << 23);
+      };
+      const uint8_t* low = reinterpret_cast<const uint8_t*>(below + key0) + 4 * kb + u;      // of key 4 m + key0 64 m on
+      auto convert = [&](int i, int m, uint4 (&v)[2]) {
+        const uint2 l2 = lut[min(static_cast<uint32_t>(low[64 * m + 8 * i]), 15u)];
+        const uint4 x = code[m][i];
+        const uint2 a0 = fp4x8_to_e4m3(l2, x.x, p.two16, p.two31), a1 = fp4x8_to_e4m3(l2, x.y, p.two16, p.two31);
+        const uint2 a2 = fp4x8_to_e4m3(l2, x.z, p.two16, p.two31), a3 = fp4x8_to_e4m3(l2, x.w, p.two16, p.two31);
+        v[0] = make_uint4(a0.x, a0.y, a1.x, a1.y);
+        v[1] = make_uint4(a2.x, a2.y, a3.x, a3.y);
+      };
+      auto put = [&](int i) {
 #pragma unroll
-        for (int y = 0; y < KL; ++y) K[y] = max(K[y], __shfl_xor_sync(0xFFFFFFFFu, K[y], o));
-      // k_pe and the scale: free after QK of tile gt - 2 and its softmax, and so after its PV
-      if (gt >= 2 && !warp_wait(&pv_part[h * C::kParts], used, abort_flag)) break;
+        for (int m = 0; m < 4; ++m) {
+          uint4 v[2];
+          convert(i, m, v);
+          if (4 * m + key0 >= KW) continue;
+          uint8_t* at = tile + (2 * i + kb) * C::kSlot + 512 * m;
+          const uint32_t o = o0 ^ ((m & 1) << 6);
+          *reinterpret_cast<uint4*>(at + o) = v[0];
+          *reinterpret_cast<uint4*>(at + (o ^ 16u)) = v[1];
+        }
+        written(i);
+      };
+      if (!free_slots(0)) break;
       if (w == 0 && lane == 0) TL(4, 2);
-#pragma unroll
-      for (int y = 0; y < KL; ++y) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<uint4*>(tile + 4 * kSlotBytes + 1024 * y + (KW * w + key) * 128 + ((piece(i) ^ key) << 4)) = rope[y][i];
-        if (u == y)      // exponent 255: a NaN in the record; -1: no such key
-          scl[h * kTile + KW * w + 8 * y + key] = !live[y] ? -1.f : K[y] == 255u ? CUDART_NAN_F : __uint_as_float((K[y] - 6u) << 23);
+      if constexpr (C::kRopes == 2) put_rope();
+      put(0);
+      if (w == 0 && lane == 0) TL(4, 4);
+      ok = free_slots(1);
+      if constexpr (C::kRopes == 1) {
+        ok = ok && (gt < 1 || warp_spin(&s_full[h ^ 1], static_cast<uint32_t>((gt - 1) >> 1) & 1u, abort_flag));
+        if (ok) put_rope();
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (C::kParts > 1 && i == 2 && gt >= 2) ok = ok && warp_wait(&pv_part[h * C::kParts + 1], used, abort_flag);
-#pragma unroll
-        for (int y = 0; y < KL; ++y) {
-          const uint2 l2 = lut[min(K[y] - e[y][i], 15u)];
-          const uint2 a0 = fp4x8_to_e4m3(l2, code[y][i].x, p.two16, p.two31), a1 = fp4x8_to_e4m3(l2, code[y][i].y, p.two16, p.two31);
-          const uint2 a2 = fp4x8_to_e4m3(l2, code[y][i].z, p.two16, p.two31), a3 = fp4x8_to_e4m3(l2, code[y][i].w, p.two16, p.two31);
-          *reinterpret_cast<uint4*>(tile + i * kSlotBytes + 1024 * y + o0) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-          *reinterpret_cast<uint4*>(tile + i * kSlotBytes + 1024 * y + o1) = make_uint4(a2.x, a2.y, a3.x, a3.y);
-        }
-        if (i & 1) written(i);
-      }
+      if (!ok) break;
+      if (w == 0 && lane == 0) TL(4, 5);
+      put(1);
       if (w == 0 && lane == 0) TL(4, 3);
       // (the block ids are looked at before new loads are on their way, whose scoreboards they may share)
-      const Records after = found(asked);
-      prefetch(after);
+      const uint8_t* after = found(asked);
+      prefetch(after, asked.at);
       load_tile(next);
       advance(c);
       asked = ask(c);
@@ -626,6 +695,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     errbits = __reduce_or_sync(0xFFFFFFFFu, errbits);
     if (lane == 0 && errbits) set_device_error(p.err, errbits);
   } else {
+    if constexpr (C::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     // ------------------------------------------------------------------ softmax, query, epilogue
     constexpr int NT = 32 * C::kSW, NC = C::NC;
     const int quad = warp & 3;
@@ -633,8 +703,8 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     const int stid = tid - 32 * C::kFirstSm;
     const int c0 = (stid >> 7) * NC;            // first column of this thread
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    // w = 2^(s' - m + kPExp) <= 2^(kTau + kPExp) = 2^8.  mref holds m - kPExp.
-    constexpr float kTau = 7.f, kPExp = 1.f;
+    // w = 2^(s' - m + kPExp) <= 2^(kTau + kPExp).  mref holds m - kPExp.
+    constexpr float kTau = C::kTau, kPExp = C::kPExp;
     // the query of an item: thread (c = stid / 8, part = stid % 8) takes elements 64 part .. + 63 of a column
     auto prep_query = [&](const WorkItem& qi) {
 #pragma unroll 1
@@ -675,8 +745,8 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
             const uint32_t h01 = e4m3x2_sat(x0, x1), h23 = e4m3x2_sat(x2, x3);
             const float2 f01 = e4m3x2_to_float2(h01), f23 = e4m3x2_to_float2(h23);
             hw[y] = h01 | (h23 << 16);
-            lw[y] = e4m3x2_sat(16.f * (x0 - f01.x), 16.f * (x1 - f01.y)) |
-                    (e4m3x2_sat(16.f * (x2 - f23.x), 16.f * (x3 - f23.y)) << 16);
+            lw[y] = e4m3x2_sat(C::kLo * (x0 - f01.x), C::kLo * (x1 - f01.y)) |
+                    (e4m3x2_sat(C::kLo * (x2 - f23.x), C::kLo * (x3 - f23.y)) << 16);
           }
           const int chunk = (part & 1) * 4 + i;
           *reinterpret_cast<uint4*>(base + sw128(c, chunk)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
@@ -709,7 +779,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       // s' of this thread's key for its columns, masked; ks: the key's 2^(K - 6)
       auto load_s = [&](float (&s)[NC], int gt, int t, float ks) {
         const uint32_t ts = tl + (gt & 1) * C::kS + c0;
-        const int kpos = it.k0 + t * kTile + row;
+        const int kpos = it.k0 + t * C::kKeys + row;
         const bool rv = kpos < it.k0 + it.n && !(ks < 0.f);
         // (the rows of absent keys are zeros: 0 * 0 - inf)
         const float kexp = rv ? static_cast<float>(static_cast<int>(__float_as_uint(ks) >> 23) - 127) : -CUDART_INF_F;
@@ -718,18 +788,23 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         for (int c1 = 0; c1 < NC; c1 += 16) {
           float a[16], r[16];
           tmem_ld16(ts + c1, a);
-          tmem_ld16(ts + NQ + c1, r);
-          tmem_ld_wait();
+          if constexpr (!C::kWide) {
+            tmem_ld16(ts + NQ + c1, r);
+            tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 16; ++c) a[c] = fmaf(r[c], 0.0625f, a[c]);
-          tmem_ld16(ts + 2 * NQ + c1, r);
+            for (int c = 0; c < 16; ++c) a[c] = fmaf(r[c], 0.0625f, a[c]);
+          }
+          tmem_ld16(ts + C::kN + c1, r);
           tmem_ld_wait();
 #pragma unroll
           for (int c = 0; c < 16; c += 4) {
             const float4 f4 = *reinterpret_cast<const float4*>(colf + c0 + c1 + c);
             const float ff[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-            for (int y = 0; y < 4; ++y) s[c1 + c + y] = fmaf(a[c + y], ff[y] * km, fmaf(r[c + y], p.sig2, kexp));
+            for (int y = 0; y < 4; ++y) {
+              s[c1 + c + y] = fmaf(a[c + y], ff[y] * km, fmaf(r[c + y], p.sig2, kexp));
+              if (C::kKeys < kTile && !rv) s[c1 + c + y] = -CUDART_INF_F;      // (rows past the tile are anything)
+            }
           }
         }
         // spec-verify: query token qi sees keys up to L - q_len + qi
@@ -745,11 +820,11 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         // (the tile's scales, written with its first slots, are there long before S)
         w = true;
         if (warp == C::kFirstSm)
-          w = warp_wait(&full[(gt & 1) * NB + 1], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag) &&
-              warp_wait(&s_full[gt & 1], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag);
+          w = warp_wait(&full[2 * (gt & 1) + (C::kRopes == 1 ? 1 : 0)], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag) &&
+              warp_spin(&s_full[gt & 1], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag);
         w = named_bar_and(1, NT, w);
         tc_fence_after();
-        const float ks = scl[(gt & 1) * kTile + row];
+        const float ks = row < C::kKeys ? scl[(gt & 1) * kTile + row] : -1.f;
         if (stid == 0) TL(3, 1);
         float d[NC];              // s', then s' - m + kPExp, then the weights
         load_s(d, gt, t, ks);
@@ -803,12 +878,12 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
           for (int c = 0; c < NC; ++c) l_part[c] *= alph[c0 + c];
           // O of the previous tiles moves to the new reference once PV of the last tile is done
           if (t > 0) {
-            w = warp_wait(&pv_part[((gt - 1) & 1) * C::kParts + C::kParts - 1], static_cast<uint32_t>((gt - 1) >> 1) & 1u, abort_flag);
+            w = warp_spin(&pv_part[((gt - 1) & 1) * C::kParts + C::kParts - 1], static_cast<uint32_t>((gt - 1) >> 1) & 1u, abort_flag);
             tc_fence_after();
             pv_waited = true;
             if (w && resc) {
 #pragma unroll 1
-              for (int x = 0; x < 8 * NQ; x += NQ) {      // O_j: this thread's hi columns, then its lo columns
+              for (int x = 0; x < 4 * C::kN; x += NQ) {      // O_j: this thread's hi columns, then its lo columns
 #pragma unroll 1
                 for (int c1 = c0; c1 < c0 + NC; c1 += 16) {
                   float o[16];
@@ -843,14 +918,15 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
             const __half2 a = __floats2half2_rn(d[4 * y + 2 * z], d[4 * y + 2 * z + 1]);
             hi[z] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(a), __NV_SATFINITE, __NV_E4M3);
             const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi[z]), __NV_E4M3);
-            const __half2 r = __hmul2(__hsub2(a, __half2(b)), __float2half2_rn(16.f));
+            __half2 r = __hsub2(a, __half2(b));
+            if constexpr (!C::kWide) r = __hmul2(r, __float2half2_rn(C::kLo));
             lo[z] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
           }
           hw[y] = hi[0] | (hi[1] << 16);
           lw[y] = lo[0] | (lo[1] << 16);
         }
         if (t > 0 && !pv_waited) {
-          w = warp_wait(&pv_part[((gt - 1) & 1) * C::kParts + C::kParts - 1], static_cast<uint32_t>((gt - 1) >> 1) & 1u, abort_flag);   // P is free
+          w = warp_spin(&pv_part[((gt - 1) & 1) * C::kParts + C::kParts - 1], static_cast<uint32_t>((gt - 1) >> 1) & 1u, abort_flag);   // P is free
           tc_fence_after();
         }
         if (stid == 0) TL(3, 4);
@@ -882,7 +958,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       // ---- epilogue: O / l and the LSE of every column of the item
       if (stid == 0) TL(3, 6);
       {
-        w = warp_wait(&pv_part[((g + it.ntiles - 1) & 1) * C::kParts + C::kParts - 1], static_cast<uint32_t>((g + it.ntiles - 1) >> 1) & 1u, abort_flag);
+        w = warp_spin(&pv_part[((g + it.ntiles - 1) & 1) * C::kParts + C::kParts - 1], static_cast<uint32_t>((g + it.ntiles - 1) >> 1) & 1u, abort_flag);
         tc_fence_after();
       }
       g += it.ntiles;
@@ -910,12 +986,16 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       for (int jc = 0; jc < 4 * (NC / 16); ++jc) {
         const int jj = jc / (NC / 16), c1 = 16 * (jc % (NC / 16));
         if (c1 >= ncol) continue;
-        float o[16], lo[16];
-        tmem_ld16(tl + C::kTmemO + 2 * NQ * jj + c0 + c1, o);
-        tmem_ld16(tl + C::kTmemO + 2 * NQ * jj + NQ + c0 + c1, lo);
-        tmem_ld_wait();
+        float o[16];
+        tmem_ld16(tl + C::kTmemO + C::kN * jj + c0 + c1, o);
+        if constexpr (!C::kWide) {
+          float lo[16];
+          tmem_ld16(tl + C::kTmemO + C::kN * jj + NQ + c0 + c1, lo);
+          tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) o[c] = fmaf(lo[c], 0.0625f, o[c]);
+          for (int c = 0; c < 16; ++c) o[c] = fmaf(lo[c], 0.0625f, o[c]);
+        }
+        tmem_ld_wait();
         const int d = 128 * jj + row;
         if (final_out) {
           int h = (cgb + c1) % p.H;

@@ -236,6 +236,42 @@ def test_decode_long(m):
     run_decode(m, np.random.default_rng(11), [20011], H=16, scale=0.3)
 
 
+@pytest.mark.parametrize("q_len,H,scale", [(1, 48, 0.3), (4, 16, SCALE), (1, 128, 0.1)])
+def test_decode_long_of_many_columns(m, q_len, H, scale):
+    run_decode(m, np.random.default_rng(H), [9011, 30, 2300], q_len=q_len, H=H, scale=scale)
+
+
+@pytest.mark.parametrize("lens", [[111, 112, 113, 1], [224, 225, 0, 223, 336], [14, 15, 28, 98, 99]])
+@pytest.mark.parametrize("bs", [3, 16, 64])
+def test_decode_ends_of_short_tiles(m, lens, bs):
+    """More than 32 columns take tiles of 112 keys, 14 a loader warp."""
+    run_decode(m, np.random.default_rng(bs), lens, H=50, bs=bs)
+
+
+@pytest.mark.parametrize("H", [16, 32, 40, 100])
+def test_nan_keys_of_other_requests(m, H):
+    """Several requests a CTA, every third with nothing but NaN keys: the others' results keep their bits."""
+    rng = np.random.default_rng(H)
+    bs, B = 64, 900
+    lens = rng.integers(1, 300, B).astype(np.int32)
+    nb = 24
+    cache = make_cache(rng, 2 * nb, bs)
+    table = rng.integers(0, nb, (B, 5)).astype(np.int32)
+    table[::3] += nb                # of their own
+    bad = cache.copy()
+    bad[nb:, :, 256:] = 255
+    q = ref.bf16(rng.standard_normal((B, H, 576))).cuda()
+    run = lambda c: m.paged_decode(q, torch.from_numpy(c).cuda(), torch.from_numpy(table).cuda(), torch.from_numpy(lens).cuda(), fmt="mxfp4",
+                                   max_context=300, softmax_scale=SCALE, return_lse=True)
+    (out, lse), (o2, l2) = run(cache), run(bad)
+    keep = torch.arange(B, device="cuda") % 3 != 0
+    assert torch.equal(o2[keep], out[keep]) and torch.equal(l2[keep], lse[keep])
+    assert bool(torch.isnan(o2[~keep]).all()) and not bool(torch.isnan(out).any())
+    some = [1, 2, 4, 449, 898]
+    want = ref.decode(q[some].double().cpu().numpy(), cache, table[some], [int(x) for x in lens[some]], bs, 1, SCALE)
+    check(out[some], lse[some], want)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.07, 1e-6, 4.0])
 def test_decode_scales(m, scale):
     run_decode(m, np.random.default_rng(12), [333, 128], scale=scale)

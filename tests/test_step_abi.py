@@ -141,7 +141,7 @@ def test_the_decode_s_workspace(m, L):
         assert n(fmt, 64, 4, 16) == L.mla_paged_decode_workspace_size(64, 4, 16, 131072, 152) > 0
     # two partials of 512 values and a log-sum-exp a run and column; runs x groups of columns fill the SMs
     up = lambda x: -(-x // 256) * 256
-    for q, H, runs in ((1, 16, 152), (1, 17, 152), (1, 32, 152), (1, 33, 76), (1, 128, 38), (4, 16, 76), (7, 128, 5), (64, 128, 1)):
+    for q, H, runs in ((1, 16, 152), (1, 17, 152), (1, 32, 152), (1, 33, 152), (4, 16, 152), (1, 65, 76), (1, 128, 76), (7, 128, 10), (64, 128, 1)):
         cols = q * H
         assert n(MXFP4, 9, q, H) == up(2 * runs * cols * 2048) + up(2 * runs * cols * 4) + up((2 * runs + 1) * 8)
     assert n(MXFP4, 1, 1, 16) == n(MXFP4, 500, 1, 16) == n(MXFP4, 1, 1, 16, 64)     # neither requests nor lengths
