@@ -17,7 +17,7 @@
 //   * Two tiles in shared memory, each four slots of E4M3 codes of 128 values and bf16 k_pe, K-major with 128-byte swizzle, read by
 //     both products.  Up to 32 columns take tiles of 128 keys.  More take 64 at once: what bounds them is a tile's conversion
 //     and the products' reads of it, whose cost hardly depends on the columns (4 x 16 rows over 16k to 128k keys, 64 requests:
-//     two groups of 32 1350 us, one of 64 1010).  64 columns leave room for two tiles of 112 keys (14 a loader warp), of which
+//     two groups of 32 1350 us, one of 64 1030).  64 columns leave room for two tiles of 112 keys (14 a loader warp), of which
 //     the products' last 16 rows are taken from what lies behind; of 128 keys only seven slots of eight fit, so that a tile
 //     waited for the PV of the one before (1071 us).
 //   * Eight loader warps take 16 (14) keys of a tile each: 16-byte loads straight from the pages one tile ahead in
@@ -33,8 +33,9 @@
 //     The reference m moves only when a logit passes it by kTau.
 //   * hi and lo terms are stacked along N, with accumulators of their own that the epilogue adds; at 64 columns the tensor memory has
 //     no room for those, and hi and the plain rest lo = x - hi go to the same accumulator, one after the other along K.  A
-//     rest is then kept to 2^-10 of the scaled range: a query's value to 2^-18 of the column's largest, a weight to 2^-13 of the
-//     reference (which lies higher in E4M3's range for it, and kTau lower).
+//     rest is then kept to 2^-10 of the scaled range: a query's value to 2^-18 of the column's largest, a weight to 2^-14 of the
+//     reference, which lies higher in E4M3's range for it, and kTau lower: a reference that moves costs 2.8 us (kTau 5 and 2^-13: 2 %
+//     less time, error of the output 0.0020 against 0.0018; kTau 3: 2 % more, 0.0017).
 //   * Roles hand over through mbarriers, each waited with a time limit.  Waits between the products and what feeds them are
 //     polled: a suspended thread (try_wait) was woken 0.5 to 1 us late, four times a tile (1390 -> 1095 us; of 16 columns 43 ->
 //     39).  The scheduler and the wait for a work item are not in a hurry.
@@ -123,7 +124,7 @@ struct Fp4Cfg {
   static_assert(kTmemO + 4 * kN <= kTmemCols, "TMEM budget");
   // The lo terms of E4M3 pairs: 16 times the rest where they have columns of their own, the rest itself where they add to
   // the hi terms' (rests below 2^-10 are lost).  The weights are 2^(kPExp + kTau) at most (2^8.75 of 448).
-  static constexpr float kLo = kWide ? 1.f : 16.f, kTau = kWide ? 5.f : 7.f, kPExp = kWide ? 3.75f : 1.f;
+  static constexpr float kLo = kWide ? 1.f : 16.f, kTau = kWide ? 4.f : 7.f, kPExp = kWide ? 4.75f : 1.f;
 };
 
 // The E4M3 bytes of eight codes: the magnitudes picked by permutes from the eight bytes of lut, with the codes as
