@@ -334,41 +334,48 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       const int src = who ? __ffs(who) - 1 : 0;
       b = __shfl_sync(0xFFFFFFFFu, b, src);
       t0 = __shfl_sync(0xFFFFFFFFu, t0, src);
-      if (lane == 0) {
-        TL(0, 3);
-        if (blockIdx.x == 0) p.span[2 * p.W] = run;
-        int64_t t = lo, on_t = 0, on_b = -1;
-        for (int nitem = 0;; ++nitem) {
-          WorkItem it{};
-          it.b = -1;
-          if (t < hi) {
-            const int64_t n = tiles_of(b);
-            it.b = b;
-            it.g = g;
-            it.L = p.seq_lens[b];
-            it.ntiles = static_cast<int>(min(hi, t0 + n) - t);
-            it.k0 = static_cast<int>((t - t0) * C::kKeys);
-            it.n = static_cast<int>(min(static_cast<int64_t>(it.L) - it.k0, static_cast<int64_t>(it.ntiles) * C::kKeys));
-            it.pad = it.ntiles == n;                      // the whole request: final
-            it.s = 2 * w + (t == t0 ? 1 : 0);
-            if (t == t0 && it.ntiles < n) on_t = t0, on_b = b;
-            t += it.ntiles;
-            if (t == t0 + n) {
-              t0 = t;
-              do ++b;
-              while (b < p.B && p.seq_lens[b] <= 0);
+      if (lane == 0) TL(0, 3);
+      if (lane == 0 && blockIdx.x == 0) p.span[2 * p.W] = run;
+      int64_t t = lo, on_t = 0;
+      int on_b = -1;
+      for (int nitem = 0;; ++nitem) {
+        WorkItem it{};
+        it.b = -1;
+        if (t < hi) {
+          const int64_t n = tiles_of(b);
+          it.b = b;
+          it.g = g;
+          it.L = p.seq_lens[b];
+          it.ntiles = static_cast<int>(min(hi, t0 + n) - t);
+          it.k0 = static_cast<int>((t - t0) * C::kKeys);
+          it.n = static_cast<int>(min(static_cast<int64_t>(it.L) - it.k0, static_cast<int64_t>(it.ntiles) * C::kKeys));
+          it.pad = it.ntiles == n;                      // the whole request: final
+          it.s = 2 * w + (t == t0 ? 1 : 0);
+          if (t == t0 && it.ntiles < n) on_t = t0, on_b = b;
+          t += it.ntiles;
+          if (t < hi) {      // the next request with keys, 32 at a time (a padded batch has many without)
+            t0 = t;
+            uint32_t some = 0;
+            for (++b; b < p.B; b += 32) {
+              some = __ballot_sync(0xFFFFFFFFu, b + lane < p.B && p.seq_lens[b + lane] > 0);
+              if (some) break;
             }
+            if (some) b += __ffs(some) - 1;
           }
-          const int k = nitem % kItemDepth;
-          if (nitem >= kItemDepth && !slow_wait(&item_empty[k], static_cast<uint32_t>((nitem / kItemDepth) - 1) & 1u, abort_flag)) break;
+        }
+        const int k = nitem % kItemDepth;
+        bool w_ok = true;
+        if (lane == 0 && nitem >= kItemDepth) w_ok = slow_wait(&item_empty[k], static_cast<uint32_t>((nitem / kItemDepth) - 1) & 1u, abort_flag);
+        if (!__all_sync(0xFFFFFFFFu, w_ok)) break;
+        if (lane == 0) {
           items[k] = it;
           mbar_arrive(&item_full[k]);
-          if (it.b < 0) break;
         }
-        if (g == 0) {
-          p.span[2 * w] = on_t;
-          p.span[2 * w + 1] = on_b;
-        }
+        if (it.b < 0) break;
+      }
+      if (lane == 0 && g == 0) {
+        p.span[2 * w] = on_t;
+        p.span[2 * w + 1] = on_b;
       }
       __syncwarp();
       // requests without keys: zeros, every W-th one

@@ -248,6 +248,17 @@ def test_decode_ends_of_short_tiles(m, lens, bs):
     run_decode(m, np.random.default_rng(bs), lens, H=50, bs=bs)
 
 
+@pytest.mark.parametrize("H", [16, 64])
+def test_padded_batches(m, H):
+    """Many requests without keys before, between and behind the others."""
+    rng = np.random.default_rng(H)
+    for where in ([0], [599], [0, 33, 64, 599], [31, 32, 300, 301, 450]):
+        lens = [0] * 600
+        for b in where:
+            lens[b] = int(rng.integers(1, 900))
+        run_decode(m, rng, lens, H=H)
+
+
 @pytest.mark.parametrize("H", [16, 32, 40, 100])
 def test_nan_keys_of_other_requests(m, H):
     """Several requests a CTA, every third with nothing but NaN keys: the others' results keep their bits."""
