@@ -632,12 +632,13 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t R = static_cast<int32_t>(cs.size[1]);
   k = ko = Tensor{};
   if (a[3] == Py_None) {
-    if (a[9] != Py_None) return not_plain();
+    if (a[9] != Py_None || k_at >= 0) return not_plain();
   } else if (!read(a[3], dev, 3, &k, type) || k.size[0] != T || k.size[1] > INT32_MAX || k.size[2] > 1024 ||
              !output(a[9], dev, 3, k.size, type, nullptr, device.p, &ko, &k_out)) {
     return not_plain();
   }
   const int32_t D = static_cast<int32_t>(q.size[2]), Dk = static_cast<int32_t>(k.size[2]);
+  if (D < R || q_at > D - R || (k_out.p && (Dk < R || k_at > Dk - R))) return not_plain();
   cudaStream_t stream;
   if (!stream_of(dev, &stream)) return not_plain();
   int rc;

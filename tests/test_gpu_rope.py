@@ -221,3 +221,14 @@ def test_both_marshallings_give_the_same(m, monkeypatch):
     monkeypatch.setattr(m, "_step", m._DeclinedStep)
     b = (*m.rope(q, pos, tab, k, **kw), m.rope(q, pos, tab, **kw))
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_arguments_of_keys_need_keys(m):
+    x, pos, tab = torch.randn((2, 3, 64), device="cuda"), torch.arange(2, device="cuda"), table(9, 64).cuda()
+    for kw in (dict(k_at=0), dict(k_out=torch.empty_like(x))):
+        with pytest.raises(ValueError, match="need k"):
+            m.rope(x, pos, tab, **kw)
+    with pytest.raises(ValueError, match="fit"):
+        m.rope(x, pos, tab, q_at=1)
+    with pytest.raises(m.MLAError):        # in place one, not the other
+        m.rope(x, pos, tab, x.clone(), q_out=x)
