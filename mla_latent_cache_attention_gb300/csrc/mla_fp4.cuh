@@ -170,14 +170,6 @@ __device__ __forceinline__ void mma_commit_if(bool on, uint64_t* bar) {
       : "memory");
 }
 
-// A group of warps waits through its first one, the others at a hardware barrier: a warp that polls takes issue slots from
-// the others (a try_wait comes back after some 70 ns, whatever its time limit; polled by every softmax and loader warp, the
-// waits were 4500 of 10000 instructions a tile).  Every thread of the group leaves with the same answer.
-__device__ __forceinline__ bool group_wait(bool first, uint32_t id, uint32_t threads, uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  bool w = true;
-  if (first) w = warp_wait(bar, parity, abort_flag);
-  return named_bar_and(id, threads, w);
-}
 // A wait that is in a hurry: an issuer's, polled.
 __device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   uint64_t t0 = 0;
@@ -199,6 +191,13 @@ __device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t parity, volati
   bool w = true;
   if ((threadIdx.x & 31) == 0) w = spin_wait(bar, parity, abort_flag);
   return __shfl_sync(0xFFFFFFFFu, w ? 1 : 0, 0) != 0;
+}
+// A group of warps waits through its first one, the others at a hardware barrier: a warp that polls takes issue slots from
+// the others (polled by every softmax and loader warp, the waits were 4500 of 10000 instructions a tile).  Every thread of the group leaves with the same answer.
+__device__ __forceinline__ bool group_wait(bool first, uint32_t id, uint32_t threads, uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  bool w = true;
+  if (first) w = warp_spin(bar, parity, abort_flag);
+  return named_bar_and(id, threads, w);
 }
 // A wait that is in no hurry.
 __device__ __forceinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -403,17 +402,17 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         int nit = 0, nq = 0, g = 0;
         while (ok) {
           const int k = nit % kItemDepth;
-          if (!warp_wait(&item_full[k], (nit / kItemDepth) & 1, abort_flag)) break;
+          if (!warp_spin(&item_full[k], (nit / kItemDepth) & 1, abort_flag)) break;
           const WorkItem it = items[k];
           __syncwarp();
           if (one) mbar_arrive(&item_empty[k]);
           ++nit;
           if (it.b < 0) break;
-          if (!warp_wait(q_full, nq & 1, abort_flag)) break;
+          if (!warp_spin(q_full, nq & 1, abort_flag)) break;
           ++nq;
           for (int t = 0; t < it.ntiles && ok; ++t) {
             const int gt = g + t, h = gt & 1;
-            if (gt >= 2 && !warp_wait(&s_free[h], static_cast<uint32_t>((gt - 2) >> 1) & 1u, abort_flag)) ok = false;
+            if (gt >= 2 && !warp_spin(&s_free[h], static_cast<uint32_t>((gt - 2) >> 1) & 1u, abort_flag)) ok = false;
             if (!ok) break;
             if (lane == 0) TL(1, 1);
             const uint32_t dS = tmem + h * C::kS;
@@ -828,15 +827,13 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         // (the tile's scales, written with its first slots, are there long before S)
         w = true;
         if (warp == C::kFirstSm)
-          w = warp_wait(&full[2 * (gt & 1) + (C::kRopes == 1 ? 1 : 0)], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag) &&
+          w = warp_spin(&full[2 * (gt & 1) + (C::kRopes == 1 ? 1 : 0)], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag) &&
               warp_spin(&s_full[gt & 1], static_cast<uint32_t>(gt >> 1) & 1u, abort_flag);
         w = named_bar_and(1, NT, w);
         tc_fence_after();
         const float ks = row < C::kKeys ? scl[(gt & 1) * kTile + row] : -1.f;
         if (stid == 0) TL(3, 1);
         float d[NC];              // s', then s' - m + kPExp, then the weights
-        load_s(d, gt, t, ks);
-        if (stid == 0) TL(3, 2);
         auto against = [&]() {
 #pragma unroll
           for (int c = 0; c < NC; c += 4) {
@@ -847,15 +844,21 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
             d[c + 3] -= m4.w;
           }
         };
-        against();
-        float most = d[0];
+        // (an item begins without a reference; more columns have no registers for the shorter way: 1030 -> 1070 us)
+        bool rare = NQ == 16 && t == 0;
+        if (!rare) {
+          load_s(d, gt, t, ks);
+          if (stid == 0) TL(3, 2);
+          against();
+          float most = d[0];
 #pragma unroll
-        for (int c = 1; c < NC; ++c) most = fmaxf(most, d[c]);
-        // (the weights for the reference as it is, while the other warps come to the barrier)
+          for (int c = 1; c < NC; ++c) most = fmaxf(most, d[c]);
+          // (the weights for the reference as it is, while the other warps come to the barrier)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) d[c] = ex2(d[c]);
-        tc_fence_before();
-        const bool rare = named_bar_or(1, NT, most > kTau + kPExp || !w || failed);
+          for (int c = 0; c < NC; ++c) d[c] = ex2(d[c]);
+          tc_fence_before();
+          rare = named_bar_or(1, NT, most > kTau + kPExp || !w || failed);
+        }
         bool pv_waited = false;
         // every thread has read S[gt & 1]; a tile that moves the reference reads it again below
         if (stid == 0 && !rare) mbar_arrive(&s_free[gt & 1]);
