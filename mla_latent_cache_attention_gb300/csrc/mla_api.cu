@@ -751,7 +751,7 @@ size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
 size_t mla::fp4_workspace_bytes(int q_len, int H, int sms) {
   const size_t parts = static_cast<size_t>(2 * fp4_plan(q_len, H, sms).W) * q_len * H;
-  return round256(parts * kLora * sizeof(float)) + round256(parts * sizeof(float)) + round256((2 * static_cast<size_t>(fp4_plan(q_len, H, sms).W) + 1) * sizeof(int64_t));
+  return round256(parts * kLora * sizeof(float)) + round256(parts * sizeof(float)) + round256(static_cast<size_t>(fp4_plan(q_len, H, sms).W) * sizeof(int2));
 }
 
 int mla::run_fp4_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache, int64_t num_blocks,
@@ -788,9 +788,14 @@ int mla::run_fp4_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* k
   p.seq_lens = seq_lens;
   p.num_blocks = static_cast<uint32_t>(num_blocks < (int64_t(1) << 31) ? num_blocks : int64_t(1) << 31);
   p.block_size = block_size;
-  while ((int64_t(1) << p.bs_shift) < block_size) ++p.bs_shift;
-  p.bs_magic = static_cast<uint32_t>(((uint64_t(1) << (31 + p.bs_shift)) + block_size - 1) / block_size);
   p.W = static_cast<int>(plan.W);
+  auto by_product = [](uint32_t d, int* shift, uint32_t* magic) {
+    *shift = 0;
+    while ((int64_t(1) << *shift) < d) ++*shift;
+    *magic = static_cast<uint32_t>(((uint64_t(1) << (31 + *shift)) + d - 1) / d);
+  };
+  by_product(block_size, &p.bs_shift, &p.bs_magic);
+  by_product(p.W, &p.w_shift, &p.w_magic);
   p.sig2 = softmax_scale * 1.4426950408889634f;
   p.out = static_cast<uint8_t*>(out);
   p.o_s0b = o_s0 * 2;
@@ -798,7 +803,7 @@ int mla::run_fp4_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* k
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_lse = reinterpret_cast<float*>(ws + round256(parts * kLora * sizeof(float)));
-  p.span = reinterpret_cast<int64_t*>(ws + round256(parts * kLora * sizeof(float)) + round256(parts * sizeof(float)));
+  p.span = reinterpret_cast<int2*>(ws + round256(parts * kLora * sizeof(float)) + round256(parts * sizeof(float)));
   p.err = d->err;
   p.wait_us = g_stall_next_us;
   p.stall = g_stall_next_us > 0 ? 1 : 0;

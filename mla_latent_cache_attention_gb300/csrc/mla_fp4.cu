@@ -12,19 +12,26 @@ constexpr int kJoin = 16;      // loads of a thread on their way at once
 __global__ void __launch_bounds__(256) mla_fp4_merge_kernel(const __grid_constant__ Fp4Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, w0 = blockIdx.y, tid = threadIdx.x;
-  const int64_t b = p.span[2 * w0 + 1];
-  if (b < 0) return;
-  const int64_t run = p.span[2 * p.W], t1 = p.span[2 * w0] + (static_cast<int64_t>(p.seq_lens[b]) + p.keys - 1) / p.keys;
-  const int n = static_cast<int>((t1 - 1) / run) - w0 + 1;
+  const int2 span = p.span[w0];
+  const int n = span.y;
+  if (span.x < 0) return;
+  const int64_t b = span.x;
   // part i is slot 2 (w0 + i), the first one 2 w0 + 1
   auto at = [&](int i) -> int64_t { return (2 * static_cast<int64_t>(w0 + i) + (i == 0 ? 1 : 0)) * p.cols + c; };
   __shared__ float wt[256];
   __shared__ float red[8];
   const int lane = tid & 31, warp = tid >> 5;
+  float2 o[kJoin];
+  auto load = [&](int i, int k) {
+#pragma unroll
+    for (int y = 0; y < kJoin; ++y)
+      o[y] = i + y < k ? reinterpret_cast<const float2*>(p.part_o + at(i + y) * kLora)[tid] : make_float2(0.f, 0.f);
+  };
+  load(0, n);      // on their way before the weights are known
   float m = -CUDART_INF_F;
   for (int i = tid; i < n; i += 256) m = fmaxf(m, p.part_lse[at(i)]);
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  for (int s = 16; s >= 1; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
   if (lane == 0) red[warp] = m;
   __syncthreads();
 #pragma unroll
@@ -38,10 +45,7 @@ __global__ void __launch_bounds__(256) mla_fp4_merge_kernel(const __grid_constan
     __syncthreads();
     const int k = min(n - i0, 256);
     for (int i = 0; i < k; i += kJoin) {
-      float2 o[kJoin];
-#pragma unroll
-      for (int y = 0; y < kJoin; ++y)
-        o[y] = i + y < k ? reinterpret_cast<const float2*>(p.part_o + at(i0 + i + y) * kLora)[tid] : make_float2(0.f, 0.f);
+      if (i0 + i > 0) load(i0 + i, n);
 #pragma unroll
       for (int y = 0; y < kJoin; ++y) {
         const float x = i + y < k ? wt[i + y] : 0.f;
@@ -62,9 +66,8 @@ __global__ void __launch_bounds__(256) mla_fp4_merge_kernel(const __grid_constan
 }
 
 template <int NQ>
-cudaError_t launch_nq(Fp4Params& p, int grid, cudaStream_t stream) {
+cudaError_t launch_nq(const Fp4Params& p, cudaStream_t stream) {
   using C = Fp4Cfg<NQ>;
-  p.keys = C::kKeys;
   static std::atomic<bool> configured[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -75,14 +78,13 @@ cudaError_t launch_nq(Fp4Params& p, int grid, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  return launch_pdl(mla_fp4_kernel<NQ>, dim3(grid), dim3(C::kThreads), C::kAlloc, stream, p);
+  return launch_pdl(mla_fp4_kernel<NQ>, dim3(p.G, p.W), dim3(C::kThreads), C::kAlloc, stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_fp4_paged(int nq, Fp4Params& p, cudaStream_t stream) {
-  const int grid = p.W * p.G;
-  return nq == 16 ? launch_nq<16>(p, grid, stream) : nq == 32 ? launch_nq<32>(p, grid, stream) : launch_nq<64>(p, grid, stream);
+cudaError_t launch_fp4_paged(int nq, const Fp4Params& p, cudaStream_t stream) {
+  return nq == 16 ? launch_nq<16>(p, stream) : nq == 32 ? launch_nq<32>(p, stream) : launch_nq<64>(p, stream);
 }
 
 cudaError_t launch_fp4_merge(const Fp4Params& p, cudaStream_t stream) {

@@ -67,15 +67,16 @@ struct Fp4Params {
   uint32_t num_blocks;
   int block_size, bs_shift;       // n / block_size = n bs_magic / 2^(31 + bs_shift) for n < 2^31: bs_shift = ceil(log2(block_size)),
   uint32_t bs_magic;              // bs_magic = ceil(2^(31 + bs_shift) / block_size)
-  int W, keys;                    // runs of tiles: the grid is W x G; keys of a tile (Fp4Cfg::kKeys)
+  int W;                          // runs of tiles: the grid is (G, W)
+  int w_shift;                    // as bs_magic, for W
+  uint32_t w_magic;
   float sig2;                     // softmax scale * log2(e)
   uint8_t* out;
   int64_t o_s0b, o_s1b;
   float* lse;
   float* part_o;                  // [2 W][q_len * H][512] fp32: slot 2 w + 1 a request that begins in run w and goes on,
   float* part_lse;                // slot 2 w one that began before
-  int64_t* span;                  // [W][2]: first tile and number of the request that begins in run w and goes on (-1: none),
-                                  // then the tiles of a run
+  int2* span;                     // [W]: the request that begins in run w and goes on (-1: none), and how many runs have part of it
   uint32_t* err;
   int wait_us, stall;             // test aids, as in PagedParams
   uint32_t two16, two31;          // 2^16, 2^31
@@ -316,12 +317,12 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         if (lane >= o) end += v;
       }
       const int64_t total = __shfl_sync(0xFFFFFFFFu, end, 31);
-      // (a division in 32 bits where that is enough: one in 64 takes a lone lane 0.3 us)
-      const int64_t run = total <= 0 ? 1
-                          : total < (int64_t(1) << 31) - p.W
-                              ? static_cast<int64_t>((static_cast<uint32_t>(total) + static_cast<uint32_t>(p.W - 1)) / static_cast<uint32_t>(p.W))
-                              : (total + p.W - 1) / p.W;
-      const int w = static_cast<int>(blockIdx.x) / p.G, g = static_cast<int>(blockIdx.x) % p.G;
+      // tiles / W, rounded up (divided by way of the product where 32 bits are enough: a lone lane's division is 0.3 us)
+      const int64_t up = total + p.W - 1;
+      const int64_t run = total <= 0                  ? 1
+                          : up < (int64_t(1) << 31) ? static_cast<int64_t>(__umulhi(2u * static_cast<uint32_t>(up), p.w_magic) >> p.w_shift)
+                                                    : up / p.W;
+      const int w = static_cast<int>(blockIdx.y), g = static_cast<int>(blockIdx.x);
       const int64_t lo = min(w * run, total), hi = min(lo + run, total);
       int b = p.B;
       int64_t t0 = end - sum;      // first tile of request b
@@ -334,8 +335,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       b = __shfl_sync(0xFFFFFFFFu, b, src);
       t0 = __shfl_sync(0xFFFFFFFFu, t0, src);
       if (lane == 0) TL(0, 3);
-      if (lane == 0 && blockIdx.x == 0) p.span[2 * p.W] = run;
-      int64_t t = lo, on_t = 0;
+      int64_t t = lo, on_t = 0;      // last tile of the request that goes on
       int on_b = -1;
       for (int nitem = 0;; ++nitem) {
         WorkItem it{};
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
           it.n = static_cast<int>(min(static_cast<int64_t>(it.L) - it.k0, static_cast<int64_t>(it.ntiles) * C::kKeys));
           it.pad = it.ntiles == n;                      // the whole request: final
           it.s = 2 * w + (t == t0 ? 1 : 0);
-          if (t == t0 && it.ntiles < n) on_t = t0, on_b = b;
+          if (t == t0 && it.ntiles < n) on_t = t0 + n - 1, on_b = b;
           t += it.ntiles;
           if (t < hi) {      // the next request with keys, 32 at a time (a padded batch has many without)
             t0 = t;
@@ -372,10 +372,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         }
         if (it.b < 0) break;
       }
-      if (lane == 0 && g == 0) {
-        p.span[2 * w] = on_t;
-        p.span[2 * w + 1] = on_b;
-      }
+      if (lane == 0 && g == 0) p.span[w] = make_int2(on_b, on_b < 0 ? 0 : static_cast<int>(on_t / run) - w + 1);
       __syncwarp();
       // requests without keys: zeros, every W-th one
       for (int z = w; z < p.B; z += p.W) {

@@ -143,7 +143,7 @@ def test_the_decode_s_workspace(m, L):
     up = lambda x: -(-x // 256) * 256
     for q, H, runs in ((1, 16, 152), (1, 17, 152), (1, 32, 152), (1, 33, 152), (4, 16, 152), (1, 65, 76), (1, 128, 76), (7, 128, 10), (64, 128, 1)):
         cols = q * H
-        assert n(MXFP4, 9, q, H) == up(2 * runs * cols * 2048) + up(2 * runs * cols * 4) + up((2 * runs + 1) * 8)
+        assert n(MXFP4, 9, q, H) == up(2 * runs * cols * 2048) + up(2 * runs * cols * 4) + up(runs * 8)
     assert n(MXFP4, 1, 1, 16) == n(MXFP4, 500, 1, 16) == n(MXFP4, 1, 1, 16, 64)     # neither requests nor lengths
     assert m.paged_decode_workspace_size(4, 1, 16, 4096, 152, fmt="mxfp4") == n(MXFP4, 4, 1, 16)
     assert m.paged_decode_workspace_size(64, 4, 16, 131072, 152) == n(0, 64, 4, 16)
