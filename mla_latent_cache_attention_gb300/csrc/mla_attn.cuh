@@ -45,11 +45,12 @@ constexpr int kTlCtas = 4, kTlRoles = 12, kTlEvents = 512;
 __device__ unsigned long long g_tl[kTlCtas][kTlRoles][kTlEvents][2];
 __device__ int g_tl_n[kTlCtas][kTlRoles];
 __device__ __forceinline__ void tl_mark(int role, int ev, int& n) {
-  if (blockIdx.x < kTlCtas && n < kTlEvents) {
-    g_tl[blockIdx.x][role][n][0] = ev;
-    g_tl[blockIdx.x][role][n][1] = globaltimer();
+  const unsigned cta = blockIdx.x + gridDim.x * blockIdx.y;
+  if (cta < kTlCtas && n < kTlEvents) {
+    g_tl[cta][role][n][0] = ev;
+    g_tl[cta][role][n][1] = globaltimer();
     ++n;
-    g_tl_n[blockIdx.x][role] = n;
+    g_tl_n[cta][role] = n;
   }
 }
 #define TL(role, ev) tl_mark(role, ev, tl_n)
