@@ -191,7 +191,9 @@ __device__ __forceinline__ bool spin_wait(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   bool w = true;
   if ((threadIdx.x & 31) == 0) w = spin_wait(bar, parity, abort_flag);
-  return __shfl_sync(0xFFFFFFFFu, w ? 1 : 0, 0) != 0;
+  w = __shfl_sync(0xFFFFFFFFu, w ? 1 : 0, 0) != 0;
+  __syncwarp();
+  return w;
 }
 // A group of warps waits through its first one, the others at a hardware barrier: a warp that polls takes issue slots from
 // the others (polled by every softmax and loader warp, the waits were 4500 of 10000 instructions a tile).  Every thread of the group leaves with the same answer.
@@ -599,7 +601,9 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       // test aid: write nothing, so that the other roles' waits run out under the launch's short limit
       ok = false;
     }
-    // tile 0 in the registers, records of tile 1, block ids of tile 2
+    // tile 0 in the registers, records of tile 1, block ids of tile 2.  (Behind tile t the loaders look at tile t + 3, which may be
+    // three items ahead: the item kItemDepth before that one has to be done without their next tile.)
+    static_assert(kItemDepth > 3, "the loaders would wait for themselves");
     bool have = c.table != nullptr, have1, have2;
     load_tile(found(ask(c)));
     advance(c);
