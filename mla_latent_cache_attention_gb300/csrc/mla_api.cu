@@ -734,13 +734,14 @@ extern "C" size_t mla_paged_decode_workspace_size_for(mla_cache_format fmt, int3
 namespace {
 
 // Query columns of a CTA, their groups, and the runs: as many as the SMs have room for beside the groups.
+// (Groups of 48 where they are as many as of 64; times in mla_fp4.cuh.)
 struct Fp4Plan {
   int nq;
   int64_t G, W;
 };
 Fp4Plan fp4_plan(int q_len, int H, int sms) {
   const int64_t cols = static_cast<int64_t>(q_len) * H;
-  const int nq = cols <= 16 ? 16 : cols <= 32 ? 32 : 64;
+  const int nq = cols <= 16 ? 16 : cols <= 32 ? 32 : (cols + 47) / 48 == (cols + 63) / 64 ? 48 : 64;
   const int64_t G = (cols + nq - 1) / nq;
   return Fp4Plan{nq, G, sms > G ? sms / G : 1};
 }

@@ -84,7 +84,7 @@ cudaError_t launch_nq(const Fp4Params& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_fp4_paged(int nq, const Fp4Params& p, cudaStream_t stream) {
-  return nq == 16 ? launch_nq<16>(p, stream) : nq == 32 ? launch_nq<32>(p, stream) : launch_nq<64>(p, stream);
+  return nq == 16 ? launch_nq<16>(p, stream) : nq == 32 ? launch_nq<32>(p, stream) : nq == 48 ? launch_nq<48>(p, stream) : launch_nq<64>(p, stream);
 }
 
 cudaError_t launch_fp4_merge(const Fp4Params& p, cudaStream_t stream) {

@@ -15,11 +15,12 @@
 //     which a second kernel joins; the lengths are read on the GPU, so a captured graph stays balanced.  (Splits of
 //     equal length, handed out by a counter: 32 requests of 1024 to 8192 keys 63 us, 41 so.)
 //   * Two tiles in shared memory, each four slots of E4M3 codes of 128 values and bf16 k_pe, K-major with 128-byte swizzle, read by
-//     both products.  Up to 32 columns take tiles of 128 keys.  More take 64 at once: what bounds them is a tile's conversion
-//     and the products' reads of it, whose cost hardly depends on the columns (4 x 16 rows over 16k to 128k keys, 64 requests:
-//     two groups of 32 1350 us, one of 64 1030).  64 columns leave room for two tiles of 112 keys (14 a loader warp), of which
-//     the products' last 16 rows are taken from what lies behind; of 128 keys only seven slots of eight fit, so that a tile
-//     waited for the PV of the one before (1071 us).
+//     both products.  A group has up to 64 columns: what bounds a tile is its conversion and the products' reads of it, whose
+//     cost hardly depends on the columns (4 x 16 rows over 16k to 128k keys, 64 requests: two groups of 32 1350 us, one of 64
+//     1030).  64 columns leave room for two tiles of 112 keys (14 a loader warp), of which the products' last 16 rows are taken
+//     from what lies behind; of 128 keys only seven slots of eight fit, so that a tile waited for the PV of the one before
+//     (1071 us).  Where groups of 48 are as many, they take tiles of 128 keys in less time (3.2 against 3.6 us; 128 requests of 96
+//     heads over 8k to 32k keys: three groups of 32 1147 us, two of 64 1126, two of 48 951).
 //   * Eight loader warps take 16 (14) keys of a tile each: 16-byte loads straight from the pages one tile ahead in
 //     registers, block ids two tiles ahead.  A group's exponent below K picks two words that hold the E4M3 bytes of the eight
 //     magnitudes at that scale; a byte permute turns four codes into four bytes.  That is 1.5 instructions a code,
@@ -31,7 +32,7 @@
 //     sum w 2^(6 - K) = 2^(s - m), so the key's scale costs one multiplication.  The weights enter
 //     O^T += V^T P as two E4M3 terms hi + 2^-4 lo (to 2^-8 of a weight, down to 2^-11 of the reference).
 //     The reference m moves only when a logit passes it by kTau.
-//   * hi and lo terms are stacked along N, with accumulators of their own that the epilogue adds; at 64 columns the tensor memory has
+//   * hi and lo terms are stacked along N, with accumulators of their own that the epilogue adds; from 48 columns on the tensor memory has
 //     no room for those, and hi and the plain rest lo = x - hi go to the same accumulator, one after the other along K.  A
 //     rest is then kept to 2^-10 of the scaled range: a query's value to 2^-18 of the column's largest, a weight to 2^-14 of the
 //     reference, which lies higher in E4M3's range for it, and kTau lower: a reference that moves costs 2.8 us (kTau 5 and 2^-13: 2 %
@@ -84,20 +85,22 @@ struct Fp4Params {
 
 template <int NQ_>
 struct Fp4Cfg {
-  static_assert(NQ_ == 16 || NQ_ == 32 || NQ_ == 64, "columns per item");
+  static_assert(NQ_ == 16 || NQ_ == 32 || NQ_ == 48 || NQ_ == 64, "columns per item");
   static constexpr int NQ = NQ_;
-  static constexpr bool kWide = NQ == 64;                         // hi and lo terms along K, short tiles (see above)
+  static constexpr bool kWide = NQ >= 48;                         // hi and lo terms along K, one slot of k_pe (see above)
   static constexpr int kN = kWide ? NQ : 2 * NQ;                  // columns of a code product
   // keys of a tile: 128, or 112 of the 128 rows of a product where the columns leave two tiles of 128 no room
-  static constexpr int kKeys = kWide ? 112 : 128, kSlot = kKeys * 128, kRopes = kWide ? 1 : 2;
-  static constexpr int NC = NQ < 32 ? NQ : 32;                    // columns of a softmax thread
+  static constexpr int kKeys = NQ == 64 ? 112 : 128, kSlot = kKeys * 128, kRopes = kWide ? 1 : 2;
+  static constexpr int NC = NQ % 32 ? 16 : 32;                    // columns of a softmax thread
   static constexpr int kSW = 4 * (NQ / NC);                       // softmax warps
   static constexpr int kLoadWarps = 8, kPvWarp = 2, kFirstSm = kWide ? 4 : 3, kFirstLoad = kFirstSm + kSW;
   static constexpr int kThreads = 32 * (kFirstLoad + kLoadWarps);
-  // 640 threads start with 96 registers; the warps of the issuers leave the others what those need (61440 in all, as at
-  // the start)
-  static constexpr int kIssueRegs = 32, kSoftmaxRegs = 120, kLoadRegs = 104;
-  static_assert(!kWide || (kThreads == 640 && 128 * kIssueRegs + 256 * kSoftmaxRegs + 256 * kLoadRegs <= 640 * 96), "registers of the launch");
+  // The threads start with the same registers each, by eights; the warps of the issuers leave the others what those need
+  static constexpr int kStartRegs = 65536 / kThreads / 8 * 8;
+  static constexpr int kIssueRegs = 32, kSoftmaxRegs = NQ == 64 ? 120 : 80, kLoadRegs = 104;
+  static_assert(!kWide || (kSW % 4 == 0 && 4 * kIssueRegs + kSW * kSoftmaxRegs + kLoadWarps * kLoadRegs <= kThreads / 32 * kStartRegs), "registers of the launch");
+  // (an increase below the start, or a decrease above it, is an illegal instruction)
+  static_assert(!kWide || (kIssueRegs <= kStartRegs && kSoftmaxRegs >= kStartRegs && kLoadRegs >= kStartRegs), "directions of the changes");
   static constexpr int kRing = 0;                                 // code tiles
   static constexpr int kPad = (128 - kKeys) * 128;                // of the last slot's products: zeros
   static constexpr int kRope = kRing + 8 * kSlot + kPad;          // k_pe
