@@ -13,7 +13,7 @@
 //     columns (a column is a (query token, head) pair); the CTAs of all groups take the same run side by side and meet
 //     its records in L2.  Where a run begins or ends inside a request its part is a partial result, at most two a CTA,
 //     which a second kernel joins; the lengths are read on the GPU, so a captured graph stays balanced.  (Splits of
-//     equal length, handed out by a counter: 32 requests of 1024 to 8192 keys 63 us, 41 so.)
+//     equal length, handed out by a counter: 32 requests of 1024 to 8192 keys 63 us, 39 so.)
 //   * Two tiles in shared memory, each four slots of E4M3 codes of 128 values and bf16 k_pe, K-major with 128-byte swizzle, read by
 //     both products.  A group has up to 64 columns: what bounds a tile is its conversion and the products' reads of it, whose
 //     cost hardly depends on the columns (4 x 16 rows over 16k to 128k keys, 64 requests: two groups of 32 1350 us, one of 64
@@ -39,7 +39,7 @@
 //     less time, error of the output 0.0020 against 0.0018; kTau 3: 2 % more, 0.0017).
 //   * Roles hand over through mbarriers, each waited with a time limit.  Waits between the products and what feeds them are
 //     polled: a suspended thread (try_wait) was woken 0.5 to 1 us late, four times a tile (1390 -> 1095 us; of 16 columns 43 ->
-//     39).  The scheduler and the wait for a work item are not in a hurry.
+//     39).
 //
 // What bounds it now, 64 columns (3.6 us a tile of 112 keys): loaders (3.4 us: load latency, then conversion and 1.4 us of stores),
 // softmax (1.8 us, ordered after QK) and the tensor pipe, whose operand reads (6 KB a product of 33 cycles) share
@@ -91,16 +91,18 @@ struct Fp4Cfg {
   static constexpr int kN = kWide ? NQ : 2 * NQ;                  // columns of a code product
   // keys of a tile: 128, or 112 of the 128 rows of a product where the columns leave two tiles of 128 no room
   static constexpr int kKeys = NQ == 64 ? 112 : 128, kSlot = kKeys * 128, kRopes = kWide ? 1 : 2;
-  static constexpr int NC = NQ % 32 ? 16 : 32;                    // columns of a softmax thread
-  static constexpr int kSW = 4 * (NQ / NC);                       // softmax warps
-  static constexpr int kLoadWarps = 8, kPvWarp = 2, kFirstSm = kWide ? 4 : 3, kFirstLoad = kFirstSm + kSW;
+  // columns of a softmax thread, and the softmax warps: 16 (of 32 in 8 warps instead of 32 in 4: 32 requests of 1024 to 8192 keys
+  // 54 -> 47 us), 32 of 64, where four times four warps would leave a thread 64 registers
+  static constexpr int NC = NQ == 64 ? 32 : 16, kSW = 4 * (NQ / NC);
+  static constexpr bool kSetRegs = NQ > 16;
+  static constexpr int kLoadWarps = 8, kPvWarp = 2, kFirstSm = kSetRegs ? 4 : 3, kFirstLoad = kFirstSm + kSW;
   static constexpr int kThreads = 32 * (kFirstLoad + kLoadWarps);
   // The threads start with the same registers each, by eights; the warps of the issuers leave the others what those need
   static constexpr int kStartRegs = 65536 / kThreads / 8 * 8;
-  static constexpr int kIssueRegs = 32, kSoftmaxRegs = NQ == 64 ? 120 : 80, kLoadRegs = 104;
-  static_assert(!kWide || (kSW % 4 == 0 && 4 * kIssueRegs + kSW * kSoftmaxRegs + kLoadWarps * kLoadRegs <= kThreads / 32 * kStartRegs), "registers of the launch");
+  static constexpr int kIssueRegs = 32, kSoftmaxRegs = NQ == 64 ? 120 : NQ == 48 ? 80 : 112, kLoadRegs = NQ == 32 ? 112 : 104;
+  static_assert(!kSetRegs || (kSW % 4 == 0 && 4 * kIssueRegs + kSW * kSoftmaxRegs + kLoadWarps * kLoadRegs <= kThreads / 32 * kStartRegs), "registers of the launch");
   // (an increase below the start, or a decrease above it, is an illegal instruction)
-  static_assert(!kWide || (kIssueRegs <= kStartRegs && kSoftmaxRegs >= kStartRegs && kLoadRegs >= kStartRegs), "directions of the changes");
+  static_assert(!kSetRegs || (kIssueRegs <= kStartRegs && kSoftmaxRegs >= kStartRegs && kLoadRegs >= kStartRegs), "directions of the changes");
   static constexpr int kRing = 0;                                 // code tiles
   static constexpr int kPad = (128 - kKeys) * 128;                // of the last slot's products: zeros
   static constexpr int kRope = kRing + 8 * kSlot + kPad;          // k_pe
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
 
   // (the registers are set inside the roles' branches: the compiler gives a branch what it sets)
   if (warp < C::kFirstSm) {
-    if constexpr (C::kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
+    if constexpr (C::kSetRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kIssueRegs));
     if (warp == 0) {
       // ------------------------------------------------------------------ scheduler
       auto tiles_of = [&](int b) -> int64_t { return static_cast<int64_t>((static_cast<uint32_t>(max(p.seq_lens[b], 0)) + (C::kKeys - 1)) / C::kKeys); };
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       __syncwarp();
     }
   } else if (warp >= C::kFirstLoad) {
-    if constexpr (C::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kLoadRegs));
+    if constexpr (C::kSetRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kLoadRegs));
     // ------------------------------------------------------------------ loaders
     // Warp w owns keys KW w .. KW w + KW - 1 of every tile.  Lane k < 16 finds key k's record and has its exponents; the
     // codes and k_pe are loaded eight lanes a key, 128 bytes in a row: lane 16 a + 8 b + 4 c + u takes, of keys 4 m + 2 a + c, the
@@ -706,7 +708,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     errbits = __reduce_or_sync(0xFFFFFFFFu, errbits);
     if (lane == 0 && errbits) set_device_error(p.err, errbits);
   } else {
-    if constexpr (C::kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
+    if constexpr (C::kSetRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftmaxRegs));
     // ------------------------------------------------------------------ softmax, query, epilogue
     constexpr int NT = 32 * C::kSW, NC = C::NC;
     const int quad = warp & 3;
