@@ -6,21 +6,39 @@ namespace mla {
 namespace {
 
 // The joined results of requests that several runs share: out = sum_i e^{lse_i - lse} O_i over the request's parts.  Grid
-// (query columns, W): CTA (c, w) joins column c of the request that begins in run w and goes on, if there is one.
+// (query columns, min(B, W)): CTA (c, y) joins column c of the y-th such request, if there are as many.
 constexpr int kJoin = 16;      // loads of a thread on their way at once
 
 __global__ void __launch_bounds__(256) mla_fp4_merge_kernel(const __grid_constant__ Fp4Params p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, w0 = blockIdx.y, tid = threadIdx.x;
-  const int2 span = p.span[w0];
-  const int n = span.y;
-  if (span.x < 0) return;
-  const int64_t b = span.x;
+  const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int found[8], mine[3];
+  int w0 = -1, n = 0, left = blockIdx.y;      // requests before this one
+  int64_t b = -1;
+  for (int i0 = 0; i0 < p.W; i0 += 256) {
+    const int2 span = i0 + tid < p.W ? p.span[i0 + tid] : make_int2(-1, 0);
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, span.x >= 0);
+    if (lane == 0) found[warp] = __popc(some);
+    __syncthreads();
+    int before = __popc(some & ((1u << lane) - 1u)), all = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i < warp) before += found[i];
+      all += found[i];
+    }
+    if (span.x >= 0 && before == left) mine[0] = i0 + tid, mine[1] = span.x, mine[2] = span.y;
+    __syncthreads();
+    if (left < all) {
+      w0 = mine[0], b = mine[1], n = mine[2];
+      break;
+    }
+    left -= all;
+  }
+  if (w0 < 0) return;
   // part i is slot 2 (w0 + i), the first one 2 w0 + 1
   auto at = [&](int i) -> int64_t { return (2 * static_cast<int64_t>(w0 + i) + (i == 0 ? 1 : 0)) * p.cols + c; };
   __shared__ float wt[256];
   __shared__ float red[8];
-  const int lane = tid & 31, warp = tid >> 5;
   float2 o[kJoin];
   auto load = [&](int i, int k) {
 #pragma unroll
@@ -88,7 +106,7 @@ cudaError_t launch_fp4_paged(int nq, const Fp4Params& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_fp4_merge(const Fp4Params& p, cudaStream_t stream) {
-  return launch_pdl(mla_fp4_merge_kernel, dim3(p.cols, p.W), dim3(256), 0, stream, p);
+  return launch_pdl(mla_fp4_merge_kernel, dim3(p.cols, p.B < p.W ? p.B : p.W), dim3(256), 0, stream, p);
 }
 
 }  // namespace mla
