@@ -538,6 +538,24 @@ def test_wait_limit_is_reported(m):
     assert torch.equal(o, out) and torch.equal(l, lse) and m.read_device_errors() == 0
 
 
+@pytest.mark.parametrize("H", [32, 48, 64, 128])
+def test_wait_limit_of_more_columns(m, H):
+    rng = np.random.default_rng(25)
+    args, kw, out, lse = run_decode(m, rng, [300, 40, 700], H=H)
+    m.lib().mla_debug_stall_next_decode(20000)
+    m.paged_decode(*args, **kw)
+    assert m.read_device_errors() & 16
+    o, l = m.paged_decode(*args, **kw)
+    assert torch.equal(o, out) and torch.equal(l, lse) and m.read_device_errors() == 0
+
+
+@pytest.mark.parametrize("B,H", [(1, 16), (1, 48), (2, 128), (12, 16), (19, 16), (20, 16)])
+def test_joins_of_many_and_few_parts(m, B, H):
+    """Requests that many runs share, around the number from which on a join has fewer loads on their way."""
+    rng = np.random.default_rng(B)
+    run_decode(m, rng, [int(x) for x in rng.integers(2500, 4000, B)], H=H)
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_fuzz(m, seed):
     rng = np.random.default_rng(1000 + seed)
