@@ -493,7 +493,7 @@ MLA_API int mla_rope_table(float* out, int64_t max_position, int32_t R, double b
  *   free_blocks  device int32 [capacity]; num_free  device int32 [1].
  *   seq_out      device out int32 [B]: L + n (L where not served); may be seq_lens itself.
  *   num_free_out device out int32 [1]; may be num_free itself.
- *   served       device out bytes [B]: 1, or 0 where not served.
+ *   served       device out bytes [B]: 1, or 0 where not served.  NULL: not wanted (B <= 1024).
  *   cu_q_lens    device out int32 [B + 1] (no more than T).
  *   slots, positions  device out int64 [T].
  * Whole numbers only: the same inputs give the same outputs.

@@ -1087,8 +1087,9 @@ def plan_step(seq_lens, new_lens, block_table, free_blocks, num_free, *, block_s
     cu_q_lens = vector(cu_q_lens, "cu_q_lens", _I32, B + 1)
     seq_lens_out = vector(seq_lens_out, "seq_lens_out", _I32, B)
     num_free_out = vector(num_free_out, "num_free_out", _I32, 1)
-    served = vector(served, "served", flags, B)
+    if served is not None or B > 1024:      # (more requests need it inside)
+        served = vector(served, "served", flags, B)
     _call(lib().mla_plan_step, dev, seq_lens.data_ptr(), new_lens.data_ptr(), None if finished is None else finished.data_ptr(), table,
           tstride, cols, free_blocks.data_ptr(), free_blocks.shape[0], num_free.data_ptr(), seq_lens_out.data_ptr(),
-          num_free_out.data_ptr(), served.data_ptr(), cu_q_lens.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), B, T, block_size)
+          num_free_out.data_ptr(), None if served is None else served.data_ptr(), cu_q_lens.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), B, T, block_size)
     return slot_mapping, positions, cu_q_lens, seq_lens_out, num_free_out

@@ -666,11 +666,11 @@ PyObject* py_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return not_plain();
   const int64_t B = seq.size[0], B1 = B + 1, one = 1, rows = T;
   if (B < 1 || B >= INT32_MAX || nw.size[0] != B || !read_table(a[2], B, dev, &tab) || tab.cols > INT32_MAX) return not_plain();
-  fin.ptr = nullptr;
+  fin.ptr = tsv.ptr = nullptr;      // (served is not made where nobody asks: more requests need it between the kernel's parts)
   if (a[7] != Py_None && (!read(a[7], dev, 1, &fin, g_bool, g_u8) || fin.size[0] != B)) return not_plain();
   if (!output(a[11], dev, 1, &rows, g_i64, nullptr, device.p, &tsl, &sl) || !output(a[12], dev, 1, &rows, g_i64, nullptr, device.p, &tpo, &po) ||
       !output(a[13], dev, 1, &B1, g_i32, nullptr, device.p, &tcu, &cu) || !output(a[8], dev, 1, &B, g_i32, nullptr, device.p, &tso, &so) ||
-      !output(a[9], dev, 1, &one, g_i32, nullptr, device.p, &tno, &no) || !output(a[10], dev, 1, &B, g_bool, g_u8, device.p, &tsv, &sv))
+      !output(a[9], dev, 1, &one, g_i32, nullptr, device.p, &tno, &no) || ((a[10] != Py_None || B > 1024) && !output(a[10], dev, 1, &B, g_bool, g_u8, device.p, &tsv, &sv)))
     return not_plain();
   cudaStream_t stream;
   if (!stream_of(dev, &stream)) return not_plain();

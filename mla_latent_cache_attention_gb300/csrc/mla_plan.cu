@@ -14,7 +14,7 @@
 namespace mla {
 namespace {
 
-constexpr int kPlanThreads = 1024, kPlanCtas = 8;
+constexpr int kPlanThreads = kPlanKept, kPlanCtas = 8;
 constexpr uint32_t kErrFree = 32u;      // MLA_DEVERR_FREE
 
 struct Pair {
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         p.cu[b] = at;
         if (b == p.B - 1) p.cu[p.B] = end;
         p.seq_out[b] = len;
-        p.served[b] = served;
+        if (p.served) p.served[b] = served;
         if (!served) err |= kErrFree;
       }
     }

@@ -38,6 +38,7 @@ struct RopeTableParams {
 };
 cudaError_t launch_rope_table(const RopeTableParams& p, cudaStream_t stream);
 
+constexpr int kPlanKept = 1024;          // requests whose sums are kept on chip
 struct PlanParams {
   const int32_t* seq_lens;
   const int32_t* new_lens;
@@ -49,7 +50,7 @@ struct PlanParams {
   const int32_t* num_free;
   int32_t* seq_out;
   int32_t* num_free_out;
-  uint8_t* served;                     // [B]
+  uint8_t* served;                     // [B]; null: not wanted (B <= kPlanKept)
   int32_t* cu;                         // [B + 1]
   int64_t* slots;                      // [T]
   int64_t* positions;                  // [T]

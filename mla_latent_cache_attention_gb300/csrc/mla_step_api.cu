@@ -125,8 +125,8 @@ extern "C" int mla_plan_step(const int32_t* seq_lens, const int32_t* new_lens, c
   if (block_size < 1) return fail(MLA_ERR_INVALID, "block_size must be >= 1");
   if (cols < 1 || t_stride < cols) return fail(MLA_ERR_INVALID, "bad block table: %d columns, row stride %lld", cols, static_cast<long long>(t_stride));
   if (capacity < 0 || capacity > 0x7FFFFFFF) return fail(MLA_ERR_INVALID, "bad capacity of the free blocks");
-  if (!seq_lens || !new_lens || !block_table || (capacity > 0 && !free_blocks) || !num_free || !seq_out || !num_free_out || !served ||
-      !cu_q_lens || (T > 0 && (!slots || !positions)))
+  if (!seq_lens || !new_lens || !block_table || (capacity > 0 && !free_blocks) || !num_free || !seq_out || !num_free_out ||
+      (!served && B > kPlanKept) || !cu_q_lens || (T > 0 && (!slots || !positions)))
     return fail(MLA_ERR_INVALID, "a required pointer is NULL");
   if (!aligned(seq_lens, 4) || !aligned(new_lens, 4) || !aligned(block_table, 4) || !aligned(free_blocks, 4) || !aligned(num_free, 4) ||
       !aligned(seq_out, 4) || !aligned(num_free_out, 4) || !aligned(cu_q_lens, 4) || !aligned(slots, 8) || !aligned(positions, 8))

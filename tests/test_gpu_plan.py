@@ -213,3 +213,25 @@ def test_a_server_s_steps(m):
                 assert np.all(np.abs(out[b].double().cpu().numpy() - o) <= tol) and np.all(np.abs(lse[b].double().cpu().numpy() - l) <= ltol)
                 at += n
     assert m.read_device_errors() == 0
+
+
+@pytest.mark.parametrize("B", [1, 5, 1024, 1025, 3000])
+def test_without_the_served_flags(m, monkeypatch, B):
+    """The same step whether anybody asks who was served or not, in both forms of the binding; a third of the requests do not fit."""
+    g = torch.Generator(device="cuda").manual_seed(B)
+    seq, new = (torch.randint(0, n, (B,), generator=g, device="cuda", dtype=torch.int32) for n in (90, 40))
+    new[::3] = 1000
+    done = torch.rand(B, generator=g, device="cuda") < 0.2
+
+    def run(**kw):
+        table = torch.arange(B * 12, dtype=torch.int32, device="cuda").view(B, 12)
+        free = torch.arange(B * 12, B * 18, dtype=torch.int32, device="cuda")
+        nf = torch.tensor([B * 5], dtype=torch.int32, device="cuda")
+        out = m.plan_step(seq, new, table, free, nf, block_size=16, num_tokens=20 * B, finished=done, **kw)
+        assert m.read_device_errors() == 32
+        return [*out, table, free]
+
+    want = run(served=torch.empty(B, dtype=torch.bool, device="cuda"))
+    for _ in range(2):
+        assert all(torch.equal(x, y) for x, y in zip(run(), want))
+        monkeypatch.setattr(m, "_step", m._DeclinedStep)

@@ -80,7 +80,7 @@ def plan(L, **kw):
 @pytest.mark.parametrize("want,kw", [
     (INVALID, dict(B=0)), (INVALID, dict(B=-1)), (INVALID, dict(T=-1)), (INVALID, dict(bs=0)), (INVALID, dict(cols=0)), (INVALID, dict(bts=3)),
     (INVALID, dict(cap=-1)), (INVALID, dict(cap=1 << 31)), (INVALID, dict(seq=NULL)), (INVALID, dict(new=NULL)), (INVALID, dict(bt=NULL)),
-    (INVALID, dict(free=NULL)), (INVALID, dict(nf=NULL)), (INVALID, dict(so=NULL)), (INVALID, dict(nfo=NULL)), (INVALID, dict(served=NULL)),
+    (INVALID, dict(free=NULL)), (INVALID, dict(nf=NULL)), (INVALID, dict(so=NULL)), (INVALID, dict(nfo=NULL)), (INVALID, dict(served=NULL, B=1025)),
     (INVALID, dict(cu=NULL)), (INVALID, dict(slots=NULL)), (INVALID, dict(pos=NULL)), (INVALID, dict(seq=HALF)), (INVALID, dict(bt=HALF)),
     (INVALID, dict(slots=HALF)), (INVALID, dict(pos=HALF)), (INVALID, dict(cu=HALF)), (INVALID, dict(free=HALF)),
 ])
