@@ -16,12 +16,12 @@
 //     equal length, handed out by a counter: 32 requests of 1024 to 8192 keys 63 us, 39 so.)
 //   * Two tiles in shared memory, each four slots of E4M3 codes of 128 values and bf16 k_pe, K-major with 128-byte swizzle, read by
 //     both products.  A group has up to 64 columns: what bounds a tile is its conversion and the products' reads of it, whose
-//     cost hardly depends on the columns (4 x 16 rows over 16k to 128k keys, 64 requests: two groups of 32 1350 us, one of 64
-//     1030).  64 columns leave room for two tiles of 112 keys (14 a loader warp), of which the products' last 16 rows are taken
-//     from what lies behind; of 128 keys only seven slots of eight fit, so that a tile waited for the PV of the one before
-//     (1071 us).  Where groups of 48 are as many, they take tiles of 128 keys in less time (3.2 against 3.6 us; 128 requests of 96
-//     heads over 8k to 32k keys: three groups of 32 1147 us, two of 64 1126, two of 48 951).
-//   * Eight loader warps take 16 (14) keys of a tile each: 16-byte loads straight from the pages one tile ahead in
+//     cost hardly depends on the columns (4 x 16 rows over 16k to 128k keys, 64 requests, with two terms a weight: two groups of
+//     32 1350 us, one of 64 1030).  64 columns and three terms leave room for two tiles of 96 keys (12 a loader warp): QK takes
+//     the other 32 of its 128 rows from what lies behind, and their scores are masked.  Where groups of 48 are as many, they
+//     take tiles of 128 keys in less time (128 requests of 96 heads over 8k to 32k keys, two terms: three groups of 32 1147 us, two
+//     of 64 1126, two of 48 951).
+//   * Eight loader warps take 16 (12) keys of a tile each: 16-byte loads straight from the pages one tile ahead in
 //     registers, block ids two tiles ahead.  A group's exponent below K picks two words that hold the E4M3 bytes of the eight
 //     magnitudes at that scale; a byte permute turns four codes into four bytes.  That is 1.5 instructions a code,
 //     where the conversion instructions by way of f16 take as many but run at half rate.
@@ -30,21 +30,28 @@
 //     of the scaled range's 448); k_pe . q_pe as a bf16 product of its own.
 //   * Online softmax over s' = s + K - 6: the weight of a key's codes is w = 2^(s' - m), its share of the row
 //     sum w 2^(6 - K) = 2^(s - m), so the key's scale costs one multiplication.  The weights enter
-//     O^T += V^T P as two E4M3 terms hi + 2^-4 lo (to 2^-8 of a weight, down to 2^-11 of the reference).
-//     The reference m moves only when a logit passes it by kTau.
-//   * hi and lo terms are stacked along N, with accumulators of their own that the epilogue adds; from 48 columns on the tensor memory has
-//     no room for those, and hi and the plain rest lo = x - hi go to the same accumulator, one after the other along K.  A
-//     rest is then kept to 2^-10 of the scaled range: a query's value to 2^-18 of the column's largest, a weight to 2^-14 of the
-//     reference, which lies higher in E4M3's range for it, and kTau lower: a reference that moves costs 2.8 us (kTau 5 and 2^-13: 2 %
-//     less time, error of the output 0.0020 against 0.0018; kTau 3: 2 % more, 0.0017).
+//     O^T += V^T P as three E5M2 terms, each the rest rounded to nearest: a weight is off by 2^-10 of itself at most (half a step
+//     of the last term, 2^-11, and of the f16 that is split, 2^-11), and nothing is lost above 2^-27 of the reference, which
+//     may stand far above most weights of a row (one large key in front; two E4M3 terms ended at 2^-15 and dropped up to
+//     half of such a row's output).  Over 2^17 keys that is 2^-10 of the largest weight.  The reference m moves only when a
+//     logit passes it by kTau, a move costs 2.8 us: the higher kTau, the earlier E5M2 ends below the reference (4 x 16 rows as
+//     above, 128 requests of 96 heads as above and 32 requests of 1024 to 8192 keys: kTau 4.75 1127, 1005 and 39.5 us, 5.75 1099, 1003 and 39.1;
+//     the two E4M3 terms took 1025, 939 and 37.2).  The largest weight of an item's first tile is 2^kPExp, a term exactly.
+//   * The tensor cores add in fp32 and cut off: 2^-23 of an accumulator a product, of 32 keys.  Terms of both signs make less
+//     of it (131072 flat keys behind one of 15 nats more: output 0.0009 too small; 2^20 keys: 0.002).
+//   * The terms of a weight stand side by side along N with accumulators of their own that the epilogue adds (16 columns), or as
+//     many as the tensor memory has room for, and the others add to the last accumulators by products of their own, one after the
+//     other along K (32 columns: two and one; more: one each).
+//   * hi and lo terms of the query are stacked along N; from 48 columns on the tensor memory has no room for that, and hi and the
+//     plain rest lo = x - hi go to the same scores.  A rest is then kept to 2^-10 of the scaled range: a query's value to 2^-18
+//     of the column's largest.
 //   * Roles hand over through mbarriers, each waited with a time limit.  Waits between the products and what feeds them are
 //     polled: a suspended thread (try_wait) was woken 0.5 to 1 us late, four times a tile (1390 -> 1095 us; of 16 columns 43 ->
 //     39).
 //
-// What bounds it now, 64 columns (3.6 us a tile of 112 keys): loaders (3.4 us: load latency, then conversion and 1.4 us of stores),
-// softmax (1.8 us, ordered after QK) and the tensor pipe, whose operand reads (6 KB a product of 33 cycles) share
-// the data path of shared memory with both: 2.5 us of 68 products at 75 cycles each.  Up to 32 columns: the chain of load, conversion,
-// QK, softmax and PV of two tiles (2.7 us a tile).
+// What bounds it now, 64 columns: loaders (load latency, then conversion and stores), softmax (ordered after QK) and the tensor
+// pipe, whose operand reads (6 KB a product of 33 cycles) share the data path of shared memory with both: 72 products a tile at
+// 75 cycles each.  Up to 32 columns: the chain of load, conversion, QK, softmax and PV of two tiles (2.5 us a tile).
 //
 // Warps: 0 scheduler, 1 QK issuer (TMEM owner), 2 PV issuer, then the softmax warps (which also prepare the query and
 // write the results), then 8 loaders.
@@ -89,8 +96,10 @@ struct Fp4Cfg {
   static constexpr int NQ = NQ_;
   static constexpr bool kWide = NQ >= 48;                         // hi and lo terms along K, one slot of k_pe (see above)
   static constexpr int kN = kWide ? NQ : 2 * NQ;                  // columns of a code product
-  // keys of a tile: 128, or 112 of the 128 rows of a product where the columns leave two tiles of 128 no room
-  static constexpr int kKeys = NQ == 64 ? 112 : 128, kSlot = kKeys * 128, kRopes = kWide ? 1 : 2;
+  // keys of a tile: 128, or 96 where the columns leave two tiles of 128 no room
+  static constexpr int kKeys = NQ == 64 ? 96 : 128, kSlot = kKeys * 128, kRopes = kWide ? 1 : 2;
+  // terms of a weight, and how many of them stand side by side along N
+  static constexpr int kTerms = 3, kStack = NQ == 16 ? 3 : NQ == 32 ? 2 : 1, kNO = kStack * NQ;
   // columns of a softmax thread, and the softmax warps: 16 (of 32 in 8 warps instead of 32 in 4: 32 requests of 1024 to 8192 keys
   // 54 -> 47 us), 32 of 64, where four times four warps would leave a thread 64 registers
   static constexpr int NC = NQ == 64 ? 32 : 16, kSW = 4 * (NQ / NC);
@@ -104,12 +113,11 @@ struct Fp4Cfg {
   // (an increase below the start, or a decrease above it, is an illegal instruction)
   static_assert(!kSetRegs || (kIssueRegs <= kStartRegs && kSoftmaxRegs >= kStartRegs && kLoadRegs >= kStartRegs), "directions of the changes");
   static constexpr int kRing = 0;                                 // code tiles
-  static constexpr int kPad = (128 - kKeys) * 128;                // of the last slot's products: zeros
-  static constexpr int kRope = kRing + 8 * kSlot + kPad;          // k_pe
+  static constexpr int kRope = kRing + 8 * kSlot;                 // k_pe
   static constexpr int kQ = kRope + kRopes * kSlot;               // 4 x (2 NQ rows x 128 B): hi rows, then lo rows
   static constexpr int kQRope = kQ + 4 * 2 * NQ * 128;            // NQ x 128 B
-  static constexpr int kP = kQRope + NQ * 128;                    // 128 keys x 2 NQ
-  static constexpr int kScale = kP + kTile * 2 * NQ;              // [2][128] fp32: 2^(K - 6), -1 masked
+  static constexpr int kP = kQRope + NQ * 128;                    // keys x 3 NQ
+  static constexpr int kScale = kP + kKeys * kTerms * NQ;         // [2][128] fp32: 2^(K - 6), -1 masked
   static constexpr int kRed = kScale + 2 * kTile * 4;             // [2][NQ][4] max, [NQ][4] sum
   static constexpr int kColF = kRed + 3 * NQ * 4 * 4;             // [NQ] sig2 2^-e
   static constexpr int kMref = kColF + NQ * 4;                    // [NQ]
@@ -125,12 +133,12 @@ struct Fp4Cfg {
   static constexpr int kAlloc = kTotal + 1024;
   static_assert(kAlloc <= kSmemLimit, "shared memory budget");
   static constexpr int kS = kN + NQ;                              // S: codes, then rope columns; two of them
-  static constexpr int kTmemO = 2 * kS;                           // O_j at kTmemO + kN j
-  static constexpr int kTmemCols = kTmemO + 4 * kN <= 256 ? 256 : 512;
-  static_assert(kTmemO + 4 * kN <= kTmemCols, "TMEM budget");
-  // The lo terms of E4M3 pairs: 16 times the rest where they have columns of their own, the rest itself where they add to
-  // the hi terms' (rests below 2^-10 are lost).  The weights are 2^(kPExp + kTau) at most (2^8.75 of 448).
-  static constexpr float kLo = kWide ? 1.f : 16.f, kTau = kWide ? 4.f : 7.f, kPExp = kWide ? 4.75f : 1.f;
+  static constexpr int kTmemO = 2 * kS;                           // O_j at kTmemO + kNO j
+  static constexpr int kTmemCols = kTmemO + 4 * kNO <= 256 ? 256 : 512;
+  static_assert(kTmemO + 4 * kNO <= kTmemCols, "TMEM budget");
+  // The query's lo terms: 16 times the rest where they have columns of their own, the rest itself where they add to
+  // the hi terms' (rests below 2^-10 are lost).  The weights are 2^(kPExp + kTau) = 2^15.75 at most, of E5M2's 1.75 * 2^15.
+  static constexpr float kLo = kWide ? 1.f : 16.f, kTau = 5.75f, kPExp = 10.f;
 };
 
 // The E4M3 bytes of eight codes: the magnitudes picked by permutes from the eight bytes of lut, with the codes as
@@ -277,11 +285,6 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
-  // Products read 128 rows: of a shorter tile's last ones they take those behind the slot (the next slot's codes, in the end a
-  // pad), whose scores are masked and whose weights are zeros: numbers all of them, once these are zeros.
-  if constexpr (C::kKeys < kTile)
-    for (int i = tid; i < 9 * C::kPad / 16; i += C::kThreads)
-      *reinterpret_cast<uint4*>(ring + i / (C::kPad / 16) * C::kSlot + i % (C::kPad / 16) * 16) = make_uint4(0, 0, 0, 0);
   if (warp == 0 && lane < 16) {
     // magnitudes 0, .5, 1, 1.5 | 2, 3, 4, 6 times 2^(6 - lane) in E4M3: exact down to 2^-9, zero below
     // (entry 15 is all zeros)
@@ -296,7 +299,6 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     }
     lut[lane] = make_uint2(w[0], w[1]);
   }
-  if (C::kKeys < kTile) fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -462,8 +464,9 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       {
         const bool one = elect_one();
         const uint64_t dV0 = smem_desc(smem_u32(ring), C::kSlot, 1024, kSwizzle128B);
-        const uint64_t dP0 = smem_desc(smem_u32(ps), 2 * NQ * 8, 128, kSwizzleNone);
-        constexpr uint32_t kIdPv = idesc_e4m3(128, C::kN, 1, 1);
+        const uint64_t dP0 = smem_desc(smem_u32(ps), C::kTerms * NQ * 8, 128, kSwizzleNone);
+        // (B, the weights, in E5M2)
+        constexpr uint32_t kIdStack = idesc_e4m3(128, C::kNO, 1, 1) | (1u << 10), kIdTerm = idesc_e4m3(128, NQ, 1, 1) | (1u << 10);
         bool ok = true;
         int nit = 0, g = 0;
         while (ok) {
@@ -487,10 +490,13 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
             for (int j = 0; j < 4; ++j) {
               const uint64_t aV = desc_add(dV0, static_cast<uint32_t>((4 * (gt & 1) + j) * (C::kSlot >> 4)));
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                mma_f8_if(one, tmem + C::kTmemO + C::kN * j, desc_add(aV, (kk * 4096) >> 4), desc_add(dP0, (kk * NQ * 64) >> 4), kIdPv, kk > 0 ? 1u : acc0);
-                if constexpr (C::kWide)
-                  mma_f8_if(one, tmem + C::kTmemO + C::kN * j, desc_add(aV, (kk * 4096) >> 4), desc_add(dP0, (kk * NQ * 64 + NQ * 8) >> 4), kIdPv, 1u);
+              for (int kk = 0; kk < C::kKeys / 32; ++kk) {
+                // (32 keys are four groups of eight; the terms beyond the stacked ones add to the last of those)
+                const uint32_t dO = tmem + C::kTmemO + C::kNO * j, at = kk * 4 * C::kTerms * NQ * 8;
+                mma_f8_if(one, dO, desc_add(aV, (kk * 4096) >> 4), desc_add(dP0, at >> 4), kIdStack, kk > 0 ? 1u : acc0);
+#pragma unroll
+                for (int x = C::kStack; x < C::kTerms; ++x)
+                  mma_f8_if(one, dO + C::kNO - NQ, desc_add(aV, (kk * 4096) >> 4), desc_add(dP0, (at + x * NQ * 8) >> 4), kIdTerm, 1u);
               }
               if ((j + 1) % (4 / C::kParts) == 0) mma_commit_if(one, &pv_part[(gt & 1) * C::kParts + j / (4 / C::kParts)]);
             }
@@ -511,8 +517,8 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     // codes and k_pe are loaded eight lanes a key, 128 bytes in a row: lane 16 a + 8 b + 4 c + u takes, of keys 4 m + 2 a + c, the
     // groups 8 h + 4 b + u (code tile 2 h + b) and a piece of k_pe.  A quarter of the warp so stores an even and the next odd
     // row, whose columns the swizzle keeps apart.  (Four lanes a key, 64 bytes in a row: a third more time in the loads.)
-    constexpr int KW = C::kKeys / C::kLoadWarps;      // 16 or 14
-    static_assert(KW <= 16 && KW % 2 == 0, "a lane of half a warp for each key");
+    constexpr int KW = C::kKeys / C::kLoadWarps, KM = KW / 4;      // 16 or 12
+    static_assert(KW <= 16 && KW % 4 == 0, "a lane of half a warp for each key, four keys a step");
     const int w = warp - C::kFirstLoad;
     const int u = lane & 3, kb = (lane >> 3) & 1, key0 = 2 * (lane >> 4) + ((lane >> 2) & 1);      // key of m: 4 m + key0
     uint4* below = reinterpret_cast<uint4*>(smem + C::kBelow) + 16 * w;                             // [key] 16 bytes: exponents below K
@@ -583,13 +589,13 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
     // k_pe's piece of this lane: the halves of 64 bytes in the other order in odd rows (whose columns the swizzle takes to
     // the even rows' then)
     const int piece = u + 4 * (kb ^ (key0 & 1));
-    uint4 code[4][2], rope[4], ex = make_uint4(0, 0, 0, 0);
+    uint4 code[KM][2], rope[KM], ex = make_uint4(0, 0, 0, 0);
     bool live = false;      // lane k: key k is there
     auto load_tile = [&](const uint8_t* own) {
       live = own != nullptr;
       ex = live ? __ldg(reinterpret_cast<const uint4*>(own + kFp4Exps)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
+      for (int m = 0; m < KM; ++m) {
         const uint8_t* r = reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(own), 4 * m + key0));
         if (r) {
           rope[m] = __ldg(reinterpret_cast<const uint4*>(r + kFp4Rope) + piece);
@@ -653,8 +659,8 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       auto put_rope = [&]() {
         uint8_t* at = smem + C::kRope + (gt % C::kRopes) * C::kSlot;
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
-          if (4 * m + key0 < KW) *reinterpret_cast<uint4*>(at + 512 * m + (r0 ^ ((m & 1) << 6))) = rope[m];
+        for (int m = 0; m < KM; ++m)
+          *reinterpret_cast<uint4*>(at + 512 * m + (r0 ^ ((m & 1) << 6))) = rope[m];
         if (lane < KW)      // exponent 255: a NaN in the record; -1: no such key
           scl[h * kTile + KW * w + lane] = !live ? -1.f : K == 255u ? CUDART_NAN_F : __uint_as_float((K - 6u) << 23);
       };
@@ -669,10 +675,9 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       };
       auto put = [&](int i) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
+        for (int m = 0; m < KM; ++m) {
           uint4 v[2];
           convert(i, m, v);
-          if (4 * m + key0 >= KW) continue;
           uint8_t* at = tile + (2 * i + kb) * C::kSlot + 512 * m;
           const uint32_t o = o0 ^ ((m & 1) << 6);
           *reinterpret_cast<uint4*>(at + o) = v[0];
@@ -900,7 +905,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
             pv_waited = true;
             if (w && resc) {
 #pragma unroll 1
-              for (int x = 0; x < 4 * C::kN; x += NQ) {      // O_j: this thread's hi columns, then its lo columns
+              for (int x = 0; x < 4 * C::kNO; x += NQ) {      // this thread's columns of every O_j
 #pragma unroll 1
                 for (int c1 = c0; c1 < c0 + NC; c1 += 16) {
                   float o[16];
@@ -924,35 +929,39 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         }
         if (stid == 0) TL(3, rare ? 30 : 3);
         const float ik = __uint_as_float((254u << 23) - __float_as_uint(ks < 0.f ? 1.f : ks));      // 1 / ks
-        // hi = E4M3 of the weight in f16 (11 bits of it are more than the two terms keep), lo = E4M3 of 16 times the
-        // exact rest
-        uint32_t hw[NC / 4], lw[NC / 4];
+        // A weight in f16 (11 bits, steps of 2^-24 below 2^-14) as three E5M2 terms, each the rest rounded to nearest (three bits and
+        // a sign; the next rest is an f16 exactly, and an E5M2 the upper byte of an f16): to 2^-11 of the weight, or 2^-17
+        // where E5M2 ends.
+        uint32_t pw[C::kTerms][NC / 4];
 #pragma unroll
         for (int y = 0; y < NC / 4; ++y) {
-          uint32_t hi[2], lo[2];
+          uint32_t e[C::kTerms][2];
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const __half2 a = __floats2half2_rn(d[4 * y + 2 * z], d[4 * y + 2 * z + 1]);
-            hi[z] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(a), __NV_SATFINITE, __NV_E4M3);
-            const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi[z]), __NV_E4M3);
-            __half2 r = __hsub2(a, __half2(b));
-            if constexpr (!C::kWide) r = __hmul2(r, __float2half2_rn(C::kLo));
-            lo[z] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(r), __NV_SATFINITE, __NV_E4M3);
+            __half2 rest = __floats2half2_rn(d[4 * y + 2 * z], d[4 * y + 2 * z + 1]);
+#pragma unroll
+            for (int x = 0; x < C::kTerms; ++x) {
+              e[x][z] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E5M2);
+              const uint32_t term = __byte_perm(e[x][z], 0u, 0x1404);
+              if (x + 1 < C::kTerms) rest = __hsub2(rest, *reinterpret_cast<const __half2*>(&term));
+            }
           }
-          hw[y] = hi[0] | (hi[1] << 16);
-          lw[y] = lo[0] | (lo[1] << 16);
+#pragma unroll
+          for (int x = 0; x < C::kTerms; ++x) pw[x][y] = __byte_perm(e[x][0], e[x][1], 0x5410);
         }
         if (t > 0 && !pv_waited) {
           w = warp_spin(&pv_part[((gt - 1) & 1) * C::kParts + C::kParts - 1], static_cast<uint32_t>((gt - 1) >> 1) & 1u, abort_flag);   // P is free
           tc_fence_after();
         }
         if (stid == 0) TL(3, 4);
-        // 8 keys x 16 columns core matrices, 8-key groups 16 NQ bytes apart; hi columns, then lo columns
-        uint8_t* prow = ps + (row >> 3) * (16 * NQ) + (row & 7) * 16;
+        // 8 keys x 16 columns core matrices, 8-key groups 8 NQ bytes a term apart; one term's columns after the other's
+        if (C::kKeys == kTile || row < C::kKeys) {
+          uint8_t* prow = ps + (row >> 3) * (C::kTerms * 8 * NQ) + (row & 7) * 16;
 #pragma unroll
-        for (int y = 0; y < NC / 4; y += 4) {
-          *reinterpret_cast<uint4*>(prow + (c0 / 16 + y / 4) * 128) = make_uint4(hw[y], hw[y + 1], hw[y + 2], hw[y + 3]);
-          *reinterpret_cast<uint4*>(prow + ((NQ + c0) / 16 + y / 4) * 128) = make_uint4(lw[y], lw[y + 1], lw[y + 2], lw[y + 3]);
+          for (int x = 0; x < C::kTerms; ++x)
+#pragma unroll
+            for (int y = 0; y < NC / 4; y += 4)
+              *reinterpret_cast<uint4*>(prow + ((x * NQ + c0) / 16 + y / 4) * 128) = make_uint4(pw[x][y], pw[x][y + 1], pw[x][y + 2], pw[x][y + 3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -1003,16 +1012,15 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       for (int jc = 0; jc < 4 * (NC / 16); ++jc) {
         const int jj = jc / (NC / 16), c1 = 16 * (jc % (NC / 16));
         if (c1 >= ncol) continue;
-        float o[16];
-        tmem_ld16(tl + C::kTmemO + C::kN * jj + c0 + c1, o);
-        if constexpr (!C::kWide) {
-          float lo[16];
-          tmem_ld16(tl + C::kTmemO + C::kN * jj + NQ + c0 + c1, lo);
-          tmem_ld_wait();
+        float part[C::kStack][16];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) o[c] = fmaf(lo[c], 0.0625f, o[c]);
-        }
+        for (int x = 0; x < C::kStack; ++x) tmem_ld16(tl + C::kTmemO + C::kNO * jj + x * NQ + c0 + c1, part[x]);
         tmem_ld_wait();
+        float (&o)[16] = part[0];
+#pragma unroll
+        for (int x = 1; x < C::kStack; ++x)
+#pragma unroll
+          for (int c = 0; c < 16; ++c) o[c] += part[x][c];
         const int d = 128 * jj + row;
         if (final_out) {
           int h = (cgb + c1) % p.H;
