@@ -210,9 +210,11 @@ __device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t parity, volati
 }
 // A group of warps waits through its first one, the others at a hardware barrier: a warp that polls takes issue slots from
 // the others (polled by every softmax and loader warp, the waits were 4500 of 10000 instructions a tile).  Every thread of the group leaves with the same answer.
-__device__ __forceinline__ bool group_wait(bool first, uint32_t id, uint32_t threads, uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  bool w = true;
-  if (first) w = warp_spin(bar, parity, abort_flag);
+// `so_far`: false where a wait of this warp's own ran out before, which ends the group.
+__device__ __forceinline__ bool group_wait(bool first, uint32_t id, uint32_t threads, uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                           bool so_far = true) {
+  bool w = so_far;
+  if (first && w) w = warp_spin(bar, parity, abort_flag);
   return named_bar_and(id, threads, w);
 }
 // A wait that is in no hurry.
@@ -526,26 +528,26 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       const int32_t* table;      // the request's block ids; null: past the last tile
       int kp, end, left;         // this lane's key of the tile, the item's end, tiles after this one
     };
+    // ok is every loader warp's alike.  mine: this warp's waits have not run out; one of them may, at the edge of its limit, where
+    // another warp's on the same barrier does not, so the warp goes on without writing to the barrier at the next item, where
+    // all of them stop.
     int nit = 0;
-    bool ok = true;
+    bool ok = true, mine = true;
     auto next_item = [&](Cursor& c) {
-      for (;;) {
-        const int k = nit % kItemDepth;
-        if (!group_wait(w == 0, 2, 32 * C::kLoadWarps, &item_full[k], (nit / kItemDepth) & 1, abort_flag)) {
-          ok = false;
-          c.table = nullptr;
-          return;
-        }
-        const int b = items[k].b, k0 = items[k].k0, n = items[k].n, ntiles = items[k].ntiles;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&item_empty[k]);
-        ++nit;
-        c.table = b < 0 ? nullptr : p.block_table + static_cast<int64_t>(b) * p.bt_stride;
-        c.kp = k0 + KW * w + lane;
-        c.end = k0 + n;
-        c.left = ntiles - 1;
+      const int k = nit % kItemDepth;
+      if (!group_wait(w == 0, 2, 32 * C::kLoadWarps, &item_full[k], (nit / kItemDepth) & 1, abort_flag, mine)) {
+        ok = false;
+        c.table = nullptr;
         return;
       }
+      const int b = items[k].b, k0 = items[k].k0, n = items[k].n, ntiles = items[k].ntiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&item_empty[k]);
+      ++nit;
+      c.table = b < 0 ? nullptr : p.block_table + static_cast<int64_t>(b) * p.bt_stride;
+      c.kp = k0 + KW * w + lane;
+      c.end = k0 + n;
+      c.left = ntiles - 1;
     };
     auto advance = [&](Cursor& c) {
       if (!c.table) return;
@@ -685,17 +687,17 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
         }
         written(i);
       };
-      if (!free_slots(0)) break;
+      if (!(mine = free_slots(0))) break;
       if (w == 0 && lane == 0) TL(4, 2);
       if constexpr (C::kRopes == 2) put_rope();
       put(0);
       if (w == 0 && lane == 0) TL(4, 4);
-      ok = free_slots(1);
+      mine = free_slots(1);
       if constexpr (C::kRopes == 1) {
-        ok = ok && (gt < 1 || warp_spin(&s_full[h ^ 1], static_cast<uint32_t>((gt - 1) >> 1) & 1u, abort_flag));
-        if (ok) put_rope();
+        mine = mine && (gt < 1 || warp_spin(&s_full[h ^ 1], static_cast<uint32_t>((gt - 1) >> 1) & 1u, abort_flag));
+        if (mine) put_rope();
       }
-      if (!ok) break;
+      if (!mine) break;
       if (w == 0 && lane == 0) TL(4, 5);
       put(1);
       if (w == 0 && lane == 0) TL(4, 3);
@@ -710,6 +712,8 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       have1 = have2;
       have2 = c.table != nullptr;
     }
+    if (!mine)
+      while (c.table) advance(c);
     errbits = __reduce_or_sync(0xFFFFFFFFu, errbits);
     if (lane == 0 && errbits) set_device_error(p.err, errbits);
   } else {
