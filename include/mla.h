@@ -485,9 +485,11 @@ MLA_API int mla_rope_table(float* out, int64_t max_position, int32_t R, double b
  *      new blocks from the top of the stack, in the order of the requests, into its next table entries.
  *   3. Its rows cu_q_lens[b] .. cu_q_lens[b+1]-1 of the step hold positions L .. L + n - 1 and their slots
  *      (block * block_size + offset).  Rows past the last request's get position 0 and slot -1.
- * A request whose blocks are no longer there, whose table row is too short or whose rows end past T is not served
- * (later ones that need no more than is left are): it takes nothing, keeps its length, its rows have slot -1, and
- * MLA_DEVERR_FREE is set; so too where returned blocks pass the stack's capacity (those are lost).
+ * Requests are served in order.  One is not served where its table row is too short; where its rows, behind those of the
+ * requests before it, end past T; and where it needs more blocks than are left, or any after such a request: from the
+ * first one on that finds too few, those that need no new block are served and no others, so that none is overtaken.  It
+ * takes nothing, keeps its length, its rows have slot -1, and MLA_DEVERR_FREE is set; so too where returned blocks
+ * pass the stack's capacity (those are lost).
  *
  *   seq_lens     device int32 [B]: cached tokens before the step (negative: 0).   new_lens  device int32 [B].
  *   finished     device bytes [B], or NULL (none).

@@ -1055,7 +1055,8 @@ def plan_step(seq_lens, new_lens, block_table, free_blocks, num_free, *, block_s
     request takes those that its new tokens need, in order.  Returns (slot_mapping int64 [num_tokens], -1 in rows of no
     request; positions int64 [num_tokens]; cu_q_lens int32 [B + 1]; the new lengths int32 [B]; the new num_free int32 [1]).
     seq_lens_out and num_free_out may be seq_lens and num_free themselves; served (bool [B]) says which requests got
-    their blocks: the others keep their length, and their rows have slot -1 (device error 32)."""
+    their blocks: the others keep their length, and their rows have slot -1 (device error 32).  From the first request on that
+    finds too few blocks, only those that need no new one are served."""
     done = (_step or _plain_step()).plan(seq_lens, new_lens, block_table, free_blocks, num_free, block_size, num_tokens, finished, seq_lens_out,
                                          num_free_out, served, slot_mapping, positions, cu_q_lens)
     if done is not None:
