@@ -442,7 +442,7 @@ MLA_API int mla_v_up_proj(const void* latent, int64_t l_s0, int64_t l_s1, const 
  *
  *   type         MLA_TYPE_BF16, MLA_TYPE_FP16 or MLA_TYPE_FP32, of all four tensors.
  *   q            device [T, H, D], element strides (q_s0, q_s1); the R values from q_at on of every head are rotated,
- *                the others copied.  D <= 1024.
+ *                the others copied.  D <= 1024, H * D < 2^31.
  *   q_out        device out [T, H, D], strides (qo_s0, qo_s1): q itself (same address and strides: in place) or memory
  *                that does not meet q's.
  *   k, k_out     the same for [T, Hk, Dk] with k_at; both NULL: none.  In place both or neither.
@@ -500,7 +500,7 @@ MLA_API int mla_rope_table(float* out, int64_t max_position, int32_t R, double b
  *   served       device out bytes [B]: 1, or 0 where not served.  NULL: not wanted (B <= 1024).
  *   cu_q_lens    device out int32 [B + 1] (no more than T).
  *   slots, positions  device out int64 [T].
- * Whole numbers only: the same inputs give the same outputs.
+ * Whole numbers only: the same inputs give the same outputs.  B and T up to 2^31 - 2^13 - 1 (MLA_ERR_UNSUPPORTED beyond).
  */
 MLA_API int mla_plan_step(const int32_t* seq_lens, const int32_t* new_lens, const uint8_t* finished, int32_t* block_table,
                           int64_t t_stride, int32_t cols, int32_t* free_blocks, int64_t capacity, const int32_t* num_free,

@@ -39,6 +39,7 @@ struct RopeTableParams {
 cudaError_t launch_rope_table(const RopeTableParams& p, cudaStream_t stream);
 
 constexpr int kPlanKept = 1024;          // requests whose sums are kept on chip
+constexpr int kPlanMost = 0x7FFFFFFF - 8 * kPlanKept;      // requests or rows: one more round of all threads still counts in 32 bits
 struct PlanParams {
   const int32_t* seq_lens;
   const int32_t* new_lens;

@@ -20,6 +20,8 @@ int rope_tensor(const char* name, const void* in, int64_t i_s0, int64_t i_s1, vo
                 int32_t D, int32_t at, int32_t R, int bytes, bool half, RopeTensor* x, bool* vec, bool* inplace) {
   if (H < 1 || D < R || at < 0 || at > D - R) return fail(MLA_ERR_INVALID, "%s: bad shape H=%d D=%d at=%d R=%d", name, H, D, at, R);
   if (D > 1024) return fail(MLA_ERR_UNSUPPORTED, "%s: D must be <= 1024, got %d", name, D);
+  // (a token's values are counted in 32 bits)
+  if (static_cast<int64_t>(H) * D >= (int64_t(1) << 31)) return fail(MLA_ERR_UNSUPPORTED, "%s: a token of %d heads is too large", name, H);
   if (!in || !out) return fail(MLA_ERR_INVALID, "%s: a required pointer is NULL", name);
   if (!aligned(in, bytes) || !aligned(out, bytes)) return fail(MLA_ERR_INVALID, "%s must be aligned to its type", name);
   if (i_s1 < D || i_s0 < static_cast<int64_t>(H) * i_s1 || o_s1 < D || o_s0 < static_cast<int64_t>(H) * o_s1)
@@ -122,6 +124,7 @@ extern "C" int mla_plan_step(const int32_t* seq_lens, const int32_t* new_lens, c
                              int32_t* seq_out, int32_t* num_free_out, uint8_t* served, int32_t* cu_q_lens, int64_t* slots,
                              int64_t* positions, int32_t B, int32_t T, int32_t block_size, cudaStream_t stream) {
   if (B < 1 || T < 0) return fail(MLA_ERR_INVALID, "bad shape B=%d T=%d", B, T);
+  if (B > kPlanMost || T > kPlanMost) return fail(MLA_ERR_UNSUPPORTED, "B and T must be <= %d, got %d and %d", kPlanMost, B, T);
   if (block_size < 1) return fail(MLA_ERR_INVALID, "block_size must be >= 1");
   if (cols < 1 || t_stride < cols) return fail(MLA_ERR_INVALID, "bad block table: %d columns, row stride %lld", cols, static_cast<long long>(t_stride));
   if (capacity < 0 || capacity > 0x7FFFFFFF) return fail(MLA_ERR_INVALID, "bad capacity of the free blocks");
