@@ -627,7 +627,7 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   PyObject* type = types[q.type];
   const int64_t T = q.size[0];
   if (T > INT32_MAX || q.size[1] > INT32_MAX || q.size[2] > 1024 || a[1] == Py_None || !read_rotation(a[1], a[2], T, -1, dev, &pos, &cs) ||
-      cs.size[1] > 512 || !output(a[8], dev, 3, q.size, type, nullptr, device.p, &qo, &q_out))
+      cs.size[1] < 2 || cs.size[1] % 2 || cs.size[1] > 512 || !output(a[8], dev, 3, q.size, type, nullptr, device.p, &qo, &q_out))
     return not_plain();
   const int32_t R = static_cast<int32_t>(cs.size[1]);
   k = ko = Tensor{};
