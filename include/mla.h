@@ -306,7 +306,9 @@ MLA_API size_t mla_paged_decode_workspace_size_for(mla_cache_format fmt, int32_t
  *                aligned (may be NULL when that size is 0).  Contents need no initialising
  *                and are garbage afterwards.
  * A query row with no visible key gets out = 0 and lse = -inf.
- * MXFP4: a softmax weight enters the output to 2^-10 of itself; what is below 2^-27 of the largest one (with the power of two
+ * MXFP4: a group whose scale is below 2^(K - 14), with 2^K the largest scale of its record and K at least -60, is read as zeros:
+ *   of what an insert writes, values below 6 * 2^-75 alone (mla_gather_context reads all of them as they are).
+ *   A softmax weight enters the output to 2^-10 of itself; what is below 2^-27 of the largest one (with the power of two
  *   of its key's values) is cut off there, at most 2^-27 a key: 2^-10 over 131072 keys.  The lse misses nothing.
  */
 MLA_API int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache,

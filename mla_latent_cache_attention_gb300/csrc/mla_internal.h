@@ -197,7 +197,7 @@ cudaError_t launch_paged_tma_bf16(int nq, const PagedParams& p, const void* tkv,
 cudaError_t launch_paged_tma_fp8(int nq, const PagedParams& p, const void* tkv, const void* tq, int grid,
                                  cudaStream_t stream);
 
-// mxfp4 paged decode, nq (16 or 32) query columns per CTA, and the join of its partial results
+// mxfp4 paged decode, nq (16, 32, 48 or 64) query columns per CTA, and the join of its partial results
 cudaError_t launch_fp4_paged(int nq, const Fp4Params& p, cudaStream_t stream);
 cudaError_t launch_fp4_merge(const Fp4Params& p, cudaStream_t stream);
 

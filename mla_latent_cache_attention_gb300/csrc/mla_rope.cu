@@ -158,7 +158,7 @@ __device__ __forceinline__ void rope_scalar(const RopeTensor& x, const RopeParam
   }
 }
 
-// (42 registers a thread: with the 64 of two CTAs of 512 the prefill above takes 60 us, with 32 they spill: 99 us)
+// (40 registers a thread: with the 64 of two CTAs of 512 the prefill above takes 60 us, with 32 they spill: 99 us)
 template <int kType, bool kHalf, bool kVec, bool kCopy, bool kStream>
 __global__ void __launch_bounds__(512, 3) rope_kernel(const __grid_constant__ RopeParams p) {
   const int64_t t = blockIdx.x;
