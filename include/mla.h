@@ -306,6 +306,8 @@ MLA_API size_t mla_paged_decode_workspace_size_for(mla_cache_format fmt, int32_t
  *                aligned (may be NULL when that size is 0).  Contents need no initialising
  *                and are garbage afterwards.
  * A query row with no visible key gets out = 0 and lse = -inf.
+ * FP8: a softmax weight enters the output to 2^-7 of itself, below 2^-10 of the row's largest to 2^-3 (rounded to nearest: many
+ *   of them, not alike, average out), and what is below 2^-21 of it not at all.  The lse misses nothing.
  * MXFP4: a group whose scale is below 2^(K - 14), with 2^K the largest scale of its record and K at least -60, is read as zeros:
  *   of what an insert writes, values below 6 * 2^-75 alone (mla_gather_context reads all of them as they are).
  *   A softmax weight enters the output to 2^-10 of itself; what is below 2^-27 of the largest one (with the power of two
