@@ -49,9 +49,9 @@
 //     polled: a suspended thread (try_wait) was woken 0.5 to 1 us late, four times a tile (1390 -> 1095 us; of 16 columns 43 ->
 //     39).
 //
-// What bounds it now, 64 columns: loaders (load latency, then conversion and stores), softmax (ordered after QK) and the tensor
-// pipe, whose operand reads (6 KB a product of 33 cycles) share the data path of shared memory with both: 72 products a tile at
-// 75 cycles each.  Up to 32 columns: the chain of load, conversion, QK, softmax and PV of two tiles (2.5 us a tile).
+// What bounds it now, 64 columns (3.3 us a tile of 96 keys; 48: 3.7 us of 128): loaders (load latency, then conversion and stores), softmax (ordered after QK) and the tensor
+// pipe, whose operand reads (6 KB a product of 33 cycles) share the data path of shared memory with both: 72 (84) products a tile
+// at 75 cycles each.  Up to 32 columns: the chain of load, conversion, QK, softmax and PV of two tiles (2.5 us a tile).
 //
 // Warps: 0 scheduler, 1 QK issuer (TMEM owner), 2 PV issuer, then the softmax warps (which also prepare the query and
 // write the results), then 8 loaders.
