@@ -312,6 +312,8 @@ MLA_API size_t mla_paged_decode_workspace_size_for(mla_cache_format fmt, int32_t
  *   of what an insert writes, values below 6 * 2^-75 alone (mla_gather_context reads all of them as they are).
  *   A softmax weight enters the output to 2^-10 of itself; what is below 2^-27 of the largest one (with the power of two
  *   of its key's values) is cut off there, at most 2^-27 a key: 2^-10 over 131072 keys.  The lse misses nothing.
+ *   A query value enters as it is from 2^-10 of its row's largest on, below that to 2^-17 of the largest (to 2^-21 where q_len * H
+ *   is at most 32).
  */
 MLA_API int mla_paged_decode(const void* q, int64_t q_s0, int64_t q_s1, const void* kv_cache,
                      mla_cache_format fmt, int64_t num_blocks, int64_t block_stride_bytes,
