@@ -32,11 +32,11 @@
 //     sum w 2^(6 - K) = 2^(s - m), so the key's scale costs one multiplication.  The weights enter
 //     O^T += V^T P as three E5M2 terms, each the rest rounded to nearest: a weight is off by 2^-10 of itself at most (half a step
 //     of the last term, 2^-11, and of the f16 that is split, 2^-11), and nothing is lost above 2^-27 of the reference, which
-//     may stand far above most weights of a row (one large key in front; two E4M3 terms ended at 2^-15 and dropped up to
-//     half of such a row's output).  Over 2^17 keys that is 2^-10 of the largest weight.  The reference m moves only when a
+//     may stand far above most weights of a row (one large key in front; two E4M3 terms ended at 2^-15 and dropped 4 to
+//     35 % of such a row's output).  Over 2^17 keys that is 2^-10 of the largest weight.  The reference m moves only when a
 //     logit passes it by kTau, a move costs 2.8 us: the higher kTau, the earlier E5M2 ends below the reference (4 x 16 rows as
-//     above, 128 requests of 96 heads as above and 32 requests of 1024 to 8192 keys: kTau 4.75 1127, 1005 and 39.5 us, 5.75 1099, 1003 and 39.1;
-//     the two E4M3 terms took 1025, 939 and 37.2).  The largest weight of an item's first tile is 2^kPExp, a term exactly.
+//     above, 128 requests of 96 heads as above and 32 requests of 1024 to 8192 keys: kTau 4.75 1127, 1005 and 39.5 us, 5.75
+//     1099, 1003 and 39.1; the two E4M3 terms took 1025, 939 and 37.2).  The largest weight of an item's first tile is 2^kPExp, a term exactly.
 //   * The tensor cores add in fp32 and cut off: 2^-23 of an accumulator a product, of 32 keys.  Terms of both signs make less
 //     of it (131072 flat keys behind one of 15 nats more: output 0.0009 too small; 2^20 keys: 0.002).
 //   * The terms of a weight stand side by side along N with accumulators of their own that the epilogue adds (16 columns), or as
@@ -49,9 +49,9 @@
 //     polled: a suspended thread (try_wait) was woken 0.5 to 1 us late, four times a tile (1390 -> 1095 us; of 16 columns 43 ->
 //     39).
 //
-// What bounds it now, 64 columns (3.3 us a tile of 96 keys; 48: 3.7 us of 128): loaders (load latency, then conversion and stores), softmax (ordered after QK) and the tensor
-// pipe, whose operand reads (6 KB a product of 33 cycles) share the data path of shared memory with both: 72 (84) products a tile
-// at 75 cycles each.  Up to 32 columns: the chain of load, conversion, QK, softmax and PV of two tiles (2.5 us a tile).
+// What bounds it now, 64 columns (3.3 us a tile of 96 keys; 48: 3.7 us of 128): loaders (load latency, then conversion and
+// stores), softmax (ordered after QK) and the tensor pipe, whose operand reads (6 KB a product of 33 cycles) share the data
+// path of shared memory with both: 72 (84) products a tile at 75 cycles each.  Up to 32 columns: the chain of load, conversion, QK, softmax and PV of two tiles (2.5 us a tile).
 //
 // Warps: 0 scheduler, 1 QK issuer (TMEM owner), 2 PV issuer, then the softmax warps (which also prepare the query and
 // write the results), then 8 loaders.
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(Fp4Cfg<NQ>::kThreads, 1) mla_fp4_kernel(const 
       int kp, end, left;         // this lane's key of the tile, the item's end, tiles after this one
     };
     // ok is every loader warp's alike.  mine: this warp's waits have not run out; one of them may, at the edge of its limit, where
-    // another warp's on the same barrier does not, so the warp goes on without writing to the barrier at the next item, where
+    // another warp's on the same barrier does not: the warp leaves its tiles and goes on to the barrier of the next item, where
     // all of them stop.
     int nit = 0;
     bool ok = true, mine = true;
